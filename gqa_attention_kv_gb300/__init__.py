@@ -21,12 +21,13 @@ LIB_PATH = os.path.join(_HERE, "libgqa_attn_kv.so")
 ATTN_OK = 0
 STATUS_NAMES = {0: "ATTN_OK", 1: "ATTN_ERR_NULL", 2: "ATTN_ERR_SHAPE", 3: "ATTN_ERR_UNSUPPORTED",
                 4: "ATTN_ERR_WORKSPACE", 5: "ATTN_ERR_BOUNDS", 6: "ATTN_ERR_TIMEOUT",
-                7: "ATTN_ERR_CUDA", 8: "ATTN_ERR_ALIGN"}
+                7: "ATTN_ERR_CUDA", 8: "ATTN_ERR_ALIGN", 9: "ATTN_ERR_PAGES"}
 for _code, _name in STATUS_NAMES.items():
     globals()[_name] = _code
 ATTN_DECODE_TABLES_EARLY = 1  # attn_decode_append flags (include/attn_kv.h)
 ATTN_DECODE_CACHE_EARLY = 2
 ATTN_KV_BF16, ATTN_KV_FP8_E4M3 = 0, 1  # cache element types (attn_kv_dtype)
+ATTN_KV_FP8_E4M3_SCALED, ATTN_KV_INT8_SCALED = 2, 3
 ATTN_LAYOUT_BSHD, ATTN_LAYOUT_BHSD = 0, 1  # cache layouts (attn_kv_layout)
 
 _lock = threading.Lock()
@@ -48,7 +49,9 @@ class _Cache(ctypes.Structure):
                 ("num_slots", ctypes.c_int64), ("slots_per_seq", ctypes.c_int32),
                 ("block_table", ctypes.c_void_p), ("block_size", ctypes.c_int32),
                 ("max_blocks_per_seq", ctypes.c_int32), ("dtype", ctypes.c_int32),
-                ("k_ref", ctypes.c_void_p), ("layout", ctypes.c_int32)]
+                ("k_ref", ctypes.c_void_p), ("layout", ctypes.c_int32),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("scale_block", ctypes.c_int32)]
 
 
 def lib():
@@ -85,6 +88,27 @@ def lib():
             L.attn_prefill.argtypes = [p, p, p, i32, i32, i32, i32, i32, i32, ctypes.c_float, p,
                                        p, p]
             L.attn_prefill.restype = i32
+            L.attn_decode_sinks_workspace_size.argtypes = [cp, i32, i32, i32, i32, i32, i32, i32,
+                                                           i32]
+            L.attn_decode_sinks_workspace_size.restype = sz
+            L.attn_decode_sinks.argtypes = [p, cp, p, p, i32, i32, i32, i32, i32, i32, i32, i32,
+                                            ctypes.c_float, p, p, sz, p, p]
+            L.attn_decode_sinks.restype = i32
+            L.attn_prefill_sinks.argtypes = [p, p, p, i32, i32, i32, i32, i32, i32, i32,
+                                             ctypes.c_float, p, p, p]
+            L.attn_prefill_sinks.restype = i32
+            L.attn_pages_free.argtypes = [p, i32, i32, p, p, p, i32, p, i32, p, p]
+            L.attn_pages_free.restype = i32
+            L.attn_pages_reserve.argtypes = [p, i32, i32, p, p, p, i32, p, i32, p, p]
+            L.attn_pages_reserve.restype = i32
+            L.attn_pages_fork.argtypes = [p, i32, i32, p, p, p, i32, i32, p, i32, p, i32, p, p, p]
+            L.attn_pages_fork.restype = i32
+            L.attn_pages_workspace_size.argtypes = [i32]
+            L.attn_pages_workspace_size.restype = sz
+            L.attn_pages_compact.argtypes = [p, i32, i32, i32, p, i32, p, i32, p, p, p, sz, p, p]
+            L.attn_pages_compact.restype = i32
+            L.attn_pages_copy.argtypes = [cp, i32, i32, i32, p, p, i32, p, p]
+            L.attn_pages_copy.restype = i32
             L.attn_status_string.argtypes = [i32]
             L.attn_status_string.restype = ctypes.c_char_p
             L.attn_version.restype = ctypes.c_char_p
@@ -128,13 +152,19 @@ class KVCache:
     head_dim] (rows = slots_per_seq, or block_size when paged); slots are
     numbered as in the slot-major layout.
 
+    dtypes ATTN_KV_FP8_E4M3_SCALED (uint8 codes) and ATTN_KV_INT8_SCALED (int8):
+    scale_block consecutive slots of a head share the scales k_scale and
+    v_scale, float32 [num_slots // scale_block, n_kv_heads], which
+    attn_kv_append keeps.
+
     kind LINEAR: slots_per_seq = per-request capacity.
     kind PAGED : block_table int32 [batch, max_blocks_per_seq] (device), block_size.
     kind RING  : slots_per_seq = ring size.
     """
 
     def __init__(self, kind, k, v, slots_per_seq=0, block_table=None, block_size=0,
-                 dtype=ATTN_KV_BF16, k_ref=None, layout=ATTN_LAYOUT_BSHD):
+                 dtype=ATTN_KV_BF16, k_ref=None, layout=ATTN_LAYOUT_BSHD, k_scale=None,
+                 v_scale=None, scale_block=0):
         self.kind, self.k, self.v = int(kind), k, v
         self.slots_per_seq = int(slots_per_seq)
         self.block_table = block_table
@@ -142,6 +172,8 @@ class KVCache:
         self.dtype = int(dtype)
         self.k_ref = k_ref
         self.layout = int(layout)
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.scale_block = int(scale_block)
 
     @property
     def n_kv_heads(self):
@@ -160,7 +192,10 @@ class KVCache:
         return _Cache(self.kind, self.k.data_ptr(), self.v.data_ptr(), self.num_slots,
                       self.slots_per_seq, None if bt is None else bt.data_ptr(),
                       self.block_size, 0 if bt is None else bt.shape[-1], self.dtype,
-                      None if self.k_ref is None else self.k_ref.data_ptr(), self.layout)
+                      None if self.k_ref is None else self.k_ref.data_ptr(), self.layout,
+                      None if self.k_scale is None else self.k_scale.data_ptr(),
+                      None if self.v_scale is None else self.v_scale.data_ptr(),
+                      self.scale_block)
 
 
 def attn_kv_append(k_new, v_new, slot_mapping, cache: KVCache, err=None, stream=None):
@@ -299,3 +334,127 @@ def attn_decode_noalloc(q, cache: KVCache, seq_lens, positions, max_seq_len, win
            _stream(stream))
     _check(rc, "attn_decode_noalloc")
     return out
+
+
+def attn_decode_sinks_workspace_size(cache: KVCache, batch, q_rows, n_q_heads, max_seq_len,
+                                     window, n_sinks) -> int:
+    c = cache.struct()
+    n = lib().attn_decode_sinks_workspace_size(ctypes.byref(c), batch, q_rows, n_q_heads,
+                                               cache.n_kv_heads, cache.head_dim, max_seq_len,
+                                               window, n_sinks)
+    if n == ctypes.c_size_t(-1).value:
+        raise AttnError(ATTN_ERR_SHAPE, "attn_decode_sinks_workspace_size")
+    return int(n)
+
+
+def attn_decode_sinks(q, cache: KVCache, seq_lens, positions, max_seq_len, window, n_sinks, scale,
+                      out=None, workspace=None, err=None, stream=None):
+    """attn_decode under a sliding window whose first n_sinks tokens stay
+    visible: a row at position pos attends t <= pos with t < n_sinks or
+    pos - t < window (window <= 0: every t).  RING caches keep the sinks in
+    each request's first n_sinks slots and turn the others.  The workspace
+    (at least attn_decode_sinks_workspace_size bytes) needs no zeroing; it is
+    allocated if not given."""
+    import torch
+
+    B, R, Hq, D = q.shape
+    if out is None:
+        out = torch.empty_like(q)
+    if workspace is None:
+        need = attn_decode_sinks_workspace_size(cache, B, R, Hq, max_seq_len, window, n_sinks)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+    c = cache.struct()
+    rc = lib().attn_decode_sinks(
+        _ptr(q), ctypes.byref(c), _ptr(seq_lens), _ptr(positions), B, R, int(max_seq_len),
+        int(window), int(n_sinks), Hq, cache.n_kv_heads, D, float(scale), _ptr(out),
+        _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(err),
+        _stream(stream))
+    _check(rc, "attn_decode_sinks")
+    return out
+
+
+def attn_prefill_sinks(q, k, v, window, n_sinks, scale, out=None, err=None, stream=None):
+    """attn_prefill under a sliding window whose first n_sinks tokens of each
+    sequence stay visible.  Shapes as attn_prefill's."""
+    import torch
+
+    B, T, Hq, D = q.shape
+    if out is None:
+        out = torch.empty_like(q)
+    rc = lib().attn_prefill_sinks(_ptr(q), _ptr(k), _ptr(v), B, T, int(window), int(n_sinks), Hq,
+                                  k.shape[2], D, float(scale), _ptr(out), _ptr(err),
+                                  _stream(stream))
+    _check(rc, "attn_prefill_sinks")
+    return out
+
+
+def attn_pages_free(block_table, refs, rows, from_block, to_block, err=None, stream=None):
+    """Entries from_block[i] .. to_block[i] - 1 of row rows[i] of block_table
+    (int32 [table_rows, max_blocks]) give their page back (refs, int32
+    [num_pages], counts a page's entries) and become -1.  rows, from_block,
+    to_block: int32 [n] on the device."""
+    rc = lib().attn_pages_free(_ptr(block_table), block_table.shape[1], block_table.shape[0],
+                               _ptr(rows), _ptr(from_block), _ptr(to_block), rows.shape[0],
+                               _ptr(refs), refs.shape[0], _ptr(err), _stream(stream))
+    _check(rc, "attn_pages_free")
+
+
+def attn_pages_reserve(block_table, refs, rows, from_block, to_block, err=None, stream=None):
+    """Entries from_block[i] .. to_block[i] - 1 of row rows[i] that are -1 take
+    the lowest free pages (refs 0), in order.  ATTN_ERR_PAGES in err when the
+    pool runs out."""
+    rc = lib().attn_pages_reserve(_ptr(block_table), block_table.shape[1], block_table.shape[0],
+                                  _ptr(rows), _ptr(from_block), _ptr(to_block), rows.shape[0],
+                                  _ptr(refs), refs.shape[0], _ptr(err), _stream(stream))
+    _check(rc, "attn_pages_reserve")
+
+
+def attn_pages_fork(block_table, refs, src_rows, dst_rows, seq_lens, block_size, moves, n_moves,
+                    err=None, stream=None):
+    """Row dst_rows[i] becomes the first seq_lens[i] tokens of row src_rows[i]:
+    full pages shared, a partial last page replaced by a free one.  moves (int32
+    [at least n, 3]) and n_moves (int32 [1]) receive the copies to carry out
+    with attn_pages_copy."""
+    rc = lib().attn_pages_fork(_ptr(block_table), block_table.shape[1], block_table.shape[0],
+                               _ptr(src_rows), _ptr(dst_rows), _ptr(seq_lens), src_rows.shape[0],
+                               int(block_size), _ptr(refs), refs.shape[0], _ptr(moves),
+                               moves.shape[0], _ptr(n_moves), _ptr(err), _stream(stream))
+    _check(rc, "attn_pages_fork")
+
+
+def attn_pages_workspace_size(num_pages) -> int:
+    n = lib().attn_pages_workspace_size(int(num_pages))
+    if n == ctypes.c_size_t(-1).value:
+        raise AttnError(ATTN_ERR_SHAPE, "attn_pages_workspace_size")
+    return int(n)
+
+
+def attn_pages_compact(block_table, refs, block_size, moves, n_moves, used, workspace=None,
+                       err=None, stream=None):
+    """Pages in use move to the lowest page ids: block_table and refs follow,
+    used (int32 [1]) receives how many pages are in use, moves / n_moves the
+    copies to carry out with attn_pages_copy."""
+    import torch
+
+    if workspace is None:
+        workspace = torch.empty(attn_pages_workspace_size(refs.shape[0]), dtype=torch.uint8,
+                                device=refs.device)
+    rc = lib().attn_pages_compact(_ptr(block_table), block_table.shape[1], block_table.shape[0],
+                                  int(block_size), _ptr(refs), refs.shape[0], _ptr(moves),
+                                  moves.shape[0], _ptr(n_moves), _ptr(used), _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), _ptr(err),
+                                  _stream(stream))
+    _check(rc, "attn_pages_compact")
+
+
+def attn_pages_copy(caches, moves, n_moves, err=None, stream=None):
+    """Carries out n_moves (int32 [1], device) page copies listed in moves in
+    each of the paged caches (a KVCache, or a list of them, one per layer)."""
+    if isinstance(caches, KVCache):
+        caches = [caches]
+    arr = (_Cache * max(1, len(caches)))(*[c.struct() for c in caches])
+    Hkv, D = (caches[0].n_kv_heads, caches[0].head_dim) if caches else (1, 128)
+    rc = lib().attn_pages_copy(arr, len(caches), Hkv, D, _ptr(moves), _ptr(n_moves),
+                               moves.shape[0], _ptr(err), _stream(stream))
+    _check(rc, "attn_pages_copy")

@@ -114,6 +114,27 @@ int check_layout(const attn_kv_cache *c) {
     return ATTN_OK;
 }
 
+// The fields of a scaled cache: whole scale blocks in every request's slots or
+// page, and the scales themselves (unless only sizes are asked for).
+int check_scaled(const attn_kv_cache *c, bool pointers) {
+    const int sb = c->scale_block;
+    if (sb != 16 && sb != 32 && sb != 64 && sb != 128) return ATTN_ERR_UNSUPPORTED;
+    int64_t rows;
+    if (c->kind == ATTN_CACHE_LINEAR)
+        rows = c->slots_per_seq;
+    else if (c->kind == ATTN_CACHE_PAGED)
+        rows = c->block_size;
+    else  // a ring overwrites blocks whose other tokens are still visible
+        return ATTN_ERR_UNSUPPORTED;
+    if (rows < 1 || rows % sb != 0 || c->num_slots % sb != 0) return ATTN_ERR_SHAPE;
+    if (pointers) {
+        if (!c->k_scale || !c->v_scale) return ATTN_ERR_NULL;
+        if (!aligned16(c->k_scale) || !aligned16(c->v_scale) || (c->k_ref && !aligned16(c->k_ref)))
+            return ATTN_ERR_ALIGN;
+    }
+    return ATTN_OK;
+}
+
 // Validation shared by attn_decode and attn_decode_workspace_size.
 int check_decode_shape(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads,
                        int n_kv_heads, int head_dim, int max_seq_len, int window) {
@@ -125,8 +146,11 @@ int check_decode_shape(const attn_kv_cache *cache, int batch, int q_rows, int n_
         return ATTN_ERR_SHAPE;
     }
     if (cache->num_slots < 1 || cache->num_slots >= (int64_t(1) << 31)) return ATTN_ERR_SHAPE;
-    if (cache->dtype != ATTN_KV_BF16 && cache->dtype != ATTN_KV_FP8_E4M3)
+    if (gqa::kv_scaled(cache->dtype)) {
+        if (int rc = check_scaled(cache, false); rc != ATTN_OK) return rc;
+    } else if (cache->dtype != ATTN_KV_BF16 && cache->dtype != ATTN_KV_FP8_E4M3) {
         return ATTN_ERR_UNSUPPORTED;
+    }
     if (cache->dtype == ATTN_KV_FP8_E4M3 && head_dim != 128) return ATTN_ERR_UNSUPPORTED;
     if (int rc = check_layout(cache); rc != ATTN_OK) return rc;
     if (cache->layout == ATTN_LAYOUT_BHSD &&
@@ -183,6 +207,12 @@ int attn_kv_append(const void *k_new, const void *v_new, const int64_t *slot_map
                                          gqa::kv_place(cache, n_kv_heads, head_dim, 1), err_word,
                                          reinterpret_cast<cudaStream_t>(stream));
     }
+    if (gqa::kv_scaled(cache->dtype)) {
+        if (int rc = check_scaled(cache, true); rc != ATTN_OK) return rc;
+        return gqa::launch_kv_append_scaled(k_new, v_new, slot_mapping, n, cache, n_kv_heads,
+                                            head_dim, err_word,
+                                            reinterpret_cast<cudaStream_t>(stream));
+    }
     if (cache->dtype != ATTN_KV_BF16) return ATTN_ERR_UNSUPPORTED;
     return gqa::launch_kv_append(k_new, v_new, slot_mapping, n, cache->k, cache->v,
                                  cache->num_slots, gqa::kv_place(cache, n_kv_heads, head_dim, 2),
@@ -206,6 +236,13 @@ size_t attn_decode_workspace_size(const attn_kv_cache *cache, int batch, int q_r
                            window) != ATTN_OK)
         return (size_t)-1;
     if (batch == 0) return 0;
+    if (gqa::kv_scaled(cache->dtype)) {
+        gqa::AttendPlan ap;
+        return gqa::plan_attend(cache, batch, q_rows, n_q_heads, n_kv_heads, head_dim, max_seq_len,
+                                window, 0, &ap) == ATTN_OK
+                   ? ap.workspace
+                   : (size_t)-1;
+    }
     gqa::DecodePlan plan;
     gqa::plan_decode(cache, batch, q_rows, n_q_heads, n_kv_heads, head_dim, max_seq_len, window,
                      &plan);
@@ -220,6 +257,13 @@ int attn_decode_kernel_launches(const attn_kv_cache *cache, int batch, int q_row
                            window) != ATTN_OK)
         return -1;
     if (batch == 0) return 0;
+    if (gqa::kv_scaled(cache->dtype)) {
+        gqa::AttendPlan ap;
+        return gqa::plan_attend(cache, batch, q_rows, n_q_heads, n_kv_heads, head_dim, max_seq_len,
+                                window, 0, &ap) == ATTN_OK && !with_rope
+                   ? ap.launches + (with_append ? 1 : 0)
+                   : -1;
+    }
     gqa::DecodePlan plan;
     gqa::plan_decode(cache, batch, q_rows, n_q_heads, n_kv_heads, head_dim, max_seq_len, window,
                      &plan);
@@ -251,6 +295,42 @@ int validate_decode(const void *q, const attn_kv_cache *cache, const int32_t *se
 
 }  // namespace gqa
 
+namespace {
+
+// The register-fed decode of a validated call (batch > 0).
+int attend(const void *q, const attn_kv_cache *cache, const int32_t *seq_lens,
+           const int32_t *positions, int batch, int q_rows, int max_seq_len, int window,
+           int n_sinks, int n_q_heads, int n_kv_heads, int head_dim, float scale, void *out,
+           void *workspace, size_t workspace_bytes, int32_t *err_word, attn_stream_t stream,
+           bool dry_run = false) {
+    if (gqa::kv_scaled(cache->dtype))
+        if (int rc = check_scaled(cache, true); rc != ATTN_OK) return rc;
+    gqa::AttendPlan ap;
+    if (int rc = gqa::plan_attend(cache, batch, q_rows, n_q_heads, n_kv_heads, head_dim,
+                                  max_seq_len, window, n_sinks, &ap);
+        rc != ATTN_OK)
+        return rc;
+    if (!workspace) return ATTN_ERR_NULL;
+    if (workspace_bytes < ap.workspace) return ATTN_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return ATTN_ERR_ALIGN;
+    if (dry_run) return ATTN_OK;
+    return gqa::launch_attend(ap, q, cache, seq_lens, positions, q_rows, max_seq_len, window,
+                              n_sinks, n_q_heads, n_kv_heads, head_dim, scale, out, workspace,
+                              err_word, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// What a window with sinks asks beyond check_decode_shape.
+int check_sinks(const attn_kv_cache *cache, int q_rows, int window, int n_sinks) {
+    if (n_sinks < 0) return ATTN_ERR_SHAPE;
+    // the sinks keep their slots: the rest of a ring has to hold the window
+    if (cache->kind == ATTN_CACHE_RING &&
+        (int64_t)cache->slots_per_seq - n_sinks < (int64_t)window + q_rows - 1)
+        return ATTN_ERR_SHAPE;
+    return ATTN_OK;
+}
+
+}  // namespace
+
 extern "C" {
 
 int attn_decode(const void *q, const attn_kv_cache *cache, const int32_t *seq_lens,
@@ -263,6 +343,10 @@ int attn_decode(const void *q, const attn_kv_cache *cache, const int32_t *seq_le
                                         window, n_q_heads, n_kv_heads, head_dim, scale, out,
                                         &plan);
     if (rc != ATTN_OK || batch == 0) return rc;
+    if (gqa::kv_scaled(cache->dtype))
+        return attend(q, cache, seq_lens, positions, batch, q_rows, max_seq_len, window, 0,
+                      n_q_heads, n_kv_heads, head_dim, scale, out, workspace, workspace_bytes,
+                      err_word, stream);
     if (plan.workspace > 0) {
         if (!workspace) return ATTN_ERR_NULL;
         if (workspace_bytes < plan.workspace) return ATTN_ERR_WORKSPACE;
@@ -288,7 +372,8 @@ int attn_decode_append(const void *q, const void *k_new, const void *v_new,
         return ATTN_ERR_UNSUPPORTED;
     // FP8 caches: the rows are encoded as attn_kv_append encodes them; the
     // rotary embedding is not combined with them here
-    if (cache->dtype == ATTN_KV_FP8_E4M3 && rope_inv_freq) return ATTN_ERR_UNSUPPORTED;
+    const bool scaled = gqa::kv_scaled(cache->dtype);
+    if ((cache->dtype == ATTN_KV_FP8_E4M3 || scaled) && rope_inv_freq) return ATTN_ERR_UNSUPPORTED;
     if (cache->dtype == ATTN_KV_FP8_E4M3 && cache->k_ref && !aligned16(cache->k_ref))
         return ATTN_ERR_ALIGN;
     if (batch == 0) return ATTN_OK;
@@ -299,6 +384,20 @@ int attn_decode_append(const void *q, const void *k_new, const void *v_new,
     if (!aligned16(q) || !aligned16(out) || !aligned16(cache->k) || !aligned16(cache->v) ||
         !aligned16(k_new) || !aligned16(v_new))
         return ATTN_ERR_ALIGN;
+    if (scaled) {
+        // a new row may change the scale of its block: appended first, whole
+        rc = attend(q, cache, seq_lens, positions, batch, q_rows, max_seq_len, window, 0,
+                    n_q_heads, n_kv_heads, head_dim, scale, out, workspace, workspace_bytes,
+                    err_word, stream, true);
+        if (rc != ATTN_OK) return rc;
+        rc = gqa::launch_kv_append_scaled(k_new, v_new, slot_mapping, (int64_t)batch * q_rows,
+                                          cache, n_kv_heads, head_dim, err_word,
+                                          reinterpret_cast<cudaStream_t>(stream));
+        if (rc != ATTN_OK) return rc;
+        return attend(q, cache, seq_lens, positions, batch, q_rows, max_seq_len, window, 0,
+                      n_q_heads, n_kv_heads, head_dim, scale, out, workspace, workspace_bytes,
+                      err_word, stream);
+    }
     gqa::DecodePlan plan;
     gqa::plan_decode(cache, batch, q_rows, n_q_heads, n_kv_heads, head_dim, max_seq_len, window,
                      &plan);
@@ -314,9 +413,43 @@ int attn_decode_append(const void *q, const void *k_new, const void *v_new,
                               (flags & ATTN_DECODE_CACHE_EARLY) != 0);
 }
 
-int attn_prefill(const void *q, const void *k, const void *v, int batch, int seq_len, int window,
-                 int n_q_heads, int n_kv_heads, int head_dim, float scale, void *out,
-                 int32_t *err_word, attn_stream_t stream) {
+size_t attn_decode_sinks_workspace_size(const attn_kv_cache *cache, int batch, int q_rows,
+                                        int n_q_heads, int n_kv_heads, int head_dim,
+                                        int max_seq_len, int window, int n_sinks) {
+    gqa::AttendPlan ap;
+    if (check_decode_shape(cache, batch, q_rows, n_q_heads, n_kv_heads, head_dim, max_seq_len,
+                           window) != ATTN_OK ||
+        check_sinks(cache, q_rows, window, n_sinks) != ATTN_OK)
+        return (size_t)-1;
+    if (batch == 0) return 0;
+    if (gqa::plan_attend(cache, batch, q_rows, n_q_heads, n_kv_heads, head_dim, max_seq_len,
+                         window, n_sinks, &ap) != ATTN_OK)
+        return (size_t)-1;
+    return ap.workspace;
+}
+
+int attn_decode_sinks(const void *q, const attn_kv_cache *cache, const int32_t *seq_lens,
+                      const int32_t *positions, int batch, int q_rows, int max_seq_len, int window,
+                      int n_sinks, int n_q_heads, int n_kv_heads, int head_dim, float scale,
+                      void *out, void *workspace, size_t workspace_bytes, int32_t *err_word,
+                      attn_stream_t stream) {
+    gqa::DecodePlan plan;
+    int rc = gqa::validate_decode(q, cache, seq_lens, positions, batch, q_rows, max_seq_len, window,
+                                  n_q_heads, n_kv_heads, head_dim, scale, out, &plan);
+    if (rc == ATTN_OK) rc = check_sinks(cache, q_rows, window, n_sinks);
+    if (rc != ATTN_OK || batch == 0) return rc;
+    return attend(q, cache, seq_lens, positions, batch, q_rows, max_seq_len, window, n_sinks,
+                  n_q_heads, n_kv_heads, head_dim, scale, out, workspace, workspace_bytes,
+                  err_word, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+int prefill(const void *q, const void *k, const void *v, int batch, int seq_len, int window,
+            int n_sinks, int n_q_heads, int n_kv_heads, int head_dim, float scale, void *out,
+            int32_t *err_word, attn_stream_t stream) {
     if (batch < 0 || seq_len < 0) return ATTN_ERR_SHAPE;
     if (!heads_ok(n_q_heads, n_kv_heads, head_dim)) {
         if (n_kv_heads >= 1 && n_q_heads >= 1 && n_q_heads % n_kv_heads == 0)
@@ -330,7 +463,133 @@ int attn_prefill(const void *q, const void *k, const void *v, int batch, int seq
     const int64_t tiles = ((int64_t)seq_len + 127) / 128 * n_q_heads * (int64_t)batch;
     if (tiles >= (int64_t(1) << 31)) return ATTN_ERR_SHAPE;
     return gqa::launch_prefill(q, k, v, batch, seq_len, window, n_q_heads, n_kv_heads, head_dim,
-                               scale, out, err_word, reinterpret_cast<cudaStream_t>(stream));
+                               scale, out, err_word, reinterpret_cast<cudaStream_t>(stream),
+                               n_sinks);
+}
+
+// The table, pool and row arguments the page operations share.
+int check_pool(const int32_t *block_table, int max_blocks, int table_rows, const int32_t *refs,
+               int num_pages) {
+    if (max_blocks < 1 || table_rows < 0 || num_pages < 1 ||
+        num_pages > (1 << 30))  // page numbers of a tile stay in 32 bits
+        return ATTN_ERR_SHAPE;
+    if (!block_table || !refs) return ATTN_ERR_NULL;
+    if (!aligned16(block_table) || !aligned16(refs)) return ATTN_ERR_ALIGN;
+    return ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_prefill(const void *q, const void *k, const void *v, int batch, int seq_len, int window,
+                 int n_q_heads, int n_kv_heads, int head_dim, float scale, void *out,
+                 int32_t *err_word, attn_stream_t stream) {
+    return prefill(q, k, v, batch, seq_len, window, 0, n_q_heads, n_kv_heads, head_dim, scale, out,
+                   err_word, stream);
+}
+
+int attn_prefill_sinks(const void *q, const void *k, const void *v, int batch, int seq_len,
+                       int window, int n_sinks, int n_q_heads, int n_kv_heads, int head_dim,
+                       float scale, void *out, int32_t *err_word, attn_stream_t stream) {
+    if (n_sinks < 0) return ATTN_ERR_SHAPE;
+    return prefill(q, k, v, batch, seq_len, window, n_sinks, n_q_heads, n_kv_heads, head_dim,
+                   scale, out, err_word, stream);
+}
+
+int attn_pages_free(int32_t *block_table, int max_blocks, int table_rows, const int32_t *rows,
+                    const int32_t *from_block, const int32_t *to_block, int n, int32_t *refs,
+                    int num_pages, int32_t *err_word, attn_stream_t stream) {
+    if (int rc = check_pool(block_table, max_blocks, table_rows, refs, num_pages); rc != ATTN_OK)
+        return rc;
+    if (n < 0) return ATTN_ERR_SHAPE;
+    if (n == 0) return ATTN_OK;
+    if (!rows || !from_block || !to_block) return ATTN_ERR_NULL;
+    return gqa::launch_pages_free(block_table, max_blocks, table_rows, rows, from_block, to_block,
+                                  n, refs, num_pages, err_word,
+                                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_pages_reserve(int32_t *block_table, int max_blocks, int table_rows, const int32_t *rows,
+                       const int32_t *from_block, const int32_t *to_block, int n, int32_t *refs,
+                       int num_pages, int32_t *err_word, attn_stream_t stream) {
+    if (int rc = check_pool(block_table, max_blocks, table_rows, refs, num_pages); rc != ATTN_OK)
+        return rc;
+    if (n < 0) return ATTN_ERR_SHAPE;
+    if (n == 0) return ATTN_OK;
+    if (!rows || !from_block || !to_block) return ATTN_ERR_NULL;
+    return gqa::launch_pages_reserve(block_table, max_blocks, table_rows, rows, from_block,
+                                     to_block, n, refs, num_pages, err_word,
+                                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_pages_fork(int32_t *block_table, int max_blocks, int table_rows, const int32_t *src_rows,
+                    const int32_t *dst_rows, const int32_t *seq_lens, int n, int block_size,
+                    int32_t *refs, int num_pages, int32_t *moves, int max_moves, int32_t *n_moves,
+                    int32_t *err_word, attn_stream_t stream) {
+    if (int rc = check_pool(block_table, max_blocks, table_rows, refs, num_pages); rc != ATTN_OK)
+        return rc;
+    if (n < 0 || block_size < 1 || max_moves < n || n > (1 << 29)) return ATTN_ERR_SHAPE;
+    if (!n_moves || (n > 0 && (!src_rows || !dst_rows || !seq_lens || !moves))) return ATTN_ERR_NULL;
+    return gqa::launch_pages_fork(block_table, max_blocks, table_rows, src_rows, dst_rows,
+                                  seq_lens, n, block_size, refs, num_pages, moves, n_moves,
+                                  err_word, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t attn_pages_workspace_size(int num_pages) {
+    if (num_pages < 1 || num_pages > (1 << 30)) return (size_t)-1;
+    return gqa::pages_workspace(num_pages);
+}
+
+int attn_pages_compact(int32_t *block_table, int max_blocks, int table_rows, int block_size,
+                       int32_t *refs, int num_pages, int32_t *moves, int max_moves,
+                       int32_t *n_moves, int32_t *used, void *workspace, size_t workspace_bytes,
+                       int32_t *err_word, attn_stream_t stream) {
+    if (int rc = check_pool(block_table, max_blocks, table_rows, refs, num_pages); rc != ATTN_OK)
+        return rc;
+    if (block_size < 1 || max_moves < 0) return ATTN_ERR_SHAPE;
+    if (!n_moves || !used || !workspace || (max_moves > 0 && !moves)) return ATTN_ERR_NULL;
+    if (workspace_bytes < gqa::pages_workspace(num_pages)) return ATTN_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return ATTN_ERR_ALIGN;
+    if (max_moves > (1 << 29)) max_moves = 1 << 29;
+    return gqa::launch_pages_compact(block_table, max_blocks, table_rows, block_size, refs,
+                                     num_pages, moves, max_moves, n_moves, used, workspace,
+                                     err_word, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_pages_copy(const attn_kv_cache *caches, int n_caches, int n_kv_heads, int head_dim,
+                    const int32_t *moves, const int32_t *n_moves, int max_moves, int32_t *err_word,
+                    attn_stream_t stream) {
+    if (n_caches < 0 || max_moves < 0 || max_moves > (1 << 29) || n_kv_heads < 1)
+        return ATTN_ERR_SHAPE;
+    if (head_dim != 64 && head_dim != 128) return ATTN_ERR_UNSUPPORTED;
+    if (n_caches == 0) return ATTN_OK;
+    if (!caches) return ATTN_ERR_NULL;
+    for (int i = 0; i < n_caches; ++i) {
+        const attn_kv_cache &c = caches[i], &c0 = caches[0];
+        const bool scaled = gqa::kv_scaled(c.dtype);
+        if (c.kind != ATTN_CACHE_PAGED) return ATTN_ERR_UNSUPPORTED;
+        if (c.dtype != ATTN_KV_BF16 && c.dtype != ATTN_KV_FP8_E4M3 && !scaled)
+            return ATTN_ERR_UNSUPPORTED;
+        if (c.block_size < 1 || c.num_slots < c.block_size || c.num_slots >= (int64_t(1) << 31))
+            return ATTN_ERR_SHAPE;
+        if (int rc = check_layout(&c); rc != ATTN_OK) return rc;
+        if (!c.k || !c.v) return ATTN_ERR_NULL;
+        if (!aligned16(c.k) || !aligned16(c.v)) return ATTN_ERR_ALIGN;
+        if (scaled)
+            if (int rc = check_scaled(&c, true); rc != ATTN_OK) return rc;
+        // one launch serves all layers: they have to be laid out alike
+        if (c.dtype != c0.dtype || c.layout != c0.layout || c.block_size != c0.block_size ||
+            c.num_slots != c0.num_slots || (scaled && c.scale_block != c0.scale_block))
+            return ATTN_ERR_SHAPE;
+    }
+    // 16-byte pieces of a page are counted in 32 bits
+    if ((int64_t)caches[0].block_size * n_kv_heads * head_dim >= (int64_t(1) << 31))
+        return ATTN_ERR_SHAPE;
+    if (max_moves == 0) return ATTN_OK;
+    if (!moves || !n_moves) return ATTN_ERR_NULL;
+    return gqa::launch_pages_copy(caches, n_caches, n_kv_heads, head_dim, moves, n_moves,
+                                  max_moves, err_word, reinterpret_cast<cudaStream_t>(stream));
 }
 
 const char *attn_status_string(int status) {
@@ -346,6 +605,7 @@ const char *attn_status_string(int status) {
     case ATTN_ERR_TIMEOUT: return "a bounded device wait gave up";
     case ATTN_ERR_CUDA: return "the CUDA runtime rejected a launch";
     case ATTN_ERR_ALIGN: return "a base pointer is not 16-byte aligned";
+    case ATTN_ERR_PAGES: return "no free page left";
     default: return "unknown status";
     }
 }

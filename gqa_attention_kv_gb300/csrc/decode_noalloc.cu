@@ -115,6 +115,7 @@ extern "C" int attn_decode_noalloc(const void *q, const attn_kv_cache *cache,
                                    int n_kv_heads, int head_dim, float scale, void *out,
                                    int32_t *err_word, attn_stream_t stream) {
     // every host check first: a refused call enqueues nothing
+    if (cache && gqa::kv_scaled(cache->dtype)) return ATTN_ERR_UNSUPPORTED;
     gqa::DecodePlan plan;
     const int rc = gqa::validate_decode(q, cache, seq_lens, positions, batch, q_rows, max_seq_len,
                                         window, n_q_heads, n_kv_heads, head_dim, scale, out,

@@ -146,8 +146,57 @@ int launch_decode(const DecodePlan &plan, const void *q, const attn_kv_cache *ca
                   const int64_t *slot_mapping = nullptr, const float *rope_inv_freq = nullptr,
                   bool tables_early = false, bool cache_early = false);
 
+// Whether a cache's elements are 8-bit codes with a scale per block and head.
+inline bool kv_scaled(int dtype) {
+    return dtype == ATTN_KV_FP8_E4M3_SCALED || dtype == ATTN_KV_INT8_SCALED;
+}
+
+// Append to a scaled cache (scale_block slots and a head share a scale).
+int launch_kv_append_scaled(const void *k_new, const void *v_new, const int64_t *slot_mapping,
+                            int64_t n, const attn_kv_cache *cache, int n_kv_heads, int head_dim,
+                            int32_t *err, cudaStream_t stream);
+
+// Plan of the register-fed decode (attend.cu): scaled caches, and any cache
+// under a sliding window with sinks.  (request, row block) pairs go to the
+// kernel per_launch at a time.
+struct AttendPlan {
+    int mt;  // 0: up to 8 rows per unit, 1: 16
+    int row_blocks, entries, per_launch, grid, launches;
+    bool merge;  // units may be cut across CTAs: the merge kernel follows
+    size_t parts_offset, lse_offset, o_offset, workspace;
+};
+
+// ATTN_OK, or ATTN_ERR_SHAPE for sizes past the kernel's index range.
+int plan_attend(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads, int n_kv_heads,
+                int head_dim, int max_seq_len, int window, int sinks, AttendPlan *plan);
+
+int launch_attend(const AttendPlan &plan, const void *q, const attn_kv_cache *cache,
+                  const int32_t *seq_lens, const int32_t *positions, int q_rows, int max_seq_len,
+                  int window, int sinks, int n_q_heads, int n_kv_heads, int head_dim, float scale,
+                  void *out, void *workspace, int32_t *err, cudaStream_t stream);
+
+// Page operations (pages.cu).
+int launch_pages_free(int32_t *block_table, int max_blocks, int table_rows, const int32_t *rows,
+                      const int32_t *from_block, const int32_t *to_block, int n, int32_t *refs,
+                      int num_pages, int32_t *err, cudaStream_t stream);
+int launch_pages_reserve(int32_t *block_table, int max_blocks, int table_rows,
+                         const int32_t *rows, const int32_t *from_block, const int32_t *to_block,
+                         int n, int32_t *refs, int num_pages, int32_t *err, cudaStream_t stream);
+int launch_pages_fork(int32_t *block_table, int max_blocks, int table_rows,
+                      const int32_t *src_rows, const int32_t *dst_rows, const int32_t *seq_lens,
+                      int n, int block_size, int32_t *refs, int num_pages, int32_t *moves,
+                      int32_t *n_moves, int32_t *err, cudaStream_t stream);
+size_t pages_workspace(int num_pages);
+int launch_pages_compact(int32_t *block_table, int max_blocks, int table_rows, int block_size,
+                         int32_t *refs, int num_pages, int32_t *moves, int max_moves,
+                         int32_t *n_moves, int32_t *used, void *workspace, int32_t *err,
+                         cudaStream_t stream);
+int launch_pages_copy(const attn_kv_cache *caches, int n_caches, int n_kv_heads, int head_dim,
+                      const int32_t *moves, const int32_t *n_moves, int max_moves, int32_t *err,
+                      cudaStream_t stream);
+
 int launch_prefill(const void *q, const void *k, const void *v, int batch, int seq_len,
                    int window, int n_q_heads, int n_kv_heads, int head_dim, float scale,
-                   void *out, int32_t *err, cudaStream_t stream);
+                   void *out, int32_t *err, cudaStream_t stream, int sinks = 0);
 
 }  // namespace gqa

@@ -90,9 +90,19 @@ struct Params {
     int single;   // 1: one Q tile per CTA (the second tile is absent)
     float scale_log2;
     int32_t *err;
+    int sinks;  // first keys that stay visible outside the window
 };
 
-template <int HD>
+// NaN if either operand is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// SINKS: the first p.sinks keys are visible to every later row, whatever the
+// window (a sliding window with sinks): their tiles come before the window's.
+template <int HD, bool SINKS>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -130,13 +140,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int key_hi = min(p.seq_len, q0 + rows);  // exclusive
     const int key_lo = p.window > 0 ? max(0, q0 - p.window + 1) : 0;
     const int kt0 = key_lo / kBN;
-    const int n_kt = (key_hi + kBN - 1) / kBN - kt0;
+    // tiles of sinks before the window's first
+    const int n_sink = SINKS ? min(kt0, (p.sinks + kBN - 1) / kBN) : 0;
+    const int n_kt = (key_hi + kBN - 1) / kBN - kt0 + n_sink;
     // The G heads of a KV group read the same K/V tiles; each starts its walk
     // over them at a different tile (the order of the tiles does not change
     // the result of the online softmax), so the CTAs resident at one time do
     // not all ask L2 for the same lines at once.
     const int rot = n_kt > 0 ? (int)(((int64_t)(h % p.group) * n_kt) / p.group) : 0;
-    auto tile_of = [&](int j) { const int t = j + rot; return kt0 + (t >= n_kt ? t - n_kt : t); };
+    auto tile_of = [&](int j) {
+        int t = j + rot;
+        t = t >= n_kt ? t - n_kt : t;
+        if constexpr (SINKS) return t < n_sink ? t : kt0 + t - n_sink;
+        return kt0 + t;
+    };
     // Tile j is dead for query tile a when no row of a may see any of its
     // keys: all keys after a's last row, all before the window of a's first
     // row, or a's rows all past the sequence.  Its S and P V are never
@@ -144,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto live = [&](int a, int j) -> bool {
         const int qa = q0 + a * kBM, key0 = tile_of(j) * kBN;
         return (a == 0 || !p.single) && qa < p.seq_len && key0 <= qa + kBM - 1 &&
-               (p.window <= 0 || qa - (key0 + kBN - 1) < p.window);
+               (p.window <= 0 || qa - (key0 + kBN - 1) < p.window || (SINKS && key0 < p.sinks));
     };
 
     // The next kernel may start its own prologue on SMs this grid leaves
@@ -324,8 +341,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Each V tile is rewritten in place, bf16 -> f16 (exact for
         // magnitudes in [2^-14, 2^16); below that f16 keeps 2^-24 absolute
         // precision).  A magnitude of 2^16 or more has no f16: it saturates to
-        // 65504 and the error word gets ATTN_ERR_UNSUPPORTED.  The writes are
-        // made visible to the tensor core's proxy before the arrive.
+        // 65504 and the error word gets ATTN_ERR_UNSUPPORTED (with sinks a NaN
+        // does too, and becomes 0: 0 times it would reach the rows that do not
+        // see its key).  The writes are made visible to the tensor core's proxy before the arrive.
         const int ct = threadIdx.x - 64;  // 0 .. 63
         int vst = 0, vph = 0;
         bool ok = true;
@@ -343,12 +361,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int e = 0; e < 4; ++e) {
                     const float x0 = __uint_as_float(u[e] << 16);
                     const float x1 = __uint_as_float(u[e] & 0xFFFF0000u);
-                    amax = max3(amax, fabsf(x0), fabsf(x1));
+                    if constexpr (SINKS)
+                        amax = max_nan(amax, max_nan(fabsf(x0), fabsf(x1)));
+                    else
+                        amax = max3(amax, fabsf(x0), fabsf(x1));
                     u[e] = pack_f16x2_sat(x0, x1);
                 }
                 st_shared_v4(base + i * 16, w);
             }
             if (!(amax < 65536.f)) report_error(p.err, ATTN_ERR_UNSUPPORTED);
+            if (SINKS && amax != amax) {  // this thread's pieces hold a NaN
+                for (int i = ct; i < C::kVBytes / 16; i += 64) {
+                    uint4 w = ld_shared_v4(base + i * 16);
+                    uint32_t *u = &w.x;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if ((u[e] & 0x7FFFu) > 0x7C00u) u[e] &= 0xFFFF0000u;
+                        if ((u[e] & 0x7FFF0000u) > 0x7C000000u) u[e] &= 0xFFFFu;
+                    }
+                    st_shared_v4(base + i * 16, w);
+                }
+            }
             fence_proxy_async_smem();
             mbar_arrive(&v_conv[vst]);
             if (++vst == C::kVStages) {
@@ -389,15 +422,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int key0 = tile_of(j) * kBN;
             const bool needs_mask =
-                key0 + kBN - 1 > qa0 || (p.window > 0 && qa0 + kBM - 1 - key0 >= p.window);
+                key0 + kBN - 1 > qa0 || (p.window > 0 && qa0 + kBM - 1 - key0 >= p.window &&
+                                         !(SINKS && key0 + kBN <= p.sinks));
             if (needs_mask) {
                 // row sees columns lo <= c <= hi (c = key - key0): per element
                 // one compare with an immediate (two with a window) and a select
                 const int hi = qa0 + row - key0;
                 if (p.window > 0) {
                     const int lo = hi - p.window + 1;
+                    if constexpr (SINKS) {
+                        // or one of the sinks c < first
+                        const int first = min(p.sinks - key0, hi + 1);
 #pragma unroll
-                    for (int c = 0; c < kBN; ++c) s[c] = (c <= hi && c >= lo) ? s[c] : -INFINITY;
+                        for (int c = 0; c < kBN; ++c)
+                            s[c] = ((c <= hi && c >= lo) || c < first) ? s[c] : -INFINITY;
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < kBN; ++c)
+                            s[c] = (c <= hi && c >= lo) ? s[c] : -INFINITY;
+                    }
                 } else {
 #pragma unroll
                     for (int c = 0; c < kBN; ++c) s[c] = c <= hi ? s[c] : -INFINITY;
@@ -508,10 +551,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int HD>
+template <int HD, bool SINKS>
 int launch(const Params &p, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
            const CUtensorMap &to, cudaStream_t stream) {
-    auto kern = prefill_kernel<HD>;
+    auto kern = prefill_kernel<HD, SINKS>;
     static int configured_device = -1;
     int dev = 0;
     cudaGetDevice(&dev);
@@ -535,8 +578,9 @@ int launch(const Params &p, const CUtensorMap &tq, const CUtensorMap &tk, const 
 
 int launch_prefill(const void *q, const void *k, const void *v, int batch, int seq_len,
                    int window, int n_q_heads, int n_kv_heads, int head_dim, float scale,
-                   void *out, int32_t *err, cudaStream_t stream) {
+                   void *out, int32_t *err, cudaStream_t stream, int sinks) {
     pre::Params p;
+    p.sinks = window > 0 && sinks > 0 ? (sinks < seq_len ? sinks : seq_len) : 0;
     p.batch = batch;
     p.seq_len = seq_len;
     p.window = window;
@@ -567,8 +611,11 @@ int launch_prefill(const void *q, const void *k, const void *v, int batch, int s
         !encode_tensor_map(&tv, v, 3, dk, sk, box, true) ||
         !encode_tensor_map(&to, out, 3, dq, sq, box, true))
         return ATTN_ERR_CUDA;
-    return head_dim == 128 ? pre::launch<128>(p, tq, tk, tv, to, stream)
-                           : pre::launch<64>(p, tq, tk, tv, to, stream);
+    if (p.sinks > 0)
+        return head_dim == 128 ? pre::launch<128, true>(p, tq, tk, tv, to, stream)
+                               : pre::launch<64, true>(p, tq, tk, tv, to, stream);
+    return head_dim == 128 ? pre::launch<128, false>(p, tq, tk, tv, to, stream)
+                           : pre::launch<64, false>(p, tq, tk, tv, to, stream);
 }
 
 }  // namespace gqa

@@ -1,7 +1,7 @@
 /*
  * attn_kv.h -- C ABI of the GB300 grouped-query attention library.
  *
- * Three operations on one decoder KV cache, each a few kernel launches on the
+ * Operations on one decoder KV cache, each a few kernel launches on the
  * caller's stream:
  *
  *   attn_kv_append  write new K/V rows into the cache slots a slot_mapping names
@@ -10,6 +10,14 @@
  *                   cache, as a split-KV flash-decode plus a merge of the
  *                   partial softmax states
  *   attn_prefill    causal (optionally windowed) GQA prefill attention
+ *   attn_decode_sinks, attn_prefill_sinks
+ *                   the same under a sliding window whose first few tokens
+ *                   (sinks) stay visible
+ *   attn_pages_*    pages of a paged cache: reserved, freed, forked, compacted
+ *                   and copied on the device
+ *
+ * Append and decode also take caches of 8-bit codes with a scale for each
+ * block of tokens and head.
  *
  * Sources for the operations (cited by page title and section):
  *   - vibevoice.c, "The kernels that matter", "Attention backends", "Paged KV
@@ -68,7 +76,8 @@ typedef enum {
     ATTN_ERR_BOUNDS = 5,      /* device: slot / page / position outside its buffer */
     ATTN_ERR_TIMEOUT = 6,     /* device: a bounded wait gave up */
     ATTN_ERR_CUDA = 7,        /* the CUDA runtime rejected a launch */
-    ATTN_ERR_ALIGN = 8        /* a base pointer is not 16-byte aligned */
+    ATTN_ERR_ALIGN = 8,       /* a base pointer is not 16-byte aligned */
+    ATTN_ERR_PAGES = 9        /* device: no free page left */
 } attn_status;
 
 typedef enum {
@@ -84,7 +93,9 @@ typedef enum {
 
 typedef enum {
     ATTN_KV_BF16 = 0,    /* 16-bit bf16 elements */
-    ATTN_KV_FP8_E4M3 = 1 /* 8-bit E4M3 elements, K stored relative to k_ref */
+    ATTN_KV_FP8_E4M3 = 1, /* 8-bit E4M3 elements, K stored relative to k_ref */
+    ATTN_KV_FP8_E4M3_SCALED = 2, /* E4M3 codes with a scale per block of tokens and head */
+    ATTN_KV_INT8_SCALED = 3      /* signed 8-bit codes with a scale per block and head */
 } attn_kv_dtype;
 
 /*
@@ -124,6 +135,34 @@ typedef enum {
  * the slot-major layout; only the placement differs, so one KV head's keys of
  * a block are contiguous.  num_slots must be a multiple of rows.
  * A zero-initialised struct is a bf16, slot-major cache.
+ *
+ * dtypes ATTN_KV_FP8_E4M3_SCALED and ATTN_KV_INT8_SCALED: each element is one
+ * byte, an E4M3 code or a signed integer in -127 .. 127, and scale_block
+ * consecutive slots (16, 32, 64 or 128) share one float32 scale per KV head:
+ *     key   = code * k_scale[slot / scale_block][head]   (less k_ref, as above)
+ *     value = code * v_scale[slot / scale_block][head]
+ * A request's slots (LINEAR) or a page (PAGED) hold whole blocks: slots_per_seq
+ * or block_size, and num_slots, are multiples of scale_block.  RING caches are
+ * not supported: a block begun anew would take the scale of tokens that are
+ * still visible with it.  head_dim 64 or 128, both layouts.  The last three
+ * fields of the struct are read for these dtypes only.
+ *
+ * attn_kv_append keeps the scales.  For each block and head, with x the call's
+ * rows of that block (K less k_ref) and qmax = 448 (E4M3) or 127 (INT8):
+ *     a  = the largest finite |x|
+ *     s' = max(s, a / qmax, 2^-64),  s = the scale held, or 0 when the call
+ *          writes the block's first slot (the block starts anew)
+ *     r  = 1 / s';  a new row's codes are round(x * r); when s' > s > 0 the
+ *          block's other codes become round(code * (s * r))
+ * a / qmax, r and s * r are rounded to float32.  E4M3 rounds the float32
+ * product to nearest even, saturating at 448 (an infinity too; a NaN stays
+ * one); INT8 rounds the exact product to nearest even, saturating at 127, and
+ * a NaN becomes 0 with ATTN_ERR_UNSUPPORTED in *err_word.  A block's scale only
+ * grows until it starts anew, so no stored value is ever clipped by a later
+ * one; rows that are not written keep their codes when the scale keeps its
+ * value.  In one call the rows of a block must stand next to each other in
+ * slot_mapping (in any order; rows with a slot outside the cache do not count):
+ * rows of one block at separate places leave its codes and scales unspecified.
  */
 typedef struct {
     int32_t kind;               /* attn_cache_kind */
@@ -137,6 +176,9 @@ typedef struct {
     int32_t dtype;              /* attn_kv_dtype */
     const float *k_ref;         /* FP8 only: float32 [n_kv_heads, head_dim], device, or NULL */
     int32_t layout;             /* attn_kv_layout */
+    float *k_scale;             /* scaled dtypes: float32 [num_slots / scale_block, n_kv_heads] */
+    float *v_scale;             /* likewise */
+    int32_t scale_block;        /* scaled dtypes: slots that share a scale */
 } attn_kv_cache;
 
 /*
@@ -254,6 +296,12 @@ int attn_decode_kernel_launches(const attn_kv_cache *cache, int batch, int q_row
  *   and values to f16 (exact), takes q in f16 (|q| must stay below 65504;
  *   magnitudes under 2^-14 lose precision) and the softmax weights in f16,
  *   and accumulates in fp32.
+ *   A scaled cache is read as stored too: codes convert to f16 exactly, q is
+ *   taken in f16 (a magnitude of 65520 or more is reported as
+ *   ATTN_ERR_UNSUPPORTED), the scales multiply scores and softmax weights in
+ *   float32, and the weights are rounded once to f16.  A scale is finite and at
+ *   least 2^-64 (a v_scale below reads as 2^-64).  Its workspace needs no
+ *   zeroing, and keeps out of the counters of the other caches' calls.
  *   A group of 64 or more query rows (q_rows x n_q_heads / n_kv_heads) over a
  *   linear slot-major bf16 cache is a prefill chunk and computes as
  *   attn_prefill does: P V from f16 softmax weights and f16 values, with the
@@ -315,6 +363,9 @@ int attn_decode(const void *q, const attn_kv_cache *cache, const int32_t *seq_le
  *   An FP8 cache receives the rows encoded exactly as attn_kv_append encodes
  *   them (K minus k_ref), and the decode reads those codes; rope_inv_freq must
  *   then be NULL (ATTN_ERR_UNSUPPORTED otherwise).
+ *   A scaled cache is appended to by a launch of its own before the decode's
+ *   (a new row may change the scale of its block): the result is that of the
+ *   two calls, flags change nothing, and rope_inv_freq must be NULL.
  */
 #define ATTN_DECODE_TABLES_EARLY 1u
 #define ATTN_DECODE_CACHE_EARLY 2u
@@ -338,6 +389,7 @@ int attn_decode_append(const void *q, const void *k_new, const void *v_new,
  * ATTN_DECODE_NOALLOC_SCRATCH_BYTES inside the library, present on every GPU
  * that loads the library until the process exits.  Nothing is allocated.
  *
+ *   Scaled caches are not supported (ATTN_ERR_UNSUPPORTED).
  *   Returns ATTN_ERR_WORKSPACE, before any launch, when
  *   attn_decode_workspace_size(...) for these arguments exceeds that size;
  *   otherwise the same statuses as attn_decode, every host check made before
@@ -384,6 +436,116 @@ int attn_decode_noalloc(const void *q, const attn_kv_cache *cache, const int32_t
 int attn_prefill(const void *q, const void *k, const void *v, int batch, int seq_len, int window,
                  int n_q_heads, int n_kv_heads, int head_dim, float scale, void *out,
                  int32_t *err_word, attn_stream_t stream);
+
+/*
+ * attn_decode_sinks -- attn_decode under a sliding window whose first n_sinks
+ * tokens stay visible.  The pages have no counterpart to it.
+ *
+ *   Row (b, r) at position pos attends key position t iff
+ *       0 <= t < seq_lens[b],  t <= pos,  and
+ *       t < n_sinks  or  window <= 0  or  pos - t < window.
+ *   n_sinks >= 0; 0 leaves the plain window.  Keys between the sinks and the
+ *   window of a request's earliest row are not read, and a PAGED cache's table
+ *   entries for pages that hold only such keys are not either: those pages may
+ *   be given back (attn_pages_free).
+ *   RING: the sinks keep their slots and the rest of the ring turns: position t
+ *   of request b lives in slot b*R + t for t < n_sinks, else in
+ *       b*R + n_sinks + (t - n_sinks) % (R - n_sinks),  R = slots_per_seq;
+ *   R - n_sinks >= window + q_rows - 1.  With n_sinks 0 that is the plain ring.
+ *   Every cache dtype, kind and layout that attn_decode takes (unscaled FP8 at
+ *   head_dim 128).  A position below 0 marks a row without keys (zeros).  A
+ *   value that is not finite reaches only the rows that attend its key.
+ *   workspace: at least attn_decode_sinks_workspace_size(...) bytes (which
+ *   returns (size_t)-1 for arguments this call would reject), 16-byte aligned;
+ *   it needs no zeroing, and one workspace may serve this call and attn_decode.
+ *   Calls whose kernels overlap on the GPU, graphs replayed at the same time
+ *   among them, need separate workspaces.
+ *   Every other argument and status is attn_decode's.
+ */
+size_t attn_decode_sinks_workspace_size(const attn_kv_cache *cache, int batch, int q_rows,
+                                        int n_q_heads, int n_kv_heads, int head_dim,
+                                        int max_seq_len, int window, int n_sinks);
+int attn_decode_sinks(const void *q, const attn_kv_cache *cache, const int32_t *seq_lens,
+                      const int32_t *positions, int batch, int q_rows, int max_seq_len, int window,
+                      int n_sinks, int n_q_heads, int n_kv_heads, int head_dim, float scale,
+                      void *out, void *workspace, size_t workspace_bytes, int32_t *err_word,
+                      attn_stream_t stream);
+
+/*
+ * attn_prefill_sinks -- attn_prefill under a sliding window whose first n_sinks
+ * tokens of each sequence stay visible: query i attends key t <= i with
+ * t < n_sinks, window <= 0 or i - t < window.  n_sinks >= 0.  Every other
+ * argument and the arithmetic are attn_prefill's, but that a NaN in v is
+ * reported like a magnitude without an f16 (ATTN_ERR_UNSUPPORTED) and taken
+ * as 0 when n_sinks > 0 and window > 0.
+ */
+int attn_prefill_sinks(const void *q, const void *k, const void *v, int batch, int seq_len,
+                       int window, int n_sinks, int n_q_heads, int n_kv_heads, int head_dim,
+                       float scale, void *out, int32_t *err_word, attn_stream_t stream);
+
+/*
+ * attn_pages_* -- pages of a paged cache (vibevoice.c, "Paged KV cache": pages
+ * of a pool named by a device-side table), kept on the device.
+ *
+ *   block_table  int32 [table_rows, max_blocks], device: page ids, -1 where a
+ *                row has no page
+ *   refs         int32 [num_pages], device: how many table entries name a page;
+ *                0 is a free page.  One table and one pool serve all layers.
+ *   rows ...     int32 [n], device: the table rows a call works on
+ *   moves        int32 [max_moves, 3], device: (source page, destination page,
+ *                rows to copy), n_moves (int32, device) of them; entries past
+ *                *n_moves are left as they were
+ * Free pages are handed out lowest first, so results do not depend on timing.
+ * A row, length or page outside its array skips what it names and stores
+ * ATTN_ERR_BOUNDS in *err_word.  block_table, refs and workspace must be
+ * 16-byte aligned.  Calls on one table or pool must be ordered (one stream, or
+ * events).  All may be captured into graphs.
+ *
+ * attn_pages_free     entries from_block[i] .. to_block[i] - 1 of row rows[i]
+ *   (clipped to the row) give back their page and become -1; entries that are
+ *   -1 already are skipped.  A whole request is freed with 0 .. max_blocks; the
+ *   pages that a window with sinks has left behind with
+ *   ceil(n_sinks / block_size) .. floor((first visible position) / block_size).
+ * attn_pages_reserve  entries from_block[i] .. to_block[i] - 1 of row rows[i]
+ *   that are -1 take free pages, in the order of i and then of the entry.
+ *   Entries for which no page is left stay -1 (ATTN_ERR_PAGES).  Rows distinct.
+ * attn_pages_fork     row dst_rows[i] becomes the first seq_lens[i] tokens of
+ *   row src_rows[i]: full pages are shared (-1 entries stay -1), a partial last
+ *   page is replaced by a free page that the moves copy its rows to, entries
+ *   behind are -1.  The destination rows' old entries are not given back (free
+ *   them first).  Destinations are distinct and none is a source.  Where no page is
+ *   left for a partial one its entry is -1 (ATTN_ERR_PAGES).  max_moves >= n.
+ *   Carry the moves out (attn_pages_copy) before either row is written to.
+ * attn_pages_compact  with U pages in use (*used, int32, device), the i-th
+ *   page in use at or above U (ascending) moves to the i-th free page below U:
+ *   refs and every entry of the table follow, and the moves copy whole pages.
+ *   max_moves >= the pages that move (at most num_pages / 2): past it no page
+ *   moves, and ATTN_ERR_WORKSPACE is stored in *err_word.  A source page's
+ *   rows stay readable until its new owner writes them.
+ *   workspace: attn_pages_workspace_size(num_pages) bytes, no zeroing.
+ * attn_pages_copy     carries the moves out in n_caches caches (K, V and, for
+ *   scaled dtypes, the scales of the rows' blocks): PAGED caches alike in
+ *   dtype, layout and sizes, one per layer.  No page may be the destination of
+ *   two moves, nor the source of one and the destination of another.
+ */
+int attn_pages_free(int32_t *block_table, int max_blocks, int table_rows, const int32_t *rows,
+                    const int32_t *from_block, const int32_t *to_block, int n, int32_t *refs,
+                    int num_pages, int32_t *err_word, attn_stream_t stream);
+int attn_pages_reserve(int32_t *block_table, int max_blocks, int table_rows, const int32_t *rows,
+                       const int32_t *from_block, const int32_t *to_block, int n, int32_t *refs,
+                       int num_pages, int32_t *err_word, attn_stream_t stream);
+int attn_pages_fork(int32_t *block_table, int max_blocks, int table_rows, const int32_t *src_rows,
+                    const int32_t *dst_rows, const int32_t *seq_lens, int n, int block_size,
+                    int32_t *refs, int num_pages, int32_t *moves, int max_moves, int32_t *n_moves,
+                    int32_t *err_word, attn_stream_t stream);
+size_t attn_pages_workspace_size(int num_pages);
+int attn_pages_compact(int32_t *block_table, int max_blocks, int table_rows, int block_size,
+                       int32_t *refs, int num_pages, int32_t *moves, int max_moves,
+                       int32_t *n_moves, int32_t *used, void *workspace, size_t workspace_bytes,
+                       int32_t *err_word, attn_stream_t stream);
+int attn_pages_copy(const attn_kv_cache *caches, int n_caches, int n_kv_heads, int head_dim,
+                    const int32_t *moves, const int32_t *n_moves, int max_moves, int32_t *err_word,
+                    attn_stream_t stream);
 
 /* Human-readable name of an attn_status. */
 const char *attn_status_string(int status);

@@ -1,0 +1,167 @@
+"""Refusals of the scaled caches, the windows with sinks and the page
+operations: made on the host, before any launch, so they need no GPU."""
+import ctypes
+
+import pytest
+
+import gqa_attention_kv_gb300 as gq
+from test_capi_host import FakeTensor, lib  # noqa: F401
+
+E4, I8 = gq.ATTN_KV_FP8_E4M3_SCALED, gq.ATTN_KV_INT8_SCALED
+BIG = 1 << 30
+
+
+def cache(kind=gq.LINEAR, dtype=E4, slots=1024, sps=512, bs=0, sb=16, D=128, Hkv=8, ks=4096,
+          vs=8192, layout=gq.ATTN_LAYOUT_BSHD, blocks=64, k=4096, v=8192, ref=None):
+    per = bs if kind == gq.PAGED else sps
+    shape = (slots, Hkv, D) if layout == gq.ATTN_LAYOUT_BSHD else (slots // per, Hkv, per, D)
+    fake = lambda a: None if a is None else FakeTensor(a, (1,))  # noqa: E731
+    return gq.KVCache(kind, FakeTensor(k, shape), FakeTensor(v, shape), slots_per_seq=sps,
+                      block_table=FakeTensor(1 << 20, (2, blocks)) if kind == gq.PAGED else None,
+                      block_size=bs, dtype=dtype, layout=layout, k_scale=fake(ks),
+                      v_scale=fake(vs), scale_block=sb, k_ref=fake(ref))
+
+
+def append_rc(lib, c, n=4, D=128):
+    return lib.attn_kv_append(16, 32, 64, n, ctypes.byref(c.struct()), 8, D, None, None)
+
+
+def decode_rc(lib, c, W=0, S=None, B=2, R=1, L=512, D=128, ws=1 << 20, ws_bytes=BIG, scale=0.1):
+    cs = c.struct()
+    if S is None:
+        return lib.attn_decode(16, ctypes.byref(cs), 64, 128, B, R, L, W, 32, 8, D, scale, 32, ws,
+                               ws_bytes, None, None)
+    return lib.attn_decode_sinks(16, ctypes.byref(cs), 64, 128, B, R, L, W, S, 32, 8, D, scale, 32,
+                                 ws, ws_bytes, None, None)
+
+
+@pytest.mark.parametrize("dtype", [E4, I8])
+def test_scaled_cache_refusals(lib, dtype):  # noqa: F811
+    for rc in (append_rc, decode_rc):
+        assert rc(lib, cache(dtype=dtype, sb=24)) == gq.ATTN_ERR_UNSUPPORTED
+        assert rc(lib, cache(dtype=dtype, sb=0)) == gq.ATTN_ERR_UNSUPPORTED
+        assert rc(lib, cache(dtype=dtype, sb=256)) == gq.ATTN_ERR_UNSUPPORTED
+        # whole blocks in a request's slots, a page and the cache
+        assert rc(lib, cache(dtype=dtype, sps=504)) == gq.ATTN_ERR_SHAPE
+        assert rc(lib, cache(gq.PAGED, dtype, sps=0, bs=8)) == gq.ATTN_ERR_SHAPE
+        assert rc(lib, cache(gq.PAGED, dtype, sps=0, bs=16, sb=32)) == gq.ATTN_ERR_SHAPE
+        assert rc(lib, cache(dtype=dtype, slots=1032)) == gq.ATTN_ERR_SHAPE
+        assert rc(lib, cache(dtype=dtype, ks=None)) == gq.ATTN_ERR_NULL
+        assert rc(lib, cache(dtype=dtype, vs=None)) == gq.ATTN_ERR_NULL
+        assert rc(lib, cache(dtype=dtype, vs=8196)) == gq.ATTN_ERR_ALIGN
+        assert rc(lib, cache(dtype=dtype, k=4100)) == gq.ATTN_ERR_ALIGN
+        assert rc(lib, cache(dtype=dtype), D=96) == gq.ATTN_ERR_UNSUPPORTED
+    assert append_rc(lib, cache(dtype=dtype, ref=4100)) == gq.ATTN_ERR_ALIGN
+    ring = cache(gq.RING, dtype)
+    assert append_rc(lib, ring) == gq.ATTN_ERR_UNSUPPORTED
+    assert decode_rc(lib, ring, W=64) == gq.ATTN_ERR_UNSUPPORTED
+    assert append_rc(lib, cache(dtype=dtype), n=0) == gq.ATTN_OK
+    assert append_rc(lib, cache(dtype=4)) == gq.ATTN_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("dtype", [E4, I8])
+def test_scaled_decode_refusals(lib, dtype):  # noqa: F811
+    c = cache(dtype=dtype)
+    cs = c.struct()
+    need = lib.attn_decode_workspace_size(ctypes.byref(cs), 2, 1, 32, 8, 128, 512, 0)
+    assert 0 < need < BIG
+    assert decode_rc(lib, c, ws=None, ws_bytes=0) == gq.ATTN_ERR_NULL
+    assert decode_rc(lib, c, ws_bytes=need - 1) == gq.ATTN_ERR_WORKSPACE
+    assert decode_rc(lib, c, ws=(1 << 20) + 8) == gq.ATTN_ERR_ALIGN
+    assert decode_rc(lib, c, scale=float("nan")) == gq.ATTN_ERR_SHAPE
+    assert decode_rc(lib, c, B=0) == gq.ATTN_OK
+    args = (2, 1, 512, 0, 32, 8, 128, 0.1, 32)
+    assert lib.attn_decode_noalloc(16, ctypes.byref(cs), 64, 128, *args, None,
+                                   None) == gq.ATTN_ERR_UNSUPPORTED
+    # the fused step: no rotary embedding, a workspace before anything is appended
+    step = lambda rope, ws: lib.attn_decode_append(  # noqa: E731
+        16, 32, 48, 64, rope, ctypes.byref(cs), 64, 128, *args, ws, BIG, None, 0, None)
+    assert step(4096, 1 << 20) == gq.ATTN_ERR_UNSUPPORTED
+    assert step(None, None) == gq.ATTN_ERR_NULL
+    assert gq.attn_decode_kernel_launches(c, 2, 1, 32, 512) == 2
+    assert gq.attn_decode_kernel_launches(c, 2, 1, 32, 512, with_append=True) == 3
+    with pytest.raises(gq.AttnError):
+        gq.attn_decode_kernel_launches(c, 2, 1, 32, 512, with_append=True, with_rope=True)
+
+
+def test_sinks_refusals(lib):  # noqa: F811
+    bf = lambda kind=gq.LINEAR, **kw: cache(kind, gq.ATTN_KV_BF16, **kw)  # noqa: E731
+    assert decode_rc(lib, bf(), W=64, S=-1) == gq.ATTN_ERR_SHAPE
+    # a ring holds the sinks beside the window
+    assert decode_rc(lib, bf(gq.RING), W=500, S=13) == gq.ATTN_ERR_SHAPE
+    assert decode_rc(lib, bf(gq.RING), W=500, S=12, R=2) == gq.ATTN_ERR_SHAPE
+    assert decode_rc(lib, bf(gq.RING), W=500, S=12, ws_bytes=8) == gq.ATTN_ERR_WORKSPACE
+    assert decode_rc(lib, bf(gq.RING), W=0, S=4) == gq.ATTN_ERR_SHAPE
+    assert decode_rc(lib, bf(), W=64, S=4, ws=None) == gq.ATTN_ERR_NULL
+    assert decode_rc(lib, bf(), W=64, S=4, D=96) == gq.ATTN_ERR_UNSUPPORTED
+    assert decode_rc(lib, bf(), W=64, S=4, scale=-1.0) == gq.ATTN_ERR_SHAPE
+    assert decode_rc(lib, bf(), W=64, S=4, L=0) == gq.ATTN_ERR_SHAPE
+    assert decode_rc(lib, bf(gq.PAGED, sps=0, bs=8, blocks=8), W=64, S=4) == gq.ATTN_ERR_SHAPE
+    assert decode_rc(lib, cache(dtype=gq.ATTN_KV_FP8_E4M3, D=64), W=8, S=1,
+                     D=64) == gq.ATTN_ERR_UNSUPPORTED
+    assert decode_rc(lib, cache(gq.RING, I8), W=64, S=4) == gq.ATTN_ERR_UNSUPPORTED
+    cs = bf().struct()
+    size = lib.attn_decode_sinks_workspace_size
+    assert size(ctypes.byref(cs), 2, 1, 32, 8, 128, 512, 64, -1) == ctypes.c_size_t(-1).value
+    assert size(ctypes.byref(cs), 0, 1, 32, 8, 128, 512, 64, 4) == 0
+    pre = lambda S, Hq=8, q=16: lib.attn_prefill_sinks(  # noqa: E731
+        q, 32, 48, 1, 64, 16, S, Hq, 4, 64, 0.1, 64, None, None)
+    assert pre(-1) == gq.ATTN_ERR_SHAPE
+    assert pre(4, Hq=6) == gq.ATTN_ERR_SHAPE
+    assert pre(4, q=None) == gq.ATTN_ERR_NULL
+    assert pre(4, q=24) == gq.ATTN_ERR_ALIGN
+
+
+def test_page_operation_refusals(lib):  # noqa: F811
+    for f in (lib.attn_pages_free, lib.attn_pages_reserve):
+        assert f(16, 8, 4, 4, 4, 4, 2, None, 64, None, None) == gq.ATTN_ERR_NULL
+        assert f(None, 8, 4, 4, 4, 4, 2, 16, 64, None, None) == gq.ATTN_ERR_NULL
+        assert f(16, 0, 4, 4, 4, 4, 2, 16, 64, None, None) == gq.ATTN_ERR_SHAPE
+        assert f(16, 8, 4, 4, 4, 4, -1, 16, 64, None, None) == gq.ATTN_ERR_SHAPE
+        assert f(16, 8, 4, 4, 4, 4, 2, 16, 0, None, None) == gq.ATTN_ERR_SHAPE
+        assert f(16, 8, 4, None, 4, 4, 2, 16, 64, None, None) == gq.ATTN_ERR_NULL
+        assert f(16, 8, 4, 4, 4, 4, 2, 20, 64, None, None) == gq.ATTN_ERR_ALIGN
+        assert f(16, 8, 4, None, None, None, 0, 16, 64, None, None) == gq.ATTN_OK
+    fork = lambda n=2, bs=16, most=2, moves=16, count=16: lib.attn_pages_fork(  # noqa: E731
+        16, 8, 4, 4, 4, 4, n, bs, 16, 64, moves, most, count, None, None)
+    assert fork(n=-1) == gq.ATTN_ERR_SHAPE
+    assert fork(bs=0) == gq.ATTN_ERR_SHAPE
+    assert fork(most=1) == gq.ATTN_ERR_SHAPE
+    assert fork(moves=None) == gq.ATTN_ERR_NULL
+    assert fork(count=None) == gq.ATTN_ERR_NULL
+    need = lib.attn_pages_workspace_size(64)
+    assert lib.attn_pages_workspace_size(0) == ctypes.c_size_t(-1).value
+    compact = lambda bs=16, most=2, moves=16, used=16, ws=16, size=need: (  # noqa: E731
+        lib.attn_pages_compact(16, 8, 4, bs, 16, 64, moves, most, 16, used, ws, size, None, None))
+    assert compact(bs=0) == gq.ATTN_ERR_SHAPE
+    assert compact(most=-1) == gq.ATTN_ERR_SHAPE
+    assert compact(moves=None) == gq.ATTN_ERR_NULL
+    assert compact(used=None) == gq.ATTN_ERR_NULL
+    assert compact(ws=None) == gq.ATTN_ERR_NULL
+    assert compact(size=need - 1) == gq.ATTN_ERR_WORKSPACE
+    assert compact(ws=24) == gq.ATTN_ERR_ALIGN
+
+
+def test_page_copy_refusals(lib):  # noqa: F811
+    def rc(caches, D=128, moves=16, count=16, most=4, n=None):
+        arr = (gq._Cache * len(caches))(*[c.struct() for c in caches])
+        return lib.attn_pages_copy(arr, len(caches) if n is None else n, 8, D, moves, count, most,
+                                   None, None)
+
+    paged = lambda **kw: cache(gq.PAGED, kw.pop("dtype", I8), sps=0, bs=kw.pop("bs", 32),  # noqa: E731
+                               **kw)
+    assert rc([cache()]) == gq.ATTN_ERR_UNSUPPORTED                  # not paged
+    assert rc([paged()], D=80) == gq.ATTN_ERR_UNSUPPORTED
+    assert rc([paged(dtype=9)]) == gq.ATTN_ERR_UNSUPPORTED
+    assert rc([paged(ks=None)]) == gq.ATTN_ERR_NULL
+    assert rc([paged(k=20)]) == gq.ATTN_ERR_ALIGN
+    assert rc([paged(), paged(bs=64)]) == gq.ATTN_ERR_SHAPE          # layers alike
+    assert rc([paged(), paged(dtype=E4)]) == gq.ATTN_ERR_SHAPE
+    assert rc([paged(), paged(sb=32)]) == gq.ATTN_ERR_SHAPE
+    assert rc([paged(), paged(slots=2048)]) == gq.ATTN_ERR_SHAPE
+    assert rc([paged()], moves=None) == gq.ATTN_ERR_NULL
+    assert rc([paged()], count=None) == gq.ATTN_ERR_NULL
+    assert rc([paged()], most=-1) == gq.ATTN_ERR_SHAPE
+    assert rc([paged()], most=0) == gq.ATTN_OK
+    assert rc([paged()], n=0) == gq.ATTN_OK
+    assert "free page" in gq.attn_status_string(gq.ATTN_ERR_PAGES)
