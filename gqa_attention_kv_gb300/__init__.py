@@ -57,6 +57,8 @@ class _Cache(ctypes.Structure):
 def lib():
     """The loaded library (ctypes.CDLL).  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -126,17 +128,20 @@ def attn_version() -> str:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
     if stream is None:
         import torch
 
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        try:  # the current stream's handle without a Stream object around it (3 us a call)
+            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        except AttributeError:
+            return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
 def _check(rc, where):
@@ -189,7 +194,9 @@ class KVCache:
 
     def struct(self) -> _Cache:
         bt = self.block_table
-        return _Cache(self.kind, self.k.data_ptr(), self.v.data_ptr(), self.num_slots,
+        shape = self.k.shape
+        slots = shape[0] * (shape[2] if self.layout == ATTN_LAYOUT_BHSD else 1)
+        return _Cache(self.kind, self.k.data_ptr(), self.v.data_ptr(), slots,
                       self.slots_per_seq, None if bt is None else bt.data_ptr(),
                       self.block_size, 0 if bt is None else bt.shape[-1], self.dtype,
                       None if self.k_ref is None else self.k_ref.data_ptr(), self.layout,
@@ -257,9 +264,10 @@ def attn_decode(q, cache: KVCache, seq_lens, positions, max_seq_len, window, sca
     B, R, Hq, D = q.shape
     if out is None:
         out = torch.empty_like(q)
-    need = attn_decode_workspace_size(cache, B, R, Hq, max_seq_len, window)
-    if workspace is None and need > 0:
-        workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
+    if workspace is None:
+        need = attn_decode_workspace_size(cache, B, R, Hq, max_seq_len, window)
+        if need > 0:
+            workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
     c = cache.struct()
     rc = lib().attn_decode(_ptr(q), ctypes.byref(c), _ptr(seq_lens), _ptr(positions), B, R,
                            int(max_seq_len), int(window), Hq, cache.n_kv_heads, D, float(scale),
@@ -287,9 +295,10 @@ def attn_decode_append(q, k_new, v_new, slot_mapping, cache: KVCache, seq_lens, 
     B, R, Hq, D = q.shape
     if out is None:
         out = torch.empty_like(q)
-    need = attn_decode_workspace_size(cache, B, R, Hq, max_seq_len, window)
-    if workspace is None and need > 0:
-        workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
+    if workspace is None:
+        need = attn_decode_workspace_size(cache, B, R, Hq, max_seq_len, window)
+        if need > 0:
+            workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
     c = cache.struct()
     rc = lib().attn_decode_append(
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), _ptr(rope_inv_freq),

@@ -37,6 +37,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "kernels.h"
@@ -48,7 +49,7 @@ namespace att {
 constexpr int kChunk = 16;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxEntries = 256;  // (request, row block) pairs per launch
+constexpr int kMaxEntries = 128;  // (request, row block) pairs per launch
 constexpr int kGapChunks = 8;     // what a change of unit costs a CTA, in chunks
 constexpr int kMinChunks = 8;     // smallest share of a CTA
 constexpr float kRescaleLog2 = 8.0f;  // the reference maximum moves past this only (w <= 2^8)
@@ -63,6 +64,9 @@ struct Params {
     const float *ks, *vs;  // [slot >> scale_shift][n_kv_heads], or nullptr (all 1)
     int scale_shift;
     int kind, slots_per_seq, block_size, max_blocks, num_pages;
+    // pages of whole chunks: n / page_chunks = umulhi(n << 4, page_mul) >> page_shift, n < 2^28
+    int page_chunks, page_shift;
+    uint32_t page_mul;
     bool head_major;
     const int32_t *block_table, *seq_lens, *positions;
     int q_rows, n_q_heads, n_kv_heads, group, rows, row_blocks;
@@ -75,16 +79,30 @@ struct Params {
     int32_t *err;
 };
 
-template <int FMT, int HD>
+// A stage of a warp's ring: the K rows and the V rows of NSUB chunks.  Thread
+// (gq, tq) reads pieces tq + 4 j of K rows gq and gq + 8, and piece gq (+ 8 j)
+// of V rows 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9; rows are swizzled so that the
+// lanes of one access meet different banks.
+template <int FMT, int HD, int MT>
 struct Geo {
     static constexpr int E = FMT == kBF16 ? 2 : 1;
+    static constexpr int RB = MT == 0 ? 8 : 16;                  // query rows of a unit
     static constexpr int kRowBytes = HD * E;
-    static constexpr int kKPieces = kRowBytes / 64;        // 16-byte pieces of a key per thread
-    static constexpr int kStepsPerPiece = 4 / E;           // k-steps (of 16 dims) a piece feeds
-    static constexpr int kVBytes = kRowBytes / 8 < 16 ? 8 : 16;  // a thread's V load
+    static constexpr int kKPieces = kRowBytes / 64;              // 16-byte pieces of a key a thread
+    static constexpr int kStepsPerPiece = 4 / E;                 // k-steps (of 16 dims) of a piece
+    static constexpr int kVBytes = kRowBytes / 8 < 16 ? 8 : 16;  // a V piece
     static constexpr int kVPieces = kRowBytes / (8 * kVBytes);
-    static constexpr int kVWords = kVBytes / 4;
-    static constexpr int kVElems = kVBytes / E;            // dims of a V piece
+    static constexpr int kVWords = kVBytes / 4 * kVPieces;       // words of a key a thread
+    static constexpr int kVElems = kVBytes / E;                  // dims of a V piece
+    static constexpr int NSUB = kRowBytes == 64 ? 2 : 1;
+    static constexpr int kChunkBytes = kChunk * kRowBytes;
+    static constexpr int kStageBytes = 2 * NSUB * kChunkBytes;
+    static constexpr int kStages = 3;
+    static constexpr int CTAS = kRowBytes == 256 ? 2 : 4;        // blocks of an SM
+    static constexpr int kGroup = kWarps * NSUB;                 // chunks of a block's step
+    static constexpr int kRingBytes = kStages * kStageBytes;     // of one warp
+    static constexpr int kOStride = HD + 4;                      // floats of a parked output row
+    static_assert(RB * kOStride * 4 <= kRingBytes, "a warp's outputs are parked in its ring");
 };
 
 // Bits 0 .. n - 1, n clamped to 0 .. 16.
@@ -92,23 +110,34 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
     return n <= 0 ? 0u : n >= 16 ? 0xFFFFu : (1u << n) - 1u;
 }
 
-template <int BYTES>
-__device__ __forceinline__ void load_piece(uint32_t *dst, const uint8_t *src, bool on) {
-    if constexpr (BYTES == 16) {
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (on)
-            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                         : "l"(src));
-        dst[0] = x.x, dst[1] = x.y, dst[2] = x.z, dst[3] = x.w;
-    } else {
-        uint2 x = make_uint2(0u, 0u);
-        if (on)
-            asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
-                         : "=r"(x.x), "=r"(x.y)
-                         : "l"(src));
-        dst[0] = x.x, dst[1] = x.y;
-    }
+// Byte offset of 16-byte piece c of row r (0 .. 15) of a chunk's K rows.
+template <int ROW>
+__device__ __forceinline__ uint32_t k_offset(int r, int c) {
+    return ROW == 64 ? r * 64 + c * 16 : r * ROW + ((c ^ (4 * (r & 1))) << 4);
+}
+
+// ... of its V rows.  64-byte rows: rows 2 i and 2 i + 1 share 128 bytes, whose
+// halves change places for odd i, and the 32-byte parts of a half for i & 2.
+template <int ROW>
+__device__ __forceinline__ uint32_t v_offset(int r, int c) {
+    const int i = r >> 1;
+    return ROW == 64 ? i * 128 + (((r ^ i) & 1) << 6) + ((c ^ (i & 2)) << 4)
+                     : r * ROW + ((c ^ (2 * (i & 3))) << 4);
+}
+
+// 16 bytes to shared memory, asynchronously; zeros where !on.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(on ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const float *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Four 8-bit codes -> two f16x2 words (bytes 0, 1 and bytes 2, 3); exact.
@@ -151,12 +180,26 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
         mma_f16_16816(d, a, b0, b1);
 }
 
-// The visible keys of one (request, row block): [0, sinks) and [lo, hi), as
-// chunks 0 .. sc - 1 and clo, clo + 1, ... (cnt chunks in all); pmin, pmax the
-// rows' first and last position.
+// The visible keys of one (request, row block): positions [0, sinks) and
+// [lo, hi); pmin, pmax the rows' first and last position.
 struct Entry {
-    int cnt, sc, clo, lo, hi, pmin, pmax;
+    int lo, hi, pmin, pmax;
 };
+
+// ... as chunks 0 .. sc - 1 and clo, clo + 1, ..., cnt in all.  Where the two
+// ranges meet they are one, and the keys between them masked.
+struct Chunks {
+    int sc, clo, cnt;
+};
+__device__ __forceinline__ Chunks chunks_of(const Entry &t, int sinks) {
+    Chunks c;
+    const int chi = (t.hi + kChunk - 1) / kChunk;
+    c.clo = t.lo / kChunk;
+    c.sc = (min(sinks, t.hi) + kChunk - 1) / kChunk;
+    if (c.sc > 0 && c.clo <= c.sc) c.clo = c.sc = 0;
+    c.cnt = c.sc + chi - c.clo;
+    return c;
+}
 
 __device__ __forceinline__ Entry make_entry(const Params &p, int e, int rb_rows, bool report) {
     Entry t = {};
@@ -177,41 +220,44 @@ __device__ __forceinline__ Entry make_entry(const Params &p, int e, int rb_rows,
         t.pmax = max(t.pmax, pos);
         if (pos >= 0) oldest = min(oldest, pos);
     }
-    t.hi = (int)min((int64_t)len, (int64_t)t.pmax + 1);
-    if (t.hi <= 0) return t;
+    t.hi = max(0, (int)min((int64_t)len, (int64_t)t.pmax + 1));
+    if (t.hi == 0) return t;
     t.lo = p.window > 0 ? max(0, min(t.hi, oldest - p.window + 1)) : 0;
     if (p.kind == ATTN_CACHE_RING)  // what the turning part of the ring still holds
         t.lo = max(t.lo, min(t.hi, len - (p.slots_per_seq - p.sinks)));
-    const int chi = (t.hi + kChunk - 1) / kChunk;
-    t.clo = t.lo / kChunk;
-    t.sc = (min(p.sinks, t.hi) + kChunk - 1) / kChunk;
-    if (t.clo <= t.sc) t.clo = t.sc = 0;  // one range: the keys between are masked
-    if (t.sc == 0 && p.sinks <= 0) {
-        t.cnt = t.lo < t.hi ? chi - t.clo : 0;
-    } else {
-        t.cnt = t.sc + (t.lo < t.hi || t.sc == 0 ? chi - t.clo : 0);
-    }
     return t;
 }
 
-template <int FMT, int HD, int MT>
-struct Smem {
-    static constexpr int RB = MT == 0 ? 8 : 16;
-    static constexpr int kStride = HD + 4;
-    float o[kWarps][RB][kStride];
-    float m[kWarps][RB], l[kWarps][RB], w[kWarps][RB], lse[RB];
-    int prefix[kMaxEntries + 1];
-    Entry entry[kMaxEntries];
+// What a warp notes about a chunk in its ring.
+struct Note {
+    uint32_t mask;  // keys present
+    float ks, vs;
+    uint32_t pad;
 };
 
 template <int FMT, int HD, int MT>
-__global__ void __launch_bounds__(kThreads, FMT == kBF16 ? (MT == 0 ? 3 : 2) : (MT == 0 ? 4 : 3))
+struct __align__(16) Smem {
+    using G = Geo<FMT, HD, MT>;
+    // a warp's ring; at the end of a unit its output rows (float [RB][kOStride])
+    uint8_t ring[kWarps][G::kRingBytes];
+    uint32_t q[HD / 16][32][MT == 0 ? 2 : 4];  // q fragments of a unit, as a lane reads them
+    Note note[kWarps][G::kStages][G::NSUB];
+    float m[kWarps][G::RB], l[kWarps][G::RB], w[kWarps][G::RB], lse[G::RB];
+    Entry entry[kMaxEntries];
+    int prefix[kMaxEntries + 1];
+    __device__ __forceinline__ float *out_row(int warp, int row) {
+        return reinterpret_cast<float *>(ring[warp]) + row * G::kOStride;
+    }
+};
+
+template <int FMT, int HD, int MT>
+__global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
     attend_kernel(const Params p) {
-    using G = Geo<FMT, HD>;
-    using S = Smem<FMT, HD, MT>;
-    constexpr int RB = S::RB;
+    using G = Geo<FMT, HD, MT>;
+    constexpr int RB = G::RB;
     constexpr int kSteps = HD / 16;
-    __shared__ __align__(16) S sm;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    Smem<FMT, HD, MT> &sm = *reinterpret_cast<Smem<FMT, HD, MT> *>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gq = lane >> 2, tq = lane & 3;
     pdl_wait();
@@ -226,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, FMT == kBF16 ? (MT == 0 ? 3 : 2) : (
         if (lane == 0) sm.prefix[0] = 0;
         for (int base = 0; base < p.n_entries; base += 32) {
             const int i = base + lane;
-            const int n = i < p.n_entries ? sm.entry[i].cnt : 0;
+            const int n = i < p.n_entries ? chunks_of(sm.entry[i], p.sinks).cnt : 0;
             int x = n > 0 ? (n + kGapChunks) * p.n_kv_heads : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -246,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, FMT == kBF16 ? (MT == 0 ? 3 : 2) : (
     if (blockIdx.x == 0) {
         // rows of a unit without keys are zeros, and it has no parts
         for (int i = warp; i < p.n_entries; i += kWarps) {
-            if (sm.entry[i].cnt != 0) continue;
+            if (chunks_of(sm.entry[i], p.sinks).cnt != 0) continue;
             const int e = p.e0 + i, b = e / p.row_blocks, rb = e - b * p.row_blocks;
             const int row0 = rb * RB, n = min(p.rows, row0 + RB) - row0;
             for (int kvh = 0; kvh < p.n_kv_heads; ++kvh) {
@@ -269,18 +315,19 @@ __global__ void __launch_bounds__(kThreads, FMT == kBF16 ? (MT == 0 ? 3 : 2) : (
             if (sm.prefix[mid] <= g) lo_e = mid; else hi_e = mid;
         }
         const Entry en = sm.entry[lo_e];
-        const int span = en.cnt + kGapChunks;
+        const Chunks ch = chunks_of(en, p.sinks);
+        const int span = ch.cnt + kGapChunks;
         int off = g - sm.prefix[lo_e];
         const int kvh = off / span;
         off -= kvh * span;
         const int unit_start = g - off;
-        if (off >= en.cnt) {  // in the gap behind the unit
+        if (off >= ch.cnt) {  // in the gap behind the unit
             g = unit_start + span;
             continue;
         }
-        const int c_end = min(en.cnt, off + (g_end - g));
+        const int c_end = min(ch.cnt, off + (g_end - g));
         const int unit = lo_e * p.n_kv_heads + kvh;
-        const int first = unit_start / share, last = (unit_start + en.cnt - 1) / share;
+        const int first = unit_start / share, last = (unit_start + ch.cnt - 1) / share;
         const int e = p.e0 + lo_e, b = e / p.row_blocks, rb = e - b * p.row_blocks;
         const int row0 = rb * RB, n_rows = min(p.rows, row0 + RB) - row0;
 
@@ -295,32 +342,31 @@ __global__ void __launch_bounds__(kThreads, FMT == kBF16 ? (MT == 0 ? 3 : 2) : (
             return p.positions[(int64_t)b * p.q_rows + (row0 + min(rr, n_rows - 1)) / p.group];
         };
         constexpr int kQRows = MT == 0 ? 1 : 2;
-        uint32_t qf[kSteps][2 * kQRows];
         bool q_big = false;
+        for (int kk = warp; kk < kSteps; kk += kWarps) {
+            const int j = kk / G::kStepsPerPiece, st = kk % G::kStepsPerPiece;
+            const int d0 = (16 / G::E) * (tq + 4 * j) + 4 * st;
 #pragma unroll
-        for (int hr = 0; hr < kQRows; ++hr) {
-            const uint32_t *src = reinterpret_cast<const uint32_t *>(qb + row_of(gq + 8 * hr));
-#pragma unroll
-            for (int kk = 0; kk < kSteps; ++kk) {
-                const int j = kk / G::kStepsPerPiece, s = kk % G::kStepsPerPiece;
-                const int d0 = (16 / G::E) * (tq + 4 * j) + 4 * s;
-                uint2 x = *reinterpret_cast<const uint2 *>(src + d0 / 2);
+            for (int hr = 0; hr < kQRows; ++hr) {
+                uint2 x = *reinterpret_cast<const uint2 *>(qb + row_of(gq + 8 * hr) + d0);
                 if constexpr (FMT != kBF16) {  // f16 holds |q| < 65520
                     x.x = bf16x2_to_f16x2(x.x);
                     x.y = bf16x2_to_f16x2(x.y);
                     q_big |= (x.x & 0x7C00u) == 0x7C00u || (x.x & 0x7C000000u) == 0x7C000000u ||
                              (x.y & 0x7C00u) == 0x7C00u || (x.y & 0x7C000000u) == 0x7C000000u;
                 }
-                qf[kk][hr] = x.x;
-                qf[kk][kQRows + hr] = x.y;
+                sm.q[kk][lane][hr] = x.x;
+                sm.q[kk][lane][kQRows + hr] = x.y;
             }
         }
         if (q_big) report_error(p.err, ATTN_ERR_UNSUPPORTED);
         int rpos[2];  // positions of the two rows this thread keeps scores of
         rpos[0] = MT == 0 ? pos_of(2 * tq) : pos_of(gq);
         rpos[1] = MT == 0 ? pos_of(2 * tq + 1) : pos_of(gq + 8);
+        __syncthreads();
 
         // ---- where chunks lie
+        constexpr int NSUB = G::NSUB, kStages = G::kStages;
         const int32_t *bt = p.block_table + (int64_t)b * p.max_blocks;
         const int blk_rows = p.kind == ATTN_CACHE_PAGED ? p.block_size : p.slots_per_seq;
         const uint32_t row_step = p.head_major ? 1u : (uint32_t)p.n_kv_heads;
@@ -331,15 +377,21 @@ __global__ void __launch_bounds__(kThreads, FMT == kBF16 ? (MT == 0 ? 3 : 2) : (
             return p.head_major ? ((uint32_t)block * p.n_kv_heads + kvh) * blk_rows + r
                                 : ((uint32_t)block * blk_rows + r) * p.n_kv_heads + kvh;
         };
-        auto chunk_t0 = [&](int c) { return (c < en.sc ? c : c - en.sc + en.clo) * kChunk; };
+        auto real_chunk = [&](int c) { return c < ch.sc ? c : c - ch.sc + ch.clo; };
         auto chunk_mask = [&](int t0) -> uint32_t {
             return (bits_below(p.sinks - t0) | (0xFFFFu & ~bits_below(en.lo - t0))) &
                    bits_below(en.hi - t0);
         };
-        // the table entry of an evenly spaced chunk (read a chunk ahead of its rows)
-        auto chunk_page = [&](int c) -> int {
-            if (p.kind != ATTN_CACHE_PAGED || !even || c >= c_end) return b;
-            return __ldg(bt + chunk_t0(c) / p.block_size);
+        auto page_of_chunk = [&](int rc) {
+            return (int)(__umulhi((uint32_t)rc << 4, p.page_mul) >> p.page_shift);
+        };
+        // the table entries of a step's evenly spaced chunks (read a step ahead of the rows)
+        int page[NSUB];
+        auto read_pages = [&](int c) {
+            if (p.kind == ATTN_CACHE_PAGED && even)
+#pragma unroll
+                for (int i = 0; i < NSUB; ++i)
+                    if (c + i < c_end) page[i] = __ldg(bt + page_of_chunk(real_chunk(c + i)));
         };
 
         float o[MT == 0 ? HD / 16 : HD / 8][4];
@@ -347,178 +399,211 @@ __global__ void __launch_bounds__(kThreads, FMT == kBF16 ? (MT == 0 ? 3 : 2) : (
         for (auto &x : o) x[0] = x[1] = x[2] = x[3] = 0.f;
         float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
 
-        // the chunk in flight
-        uint32_t kw[2][4 * G::kKPieces], vw[4][G::kVWords * G::kVPieces];
-        uint32_t mask = 0, base = 0, spread = 0;
-        float sk = 1.f, sv = 1.f;
-        int t0 = 0;
-        // finds chunk c's rows: even chunks have row `base + key * row_step`,
-        // others lane key & 15 holds row `spread`; `mask` the keys present
-        auto locate = [&](int c, int page) {
-            t0 = chunk_t0(c);
-            mask = chunk_mask(t0);
-            int slot = 0;
-            if (even) {
-                if (p.kind == ATTN_CACHE_PAGED) {
-                    if ((unsigned)page >= (unsigned)p.num_pages) {
-                        if (lane == 0) report_error(p.err, ATTN_ERR_BOUNDS);
-                        mask = 0, page = 0;
-                    }
-                    const int r = t0 % p.block_size;
-                    base = row_index(page, r);
-                    slot = page * p.block_size + r;
-                } else {
-                    base = row_index(b, t0);
-                    slot = b * p.slots_per_seq + t0;
-                }
-            } else {
-                const int t = t0 + (lane & 15);
-                bool on = (mask >> (lane & 15)) & 1u;
-                spread = 0;
-                if (on) {
-                    if (p.kind == ATTN_CACHE_PAGED) {
-                        const int pi = t / p.block_size, id = __ldg(bt + pi);
-                        if ((unsigned)id >= (unsigned)p.num_pages) {
-                            report_error(p.err, ATTN_ERR_BOUNDS);
-                            on = false;
+        // ---- copies of a step's keys into stage `st` (nothing past c_end)
+        constexpr int kPer = G::kRowBytes / 16;  // 16-byte pieces of a row
+        constexpr int kRowsPer = 32 / kPer;      // rows of one copy instruction
+        const int my_row = lane / kPer, my_piece = lane % kPer;
+        const uint32_t ring = smem_u32(sm.ring[warp]);
+        auto request = [&](int c, int st) {
+#pragma unroll
+            for (int i = 0; i < NSUB; ++i) {
+                if (c + i < c_end) {
+                    const int rc = real_chunk(c + i), t0 = rc * kChunk;
+                    uint32_t mask = chunk_mask(t0), first = 0, spread = 0;
+                    int slot = 0;
+                    if (even) {
+                        if (p.kind == ATTN_CACHE_PAGED) {
+                            int id = page[i];
+                            if ((unsigned)id >= (unsigned)p.num_pages) {
+                                if (lane == 0) report_error(p.err, ATTN_ERR_BOUNDS);
+                                mask = 0, id = 0;
+                            }
+                            const int r = (rc - page_of_chunk(rc) * p.page_chunks) * kChunk;
+                            first = row_index(id, r);
+                            slot = id * p.block_size + r;
                         } else {
-                            spread = row_index(id, t - pi * p.block_size);
+                            first = row_index(b, t0);
+                            slot = b * p.slots_per_seq + t0;
                         }
                     } else {
-                        spread = row_index(b, t < p.sinks ? t
+                        const int t = t0 + (lane & 15);
+                        bool on = (mask >> (lane & 15)) & 1u;
+                        if (on) {
+                            if (p.kind == ATTN_CACHE_PAGED) {
+                                const int pi = t / p.block_size, id = __ldg(bt + pi);
+                                if ((unsigned)id >= (unsigned)p.num_pages) {
+                                    report_error(p.err, ATTN_ERR_BOUNDS);
+                                    on = false;
+                                } else {
+                                    spread = row_index(id, t - pi * p.block_size);
+                                }
+                            } else {
+                                spread = row_index(b, t < p.sinks
+                                                          ? t
                                                           : p.sinks + (t - p.sinks) %
                                                                           (p.slots_per_seq - p.sinks));
+                            }
+                        }
+                        mask = __ballot_sync(0xffffffffu, on) & 0xFFFFu;
+                    }
+                    const uint32_t k_dst = ring + st * G::kStageBytes + 2 * i * G::kChunkBytes;
+                    const uint32_t v_dst = k_dst + G::kChunkBytes;
+#pragma unroll
+                    for (int n = 0; n < kChunk / kRowsPer; ++n) {
+                        const int r = my_row + n * kRowsPer;
+                        const uint32_t row = even ? first + r * row_step
+                                                  : __shfl_sync(0xffffffffu, spread, r);
+                        const bool on = (mask >> r) & 1u;
+                        // a row that is not copied has no address of its own
+                        const uint64_t at =
+                            on ? (uint64_t)row * G::kRowBytes + my_piece * 16 : (uint64_t)0;
+                        copy16(k_dst + k_offset<G::kRowBytes>(r, my_piece), p.k + at, on);
+                        copy16(v_dst + v_offset<G::kRowBytes>(r, my_piece), p.v + at, on);
+                    }
+                    Note &note = sm.note[warp][st][i];
+                    if (lane == 0) note.mask = mask;
+                    if constexpr (FMT != kBF16) {
+                        if (p.ks == nullptr || mask == 0) {
+                            if (lane == 0) note.ks = note.vs = 1.f;
+                        } else if (lane < 2) {
+                            const int64_t at =
+                                (int64_t)(slot >> p.scale_shift) * p.n_kv_heads + kvh;
+                            copy4(smem_u32(lane == 0 ? &note.ks : &note.vs),
+                                  (lane == 0 ? p.ks : p.vs) + at);
+                        }
                     }
                 }
-                mask = __ballot_sync(0xffffffffu, on) & 0xFFFFu;
             }
-            if constexpr (FMT != kBF16) {
-                if (p.ks != nullptr && mask != 0) {
-                    const int64_t i = (int64_t)(slot >> p.scale_shift) * p.n_kv_heads + kvh;
-                    sk = __ldg(p.ks + i);
-                    sv = __ldg(p.vs + i);
-                }
-            }
-        };
-        auto row_ptr = [&](const uint8_t *cache, int key) {
-            const uint32_t r = even ? base + key * row_step : __shfl_sync(0xffffffffu, spread, key);
-            return cache + (uint64_t)r * G::kRowBytes;
-        };
-        auto load_k = [&]() {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int key = gq + 8 * h;
-                const uint8_t *src = row_ptr(p.k, key) + tq * 16;
-                const bool on = (mask >> key) & 1u;
-#pragma unroll
-                for (int j = 0; j < G::kKPieces; ++j)
-                    load_piece<16>(&kw[h][4 * j], src + 64 * j, on);
-            }
-        };
-        auto load_v = [&]() {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int key = 2 * tq + (i & 1) + 8 * (i >> 1);
-                const uint8_t *src = row_ptr(p.v, key) + gq * G::kVBytes;
-                const bool on = (mask >> key) & 1u;
-#pragma unroll
-                for (int j = 0; j < G::kVPieces; ++j)
-                    load_piece<G::kVBytes>(&vw[i][G::kVWords * j], src + 8 * G::kVBytes * j, on);
-            }
+            copies_commit();
         };
 
-        const int c0 = off + warp;
-        int page = chunk_page(c0);
-        if (c0 < c_end) {
-            locate(c0, page);
-            load_k();
-            load_v();
-        }
-        page = chunk_page(c0 + kWarps);
-        for (int c = c0; c < c_end; c += kWarps) {
-            const bool more = c + kWarps < c_end;
-            const uint32_t cur_mask = mask;
-            const int cur_t0 = t0;
-            const float cur_sk = sk, cur_sv = fmaxf(sv, kScaleFloor);
-            // ---- scores: MT 0 keys are the rows of S^T = K Q^T, MT 1 the columns of S = Q K^T
-            float s[2][4];
+        const int c0 = off + warp * NSUB;
+        read_pages(c0);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+        for (int st = 0; st < kStages - 1; ++st) {
+            request(c0 + st * G::kGroup, st);
+            read_pages(c0 + (st + 1) * G::kGroup);
+        }
+        int st = 0;
+        for (int c = c0; c < c_end; c += G::kGroup, st = st + 1 == kStages ? 0 : st + 1) {
+            copies_wait<kStages - 2>();
+            __syncwarp();  // the step has landed for all lanes, and the step before is read
+            request(c + (kStages - 1) * G::kGroup, st == 0 ? kStages - 1 : st - 1);
+            read_pages(c + kStages * G::kGroup);
+            const uint8_t *stage = sm.ring[warp] + st * G::kStageBytes;
+            uint32_t cur_mask[NSUB];
+            float cur_sk[NSUB], cur_sv[NSUB];
+            uint32_t kw[NSUB][2][4 * G::kKPieces];
+#pragma unroll
+            for (int i = 0; i < NSUB; ++i) {
+                const bool in = c + i < c_end;
+                const Note note = sm.note[warp][st][i];
+                cur_mask[i] = in ? note.mask : 0u;
+                cur_sk[i] = in && FMT != kBF16 ? note.ks : 1.f;
+                cur_sv[i] = in && FMT != kBF16 ? fmaxf(note.vs, kScaleFloor) : 1.f;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < G::kKPieces; ++j) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(
+                            stage + 2 * i * G::kChunkBytes +
+                            k_offset<G::kRowBytes>(gq + 8 * h, tq + 4 * j));
+                        kw[i][h][4 * j] = x.x, kw[i][h][4 * j + 1] = x.y;
+                        kw[i][h][4 * j + 2] = x.z, kw[i][h][4 * j + 3] = x.w;
+                    }
+            }
+            // ---- scores: MT 0 keys are the rows of S^T = K Q^T, MT 1 the columns of S = Q K^T
+            constexpr int NJ = MT == 0 ? 1 : 2;
+            float s[NSUB][NJ][4];
+#pragma unroll
+            for (int i = 0; i < NSUB; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) s[i][j][0] = s[i][j][1] = s[i][j][2] = s[i][j][3] = 0.f;
 #pragma unroll
             for (int kk = 0; kk < kSteps; ++kk) {
-                const int j = kk / G::kStepsPerPiece, st = kk % G::kStepsPerPiece;
-                uint32_t x[2][2];
+                uint32_t qf[2 * kQRows];
+                if constexpr (MT == 0) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(sm.q[kk][lane]);
+                    qf[0] = x.x, qf[1] = x.y;
+                } else {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(sm.q[kk][lane]);
+                    qf[0] = x.x, qf[1] = x.y, qf[2] = x.z, qf[3] = x.w;
+                }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if constexpr (FMT == kBF16) {
-                        x[h][0] = kw[h][4 * j + 2 * st];
-                        x[h][1] = kw[h][4 * j + 2 * st + 1];
+                for (int i = 0; i < NSUB; ++i) {
+                    uint32_t x[2][2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if constexpr (FMT == kBF16) {
+                            x[h][0] = kw[i][h][2 * kk];
+                            x[h][1] = kw[i][h][2 * kk + 1];
+                        } else {
+                            codes_to_f16<FMT>(kw[i][h][kk], x[h][0], x[h][1]);
+                        }
+                    }
+                    if constexpr (MT == 0) {
+                        const uint32_t a[4] = {x[0][0], x[1][0], x[0][1], x[1][1]};
+                        mma16<FMT>(s[i][0], a, qf[0], qf[1]);
                     } else {
-                        codes_to_f16<FMT>(kw[h][4 * j + st], x[h][0], x[h][1]);
+                        mma16<FMT>(s[i][0], qf, x[0][0], x[0][1]);
+                        mma16<FMT>(s[i][1], qf, x[1][0], x[1][1]);
                     }
                 }
-                if constexpr (MT == 0) {
-                    const uint32_t a[4] = {x[0][0], x[1][0], x[0][1], x[1][1]};
-                    mma16<FMT>(s[kk & 1], a, qf[kk][0], qf[kk][1]);
-                } else {
-                    mma16<FMT>(s[0], qf[kk], x[0][0], x[0][1]);
-                    mma16<FMT>(s[1], qf[kk], x[1][0], x[1][1]);
-                }
             }
-            if constexpr (MT == 0) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[0][i] += s[1][i];
-            }
-            // ---- the next chunk's keys
-            if (more) {
-                locate(c + kWarps, page);
-                load_k();
-            }
-            page = chunk_page(c + 2 * kWarps);
-            // ---- mask and weights.  x(row, key): element (i, j) of the thread is
-            // MT 0: row i & 1, key gq + 8 (i >> 1); MT 1: row i >> 1, key 8 j + 2 tq + (i & 1)
-            constexpr int NJ = MT == 0 ? 1 : 2;
-            const float f = cur_sk * p.scale_log2;
-            float lv = 0.f, inv_sv = 1.f;
-            if constexpr (FMT != kBF16) {
-                lv = __log2f(cur_sv);
-                inv_sv = __frcp_rn(cur_sv);
-            }
-            const bool open = cur_mask == 0xFFFFu && cur_t0 + kChunk - 1 <= en.pmin &&
-                              (p.window <= 0 || en.pmax - cur_t0 < p.window ||
-                               cur_t0 + kChunk <= p.sinks);
-            auto row_i = [](int i) { return MT == 0 ? (i & 1) : (i >> 1); };
-            auto sees = [&](int i_row, int key) {
-                const int t = cur_t0 + key, pos = rpos[i_row];
-                return ((cur_mask >> key) & 1u) && t <= pos &&
+            // ---- mask and weights.  x(row, key): element e of s[i][j] is
+            // MT 0: row e & 1, key gq + 8 (e >> 1); MT 1: row e >> 1, key 8 j + 2 tq + (e & 1)
+            auto row_e = [](int e) { return MT == 0 ? (e & 1) : (e >> 1); };
+            auto sees = [&](int i, int row, int key) {
+                const int t = real_chunk(c + i) * kChunk + key, pos = rpos[row];
+                return ((cur_mask[i] >> key) & 1u) && t <= pos &&
                        (p.window <= 0 || pos - t < p.window || t < p.sinks);
             };
+            float inv_sv[NSUB];
+            bool open = true;  // every row sees every key of the step
 #pragma unroll
-            for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[j][i] = fmaf(s[j][i], f, lv);
-            if (!open) {
+            for (int i = 0; i < NSUB; ++i) {
+                const int t0 = real_chunk(c + i) * kChunk;
+                open &= cur_mask[i] == 0xFFFFu && t0 + kChunk - 1 <= en.pmin &&
+                        (p.window <= 0 || en.pmax - t0 < p.window || t0 + kChunk <= p.sinks);
+                const float f = cur_sk[i] * p.scale_log2;
+                float lv = 0.f;
+                inv_sv[i] = 1.f;
+                if constexpr (FMT != kBF16) {
+                    lv = __log2f(cur_sv[i]);
+                    inv_sv[i] = __fdividef(1.f, cur_sv[i]);
+                }
 #pragma unroll
                 for (int j = 0; j < NJ; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int key = MT == 0 ? gq + 8 * (i >> 1) : 8 * j + 2 * tq + (i & 1);
-                        s[j][i] = sees(row_i(i), key) ? s[j][i] : -INFINITY;
-                    }
+                    for (int e = 0; e < 4; ++e) s[i][j][e] = fmaf(s[i][j][e], f, lv);
+            }
+            if (!open) {
+#pragma unroll
+                for (int i = 0; i < NSUB; ++i)
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = MT == 0 ? gq + 8 * (e >> 1) : 8 * j + 2 * tq + (e & 1);
+                            s[i][j][e] = sees(i, row_e(e), key) ? s[i][j][e] : -INFINITY;
+                        }
             }
             float alpha[2];
             bool moved = false;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                float mx;
+                float mx = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < NSUB; ++i)
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j)
+                        mx = max3(mx, s[i][j][MT == 0 ? r : 2 * r],
+                                  s[i][j][MT == 0 ? r + 2 : 2 * r + 1]);
                 if constexpr (MT == 0) {
-                    mx = fmaxf(s[0][r], s[0][r + 2]);
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                 } else {
-                    mx = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]),
-                               fmaxf(s[1][2 * r], s[1][2 * r + 1]));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 }
@@ -528,134 +613,167 @@ __global__ void __launch_bounds__(kThreads, FMT == kBF16 ? (MT == 0 ? 3 : 2) : (
                 alpha[r] = m_new == m_old ? 1.f : fast_exp2(m_old - m_use);
                 moved |= m_new != m_old;
                 m_run[r] = m_new;
-                float sum = 0.f;
+                l_run[r] *= alpha[r];
 #pragma unroll
-                for (int j = 0; j < NJ; ++j)
+                for (int i = 0; i < NSUB; ++i) {
+                    float sum = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (row_i(i) == r) {
-                            s[j][i] = fast_exp2(s[j][i] - m_use);
-                            sum += s[j][i];
-                        }
-                l_run[r] = l_run[r] * alpha[r] + sum * inv_sv;
+                    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (row_e(e) == r) {
+                                s[i][j][e] = fast_exp2(s[i][j][e] - m_use);
+                                sum += s[i][j][e];
+                            }
+                    l_run[r] = fmaf(sum, inv_sv[i], l_run[r]);
+                }
             }
             if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
                 for (auto &x : o)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[i] *= alpha[row_i(i)];
+                    for (int e = 0; e < 4; ++e) x[e] *= alpha[row_e(e)];
             }
-            // ---- weights as the operand of P V: f16 (one rounding: 11 bits), or for
-            // a bf16 cache two bf16 halves (16 bits), since one bf16 rounding of P
-            // would cost as much as the output's own
+            // ---- P V, a chunk at a time.  Weights as its operand: f16 (one rounding:
+            // 11 bits), or for a bf16 cache two bf16 halves (16 bits), since one
+            // bf16 rounding of P would cost as much as the output's own
             constexpr int NP = MT == 0 ? 2 : 4;
-            uint32_t ph[NP], pl[NP];
-            if constexpr (MT == 0) {
-                if constexpr (FMT == kBF16) {
-                    split_bf16x2(s[0][0], s[0][1], ph[0], pl[0]);
-                    split_bf16x2(s[0][2], s[0][3], ph[1], pl[1]);
-                    pl[0] = movmatrix_trans(pl[0]);
-                    pl[1] = movmatrix_trans(pl[1]);
-                } else {
-                    ph[0] = pack_f16x2(s[0][0], s[0][1]);
-                    ph[1] = pack_f16x2(s[0][2], s[0][3]);
-                }
-                ph[0] = movmatrix_trans(ph[0]);
-                ph[1] = movmatrix_trans(ph[1]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = i >> 1, r = i & 1;
-                    if constexpr (FMT == kBF16)
-                        split_bf16x2(s[j][2 * r], s[j][2 * r + 1], ph[i], pl[i]);
-                    else
-                        ph[i] = pack_f16x2(s[j][2 * r], s[j][2 * r + 1]);
-                }
-            }
-            // V operands of two neighbouring dims (word w of the pieces): x[0] and
-            // x[1] dim 0 and 1 over keys 2 tq, 2 tq + 1, x[2] and x[3] over + 8
-            auto v_pair = [&](const uint32_t (&w)[4], int hi, uint32_t (&x)[4]) {
-                if constexpr (FMT == kBF16) {
-                    x[0] = __byte_perm(w[0], w[1], 0x5410u);
-                    x[1] = __byte_perm(w[0], w[1], 0x7632u);
-                    x[2] = __byte_perm(w[2], w[3], 0x5410u);
-                    x[3] = __byte_perm(w[2], w[3], 0x7632u);
-                } else {
-                    const uint32_t sel = hi ? 0x7362u : 0x5140u;
-                    codes_to_f16<FMT>(__byte_perm(w[0], w[1], sel), x[0], x[1]);
-                    codes_to_f16<FMT>(__byte_perm(w[2], w[3], sel), x[2], x[3]);
-                }
-            };
             constexpr int kPairs = HD / 16;            // pairs of dims of a thread
             constexpr int kPairsPerWord = 2 / G::E;
-            auto add_pv = [&](int d, const uint32_t (&x)[4], float (&oa)[4], float (&ob)[4]) {
-                if constexpr (MT == 0) {  // rows of O^T: dim 0 in elements 0, 1, dim 1 in 2, 3
-                    mma16<FMT>(oa, x, ph[0], ph[1]);
-                    if constexpr (FMT == kBF16) mma16<FMT>(oa, x, pl[0], pl[1]);
-                } else {
-                    mma16<FMT>(oa, ph, x[0], x[2]);
-                    mma16<FMT>(ob, ph, x[1], x[3]);
+#pragma unroll
+            for (int i = 0; i < NSUB; ++i) {
+                uint32_t ph[NP], pl[NP];
+                if constexpr (MT == 0) {
                     if constexpr (FMT == kBF16) {
-                        mma16<FMT>(oa, pl, x[0], x[2]);
-                        mma16<FMT>(ob, pl, x[1], x[3]);
+                        split_bf16x2(s[i][0][0], s[i][0][1], ph[0], pl[0]);
+                        split_bf16x2(s[i][0][2], s[i][0][3], ph[1], pl[1]);
+                        pl[0] = movmatrix_trans(pl[0]);
+                        pl[1] = movmatrix_trans(pl[1]);
+                    } else {
+                        ph[0] = pack_f16x2(s[i][0][0], s[i][0][1]);
+                        ph[1] = pack_f16x2(s[i][0][2], s[i][0][3]);
+                    }
+                    ph[0] = movmatrix_trans(ph[0]);
+                    ph[1] = movmatrix_trans(ph[1]);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const int j = n >> 1, r = n & 1;
+                        if constexpr (FMT == kBF16)
+                            split_bf16x2(s[i][j][2 * r], s[i][j][2 * r + 1], ph[n], pl[n]);
+                        else
+                            ph[n] = pack_f16x2(s[i][j][2 * r], s[i][j][2 * r + 1]);
                     }
                 }
-            };
-            if constexpr (FMT != kINT8) {
-                if (!open) {
-                    // A value that is not finite reaches only the rows that see its
-                    // key: 0 times it would be NaN in every row.  Such keys are
-                    // multiplied alone, added where seen, and taken out.
-                    uint32_t odd = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int w = 0; w < G::kVWords * G::kVPieces; ++w)
-                            if (word_not_finite<FMT>(vw[i][w]))
-                                odd |= 1u << (2 * tq + (i & 1) + 8 * (i >> 1));
-                    odd = __reduce_or_sync(0xffffffffu, odd);
-                    while (odd != 0) {
-                        const int n = __ffs(odd) - 1;
-                        odd &= odd - 1;
-#pragma unroll
-                        for (int d = 0; d < kPairs; ++d) {
-                            uint32_t w[4], x[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                w[i] = n == 2 * tq + (i & 1) + 8 * (i >> 1)
-                                           ? vw[i][d / kPairsPerWord]
-                                           : 0u;
-                            v_pair(w, d % kPairsPerWord, x);
-                            float ta[4] = {0.f, 0.f, 0.f, 0.f}, tb[4] = {0.f, 0.f, 0.f, 0.f};
-                            add_pv(d, x, ta, tb);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (sees(row_i(i), n)) {
-                                    o[MT == 0 ? d : 2 * d][i] += ta[i];
-                                    if constexpr (MT != 0) o[2 * d + 1][i] += tb[i];
-                                }
+                // V operands of two neighbouring dims (word w of a thread's share): x[0]
+                // and x[1] dim 0 and 1 over keys 2 tq, 2 tq + 1, x[2] and x[3] over + 8
+                auto v_pair = [&](const uint32_t (&w)[4], int hi, uint32_t (&x)[4]) {
+                    if constexpr (FMT == kBF16) {
+                        x[0] = __byte_perm(w[0], w[1], 0x5410u);
+                        x[1] = __byte_perm(w[0], w[1], 0x7632u);
+                        x[2] = __byte_perm(w[2], w[3], 0x5410u);
+                        x[3] = __byte_perm(w[2], w[3], 0x7632u);
+                    } else {
+                        const uint32_t sel = hi ? 0x7362u : 0x5140u;
+                        codes_to_f16<FMT>(__byte_perm(w[0], w[1], sel), x[0], x[1]);
+                        codes_to_f16<FMT>(__byte_perm(w[2], w[3], sel), x[2], x[3]);
+                    }
+                };
+                auto add_pv = [&](const uint32_t (&x)[4], float (&oa)[4], float (&ob)[4]) {
+                    if constexpr (MT == 0) {  // O^T: dim 0 in elements 0, 1, dim 1 in 2, 3
+                        mma16<FMT>(oa, x, ph[0], ph[1]);
+                        if constexpr (FMT == kBF16) mma16<FMT>(oa, x, pl[0], pl[1]);
+                    } else {
+                        mma16<FMT>(oa, ph, x[0], x[2]);
+                        mma16<FMT>(ob, ph, x[1], x[3]);
+                        if constexpr (FMT == kBF16) {
+                            mma16<FMT>(oa, pl, x[0], x[2]);
+                            mma16<FMT>(ob, pl, x[1], x[3]);
                         }
+                    }
+                };
+                uint32_t vw[4][G::kVWords];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (n == 2 * tq + (i & 1) + 8 * (i >> 1))
+                for (int n = 0; n < 4; ++n) {
+                    const uint8_t *src = stage + (2 * i + 1) * G::kChunkBytes;
+                    const int key = 2 * tq + (n & 1) + 8 * (n >> 1);
+                    if constexpr (G::kVBytes == 8) {
+                        const uint2 x = *reinterpret_cast<const uint2 *>(
+                            src + v_offset<G::kRowBytes>(key, gq >> 1) + 8 * (gq & 1));
+                        vw[n][0] = x.x, vw[n][1] = x.y;
+                    } else {
 #pragma unroll
-                                for (int w = 0; w < G::kVWords * G::kVPieces; ++w) vw[i][w] = 0u;
+                        for (int j = 0; j < G::kVPieces; ++j) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(
+                                src + v_offset<G::kRowBytes>(key, gq + 8 * j));
+                            vw[n][4 * j] = x.x, vw[n][4 * j + 1] = x.y;
+                            vw[n][4 * j + 2] = x.z, vw[n][4 * j + 3] = x.w;
+                        }
                     }
                 }
-            }
+                if (NSUB > 1 && c + i >= c_end) {  // a chunk that the last step does not have
 #pragma unroll
-            for (int d = 0; d < kPairs; ++d) {
-                uint32_t w[4], x[4];
+                    for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = vw[i][d / kPairsPerWord];
-                v_pair(w, d % kPairsPerWord, x);
-                if constexpr (MT == 0)
-                    add_pv(d, x, o[d], o[d]);
-                else
-                    add_pv(d, x, o[2 * d], o[2 * d + 1]);
+                        for (int w = 0; w < G::kVWords; ++w) vw[n][w] = 0u;
+                }
+                if constexpr (FMT != kINT8) {
+                    if (!open) {
+                        // A value that is not finite reaches only the rows that see its
+                        // key: 0 times it would be NaN in every row.  Such keys are
+                        // multiplied alone, added where seen, and taken out.
+                        uint32_t odd = 0;
+#pragma unroll
+                        for (int n = 0; n < 4; ++n)
+#pragma unroll
+                            for (int w = 0; w < G::kVWords; ++w)
+                                if (word_not_finite<FMT>(vw[n][w]))
+                                    odd |= 1u << (2 * tq + (n & 1) + 8 * (n >> 1));
+                        odd = __reduce_or_sync(0xffffffffu, odd);
+                        while (odd != 0) {
+                            const int key = __ffs(odd) - 1;
+                            odd &= odd - 1;
+#pragma unroll
+                            for (int d = 0; d < kPairs; ++d) {
+                                uint32_t w[4], x[4];
+#pragma unroll
+                                for (int n = 0; n < 4; ++n)
+                                    w[n] = key == 2 * tq + (n & 1) + 8 * (n >> 1)
+                                               ? vw[n][d / kPairsPerWord]
+                                               : 0u;
+                                v_pair(w, d % kPairsPerWord, x);
+                                float ta[4] = {0.f, 0.f, 0.f, 0.f}, tb[4] = {0.f, 0.f, 0.f, 0.f};
+                                add_pv(x, ta, tb);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (sees(i, row_e(e), key)) {
+                                        o[MT == 0 ? d : 2 * d][e] += ta[e];
+                                        if constexpr (MT != 0) o[2 * d + 1][e] += tb[e];
+                                    }
+                            }
+#pragma unroll
+                            for (int n = 0; n < 4; ++n)
+                                if (key == 2 * tq + (n & 1) + 8 * (n >> 1))
+#pragma unroll
+                                    for (int w = 0; w < G::kVWords; ++w) vw[n][w] = 0u;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int d = 0; d < kPairs; ++d) {
+                    uint32_t w[4], x[4];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) w[n] = vw[n][d / kPairsPerWord];
+                    v_pair(w, d % kPairsPerWord, x);
+                    if constexpr (MT == 0)
+                        add_pv(x, o[d], o[d]);
+                    else
+                        add_pv(x, o[2 * d], o[2 * d + 1]);
+                }
             }
-            if (more) load_v();
         }
+        copies_wait<0>();
+        __syncwarp();  // the ring is this warp's to write
 
         // ---- the four warps' states -> one
 #pragma unroll
@@ -674,8 +792,8 @@ __global__ void __launch_bounds__(kThreads, FMT == kBF16 ? (MT == 0 ? 3 : 2) : (
                 sm.l[warp][row] = l_run[r];
             }
         }
-        // dim of element e of V piece j of thread group g8
-        auto dim_of = [](int g8, int d) {  // d: dim index 0 .. HD / 8 - 1 of the group
+        // dim d (0 .. HD / 8 - 1) of a thread group
+        auto dim_of = [](int g8, int d) {
             return G::kVElems * (g8 + 8 * (d / G::kVElems)) + d % G::kVElems;
         };
         if constexpr (MT == 0) {
@@ -683,15 +801,15 @@ __global__ void __launch_bounds__(kThreads, FMT == kBF16 ? (MT == 0 ? 3 : 2) : (
             for (int d = 0; d < HD / 16; ++d)
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
-                    *reinterpret_cast<float2 *>(&sm.o[warp][2 * tq + r][dim_of(gq, 2 * d)]) =
+                    *reinterpret_cast<float2 *>(sm.out_row(warp, 2 * tq + r) + dim_of(gq, 2 * d)) =
                         make_float2(o[d][r], o[d][r + 2]);
         } else {
 #pragma unroll
             for (int d = 0; d < HD / 16; ++d)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<float2 *>(
-                        &sm.o[warp][gq + 8 * (i >> 1)][dim_of(2 * tq + (i & 1), 2 * d)]) =
+                    *reinterpret_cast<float2 *>(sm.out_row(warp, gq + 8 * (i >> 1)) +
+                                                dim_of(2 * tq + (i & 1), 2 * d)) =
                         make_float2(o[2 * d][i], o[2 * d + 1][i]);
         }
         __syncthreads();
@@ -720,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, FMT == kBF16 ? (MT == 0 ? 3 : 2) : (
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float4 x = *reinterpret_cast<const float4 *>(&sm.o[w][row][d]);
+                const float4 x = *reinterpret_cast<const float4 *>(sm.out_row(w, row) + d);
                 const float f = sm.w[w][row];
                 a.x += f * x.x, a.y += f * x.y, a.z += f * x.z, a.w += f * x.w;
             }
@@ -793,8 +911,22 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const Params p) {
 template <int FMT, int HD, int MT>
 int launch(const Params &p, bool merge, cudaStream_t stream) {
     constexpr int RB = MT == 0 ? 8 : 16;
-    if (launch_pdl(attend_kernel<FMT, HD, MT>, dim3((unsigned)p.grid), dim3(kThreads), 0, stream,
-                   p) != cudaSuccess)
+    constexpr size_t kBytes = sizeof(Smem<FMT, HD, MT>);
+    static std::atomic<uint64_t> configured{0};  // a bit per device
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (!(configured.load(std::memory_order_relaxed) & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            attend_kernel<FMT, HD, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes);
+        if (e != cudaSuccess) {
+            note_cuda_error(e);
+            return ATTN_ERR_CUDA;
+        }
+        configured.fetch_or(bit, std::memory_order_relaxed);
+    }
+    if (launch_pdl(attend_kernel<FMT, HD, MT>, dim3((unsigned)p.grid), dim3(kThreads), kBytes,
+                   stream, p) != cudaSuccess)
         return ATTN_ERR_CUDA;
     if (!merge) return ATTN_OK;
     const int64_t warps = (int64_t)p.n_entries * p.n_kv_heads * RB;
@@ -829,8 +961,7 @@ int plan_attend(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
     plan->per_launch = (int)std::max<int64_t>(
         1, std::min<int64_t>(std::min<int64_t>(entries, att::kMaxEntries),
                              (int64_t(1) << 30) / per_entry));
-    const bool bf16 = cache->dtype == ATTN_KV_BF16;
-    const int per_sm = bf16 ? (plan->mt == 0 ? 3 : 2) : (plan->mt == 0 ? 4 : 3);
+    const int per_sm = cache->dtype == ATTN_KV_BF16 && head_dim == 128 ? 2 : 4;
     const int64_t needed = ((int64_t)plan->per_launch * (usual + att::kGapChunks) * n_kv_heads +
                             att::kMinChunks - 1) / att::kMinChunks;
     plan->grid = (int)std::max<int64_t>(
@@ -868,6 +999,14 @@ int launch_attend(const AttendPlan &plan, const void *q, const attn_kv_cache *ca
     p.block_size = cache->block_size;
     p.max_blocks = cache->max_blocks_per_seq;
     p.num_pages = cache->kind == ATTN_CACHE_PAGED ? (int)(cache->num_slots / cache->block_size) : 0;
+    if (cache->kind == ATTN_CACHE_PAGED && cache->block_size % att::kChunk == 0) {
+        // n / d as n m / 2^(28 + s), m = floor(2^(28 + s) / d) + 1, 2^s >= d: m is at most 1
+        // too large, so the quotient at most n / 2^(28 + s) < 1 / d, and its floor is exact
+        const uint32_t d = (uint32_t)(cache->block_size / att::kChunk);
+        while ((1u << p.page_shift) < d) ++p.page_shift;
+        p.page_mul = (uint32_t)((uint64_t(1) << (28 + p.page_shift)) / d + 1);
+        p.page_chunks = (int)d;
+    }
     p.head_major = cache->layout == ATTN_LAYOUT_BHSD;
     p.block_table = cache->kind == ATTN_CACHE_PAGED ? cache->block_table : nullptr;
     p.seq_lens = seq_lens;

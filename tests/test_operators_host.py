@@ -93,6 +93,7 @@ def test_sinks_refusals(lib):  # noqa: F811
     assert decode_rc(lib, bf(gq.RING), W=500, S=12, ws_bytes=8) == gq.ATTN_ERR_WORKSPACE
     assert decode_rc(lib, bf(gq.RING), W=0, S=4) == gq.ATTN_ERR_SHAPE
     assert decode_rc(lib, bf(), W=64, S=4, ws=None) == gq.ATTN_ERR_NULL
+    assert decode_rc(lib, bf(k=4104), W=64, S=4) == gq.ATTN_ERR_ALIGN
     assert decode_rc(lib, bf(), W=64, S=4, D=96) == gq.ATTN_ERR_UNSUPPORTED
     assert decode_rc(lib, bf(), W=64, S=4, scale=-1.0) == gq.ATTN_ERR_SHAPE
     assert decode_rc(lib, bf(), W=64, S=4, L=0) == gq.ATTN_ERR_SHAPE
