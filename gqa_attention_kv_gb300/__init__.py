@@ -361,9 +361,9 @@ def attn_decode_sinks(q, cache: KVCache, seq_lens, positions, max_seq_len, windo
     """attn_decode under a sliding window whose first n_sinks tokens stay
     visible: a row at position pos attends t <= pos with t < n_sinks or
     pos - t < window (window <= 0: every t).  RING caches keep the sinks in
-    each request's first n_sinks slots and turn the others.  The workspace
-    (at least attn_decode_sinks_workspace_size bytes) needs no zeroing; it is
-    allocated if not given."""
+    each request's first n_sinks slots and turn the others.  A workspace (at
+    least attn_decode_sinks_workspace_size bytes, zero-filled before its first
+    use) is allocated if not given."""
     import torch
 
     B, R, Hq, D = q.shape
@@ -371,7 +371,7 @@ def attn_decode_sinks(q, cache: KVCache, seq_lens, positions, max_seq_len, windo
         out = torch.empty_like(q)
     if workspace is None:
         need = attn_decode_sinks_workspace_size(cache, B, R, Hq, max_seq_len, window, n_sinks)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+        workspace = torch.zeros(need, dtype=torch.uint8, device=q.device) if need > 0 else None
     c = cache.struct()
     rc = lib().attn_decode_sinks(
         _ptr(q), ctypes.byref(c), _ptr(seq_lens), _ptr(positions), B, R, int(max_seq_len),

@@ -50,8 +50,9 @@ constexpr int kChunk = 16;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxEntries = 128;  // (request, row block) pairs per launch
-constexpr int kGapChunks = 8;     // what a change of unit costs a CTA, in chunks
+constexpr int kGapChunks = 24;    // what a change of unit costs a CTA, in chunks
 constexpr int kMinChunks = 8;     // smallest share of a CTA
+constexpr int kKernelParts = 12;  // parts of a unit that its last block adds up
 constexpr float kRescaleLog2 = 8.0f;  // the reference maximum moves past this only (w <= 2^8)
 constexpr float kScaleFloor = 5.421010862427522e-20f;  // 2^-64, the smallest scale
 
@@ -75,11 +76,12 @@ struct Params {
     int grid;
     float scale_log2;
     float *ws_o, *ws_lse;
-    int2 *ws_parts;  // per unit: first and last CTA
+    int2 *ws_parts;     // per unit: first and last CTA (merge kernel)
+    int32_t *ws_count;  // per unit: parts stored (0 between calls), or nullptr: merge kernel
     int32_t *err;
 };
 
-// A stage of a warp's ring: the K rows and the V rows of NSUB chunks.  Thread
+// A stage of a warp's ring: the K rows and the V rows of a step, NSUB chunks.  Thread
 // (gq, tq) reads pieces tq + 4 j of K rows gq and gq + 8, and piece gq (+ 8 j)
 // of V rows 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9; rows are swizzled so that the
 // lanes of one access meet different banks.
@@ -94,14 +96,14 @@ struct Geo {
     static constexpr int kVPieces = kRowBytes / (8 * kVBytes);
     static constexpr int kVWords = kVBytes / 4 * kVPieces;       // words of a key a thread
     static constexpr int kVElems = kVBytes / E;                  // dims of a V piece
-    static constexpr int NSUB = kRowBytes == 64 ? 2 : 1;
+    static constexpr int NSUB = kRowBytes == 64 ? 2 : 1;         // chunks of a step
     static constexpr int kChunkBytes = kChunk * kRowBytes;
-    static constexpr int kStageBytes = 2 * NSUB * kChunkBytes;
+    static constexpr int kStepBytes = NSUB * kChunkBytes;        // K (or V) of a step
     static constexpr int kStages = 3;
-    static constexpr int CTAS = kRowBytes == 256 ? 2 : 4;        // blocks of an SM
+    static constexpr int CTAS = kRowBytes == 256 ? 2 : FMT == kBF16 ? 3 : 4;  // blocks of an SM
     static constexpr int kGroup = kWarps * NSUB;                 // chunks of a block's step
-    static constexpr int kRingBytes = kStages * kStageBytes;     // of one warp
     static constexpr int kOStride = HD + 4;                      // floats of a parked output row
+    static constexpr int kRingBytes = kStages * 2 * kStepBytes;  // of one warp
     static_assert(RB * kOStride * 4 <= kRingBytes, "a warp's outputs are parked in its ring");
 };
 
@@ -131,8 +133,16 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, bool on
                  "r"(on ? 16 : 0)
                  : "memory");
 }
+__device__ __forceinline__ void cp_async_16_to(uint32_t dst, const uint8_t *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy4(uint32_t dst, const float *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -143,6 +153,15 @@ __device__ __forceinline__ void copies_wait() {
 // Four 8-bit codes -> two f16x2 words (bytes 0, 1 and bytes 2, 3); exact.
 // INT8: a byte with its sign bit flipped is c + 128; behind the byte 0x64 it is
 // the f16 1024 + (c + 128), from which 1152 is subtracted without rounding.
+// Four codes of a key -> two f16x2 words for Q K^T.  INT8: a byte with its sign
+// bit flipped, c + 128, is the f16 (c + 128) 2^-24, a subnormal the tensor
+// cores take exactly; the accumulators start at -128 2^-24 sum(q), so a score
+// comes out as 2^-24 q . c.  (V keeps the subtraction: there the offset would
+// be carried through every key's addition to O.)
+template <int FMT>
+__device__ __forceinline__ void key_codes_to_f16(uint32_t x, uint32_t &lo, uint32_t &hi);
+constexpr uint32_t kMinus128 = 0x80808080u;  // f16x2 of -128 2^-24
+
 template <int FMT>
 __device__ __forceinline__ void codes_to_f16(uint32_t x, uint32_t &lo, uint32_t &hi) {
     if constexpr (FMT == kE4M3) {
@@ -160,6 +179,17 @@ __device__ __forceinline__ void codes_to_f16(uint32_t x, uint32_t &lo, uint32_t 
     }
 }
 
+template <int FMT>
+__device__ __forceinline__ void key_codes_to_f16(uint32_t x, uint32_t &lo, uint32_t &hi) {
+    if constexpr (FMT == kINT8) {
+        x ^= 0x80808080u;
+        lo = __byte_perm(x, 0u, 0x4140u);
+        hi = __byte_perm(x, 0u, 0x4342u);
+    } else {
+        codes_to_f16<FMT>(x, lo, hi);
+    }
+}
+
 // Whether a word of V holds a value that is not finite.
 template <int FMT>
 __device__ __forceinline__ bool word_not_finite(uint32_t w) {
@@ -169,6 +199,17 @@ __device__ __forceinline__ bool word_not_finite(uint32_t w) {
         return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u;
     else
         return false;
+}
+
+__device__ __forceinline__ float fast_log2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 template <int FMT>
@@ -228,27 +269,99 @@ __device__ __forceinline__ Entry make_entry(const Params &p, int e, int rb_rows,
     return t;
 }
 
-// What a warp notes about a chunk in its ring.
-struct Note {
-    uint32_t mask;  // keys present
-    float ks, vs;
-    uint32_t pad;
+// What a warp notes about a step in its ring: whether every key of it is there,
+// else the keys of each chunk that are; the scales of its chunks.
+template <int NSUB>
+struct __align__(16) Note {
+    uint32_t full, mask[NSUB];
+    float scale[NSUB][2];
 };
 
 template <int FMT, int HD, int MT>
 struct __align__(16) Smem {
     using G = Geo<FMT, HD, MT>;
-    // a warp's ring; at the end of a unit its output rows (float [RB][kOStride])
-    uint8_t ring[kWarps][G::kRingBytes];
+    uint8_t buf[kWarps][G::kRingBytes];  // at the end of a unit a warp's output rows
     uint32_t q[HD / 16][32][MT == 0 ? 2 : 4];  // q fragments of a unit, as a lane reads them
-    Note note[kWarps][G::kStages][G::NSUB];
+    Note<G::NSUB> note[kWarps][G::kStages];
     float m[kWarps][G::RB], l[kWarps][G::RB], w[kWarps][G::RB], lse[G::RB];
     Entry entry[kMaxEntries];
     int prefix[kMaxEntries + 1];
+    int last_part;
     __device__ __forceinline__ float *out_row(int warp, int row) {
-        return reinterpret_cast<float *>(ring[warp]) + row * G::kOStride;
+        return reinterpret_cast<float *>(buf[warp]) + row * G::kOStride;
     }
 };
+
+// The rows of a unit from its parts first .. last, by a block's four warps: rows
+// warp, warp + 4, ... each, a lane HD / 32 dims of every row.  The log-sum-exps
+// of 32 parts come in one load a row; the parts' outputs then wait for nothing.
+template <int HD, int RB>
+__device__ __forceinline__ void merge_unit(const Params &p, int64_t unit, int first, int last,
+                                           int row0, int n_rows, int b, int kvh) {
+    constexpr int V = HD / 32, R = RB / kWarps;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float m[R], sum[R], acc[R][V];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        m[r] = -INFINITY, sum[r] = 0.f;
+#pragma unroll
+        for (int d = 0; d < V; ++d) acc[r][d] = 0.f;
+    }
+    for (int c0 = first; c0 <= last; c0 += 32) {
+        const int n = min(32, last - c0 + 1);
+        float f[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int row = warp + kWarps * r;
+            f[r] = lane < n && row < n_rows ? __ldcg(p.ws_lse + (unit + c0 + lane) * RB + row)
+                                            : -INFINITY;
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float mx = f[r];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float m_new = fmaxf(m[r], mx), m_use = m_new == -INFINITY ? 0.f : m_new;
+            const float old = fast_exp2(m[r] - m_use);
+            f[r] = fast_exp2(f[r] - m_use);
+            m[r] = m_new;
+            sum[r] *= old;
+#pragma unroll
+            for (int d = 0; d < V; ++d) acc[r][d] *= old;
+        }
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int row = min(warp + kWarps * r, n_rows - 1);
+                const float w = __shfl_sync(0xffffffffu, f[r], k);
+                const float *src = p.ws_o + ((unit + c0 + k) * RB + row) * HD + lane * V;
+                sum[r] += w;
+                if constexpr (V == 4) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+                    acc[r][0] += w * x.x, acc[r][1] += w * x.y;
+                    acc[r][2] += w * x.z, acc[r][3] += w * x.w;
+                } else {
+                    const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
+                    acc[r][0] += w * x.x, acc[r][1] += w * x.y;
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int row = warp + kWarps * r;
+        if (row >= n_rows) continue;
+        const float inv = sum[r] == 0.f ? 0.f : 1.f / sum[r];
+        const int q_row = row0 + row, qr = q_row / p.group;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(
+            p.out + (((int64_t)b * p.q_rows + qr) * p.n_q_heads + kvh * p.group +
+                     (q_row - qr * p.group)) * HD + lane * V);
+#pragma unroll
+        for (int d = 0; d < V / 2; ++d)
+            dst[d] = pack_bf16x2(acc[r][2 * d] * inv, acc[r][2 * d + 1] * inv);
+    }
+}
 
 template <int FMT, int HD, int MT>
 __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
@@ -296,7 +409,8 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
             const int e = p.e0 + i, b = e / p.row_blocks, rb = e - b * p.row_blocks;
             const int row0 = rb * RB, n = min(p.rows, row0 + RB) - row0;
             for (int kvh = 0; kvh < p.n_kv_heads; ++kvh) {
-                if (lane == 0) p.ws_parts[i * p.n_kv_heads + kvh] = make_int2(0, -1);
+                if (lane == 0 && p.ws_count == nullptr)
+                    p.ws_parts[i * p.n_kv_heads + kvh] = make_int2(0, -1);
                 for (int j = lane; j < n * (HD / 8); j += 32) {
                     const int row = row0 + j / (HD / 8), r = row / p.group, gr = row - r * p.group;
                     reinterpret_cast<uint4 *>(
@@ -331,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
         const int e = p.e0 + lo_e, b = e / p.row_blocks, rb = e - b * p.row_blocks;
         const int row0 = rb * RB, n_rows = min(p.rows, row0 + RB) - row0;
 
-        // ---- q fragments and positions
+        // ---- q rows
         const __nv_bfloat16 *qb =
             p.q + ((int64_t)b * p.q_rows * p.n_q_heads + kvh * p.group) * HD;
         auto row_of = [&](int rr) {  // row rr of the unit, in q and out
@@ -341,32 +455,11 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
         auto pos_of = [&](int rr) {
             return p.positions[(int64_t)b * p.q_rows + (row0 + min(rr, n_rows - 1)) / p.group];
         };
-        constexpr int kQRows = MT == 0 ? 1 : 2;
-        bool q_big = false;
-        for (int kk = warp; kk < kSteps; kk += kWarps) {
-            const int j = kk / G::kStepsPerPiece, st = kk % G::kStepsPerPiece;
-            const int d0 = (16 / G::E) * (tq + 4 * j) + 4 * st;
-#pragma unroll
-            for (int hr = 0; hr < kQRows; ++hr) {
-                uint2 x = *reinterpret_cast<const uint2 *>(qb + row_of(gq + 8 * hr) + d0);
-                if constexpr (FMT != kBF16) {  // f16 holds |q| < 65520
-                    x.x = bf16x2_to_f16x2(x.x);
-                    x.y = bf16x2_to_f16x2(x.y);
-                    q_big |= (x.x & 0x7C00u) == 0x7C00u || (x.x & 0x7C000000u) == 0x7C000000u ||
-                             (x.y & 0x7C00u) == 0x7C00u || (x.y & 0x7C000000u) == 0x7C000000u;
-                }
-                sm.q[kk][lane][hr] = x.x;
-                sm.q[kk][lane][kQRows + hr] = x.y;
-            }
-        }
-        if (q_big) report_error(p.err, ATTN_ERR_UNSUPPORTED);
-        int rpos[2];  // positions of the two rows this thread keeps scores of
-        rpos[0] = MT == 0 ? pos_of(2 * tq) : pos_of(gq);
-        rpos[1] = MT == 0 ? pos_of(2 * tq + 1) : pos_of(gq + 8);
-        __syncthreads();
+        // the row (0 or 1 of the thread's two) of accumulator element e
+        auto row_e = [](int e) { return MT == 0 ? (e & 1) : (e >> 1); };
 
         // ---- where chunks lie
-        constexpr int NSUB = G::NSUB, kStages = G::kStages;
+        constexpr int NSUB = G::NSUB;
         const int32_t *bt = p.block_table + (int64_t)b * p.max_blocks;
         const int blk_rows = p.kind == ATTN_CACHE_PAGED ? p.block_size : p.slots_per_seq;
         const uint32_t row_step = p.head_major ? 1u : (uint32_t)p.n_kv_heads;
@@ -399,126 +492,235 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
         for (auto &x : o) x[0] = x[1] = x[2] = x[3] = 0.f;
         float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
 
-        // ---- copies of a step's keys into stage `st` (nothing past c_end)
+        // ---- copies of a step's keys
         constexpr int kPer = G::kRowBytes / 16;  // 16-byte pieces of a row
         constexpr int kRowsPer = 32 / kPer;      // rows of one copy instruction
         const int my_row = lane / kPer, my_piece = lane % kPer;
-        const uint32_t ring = smem_u32(sm.ring[warp]);
+        const uint32_t ring = smem_u32(sm.buf[warp]);
+        // this lane's first piece of an evenly spaced chunk, and from one to the next
+        const uint32_t lane_at = my_row * row_step * G::kRowBytes + my_piece * 16;
+        const uint8_t *const k_lane = p.k + lane_at, *const v_lane = p.v + lane_at;
+        const uint32_t copy_step = kRowsPer * row_step * G::kRowBytes;
+        const uint32_t k_to = k_offset<G::kRowBytes>(my_row, my_piece);
+        const uint32_t v_to = v_offset<G::kRowBytes>(my_row, my_piece);
+        // where this thread reads its share of K and V in a chunk
+        const uint32_t k_from = k_offset<G::kRowBytes>(gq, tq);
+        const uint32_t v_from = G::kVBytes == 8
+                                    ? v_offset<G::kRowBytes>(2 * tq, gq >> 1) + 8 * (gq & 1)
+                                    : v_offset<G::kRowBytes>(2 * tq, gq);
+        // where position t of a ring lies in it
+        auto ring_row = [&](int t) {
+            return t < p.sinks ? t : p.sinks + (t - p.sinks) % (p.slots_per_seq - p.sinks);
+        };
+        // an evenly spaced chunk's first row; false (and reported) for a page outside the pool
+        auto find = [&](int rc, int id, uint32_t &row, int &slot) {
+            if (p.kind == ATTN_CACHE_RING) {
+                row = row_index(b, ring_row(rc * kChunk));
+                slot = 0;
+                return true;
+            }
+            if (p.kind != ATTN_CACHE_PAGED) {
+                row = row_index(b, rc * kChunk);
+                slot = b * p.slots_per_seq + rc * kChunk;
+                return true;
+            }
+            const bool good = (unsigned)id < (unsigned)p.num_pages;
+            if (!good) {
+                if (lane == 0) report_error(p.err, ATTN_ERR_BOUNDS);
+                id = 0;
+            }
+            const int r = (rc - page_of_chunk(rc) * p.page_chunks) * kChunk;
+            row = row_index(id, r);
+            slot = id * p.block_size + r;
+            return good;
+        };
+        // requests step c (nothing past c_end) into stage st
         auto request = [&](int c, int st) {
+            const uint32_t k_buf = ring + st * 2 * G::kStepBytes, v_buf = k_buf + G::kStepBytes;
+            Note<NSUB> &note = sm.note[warp][st];
+            auto read_scales = [&](int i, int slot) {
+                if constexpr (FMT != kBF16)
+                    if (p.ks != nullptr && lane < 2)
+                        copy4(smem_u32(&note.scale[i][lane]),
+                              (lane == 0 ? p.ks : p.vs) +
+                                  (int64_t)(slot >> p.scale_shift) * p.n_kv_heads + kvh);
+            };
+            const int rc0 = real_chunk(c), t0 = rc0 * kChunk, t1 = t0 + NSUB * kChunk;
+            bool full = (even || p.kind == ATTN_CACHE_RING) && c + NSUB <= c_end &&
+                        (c >= ch.sc || c + NSUB <= ch.sc) && t1 <= en.hi &&
+                        (t0 >= en.lo || t1 <= p.sinks);
+            if (p.kind == ATTN_CACHE_RING)  // within the sinks, or the turning part without its end
+                full &= t1 <= p.sinks ||
+                        (t0 >= p.sinks && ring_row(t0) + NSUB * kChunk <= p.slots_per_seq);
+            if (full) {
+                uint32_t top[NSUB];  // each chunk's first row
+                int slot[NSUB];
 #pragma unroll
-            for (int i = 0; i < NSUB; ++i) {
-                if (c + i < c_end) {
-                    const int rc = real_chunk(c + i), t0 = rc * kChunk;
-                    uint32_t mask = chunk_mask(t0), first = 0, spread = 0;
-                    int slot = 0;
-                    if (even) {
-                        if (p.kind == ATTN_CACHE_PAGED) {
-                            int id = page[i];
-                            if ((unsigned)id >= (unsigned)p.num_pages) {
-                                if (lane == 0) report_error(p.err, ATTN_ERR_BOUNDS);
-                                mask = 0, id = 0;
-                            }
-                            const int r = (rc - page_of_chunk(rc) * p.page_chunks) * kChunk;
-                            first = row_index(id, r);
-                            slot = id * p.block_size + r;
-                        } else {
-                            first = row_index(b, t0);
-                            slot = b * p.slots_per_seq + t0;
-                        }
-                    } else {
-                        const int t = t0 + (lane & 15);
-                        bool on = (mask >> (lane & 15)) & 1u;
-                        if (on) {
-                            if (p.kind == ATTN_CACHE_PAGED) {
-                                const int pi = t / p.block_size, id = __ldg(bt + pi);
-                                if ((unsigned)id >= (unsigned)p.num_pages) {
-                                    report_error(p.err, ATTN_ERR_BOUNDS);
-                                    on = false;
-                                } else {
-                                    spread = row_index(id, t - pi * p.block_size);
-                                }
-                            } else {
-                                spread = row_index(b, t < p.sinks
-                                                          ? t
-                                                          : p.sinks + (t - p.sinks) %
-                                                                          (p.slots_per_seq - p.sinks));
-                            }
-                        }
-                        mask = __ballot_sync(0xffffffffu, on) & 0xFFFFu;
-                    }
-                    const uint32_t k_dst = ring + st * G::kStageBytes + 2 * i * G::kChunkBytes;
-                    const uint32_t v_dst = k_dst + G::kChunkBytes;
+                for (int i = 0; i < NSUB; ++i) full &= find(rc0 + i, page[i], top[i], slot[i]);
+                if (full) {
 #pragma unroll
-                    for (int n = 0; n < kChunk / kRowsPer; ++n) {
-                        const int r = my_row + n * kRowsPer;
-                        const uint32_t row = even ? first + r * row_step
-                                                  : __shfl_sync(0xffffffffu, spread, r);
-                        const bool on = (mask >> r) & 1u;
-                        // a row that is not copied has no address of its own
-                        const uint64_t at =
-                            on ? (uint64_t)row * G::kRowBytes + my_piece * 16 : (uint64_t)0;
-                        copy16(k_dst + k_offset<G::kRowBytes>(r, my_piece), p.k + at, on);
-                        copy16(v_dst + v_offset<G::kRowBytes>(r, my_piece), p.v + at, on);
-                    }
-                    Note &note = sm.note[warp][st][i];
-                    if (lane == 0) note.mask = mask;
-                    if constexpr (FMT != kBF16) {
-                        if (p.ks == nullptr || mask == 0) {
-                            if (lane == 0) note.ks = note.vs = 1.f;
-                        } else if (lane < 2) {
-                            const int64_t at =
-                                (int64_t)(slot >> p.scale_shift) * p.n_kv_heads + kvh;
-                            copy4(smem_u32(lane == 0 ? &note.ks : &note.vs),
-                                  (lane == 0 ? p.ks : p.vs) + at);
+                    for (int i = 0; i < NSUB; ++i) {
+                        const uint64_t at = (uint64_t)top[i] * G::kRowBytes;
+                        const uint8_t *ks = k_lane + at, *vs = v_lane + at;
+#pragma unroll
+                        for (int n = 0; n < kChunk / kRowsPer; ++n) {
+                            // v_offset of row my_row + n kRowsPer against my_row's
+                            const int flip = G::kRowBytes == 128   ? 64 * (n & 1)
+                                             : G::kRowBytes == 256 ? 32 * (n & 3)
+                                                                   : 0;
+                            const int to = i * G::kChunkBytes + n * 512;
+                            cp_async_16_to(k_buf + k_to + to, ks);
+                            cp_async_16_to(v_buf + (v_to ^ flip) + to, vs);
+                            ks += copy_step;
+                            vs += copy_step;
                         }
+                        read_scales(i, slot[i]);
                     }
                 }
             }
-            copies_commit();
+            if (lane == 0) note.full = full;
+            if (!full) {
+                // key by key; keys that are absent become zeros
+#pragma unroll
+                for (int i = 0; i < NSUB; ++i) {
+                    const bool in = c + i < c_end;
+                    const int rc = real_chunk(c + i), t = rc * kChunk + (lane & 15);
+                    uint32_t mask = in ? chunk_mask(rc * kChunk) : 0u, top = 0, spread = 0;
+                    if (even && in) {
+                        int slot;
+                        if (!find(rc, page[i], top, slot)) mask = 0;  // (page 0's scales)
+                        read_scales(i, slot);
+                    } else if (FMT != kBF16 && lane < 2) {
+                        note.scale[i][lane] = 1.f;
+                    }
+                    if (!even) {
+                        bool on = (mask >> (lane & 15)) & 1u;
+                        if (on && p.kind == ATTN_CACHE_PAGED) {
+                            const int pi = t / p.block_size, id = __ldg(bt + pi);
+                            if ((unsigned)id >= (unsigned)p.num_pages) {
+                                report_error(p.err, ATTN_ERR_BOUNDS);
+                                on = false;
+                            } else {
+                                spread = row_index(id, t - pi * p.block_size);
+                            }
+                        } else if (on) {
+                            spread = row_index(b, ring_row(t));
+                        }
+                        mask = __ballot_sync(0xffffffffu, on) & 0xFFFFu;
+                    }
+                    if (lane == 0) note.mask[i] = mask;
+#pragma unroll
+                    for (int n = 0; n < kChunk / kRowsPer; ++n) {
+                        const int r = my_row + n * kRowsPer;
+                        const uint32_t row = even ? top + r * row_step
+                                                  : __shfl_sync(0xffffffffu, spread, r);
+                        const bool on = (mask >> r) & 1u;
+                        const uint64_t at =
+                            on ? (uint64_t)row * G::kRowBytes + my_piece * 16 : (uint64_t)0;
+                        const int to = i * G::kChunkBytes;
+                        copy16(k_buf + to + k_offset<G::kRowBytes>(r, my_piece), p.k + at, on);
+                        copy16(v_buf + to + v_offset<G::kRowBytes>(r, my_piece), p.v + at, on);
+                    }
+                }
+            }
         };
 
         const int c0 = off + warp * NSUB;
         read_pages(c0);
 #pragma unroll
-        for (int st = 0; st < kStages - 1; ++st) {
-            request(c0 + st * G::kGroup, st);
-            read_pages(c0 + (st + 1) * G::kGroup);
+        for (int st = 0; st < G::kStages - 1; ++st) {
+            const int c = c0 + st * G::kGroup;
+            if (c < c_end) request(c, st);
+            copies_commit();
+            read_pages(c + G::kGroup);
+        }
+        // ---- q fragments and positions, while the first keys are under way
+        constexpr int kQRows = MT == 0 ? 1 : 2;
+        bool q_big = false;
+        for (int kk = warp; kk < kSteps; kk += kWarps) {
+            const int j = kk / G::kStepsPerPiece, st = kk % G::kStepsPerPiece;
+            const int d0 = (16 / G::E) * (tq + 4 * j) + 4 * st;
+#pragma unroll
+            for (int hr = 0; hr < kQRows; ++hr) {
+                uint2 x = *reinterpret_cast<const uint2 *>(qb + row_of(gq + 8 * hr) + d0);
+                if constexpr (FMT != kBF16) {  // f16 holds |q| < 65520
+                    x.x = bf16x2_to_f16x2(x.x);
+                    x.y = bf16x2_to_f16x2(x.y);
+                    q_big |= (x.x & 0x7C00u) == 0x7C00u || (x.x & 0x7C000000u) == 0x7C000000u ||
+                             (x.y & 0x7C00u) == 0x7C00u || (x.y & 0x7C000000u) == 0x7C000000u;
+                }
+                sm.q[kk][lane][hr] = x.x;
+                sm.q[kk][lane][kQRows + hr] = x.y;
+            }
+        }
+        if (q_big) report_error(p.err, ATTN_ERR_UNSUPPORTED);
+        int rpos[2];  // positions of the two rows this thread keeps scores of
+        rpos[0] = MT == 0 ? pos_of(2 * tq) : pos_of(gq);
+        rpos[1] = MT == 0 ? pos_of(2 * tq + 1) : pos_of(gq + 8);
+        __syncthreads();
+
+        float q_bias[2] = {0.f, 0.f};  // -128 2^-24 sum(q) of the two rows
+        if constexpr (FMT == kINT8) {
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint32_t a[4] = {kMinus128, kMinus128, kMinus128, kMinus128};
+#pragma unroll
+            for (int kk = 0; kk < kSteps; ++kk) {
+                if constexpr (MT == 0) {
+                    mma_f16_16816(sum, a, sm.q[kk][lane][0], sm.q[kk][lane][1]);
+                } else {
+                    const uint32_t qa[4] = {sm.q[kk][lane][0], sm.q[kk][lane][1],
+                                            sm.q[kk][lane][2], sm.q[kk][lane][3]};
+                    mma_f16_16816(sum, qa, kMinus128, kMinus128);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) q_bias[row_e(e)] = sum[e];
         }
         int st = 0;
-        for (int c = c0; c < c_end; c += G::kGroup, st = st + 1 == kStages ? 0 : st + 1) {
-            copies_wait<kStages - 2>();
+        for (int c = c0; c < c_end; c += G::kGroup, st = st + 1 == G::kStages ? 0 : st + 1) {
+            copies_wait<G::kStages - 2>();
             __syncwarp();  // the step has landed for all lanes, and the step before is read
-            request(c + (kStages - 1) * G::kGroup, st == 0 ? kStages - 1 : st - 1);
-            read_pages(c + kStages * G::kGroup);
-            const uint8_t *stage = sm.ring[warp] + st * G::kStageBytes;
-            uint32_t cur_mask[NSUB];
+            if (c + (G::kStages - 1) * G::kGroup < c_end)
+                request(c + (G::kStages - 1) * G::kGroup, st == 0 ? G::kStages - 1 : st - 1);
+            copies_commit();
+            read_pages(c + G::kStages * G::kGroup);
+            const uint32_t k_buf = ring + st * 2 * G::kStepBytes, v_buf = k_buf + G::kStepBytes;
+            const Note<NSUB> &note = sm.note[warp][st];
+            const bool cur_full = note.full != 0;
             float cur_sk[NSUB], cur_sv[NSUB];
             uint32_t kw[NSUB][2][4 * G::kKPieces];
 #pragma unroll
             for (int i = 0; i < NSUB; ++i) {
-                const bool in = c + i < c_end;
-                const Note note = sm.note[warp][st][i];
-                cur_mask[i] = in ? note.mask : 0u;
-                cur_sk[i] = in && FMT != kBF16 ? note.ks : 1.f;
-                cur_sv[i] = in && FMT != kBF16 ? fmaxf(note.vs, kScaleFloor) : 1.f;
+                cur_sk[i] = cur_sv[i] = 1.f;
+                if (FMT != kBF16 && p.ks != nullptr) {
+                    cur_sk[i] = fmaxf(note.scale[i][0], kScaleFloor);
+                    cur_sv[i] = fmaxf(note.scale[i][1], kScaleFloor);
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int j = 0; j < G::kKPieces; ++j) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(
-                            stage + 2 * i * G::kChunkBytes +
-                            k_offset<G::kRowBytes>(gq + 8 * h, tq + 4 * j));
+                        // piece tq + 4 j of row gq + 8 h
+                        const uint4 x = ld_shared_v4(k_buf + i * G::kChunkBytes +
+                                                     8 * h * G::kRowBytes +
+                                                     (k_from ^ (64 * (j & 1))) + 128 * (j >> 1));
                         kw[i][h][4 * j] = x.x, kw[i][h][4 * j + 1] = x.y;
                         kw[i][h][4 * j + 2] = x.z, kw[i][h][4 * j + 3] = x.w;
                     }
             }
-            // ---- scores: MT 0 keys are the rows of S^T = K Q^T, MT 1 the columns of S = Q K^T
+            // ---- scores: MT 0 keys are the rows of S^T = K Q^T, MT 1 the columns of S = Q K^T.
+            // Even and odd k-steps add up apart: a product waits for half as many before it
             constexpr int NJ = MT == 0 ? 1 : 2;
-            float s[NSUB][NJ][4];
+            float s[NSUB][NJ][4], s_odd[NSUB][NJ][4];
 #pragma unroll
             for (int i = 0; i < NSUB; ++i)
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) s[i][j][0] = s[i][j][1] = s[i][j][2] = s[i][j][3] = 0.f;
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s[i][j][e] = FMT == kINT8 ? q_bias[row_e(e)] : 0.f;
+                        s_odd[i][j][e] = 0.f;
+                    }
 #pragma unroll
             for (int kk = 0; kk < kSteps; ++kk) {
                 uint32_t qf[2 * kQRows];
@@ -538,44 +740,45 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
                             x[h][0] = kw[i][h][2 * kk];
                             x[h][1] = kw[i][h][2 * kk + 1];
                         } else {
-                            codes_to_f16<FMT>(kw[i][h][kk], x[h][0], x[h][1]);
+                            key_codes_to_f16<FMT>(kw[i][h][kk], x[h][0], x[h][1]);
                         }
                     }
                     if constexpr (MT == 0) {
                         const uint32_t a[4] = {x[0][0], x[1][0], x[0][1], x[1][1]};
-                        mma16<FMT>(s[i][0], a, qf[0], qf[1]);
+                        mma16<FMT>(kk & 1 ? s_odd[i][0] : s[i][0], a, qf[0], qf[1]);
                     } else {
-                        mma16<FMT>(s[i][0], qf, x[0][0], x[0][1]);
-                        mma16<FMT>(s[i][1], qf, x[1][0], x[1][1]);
+                        mma16<FMT>(kk & 1 ? s_odd[i][0] : s[i][0], qf, x[0][0], x[0][1]);
+                        mma16<FMT>(kk & 1 ? s_odd[i][1] : s[i][1], qf, x[1][0], x[1][1]);
                     }
                 }
             }
-            // ---- mask and weights.  x(row, key): element e of s[i][j] is
-            // MT 0: row e & 1, key gq + 8 (e >> 1); MT 1: row e >> 1, key 8 j + 2 tq + (e & 1)
-            auto row_e = [](int e) { return MT == 0 ? (e & 1) : (e >> 1); };
-            auto sees = [&](int i, int row, int key) {
-                const int t = real_chunk(c + i) * kChunk + key, pos = rpos[row];
-                return ((cur_mask[i] >> key) & 1u) && t <= pos &&
-                       (p.window <= 0 || pos - t < p.window || t < p.sinks);
-            };
-            float inv_sv[NSUB];
-            bool open = true;  // every row sees every key of the step
 #pragma unroll
-            for (int i = 0; i < NSUB; ++i) {
-                const int t0 = real_chunk(c + i) * kChunk;
-                open &= cur_mask[i] == 0xFFFFu && t0 + kChunk - 1 <= en.pmin &&
-                        (p.window <= 0 || en.pmax - t0 < p.window || t0 + kChunk <= p.sinks);
-                const float f = cur_sk[i] * p.scale_log2;
-                float lv = 0.f;
-                inv_sv[i] = 1.f;
-                if constexpr (FMT != kBF16) {
-                    lv = __log2f(cur_sv[i]);
-                    inv_sv[i] = __fdividef(1.f, cur_sv[i]);
-                }
+            for (int i = 0; i < NSUB; ++i)
 #pragma unroll
                 for (int j = 0; j < NJ; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[i][j][e] = fmaf(s[i][j][e], f, lv);
+                    for (int e = 0; e < 4; ++e) s[i][j][e] += s_odd[i][j][e];
+            // ---- mask and weights.  x(row, key): element e of s[i][j] is
+            // MT 0: row e & 1, key gq + 8 (e >> 1); MT 1: row e >> 1, key 8 j + 2 tq + (e & 1)
+            auto sees = [&](int i, int row, int key) {
+                const int t = real_chunk(c + i) * kChunk + key, pos = rpos[row];
+                return (cur_full || ((note.mask[i] >> key) & 1u)) && t <= pos &&
+                       (p.window <= 0 || pos - t < p.window || t < p.sinks);
+            };
+            float f[NSUB], lv[NSUB], inv_sv[NSUB];
+            const int first_t = real_chunk(c) * kChunk, end_t = first_t + NSUB * kChunk;
+            // every row sees every key of the step
+            const bool open = cur_full && end_t - 1 <= en.pmin &&
+                              (p.window <= 0 || en.pmax - first_t < p.window || end_t <= p.sinks);
+#pragma unroll
+            for (int i = 0; i < NSUB; ++i) {
+                f[i] = cur_sk[i] * (FMT == kINT8 ? p.scale_log2 * 16777216.f : p.scale_log2);
+                lv[i] = 0.f;
+                inv_sv[i] = 1.f;
+                if constexpr (FMT != kBF16) {
+                    lv[i] = fast_log2(cur_sv[i]);
+                    inv_sv[i] = fast_rcp(cur_sv[i]);
+                }
             }
             if (!open) {
 #pragma unroll
@@ -592,13 +795,14 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
             bool moved = false;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
+                // x = s f + lv grows with s (f > 0): its maximum is that of s
                 float mx = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < NSUB; ++i)
-#pragma unroll
-                    for (int j = 0; j < NJ; ++j)
-                        mx = max3(mx, s[i][j][MT == 0 ? r : 2 * r],
-                                  s[i][j][MT == 0 ? r + 2 : 2 * r + 1]);
+                for (int i = 0; i < NSUB; ++i) {
+                    float ms = fmaxf(s[i][0][MT == 0 ? r : 2 * r], s[i][0][MT == 0 ? r + 2 : 2 * r + 1]);
+                    if constexpr (NJ > 1) ms = max3(ms, s[i][1][2 * r], s[i][1][2 * r + 1]);
+                    mx = fmaxf(mx, fmaf(ms, f[i], lv[i]));
+                }
                 if constexpr (MT == 0) {
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
@@ -616,13 +820,14 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
                 l_run[r] *= alpha[r];
 #pragma unroll
                 for (int i = 0; i < NSUB; ++i) {
+                    const float shift = lv[i] - m_use;
                     float sum = 0.f;
 #pragma unroll
                     for (int j = 0; j < NJ; ++j)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             if (row_e(e) == r) {
-                                s[i][j][e] = fast_exp2(s[i][j][e] - m_use);
+                                s[i][j][e] = fast_exp2(fmaf(s[i][j][e], f[i], shift));
                                 sum += s[i][j][e];
                             }
                     l_run[r] = fmaf(sum, inv_sv[i], l_run[r]);
@@ -695,27 +900,20 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
                 uint32_t vw[4][G::kVWords];
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
-                    const uint8_t *src = stage + (2 * i + 1) * G::kChunkBytes;
-                    const int key = 2 * tq + (n & 1) + 8 * (n >> 1);
+                    const uint32_t src =
+                        v_buf + i * G::kChunkBytes + 8 * (n >> 1) * G::kRowBytes;
                     if constexpr (G::kVBytes == 8) {
-                        const uint2 x = *reinterpret_cast<const uint2 *>(
-                            src + v_offset<G::kRowBytes>(key, gq >> 1) + 8 * (gq & 1));
+                        const uint2 x = ld_shared_v2(src + (v_from ^ (64 * (n & 1))));
                         vw[n][0] = x.x, vw[n][1] = x.y;
                     } else {
 #pragma unroll
                         for (int j = 0; j < G::kVPieces; ++j) {
-                            const uint4 x = *reinterpret_cast<const uint4 *>(
-                                src + v_offset<G::kRowBytes>(key, gq + 8 * j));
+                            const uint4 x =
+                                ld_shared_v4(src + v_from + (n & 1) * G::kRowBytes + 128 * j);
                             vw[n][4 * j] = x.x, vw[n][4 * j + 1] = x.y;
                             vw[n][4 * j + 2] = x.z, vw[n][4 * j + 3] = x.w;
                         }
                     }
-                }
-                if (NSUB > 1 && c + i >= c_end) {  // a chunk that the last step does not have
-#pragma unroll
-                    for (int n = 0; n < 4; ++n)
-#pragma unroll
-                        for (int w = 0; w < G::kVWords; ++w) vw[n][w] = 0u;
                 }
                 if constexpr (FMT != kINT8) {
                     if (!open) {
@@ -854,49 +1052,93 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
             }
         }
         if (!whole && threadIdx.x < n_rows) p.ws_lse[slot * RB + threadIdx.x] = sm.lse[threadIdx.x];
-        if (off == 0 && threadIdx.x == 0) p.ws_parts[unit] = make_int2(first, last);
+        if (p.ws_count == nullptr) {
+            if (off == 0 && threadIdx.x == 0) p.ws_parts[unit] = make_int2(first, last);
+        } else if (!whole) {
+            // the block that stores a unit's last part adds them all, in order
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                const bool mine = atom_add_acq_rel_gpu(p.ws_count + unit, 1) == last - first;
+                if (mine) p.ws_count[unit] = 0;
+                sm.last_part = mine;
+            }
+            __syncthreads();
+            if (sm.last_part)
+                merge_unit<HD, RB>(p, unit, first, last, row0, n_rows, b, kvh);
+        }
         __syncthreads();  // the shared states are free again
         g += c_end - off;
     }
 }
 
-// Adds the partial states of every unit that more than one CTA held: a warp
-// per (unit, row), its lanes along the head, parts in CTA order.
-template <int HD, int RB>
+// Adds the partial states of every unit that more than one CTA held, in part
+// order within a warp and in warp order across them.  A row of a unit is read
+// by SPLIT warps, each every SPLIT-th part, its lanes along the head; all of a
+// warp's log-sum-exps come in one load a 32 parts, so its reads of the partial
+// outputs wait for nothing but that.
+template <int HD, int RB, int SPLIT>
 __global__ void __launch_bounds__(256) attend_merge_kernel(const Params p) {
-    pdl_wait();
-    pdl_launch_dependents();
-    constexpr int V = HD / 32;  // dims of a lane
-    const int lane = threadIdx.x & 31;
-    const int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    constexpr int V = HD / 32;           // dims of a lane
+    constexpr int kRows = 8 / SPLIT;     // rows of a block
+    __shared__ float sm_acc[8][HD];
+    __shared__ float sm_m[8], sm_sum[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t i = (int64_t)blockIdx.x * kRows + warp / SPLIT;
     const int64_t unit = i / RB;
     const int row = (int)(i - unit * RB);
-    if (unit >= (int64_t)p.n_entries * p.n_kv_heads) return;
-    const int2 parts = p.ws_parts[unit];
-    if (parts.y <= parts.x) return;
     const int entry = (int)(unit / p.n_kv_heads), kvh = (int)(unit - (int64_t)entry * p.n_kv_heads);
     const int e = p.e0 + entry, b = e / p.row_blocks, rb = e - b * p.row_blocks;
     const int q_row = rb * RB + row;
-    if (q_row >= p.rows) return;
-    float m = -INFINITY;
-    for (int c = parts.x + lane; c <= parts.y; c += 32)
-        m = fmaxf(m, __ldcg(p.ws_lse + (unit + c) * RB + row));
+    pdl_wait();
+    pdl_launch_dependents();
+    int2 parts = make_int2(0, -1);
+    if (entry < p.n_entries && q_row < p.rows) parts = p.ws_parts[unit];
+    const bool live = parts.y > parts.x;
+    if (SPLIT == 1 && !live) return;
+    float m = -INFINITY, sum = 0.f, acc[V] = {};
+    if (live) {
+        for (int c0 = parts.x + warp % SPLIT; c0 <= parts.y; c0 += 32 * SPLIT) {
+            const int mine = c0 + lane * SPLIT;
+            const float lse = mine <= parts.y ? __ldcg(p.ws_lse + (unit + mine) * RB + row) : -INFINITY;
+            float mx = lse;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (m == -INFINITY) m = 0.f;  // no part has a key: every weight below is 0
-    float acc[V] = {}, sum = 0.f;
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float m_new = fmaxf(m, mx), m_use = m_new == -INFINITY ? 0.f : m_new;
+            const float old = m == -INFINITY ? 0.f : fast_exp2(m - m_use);
+            const float f = fast_exp2(lse - m_use);
+            m = m_new;
+            sum *= old;
+#pragma unroll
+            for (int d = 0; d < V; ++d) acc[d] *= old;
+            const int n = min(32, (parts.y - c0) / SPLIT + 1);
+            const float *src = p.ws_o + ((unit + c0) * RB + row) * HD + lane * V;
 #pragma unroll 8
-    for (int c = parts.x; c <= parts.y; ++c) {
-        const int64_t at = (unit + c) * RB + row;
-        const float f = fast_exp2(__ldcg(p.ws_lse + at) - m);
-        sum += f;
-        const float *src = p.ws_o + at * HD + lane * V;
-        if constexpr (V == 4) {
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
-            acc[0] += f * x.x, acc[1] += f * x.y, acc[2] += f * x.z, acc[3] += f * x.w;
-        } else {
-            const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
-            acc[0] += f * x.x, acc[1] += f * x.y;
+            for (int k = 0; k < n; ++k, src += (int64_t)SPLIT * RB * HD) {
+                const float w = __shfl_sync(0xffffffffu, f, k);
+                sum += w;
+                if constexpr (V == 4) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+                    acc[0] += w * x.x, acc[1] += w * x.y, acc[2] += w * x.z, acc[3] += w * x.w;
+                } else {
+                    const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
+                    acc[0] += w * x.x, acc[1] += w * x.y;
+                }
+            }
+        }
+    }
+    if constexpr (SPLIT > 1) {
+#pragma unroll
+        for (int d = 0; d < V; ++d) sm_acc[warp][lane * V + d] = acc[d];
+        if (lane == 0) sm_m[warp] = m, sm_sum[warp] = sum;
+        __syncthreads();
+        if (warp % SPLIT != 0 || !live) return;
+        for (int w = warp + 1; w < warp + SPLIT; ++w) {
+            const float m_new = fmaxf(m, sm_m[w]), m_use = m_new == -INFINITY ? 0.f : m_new;
+            const float fa = fast_exp2(m - m_use), fb = fast_exp2(sm_m[w] - m_use);
+            m = m_new;
+            sum = sum * fa + sm_sum[w] * fb;
+#pragma unroll
+            for (int d = 0; d < V; ++d) acc[d] = acc[d] * fa + sm_acc[w][lane * V + d] * fb;
         }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -925,15 +1167,18 @@ int launch(const Params &p, bool merge, cudaStream_t stream) {
         }
         configured.fetch_or(bit, std::memory_order_relaxed);
     }
-    if (launch_pdl(attend_kernel<FMT, HD, MT>, dim3((unsigned)p.grid), dim3(kThreads), kBytes,
-                   stream, p) != cudaSuccess)
-        return ATTN_ERR_CUDA;
+    const cudaError_t e0 = launch_pdl(attend_kernel<FMT, HD, MT>, dim3((unsigned)p.grid), dim3(kThreads), kBytes,
+                                      stream, p);
+    if (e0 != cudaSuccess) return ATTN_ERR_CUDA;
     if (!merge) return ATTN_OK;
-    const int64_t warps = (int64_t)p.n_entries * p.n_kv_heads * RB;
-    return launch_pdl(attend_merge_kernel<HD, RB>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0,
-                      stream, p) == cudaSuccess
-               ? ATTN_OK
-               : ATTN_ERR_CUDA;
+    // Units that lie in many parts (few units, long contexts) have eight warps a row
+    const int64_t units = (int64_t)p.n_entries * p.n_kv_heads, rows = units * RB;
+    const cudaError_t e =
+        p.grid > 8 * units
+            ? launch_pdl(attend_merge_kernel<HD, RB, 8>, dim3((unsigned)rows), dim3(256), 0, stream, p)
+            : launch_pdl(attend_merge_kernel<HD, RB, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256),
+                         0, stream, p);
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // namespace att
@@ -961,17 +1206,24 @@ int plan_attend(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
     plan->per_launch = (int)std::max<int64_t>(
         1, std::min<int64_t>(std::min<int64_t>(entries, att::kMaxEntries),
                              (int64_t(1) << 30) / per_entry));
-    const int per_sm = cache->dtype == ATTN_KV_BF16 && head_dim == 128 ? 2 : 4;
+    const int per_sm = cache->dtype != ATTN_KV_BF16 ? 4 : head_dim == 64 ? 3 : 2;
     const int64_t needed = ((int64_t)plan->per_launch * (usual + att::kGapChunks) * n_kv_heads +
                             att::kMinChunks - 1) / att::kMinChunks;
     plan->grid = (int)std::max<int64_t>(
         1, std::min<int64_t>(needed, (int64_t)per_sm * device_sm_count()));
-    plan->merge = plan->grid > 1;
     const size_t units = (size_t)plan->per_launch * n_kv_heads, slots = units + plan->grid;
-    // behind the counters of attn_decode's other kernels, which have to stay zero
-    // in a workspace that serves both
+    // How many blocks a unit spans when all are as long as they can be.  Up to
+    // kKernelParts the last of them adds the parts up; a unit in more of them
+    // has the merge kernel's eight warps a row (measured where few requests meet
+    // long contexts: 2 x 4 units of 24k keys in 76 parts)
+    const int64_t share = std::max<int64_t>(
+        att::kMinChunks, (int64_t)units * (usual + att::kGapChunks) / plan->grid);
+    plan->merge = usual / share + 1 > att::kKernelParts;
+    // the counters are attn_decode's (zero between calls: one workspace serves both),
+    // the rest lies behind them
     DecodePlan dp;
     plan_decode(cache, batch, q_rows, n_q_heads, n_kv_heads, head_dim, max_seq_len, window, &dp);
+    plan->count_offset = dp.counter_offset;
     plan->parts_offset = (dp.counter_bytes + 255) & ~size_t(255);
     plan->lse_offset = (plan->parts_offset + units * sizeof(int2) + 255) & ~size_t(255);
     plan->o_offset = (plan->lse_offset + slots * rb * sizeof(float) + 255) & ~size_t(255);
@@ -1024,6 +1276,7 @@ int launch_attend(const AttendPlan &plan, const void *q, const attn_kv_cache *ca
     p.scale_log2 = scale * 1.4426950408889634f;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.ws_parts = reinterpret_cast<int2 *>(ws + plan.parts_offset);
+    p.ws_count = plan.merge ? nullptr : reinterpret_cast<int32_t *>(ws + plan.count_offset);
     p.ws_lse = reinterpret_cast<float *>(ws + plan.lse_offset);
     p.ws_o = reinterpret_cast<float *>(ws + plan.o_offset);
     p.err = err;

@@ -162,8 +162,8 @@ int launch_kv_append_scaled(const void *k_new, const void *v_new, const int64_t 
 struct AttendPlan {
     int mt;  // 0: up to 8 rows per unit, 1: 16
     int row_blocks, entries, per_launch, grid, launches;
-    bool merge;  // units may be cut across CTAs: the merge kernel follows
-    size_t parts_offset, lse_offset, o_offset, workspace;
+    bool merge;  // the parts of a unit are added up by a second kernel
+    size_t count_offset, parts_offset, lse_offset, o_offset, workspace;
 };
 
 // ATTN_OK, or ATTN_ERR_SHAPE for sizes past the kernel's index range.

@@ -300,8 +300,8 @@ int attn_decode_kernel_launches(const attn_kv_cache *cache, int batch, int q_row
  *   taken in f16 (a magnitude of 65520 or more is reported as
  *   ATTN_ERR_UNSUPPORTED), the scales multiply scores and softmax weights in
  *   float32, and the weights are rounded once to f16.  A scale is finite and at
- *   least 2^-64 (a v_scale below reads as 2^-64).  Its workspace needs no
- *   zeroing, and keeps out of the counters of the other caches' calls.
+ *   least 2^-64 (one below reads as 2^-64).  Its workspace
+ *   is like any other's (zero-filled before its first use).
  *   A group of 64 or more query rows (q_rows x n_q_heads / n_kv_heads) over a
  *   linear slot-major bf16 cache is a prefill chunk and computes as
  *   attn_prefill does: P V from f16 softmax weights and f16 values, with the
@@ -456,8 +456,9 @@ int attn_prefill(const void *q, const void *k, const void *v, int batch, int seq
  *   head_dim 128).  A position below 0 marks a row without keys (zeros).  A
  *   value that is not finite reaches only the rows that attend its key.
  *   workspace: at least attn_decode_sinks_workspace_size(...) bytes (which
- *   returns (size_t)-1 for arguments this call would reject), 16-byte aligned;
- *   it needs no zeroing, and one workspace may serve this call and attn_decode.
+ *   returns (size_t)-1 for arguments this call would reject), 16-byte aligned,
+ *   zero-filled before its first use; one workspace may serve this call and
+ *   attn_decode.
  *   Calls whose kernels overlap on the GPU, graphs replayed at the same time
  *   among them, need separate workspaces.
  *   Every other argument and status is attn_decode's.

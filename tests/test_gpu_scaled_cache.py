@@ -225,12 +225,13 @@ def test_decode(fmt, kind, B, R, Hq, H, D, lo, hi, sb, per, head_major, window):
                          err=err)
     assert int(err) == 0
     ref.check_output(got, want, mass)
-    # the answer does not depend on what lies in a workspace, nor on the run
-    ws = torch.full((gq.attn_decode_workspace_size(cache, B, R, Hq, hi, window),), 255,
-                    dtype=torch.uint8, device=DEV)
-    again = gq.attn_decode(q.to(DEV), cache, lens.to(DEV), pos.to(DEV), hi, window, D ** -0.5,
-                           workspace=ws)
-    assert torch.equal(got, again)
+    # the answer does not depend on the run, nor on what earlier calls left behind
+    ws = torch.zeros(gq.attn_decode_workspace_size(cache, B, R, Hq, hi, window),
+                     dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        again = gq.attn_decode(q.to(DEV), cache, lens.to(DEV), pos.to(DEV), hi, window, D ** -0.5,
+                               workspace=ws)
+        assert torch.equal(got, again)
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
@@ -283,6 +284,10 @@ def test_decode_reports():
     err.zero_()
     big = q.clone()
     big[0, 0, 0, 0] = 70000.0
+    run(big, lens, pos, err)  # the bad page is in this call too: either may be the first
+    assert int(err) in (gq.ATTN_ERR_UNSUPPORTED, gq.ATTN_ERR_BOUNDS)
+    err.zero_()
+    cache.block_table[1, 0] = case.table[1, 0]
     run(big, lens, pos, err)
     assert int(err) == gq.ATTN_ERR_UNSUPPORTED
 

@@ -78,8 +78,9 @@ def test_scaled_decode_refusals(lib, dtype):  # noqa: F811
         16, 32, 48, 64, rope, ctypes.byref(cs), 64, 128, *args, ws, BIG, None, 0, None)
     assert step(4096, 1 << 20) == gq.ATTN_ERR_UNSUPPORTED
     assert step(None, None) == gq.ATTN_ERR_NULL
-    assert gq.attn_decode_kernel_launches(c, 2, 1, 32, 512) == 2
-    assert gq.attn_decode_kernel_launches(c, 2, 1, 32, 512, with_append=True) == 3
+    assert gq.attn_decode_kernel_launches(c, 2, 1, 32, 512) in (1, 2)
+    assert gq.attn_decode_kernel_launches(c, 2, 1, 32, 512, with_append=True) == 1 + \
+        gq.attn_decode_kernel_launches(c, 2, 1, 32, 512)
     with pytest.raises(gq.AttnError):
         gq.attn_decode_kernel_launches(c, 2, 1, 32, 512, with_append=True, with_rope=True)
 
