@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from .synth import LINEAR, PAGED, RING  # noqa: F401  (cache-kind constants)
@@ -54,6 +55,10 @@ class _Cache(ctypes.Structure):
                 ("scale_block", ctypes.c_int32)]
 
 
+# _Cache in its C layout: packing it costs half of what building a ctypes structure does
+_PACK = struct.Struct("@iPPqiPiiiPiPPi0P").pack
+
+
 def lib():
     """The loaded library (ctypes.CDLL).  Raises if it has not been built."""
     global _lib
@@ -67,7 +72,7 @@ def lib():
                     "`python -m gqa_attention_kv_gb300.build` (nvcc, sm_103a)")
             L = ctypes.CDLL(LIB_PATH)
             p, i32, i64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
-            cp = ctypes.POINTER(_Cache)
+            cp = p  # attn_kv_cache *: a _Cache by reference, or its bytes
             L.attn_kv_append.argtypes = [p, p, p, i64, cp, i32, i32, p, p]
             L.attn_kv_append.restype = i32
             L.attn_decode_workspace_size.argtypes = [cp, i32, i32, i32, i32, i32, i32, i32]
@@ -192,24 +197,27 @@ class KVCache:
     def num_slots(self):
         return self.k.shape[0] * (self.k.shape[2] if self.layout == ATTN_LAYOUT_BHSD else 1)
 
-    def struct(self) -> _Cache:
-        bt = self.block_table
+    def packed(self) -> bytes:
+        """struct(), as the bytes of the C structure."""
+        bt, ref, ks, vs = self.block_table, self.k_ref, self.k_scale, self.v_scale
         shape = self.k.shape
-        slots = shape[0] * (shape[2] if self.layout == ATTN_LAYOUT_BHSD else 1)
-        return _Cache(self.kind, self.k.data_ptr(), self.v.data_ptr(), slots,
-                      self.slots_per_seq, None if bt is None else bt.data_ptr(),
-                      self.block_size, 0 if bt is None else bt.shape[-1], self.dtype,
-                      None if self.k_ref is None else self.k_ref.data_ptr(), self.layout,
-                      None if self.k_scale is None else self.k_scale.data_ptr(),
-                      None if self.v_scale is None else self.v_scale.data_ptr(),
-                      self.scale_block)
+        return _PACK(self.kind, self.k.data_ptr(), self.v.data_ptr(),
+                     shape[0] * (shape[2] if self.layout == ATTN_LAYOUT_BHSD else 1),
+                     self.slots_per_seq, 0 if bt is None else bt.data_ptr(), self.block_size,
+                     0 if bt is None else bt.shape[-1], self.dtype,
+                     0 if ref is None else ref.data_ptr(), self.layout,
+                     0 if ks is None else ks.data_ptr(), 0 if vs is None else vs.data_ptr(),
+                     self.scale_block)
+
+    def struct(self) -> _Cache:
+        return _Cache.from_buffer_copy(self.packed())
 
 
 def attn_kv_append(k_new, v_new, slot_mapping, cache: KVCache, err=None, stream=None):
     """cache.k[slot_mapping[i]] = k_new[i] (same for v); slot_mapping int64 [n]."""
-    c = cache.struct()
+    c = cache.packed()
     rc = lib().attn_kv_append(_ptr(k_new), _ptr(v_new), _ptr(slot_mapping),
-                              slot_mapping.shape[0], ctypes.byref(c), cache.n_kv_heads,
+                              slot_mapping.shape[0], c, cache.n_kv_heads,
                               cache.head_dim, _ptr(err), _stream(stream))
     _check(rc, "attn_kv_append")
 
@@ -229,8 +237,8 @@ def attn_kv_reference(k, ref=None, stream=None):
 
 def attn_decode_workspace_size(cache: KVCache, batch, q_rows, n_q_heads, max_seq_len,
                                window=0) -> int:
-    c = cache.struct()
-    n = lib().attn_decode_workspace_size(ctypes.byref(c), batch, q_rows, n_q_heads,
+    c = cache.packed()
+    n = lib().attn_decode_workspace_size(c, batch, q_rows, n_q_heads,
                                          cache.n_kv_heads, cache.head_dim, max_seq_len, window)
     if n == ctypes.c_size_t(-1).value:
         raise AttnError(ATTN_ERR_SHAPE, "attn_decode_workspace_size")
@@ -243,8 +251,8 @@ def attn_decode_kernel_launches(cache: KVCache, batch, q_rows, n_q_heads, max_se
     """Kernels one attn_decode (with_append: attn_decode_append; with_rope:
     with a rotary embedding; tables_early: with ATTN_DECODE_TABLES_EARLY)
     call of this shape launches (host-side plan; nothing runs on the device)."""
-    c = cache.struct()
-    n = lib().attn_decode_kernel_launches(ctypes.byref(c), batch, q_rows, n_q_heads,
+    c = cache.packed()
+    n = lib().attn_decode_kernel_launches(c, batch, q_rows, n_q_heads,
                                           cache.n_kv_heads, cache.head_dim, max_seq_len, window,
                                           int(bool(with_append)), int(bool(with_rope)),
                                           ATTN_DECODE_TABLES_EARLY if tables_early else 0)
@@ -268,8 +276,8 @@ def attn_decode(q, cache: KVCache, seq_lens, positions, max_seq_len, window, sca
         need = attn_decode_workspace_size(cache, B, R, Hq, max_seq_len, window)
         if need > 0:
             workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
-    c = cache.struct()
-    rc = lib().attn_decode(_ptr(q), ctypes.byref(c), _ptr(seq_lens), _ptr(positions), B, R,
+    c = cache.packed()
+    rc = lib().attn_decode(_ptr(q), c, _ptr(seq_lens), _ptr(positions), B, R,
                            int(max_seq_len), int(window), Hq, cache.n_kv_heads, D, float(scale),
                            _ptr(out), _ptr(workspace),
                            0 if workspace is None else workspace.numel() * workspace.element_size(),
@@ -299,10 +307,10 @@ def attn_decode_append(q, k_new, v_new, slot_mapping, cache: KVCache, seq_lens, 
         need = attn_decode_workspace_size(cache, B, R, Hq, max_seq_len, window)
         if need > 0:
             workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
-    c = cache.struct()
+    c = cache.packed()
     rc = lib().attn_decode_append(
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), _ptr(rope_inv_freq),
-        ctypes.byref(c), _ptr(seq_lens),
+        c, _ptr(seq_lens),
         _ptr(positions), B, R, int(max_seq_len), int(window), Hq, cache.n_kv_heads, D,
         float(scale), _ptr(out), _ptr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(err),
@@ -337,8 +345,8 @@ def attn_decode_noalloc(q, cache: KVCache, seq_lens, positions, max_seq_len, win
     B, R, Hq, D = q.shape
     if out is None:
         out = torch.empty_like(q)
-    c = cache.struct()
-    rc = f(_ptr(q), ctypes.byref(c), _ptr(seq_lens), _ptr(positions), B, R, int(max_seq_len),
+    c = cache.packed()
+    rc = f(_ptr(q), c, _ptr(seq_lens), _ptr(positions), B, R, int(max_seq_len),
            int(window), Hq, cache.n_kv_heads, D, float(scale), _ptr(out), _ptr(err),
            _stream(stream))
     _check(rc, "attn_decode_noalloc")
@@ -347,8 +355,8 @@ def attn_decode_noalloc(q, cache: KVCache, seq_lens, positions, max_seq_len, win
 
 def attn_decode_sinks_workspace_size(cache: KVCache, batch, q_rows, n_q_heads, max_seq_len,
                                      window, n_sinks) -> int:
-    c = cache.struct()
-    n = lib().attn_decode_sinks_workspace_size(ctypes.byref(c), batch, q_rows, n_q_heads,
+    c = cache.packed()
+    n = lib().attn_decode_sinks_workspace_size(c, batch, q_rows, n_q_heads,
                                                cache.n_kv_heads, cache.head_dim, max_seq_len,
                                                window, n_sinks)
     if n == ctypes.c_size_t(-1).value:
@@ -372,9 +380,9 @@ def attn_decode_sinks(q, cache: KVCache, seq_lens, positions, max_seq_len, windo
     if workspace is None:
         need = attn_decode_sinks_workspace_size(cache, B, R, Hq, max_seq_len, window, n_sinks)
         workspace = torch.zeros(need, dtype=torch.uint8, device=q.device) if need > 0 else None
-    c = cache.struct()
+    c = cache.packed()
     rc = lib().attn_decode_sinks(
-        _ptr(q), ctypes.byref(c), _ptr(seq_lens), _ptr(positions), B, R, int(max_seq_len),
+        _ptr(q), c, _ptr(seq_lens), _ptr(positions), B, R, int(max_seq_len),
         int(window), int(n_sinks), Hq, cache.n_kv_heads, D, float(scale), _ptr(out),
         _ptr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(err),
@@ -462,8 +470,7 @@ def attn_pages_copy(caches, moves, n_moves, err=None, stream=None):
     each of the paged caches (a KVCache, or a list of them, one per layer)."""
     if isinstance(caches, KVCache):
         caches = [caches]
-    arr = (_Cache * max(1, len(caches)))(*[c.struct() for c in caches])
     Hkv, D = (caches[0].n_kv_heads, caches[0].head_dim) if caches else (1, 128)
-    rc = lib().attn_pages_copy(arr, len(caches), Hkv, D, _ptr(moves), _ptr(n_moves),
+    rc = lib().attn_pages_copy(b"".join([c.packed() for c in caches]), len(caches), Hkv, D, _ptr(moves), _ptr(n_moves),
                                moves.shape[0], _ptr(err), _stream(stream))
     _check(rc, "attn_pages_copy")

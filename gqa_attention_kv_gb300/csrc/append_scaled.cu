@@ -45,18 +45,27 @@ struct ScaledParams {
 };
 
 // The code of the exact product x * r, |x * r| < 2^21, as a byte.
+template <bool CLAMP>
 __device__ __forceinline__ uint32_t int8_code(float x, float r) {
     const float big = 12582912.f;  // 1.5 * 2^23
-    const float t = fminf(fmaxf(fmaf(x, r, big), big - 127.f), big + 127.f);
-    return __float_as_uint(t) & 0xFFu;
+    float t = fmaf(x, r, big);
+    if constexpr (CLAMP) t = fminf(fmaxf(t, big - 127.f), big + 127.f);
+    return __float_as_uint(t);
+}
+
+// The larger of each half, NaN if either is.
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
 // Codes of four values.
-template <bool INT8>
+template <bool INT8, bool CLAMP = true>
 __device__ __forceinline__ uint32_t encode4(const float *x, float r) {
     if constexpr (INT8) {
-        const uint32_t a = int8_code(x[0], r), b = int8_code(x[1], r), c = int8_code(x[2], r),
-                       d = int8_code(x[3], r);
+        const uint32_t a = int8_code<CLAMP>(x[0], r), b = int8_code<CLAMP>(x[1], r);
+        const uint32_t c = int8_code<CLAMP>(x[2], r), d = int8_code<CLAMP>(x[3], r);
         return __byte_perm(__byte_perm(a, b, 0x0040u), __byte_perm(c, d, 0x0040u), 0x5410u);
     } else {
         return f32x2_to_e4m3x2(__fmul_rn(x[0], r), __fmul_rn(x[1], r)) |
@@ -83,7 +92,7 @@ __device__ __forceinline__ void decode4(uint32_t w, float *x) {
 }
 
 template <bool INT8, int HD>
-__global__ void __launch_bounds__(128) kv_append_scaled_kernel(const ScaledParams p) {
+__global__ void __launch_bounds__(128, 6) kv_append_scaled_kernel(const ScaledParams p) {
     constexpr int kLanes = HD / 8;           // lanes of a row: 16 bytes of bf16, 8 codes each
     constexpr int kRows = 32 / kLanes;       // rows of a pass
     constexpr float kQMax = INT8 ? 127.f : 448.f;
@@ -104,47 +113,72 @@ __global__ void __launch_bounds__(128) kv_append_scaled_kernel(const ScaledParam
                            : nullptr;
     auto good = [&](int64_t s) { return s >= 0 && s < p.num_slots; };
 
+    // Slots of rows first_row - 1 .. first_row + 30, a lane each, and the window's
+    // rows themselves: nothing below waits for a second load where a run starts
+    // with the window and ends in these 32 rows, as a prompt's do.
+    const int64_t seen = first_row - 1 + lane;
+    const int64_t my_slot = seen >= 0 && seen < p.n ? __ldg(p.slots + seen) : -1;
+    uint4 x[kPasses];
+    auto fetch = [&](int64_t base, int64_t end, bool check) {
+#pragma unroll
+        for (int u = 0; u < kPasses; ++u) {
+            const int64_t i = base + u * kRows + lane / kLanes;
+            x[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (i < end && (!check || good(__ldg(p.slots + i))))
+                x[u] = __ldg(src + (i * heads + h) * kLanes + (lane & (kLanes - 1)));
+        }
+    };
+    fetch(first_row, min(p.n, first_row + min(p.window, kPasses * kRows)), false);
     // rows of this window that start a run
     bool start = false;
-    if (lane < p.window && first_row + lane < p.n) {
-        const int64_t i = first_row + lane, s = __ldg(p.slots + i);
-        if (good(s)) {
-            int64_t j = i - 1, t = -1;
-            while (j >= 0 && !good(t = __ldg(p.slots + j))) --j;  // rows skipped below
-            start = j < 0 || (t >> p.shift) != (s >> p.shift);
+    const int64_t before = __shfl_up_sync(0xffffffffu, my_slot, 1);
+    if (lane >= 1 && lane <= p.window && seen < p.n) {
+        if (good(my_slot)) {
+            int64_t j = seen - 1, t = before;
+            while (j >= 0 && !good(t))  // rows that are skipped do not end a run
+                if (--j >= 0) t = __ldg(p.slots + j);
+            start = j < 0 || (t >> p.shift) != (my_slot >> p.shift);
         } else if (rem == 0) {
             report_error(p.err, ATTN_ERR_BOUNDS);
         }
     }
     uint32_t starts = __ballot_sync(0xffffffffu, start);
     while (starts != 0) {
-        const int64_t i0 = first_row + __ffs(starts) - 1;
+        const int at_lane = __ffs(starts) - 1;  // of the run's first row
+        const int64_t i0 = first_row - 1 + at_lane;
         starts &= starts - 1;
-        const int64_t block = __ldg(p.slots + i0) >> p.shift;
+        const int64_t block = __shfl_sync(0xffffffffu, my_slot, at_lane) >> p.shift;
+        const int64_t inside = (int64_t(1) << p.shift) - 1;
         // the run: rows up to the first good slot of another block
-        int64_t i1 = i0;
-        bool fresh = false;
-        for (;;) {
-            const int64_t i = i1 + lane;
-            const int64_t s = i < p.n ? __ldg(p.slots + i) : 0;
-            const bool in = i < p.n && (!good(s) || (s >> p.shift) == block);
-            const uint32_t out = ~__ballot_sync(0xffffffffu, in);
-            const int take = out == 0 ? 32 : __ffs(out) - 1;
-            fresh |= __any_sync(0xffffffffu, lane < take && good(s) &&
-                                                 (s & ((int64_t(1) << p.shift) - 1)) == 0);
-            i1 += take;
-            if (take < 32) break;
-        }
-        uint4 x[kPasses];
-        auto load = [&](int64_t base) {
-#pragma unroll
-            for (int u = 0; u < kPasses; ++u) {
-                const int64_t i = base + u * kRows + lane / kLanes;
-                x[u] = make_uint4(0u, 0u, 0u, 0u);
-                if (i < i1 && good(__ldg(p.slots + i)))
-                    x[u] = __ldg(src + (i * heads + h) * kLanes + (lane & (kLanes - 1)));
+        int64_t i1;
+        bool fresh;
+        {
+            const bool in = seen < p.n && (!good(my_slot) || (my_slot >> p.shift) == block);
+            const uint32_t out = ~__ballot_sync(0xffffffffu, in) & (0xffffffffu << at_lane);
+            const int stop = out == 0 ? 32 : __ffs(out) - 1;
+            i1 = first_row - 1 + stop;
+            fresh = __any_sync(0xffffffffu, lane >= at_lane && lane < stop && good(my_slot) &&
+                                                (my_slot & inside) == 0);
+            while (i1 - (first_row - 1) >= 32 && i1 < p.n) {  // it goes on behind the 32 rows
+                const int64_t i = i1 + lane;
+                const int64_t s = i < p.n ? __ldg(p.slots + i) : 0;
+                const uint32_t past = ~__ballot_sync(
+                    0xffffffffu, i < p.n && (!good(s) || (s >> p.shift) == block));
+                const int take = past == 0 ? 32 : __ffs(past) - 1;
+                fresh |= __any_sync(0xffffffffu, lane < take && good(s) && (s & inside) == 0);
+                i1 += take;
+                if (take < 32) break;
             }
+        }
+        // whether the window's rows in registers are all of the run's; a run's rows
+        // without a slot are not stored, nor counted
+        const bool held_rows = i0 == first_row && i1 <= first_row + min(p.window, kPasses * kRows);
+        auto slot_of = [&](int64_t i) -> int64_t {  // all lanes together
+            const int64_t l = i - (first_row - 1);
+            const int64_t s = __shfl_sync(0xffffffffu, my_slot, (int)(l & 31));
+            return l < 32 ? s : __ldg(p.slots + min(i, p.n - 1));
         };
+        auto load = [&](int64_t base) { fetch(base, i1, true); };
         // the eight values of a lane's piece
         auto values = [&](const uint4 &w, float *f) {
             const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -157,14 +191,42 @@ __global__ void __launch_bounds__(128) kv_append_scaled_kernel(const ScaledParam
 #pragma unroll
                 for (int e = 0; e < 8; ++e) f[e] = __fsub_rn(f[e], __ldg(ref + e));
         };
+        // The short way, a prompt's and a step's: the rows are in registers, in
+        // consecutive slots, finite, and K has no reference.  Maxima are taken of bf16
+        // pairs, INT8 codes need no clamp (|x r| <= 127 (1 + 2^-22)), addresses advance
+        // by one stride.
+        const int64_t slot0 = __shfl_sync(0xffffffffu, my_slot, at_lane);
+        bool short_way =
+            held_rows && ref == nullptr &&
+            __all_sync(0xffffffffu, lane < at_lane || seen >= i1 ||
+                                        my_slot == slot0 + (lane - at_lane));
         float amax = 0.f;
         bool nan = false;
-        for (int64_t base = i0; base < i1; base += kPasses * kRows) {
-            load(base);
+        if (short_way) {
+            uint32_t mx = 0;
 #pragma unroll
             for (int u = 0; u < kPasses; ++u) {
-                const int64_t i = base + u * kRows + lane / kLanes;
-                if (i >= i1 || !good(__ldg(p.slots + i))) continue;
+                if (i0 + u * kRows + lane / kLanes >= i1) continue;  // another run's rows
+                mx = max_nan_bf16x2(mx, x[u].x & 0x7FFF7FFFu);
+                mx = max_nan_bf16x2(mx, x[u].y & 0x7FFF7FFFu);
+                mx = max_nan_bf16x2(mx, x[u].z & 0x7FFF7FFFu);
+                mx = max_nan_bf16x2(mx, x[u].w & 0x7FFF7FFFu);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                mx = max_nan_bf16x2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float lo = __uint_as_float(mx << 16), hi = __uint_as_float(mx & 0xFFFF0000u);
+            short_way = lo < INFINITY && hi < INFINITY;
+            amax = fmaxf(lo, hi);
+        }
+        if (!short_way) {
+        amax = 0.f;
+        for (int64_t base = i0; base < i1; base += kPasses * kRows) {
+            if (!held_rows) load(base);
+#pragma unroll
+            for (int u = 0; u < kPasses; ++u) {
+                const int64_t i = base + u * kRows + lane / kLanes, s = slot_of(i);
+                if (i >= i1 || !good(s)) continue;
                 float f[8];
                 values(x[u], f);
 #pragma unroll
@@ -177,6 +239,7 @@ __global__ void __launch_bounds__(128) kv_append_scaled_kernel(const ScaledParam
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        }
         const int64_t at = block * heads + h;
         const float held = fresh ? 0.f : fmaxf(scales[at], 0.f);
         const float now = fmaxf(fmaxf(held, __fdiv_rn(amax, kQMax)), kScaleFloor);
@@ -208,15 +271,34 @@ __global__ void __launch_bounds__(128) kv_append_scaled_kernel(const ScaledParam
             if (lane == 0) report_error(p.err, ATTN_ERR_UNSUPPORTED);
             nan = true;
         }
-        const bool kept = i1 - i0 <= kPasses * kRows;
+        if (short_way) {
+            uint8_t *dst = cache + p.place.head_offset(slot0 + lane / kLanes, h) +
+                           (lane & (kLanes - 1)) * 8;
+            const int64_t step =
+                (int64_t)kRows * p.place.head_bytes * (p.place.rows == 0 ? heads : 1);
+#pragma unroll
+            for (int u = 0; u < kPasses; ++u, dst += step) {
+                if (i0 + u * kRows + lane / kLanes >= i1) break;
+                const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    f[2 * e] = __uint_as_float(w[e] << 16);
+                    f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+                }
+                *reinterpret_cast<uint2 *>(dst) =
+                    make_uint2(encode4<INT8, false>(f, r), encode4<INT8, false>(f + 4, r));
+            }
+            __syncwarp();
+            continue;
+        }
+        const bool kept = held_rows || i1 - i0 <= kPasses * kRows;
         for (int64_t base = i0; base < i1; base += kPasses * kRows) {
             if (!kept) load(base);
 #pragma unroll
             for (int u = 0; u < kPasses; ++u) {
-                const int64_t i = base + u * kRows + lane / kLanes;
-                if (i >= i1) continue;
-                const int64_t s = __ldg(p.slots + i);
-                if (!good(s)) continue;
+                const int64_t i = base + u * kRows + lane / kLanes, s = slot_of(i);
+                if (i >= i1 || !good(s)) continue;
                 float f[8];
                 values(x[u], f);
                 if (INT8 && nan)  // INT8 has no NaN: 0
