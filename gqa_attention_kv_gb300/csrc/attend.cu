@@ -71,6 +71,7 @@ struct Params {
     bool head_major;
     const int32_t *block_table, *seq_lens, *positions;
     int q_rows, n_q_heads, n_kv_heads, group, rows, row_blocks;
+    int n_groups;  // KV heads by the heads of a unit
     int window, sinks, max_seq_len;
     int e0, n_entries;  // this launch's (request, row block) pairs
     int grid;
@@ -85,7 +86,7 @@ struct Params {
 // (gq, tq) reads pieces tq + 4 j of K rows gq and gq + 8, and piece gq (+ 8 j)
 // of V rows 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9; rows are swizzled so that the
 // lanes of one access meet different banks.
-template <int FMT, int HD, int MT>
+template <int FMT, int HD, int MT, int HG>
 struct Geo {
     static constexpr int E = FMT == kBF16 ? 2 : 1;
     static constexpr int RB = MT == 0 ? 8 : 16;                  // query rows of a unit
@@ -101,7 +102,8 @@ struct Geo {
     static constexpr int kStepBytes = NSUB * kChunkBytes;        // K (or V) of a step
     static constexpr int kStages = 3;
     static constexpr int CTAS = kRowBytes == 256 ? 2 : FMT == kBF16 ? 3 : 4;  // blocks of an SM
-    static constexpr int kGroup = kWarps * NSUB;                 // chunks of a block's step
+    static constexpr int kHeadWarps = kWarps / HG;               // warps of a KV head
+    static constexpr int kGroup = kHeadWarps * NSUB;             // chunks of a block's step
     static constexpr int kOStride = HD + 4;                      // floats of a parked output row
     static constexpr int kRingBytes = kStages * 2 * kStepBytes;  // of one warp
     static_assert(RB * kOStride * 4 <= kRingBytes, "a warp's outputs are parked in its ring");
@@ -277,13 +279,13 @@ struct __align__(16) Note {
     float scale[NSUB][2];
 };
 
-template <int FMT, int HD, int MT>
+template <int FMT, int HD, int MT, int HG>
 struct __align__(16) Smem {
-    using G = Geo<FMT, HD, MT>;
+    using G = Geo<FMT, HD, MT, HG>;
     uint8_t buf[kWarps][G::kRingBytes];  // at the end of a unit a warp's output rows
-    uint32_t q[HD / 16][32][MT == 0 ? 2 : 4];  // q fragments of a unit, as a lane reads them
+    uint32_t q[HG][HD / 16][32][MT == 0 ? 2 : 4];  // q fragments of a unit, as a lane reads them
     Note<G::NSUB> note[kWarps][G::kStages];
-    float m[kWarps][G::RB], l[kWarps][G::RB], w[kWarps][G::RB], lse[G::RB];
+    float m[kWarps][G::RB], l[kWarps][G::RB], w[kWarps][G::RB], lse[HG][G::RB];
     Entry entry[kMaxEntries];
     int prefix[kMaxEntries + 1];
     int last_part;
@@ -295,9 +297,9 @@ struct __align__(16) Smem {
 // The rows of a unit from its parts first .. last, by a block's four warps: rows
 // warp, warp + 4, ... each, a lane HD / 32 dims of every row.  The log-sum-exps
 // of 32 parts come in one load a row; the parts' outputs then wait for nothing.
-template <int HD, int RB>
-__device__ __forceinline__ void merge_unit(const Params &p, int64_t unit, int first, int last,
-                                           int row0, int n_rows, int b, int kvh) {
+template <int HD, int RB, int HG>
+__device__ __forceinline__ void merge_unit(const Params &p, int64_t unit, int hs, int first,
+                                           int last, int row0, int n_rows, int b, int kvh) {
     constexpr int V = HD / 32, R = RB / kWarps;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float m[R], sum[R], acc[R][V];
@@ -313,7 +315,7 @@ __device__ __forceinline__ void merge_unit(const Params &p, int64_t unit, int fi
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int row = warp + kWarps * r;
-            f[r] = lane < n && row < n_rows ? __ldcg(p.ws_lse + (unit + c0 + lane) * RB + row)
+            f[r] = lane < n && row < n_rows ? __ldcg(p.ws_lse + ((unit + c0 + lane) * HG + hs) * RB + row)
                                             : -INFINITY;
         }
 #pragma unroll
@@ -335,7 +337,8 @@ __device__ __forceinline__ void merge_unit(const Params &p, int64_t unit, int fi
             for (int r = 0; r < R; ++r) {
                 const int row = min(warp + kWarps * r, n_rows - 1);
                 const float w = __shfl_sync(0xffffffffu, f[r], k);
-                const float *src = p.ws_o + ((unit + c0 + k) * RB + row) * HD + lane * V;
+                const float *src =
+                    p.ws_o + (((unit + c0 + k) * HG + hs) * RB + row) * HD + lane * V;
                 sum[r] += w;
                 if constexpr (V == 4) {
                     const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
@@ -363,14 +366,14 @@ __device__ __forceinline__ void merge_unit(const Params &p, int64_t unit, int fi
     }
 }
 
-template <int FMT, int HD, int MT>
-__global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
+template <int FMT, int HD, int MT, int HG>
+__global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
     attend_kernel(const Params p) {
-    using G = Geo<FMT, HD, MT>;
+    using G = Geo<FMT, HD, MT, HG>;
     constexpr int RB = G::RB;
     constexpr int kSteps = HD / 16;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    Smem<FMT, HD, MT> &sm = *reinterpret_cast<Smem<FMT, HD, MT> *>(smem_raw);
+    Smem<FMT, HD, MT, HG> &sm = *reinterpret_cast<Smem<FMT, HD, MT, HG> *>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gq = lane >> 2, tq = lane & 3;
     pdl_wait();
@@ -386,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
         for (int base = 0; base < p.n_entries; base += 32) {
             const int i = base + lane;
             const int n = i < p.n_entries ? chunks_of(sm.entry[i], p.sinks).cnt : 0;
-            int x = n > 0 ? (n + kGapChunks) * p.n_kv_heads : 0;
+            int x = n > 0 ? (n + kGapChunks) * p.n_groups : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -409,8 +412,8 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
             const int e = p.e0 + i, b = e / p.row_blocks, rb = e - b * p.row_blocks;
             const int row0 = rb * RB, n = min(p.rows, row0 + RB) - row0;
             for (int kvh = 0; kvh < p.n_kv_heads; ++kvh) {
-                if (lane == 0 && p.ws_count == nullptr)
-                    p.ws_parts[i * p.n_kv_heads + kvh] = make_int2(0, -1);
+                if (lane == 0 && p.ws_count == nullptr && kvh % HG == 0)
+                    p.ws_parts[i * p.n_groups + kvh / HG] = make_int2(0, -1);
                 for (int j = lane; j < n * (HD / 8); j += 32) {
                     const int row = row0 + j / (HD / 8), r = row / p.group, gr = row - r * p.group;
                     reinterpret_cast<uint4 *>(
@@ -432,22 +435,24 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
         const Chunks ch = chunks_of(en, p.sinks);
         const int span = ch.cnt + kGapChunks;
         int off = g - sm.prefix[lo_e];
-        const int kvh = off / span;
-        off -= kvh * span;
+        const int head_group = off / span;
+        off -= head_group * span;
+        const int hs = warp / G::kHeadWarps;        // which of the unit's heads is this warp's
+        const int kvh0 = head_group * HG, kvh = kvh0 + hs;
         const int unit_start = g - off;
         if (off >= ch.cnt) {  // in the gap behind the unit
             g = unit_start + span;
             continue;
         }
         const int c_end = min(ch.cnt, off + (g_end - g));
-        const int unit = lo_e * p.n_kv_heads + kvh;
+        const int unit = lo_e * p.n_groups + head_group;
         const int first = unit_start / share, last = (unit_start + ch.cnt - 1) / share;
         const int e = p.e0 + lo_e, b = e / p.row_blocks, rb = e - b * p.row_blocks;
         const int row0 = rb * RB, n_rows = min(p.rows, row0 + RB) - row0;
 
         // ---- q rows
         const __nv_bfloat16 *qb =
-            p.q + ((int64_t)b * p.q_rows * p.n_q_heads + kvh * p.group) * HD;
+            p.q + ((int64_t)b * p.q_rows * p.n_q_heads + kvh0 * p.group) * HD;
         auto row_of = [&](int rr) {  // row rr of the unit, in q and out
             const int row = row0 + min(rr, n_rows - 1), r = row / p.group;
             return ((int64_t)r * p.n_q_heads + (row - r * p.group)) * HD;
@@ -625,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
             }
         };
 
-        const int c0 = off + warp * NSUB;
+        const int c0 = off + warp % G::kHeadWarps * NSUB;
         read_pages(c0);
 #pragma unroll
         for (int st = 0; st < G::kStages - 1; ++st) {
@@ -637,20 +642,22 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
         // ---- q fragments and positions, while the first keys are under way
         constexpr int kQRows = MT == 0 ? 1 : 2;
         bool q_big = false;
-        for (int kk = warp; kk < kSteps; kk += kWarps) {
+        for (int i = warp; i < HG * kSteps; i += kWarps) {
+            const int qs = i / kSteps, kk = i % kSteps;  // head of the unit, k-step
             const int j = kk / G::kStepsPerPiece, st = kk % G::kStepsPerPiece;
             const int d0 = (16 / G::E) * (tq + 4 * j) + 4 * st;
 #pragma unroll
             for (int hr = 0; hr < kQRows; ++hr) {
-                uint2 x = *reinterpret_cast<const uint2 *>(qb + row_of(gq + 8 * hr) + d0);
+                uint2 x = *reinterpret_cast<const uint2 *>(qb + qs * p.group * HD +
+                                                            row_of(gq + 8 * hr) + d0);
                 if constexpr (FMT != kBF16) {  // f16 holds |q| < 65520
                     x.x = bf16x2_to_f16x2(x.x);
                     x.y = bf16x2_to_f16x2(x.y);
                     q_big |= (x.x & 0x7C00u) == 0x7C00u || (x.x & 0x7C000000u) == 0x7C000000u ||
                              (x.y & 0x7C00u) == 0x7C00u || (x.y & 0x7C000000u) == 0x7C000000u;
                 }
-                sm.q[kk][lane][hr] = x.x;
-                sm.q[kk][lane][kQRows + hr] = x.y;
+                sm.q[qs][kk][lane][hr] = x.x;
+                sm.q[qs][kk][lane][kQRows + hr] = x.y;
             }
         }
         if (q_big) report_error(p.err, ATTN_ERR_UNSUPPORTED);
@@ -666,10 +673,10 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
 #pragma unroll
             for (int kk = 0; kk < kSteps; ++kk) {
                 if constexpr (MT == 0) {
-                    mma_f16_16816(sum, a, sm.q[kk][lane][0], sm.q[kk][lane][1]);
+                    mma_f16_16816(sum, a, sm.q[hs][kk][lane][0], sm.q[hs][kk][lane][1]);
                 } else {
-                    const uint32_t qa[4] = {sm.q[kk][lane][0], sm.q[kk][lane][1],
-                                            sm.q[kk][lane][2], sm.q[kk][lane][3]};
+                    const uint32_t qa[4] = {sm.q[hs][kk][lane][0], sm.q[hs][kk][lane][1],
+                                            sm.q[hs][kk][lane][2], sm.q[hs][kk][lane][3]};
                     mma_f16_16816(sum, qa, kMinus128, kMinus128);
                 }
             }
@@ -725,10 +732,10 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
             for (int kk = 0; kk < kSteps; ++kk) {
                 uint32_t qf[2 * kQRows];
                 if constexpr (MT == 0) {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(sm.q[kk][lane]);
+                    const uint2 x = *reinterpret_cast<const uint2 *>(sm.q[hs][kk][lane]);
                     qf[0] = x.x, qf[1] = x.y;
                 } else {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(sm.q[kk][lane]);
+                    const uint4 x = *reinterpret_cast<const uint4 *>(sm.q[hs][kk][lane]);
                     qf[0] = x.x, qf[1] = x.y, qf[2] = x.z, qf[3] = x.w;
                 }
 #pragma unroll
@@ -1011,33 +1018,36 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
                         make_float2(o[2 * d][i], o[2 * d + 1][i]);
         }
         __syncthreads();
-        if (threadIdx.x < RB) {
-            const int row = threadIdx.x;
+        if (threadIdx.x < HG * RB) {
+            constexpr int W = G::kHeadWarps;
+            const int row = threadIdx.x % RB, h = threadIdx.x / RB, w0 = h * W;
             float m = -INFINITY, l = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.m[w][row]);
+            for (int w = 0; w < W; ++w) m = fmaxf(m, sm.m[w0 + w][row]);
             const float m_use = m == -INFINITY ? 0.f : m;
-            float f[kWarps];
+            float f[W];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                f[w] = fast_exp2(sm.m[w][row] - m_use);
-                l += f[w] * sm.l[w][row];
+            for (int w = 0; w < W; ++w) {
+                f[w] = fast_exp2(sm.m[w0 + w][row] - m_use);
+                l += f[w] * sm.l[w0 + w][row];
             }
             const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) sm.w[w][row] = f[w] * inv;
-            sm.lse[row] = l == 0.f ? -INFINITY : m_use + log2f(l);
+            for (int w = 0; w < W; ++w) sm.w[w0 + w][row] = f[w] * inv;
+            sm.lse[h][row] = l == 0.f ? -INFINITY : m_use + log2f(l);
         }
         __syncthreads();
         const bool whole = first == last;
-        const int64_t slot = unit + blockIdx.x;  // unique: shares are contiguous
-        for (int i = threadIdx.x; i < n_rows * (HD / 4); i += kThreads) {
-            const int row = i / (HD / 4), d = (i % (HD / 4)) * 4;
+        const int64_t slot = (int64_t)(unit + blockIdx.x) * HG;  // unique: shares are contiguous
+        for (int i = threadIdx.x; i < HG * n_rows * (HD / 4); i += kThreads) {
+            const int hr = i / (HD / 4), d = (i % (HD / 4)) * 4;
+            const int h = HG == 1 ? 0 : hr / n_rows, row = hr - h * n_rows;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float4 x = *reinterpret_cast<const float4 *>(sm.out_row(w, row) + d);
-                const float f = sm.w[w][row];
+            for (int w = 0; w < G::kHeadWarps; ++w) {
+                const int wi = h * G::kHeadWarps + w;
+                const float4 x = *reinterpret_cast<const float4 *>(sm.out_row(wi, row) + d);
+                const float f = sm.w[wi][row];
                 a.x += f * x.x, a.y += f * x.y, a.z += f * x.z, a.w += f * x.w;
             }
             if (whole) {
@@ -1045,13 +1055,15 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
                 y.x = pack_bf16x2(a.x, a.y);
                 y.y = pack_bf16x2(a.z, a.w);
                 *reinterpret_cast<uint2 *>(
-                    p.out + ((int64_t)b * p.q_rows * p.n_q_heads + kvh * p.group) * HD +
+                    p.out +
+                    ((int64_t)b * p.q_rows * p.n_q_heads + (kvh0 + h) * p.group) * HD +
                     row_of(row) + d) = y;
             } else {
-                *reinterpret_cast<float4 *>(p.ws_o + (slot * RB + row) * HD + d) = a;
+                *reinterpret_cast<float4 *>(p.ws_o + ((slot + h) * RB + row) * HD + d) = a;
             }
         }
-        if (!whole && threadIdx.x < n_rows) p.ws_lse[slot * RB + threadIdx.x] = sm.lse[threadIdx.x];
+        if (!whole && threadIdx.x < HG * RB && threadIdx.x % RB < n_rows)
+            p.ws_lse[slot * RB + threadIdx.x] = sm.lse[threadIdx.x / RB][threadIdx.x % RB];
         if (p.ws_count == nullptr) {
             if (off == 0 && threadIdx.x == 0) p.ws_parts[unit] = make_int2(first, last);
         } else if (!whole) {
@@ -1064,7 +1076,8 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
             }
             __syncthreads();
             if (sm.last_part)
-                merge_unit<HD, RB>(p, unit, first, last, row0, n_rows, b, kvh);
+                for (int h = 0; h < HG; ++h)
+                    merge_unit<HD, RB, HG>(p, unit, h, first, last, row0, n_rows, b, kvh0 + h);
         }
         __syncthreads();  // the shared states are free again
         g += c_end - off;
@@ -1076,7 +1089,7 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT>::CTAS)
 // by SPLIT warps, each every SPLIT-th part, its lanes along the head; all of a
 // warp's log-sum-exps come in one load a 32 parts, so its reads of the partial
 // outputs wait for nothing but that.
-template <int HD, int RB, int SPLIT>
+template <int HD, int RB, int HG, int SPLIT>
 __global__ void __launch_bounds__(256) attend_merge_kernel(const Params p) {
     constexpr int V = HD / 32;           // dims of a lane
     constexpr int kRows = 8 / SPLIT;     // rows of a block
@@ -1084,9 +1097,11 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const Params p) {
     __shared__ float sm_m[8], sm_sum[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t i = (int64_t)blockIdx.x * kRows + warp / SPLIT;
-    const int64_t unit = i / RB;
-    const int row = (int)(i - unit * RB);
-    const int entry = (int)(unit / p.n_kv_heads), kvh = (int)(unit - (int64_t)entry * p.n_kv_heads);
+    const int64_t head = i / RB;  // KV heads of all entries
+    const int row = (int)(i - head * RB);
+    const int entry = (int)(head / p.n_kv_heads), kvh = (int)(head - (int64_t)entry * p.n_kv_heads);
+    const int64_t unit = head / HG;
+    const int hs = (int)(head - unit * HG);
     const int e = p.e0 + entry, b = e / p.row_blocks, rb = e - b * p.row_blocks;
     const int q_row = rb * RB + row;
     pdl_wait();
@@ -1099,7 +1114,8 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const Params p) {
     if (live) {
         for (int c0 = parts.x + warp % SPLIT; c0 <= parts.y; c0 += 32 * SPLIT) {
             const int mine = c0 + lane * SPLIT;
-            const float lse = mine <= parts.y ? __ldcg(p.ws_lse + (unit + mine) * RB + row) : -INFINITY;
+            const float lse = mine <= parts.y ? __ldcg(p.ws_lse + ((unit + mine) * HG + hs) * RB + row)
+                                               : -INFINITY;
             float mx = lse;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -1111,9 +1127,9 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const Params p) {
 #pragma unroll
             for (int d = 0; d < V; ++d) acc[d] *= old;
             const int n = min(32, (parts.y - c0) / SPLIT + 1);
-            const float *src = p.ws_o + ((unit + c0) * RB + row) * HD + lane * V;
+            const float *src = p.ws_o + (((unit + c0) * HG + hs) * RB + row) * HD + lane * V;
 #pragma unroll 8
-            for (int k = 0; k < n; ++k, src += (int64_t)SPLIT * RB * HD) {
+            for (int k = 0; k < n; ++k, src += (int64_t)SPLIT * HG * RB * HD) {
                 const float w = __shfl_sync(0xffffffffu, f, k);
                 sum += w;
                 if constexpr (V == 4) {
@@ -1150,33 +1166,33 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const Params p) {
     for (int d = 0; d < V / 2; ++d) dst[d] = pack_bf16x2(acc[2 * d] * inv, acc[2 * d + 1] * inv);
 }
 
-template <int FMT, int HD, int MT>
+template <int FMT, int HD, int MT, int HG>
 int launch(const Params &p, bool merge, cudaStream_t stream) {
     constexpr int RB = MT == 0 ? 8 : 16;
-    constexpr size_t kBytes = sizeof(Smem<FMT, HD, MT>);
+    constexpr size_t kBytes = sizeof(Smem<FMT, HD, MT, HG>);
     static std::atomic<uint64_t> configured{0};  // a bit per device
     int dev = 0;
     cudaGetDevice(&dev);
     const uint64_t bit = uint64_t(1) << (dev & 63);
     if (!(configured.load(std::memory_order_relaxed) & bit)) {
         const cudaError_t e = cudaFuncSetAttribute(
-            attend_kernel<FMT, HD, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes);
+            attend_kernel<FMT, HD, MT, HG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes);
         if (e != cudaSuccess) {
             note_cuda_error(e);
             return ATTN_ERR_CUDA;
         }
         configured.fetch_or(bit, std::memory_order_relaxed);
     }
-    const cudaError_t e0 = launch_pdl(attend_kernel<FMT, HD, MT>, dim3((unsigned)p.grid), dim3(kThreads), kBytes,
+    const cudaError_t e0 = launch_pdl(attend_kernel<FMT, HD, MT, HG>, dim3((unsigned)p.grid), dim3(kThreads), kBytes,
                                       stream, p);
     if (e0 != cudaSuccess) return ATTN_ERR_CUDA;
     if (!merge) return ATTN_OK;
     // Units that lie in many parts (few units, long contexts) have eight warps a row
-    const int64_t units = (int64_t)p.n_entries * p.n_kv_heads, rows = units * RB;
+    const int64_t units = (int64_t)p.n_entries * p.n_groups, rows = units * HG * RB;
     const cudaError_t e =
         p.grid > 8 * units
-            ? launch_pdl(attend_merge_kernel<HD, RB, 8>, dim3((unsigned)rows), dim3(256), 0, stream, p)
-            : launch_pdl(attend_merge_kernel<HD, RB, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256),
+            ? launch_pdl(attend_merge_kernel<HD, RB, HG, 8>, dim3((unsigned)rows), dim3(256), 0, stream, p)
+            : launch_pdl(attend_merge_kernel<HD, RB, HG, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256),
                          0, stream, p);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
@@ -1196,7 +1212,10 @@ int plan_attend(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
         usual = std::min<int64_t>(chunks, ((int64_t)window + q_rows + sinks) / att::kChunk + 3);
     const int64_t entries = (int64_t)batch * row_blocks;
     // rows of one head and prefixes of chunks are counted in 32 bits
-    const int64_t per_entry = (chunks + att::kGapChunks) * n_kv_heads;
+    const bool rows64 = head_dim == 64 && cache->dtype != ATTN_KV_BF16;
+    plan->heads = rows64 && cache->layout == ATTN_LAYOUT_BSHD && n_kv_heads % 2 == 0 ? 2 : 1;
+    const int n_groups = n_kv_heads / plan->heads;
+    const int64_t per_entry = (chunks + att::kGapChunks) * n_groups;
     if (rows >= (int64_t(1) << 31) || entries >= (int64_t(1) << 31) ||
         per_entry >= (int64_t(1) << 30) ||
         cache->num_slots * n_kv_heads >= (int64_t(1) << 32))
@@ -1207,11 +1226,12 @@ int plan_attend(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
         1, std::min<int64_t>(std::min<int64_t>(entries, att::kMaxEntries),
                              (int64_t(1) << 30) / per_entry));
     const int per_sm = cache->dtype != ATTN_KV_BF16 ? 4 : head_dim == 64 ? 3 : 2;
-    const int64_t needed = ((int64_t)plan->per_launch * (usual + att::kGapChunks) * n_kv_heads +
+    const int64_t needed = ((int64_t)plan->per_launch * (usual + att::kGapChunks) * n_groups +
                             att::kMinChunks - 1) / att::kMinChunks;
     plan->grid = (int)std::max<int64_t>(
         1, std::min<int64_t>(needed, (int64_t)per_sm * device_sm_count()));
-    const size_t units = (size_t)plan->per_launch * n_kv_heads, slots = units + plan->grid;
+    const size_t units = (size_t)plan->per_launch * n_groups,
+                 slots = (units + plan->grid) * plan->heads;
     // How many blocks a unit spans when all are as long as they can be.  Up to
     // kKernelParts the last of them adds the parts up; a unit in more of them
     // has the merge kernel's eight warps a row (measured where few requests meet
@@ -1266,6 +1286,7 @@ int launch_attend(const AttendPlan &plan, const void *q, const attn_kv_cache *ca
     p.q_rows = q_rows;
     p.n_q_heads = n_q_heads;
     p.n_kv_heads = n_kv_heads;
+    p.n_groups = n_kv_heads / plan.heads;
     p.group = n_q_heads / n_kv_heads;
     p.rows = q_rows * p.group;
     p.row_blocks = plan.row_blocks;
@@ -1289,11 +1310,14 @@ int launch_attend(const AttendPlan &plan, const void *q, const attn_kv_cache *ca
         auto run = [&](auto fmt_c) {
             constexpr int F = decltype(fmt_c)::value;
             if (head_dim == 128)
-                rc = plan.mt == 0 ? att::launch<F, 128, 0>(p, plan.merge, stream)
-                                  : att::launch<F, 128, 1>(p, plan.merge, stream);
-            else
-                rc = plan.mt == 0 ? att::launch<F, 64, 0>(p, plan.merge, stream)
-                                  : att::launch<F, 64, 1>(p, plan.merge, stream);
+                rc = plan.mt == 0 ? att::launch<F, 128, 0, 1>(p, plan.merge, stream)
+                                  : att::launch<F, 128, 1, 1>(p, plan.merge, stream);
+            else if (F == att::kBF16 || plan.heads == 1)
+                rc = plan.mt == 0 ? att::launch<F, 64, 0, 1>(p, plan.merge, stream)
+                                  : att::launch<F, 64, 1, 1>(p, plan.merge, stream);
+            else if constexpr (F != att::kBF16)
+                rc = plan.mt == 0 ? att::launch<F, 64, 0, 2>(p, plan.merge, stream)
+                                  : att::launch<F, 64, 1, 2>(p, plan.merge, stream);
         };
         if (fmt == att::kBF16)
             run(std::integral_constant<int, att::kBF16>{});

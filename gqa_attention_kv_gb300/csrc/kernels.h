@@ -160,7 +160,8 @@ int launch_kv_append_scaled(const void *k_new, const void *v_new, const int64_t 
 // under a sliding window with sinks.  (request, row block) pairs go to the
 // kernel per_launch at a time.
 struct AttendPlan {
-    int mt;  // 0: up to 8 rows per unit, 1: 16
+    int mt;     // 0: up to 8 rows per unit, 1: 16
+    int heads;  // KV heads of a unit
     int row_blocks, entries, per_launch, grid, launches;
     bool merge;  // the parts of a unit are added up by a second kernel
     size_t count_offset, parts_offset, lse_offset, o_offset, workspace;
