@@ -51,7 +51,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxEntries = 128;  // (request, row block) pairs per launch
 constexpr int kGapChunks = 24;    // what a change of unit costs a CTA, in chunks
-constexpr int kMinChunks = 8;     // smallest share of a CTA
+constexpr int kMinChunks = 4;     // smallest share of a CTA
 constexpr int kKernelParts = 12;  // parts of a unit that its last block adds up
 constexpr float kRescaleLog2 = 8.0f;  // the reference maximum moves past this only (w <= 2^8)
 constexpr float kScaleFloor = 5.421010862427522e-20f;  // 2^-64, the smallest scale
@@ -97,11 +97,11 @@ struct Geo {
     static constexpr int kVPieces = kRowBytes / (8 * kVBytes);
     static constexpr int kVWords = kVBytes / 4 * kVPieces;       // words of a key a thread
     static constexpr int kVElems = kVBytes / E;                  // dims of a V piece
-    static constexpr int NSUB = kRowBytes == 64 ? 2 : 1;         // chunks of a step
+    static constexpr int NSUB = kRowBytes == 64 ? 4 : FMT != kBF16 ? 2 : 1;         // chunks of a step
     static constexpr int kChunkBytes = kChunk * kRowBytes;
     static constexpr int kStepBytes = NSUB * kChunkBytes;        // K (or V) of a step
-    static constexpr int kStages = 3;
-    static constexpr int CTAS = kRowBytes == 256 ? 2 : FMT == kBF16 ? 3 : 4;  // blocks of an SM
+    static constexpr int kStages = FMT != kBF16 ? 2 : 3;
+    static constexpr int CTAS = kRowBytes == 256 ? 2 : 3;  // blocks of an SM
     static constexpr int kHeadWarps = kWarps / HG;               // warps of a KV head
     static constexpr int kGroup = kHeadWarps * NSUB;             // chunks of a block's step
     static constexpr int kOStride = HD + 4;                      // floats of a parked output row
@@ -718,7 +718,8 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
             // ---- scores: MT 0 keys are the rows of S^T = K Q^T, MT 1 the columns of S = Q K^T.
             // Even and odd k-steps add up apart: a product waits for half as many before it
             constexpr int NJ = MT == 0 ? 1 : 2;
-            float s[NSUB][NJ][4], s_odd[NSUB][NJ][4];
+            float s[NSUB][NJ][4];
+            float s_odd[NSUB][NJ][4];
 #pragma unroll
             for (int i = 0; i < NSUB; ++i)
 #pragma unroll
@@ -754,8 +755,8 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
                         const uint32_t a[4] = {x[0][0], x[1][0], x[0][1], x[1][1]};
                         mma16<FMT>(kk & 1 ? s_odd[i][0] : s[i][0], a, qf[0], qf[1]);
                     } else {
-                        mma16<FMT>(kk & 1 ? s_odd[i][0] : s[i][0], qf, x[0][0], x[0][1]);
-                        mma16<FMT>(kk & 1 ? s_odd[i][1] : s[i][1], qf, x[1][0], x[1][1]);
+                        mma16<FMT>(s[i][0], qf, x[0][0], x[0][1]);
+                        mma16<FMT>(s[i][1], qf, x[1][0], x[1][1]);
                     }
                 }
             }
@@ -764,7 +765,8 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
 #pragma unroll
                 for (int j = 0; j < NJ; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[i][j][e] += s_odd[i][j][e];
+                    for (int e = 0; e < 4; ++e)
+                        if constexpr (MT == 0) s[i][j][e] += s_odd[i][j][e];
             // ---- mask and weights.  x(row, key): element e of s[i][j] is
             // MT 0: row e & 1, key gq + 8 (e >> 1); MT 1: row e >> 1, key 8 j + 2 tq + (e & 1)
             auto sees = [&](int i, int row, int key) {
@@ -1212,8 +1214,16 @@ int plan_attend(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
         usual = std::min<int64_t>(chunks, ((int64_t)window + q_rows + sinks) / att::kChunk + 3);
     const int64_t entries = (int64_t)batch * row_blocks;
     // rows of one head and prefixes of chunks are counted in 32 bits
-    const bool rows64 = head_dim == 64 && cache->dtype != ATTN_KV_BF16;
-    plan->heads = rows64 && cache->layout == ATTN_LAYOUT_BSHD && n_kv_heads % 2 == 0 ? 2 : 1;
+    // Two KV heads a unit where the slot-major rows of a head are so short that one
+    // head alone reads DRAM badly: 8-bit rows of 64 bytes leave half of every line
+    // (16 x 32 heads, 2,048 to 8,192 keys: 595 MB from DRAM and 102 us, with two heads
+    // 71 us), and bf16 rows of 128 bytes at up to 8 query rows (16 x 32 heads of 5,120
+    // keys 117 us, 107 with two).  8-bit rows of 128 bytes are better alone (64 x 8
+    // heads of 2,080 keys 53 us, 55 with two), as are four heads of 64 bytes (75 us).
+    plan->heads = 1;
+    if (cache->layout == ATTN_LAYOUT_BSHD && head_dim == 64 && n_kv_heads % 2 == 0 &&
+        (cache->dtype != ATTN_KV_BF16 || plan->mt == 0))
+        plan->heads = 2;
     const int n_groups = n_kv_heads / plan->heads;
     const int64_t per_entry = (chunks + att::kGapChunks) * n_groups;
     if (rows >= (int64_t(1) << 31) || entries >= (int64_t(1) << 31) ||
@@ -1225,7 +1235,7 @@ int plan_attend(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
     plan->per_launch = (int)std::max<int64_t>(
         1, std::min<int64_t>(std::min<int64_t>(entries, att::kMaxEntries),
                              (int64_t(1) << 30) / per_entry));
-    const int per_sm = cache->dtype != ATTN_KV_BF16 ? 4 : head_dim == 64 ? 3 : 2;
+    const int per_sm = cache->dtype != ATTN_KV_BF16 ? 3 : head_dim == 64 ? 3 : 2;
     const int64_t needed = ((int64_t)plan->per_launch * (usual + att::kGapChunks) * n_groups +
                             att::kMinChunks - 1) / att::kMinChunks;
     plan->grid = (int)std::max<int64_t>(
@@ -1309,15 +1319,18 @@ int launch_attend(const AttendPlan &plan, const void *q, const attn_kv_cache *ca
         int rc = ATTN_ERR_UNSUPPORTED;
         auto run = [&](auto fmt_c) {
             constexpr int F = decltype(fmt_c)::value;
-            if (head_dim == 128)
+            if (head_dim == 128) {
                 rc = plan.mt == 0 ? att::launch<F, 128, 0, 1>(p, plan.merge, stream)
                                   : att::launch<F, 128, 1, 1>(p, plan.merge, stream);
-            else if (F == att::kBF16 || plan.heads == 1)
-                rc = plan.mt == 0 ? att::launch<F, 64, 0, 1>(p, plan.merge, stream)
-                                  : att::launch<F, 64, 1, 1>(p, plan.merge, stream);
-            else if constexpr (F != att::kBF16)
-                rc = plan.mt == 0 ? att::launch<F, 64, 0, 2>(p, plan.merge, stream)
-                                  : att::launch<F, 64, 1, 2>(p, plan.merge, stream);
+            } else if (plan.mt == 0) {
+                rc = plan.heads == 1 ? att::launch<F, 64, 0, 1>(p, plan.merge, stream)
+                                     : att::launch<F, 64, 0, 2>(p, plan.merge, stream);
+            } else {
+                if (plan.heads == 1)
+                    rc = att::launch<F, 64, 1, 1>(p, plan.merge, stream);
+                else if constexpr (F != att::kBF16)
+                    rc = att::launch<F, 64, 1, 2>(p, plan.merge, stream);
+            }
         };
         if (fmt == att::kBF16)
             run(std::integral_constant<int, att::kBF16>{});
