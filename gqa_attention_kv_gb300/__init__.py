@@ -14,6 +14,8 @@ import os
 import struct
 import threading
 
+import torch
+
 from .synth import LINEAR, PAGED, RING  # noqa: F401  (cache-kind constants)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -136,14 +138,16 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it (3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-
-        try:  # the current stream's handle without a Stream object around it (3 us a call)
-            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-        except AttributeError:
+        if _raw_stream is None:
             return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -152,6 +156,17 @@ def _stream(stream):
 def _check(rc, where):
     if rc != ATTN_OK:
         raise AttnError(rc, where)
+
+
+def _want(where, dtype, *tensors):
+    """Refuses tensors that a kernel would misread: of another type, strided, or
+    not on the current device."""
+    device = _device()
+    for t in tensors:
+        if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != device:
+            raise AttnError(ATTN_ERR_UNSUPPORTED,
+                            f"{where}: a {t.dtype} tensor of shape {tuple(t.shape)} is not a "
+                            f"contiguous {dtype} tensor on the current device")
 
 
 class KVCache:
@@ -184,6 +199,13 @@ class KVCache:
         self.layout = int(layout)
         self.k_scale, self.v_scale = k_scale, v_scale
         self.scale_block = int(scale_block)
+        if self.dtype in (ATTN_KV_FP8_E4M3_SCALED, ATTN_KV_INT8_SCALED) and \
+                isinstance(k_scale, torch.Tensor) and self.scale_block > 0:
+            shape = (self.num_slots // self.scale_block, self.n_kv_heads)
+            for t in (k_scale, v_scale):
+                if t.shape != shape or t.dtype is not torch.float32 or not t.is_contiguous():
+                    raise AttnError(ATTN_ERR_SHAPE, f"KVCache: k_scale and v_scale are contiguous "
+                                                    f"float32 tensors of shape {shape}")
 
     @property
     def n_kv_heads(self):
@@ -215,18 +237,15 @@ class KVCache:
 
 def attn_kv_append(k_new, v_new, slot_mapping, cache: KVCache, err=None, stream=None):
     """cache.k[slot_mapping[i]] = k_new[i] (same for v); slot_mapping int64 [n]."""
-    c = cache.packed()
-    rc = lib().attn_kv_append(_ptr(k_new), _ptr(v_new), _ptr(slot_mapping),
-                              slot_mapping.shape[0], c, cache.n_kv_heads,
-                              cache.head_dim, _ptr(err), _stream(stream))
+    shape = cache.k.shape
+    rc = lib().attn_kv_append(_ptr(k_new), _ptr(v_new), _ptr(slot_mapping), slot_mapping.shape[0], cache.packed(), shape[1], shape[-1],
+                              _ptr(err), _stream(stream))
     _check(rc, "attn_kv_append")
 
 
 def attn_kv_reference(k, ref=None, stream=None):
     """Per-head mean of bf16 keys k [n, Hkv, D] as float32 [Hkv, D] (the FP8
     cache's reference vector).  Writes into ref if given."""
-    import torch
-
     n, Hkv, D = k.shape
     if ref is None:
         ref = torch.empty(Hkv, D, dtype=torch.float32, device=k.device)
@@ -267,8 +286,6 @@ def attn_decode(q, cache: KVCache, seq_lens, positions, max_seq_len, window, sca
     Returns out (bf16 [B, R, Hq, D]).  A workspace (zero-filled uint8 device
     tensor of at least attn_decode_workspace_size bytes) is allocated if not
     given; one kept across calls needs no clearing."""
-    import torch
-
     B, R, Hq, D = q.shape
     if out is None:
         out = torch.empty_like(q)
@@ -298,8 +315,6 @@ def attn_decode_append(q, k_new, v_new, slot_mapping, cache: KVCache, seq_lens, 
     positions and the block table were not written by the kernel launched
     just before on this stream (ATTN_DECODE_TABLES_EARLY); cache_early: nor
     are the cache's other rows (ATTN_DECODE_CACHE_EARLY, implies tables_early)."""
-    import torch
-
     B, R, Hq, D = q.shape
     if out is None:
         out = torch.empty_like(q)
@@ -322,8 +337,6 @@ def attn_decode_append(q, k_new, v_new, slot_mapping, cache: KVCache, seq_lens, 
 
 def attn_prefill(q, k, v, window, scale, out=None, err=None, stream=None):
     """Causal prefill.  q bf16 [B, T, Hq, D], k/v bf16 [B, T, Hkv, D] -> out [B, T, Hq, D]."""
-    import torch
-
     B, T, Hq, D = q.shape
     if out is None:
         out = torch.empty_like(q)
@@ -339,8 +352,6 @@ def attn_decode_noalloc(q, cache: KVCache, seq_lens, positions, max_seq_len, win
     allocate device memory: the library uses its own fixed scratch array
     (ATTN_DECODE_NOALLOC_SCRATCH_BYTES per GPU).  Calls that overlap on the
     GPU share that array and race; order them on one stream."""
-    import torch
-
     f = lib().attn_decode_noalloc
     B, R, Hq, D = q.shape
     if out is None:
@@ -372,11 +383,13 @@ def attn_decode_sinks(q, cache: KVCache, seq_lens, positions, max_seq_len, windo
     each request's first n_sinks slots and turn the others.  A workspace (at
     least attn_decode_sinks_workspace_size bytes, zero-filled before its first
     use) is allocated if not given."""
-    import torch
-
     B, R, Hq, D = q.shape
     if out is None:
         out = torch.empty_like(q)
+    _want("attn_decode_sinks", torch.bfloat16, q, out)
+    _want("attn_decode_sinks", torch.int32, seq_lens, positions)
+    if seq_lens.shape[0] < B or positions.numel() < B * R:
+        raise AttnError(ATTN_ERR_SHAPE, "attn_decode_sinks: seq_lens [B], positions [B * R]")
     if workspace is None:
         need = attn_decode_sinks_workspace_size(cache, B, R, Hq, max_seq_len, window, n_sinks)
         workspace = torch.zeros(need, dtype=torch.uint8, device=q.device) if need > 0 else None
@@ -394,11 +407,12 @@ def attn_decode_sinks(q, cache: KVCache, seq_lens, positions, max_seq_len, windo
 def attn_prefill_sinks(q, k, v, window, n_sinks, scale, out=None, err=None, stream=None):
     """attn_prefill under a sliding window whose first n_sinks tokens of each
     sequence stay visible.  Shapes as attn_prefill's."""
-    import torch
-
     B, T, Hq, D = q.shape
     if out is None:
         out = torch.empty_like(q)
+    _want("attn_prefill_sinks", torch.bfloat16, q, k, v, out)
+    if k.shape != v.shape or k.shape[:2] != q.shape[:2] or k.shape[3] != D:
+        raise AttnError(ATTN_ERR_SHAPE, "attn_prefill_sinks: k and v are [B, T, Hkv, D]")
     rc = lib().attn_prefill_sinks(_ptr(q), _ptr(k), _ptr(v), B, T, int(window), int(n_sinks), Hq,
                                   k.shape[2], D, float(scale), _ptr(out), _ptr(err),
                                   _stream(stream))
@@ -406,11 +420,25 @@ def attn_prefill_sinks(q, k, v, window, n_sinks, scale, out=None, err=None, stre
     return out
 
 
+def _want_rows(where, block_table, refs, rows, a, b):
+    _want(where, torch.int32, block_table, refs, rows, a, b)
+    if block_table.dim() != 2 or not rows.shape == a.shape == b.shape:
+        raise AttnError(ATTN_ERR_SHAPE, f"{where}: block_table is [rows, max_blocks], the row "
+                                        "arguments are of one length")
+
+
+def _want_moves(where, moves, n_moves):
+    _want(where, torch.int32, moves, n_moves)
+    if moves.dim() != 2 or moves.shape[1] != 3 or n_moves.numel() < 1:
+        raise AttnError(ATTN_ERR_SHAPE, f"{where}: moves is [n, 3], n_moves [1]")
+
+
 def attn_pages_free(block_table, refs, rows, from_block, to_block, err=None, stream=None):
     """Entries from_block[i] .. to_block[i] - 1 of row rows[i] of block_table
     (int32 [table_rows, max_blocks]) give their page back (refs, int32
     [num_pages], counts a page's entries) and become -1.  rows, from_block,
     to_block: int32 [n] on the device."""
+    _want_rows("attn_pages_free", block_table, refs, rows, from_block, to_block)
     rc = lib().attn_pages_free(_ptr(block_table), block_table.shape[1], block_table.shape[0],
                                _ptr(rows), _ptr(from_block), _ptr(to_block), rows.shape[0],
                                _ptr(refs), refs.shape[0], _ptr(err), _stream(stream))
@@ -421,6 +449,7 @@ def attn_pages_reserve(block_table, refs, rows, from_block, to_block, err=None, 
     """Entries from_block[i] .. to_block[i] - 1 of row rows[i] that are -1 take
     the lowest free pages (refs 0), in order.  ATTN_ERR_PAGES in err when the
     pool runs out."""
+    _want_rows("attn_pages_reserve", block_table, refs, rows, from_block, to_block)
     rc = lib().attn_pages_reserve(_ptr(block_table), block_table.shape[1], block_table.shape[0],
                                   _ptr(rows), _ptr(from_block), _ptr(to_block), rows.shape[0],
                                   _ptr(refs), refs.shape[0], _ptr(err), _stream(stream))
@@ -433,6 +462,8 @@ def attn_pages_fork(block_table, refs, src_rows, dst_rows, seq_lens, block_size,
     full pages shared, a partial last page replaced by a free one.  moves (int32
     [at least n, 3]) and n_moves (int32 [1]) receive the copies to carry out
     with attn_pages_copy."""
+    _want_rows("attn_pages_fork", block_table, refs, src_rows, dst_rows, seq_lens)
+    _want_moves("attn_pages_fork", moves, n_moves)
     rc = lib().attn_pages_fork(_ptr(block_table), block_table.shape[1], block_table.shape[0],
                                _ptr(src_rows), _ptr(dst_rows), _ptr(seq_lens), src_rows.shape[0],
                                int(block_size), _ptr(refs), refs.shape[0], _ptr(moves),
@@ -452,8 +483,10 @@ def attn_pages_compact(block_table, refs, block_size, moves, n_moves, used, work
     """Pages in use move to the lowest page ids: block_table and refs follow,
     used (int32 [1]) receives how many pages are in use, moves / n_moves the
     copies to carry out with attn_pages_copy."""
-    import torch
-
+    _want("attn_pages_compact", torch.int32, block_table, refs, used)
+    _want_moves("attn_pages_compact", moves, n_moves)
+    if block_table.dim() != 2 or used.numel() < 1:
+        raise AttnError(ATTN_ERR_SHAPE, "attn_pages_compact: block_table is [rows, max_blocks]")
     if workspace is None:
         workspace = torch.empty(attn_pages_workspace_size(refs.shape[0]), dtype=torch.uint8,
                                 device=refs.device)
@@ -470,6 +503,7 @@ def attn_pages_copy(caches, moves, n_moves, err=None, stream=None):
     each of the paged caches (a KVCache, or a list of them, one per layer)."""
     if isinstance(caches, KVCache):
         caches = [caches]
+    _want_moves("attn_pages_copy", moves, n_moves)
     Hkv, D = (caches[0].n_kv_heads, caches[0].head_dim) if caches else (1, 128)
     rc = lib().attn_pages_copy(b"".join([c.packed() for c in caches]), len(caches), Hkv, D, _ptr(moves), _ptr(n_moves),
                                moves.shape[0], _ptr(err), _stream(stream))

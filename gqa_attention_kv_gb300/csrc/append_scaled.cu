@@ -114,8 +114,8 @@ __global__ void __launch_bounds__(128, 6) kv_append_scaled_kernel(const ScaledPa
     auto good = [&](int64_t s) { return s >= 0 && s < p.num_slots; };
 
     // Slots of rows first_row - 1 .. first_row + 30, a lane each, and the window's
-    // rows themselves: nothing below waits for a second load where a run starts
-    // with the window and ends in these 32 rows, as a prompt's do.
+    // rows themselves: nothing below waits for a second load where a run ends in
+    // the window, as a prompt's do whose blocks begin with it.
     const int64_t seen = first_row - 1 + lane;
     const int64_t my_slot = seen >= 0 && seen < p.n ? __ldg(p.slots + seen) : -1;
     uint4 x[kPasses];
@@ -142,7 +142,10 @@ __global__ void __launch_bounds__(128, 6) kv_append_scaled_kernel(const ScaledPa
             report_error(p.err, ATTN_ERR_BOUNDS);
         }
     }
+    // the scales that the runs' blocks hold, all in one trip
+    const float my_scale = start ? scales[(my_slot >> p.shift) * heads + h] : 0.f;
     uint32_t starts = __ballot_sync(0xffffffffu, start);
+    bool intact = true;  // x holds the window's rows
     while (starts != 0) {
         const int at_lane = __ffs(starts) - 1;  // of the run's first row
         const int64_t i0 = first_row - 1 + at_lane;
@@ -170,9 +173,6 @@ __global__ void __launch_bounds__(128, 6) kv_append_scaled_kernel(const ScaledPa
                 if (take < 32) break;
             }
         }
-        // whether the window's rows in registers are all of the run's; a run's rows
-        // without a slot are not stored, nor counted
-        const bool held_rows = i0 == first_row && i1 <= first_row + min(p.window, kPasses * kRows);
         auto slot_of = [&](int64_t i) -> int64_t {  // all lanes together
             const int64_t l = i - (first_row - 1);
             const int64_t s = __shfl_sync(0xffffffffu, my_slot, (int)(l & 31));
@@ -196,9 +196,12 @@ __global__ void __launch_bounds__(128, 6) kv_append_scaled_kernel(const ScaledPa
         // pairs, INT8 codes need no clamp (|x r| <= 127 (1 + 2^-22)), addresses advance
         // by one stride.
         const int64_t slot0 = __shfl_sync(0xffffffffu, my_slot, at_lane);
+        const int r0 = at_lane - 1;                                    // rows of the window
+        const int r1 = (int)min(i1 - first_row, (int64_t)(kPasses * kRows + 1));
+        const int my_r = lane / kLanes;  // this lane's row of the first pass
         bool short_way =
-            held_rows && ref == nullptr &&
-            __all_sync(0xffffffffu, lane < at_lane || seen >= i1 ||
+            intact && ref == nullptr && r1 <= min(p.window, kPasses * kRows) &&
+            __all_sync(0xffffffffu, lane < at_lane || lane > r1 ||
                                         my_slot == slot0 + (lane - at_lane));
         float amax = 0.f;
         bool nan = false;
@@ -206,7 +209,7 @@ __global__ void __launch_bounds__(128, 6) kv_append_scaled_kernel(const ScaledPa
             uint32_t mx = 0;
 #pragma unroll
             for (int u = 0; u < kPasses; ++u) {
-                if (i0 + u * kRows + lane / kLanes >= i1) continue;  // another run's rows
+                if (my_r + u * kRows < r0 || my_r + u * kRows >= r1) continue;  // another run's
                 mx = max_nan_bf16x2(mx, x[u].x & 0x7FFF7FFFu);
                 mx = max_nan_bf16x2(mx, x[u].y & 0x7FFF7FFFu);
                 mx = max_nan_bf16x2(mx, x[u].z & 0x7FFF7FFFu);
@@ -220,9 +223,10 @@ __global__ void __launch_bounds__(128, 6) kv_append_scaled_kernel(const ScaledPa
             amax = fmaxf(lo, hi);
         }
         if (!short_way) {
+        intact = false;
         amax = 0.f;
         for (int64_t base = i0; base < i1; base += kPasses * kRows) {
-            if (!held_rows) load(base);
+            load(base);
 #pragma unroll
             for (int u = 0; u < kPasses; ++u) {
                 const int64_t i = base + u * kRows + lane / kLanes, s = slot_of(i);
@@ -241,7 +245,7 @@ __global__ void __launch_bounds__(128, 6) kv_append_scaled_kernel(const ScaledPa
         for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         }
         const int64_t at = block * heads + h;
-        const float held = fresh ? 0.f : fmaxf(scales[at], 0.f);
+        const float held = fresh ? 0.f : fmaxf(__shfl_sync(0xffffffffu, my_scale, at_lane), 0.f);
         const float now = fmaxf(fmaxf(held, __fdiv_rn(amax, kQMax)), kScaleFloor);
         const float r = __frcp_rn(now);
         if (!fresh && held > 0.f && now > held) {
@@ -272,13 +276,12 @@ __global__ void __launch_bounds__(128, 6) kv_append_scaled_kernel(const ScaledPa
             nan = true;
         }
         if (short_way) {
-            uint8_t *dst = cache + p.place.head_offset(slot0 + lane / kLanes, h) +
+            const int64_t row_bytes = (int64_t)p.place.head_bytes * (p.place.rows == 0 ? heads : 1);
+            uint8_t *dst = cache + p.place.head_offset(slot0, h) + (my_r - r0) * row_bytes +
                            (lane & (kLanes - 1)) * 8;
-            const int64_t step =
-                (int64_t)kRows * p.place.head_bytes * (p.place.rows == 0 ? heads : 1);
 #pragma unroll
-            for (int u = 0; u < kPasses; ++u, dst += step) {
-                if (i0 + u * kRows + lane / kLanes >= i1) break;
+            for (int u = 0; u < kPasses; ++u, dst += kRows * row_bytes) {
+                if (my_r + u * kRows < r0 || my_r + u * kRows >= r1) continue;
                 const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
                 float f[8];
 #pragma unroll
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(128, 6) kv_append_scaled_kernel(const ScaledPa
             __syncwarp();
             continue;
         }
-        const bool kept = held_rows || i1 - i0 <= kPasses * kRows;
+        const bool kept = i1 - i0 <= kPasses * kRows;
         for (int64_t base = i0; base < i1; base += kPasses * kRows) {
             if (!kept) load(base);
 #pragma unroll
@@ -333,10 +336,14 @@ int launch_kv_append_scaled(const void *k_new, const void *v_new, const int64_t 
     while ((1 << p.shift) < cache->scale_block) ++p.shift;
     p.place = kv_place(cache, n_kv_heads, head_dim, 1);
     p.err = err;
-    // A step's rows mostly start runs of their own: a warp each.  A prompt's
-    // are runs of a whole block: a warp takes the starts among 16 rows.
+    // A step's rows mostly start runs of their own: a warp each.  A prompt's are runs
+    // of whole blocks: a warp takes the starts among 16 rows.  Which of the two a call
+    // is shows in n alone, so a warp takes the fewest rows with which the warps are no
+    // more than 64 an SM.
     const int64_t per_row = 2ll * n_kv_heads;
-    p.window = n * per_row <= (int64_t)device_sm_count() * 32 ? 1 : 16;
+    p.window = 1;
+    while (p.window < 16 && (n + p.window - 1) / p.window * per_row > (int64_t)device_sm_count() * 64)
+        p.window *= 2;
     const int64_t warps = (n + p.window - 1) / p.window * per_row;
     const int64_t blocks = (warps + 3) / 4;
     if (blocks >= (int64_t(1) << 31)) return ATTN_ERR_SHAPE;

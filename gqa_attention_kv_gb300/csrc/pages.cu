@@ -25,8 +25,11 @@ namespace gqa {
 namespace {
 
 constexpr int kScanThreads = 1024;
-constexpr int kTile = kScanThreads * 4;  // pages a block looks at at a time
-constexpr int kListed = 8192;            // free pages held at a time (reserve)
+// Pages a block looks at at a time: 16 a thread, so a pool of 16,384 is one round
+// of loads; 4 a thread where the round's free pages are listed in shared memory.
+constexpr int kPer = 16, kTile = kScanThreads * kPer;
+constexpr int kListPer = 4, kListTile = kScanThreads * kListPer;
+constexpr int kListed = 2 * kListTile;
 
 // Exclusive prefix of v over the block, and the block's sum in `sum`.  All
 // kScanThreads threads take part.
@@ -53,15 +56,31 @@ __device__ __forceinline__ int block_scan(int v, int &sum) {
     return x - v + (warp == 0 ? 0 : before);
 }
 
-// Reference counts of pages base + 4 tid .. + 3 (1 past the pool: in use).
-__device__ __forceinline__ int4 load_refs(const int32_t *refs, int base, int num_pages) {
-    const int p = base + 4 * (int)threadIdx.x;
-    if (p + 3 < num_pages) return *reinterpret_cast<const int4 *>(refs + p);
-    int4 r = make_int4(1, 1, 1, 1);
-    if (p < num_pages) r.x = refs[p];
-    if (p + 1 < num_pages) r.y = refs[p + 1];
-    if (p + 2 < num_pages) r.z = refs[p + 2];
-    return r;
+// Which of the PER pages base + PER tid .. are free, a bit each (none past the pool).
+template <int PER>
+__device__ __forceinline__ uint32_t free_bits(const int32_t *refs, int base, int num_pages) {
+    const int p = base + PER * (int)threadIdx.x;
+    uint32_t bits = 0;
+    if (p + PER <= num_pages) {
+        int4 r[PER / 4];
+#pragma unroll
+        for (int i = 0; i < PER / 4; ++i) r[i] = *reinterpret_cast<const int4 *>(refs + p + 4 * i);
+#pragma unroll
+        for (int i = 0; i < PER / 4; ++i)
+            bits |= (uint32_t)((r[i].x <= 0) | (r[i].y <= 0) << 1 | (r[i].z <= 0) << 2 |
+                               (r[i].w <= 0) << 3) << (4 * i);
+    } else {
+        for (int i = 0; i < PER; ++i)
+            if (p + i < num_pages && refs[p + i] <= 0) bits |= 1u << i;
+    }
+    return bits;
+}
+
+// The bits of those pages that are in the pool.
+template <int PER>
+__device__ __forceinline__ uint32_t pool_bits(int base, int num_pages) {
+    const int n = num_pages - (base + PER * (int)threadIdx.x);
+    return n <= 0 ? 0u : n >= PER ? (1u << PER) - 1u : (1u << n) - 1u;
 }
 
 __global__ void __launch_bounds__(256) pages_free_kernel(int32_t *table, int max_blocks,
@@ -118,16 +137,14 @@ __global__ void __launch_bounds__(kScanThreads)
         for (int done = 0; done < total;) {
             // the lowest free pages, as many as are needed and fit the list
             int listed = 0;
-            for (int p = 0; p < num_pages && listed < total - done && listed + kTile <= kListed;
-                 p += kTile) {
-                const int4 r = load_refs(refs, p, num_pages);
+            for (int p = 0;
+                 p < num_pages && listed < total - done && listed + kListTile <= kListed;
+                 p += kListTile) {
+                uint32_t bits = free_bits<kListPer>(refs, p, num_pages);
                 int sum;
-                int at = listed + block_scan((r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0), sum);
-                const int page = p + 4 * threadIdx.x;
-                if (r.x == 0) list[at++] = page;
-                if (r.y == 0) list[at++] = page + 1;
-                if (r.z == 0) list[at++] = page + 2;
-                if (r.w == 0) list[at++] = page + 3;
+                int at = listed + block_scan(__popc(bits), sum);
+                for (; bits != 0; bits &= bits - 1)
+                    list[at++] = p + kListPer * threadIdx.x + __ffs(bits) - 1;
                 listed += sum;
             }
             __syncthreads();
@@ -232,19 +249,14 @@ __global__ void __launch_bounds__(kScanThreads) pages_fork_kernel(const ForkPara
     __syncthreads();
     int given = 0;
     for (int base = 0; base < p.num_pages && given < need; base += kTile) {
-        const int4 r = load_refs(p.refs, base, p.num_pages);
-        const int free4[4] = {r.x == 0, r.y == 0, r.z == 0, r.w == 0};
+        uint32_t bits = free_bits<kPer>(p.refs, base, p.num_pages);
         int sum;
-        int at = given + block_scan(free4[0] + free4[1] + free4[2] + free4[3], sum);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (free4[u] && at < need) {
-                const int page = base + 4 * threadIdx.x + u, i = p.moves[3 * at + 1];
-                p.table[(int64_t)p.dst_rows[i] * p.max_blocks + p.seq_lens[i] / p.block_size] = page;
-                p.moves[3 * at + 1] = page;
-                p.refs[page] = 1;
-            }
-            at += free4[u];
+        int at = given + block_scan(__popc(bits), sum);
+        for (; bits != 0 && at < need; bits &= bits - 1, ++at) {
+            const int page = base + kPer * threadIdx.x + __ffs(bits) - 1, i = p.moves[3 * at + 1];
+            p.table[(int64_t)p.dst_rows[i] * p.max_blocks + p.seq_lens[i] / p.block_size] = page;
+            p.moves[3 * at + 1] = page;
+            p.refs[page] = 1;
         }
         given += sum;
     }
@@ -268,41 +280,27 @@ __global__ void __launch_bounds__(kScanThreads)
     int U = 0;
     {
         int mine = 0;
-        for (int base = 0; base < num_pages; base += kTile) {
-            const int4 r = load_refs(refs, base, num_pages);
-            const int p = base + 4 * threadIdx.x;
-            mine += (p < num_pages && r.x > 0) + (p + 1 < num_pages && r.y > 0) +
-                    (p + 2 < num_pages && r.z > 0) + (p + 3 < num_pages && r.w > 0);
-        }
+        for (int base = 0; base < num_pages; base += kTile)
+            mine += __popc(pool_bits<kPer>(base, num_pages) &
+                           ~free_bits<kPer>(refs, base, num_pages));
         block_scan(mine, U);
     }
     int takes = 0, leaves = 0;  // free pages below U, pages in use from U on
     for (int base = 0; base < num_pages; base += kTile) {
-        const int4 r = load_refs(refs, base, num_pages);
-        const int rr[4] = {r.x, r.y, r.z, r.w};
-        const int p = base + 4 * threadIdx.x;
-        int t = 0, l = 0;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            t += p + u < U && rr[u] <= 0;
-            l += p + u >= U && p + u < num_pages && rr[u] > 0;
-        }
+        const int p = base + kPer * threadIdx.x;
+        const uint32_t free = free_bits<kPer>(refs, base, num_pages);
+        const uint32_t pool = pool_bits<kPer>(base, num_pages);
+        const uint32_t low = pool & pool_bits<kPer>(base, U);
+        uint32_t t = free & low, l = pool & ~low & ~free;
         int st, sl;
-        int at_t = takes + block_scan(t, st), at_l = leaves + block_scan(l, sl);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (p + u < U) {
-                if (rr[u] <= 0) {
-                    if (at_t < max_moves) moves[3 * at_t + 1] = p + u;
-                    ++at_t;
-                }
-            } else if (p + u < num_pages) {
-                to[p + u] = p + u;
-                if (rr[u] > 0) {
-                    if (at_l < max_moves) moves[3 * at_l] = p + u;
-                    ++at_l;
-                }
-            }
+        int at_t = takes + block_scan(__popc(t), st), at_l = leaves + block_scan(__popc(l), sl);
+        for (; t != 0; t &= t - 1, ++at_t)
+            if (at_t < max_moves) moves[3 * at_t + 1] = p + __ffs(t) - 1;
+        for (; l != 0; l &= l - 1, ++at_l)
+            if (at_l < max_moves) moves[3 * at_l] = p + __ffs(l) - 1;
+        for (uint32_t high = pool & ~low; high != 0; high &= high - 1) {
+            const int page = p + __ffs(high) - 1;
+            to[page] = page;
         }
         takes += st;
         leaves += sl;

@@ -310,6 +310,42 @@ def test_fused_step_is_append_then_decode(fmt):
     assert int(err) == 0 and torch.equal(out, want)
 
 
+@pytest.mark.parametrize("B,H,lo,hi", [(40, 2, 1, 20000),   # one long request among short ones
+                                       (1, 1, 30000, 30000)])  # one unit over the whole GPU
+def test_decode_in_very_many_parts(B, H, lo, hi):
+    """More parts of a unit than a warp looks up at once, added in the kernel and
+    by the merge kernel."""
+    g = gen(B)
+    per = -(-hi // 16) * 16
+    lens = torch.randint(1, 20, (B,), generator=g, dtype=torch.int32)
+    lens[B // 2] = hi
+    case = Case("int8", B * per, H, 64, 16, per=per)
+    for codes, scale in ((case.k, case.ks), (case.v, case.vs)):
+        codes.copy_(torch.randint(-127, 128, codes.shape, generator=g, dtype=torch.int8))
+        scale.copy_(torch.rand(scale.shape, generator=g) * 0.02 + 0.005)
+    q = torch.randn(B, 1, 2 * H, 64, generator=g).bfloat16()
+    pos = lens - 1
+    want, mass = ref.decode(q, ref.dequantized("int8", case.k, case.ks, 16),
+                            ref.dequantized("int8", case.v, case.vs, 16),
+                            lambda b, t: b * per + t, lens, pos, 0, 0, 0.125)
+    got = gq.attn_decode(q.to(DEV), case.cuda(), lens.to(DEV), pos.to(DEV), hi, 0, 0.125)
+    ref.check_output(got, want, mass)
+
+
+@pytest.mark.parametrize("n", [100, 700, 1500, 3500])
+def test_append_steps_of_many_requests(n):
+    """One row a request, from a warp a row to a warp for the runs of several."""
+    g = gen(n)
+    case = Case("e4m3", n * 16, 4, 64, 16).fill(g)
+    case.cuda()
+    k, v = new_rows(g, n, 4, 64, 5.0)
+    slots = torch.arange(n) * 16 + torch.randint(0, 16, (n,), generator=g)
+    slots = slots[torch.randperm(n, generator=g)]
+    case.append(k, v, slots)
+    assert gpu_append(case, k, v, slots) == 0
+    case.check()
+
+
 def test_one_workspace_serves_both_decodes():
     """A workspace that bf16 calls keep their zeroed counters in may serve scaled
     calls in between, graphs replayed one after the other among them."""

@@ -167,3 +167,24 @@ def test_page_copy_refusals(lib):  # noqa: F811
     assert rc([paged()], most=0) == gq.ATTN_OK
     assert rc([paged()], n=0) == gq.ATTN_OK
     assert "free page" in gq.attn_status_string(gq.ATTN_ERR_PAGES)
+
+
+def test_wrappers_refuse_what_the_kernels_would_misread():
+    """Tensors of another type, order or device, and shapes that disagree."""
+    import torch
+
+    bad = torch.zeros(2, 1, 8, 64, dtype=torch.bfloat16)  # not on a GPU
+    i32 = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises((gq.AttnError, RuntimeError)):
+        gq.attn_decode_sinks(bad, cache(dtype=gq.ATTN_KV_BF16, D=64), i32, i32, 16, 8, 4, 0.1)
+    with pytest.raises((gq.AttnError, RuntimeError)):
+        gq.attn_prefill_sinks(bad, bad, bad, 8, 4, 0.1)
+    with pytest.raises((gq.AttnError, RuntimeError)):
+        gq.attn_pages_free(i32.view(1, 2), i32, i32, i32, i32)
+    codes, scale = torch.zeros(64, 2, 64, dtype=torch.int8), torch.ones(4, 2)
+    gq.KVCache(gq.LINEAR, codes, codes, slots_per_seq=64, dtype=I8, k_scale=scale, v_scale=scale,
+               scale_block=16)
+    for other in (torch.ones(2, 4).T, torch.ones(2, 2), torch.ones(4, 2).double()):
+        with pytest.raises(gq.AttnError):
+            gq.KVCache(gq.LINEAR, codes, codes, slots_per_seq=64, dtype=I8, k_scale=scale,
+                       v_scale=other, scale_block=16)
