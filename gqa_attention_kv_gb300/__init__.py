@@ -9,6 +9,7 @@ missing or a call is refused, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -153,6 +154,18 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _allocate_on(stream):
+    """The context in which a call's own tensors are made: the stream that uses
+    them, so that they are ready for it and not handed on before it is done."""
+    if stream is None:
+        return _HERE_AND_NOW
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int)
+                             else stream)
+
+
+_HERE_AND_NOW = contextlib.nullcontext()
+
+
 def _check(rc, where):
     if rc != ATTN_OK:
         raise AttnError(rc, where)
@@ -287,12 +300,13 @@ def attn_decode(q, cache: KVCache, seq_lens, positions, max_seq_len, window, sca
     tensor of at least attn_decode_workspace_size bytes) is allocated if not
     given; one kept across calls needs no clearing."""
     B, R, Hq, D = q.shape
-    if out is None:
-        out = torch.empty_like(q)
-    if workspace is None:
-        need = attn_decode_workspace_size(cache, B, R, Hq, max_seq_len, window)
-        if need > 0:
-            workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
+    with _allocate_on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            need = attn_decode_workspace_size(cache, B, R, Hq, max_seq_len, window)
+            if need > 0:
+                workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
     c = cache.packed()
     rc = lib().attn_decode(_ptr(q), c, _ptr(seq_lens), _ptr(positions), B, R,
                            int(max_seq_len), int(window), Hq, cache.n_kv_heads, D, float(scale),
@@ -316,12 +330,13 @@ def attn_decode_append(q, k_new, v_new, slot_mapping, cache: KVCache, seq_lens, 
     just before on this stream (ATTN_DECODE_TABLES_EARLY); cache_early: nor
     are the cache's other rows (ATTN_DECODE_CACHE_EARLY, implies tables_early)."""
     B, R, Hq, D = q.shape
-    if out is None:
-        out = torch.empty_like(q)
-    if workspace is None:
-        need = attn_decode_workspace_size(cache, B, R, Hq, max_seq_len, window)
-        if need > 0:
-            workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
+    with _allocate_on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            need = attn_decode_workspace_size(cache, B, R, Hq, max_seq_len, window)
+            if need > 0:
+                workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
     c = cache.packed()
     rc = lib().attn_decode_append(
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), _ptr(rope_inv_freq),
@@ -384,15 +399,17 @@ def attn_decode_sinks(q, cache: KVCache, seq_lens, positions, max_seq_len, windo
     least attn_decode_sinks_workspace_size bytes, zero-filled before its first
     use) is allocated if not given."""
     B, R, Hq, D = q.shape
-    if out is None:
-        out = torch.empty_like(q)
+    with _allocate_on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            need = attn_decode_sinks_workspace_size(cache, B, R, Hq, max_seq_len, window, n_sinks)
+            if need > 0:
+                workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
     _want("attn_decode_sinks", torch.bfloat16, q, out)
     _want("attn_decode_sinks", torch.int32, seq_lens, positions)
     if seq_lens.shape[0] < B or positions.numel() < B * R:
         raise AttnError(ATTN_ERR_SHAPE, "attn_decode_sinks: seq_lens [B], positions [B * R]")
-    if workspace is None:
-        need = attn_decode_sinks_workspace_size(cache, B, R, Hq, max_seq_len, window, n_sinks)
-        workspace = torch.zeros(need, dtype=torch.uint8, device=q.device) if need > 0 else None
     c = cache.packed()
     rc = lib().attn_decode_sinks(
         _ptr(q), c, _ptr(seq_lens), _ptr(positions), B, R, int(max_seq_len),
@@ -408,8 +425,9 @@ def attn_prefill_sinks(q, k, v, window, n_sinks, scale, out=None, err=None, stre
     """attn_prefill under a sliding window whose first n_sinks tokens of each
     sequence stay visible.  Shapes as attn_prefill's."""
     B, T, Hq, D = q.shape
-    if out is None:
-        out = torch.empty_like(q)
+    with _allocate_on(stream):
+        if out is None:
+            out = torch.empty_like(q)
     _want("attn_prefill_sinks", torch.bfloat16, q, k, v, out)
     if k.shape != v.shape or k.shape[:2] != q.shape[:2] or k.shape[3] != D:
         raise AttnError(ATTN_ERR_SHAPE, "attn_prefill_sinks: k and v are [B, T, Hkv, D]")
@@ -488,8 +506,9 @@ def attn_pages_compact(block_table, refs, block_size, moves, n_moves, used, work
     if block_table.dim() != 2 or used.numel() < 1:
         raise AttnError(ATTN_ERR_SHAPE, "attn_pages_compact: block_table is [rows, max_blocks]")
     if workspace is None:
-        workspace = torch.empty(attn_pages_workspace_size(refs.shape[0]), dtype=torch.uint8,
-                                device=refs.device)
+        with _allocate_on(stream):
+            workspace = torch.empty(attn_pages_workspace_size(refs.shape[0]), dtype=torch.uint8,
+                                    device=refs.device)
     rc = lib().attn_pages_compact(_ptr(block_table), block_table.shape[1], block_table.shape[0],
                                   int(block_size), _ptr(refs), refs.shape[0], _ptr(moves),
                                   moves.shape[0], _ptr(n_moves), _ptr(used), _ptr(workspace),

@@ -1,5 +1,5 @@
-// attend.cu -- decode attention fed from registers: 8-bit caches with a scale
-// per block of tokens and head, and sliding windows with sinks.
+// attend.cu -- decode attention over 8-bit caches with a scale per block of tokens
+// and head, and under sliding windows with sinks.
 //
 // What is computed: for request b, query row r at position pos and query head
 // h (KV head h / group),
@@ -13,24 +13,42 @@
 // out = O / l.  M follows the maximum of x + lv, so w (rounded once to f16)
 // stays in f16's range whatever the scales are, and l is a 32-bit sum.
 //
-// GB300 mapping.  A decode reads every key once and computes little with it:
-// HBM bandwidth bounds it, so what counts is bytes in flight.  Each warp loads
-// its keys straight from global memory into the registers of the mma.sync
-// fragments that use them: the head dimension enters the k index of Q K^T in
-// a permuted order (q's fragments in the same one) so that a thread's share of
-// a key is whole 16-byte pieces, and every load instruction covers whole
-// sectors.  No shared memory, barrier or copy engine stands between a load and
-// its use: each warp runs alone over its own 16-key chunks, K of the next
-// chunk requested as soon as Q K^T has consumed this one's, V after P V, and
-// the 12 to 16 warps of an SM hide the latency of each other.  A row's address
-// is its own, so pages of any size, rings and freed pages cost no other path.
+// GB300 mapping.  A decode reads every key once and computes little with it: HBM
+// bandwidth is its floor, and what stands before the floor is the work of a
+// warp per key (unpacking codes, mma.sync fragments, the softmax), so the kernel
+// is built for many bytes in flight and few instructions a key:
+//   * Each warp runs alone over its own chunks of 16 keys and copies them into
+//     its own ring in shared memory with cp.async, 4 KB of K and 4 KB of V a step
+//     for 8-bit caches (32 keys of 128 dims), one step ahead (two for bf16).  No
+//     barrier stands between a copy and its use, a row's address is its own (pages
+//     of any size, rings and freed pages need no other kernel), and a step whose
+//     keys are all there and evenly spaced takes a path without per-key checks.
+//   * The head dimension enters the k index of Q K^T in a permuted order (q's
+//     fragments in the same one), so a thread's share of a key is whole 16-byte
+//     pieces: one LDS.128 feeds four k-steps, and codes become f16 fragments in
+//     registers, two instructions a four codes (E4M3) or three to five (INT8).
+//     V's codes of two keys are interleaved bytewise before they are converted,
+//     so no transposing load is needed.
+//   * Up to 8 query rows (MT 0) keys are the rows of the products, S^T = K Q^T
+//     and O^T = V^T P^T; up to 16 (MT 1) the query rows are.
+//   * A score's softmax reference moves only past 2^8 (lazily), and a step that
+//     every row sees whole is not masked.
+// Measured against earlier forms of this kernel (64 requests x 4 rows, 64 to 4,096
+// INT8 keys, 8 KV heads of 128, pages of 16; floor 41 us): keys loaded into the
+// fragments' registers one step ahead 127 us, in the ring 82, with in-kernel merging
+// and steps without per-key checks 74, and with 32 keys a step on twelve warps an SM
+// instead of 16 on sixteen 63 us (4.4 TB/s).  One query row: 5.1 TB/s E4M3, 6.2 bf16
+// (64 x 2,080 keys).  What bounds it now: the warps' own dependency chains (issue
+// slots about half used), and at one row a KV head DRAM.
 //
-// Work: a unit is (request, block of query rows, KV head).  All units' chunks
-// are laid end to end and cut into equal shares, one per CTA of a persistent
-// grid, whatever the lengths are; the four warps of a CTA take a share's
-// chunks in turn and merge through shared memory.  A unit cut across CTAs
-// leaves partial states that attend_merge_kernel adds in part order, so
-// results do not depend on timing.
+// Work: a unit is (request, block of query rows, one or two KV heads).  All units'
+// chunks are laid end to end and cut into equal shares, one per CTA of a
+// persistent grid, whatever the lengths are; the four warps of a CTA take a
+// share's chunks in turn (two warps a head where a unit has two) and merge
+// through shared memory.  A unit cut across CTAs leaves partial states that the
+// CTA storing the last of them adds up, in part order, so results do not depend
+// on timing; units that may lie in very many parts are left to
+// attend_merge_kernel.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -50,9 +68,17 @@ constexpr int kChunk = 16;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxEntries = 128;  // (request, row block) pairs per launch
-constexpr int kGapChunks = 24;    // what a change of unit costs a CTA, in chunks
-constexpr int kMinChunks = 4;     // smallest share of a CTA
-constexpr int kKernelParts = 12;  // parts of a unit that its last block adds up
+// What a change of unit costs a CTA, in chunks: in the share arithmetic every unit is
+// followed by so many of nothing.  64 ragged requests (64 to 4,096 keys): 73 us with
+// 12, 63 with 24, 64 with 40.
+constexpr int kGapChunks = 24;
+// Smallest share of a CTA.  One request of 9,000 tokens, window 1,024: 8.2 us with 4
+// chunks, 8.9 with 8, 9.8 with 16.
+constexpr int kMinChunks = 4;
+// Parts of a unit that its last CTA adds up itself.  17 parts: 8.9 us of GPU time
+// against 8.3 with the merge kernel, which costs the host 3 us to launch; 76 parts:
+// 22.5 against 16.4 us.
+constexpr int kKernelParts = 24;
 constexpr float kRescaleLog2 = 8.0f;  // the reference maximum moves past this only (w <= 2^8)
 constexpr float kScaleFloor = 5.421010862427522e-20f;  // 2^-64, the smallest scale
 
@@ -97,11 +123,15 @@ struct Geo {
     static constexpr int kVPieces = kRowBytes / (8 * kVBytes);
     static constexpr int kVWords = kVBytes / 4 * kVPieces;       // words of a key a thread
     static constexpr int kVElems = kVBytes / E;                  // dims of a V piece
-    static constexpr int NSUB = kRowBytes == 64 ? 4 : FMT != kBF16 ? 2 : 1;         // chunks of a step
+    // chunks of a step: 4 KB of K, but for bf16 rows of 128 bytes
+    static constexpr int NSUB = kRowBytes == 64 ? 4 : FMT != kBF16 ? 2 : 1;
     static constexpr int kChunkBytes = kChunk * kRowBytes;
     static constexpr int kStepBytes = NSUB * kChunkBytes;        // K (or V) of a step
+    // Stages and blocks an SM share its 227 KB: 8-bit steps take long enough (twelve
+    // warps unpacking) that one step ahead hides DRAM, bf16 steps do not (64 x 8 heads
+    // of 2,080 keys: 107 us with two stages and three blocks, 88 with three and two).
     static constexpr int kStages = FMT != kBF16 ? 2 : 3;
-    static constexpr int CTAS = kRowBytes == 256 ? 2 : 3;  // blocks of an SM
+    static constexpr int CTAS = kRowBytes == 256 ? 2 : 3;
     static constexpr int kHeadWarps = kWarps / HG;               // warps of a KV head
     static constexpr int kGroup = kHeadWarps * NSUB;             // chunks of a block's step
     static constexpr int kOStride = HD + 4;                      // floats of a parked output row
@@ -1242,10 +1272,8 @@ int plan_attend(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
         1, std::min<int64_t>(needed, (int64_t)per_sm * device_sm_count()));
     const size_t units = (size_t)plan->per_launch * n_groups,
                  slots = (units + plan->grid) * plan->heads;
-    // How many blocks a unit spans when all are as long as they can be.  Up to
-    // kKernelParts the last of them adds the parts up; a unit in more of them
-    // has the merge kernel's eight warps a row (measured where few requests meet
-    // long contexts: 2 x 4 units of 24k keys in 76 parts)
+    // How many CTAs a unit spans when all are as long as they can be: past
+    // kKernelParts the merge kernel adds the parts up
     const int64_t share = std::max<int64_t>(
         att::kMinChunks, (int64_t)units * (usual + att::kGapChunks) / plan->grid);
     plan->merge = usual / share + 1 > att::kKernelParts;

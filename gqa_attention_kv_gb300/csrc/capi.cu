@@ -297,7 +297,7 @@ int validate_decode(const void *q, const attn_kv_cache *cache, const int32_t *se
 
 namespace {
 
-// The register-fed decode of a validated call (batch > 0).
+// attend.cu's decode of a validated call (batch > 0).
 int attend(const void *q, const attn_kv_cache *cache, const int32_t *seq_lens,
            const int32_t *positions, int batch, int q_rows, int max_seq_len, int window,
            int n_sinks, int n_q_heads, int n_kv_heads, int head_dim, float scale, void *out,

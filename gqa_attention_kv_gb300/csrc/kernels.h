@@ -156,8 +156,8 @@ int launch_kv_append_scaled(const void *k_new, const void *v_new, const int64_t 
                             int64_t n, const attn_kv_cache *cache, int n_kv_heads, int head_dim,
                             int32_t *err, cudaStream_t stream);
 
-// Plan of the register-fed decode (attend.cu): scaled caches, and any cache
-// under a sliding window with sinks.  (request, row block) pairs go to the
+// Plan of attend.cu's decode: scaled caches, and any cache under a sliding window
+// with sinks.  (request, row block) pairs go to the
 // kernel per_launch at a time.
 struct AttendPlan {
     int mt;     // 0: up to 8 rows per unit, 1: 16

@@ -298,7 +298,7 @@ int attn_decode_kernel_launches(const attn_kv_cache *cache, int batch, int q_row
  *   and accumulates in fp32.
  *   A scaled cache is read as stored too: codes convert to f16 exactly, q is
  *   taken in f16 (a magnitude of 65520 or more is reported as
- *   ATTN_ERR_UNSUPPORTED), the scales multiply scores and softmax weights in
+ *   ATTN_ERR_UNSUPPORTED; magnitudes under 2^-14 lose precision), the scales multiply scores and softmax weights in
  *   float32, and the weights are rounded once to f16.  A scale is finite and at
  *   least 2^-64 (one below reads as 2^-64).  Its workspace
  *   is like any other's (zero-filled before its first use).

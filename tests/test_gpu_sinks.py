@@ -157,6 +157,41 @@ def test_decode_values_that_are_not_finite():
     assert torch.equal(finite, want)
 
 
+def test_calls_on_a_stream_of_their_own():
+    """Output and workspace that a call makes belong to the stream it is given,
+    as a Stream or a handle; two calls on two streams do not disturb each other."""
+    cache, q, k, v, lens, pos, slot = build(gq.LINEAR, 2, 1, 8, 2, 128, 3000, 4000, 0, 0, 0, 7)
+    q, lens, pos = q.to(DEV), lens.to(DEV), pos.to(DEV)
+    want = gq.attn_decode_sinks(q, cache, lens, pos, 4000, 0, 0, 0.1)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for i in range(12):
+        s = streams[i % 2]
+        outs.append(gq.attn_decode_sinks(q, cache, lens, pos, 4000, 0, 0, 0.1,
+                                         stream=s if i % 3 else s.cuda_stream))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    pq = torch.randn(1, 300, 4, 64, device=DEV).bfloat16()
+    one = gq.attn_prefill_sinks(pq, pq, pq, 50, 4, 0.1)
+    torch.cuda.synchronize()
+    two = gq.attn_prefill_sinks(pq, pq, pq, 50, 4, 0.1, stream=streams[0])
+    torch.cuda.synchronize()
+    assert torch.equal(one, two)
+
+
+def test_strided_and_misplaced_tensors_are_refused():
+    cache, q, k, v, lens, pos, slot = build(gq.LINEAR, 2, 2, 4, 2, 64, 50, 60, 0, 9, 2, 7)
+    q, lens, pos = q.to(DEV), lens.to(DEV), pos.to(DEV)
+    bad = [(q.transpose(2, 3).contiguous().transpose(2, 3), lens, pos), (q.float(), lens, pos),
+           (q, lens.long(), pos), (q, lens, pos[::2]), (q, lens.cpu(), pos), (q, lens[:1], pos)]
+    for args in bad:
+        with pytest.raises(gq.AttnError):
+            gq.attn_decode_sinks(args[0], cache, args[1], args[2], 60, 9, 2, 0.1)
+    with pytest.raises(gq.AttnError):
+        gq.attn_prefill_sinks(q, q, q[:, ::2], 9, 2, 0.1)
+
+
 def test_decode_past_the_tables_of_one_launch():
     """More requests than one launch's tables hold, most of them short."""
     g = gen(1)
