@@ -474,7 +474,7 @@ int check_pool(const int32_t *block_table, int max_blocks, int table_rows, const
         num_pages > (1 << 30))  // page numbers of a tile stay in 32 bits
         return ATTN_ERR_SHAPE;
     if (!block_table || !refs) return ATTN_ERR_NULL;
-    if (!aligned16(block_table) || !aligned16(refs)) return ATTN_ERR_ALIGN;
+    if (!aligned16(refs)) return ATTN_ERR_ALIGN;
     return ATTN_OK;
 }
 

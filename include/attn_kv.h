@@ -498,9 +498,11 @@ int attn_prefill_sinks(const void *q, const void *k, const void *v, int batch, i
  *                *n_moves are left as they were
  * Free pages are handed out lowest first, so results do not depend on timing.
  * A row, length or page outside its array skips what it names and stores
- * ATTN_ERR_BOUNDS in *err_word.  block_table, refs and workspace must be
- * 16-byte aligned.  Calls on one table or pool must be ordered (one stream, or
- * events).  All may be captured into graphs.
+ * ATTN_ERR_BOUNDS in *err_word.  refs and workspace must be 16-byte aligned.
+ * Calls on one table or pool must be ordered (one stream, or events).  All may
+ * be captured into graphs.  Pages named by several entries are shared: writing
+ * one of them (an append that goes back into full pages) changes every row that
+ * names it.
  *
  * attn_pages_free     entries from_block[i] .. to_block[i] - 1 of row rows[i]
  *   (clipped to the row) give back their page and become -1; entries that are
@@ -517,9 +519,10 @@ int attn_prefill_sinks(const void *q, const void *k, const void *v, int batch, i
  *   them first).  Destinations are distinct and none is a source.  Where no page is
  *   left for a partial one its entry is -1 (ATTN_ERR_PAGES).  max_moves >= n.
  *   Carry the moves out (attn_pages_copy) before either row is written to.
- * attn_pages_compact  with U pages in use (*used, int32, device), the i-th
- *   page in use at or above U (ascending) moves to the i-th free page below U:
- *   refs and every entry of the table follow, and the moves copy whole pages.
+ * attn_pages_compact  with U pages in use (*used, int32, device), the i-th page
+ *   in use at or above U (ascending) moves to the i-th free page below U: refs
+ *   and every entry of the table follow, and the moves copy whole pages.  refs
+ *   has to count this table's entries and no others.
  *   max_moves >= the pages that move (at most num_pages / 2): past it no page
  *   moves, and ATTN_ERR_WORKSPACE is stored in *err_word.  A source page's
  *   rows stay readable until its new owner writes them.
