@@ -9,7 +9,6 @@ missing or a call is refused, an exception is raised.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import struct
@@ -154,16 +153,18 @@ def _stream(stream):
     return stream.cuda_stream
 
 
-def _allocate_on(stream):
-    """The context in which a call's own tensors are made: the stream that uses
-    them, so that they are ready for it and not handed on before it is done."""
+def _made(make, like, stream, *args):
+    """make(like, *args), a tensor of the call's own, made on the stream that uses
+    it: ready for it, and not handed on before it is done."""
     if stream is None:
-        return _HERE_AND_NOW
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int)
-                             else stream)
+        return make(like, *args)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int)
+                           else stream):
+        return make(like, *args)
 
 
-_HERE_AND_NOW = contextlib.nullcontext()
+def _zeroed(like, nbytes):
+    return torch.zeros(nbytes, dtype=torch.uint8, device=like.device)
 
 
 def _check(rc, where):
@@ -171,12 +172,11 @@ def _check(rc, where):
         raise AttnError(rc, where)
 
 
-def _want(where, dtype, *tensors):
+def _want(where, device, dtype, *tensors):
     """Refuses tensors that a kernel would misread: of another type, strided, or
-    not on the current device."""
-    device = _device()
+    not on the device that the call launches on."""
     for t in tensors:
-        if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != device:
+        if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
             raise AttnError(ATTN_ERR_UNSUPPORTED,
                             f"{where}: a {t.dtype} tensor of shape {tuple(t.shape)} is not a "
                             f"contiguous {dtype} tensor on the current device")
@@ -300,18 +300,17 @@ def attn_decode(q, cache: KVCache, seq_lens, positions, max_seq_len, window, sca
     tensor of at least attn_decode_workspace_size bytes) is allocated if not
     given; one kept across calls needs no clearing."""
     B, R, Hq, D = q.shape
-    with _allocate_on(stream):
-        if out is None:
-            out = torch.empty_like(q)
-        if workspace is None:
-            need = attn_decode_workspace_size(cache, B, R, Hq, max_seq_len, window)
-            if need > 0:
-                workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
+    if out is None:
+        out = _made(torch.empty_like, q, stream)
+    if workspace is None:
+        need = attn_decode_workspace_size(cache, B, R, Hq, max_seq_len, window)
+        if need > 0:
+            workspace = _made(_zeroed, q, stream, need)
     c = cache.packed()
     rc = lib().attn_decode(_ptr(q), c, _ptr(seq_lens), _ptr(positions), B, R,
                            int(max_seq_len), int(window), Hq, cache.n_kv_heads, D, float(scale),
                            _ptr(out), _ptr(workspace),
-                           0 if workspace is None else workspace.numel() * workspace.element_size(),
+                           0 if workspace is None else workspace.nbytes,
                            _ptr(err), _stream(stream))
     _check(rc, "attn_decode")
     return out
@@ -330,20 +329,19 @@ def attn_decode_append(q, k_new, v_new, slot_mapping, cache: KVCache, seq_lens, 
     just before on this stream (ATTN_DECODE_TABLES_EARLY); cache_early: nor
     are the cache's other rows (ATTN_DECODE_CACHE_EARLY, implies tables_early)."""
     B, R, Hq, D = q.shape
-    with _allocate_on(stream):
-        if out is None:
-            out = torch.empty_like(q)
-        if workspace is None:
-            need = attn_decode_workspace_size(cache, B, R, Hq, max_seq_len, window)
-            if need > 0:
-                workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
+    if out is None:
+        out = _made(torch.empty_like, q, stream)
+    if workspace is None:
+        need = attn_decode_workspace_size(cache, B, R, Hq, max_seq_len, window)
+        if need > 0:
+            workspace = _made(_zeroed, q, stream, need)
     c = cache.packed()
     rc = lib().attn_decode_append(
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), _ptr(rope_inv_freq),
         c, _ptr(seq_lens),
         _ptr(positions), B, R, int(max_seq_len), int(window), Hq, cache.n_kv_heads, D,
         float(scale), _ptr(out), _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(err),
+        0 if workspace is None else workspace.nbytes, _ptr(err),
         (ATTN_DECODE_TABLES_EARLY if tables_early else 0) |
         (ATTN_DECODE_CACHE_EARLY if cache_early else 0), _stream(stream))
     _check(rc, "attn_decode_append")
@@ -399,15 +397,15 @@ def attn_decode_sinks(q, cache: KVCache, seq_lens, positions, max_seq_len, windo
     least attn_decode_sinks_workspace_size bytes, zero-filled before its first
     use) is allocated if not given."""
     B, R, Hq, D = q.shape
-    with _allocate_on(stream):
-        if out is None:
-            out = torch.empty_like(q)
-        if workspace is None:
-            need = attn_decode_sinks_workspace_size(cache, B, R, Hq, max_seq_len, window, n_sinks)
-            if need > 0:
-                workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
-    _want("attn_decode_sinks", torch.bfloat16, q, out)
-    _want("attn_decode_sinks", torch.int32, seq_lens, positions)
+    if out is None:
+        out = _made(torch.empty_like, q, stream)
+    if workspace is None:
+        need = attn_decode_sinks_workspace_size(cache, B, R, Hq, max_seq_len, window, n_sinks)
+        if need > 0:
+            workspace = _made(_zeroed, q, stream, need)
+    device = _device()
+    _want("attn_decode_sinks", device, torch.bfloat16, q, out)
+    _want("attn_decode_sinks", device, torch.int32, seq_lens, positions)
     if seq_lens.shape[0] < B or positions.numel() < B * R:
         raise AttnError(ATTN_ERR_SHAPE, "attn_decode_sinks: seq_lens [B], positions [B * R]")
     c = cache.packed()
@@ -415,7 +413,7 @@ def attn_decode_sinks(q, cache: KVCache, seq_lens, positions, max_seq_len, windo
         _ptr(q), c, _ptr(seq_lens), _ptr(positions), B, R, int(max_seq_len),
         int(window), int(n_sinks), Hq, cache.n_kv_heads, D, float(scale), _ptr(out),
         _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(err),
+        0 if workspace is None else workspace.nbytes, _ptr(err),
         _stream(stream))
     _check(rc, "attn_decode_sinks")
     return out
@@ -425,10 +423,9 @@ def attn_prefill_sinks(q, k, v, window, n_sinks, scale, out=None, err=None, stre
     """attn_prefill under a sliding window whose first n_sinks tokens of each
     sequence stay visible.  Shapes as attn_prefill's."""
     B, T, Hq, D = q.shape
-    with _allocate_on(stream):
-        if out is None:
-            out = torch.empty_like(q)
-    _want("attn_prefill_sinks", torch.bfloat16, q, k, v, out)
+    if out is None:
+        out = _made(torch.empty_like, q, stream)
+    _want("attn_prefill_sinks", _device(), torch.bfloat16, q, k, v, out)
     if k.shape != v.shape or k.shape[:2] != q.shape[:2] or k.shape[3] != D:
         raise AttnError(ATTN_ERR_SHAPE, "attn_prefill_sinks: k and v are [B, T, Hkv, D]")
     rc = lib().attn_prefill_sinks(_ptr(q), _ptr(k), _ptr(v), B, T, int(window), int(n_sinks), Hq,
@@ -439,14 +436,14 @@ def attn_prefill_sinks(q, k, v, window, n_sinks, scale, out=None, err=None, stre
 
 
 def _want_rows(where, block_table, refs, rows, a, b):
-    _want(where, torch.int32, block_table, refs, rows, a, b)
+    _want(where, _device(), torch.int32, block_table, refs, rows, a, b)
     if block_table.dim() != 2 or not rows.shape == a.shape == b.shape:
         raise AttnError(ATTN_ERR_SHAPE, f"{where}: block_table is [rows, max_blocks], the row "
                                         "arguments are of one length")
 
 
 def _want_moves(where, moves, n_moves):
-    _want(where, torch.int32, moves, n_moves)
+    _want(where, _device(), torch.int32, moves, n_moves)
     if moves.dim() != 2 or moves.shape[1] != 3 or n_moves.numel() < 1:
         raise AttnError(ATTN_ERR_SHAPE, f"{where}: moves is [n, 3], n_moves [1]")
 
@@ -501,18 +498,16 @@ def attn_pages_compact(block_table, refs, block_size, moves, n_moves, used, work
     """Pages in use move to the lowest page ids: block_table and refs follow,
     used (int32 [1]) receives how many pages are in use, moves / n_moves the
     copies to carry out with attn_pages_copy."""
-    _want("attn_pages_compact", torch.int32, block_table, refs, used)
+    _want("attn_pages_compact", _device(), torch.int32, block_table, refs, used)
     _want_moves("attn_pages_compact", moves, n_moves)
     if block_table.dim() != 2 or used.numel() < 1:
         raise AttnError(ATTN_ERR_SHAPE, "attn_pages_compact: block_table is [rows, max_blocks]")
     if workspace is None:
-        with _allocate_on(stream):
-            workspace = torch.empty(attn_pages_workspace_size(refs.shape[0]), dtype=torch.uint8,
-                                    device=refs.device)
+        workspace = _made(_zeroed, refs, stream, attn_pages_workspace_size(refs.shape[0]))
     rc = lib().attn_pages_compact(_ptr(block_table), block_table.shape[1], block_table.shape[0],
                                   int(block_size), _ptr(refs), refs.shape[0], _ptr(moves),
                                   moves.shape[0], _ptr(n_moves), _ptr(used), _ptr(workspace),
-                                  workspace.numel() * workspace.element_size(), _ptr(err),
+                                  workspace.nbytes, _ptr(err),
                                   _stream(stream))
     _check(rc, "attn_pages_compact")
 
@@ -524,6 +519,13 @@ def attn_pages_copy(caches, moves, n_moves, err=None, stream=None):
         caches = [caches]
     _want_moves("attn_pages_copy", moves, n_moves)
     Hkv, D = (caches[0].n_kv_heads, caches[0].head_dim) if caches else (1, 128)
-    rc = lib().attn_pages_copy(b"".join([c.packed() for c in caches]), len(caches), Hkv, D, _ptr(moves), _ptr(n_moves),
+    # the fields that copying reads
+    packed = [_PACK(c.kind, c.k.data_ptr(), c.v.data_ptr(),
+                    c.k.shape[0] if c.layout == ATTN_LAYOUT_BSHD else c.num_slots, 0, 0,
+                    c.block_size, 0, c.dtype, 0, c.layout,
+                    0 if c.k_scale is None else c.k_scale.data_ptr(),
+                    0 if c.v_scale is None else c.v_scale.data_ptr(), c.scale_block)
+              for c in caches]
+    rc = lib().attn_pages_copy(b"".join(packed), len(caches), Hkv, D, _ptr(moves), _ptr(n_moves),
                                moves.shape[0], _ptr(err), _stream(stream))
     _check(rc, "attn_pages_copy")
