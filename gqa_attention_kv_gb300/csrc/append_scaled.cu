@@ -12,11 +12,24 @@
 // against 1.5 * 2^23 leaves the integer in the low bits).  Scales only grow
 // while a block fills, so a code is never clipped by a later row.
 //
-// One warp owns a (run of rows of one block, head, tensor): the maximum, the
-// block's earlier codes and the new codes are its own, so there is nothing to
-// synchronise and no order to depend on.  The kernel is a copy with arithmetic
-// (HBM-bound): a run of up to 16 rows of 128 (32 of 64) stays in registers
-// between its maximum and its codes, so each row is read once.
+// A copy with arithmetic: HBM is its floor.  The rows of a call that lie in one block
+// are a run; nothing is shared between the warps that write different runs, so there
+// is no order to depend on.  Two kernels, by the length of runs to expect:
+//   * runs by warps: a warp takes whole runs, reading its rows once where they fit its
+//     registers (16 rows of 128, 32 of 64).  Steps, and prompts in blocks of 16:
+//     14,449 rows of 4 x 128 in 10.9 us (4.1 TB/s; issue-bound: unpacking, scaling and
+//     packing 16-bit values), 64 single rows of 8 x 128 in 2.9 us.
+//   * runs by CTAs: 64 rows (128 for blocks of 128) of one tensor and head, 16 a warp,
+//     in registers; the rows' maxima meet in shared memory, each warp finds the ends of
+//     the runs that its rows belong to in the slots around them and encodes its own
+//     rows.  Rows of a run outside the CTA are read again for their maximum.  The warp
+//     with the run's first row stores the scale and, where it grew, recodes the
+//     block's slots that the run does not write; a warp elsewhere that reads the scale
+//     after it was stored comes to the same new scale.  Many rows in longer blocks:
+//     14,449 rows in blocks of 32 14.5 us (24.0 by warps), of 64 15.5 (36.0), of 128
+//     16.5 (57.0); in blocks of 16 it would take 14.5.
+// Rows of a block in another order than their slots', or with skipped rows beside
+// them, are an irregular run: written alone by the warp that has its first row.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -28,7 +41,9 @@ namespace gqa {
 namespace {
 
 constexpr float kScaleFloor = 5.421010862427522e-20f;  // 2^-64
-constexpr int kPasses = 8;                             // row groups held in registers
+constexpr int kPasses = 8;   // row groups that a warp of the runs kernel holds in registers
+constexpr int kMaxWindow = 16, kMaxBlock = 128;
+constexpr int64_t kNone = INT64_MIN, kBad = -1;        // rows outside the call; slots outside the cache
 
 struct ScaledParams {
     const uint4 *k_new, *v_new;
@@ -39,7 +54,7 @@ struct ScaledParams {
     float *ks, *vs;
     int64_t num_slots;
     int shift;  // log2 of the slots of a block
-    int window;  // rows a warp looks for run starts in
+    int window;  // rows of a warp (runs kernel)
     KvPlace place;
     int32_t *err;
 };
@@ -60,7 +75,14 @@ __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
     return d;
 }
 
-// Codes of four values.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// Codes of four values.  CLAMP false: |x r| <= 127 (1 + 2^-22), as finite rows have
+// under a scale of their own maximum.
 template <bool INT8, bool CLAMP = true>
 __device__ __forceinline__ uint32_t encode4(const float *x, float r) {
     if constexpr (INT8) {
@@ -91,11 +113,43 @@ __device__ __forceinline__ void decode4(uint32_t w, float *x) {
     }
 }
 
+// The codes of a block's slots, times `by`, but for slots lo .. hi - 1.
 template <bool INT8, int HD>
-__global__ void __launch_bounds__(128, 6) kv_append_scaled_kernel(const ScaledParams p) {
+__device__ __forceinline__ void recode(const ScaledParams &p, uint8_t *cache, int h, int64_t block,
+                                       float by, int64_t lo, int64_t hi) {
+    constexpr int kL = HD / 16, kR = 32 / kL;  // 16 codes a lane
+    const int lane = threadIdx.x & 31;
+    for (int s0 = 0; s0 < (1 << p.shift); s0 += kR) {
+        const int64_t s = (block << p.shift) + s0 + lane / kL;
+        if (s0 + lane / kL >= (1 << p.shift) || (s >= lo && s < hi)) continue;
+        uint4 *c = reinterpret_cast<uint4 *>(cache + p.place.head_offset(s, h) +
+                                             (lane & (kL - 1)) * 16);
+        uint4 w = *c;
+        uint32_t *u = &w.x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float f[4];
+            decode4<INT8>(u[e], f);
+            u[e] = encode4<INT8>(f, by);
+        }
+        *c = w;
+    }
+    __syncwarp();
+}
+
+// s' from the scale held (0 where the block starts anew) and the rows' maximum.
+template <bool INT8>
+__device__ __forceinline__ float new_scale(float held, float amax) {
+    return fmaxf(fmaxf(held, __fdiv_rn(amax, INT8 ? 127.f : 448.f)), kScaleFloor);
+}
+
+// Runs by warps: a warp takes the runs that start among its rows (one to sixteen),
+// whatever their length, alone.  A run that ends among these rows stays in registers
+// between its maximum and its codes.
+template <bool INT8, int HD>
+__global__ void __launch_bounds__(128, 6) kv_append_runs_kernel(const ScaledParams p) {
     constexpr int kLanes = HD / 8;           // lanes of a row: 16 bytes of bf16, 8 codes each
     constexpr int kRows = 32 / kLanes;       // rows of a pass
-    constexpr float kQMax = INT8 ? 127.f : 448.f;
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
@@ -246,29 +300,11 @@ __global__ void __launch_bounds__(128, 6) kv_append_scaled_kernel(const ScaledPa
         }
         const int64_t at = block * heads + h;
         const float held = fresh ? 0.f : fmaxf(__shfl_sync(0xffffffffu, my_scale, at_lane), 0.f);
-        const float now = fmaxf(fmaxf(held, __fdiv_rn(amax, kQMax)), kScaleFloor);
+        const float now = new_scale<INT8>(held, amax);
         const float r = __frcp_rn(now);
-        if (!fresh && held > 0.f && now > held) {
-            // the block's earlier codes under the new scale (the run's rows among them:
-            // they are written below)
-            const float by = __fmul_rn(held, r);
-            constexpr int kL = HD / 16, kR = 32 / kL;  // 16 codes a lane
-            for (int s0 = 0; s0 < (1 << p.shift); s0 += kR) {
-                const int s = s0 + lane / kL;
-                if (s >= (1 << p.shift)) continue;
-                uint4 *c = reinterpret_cast<uint4 *>(
-                    cache + p.place.head_offset((block << p.shift) + s, h) + (lane & (kL - 1)) * 16);
-                uint4 w = *c;
-                uint32_t *u = &w.x;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float f[4];
-                    decode4<INT8>(u[e], f);
-                    u[e] = encode4<INT8>(f, by);
-                }
-                *c = w;
-            }
-        }
+        // the block's earlier codes (the run's rows among them are written below)
+        if (held > 0.f && now > held)
+            recode<INT8, HD>(p, cache, h, block, __fmul_rn(held, r), 0, 0);
         __syncwarp();
         if (lane == 0) scales[at] = now;
         if (INT8 && __any_sync(0xffffffffu, nan)) {
@@ -316,6 +352,257 @@ __global__ void __launch_bounds__(128, 6) kv_append_scaled_kernel(const ScaledPa
     }
 }
 
+// Runs by CTAs: for long runs.  See the head of this file.
+template <bool INT8, int HD, int W>
+__global__ void __launch_bounds__(W * 32, 24 / W)
+    kv_append_blocks_kernel(const __grid_constant__ ScaledParams p) {
+    constexpr int kLanes = HD / 8;                // lanes of a row: 16 bytes of bf16, 8 codes each
+    constexpr int kRows = 32 / kLanes;            // rows of a pass
+    constexpr int kPasses = kMaxWindow / kRows;   // of a warp's 16 rows
+    __shared__ int64_t sm_slot[2 * kMaxBlock + W * kMaxWindow];
+    __shared__ float sm_max[W * kMaxWindow];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int heads = p.place.n_kv_heads, sb = 1 << p.shift;
+    const int64_t group = blockIdx.x / (2 * heads);
+    const int rem = (int)(blockIdx.x - group * (2 * heads)), tensor = rem / heads;
+    const int h = rem - tensor * heads;
+    const int cta_rows = W * kMaxWindow;
+    const int64_t row0 = group * cta_rows;        // of the CTA
+    const int w0 = warp * kMaxWindow;               // this warp's first row, in the CTA's
+    const int n_cta = (int)min((int64_t)cta_rows, p.n - row0);
+    const uint4 *src = tensor == 0 ? p.k_new : p.v_new;
+    uint8_t *cache = tensor == 0 ? p.k : p.v;
+    float *scales = tensor == 0 ? p.ks : p.vs;
+    const int my_r = lane / kLanes, piece = lane & (kLanes - 1);
+    const float *ref = tensor == 0 && p.k_ref != nullptr ? p.k_ref + h * HD + piece * 8 : nullptr;
+
+    // ---- this warp's rows, and the slots of the CTA's rows and a block's length around
+    uint4 x[kPasses];
+#pragma unroll
+    for (int u = 0; u < kPasses; ++u) {
+        const int r = w0 + my_r + u * kRows;
+        x[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (my_r + u * kRows < kMaxWindow && r < n_cta)
+            x[u] = __ldg(src + ((row0 + r) * heads + h) * kLanes + piece);
+    }
+    for (int i = threadIdx.x; i < cta_rows + 2 * sb; i += W * 32) {
+        const int64_t row = row0 - sb + i;
+        int64_t s = row >= 0 && row < p.n ? __ldg(p.slots + row) : kNone;
+        if (s != kNone && (s < 0 || s >= p.num_slots)) {
+            s = kBad;
+            if (rem == 0 && i >= sb && i < sb + cta_rows) report_error(p.err, ATTN_ERR_BOUNDS);
+        }
+        sm_slot[i] = s;
+    }
+    __syncthreads();
+    auto slot = [&](int r) { return sm_slot[sb + r]; };  // of the CTA's row r, -sb <= r < rows + sb
+
+    // ---- the rows' maxima, and the scales of their blocks
+    const int64_t my_slot = lane < kMaxWindow && w0 + lane < n_cta ? slot(w0 + lane) : kNone;
+    const float my_scale = my_slot >= 0 ? scales[(my_slot >> p.shift) * heads + h] : 0.f;
+    auto values = [&](const uint4 &w, float *f) {  // the eight values of a lane's piece
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            f[2 * e] = __uint_as_float(u[e] << 16);
+            f[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+        }
+        if (ref != nullptr)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = __fsub_rn(f[e], __ldg(ref + e));
+    };
+    // the largest magnitude of a row, NaN if it holds one, in all of the row's lanes
+    auto row_max = [&](const uint4 &w) {
+        float m;
+        if (ref == nullptr) {
+            uint32_t a = max_nan_bf16x2(max_nan_bf16x2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                        max_nan_bf16x2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1)
+                a = max_nan_bf16x2(a, __shfl_xor_sync(0xffffffffu, a, o));
+            m = max_nan(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
+        } else {
+            float f[8];
+            values(w, f);
+            m = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(f[e]));
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1)
+                m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        }
+        return m;
+    };
+#pragma unroll
+    for (int u = 0; u < kPasses; ++u) {
+        const float m = row_max(x[u]);
+        if (piece == 0 && my_r + u * kRows < kMaxWindow) sm_max[w0 + my_r + u * kRows] = m;
+    }
+    __syncthreads();
+
+    // ---- this warp's pieces: rows in consecutive slots of one block
+    const int64_t before = lane >= 1 && lane < kMaxWindow ? slot(w0 + lane - 1) : kNone;
+    uint32_t starts = __ballot_sync(0xffffffffu, my_slot >= 0 &&
+                                                     (my_slot != before + 1 || before < 0 ||
+                                                      (my_slot & (sb - 1)) == 0));
+    const uint32_t good = __ballot_sync(0xffffffffu, my_slot >= 0);
+    while (starts != 0) {
+        const int a = __ffs(starts) - 1;  // the piece: rows w0 + a .. w0 + b - 1
+        starts &= starts - 1;
+        const uint32_t ends = (starts | ~good) & (0xffffffffu << a);
+        const int b = ends == 0 ? 32 : __ffs(ends) - 1;
+        const int64_t s_a = slot(w0 + a), block = s_a >> p.shift;
+        const int off = (int)(s_a & (sb - 1));
+        // rows before and behind it in the consecutive slots of the block
+        int r0 = w0 + a, r1 = w0 + b;
+        for (int j0 = 0; j0 < off; j0 += 32) {
+            const int j = j0 + lane + 1;
+            const uint32_t no = __ballot_sync(0xffffffffu, j > off || slot(w0 + a - j) != s_a - j);
+            const int run = no == 0 ? 32 : __ffs(no) - 1;
+            r0 -= run;
+            if (run < 32) break;
+        }
+        const int room = sb - off - (b - a);  // slots of the block behind the piece
+        for (int j0 = 0; j0 < room; j0 += 32) {
+            const int j = j0 + lane;
+            const uint32_t no = __ballot_sync(
+                0xffffffffu, j >= room || slot(w0 + b + j) != s_a + (b - a) + j);
+            const int run = no == 0 ? 32 : __ffs(no) - 1;
+            r1 += run;
+            if (run < 32) break;
+        }
+        // regular: no other row of the block beside it, nor a row without a slot
+        auto apart = [&](int r) {
+            const int64_t s = slot(r);
+            return s == kNone || (s >= 0 && (s >> p.shift) != block);
+        };
+        if (apart(r0 - 1) && apart(r1)) {
+            const int64_t first = s_a - (w0 + a - r0);  // slot of the run's first row
+            const bool fresh = (first & (sb - 1)) == 0;
+            float amax = 0.f;
+            for (int r = max(r0, 0) + lane; r < min(r1, n_cta); r += 32)
+                amax = max_nan(amax, sm_max[r]);
+            auto other = [&](int lo, int hi) {  // rows of the run that the CTA does not have
+#pragma unroll 4
+                for (int r = lo; r < hi; r += kRows) {
+                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                    if (r + my_r < hi)
+                        w = __ldg(src + ((row0 + r + my_r) * heads + h) * kLanes + piece);
+                    else if (ref != nullptr)  // (its distance from the reference is no maximum)
+                        w = __ldg(src + ((row0 + lo) * heads + h) * kLanes + piece);
+                    amax = max_nan(amax, row_max(w));
+                }
+            };
+            other(r0, min(0, r1));
+            other(max(n_cta, r0), r1);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const bool finite = amax < INFINITY;
+            bool nan = false;
+            if (!finite) {  // again, without the elements that are not
+                amax = 0.f;
+                for (int r = r0 + my_r; r < r1; r += kRows) {
+                    float f[8];
+                    values(__ldg(src + ((row0 + r) * heads + h) * kLanes + piece), f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float m = fabsf(f[e]);
+                        nan |= m != m;
+                        amax = fmaxf(amax, m < INFINITY ? m : 0.f);
+                    }
+                }
+                __syncwarp();
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                if (INT8 && nan) report_error(p.err, ATTN_ERR_UNSUPPORTED);  // INT8 has no NaN: 0
+            }
+            const float held = fresh ? 0.f : fmaxf(__shfl_sync(0xffffffffu, my_scale, a), 0.f);
+            const float now = new_scale<INT8>(held, amax), r = __frcp_rn(now);
+            if (r0 == w0 + a) {  // the run's first row is this warp's
+                if (held > 0.f && now > held)
+                    recode<INT8, HD>(p, cache, h, block, __fmul_rn(held, r), first,
+                                     first + (r1 - r0));
+                if (lane == 0) scales[block * heads + h] = now;
+            }
+            const int64_t row_bytes = (int64_t)p.place.head_bytes * (p.place.rows == 0 ? heads : 1);
+            uint8_t *dst = cache + p.place.head_offset(s_a, h) + (my_r - a) * row_bytes + piece * 8;
+#pragma unroll
+            for (int u = 0; u < kPasses; ++u, dst += kRows * row_bytes) {
+                if (my_r + u * kRows < a || my_r + u * kRows >= b) continue;
+                float f[8];
+                values(x[u], f);
+                uint2 c;
+                if (finite) {
+                    c = make_uint2(encode4<INT8, false>(f, r), encode4<INT8, false>(f + 4, r));
+                } else {
+                    if (INT8)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] = f[e] == f[e] ? f[e] : 0.f;
+                    c = make_uint2(encode4<INT8, true>(f, r), encode4<INT8, true>(f + 4, r));
+                }
+                *reinterpret_cast<uint2 *>(dst) = c;
+            }
+            __syncwarp();
+            continue;
+        }
+        // ---- an irregular run: written by the warp that has its first row
+        int64_t i = row0 + w0 + a - 1;
+        int64_t s = kNone;
+        while (i >= 0 && ((s = __ldg(p.slots + i)) < 0 || s >= p.num_slots)) --i;
+        if (i >= 0 && (s >> p.shift) == block) continue;  // its first row is another
+        const int64_t i0 = row0 + w0 + a;
+        auto in_block = [&](int64_t t) { return t >= 0 && t < p.num_slots && (t >> p.shift) == block; };
+        int64_t i1 = i0;
+        for (;; ++i1) {
+            s = i1 < p.n ? __ldg(p.slots + i1) : kNone;
+            if (s == kNone || (s >= 0 && s < p.num_slots && (s >> p.shift) != block)) break;
+        }
+        float amax = 0.f;
+        bool fresh = false, nan = false;
+        for (int64_t r = i0 + my_r; r < i1; r += kRows) {
+            s = __ldg(p.slots + r);
+            if (!in_block(s)) continue;
+            fresh |= (s & (sb - 1)) == 0;
+            float f[8];
+            values(__ldg(src + (r * heads + h) * kLanes + piece), f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float m = fabsf(f[e]);
+                nan |= m != m;
+                amax = fmaxf(amax, m < INFINITY ? m : 0.f);
+            }
+        }
+        __syncwarp();
+        fresh = __any_sync(0xffffffffu, fresh);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const float held = fresh ? 0.f : fmaxf(__shfl_sync(0xffffffffu, my_scale, a), 0.f);
+        const float now = new_scale<INT8>(held, amax), r = __frcp_rn(now);
+        // all of the block's slots: the run's are written afterwards
+        if (held > 0.f && now > held)
+            recode<INT8, HD>(p, cache, h, block, __fmul_rn(held, r), 0, 0);
+        if (INT8 && nan) report_error(p.err, ATTN_ERR_UNSUPPORTED);
+        __syncwarp();
+        if (lane == 0) scales[block * heads + h] = now;
+        for (int64_t t = i0 + my_r; t < i1; t += kRows) {
+            s = __ldg(p.slots + t);
+            if (!in_block(s)) continue;
+            float f[8];
+            values(__ldg(src + (t * heads + h) * kLanes + piece), f);
+            if (INT8)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = f[e] == f[e] ? f[e] : 0.f;
+            *reinterpret_cast<uint2 *>(cache + p.place.head_offset(s, h) + piece * 8) =
+                make_uint2(encode4<INT8, true>(f, r), encode4<INT8, true>(f + 4, r));
+        }
+        __syncwarp();
+    }
+}
+
 }  // namespace
 
 int launch_kv_append_scaled(const void *k_new, const void *v_new, const int64_t *slot_mapping,
@@ -336,28 +623,41 @@ int launch_kv_append_scaled(const void *k_new, const void *v_new, const int64_t 
     while ((1 << p.shift) < cache->scale_block) ++p.shift;
     p.place = kv_place(cache, n_kv_heads, head_dim, 1);
     p.err = err;
-    // A step's rows mostly start runs of their own: a warp each.  A prompt's are runs
-    // of whole blocks: a warp takes the starts among 16 rows.  Which of the two a call
-    // is shows in n alone, so a warp takes the fewest rows with which the warps are no
-    // more than 64 an SM.
     const int64_t per_row = 2ll * n_kv_heads;
-    p.window = 1;
-    while (p.window < 16 && (n + p.window - 1) / p.window * per_row > (int64_t)device_sm_count() * 64)
-        p.window *= 2;
-    const int64_t warps = (n + p.window - 1) / p.window * per_row;
-    const int64_t blocks = (warps + 3) / 4;
-    if (blocks >= (int64_t(1) << 31)) return ATTN_ERR_SHAPE;
-    const dim3 grid((unsigned)blocks), threads(128);
-    cudaError_t e;
-    if (cache->dtype == ATTN_KV_INT8_SCALED)
-        e = head_dim == 128
-                ? launch_pdl(kv_append_scaled_kernel<true, 128>, grid, threads, 0, stream, p)
-                : launch_pdl(kv_append_scaled_kernel<true, 64>, grid, threads, 0, stream, p);
-    else
-        e = head_dim == 128
-                ? launch_pdl(kv_append_scaled_kernel<false, 128>, grid, threads, 0, stream, p)
-                : launch_pdl(kv_append_scaled_kernel<false, 64>, grid, threads, 0, stream, p);
-    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    const bool int8 = cache->dtype == ATTN_KV_INT8_SCALED;
+    auto run = [&](auto kernel, int64_t blocks, int threads) {
+        if (blocks >= (int64_t(1) << 31)) return (int)ATTN_ERR_SHAPE;
+        return launch_pdl(kernel, dim3((unsigned)blocks), dim3(threads), 0, stream, p) == cudaSuccess
+                   ? (int)ATTN_OK
+                   : (int)ATTN_ERR_CUDA;
+    };
+    // A step's rows mostly are runs of their own, taken one after another: a row a warp
+    // is best.  A prompt's are runs of whole blocks.  Which of the two a call is shows
+    // in n alone: what a row a warp would need more warps for than the GPU holds at once
+    // (64 an SM) is taken for a prompt, in blocks of 16 by warps of 16 rows, in longer
+    // ones by CTAs.  8 x 128 in blocks of 16: a prompt of 1,024 rows takes 3.7 us by warps
+    // of 16 and 10.4 by warps of two, single rows of 1,024 requests 19.1 and 12.9; of
+    // 512, a row a warp, a prompt takes 9.4 (3.2 by warps of 16), single rows 8.8 (17.5).
+    const bool many = n * per_row > (int64_t)device_sm_count() * 64;
+    if (many && cache->scale_block > 16) {
+        const int w = cache->scale_block > 64 ? 8 : 4;
+        const int64_t blocks = (n + w * kMaxWindow - 1) / (w * kMaxWindow) * per_row;
+        if (head_dim == 128)
+            return w == 4 ? run(int8 ? kv_append_blocks_kernel<true, 128, 4>
+                                     : kv_append_blocks_kernel<false, 128, 4>, blocks, 128)
+                          : run(int8 ? kv_append_blocks_kernel<true, 128, 8>
+                                     : kv_append_blocks_kernel<false, 128, 8>, blocks, 256);
+        return w == 4 ? run(int8 ? kv_append_blocks_kernel<true, 64, 4>
+                                 : kv_append_blocks_kernel<false, 64, 4>, blocks, 128)
+                      : run(int8 ? kv_append_blocks_kernel<true, 64, 8>
+                                 : kv_append_blocks_kernel<false, 64, 8>, blocks, 256);
+    }
+    p.window = many ? kMaxWindow : 1;
+    const int64_t blocks = ((n + p.window - 1) / p.window * per_row + 3) / 4;
+    return head_dim == 128 ? run(int8 ? kv_append_runs_kernel<true, 128>
+                                      : kv_append_runs_kernel<false, 128>, blocks, 128)
+                           : run(int8 ? kv_append_runs_kernel<true, 64>
+                                      : kv_append_runs_kernel<false, 64>, blocks, 128);
 }
 
 }  // namespace gqa

@@ -310,6 +310,47 @@ def test_fused_step_is_append_then_decode(fmt):
     assert int(err) == 0 and torch.equal(out, want)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("D,H,sb,head_major,ref_vector", [
+    (128, 4, 32, False, False), (64, 5, 64, True, False), (64, 4, 128, False, True),
+    (128, 4, 64, False, True), (128, 5, 128, True, False)])
+def test_append_many_rows_of_long_blocks(fmt, D, H, sb, head_major, ref_vector):
+    """Prompts of several requests that begin and end inside blocks whose earlier rows
+    are there already, smaller and larger ones; then the same rows in disorder, with
+    skipped rows among them and values that are not finite."""
+    g = gen(D + H + sb)
+    per = 7 * sb
+    B = 9
+    k_ref = torch.randn(H, D, generator=g) if ref_vector else None
+    case = Case(fmt, B * per, H, D, sb, per=per, head_major=head_major, k_ref=k_ref).fill(g)
+    case.cuda()
+    slots = []
+    for b in range(B):
+        lo = int(torch.randint(0, 2 * sb, (1,), generator=g))
+        hi = int(torch.randint(5 * sb, per + 1, (1,), generator=g))
+        slots += range(b * per + lo, b * per + hi)
+    k, v = new_rows(g, len(slots), H, D)
+    grow = torch.exp(torch.randn(len(slots), 1, 1, generator=g) * 3)
+    k, v = (k * grow).bfloat16(), (v * grow).bfloat16()
+    at = torch.tensor(slots)
+    case.append(k, v, at)
+    assert gpu_append(case, k, v, at) == 0
+    case.check()
+    # rows of a block stay together, every third block in disorder
+    order = torch.arange(len(slots))
+    ends = [0] + [i for i in range(1, len(slots)) if slots[i] // sb != slots[i - 1] // sb]
+    for a, b in list(zip(ends, ends[1:]))[::3]:
+        order[a:b] = order[a:b][torch.randperm(b - a, generator=g)]
+    at = at[order]
+    at[ends[4] + 2] = -5
+    at[ends[8]] = B * per + 1
+    k, v = new_rows(g, len(slots), H, D, 2.0)
+    v[ends[6] + 1, 0, 3], v[ends[5] + 3, 1, 2] = float("inf"), float("-inf")
+    case.append(k, v, at)
+    assert gpu_append(case, k, v, at) == gq.ATTN_ERR_BOUNDS
+    case.check()
+
+
 @pytest.mark.parametrize("B,H,lo,hi", [(40, 2, 1, 20000),   # one long request among short ones
                                        (1, 1, 30000, 30000)])  # one unit over the whole GPU
 def test_decode_in_very_many_parts(B, H, lo, hi):
@@ -334,7 +375,7 @@ def test_decode_in_very_many_parts(B, H, lo, hi):
 
 @pytest.mark.parametrize("n", [100, 700, 1500, 3500])
 def test_append_steps_of_many_requests(n):
-    """One row a request, from a warp a row to a warp for the runs of several."""
+    """One row a request, a warp for each or for sixteen."""
     g = gen(n)
     case = Case("e4m3", n * 16, 4, 64, 16).fill(g)
     case.cuda()
