@@ -251,7 +251,8 @@ class KVCache:
 def attn_kv_append(k_new, v_new, slot_mapping, cache: KVCache, err=None, stream=None):
     """cache.k[slot_mapping[i]] = k_new[i] (same for v); slot_mapping int64 [n]."""
     shape = cache.k.shape
-    rc = lib().attn_kv_append(_ptr(k_new), _ptr(v_new), _ptr(slot_mapping), slot_mapping.shape[0], cache.packed(), shape[1], shape[-1],
+    rc = lib().attn_kv_append(_ptr(k_new), _ptr(v_new), _ptr(slot_mapping),
+                              slot_mapping.shape[0], cache.packed(), shape[1], shape[-1],
                               _ptr(err), _stream(stream))
     _check(rc, "attn_kv_append")
 
@@ -518,14 +519,18 @@ def attn_pages_copy(caches, moves, n_moves, err=None, stream=None):
     if isinstance(caches, KVCache):
         caches = [caches]
     _want_moves("attn_pages_copy", moves, n_moves)
-    Hkv, D = (caches[0].n_kv_heads, caches[0].head_dim) if caches else (1, 128)
-    # the fields that copying reads
-    packed = [_PACK(c.kind, c.k.data_ptr(), c.v.data_ptr(),
-                    c.k.shape[0] if c.layout == ATTN_LAYOUT_BSHD else c.num_slots, 0, 0,
-                    c.block_size, 0, c.dtype, 0, c.layout,
-                    0 if c.k_scale is None else c.k_scale.data_ptr(),
-                    0 if c.v_scale is None else c.v_scale.data_ptr(), c.scale_block)
-              for c in caches]
-    rc = lib().attn_pages_copy(b"".join(packed), len(caches), Hkv, D, _ptr(moves), _ptr(n_moves),
+    Hkv, D, slots, shape = 1, 128, 0, None
+    if caches:
+        first = caches[0]
+        Hkv, D, slots, shape = first.n_kv_heads, first.head_dim, first.num_slots, first.k.shape
+    packed = []
+    for c in caches:
+        if c.k.shape != shape:
+            raise AttnError(ATTN_ERR_SHAPE, "attn_pages_copy: caches of different shapes")
+        packed.append(_PACK(c.kind, c.k.data_ptr(), c.v.data_ptr(), slots, 0, 0,  # what copying reads
+                            c.block_size, 0, c.dtype, 0, c.layout,
+                            0 if c.k_scale is None else c.k_scale.data_ptr(),
+                            0 if c.v_scale is None else c.v_scale.data_ptr(), c.scale_block))
+    rc = lib().attn_pages_copy(b"".join(packed), len(packed), Hkv, D, _ptr(moves), _ptr(n_moves),
                                moves.shape[0], _ptr(err), _stream(stream))
     _check(rc, "attn_pages_copy")

@@ -8,7 +8,7 @@
 // With a scaled cache k_t = ks c_t, v_t = vs c'_t, the codes c being E4M3 or
 // INT8 and ks, vs the scales of t's block.  Both scales leave the matrix
 // products: scores are ks (q . c), and with x_t = scale ks (q . c) log2(e) and
-// lv = log2(vs), the weights that meet the codes are
+// lv = log2(vs), the weights that meet the codes are (but for a constant factor)
 //     w_t = 2^(x_t + lv_t - M),  O = sum w_t c'_t,  l = sum w_t / vs_t,
 // out = O / l.  M follows the maximum of x + lv, so w (rounded once to f16)
 // stays in f16's range whatever the scales are, and l is a 32-bit sum.
@@ -80,6 +80,9 @@ constexpr int kMinChunks = 4;
 // 22.5 against 16.4 us.
 constexpr int kKernelParts = 24;
 constexpr float kRescaleLog2 = 8.0f;  // the reference maximum moves past this only (w <= 2^8)
+// f16 weights are held times 2^7, 2^15 at most: those above 2^-21 of the largest keep
+// f16's 11 bits (2^-14 without), however small the largest's own value is
+constexpr float kWeightLog2 = 7.0f;
 constexpr float kScaleFloor = 5.421010862427522e-20f;  // 2^-64, the smallest scale
 
 enum Fmt { kBF16 = 0, kE4M3 = 1, kINT8 = 2 };
@@ -185,15 +188,6 @@ __device__ __forceinline__ void copies_wait() {
 // Four 8-bit codes -> two f16x2 words (bytes 0, 1 and bytes 2, 3); exact.
 // INT8: a byte with its sign bit flipped is c + 128; behind the byte 0x64 it is
 // the f16 1024 + (c + 128), from which 1152 is subtracted without rounding.
-// Four codes of a key -> two f16x2 words for Q K^T.  INT8: a byte with its sign
-// bit flipped, c + 128, is the f16 (c + 128) 2^-24, a subnormal the tensor
-// cores take exactly; the accumulators start at -128 2^-24 sum(q), so a score
-// comes out as 2^-24 q . c.  (V keeps the subtraction: there the offset would
-// be carried through every key's addition to O.)
-template <int FMT>
-__device__ __forceinline__ void key_codes_to_f16(uint32_t x, uint32_t &lo, uint32_t &hi);
-constexpr uint32_t kMinus128 = 0x80808080u;  // f16x2 of -128 2^-24
-
 template <int FMT>
 __device__ __forceinline__ void codes_to_f16(uint32_t x, uint32_t &lo, uint32_t &hi) {
     if constexpr (FMT == kE4M3) {
@@ -210,6 +204,13 @@ __device__ __forceinline__ void codes_to_f16(uint32_t x, uint32_t &lo, uint32_t 
         asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(bias));
     }
 }
+
+// Four codes of a key -> two f16x2 words for Q K^T.  INT8: a byte with its sign
+// bit flipped, c + 128, is the f16 (c + 128) 2^-24, a subnormal the tensor
+// cores take exactly; the accumulators start at -128 2^-24 sum(q), so a score
+// comes out as 2^-24 q . c.  (V keeps the subtraction: there the offset would
+// be carried through every key's addition to O.)
+constexpr uint32_t kMinus128 = 0x80808080u;  // f16x2 of -128 2^-24
 
 template <int FMT>
 __device__ __forceinline__ void key_codes_to_f16(uint32_t x, uint32_t &lo, uint32_t &hi) {
@@ -853,13 +854,14 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
                 const float m_old = m_run[r];
                 const float m_new = mx > m_old + kRescaleLog2 ? mx : m_old;
                 const float m_use = m_new == -INFINITY ? 0.f : m_new;
+                const float m_w = FMT == kBF16 ? m_use : m_use - kWeightLog2;
                 alpha[r] = m_new == m_old ? 1.f : fast_exp2(m_old - m_use);
                 moved |= m_new != m_old;
                 m_run[r] = m_new;
                 l_run[r] *= alpha[r];
 #pragma unroll
                 for (int i = 0; i < NSUB; ++i) {
-                    const float shift = lv[i] - m_use;
+                    const float shift = lv[i] - m_w;
                     float sum = 0.f;
 #pragma unroll
                     for (int j = 0; j < NJ; ++j)

@@ -466,17 +466,17 @@ int launch_pages_copy(const attn_kv_cache *caches, int n_caches, int n_kv_heads,
                       cudaStream_t stream) {
     if (max_moves == 0) return ATTN_OK;
     const attn_kv_cache &c0 = caches[0];
-    const int row_bytes = head_dim * (c0.dtype == ATTN_KV_BF16 ? 2 : 1);
+    const int64_t row_bytes = head_dim * (c0.dtype == ATTN_KV_BF16 ? 2 : 1);
     CopyParams p = {};
     p.moves = moves;
     p.n_moves = n_moves;
     p.max_moves = max_moves;
     p.num_pages = (int)(c0.num_slots / c0.block_size);
     p.block_size = c0.block_size;
-    p.page_pieces = c0.block_size * n_kv_heads * row_bytes / 16;
+    p.page_pieces = (int)(c0.block_size * row_bytes * n_kv_heads / 16);
     const bool head_major = c0.layout == ATTN_LAYOUT_BHSD;
-    p.run_pieces = head_major ? c0.block_size * row_bytes / 16 : p.page_pieces;
-    p.row_pieces = (head_major ? 1 : n_kv_heads) * row_bytes / 16;
+    p.run_pieces = head_major ? (int)(c0.block_size * row_bytes / 16) : p.page_pieces;
+    p.row_pieces = (int)((head_major ? 1 : n_kv_heads) * row_bytes / 16);
     p.scale_block = kv_scaled(c0.dtype) ? c0.scale_block : c0.block_size;
     p.n_kv_heads = n_kv_heads;
     constexpr int kStep = kCopyThreads * kCopyUnroll;

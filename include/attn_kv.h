@@ -298,10 +298,10 @@ int attn_decode_kernel_launches(const attn_kv_cache *cache, int batch, int q_row
  *   and accumulates in fp32.
  *   A scaled cache is read as stored too: codes convert to f16 exactly, q is
  *   taken in f16 (a magnitude of 65520 or more is reported as
- *   ATTN_ERR_UNSUPPORTED; magnitudes under 2^-14 lose precision), the scales multiply scores and softmax weights in
- *   float32, and the weights are rounded once to f16.  A scale is finite and at
- *   least 2^-64 (one below reads as 2^-64).  Its workspace
- *   is like any other's (zero-filled before its first use).
+ *   ATTN_ERR_UNSUPPORTED; magnitudes under 2^-14 lose precision), the scales
+ *   multiply scores and softmax weights in float32, and the weights are rounded
+ *   once to f16.  A scale is finite and at least 2^-64 (one below reads as
+ *   2^-64).  Its workspace is like any other's (zero-filled before its first use).
  *   A group of 64 or more query rows (q_rows x n_q_heads / n_kv_heads) over a
  *   linear slot-major bf16 cache is a prefill chunk and computes as
  *   attn_prefill does: P V from f16 softmax weights and f16 values, with the
@@ -523,8 +523,9 @@ int attn_prefill_sinks(const void *q, const void *k, const void *v, int batch, i
  *   in use at or above U (ascending) moves to the i-th free page below U: refs
  *   and every entry of the table follow, and the moves copy whole pages.  refs
  *   has to count this table's entries and no others.
- *   max_moves >= the pages that move (at most num_pages / 2): past it no page
- *   moves, and ATTN_ERR_WORKSPACE is stored in *err_word.  A source page's
+ *   max_moves >= the pages that move (at most num_pages / 2): with fewer only
+ *   the first max_moves of them move, table and refs agree with that, and
+ *   ATTN_ERR_WORKSPACE is stored in *err_word.  A source page's
  *   rows stay readable until its new owner writes them.
  *   workspace: attn_pages_workspace_size(num_pages) bytes, no zeroing.
  * attn_pages_copy     carries the moves out in n_caches caches (K, V and, for

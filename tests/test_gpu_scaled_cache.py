@@ -1,5 +1,7 @@
 """Caches of 8-bit codes with a scale per block of tokens and head: append bit
 for bit against the definition, decode against the values the cache holds."""
+import math
+
 import pytest
 import torch
 
@@ -251,6 +253,36 @@ def test_decode_scales_far_apart(fmt):
             case.k[b * 176 + int(lens[b]):(b + 1) * 176] = 0x7F
             case.v[b * 176 + int(lens[b]):(b + 1) * 176] = 0x7F
     got = gq.attn_decode(q.to(DEV), case.cuda(), lens.to(DEV), pos.to(DEV), 170, 0, 0.1)
+    ref.check_output(got, want, mass)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("group", [1, 12])
+def test_decode_small_weights_beside_zeros(fmt, group):
+    """Key j's weight is 2^(-j / 2) of the first key's and its value stands alone in
+    dim j, where all other keys have zeros: each weight shows by itself.  Weights
+    down to 2^-20 of the largest keep the precision of one rounding to 11 bits."""
+    n, D = 41, 128
+    case = Case(fmt, 64, 1, D, 16)
+    step = 0.5 * math.log(2.0)
+    for j in range(n):
+        case.k[j, 0, 0] = -j if fmt == "int8" else 0
+        case.v[j, 0, j] = 96 if fmt == "int8" else ref.encode(
+            "e4m3", torch.tensor(96.0).double(), torch.tensor(1.0).double())
+    if fmt == "e4m3":  # -j as the sum of two codes
+        j = torch.arange(n).double()
+        for d, x in ((0, -(j // 8) * 8), (1, -(j % 8))):
+            case.k[:n, 0, d] = ref.encode("e4m3", x, torch.tensor(1.0).double())
+    case.ks.fill_(1.0)
+    case.vs.copy_(torch.tensor([[1.0], [0.25], [3.0], [1.0]]))
+    q = torch.zeros(1, 1, group, D)
+    q[..., :2] = 1.0
+    q = q.bfloat16()
+    lens, pos = torch.tensor([n], dtype=torch.int32), torch.tensor([n - 1], dtype=torch.int32)
+    want, mass = ref.decode(q, ref.dequantized(fmt, case.k, case.ks, 16),
+                            ref.dequantized(fmt, case.v, case.vs, 16), lambda b, t: t, lens, pos,
+                            0, 0, step)
+    got = gq.attn_decode(q.to(DEV), case.cuda(), lens.to(DEV), pos.to(DEV), n, 0, step)
     ref.check_output(got, want, mass)
 
 
