@@ -33,13 +33,18 @@
 //     and O^T = V^T P^T; up to 16 (MT 1) the query rows are.
 //   * A score's softmax reference moves only past 2^8 (lazily), and a step that
 //     every row sees whole is not masked.
+//   * What is the same for all of a chunk's keys (its first row through the table,
+//     whether they are all visible, its scales with their logarithm and inverse) is
+//     worked out by one lane for each of the next 32 chunks, and shuffled.
 // Measured against earlier forms of this kernel (64 requests x 4 rows, 64 to 4,096
 // INT8 keys, 8 KV heads of 128, pages of 16; floor 41 us): keys loaded into the
 // fragments' registers one step ahead 127 us, in the ring 82, with in-kernel merging
-// and steps without per-key checks 74, and with 32 keys a step on twelve warps an SM
-// instead of 16 on sixteen 63 us (4.4 TB/s).  One query row: 5.1 TB/s E4M3, 6.2 bf16
-// (64 x 2,080 keys).  What bounds it now: the warps' own dependency chains (issue
-// slots about half used), and at one row a KV head DRAM.
+// and steps without per-key checks 74, with 32 keys a step on twelve warps an SM
+// instead of 16 on sixteen 63, with a lane for each of 32 chunks' rows and scales (13%
+// fewer instructions a key; 20% at head_dim 64) 60, with the shares cut anew 58 to 59 (4.7
+// TB/s).  One query row: 5.5 TB/s E4M3, 6.2 bf16 (64 x 2,080 keys).  What bounds it
+// now: the warps' own dependency chains (issue slots about half used), and at one row
+// a KV head DRAM.
 //
 // Work: a unit is (request, block of query rows, one or two KV heads).  All units'
 // chunks are laid end to end and cut into equal shares, one per CTA of a
@@ -69,9 +74,10 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxEntries = 128;  // (request, row block) pairs per launch
 // What a change of unit costs a CTA, in chunks: in the share arithmetic every unit is
-// followed by so many of nothing.  64 ragged requests (64 to 4,096 keys): 73 us with
-// 12, 63 with 24, 64 with 40.
-constexpr int kGapChunks = 24;
+// followed by so many of nothing.  64 ragged requests (64 to 4,096 keys): 65.1 us with
+// 16, 60.3 with 24, 59.0 with 28, 58.3 with 32, 59.4 with 36; 64 even ones (2,080 keys)
+// 57.6 with 24, 57.1 with 32.
+constexpr int kGapChunks = 32;
 // Smallest share of a CTA.  One request of 9,000 tokens, window 1,024: 8.2 us with 4
 // chunks, 8.9 with 8, 9.8 with 16.
 constexpr int kMinChunks = 4;
@@ -170,9 +176,6 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, bool on
 }
 __device__ __forceinline__ void cp_async_16_to(uint32_t dst, const uint8_t *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const float *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
     uint2 v;
@@ -303,11 +306,10 @@ __device__ __forceinline__ Entry make_entry(const Params &p, int e, int rb_rows,
 }
 
 // What a warp notes about a step in its ring: whether every key of it is there,
-// else the keys of each chunk that are; the scales of its chunks.
+// else the keys of each chunk that are.
 template <int NSUB>
 struct __align__(16) Note {
     uint32_t full, mask[NSUB];
-    float scale[NSUB][2];
 };
 
 template <int FMT, int HD, int MT, int HG>
@@ -514,13 +516,16 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
         auto page_of_chunk = [&](int rc) {
             return (int)(__umulhi((uint32_t)rc << 4, p.page_mul) >> p.page_shift);
         };
-        // the table entries of a step's evenly spaced chunks (read a step ahead of the rows)
-        int page[NSUB];
+        // What is the same for a whole chunk is worked out by one lane for 32 chunks at a
+        // time (kAhead steps: lane l has chunk l % NSUB of step l / NSUB) and handed out by
+        // shuffles; the table entries are read kAhead steps before that.
+        constexpr int kAhead = 32 / NSUB;
+        auto chunk_of_lane = [&](int c) { return c + lane / NSUB * G::kGroup + lane % NSUB; };
+        int page = 0;
         auto read_pages = [&](int c) {
-            if (p.kind == ATTN_CACHE_PAGED && even)
-#pragma unroll
-                for (int i = 0; i < NSUB; ++i)
-                    if (c + i < c_end) page[i] = __ldg(bt + page_of_chunk(real_chunk(c + i)));
+            const int cc = chunk_of_lane(c);
+            if (p.kind == ATTN_CACHE_PAGED && even && cc < c_end)
+                page = __ldg(bt + page_of_chunk(real_chunk(cc)));
         };
 
         float o[MT == 0 ? HD / 16 : HD / 8][4];
@@ -536,7 +541,6 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
         // this lane's first piece of an evenly spaced chunk, and from one to the next
         const uint32_t lane_at = my_row * row_step * G::kRowBytes + my_piece * 16;
         const uint8_t *const k_lane = p.k + lane_at, *const v_lane = p.v + lane_at;
-        const uint32_t copy_step = kRowsPer * row_step * G::kRowBytes;
         const uint32_t k_to = k_offset<G::kRowBytes>(my_row, my_piece);
         const uint32_t v_to = v_offset<G::kRowBytes>(my_row, my_piece);
         // where this thread reads its share of K and V in a chunk
@@ -548,69 +552,66 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
         auto ring_row = [&](int t) {
             return t < p.sinks ? t : p.sinks + (t - p.sinks) % (p.slots_per_seq - p.sinks);
         };
-        // an evenly spaced chunk's first row; false (and reported) for a page outside the pool
-        auto find = [&](int rc, int id, uint32_t &row, int &slot) {
-            if (p.kind == ATTN_CACHE_RING) {
-                row = row_index(b, ring_row(rc * kChunk));
-                slot = 0;
-                return true;
+        // For steps c .. c + (kAhead - 1) kGroup: each chunk's first row, whether it is
+        // there (a page outside the pool is reported), whether all its keys are visible
+        // and evenly spaced, and its scales
+        uint32_t top = 0, there = 0, entire = 0;
+        float next_sk = 1.f, next_sv = 1.f;
+        auto locate = [&](int c) {
+            const int cc = chunk_of_lane(c), rc = real_chunk(cc), t0 = rc * kChunk;
+            bool good = cc < c_end, run = even;
+            int slot = 0;
+            top = 0;
+            next_sk = next_sv = 1.f;
+            if (good) {
+                if (p.kind == ATTN_CACHE_RING) {
+                    const int r = ring_row(t0);
+                    top = row_index(b, r);
+                    run = t0 + kChunk <= p.sinks || (t0 >= p.sinks && r + kChunk <= p.slots_per_seq);
+                } else if (p.kind != ATTN_CACHE_PAGED) {
+                    top = row_index(b, t0);
+                    slot = b * p.slots_per_seq + t0;
+                } else if (even) {
+                    good = (unsigned)page < (unsigned)p.num_pages;
+                    if (good) {
+                        const int r = (rc - page_of_chunk(rc) * p.page_chunks) * kChunk;
+                        top = row_index(page, r);
+                        slot = page * p.block_size + r;
+                    } else {
+                        report_error(p.err, ATTN_ERR_BOUNDS);
+                    }
+                }
             }
-            if (p.kind != ATTN_CACHE_PAGED) {
-                row = row_index(b, rc * kChunk);
-                slot = b * p.slots_per_seq + rc * kChunk;
-                return true;
-            }
-            const bool good = (unsigned)id < (unsigned)p.num_pages;
-            if (!good) {
-                if (lane == 0) report_error(p.err, ATTN_ERR_BOUNDS);
-                id = 0;
-            }
-            const int r = (rc - page_of_chunk(rc) * p.page_chunks) * kChunk;
-            row = row_index(id, r);
-            slot = id * p.block_size + r;
-            return good;
+            there = __ballot_sync(0xffffffffu, good);
+            entire = __ballot_sync(0xffffffffu, good && run && chunk_mask(t0) == 0xFFFFu);
+            if constexpr (FMT != kBF16)
+                if (p.ks != nullptr && good) {
+                    const int64_t at = (int64_t)(slot >> p.scale_shift) * p.n_kv_heads + kvh;
+                    next_sk = __ldg(p.ks + at);
+                    next_sv = __ldg(p.vs + at);
+                }
         };
-        // requests step c (nothing past c_end) into stage st
-        auto request = [&](int c, int st) {
+        // requests step c (nothing past c_end), the k-th located, into stage st
+        auto request = [&](int c, int k, int st) {
             const uint32_t k_buf = ring + st * 2 * G::kStepBytes, v_buf = k_buf + G::kStepBytes;
             Note<NSUB> &note = sm.note[warp][st];
-            auto read_scales = [&](int i, int slot) {
-                if constexpr (FMT != kBF16)
-                    if (p.ks != nullptr && lane < 2)
-                        copy4(smem_u32(&note.scale[i][lane]),
-                              (lane == 0 ? p.ks : p.vs) +
-                                  (int64_t)(slot >> p.scale_shift) * p.n_kv_heads + kvh);
-            };
-            const int rc0 = real_chunk(c), t0 = rc0 * kChunk, t1 = t0 + NSUB * kChunk;
-            bool full = (even || p.kind == ATTN_CACHE_RING) && c + NSUB <= c_end &&
-                        (c >= ch.sc || c + NSUB <= ch.sc) && t1 <= en.hi &&
-                        (t0 >= en.lo || t1 <= p.sinks);
-            if (p.kind == ATTN_CACHE_RING)  // within the sinks, or the turning part without its end
-                full &= t1 <= p.sinks ||
-                        (t0 >= p.sinks && ring_row(t0) + NSUB * kChunk <= p.slots_per_seq);
+            const uint32_t all = ((1u << NSUB) - 1u) << (k * NSUB);
+            const bool full = (entire & all) == all && (c >= ch.sc || c + NSUB <= ch.sc);
             if (full) {
-                uint32_t top[NSUB];  // each chunk's first row
-                int slot[NSUB];
 #pragma unroll
-                for (int i = 0; i < NSUB; ++i) full &= find(rc0 + i, page[i], top[i], slot[i]);
-                if (full) {
+                for (int i = 0; i < NSUB; ++i) {
+                    uint32_t row = __shfl_sync(0xffffffffu, top, k * NSUB + i);
 #pragma unroll
-                    for (int i = 0; i < NSUB; ++i) {
-                        const uint64_t at = (uint64_t)top[i] * G::kRowBytes;
-                        const uint8_t *ks = k_lane + at, *vs = v_lane + at;
-#pragma unroll
-                        for (int n = 0; n < kChunk / kRowsPer; ++n) {
-                            // v_offset of row my_row + n kRowsPer against my_row's
-                            const int flip = G::kRowBytes == 128   ? 64 * (n & 1)
-                                             : G::kRowBytes == 256 ? 32 * (n & 3)
-                                                                   : 0;
-                            const int to = i * G::kChunkBytes + n * 512;
-                            cp_async_16_to(k_buf + k_to + to, ks);
-                            cp_async_16_to(v_buf + (v_to ^ flip) + to, vs);
-                            ks += copy_step;
-                            vs += copy_step;
-                        }
-                        read_scales(i, slot[i]);
+                    for (int n = 0; n < kChunk / kRowsPer; ++n) {
+                        // v_offset of row my_row + n kRowsPer against my_row's
+                        const int flip = G::kRowBytes == 128   ? 64 * (n & 1)
+                                         : G::kRowBytes == 256 ? 32 * (n & 3)
+                                                               : 0;
+                        const int to = i * G::kChunkBytes + n * 512;
+                        const uint64_t at = (uint64_t)row * G::kRowBytes;
+                        cp_async_16_to(k_buf + k_to + to, k_lane + at);
+                        cp_async_16_to(v_buf + (v_to ^ flip) + to, v_lane + at);
+                        row += kRowsPer * row_step;
                     }
                 }
             }
@@ -619,16 +620,10 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
                 // key by key; keys that are absent become zeros
 #pragma unroll
                 for (int i = 0; i < NSUB; ++i) {
-                    const bool in = c + i < c_end;
                     const int rc = real_chunk(c + i), t = rc * kChunk + (lane & 15);
-                    uint32_t mask = in ? chunk_mask(rc * kChunk) : 0u, top = 0, spread = 0;
-                    if (even && in) {
-                        int slot;
-                        if (!find(rc, page[i], top, slot)) mask = 0;  // (page 0's scales)
-                        read_scales(i, slot);
-                    } else if (FMT != kBF16 && lane < 2) {
-                        note.scale[i][lane] = 1.f;
-                    }
+                    const uint32_t first = __shfl_sync(0xffffffffu, top, k * NSUB + i);
+                    uint32_t mask = (there >> (k * NSUB + i)) & 1u ? chunk_mask(rc * kChunk) : 0u;
+                    uint32_t spread = 0;
                     if (!even) {
                         bool on = (mask >> (lane & 15)) & 1u;
                         if (on && p.kind == ATTN_CACHE_PAGED) {
@@ -648,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
 #pragma unroll
                     for (int n = 0; n < kChunk / kRowsPer; ++n) {
                         const int r = my_row + n * kRowsPer;
-                        const uint32_t row = even ? top + r * row_step
+                        const uint32_t row = even ? first + r * row_step
                                                   : __shfl_sync(0xffffffffu, spread, r);
                         const bool on = (mask >> r) & 1u;
                         const uint64_t at =
@@ -663,12 +658,13 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
 
         const int c0 = off + warp % G::kHeadWarps * NSUB;
         read_pages(c0);
+        locate(c0);
+        read_pages(c0 + kAhead * G::kGroup);
 #pragma unroll
         for (int st = 0; st < G::kStages - 1; ++st) {
             const int c = c0 + st * G::kGroup;
-            if (c < c_end) request(c, st);
+            if (c < c_end) request(c, st, st);
             copies_commit();
-            read_pages(c + G::kGroup);
         }
         // ---- q fragments and positions, while the first keys are under way
         constexpr int kQRows = MT == 0 ? 1 : 2;
@@ -714,26 +710,36 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
 #pragma unroll
             for (int e = 0; e < 4; ++e) q_bias[row_e(e)] = sum[e];
         }
-        int st = 0;
-        for (int c = c0; c < c_end; c += G::kGroup, st = st + 1 == G::kStages ? 0 : st + 1) {
+        // of 32 chunks, a lane each: what scores are multiplied with, log2 and inverse of V's scale
+        float f_lane = p.scale_log2, lv_lane = 0.f, inv_lane = 1.f;
+        int st = 0, step = 0;
+        for (int c = c0; c < c_end; c += G::kGroup, ++step, st = st + 1 == G::kStages ? 0 : st + 1) {
             copies_wait<G::kStages - 2>();
             __syncwarp();  // the step has landed for all lanes, and the step before is read
-            if (c + (G::kStages - 1) * G::kGroup < c_end)
-                request(c + (G::kStages - 1) * G::kGroup, st == 0 ? G::kStages - 1 : st - 1);
+            const int ahead = c + (G::kStages - 1) * G::kGroup;
+            if (ahead < c_end) {
+                const int k = (step + G::kStages - 1) % kAhead;
+                if (k == 0) {
+                    locate(ahead);
+                    read_pages(ahead + kAhead * G::kGroup);
+                }
+                request(ahead, k, st == 0 ? G::kStages - 1 : st - 1);
+            }
             copies_commit();
-            read_pages(c + G::kStages * G::kGroup);
+            const int of_step = step % kAhead * NSUB;  // the lane that has the step's first chunk
+            if (FMT != kBF16 && of_step == 0) {
+                const float sv = fmaxf(next_sv, kScaleFloor);
+                f_lane = fmaxf(next_sk, kScaleFloor) *
+                         (FMT == kINT8 ? p.scale_log2 * 16777216.f : p.scale_log2);
+                lv_lane = fast_log2(sv);
+                inv_lane = fast_rcp(sv);
+            }
             const uint32_t k_buf = ring + st * 2 * G::kStepBytes, v_buf = k_buf + G::kStepBytes;
             const Note<NSUB> &note = sm.note[warp][st];
             const bool cur_full = note.full != 0;
-            float cur_sk[NSUB], cur_sv[NSUB];
             uint32_t kw[NSUB][2][4 * G::kKPieces];
 #pragma unroll
             for (int i = 0; i < NSUB; ++i) {
-                cur_sk[i] = cur_sv[i] = 1.f;
-                if (FMT != kBF16 && p.ks != nullptr) {
-                    cur_sk[i] = fmaxf(note.scale[i][0], kScaleFloor);
-                    cur_sv[i] = fmaxf(note.scale[i][1], kScaleFloor);
-                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -812,13 +818,9 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
                               (p.window <= 0 || en.pmax - first_t < p.window || end_t <= p.sinks);
 #pragma unroll
             for (int i = 0; i < NSUB; ++i) {
-                f[i] = cur_sk[i] * (FMT == kINT8 ? p.scale_log2 * 16777216.f : p.scale_log2);
-                lv[i] = 0.f;
-                inv_sv[i] = 1.f;
-                if constexpr (FMT != kBF16) {
-                    lv[i] = fast_log2(cur_sv[i]);
-                    inv_sv[i] = fast_rcp(cur_sv[i]);
-                }
+                f[i] = FMT == kBF16 ? f_lane : __shfl_sync(0xffffffffu, f_lane, of_step + i);
+                lv[i] = FMT == kBF16 ? 0.f : __shfl_sync(0xffffffffu, lv_lane, of_step + i);
+                inv_sv[i] = FMT == kBF16 ? 1.f : __shfl_sync(0xffffffffu, inv_lane, of_step + i);
             }
             if (!open) {
 #pragma unroll
