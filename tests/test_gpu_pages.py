@@ -226,6 +226,21 @@ def test_copy(dtype, D, H, bs, layers, layout):
             assert torch.equal(got.cpu(), x)
 
 
+def test_copy_refuses_caches_of_different_shapes():
+    """One launch serves all layers: heads and sizes have to agree."""
+    def paged(pages, H):
+        k = torch.zeros(pages * 16, H, 64, dtype=torch.bfloat16, device=DEV)
+        table = torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+        return gq.KVCache(gq.PAGED, k, k.clone(), block_table=table, block_size=16)
+
+    moves, count = torch.zeros(1, 3, dtype=torch.int32, device=DEV), error()
+    gq.attn_pages_copy([paged(4, 2), paged(4, 2)], moves, count)
+    for other in (paged(4, 1), paged(2, 2), paged(2, 4)):
+        with pytest.raises(gq.AttnError):
+            gq.attn_pages_copy([paged(4, 2), other], moves, count)
+    gq.attn_pages_copy([], moves, count)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 def test_serving_run(fmt):
     """Pages reserved, a prompt appended, beams forked, tokens decoded under a
