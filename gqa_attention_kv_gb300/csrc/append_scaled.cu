@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(128, 6) kv_append_runs_kernel(const ScaledPara
         bool short_way =
             intact && ref == nullptr && r1 <= min(p.window, kPasses * kRows) &&
             __all_sync(0xffffffffu, lane < at_lane || lane > r1 ||
-                                        my_slot == slot0 + (lane - at_lane));
+                                        (good(my_slot) && my_slot == slot0 + (lane - at_lane)));
         float amax = 0.f;
         bool nan = false;
         if (short_way) {

@@ -383,6 +383,32 @@ def test_append_many_rows_of_long_blocks(fmt, D, H, sb, head_major, ref_vector):
     case.check()
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("D,sb,blocks", [(128, 16, 1), (128, 16, 40), (64, 16, 40), (128, 32, 20)])
+def test_append_slots_past_the_end_of_the_cache(fmt, D, sb, blocks):
+    """A prompt into the last slots whose slot mapping goes on past them: the rows
+    without a slot are skipped, and what lies behind the cache stays as it was."""
+    H, n = 8, blocks * sb
+    g = gen(D + sb + blocks)
+    case = Case(fmt, n, H, D, sb).fill(g)
+    cache = case.cuda()
+    guarded = []
+    for name in ("k", "v"):
+        x = getattr(cache, name)
+        big = torch.full((n + 32, H, D), 77, dtype=x.dtype, device=DEV)
+        big[:n] = x
+        setattr(cache, name, big[:n])
+        guarded.append(big)
+    at = torch.arange(n + 5)
+    k, v = new_rows(g, n + 5, H, D)
+    k[n:], v[n:] = 100.0, 100.0
+    case.append(k, v, at)
+    assert gpu_append(case, k, v, at) == gq.ATTN_ERR_BOUNDS
+    case.check()
+    for big in guarded:
+        assert (big[n:] == 77).all()
+
+
 @pytest.mark.parametrize("B,H,lo,hi", [(40, 2, 1, 20000),   # one long request among short ones
                                        (1, 1, 30000, 30000)])  # one unit over the whole GPU
 def test_decode_in_very_many_parts(B, H, lo, hi):
