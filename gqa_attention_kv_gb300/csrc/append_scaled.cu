@@ -19,6 +19,9 @@
 //     registers (16 rows of 128, 32 of 64).  Steps, and prompts in blocks of 16:
 //     14,449 rows of 4 x 128 in 10.9 us (4.1 TB/s; issue-bound: unpacking, scaling and
 //     packing 16-bit values), 64 single rows of 8 x 128 in 2.9 us.
+//     Of many rows a warp has 16, and the short runs among them are taken all at a time,
+//     a lane a row: single rows of 1,024 requests 5.8 us (19.1 one after another, 12.9 by
+//     a warp each), of 4,096 10.9 (40.6).
 //   * runs by CTAs: 64 rows (128 for blocks of 128) of one tensor and head, 16 a warp,
 //     in registers; the rows' maxima meet in shared memory, each warp finds the ends of
 //     the runs that its rows belong to in the slots around them and encodes its own
@@ -143,10 +146,105 @@ __device__ __forceinline__ float new_scale(float held, float amax) {
     return fmaxf(fmaxf(held, __fdiv_rn(amax, INT8 ? 127.f : 448.f)), kScaleFloor);
 }
 
+// The eight values of a lane's piece of a row, less ref's.
+__device__ __forceinline__ void piece_values(const uint4 &w, const float *ref, float *f) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        f[2 * e] = __uint_as_float(u[e] << 16);
+        f[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+    }
+    if (ref != nullptr)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = __fsub_rn(f[e], __ldg(ref + e));
+}
+
+// The largest magnitude of a row, NaN if it holds one, in all of the row's lanes.
+template <int LANES>
+__device__ __forceinline__ float row_max(const uint4 &w, const float *ref) {
+    float m;
+    if (ref == nullptr) {
+        uint32_t a = max_nan_bf16x2(max_nan_bf16x2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                    max_nan_bf16x2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1)
+            a = max_nan_bf16x2(a, __shfl_xor_sync(0xffffffffu, a, o));
+        m = max_nan(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
+    } else {
+        float f[8];
+        piece_values(w, ref, f);
+        m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(f[e]));
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
+    return m;
+}
+
+// Short runs of a warp's 16 rows, all at a time, a lane a row (lane 16 the row behind
+// them): those that begin at one of `starts`, end among the rows and hold finite values
+// in slots of the cache.  x: the rows; slot < 0: no row (kNone) or a skipped one; amax:
+// the row's largest magnitude; held: its block's scale.  Returns the rows written.
+template <bool INT8, int HD>
+__device__ __forceinline__ uint32_t append_short_runs(const ScaledParams &p, uint8_t *cache,
+                                                      float *scales, const float *ref, int h,
+                                                      const uint4 *x, int64_t slot, float amax,
+                                                      float held, uint32_t starts) {
+    constexpr int kLanes = HD / 8, kRows = 32 / kLanes;
+    const int lane = threadIdx.x & 31, heads = p.place.n_kv_heads;
+    const int64_t block = slot >> p.shift, next = __shfl_down_sync(0xffffffffu, slot, 1);
+    const bool good = slot >= 0;
+    // rows whose next row belongs to the same run, or is skipped
+    const uint32_t same =
+        __ballot_sync(0xffffffffu, good && lane < 16 && next >= 0 && (next >> p.shift) == block);
+    const uint32_t skipped = __ballot_sync(0xffffffffu, slot < 0 && slot != kNone);
+    const int last = lane + __ffs(~(same >> lane)) - 1;                   // of this lane's run
+    const uint32_t firsts = ~(same << 1) & (0xffffffffu >> (31 - lane));  // up to this lane
+    const int first = 31 - __clz(firsts);
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+        const float t = __shfl_down_sync(0xffffffffu, amax, o);
+        if (lane + o <= last) amax = max_nan(amax, t);
+    }
+    amax = __shfl_sync(0xffffffffu, amax, first);
+    const bool mine = good && lane < 16 && last < 16 && !((skipped >> (last + 1)) & 1u) &&
+                      ((starts >> first) & 1u) && amax < INFINITY;
+    const uint32_t zero = __ballot_sync(0xffffffffu, good && (slot & ((1 << p.shift) - 1)) == 0);
+    const bool fresh = ((zero >> first) & ((2u << (last - first)) - 1u)) != 0;
+    held = fresh ? 0.f : fmaxf(held, 0.f);
+    const float now = new_scale<INT8>(held, amax), r = __frcp_rn(now), by = __fmul_rn(held, r);
+    const uint32_t rows = __ballot_sync(0xffffffffu, mine);
+    uint32_t grown = __ballot_sync(0xffffffffu, mine && lane == first && held > 0.f && now > held);
+    while (grown != 0) {
+        const int a = __ffs(grown) - 1;
+        grown &= grown - 1;
+        recode<INT8, HD>(p, cache, h, __shfl_sync(0xffffffffu, block, a),
+                         __shfl_sync(0xffffffffu, by, a), 0, 0);
+    }
+    __syncwarp();
+    if (mine && lane == first) scales[block * heads + h] = now;
+#pragma unroll
+    for (int u = 0; u < 16 / kRows; ++u) {
+        const int row = u * kRows + lane / kLanes;
+        const float rr = __shfl_sync(0xffffffffu, r, row);
+        const int64_t to = __shfl_sync(0xffffffffu, slot, row);
+        if (!((rows >> row) & 1u)) continue;
+        float f[8];
+        piece_values(x[u], ref, f);
+        *reinterpret_cast<uint2 *>(cache + p.place.head_offset(to, h) +
+                                   (lane & (kLanes - 1)) * 8) =
+            make_uint2(encode4<INT8, false>(f, rr), encode4<INT8, false>(f + 4, rr));
+    }
+    __syncwarp();
+    return rows;
+}
+
 // Runs by warps: a warp takes the runs that start among its rows (one to sixteen),
 // whatever their length, alone.  A run that ends among these rows stays in registers
 // between its maximum and its codes.
-template <bool INT8, int HD>
+// SHORT: short runs are taken together where a warp's rows hold more than one.
+template <bool INT8, int HD, bool SHORT>
 __global__ void __launch_bounds__(128, 6) kv_append_runs_kernel(const ScaledParams p) {
     constexpr int kLanes = HD / 8;           // lanes of a row: 16 bytes of bf16, 8 codes each
     constexpr int kRows = 32 / kLanes;       // rows of a pass
@@ -200,6 +298,24 @@ __global__ void __launch_bounds__(128, 6) kv_append_runs_kernel(const ScaledPara
     const float my_scale = start ? scales[(my_slot >> p.shift) * heads + h] : 0.f;
     uint32_t starts = __ballot_sync(0xffffffffu, start);
     bool intact = true;  // x holds the window's rows
+    if (SHORT && (starts & (starts - 1)) != 0) {
+        float amax = 0.f;
+#pragma unroll
+        for (int u = 0; u < kMaxWindow / kRows; ++u) {
+            const float m = __shfl_sync(0xffffffffu, row_max<kLanes>(x[u], ref),
+                                        lane % kRows * kLanes);
+            if (lane / kRows == u) amax = m;
+        }
+        const int64_t s = __shfl_down_sync(0xffffffffu, my_slot, 1);
+        const float held = __shfl_down_sync(0xffffffffu, my_scale, 1);
+        const int64_t row = first_row + lane;
+        const int64_t slot = row >= p.n ? kNone : good(s) ? s : kBad;
+        // (a run's first lane has its scale)
+        const uint32_t first = (starts >> 1) & (0xffffffffu >> (31 - lane));
+        const float of_run = __shfl_sync(0xffffffffu, held, first == 0 ? 0 : 31 - __clz(first));
+        starts &= ~(append_short_runs<INT8, HD>(p, cache, scales, ref, h, x, slot, amax, of_run,
+                                                starts >> 1) << 1);
+    }
     while (starts != 0) {
         const int at_lane = __ffs(starts) - 1;  // of the run's first row
         const int64_t i0 = first_row - 1 + at_lane;
@@ -233,18 +349,7 @@ __global__ void __launch_bounds__(128, 6) kv_append_runs_kernel(const ScaledPara
             return l < 32 ? s : __ldg(p.slots + min(i, p.n - 1));
         };
         auto load = [&](int64_t base) { fetch(base, i1, true); };
-        // the eight values of a lane's piece
-        auto values = [&](const uint4 &w, float *f) {
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                f[2 * e] = __uint_as_float(u[e] << 16);
-                f[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
-            }
-            if (ref != nullptr)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = __fsub_rn(f[e], __ldg(ref + e));
-        };
+        auto values = [&](const uint4 &w, float *f) { piece_values(w, ref, f); };
         // The short way, a prompt's and a step's: the rows are in registers, in
         // consecutive slots, finite, and K has no reference.  Maxima are taken of bf16
         // pairs, INT8 codes need no clamp (|x r| <= 127 (1 + 2^-22)), addresses advance
@@ -402,42 +507,10 @@ __global__ void __launch_bounds__(W * 32, 24 / W)
     // ---- the rows' maxima, and the scales of their blocks
     const int64_t my_slot = lane < kMaxWindow && w0 + lane < n_cta ? slot(w0 + lane) : kNone;
     const float my_scale = my_slot >= 0 ? scales[(my_slot >> p.shift) * heads + h] : 0.f;
-    auto values = [&](const uint4 &w, float *f) {  // the eight values of a lane's piece
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            f[2 * e] = __uint_as_float(u[e] << 16);
-            f[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
-        }
-        if (ref != nullptr)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = __fsub_rn(f[e], __ldg(ref + e));
-    };
-    // the largest magnitude of a row, NaN if it holds one, in all of the row's lanes
-    auto row_max = [&](const uint4 &w) {
-        float m;
-        if (ref == nullptr) {
-            uint32_t a = max_nan_bf16x2(max_nan_bf16x2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
-                                        max_nan_bf16x2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
-#pragma unroll
-            for (int o = 1; o < kLanes; o <<= 1)
-                a = max_nan_bf16x2(a, __shfl_xor_sync(0xffffffffu, a, o));
-            m = max_nan(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
-        } else {
-            float f[8];
-            values(w, f);
-            m = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(f[e]));
-#pragma unroll
-            for (int o = 1; o < kLanes; o <<= 1)
-                m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-        }
-        return m;
-    };
+    auto values = [&](const uint4 &w, float *f) { piece_values(w, ref, f); };
 #pragma unroll
     for (int u = 0; u < kPasses; ++u) {
-        const float m = row_max(x[u]);
+        const float m = row_max<kLanes>(x[u], ref);
         if (piece == 0 && my_r + u * kRows < kMaxWindow) sm_max[w0 + my_r + u * kRows] = m;
     }
     __syncthreads();
@@ -447,11 +520,22 @@ __global__ void __launch_bounds__(W * 32, 24 / W)
     uint32_t starts = __ballot_sync(0xffffffffu, my_slot >= 0 &&
                                                      (my_slot != before + 1 || before < 0 ||
                                                       (my_slot & (sb - 1)) == 0));
-    const uint32_t good = __ballot_sync(0xffffffffu, my_slot >= 0);
+    const uint32_t good = __ballot_sync(0xffffffffu, my_slot >= 0), pieces = starts;
+    if (__popc(starts) > 2) {
+        // more than a block's end and another's beginning: the short runs together, a lane
+        // a row
+        const int64_t s = lane <= kMaxWindow ? slot(w0 + lane) : kNone;
+        const int64_t b4 = lane < kMaxWindow ? slot(w0 + lane - 1) : kNone;
+        const uint32_t apart = __ballot_sync(
+            0xffffffffu, s >= 0 && (b4 == kNone || (b4 >= 0 && (b4 >> p.shift) != (s >> p.shift))));
+        starts &= ~append_short_runs<INT8, HD>(
+            p, cache, scales, ref, h, x, s, lane < kMaxWindow ? sm_max[w0 + lane] : 0.f, my_scale,
+            apart);
+    }
     while (starts != 0) {
         const int a = __ffs(starts) - 1;  // the piece: rows w0 + a .. w0 + b - 1
         starts &= starts - 1;
-        const uint32_t ends = (starts | ~good) & (0xffffffffu << a);
+        const uint32_t ends = (pieces | ~good) & (0xfffffffeu << a);
         const int b = ends == 0 ? 32 : __ffs(ends) - 1;
         const int64_t s_a = slot(w0 + a), block = s_a >> p.shift;
         const int off = (int)(s_a & (sb - 1));
@@ -492,7 +576,7 @@ __global__ void __launch_bounds__(W * 32, 24 / W)
                         w = __ldg(src + ((row0 + r + my_r) * heads + h) * kLanes + piece);
                     else if (ref != nullptr)  // (its distance from the reference is no maximum)
                         w = __ldg(src + ((row0 + lo) * heads + h) * kLanes + piece);
-                    amax = max_nan(amax, row_max(w));
+                    amax = max_nan(amax, row_max<kLanes>(w, ref));
                 }
             };
             other(r0, min(0, r1));
@@ -631,14 +715,11 @@ int launch_kv_append_scaled(const void *k_new, const void *v_new, const int64_t 
                    ? (int)ATTN_OK
                    : (int)ATTN_ERR_CUDA;
     };
-    // A step's rows mostly are runs of their own, taken one after another: a row a warp
-    // is best.  A prompt's are runs of whole blocks.  Which of the two a call is shows
-    // in n alone: what a row a warp would need more warps for than the GPU holds at once
-    // (64 an SM) is taken for a prompt, in blocks of 16 by warps of 16 rows, in longer
-    // ones by CTAs.  8 x 128 in blocks of 16: a prompt of 1,024 rows takes 3.7 us by warps
-    // of 16 and 10.4 by warps of two, single rows of 1,024 requests 19.1 and 12.9; of
-    // 512, a row a warp, a prompt takes 9.4 (3.2 by warps of 16), single rows 8.8 (17.5).
-    const bool many = n * per_row > (int64_t)device_sm_count() * 64;
+    // While the GPU holds a warp for every row and head at once, each has one.  Past that
+    // warps have 16 rows (of blocks longer than 16: CTAs, a prompt's runs being long).
+    // 8 x 128: 512 single rows 8.8 us by a warp each, 5.7 by warps of 16; a prompt of 512
+    // 9.4 and 3.6; 1,024 single rows 5.8, a prompt 3.7 to 4.2.
+    const bool many = n * per_row > (int64_t)device_sm_count() * 24;
     if (many && cache->scale_block > 16) {
         const int w = cache->scale_block > 64 ? 8 : 4;
         const int64_t blocks = (n + w * kMaxWindow - 1) / (w * kMaxWindow) * per_row;
@@ -653,11 +734,19 @@ int launch_kv_append_scaled(const void *k_new, const void *v_new, const int64_t 
                                  : kv_append_blocks_kernel<false, 64, 8>, blocks, 256);
     }
     p.window = many ? kMaxWindow : 1;
-    const int64_t blocks = ((n + p.window - 1) / p.window * per_row + 3) / 4;
-    return head_dim == 128 ? run(int8 ? kv_append_runs_kernel<true, 128>
-                                      : kv_append_runs_kernel<false, 128>, blocks, 128)
-                           : run(int8 ? kv_append_runs_kernel<true, 64>
-                                      : kv_append_runs_kernel<false, 64>, blocks, 128);
+    const int64_t warps = (n + p.window - 1) / p.window * per_row, blocks = (warps + 3) / 4;
+    // Past a round and a half of such warps the rows are a prompt's: nothing is gained by
+    // short runs there, and the registers they take cost 14,449 rows of 4 x 128 12.1 us
+    // against 10.9 (single rows of that many requests would take four times as long so).
+    if (many && 2 * warps <= (int64_t)device_sm_count() * 24 * 3)
+        return head_dim == 128 ? run(int8 ? kv_append_runs_kernel<true, 128, true>
+                                          : kv_append_runs_kernel<false, 128, true>, blocks, 128)
+                               : run(int8 ? kv_append_runs_kernel<true, 64, true>
+                                          : kv_append_runs_kernel<false, 64, true>, blocks, 128);
+    return head_dim == 128 ? run(int8 ? kv_append_runs_kernel<true, 128, false>
+                                      : kv_append_runs_kernel<false, 128, false>, blocks, 128)
+                           : run(int8 ? kv_append_runs_kernel<true, 64, false>
+                                      : kv_append_runs_kernel<false, 64, false>, blocks, 128);
 }
 
 }  // namespace gqa

@@ -409,6 +409,35 @@ def test_append_slots_past_the_end_of_the_cache(fmt, D, sb, blocks):
         assert (big[n:] == 77).all()
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("D,H,sb,head_major,ref_vector", [
+    (128, 8, 16, False, False), (64, 8, 16, True, True), (128, 8, 64, False, True),
+    (64, 5, 32, False, False)])
+def test_append_short_runs(fmt, D, H, sb, head_major, ref_vector):
+    """Runs of one row to seven in blocks that hold tokens, many in a warp's rows, some
+    raising their block's scale, some across two warps, a few with values that are not
+    finite or skipped rows beside them."""
+    g = gen(D + H + sb + 1)
+    blocks = 500
+    k_ref = torch.randn(H, D, generator=g) if ref_vector else None
+    case = Case(fmt, blocks * sb, H, D, sb, per=sb * (blocks // 4), head_major=head_major,
+                k_ref=k_ref).fill(g)
+    case.cuda()
+    for longest in (1, 3, 7):
+        at = []
+        for b in torch.randperm(blocks, generator=g).tolist():
+            i = int(torch.randint(0, sb, (1,), generator=g))
+            m = int(torch.randint(1, longest + 1, (1,), generator=g))
+            at += range(b * sb + i, min(b * sb + i + m, (b + 1) * sb))
+        at = torch.tensor(at)
+        at[40], at[41], at[200] = -1, blocks * sb, -7
+        k, v = new_rows(g, len(at), H, D, 3.0)
+        k[77, 0, 5], v[99, 1, 6] = float("inf"), float("-inf")
+        case.append(k, v, at)
+        assert gpu_append(case, k, v, at) == gq.ATTN_ERR_BOUNDS
+        case.check()
+
+
 @pytest.mark.parametrize("B,H,lo,hi", [(40, 2, 1, 20000),   # one long request among short ones
                                        (1, 1, 30000, 30000)])  # one unit over the whole GPU
 def test_decode_in_very_many_parts(B, H, lo, hi):
