@@ -204,6 +204,7 @@ class KVCache:
                  dtype=ATTN_KV_BF16, k_ref=None, layout=ATTN_LAYOUT_BSHD, k_scale=None,
                  v_scale=None, scale_block=0):
         self.kind, self.k, self.v = int(kind), k, v
+        self._shape = k.shape  # what layers of one launch are compared by
         self.slots_per_seq = int(slots_per_seq)
         self.block_table = block_table
         self.block_size = int(block_size)
@@ -522,10 +523,10 @@ def attn_pages_copy(caches, moves, n_moves, err=None, stream=None):
     Hkv, D, slots, shape = 1, 128, 0, None
     if caches:
         first = caches[0]
-        Hkv, D, slots, shape = first.n_kv_heads, first.head_dim, first.num_slots, first.k.shape
+        Hkv, D, slots, shape = first.n_kv_heads, first.head_dim, first.num_slots, first._shape
     packed = []
     for c in caches:
-        if c.k.shape != shape:
+        if c._shape != shape:
             raise AttnError(ATTN_ERR_SHAPE, "attn_pages_copy: caches of different shapes")
         packed.append(_PACK(c.kind, c.k.data_ptr(), c.v.data_ptr(), slots, 0, 0,  # what copying reads
                             c.block_size, 0, c.dtype, 0, c.layout,
