@@ -136,9 +136,10 @@ struct Geo {
     static constexpr int NSUB = kRowBytes == 64 ? 4 : FMT != kBF16 ? 2 : 1;
     static constexpr int kChunkBytes = kChunk * kRowBytes;
     static constexpr int kStepBytes = NSUB * kChunkBytes;        // K (or V) of a step
-    // Stages and blocks an SM share its 227 KB: 8-bit steps take long enough (twelve
-    // warps unpacking) that one step ahead hides DRAM, bf16 steps do not (64 x 8 heads
-    // of 2,080 keys: 107 us with two stages and three blocks, 88 with three and two).
+    // Stages and blocks an SM share its 227 KB: 8-bit steps take long enough that twelve
+    // warps one step ahead do better than eight two steps ahead (64 ragged requests x 4
+    // rows 59.4 us, 64.5; 32 heads of 64 65.0, 67.2), bf16 steps do not (64 x 8 heads of
+    // 2,080 keys: 107 us with two stages and three blocks, 88 with three and two).
     static constexpr int kStages = FMT != kBF16 ? 2 : 3;
     static constexpr int CTAS = kRowBytes == 256 ? 2 : 3;
     static constexpr int kHeadWarps = kWarps / HG;               // warps of a KV head
