@@ -384,6 +384,32 @@ def test_append_many_rows_of_long_blocks(fmt, D, H, sb, head_major, ref_vector):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("D,R,per", [(128, 2, 16), (64, 2, 32), (128, 8, 16)])
+def test_decode_long_shares(fmt, D, R, per):
+    """64 requests that name the same pages: shares of hundreds of chunks, so every
+    warp works through its tables several times over, and one request to compare with.
+    Then a page outside the pool late in one of them: reported, the others unchanged."""
+    B, H, Hq, L, window = 64, 8, 16, 4001, 3900
+    case, q, lens, pos, slot = decode_case(fmt, gq.PAGED, 1, R, Hq, H, D, L, L, 16, per, False, D)
+    want, mass = ref.decode(q, ref.dequantized(fmt, case.k, case.ks, 16),
+                            ref.dequantized(fmt, case.v, case.vs, 16), slot, lens, pos, window, 0,
+                            D ** -0.5)
+    cache = case.cuda()
+    cache.block_table = cache.block_table.repeat(B, 1).contiguous()
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    args = (q.to(DEV).repeat(B, 1, 1, 1), cache, lens.to(DEV).repeat(B), pos.to(DEV).repeat(B), L,
+            window, D ** -0.5)
+    got = gq.attn_decode(*args, err=err)
+    assert int(err) == 0
+    ref.check_output(got, want.expand(B, -1, -1, -1), mass.expand(B, -1, -1, -1))
+    cache.block_table[37, (L - 200) // per] = case.k.shape[0] // per
+    again = gq.attn_decode(*args, err=err)
+    assert int(err) == gq.ATTN_ERR_BOUNDS
+    keep = [b for b in range(B) if b != 37]
+    assert torch.equal(again[keep], got[keep]) and not torch.equal(again[37], got[37])
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("D,sb,blocks", [(128, 16, 1), (128, 16, 40), (64, 16, 40), (128, 32, 20)])
 def test_append_slots_past_the_end_of_the_cache(fmt, D, sb, blocks):
     """A prompt into the last slots whose slot mapping goes on past them: the rows

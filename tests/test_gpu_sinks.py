@@ -192,6 +192,20 @@ def test_strided_and_misplaced_tensors_are_refused():
         gq.attn_prefill_sinks(q, q, q[:, ::2], 9, 2, 0.1)
 
 
+@pytest.mark.parametrize("D,R,per", [(128, 1, 16), (64, 1, 16), (64, 5, 32), (128, 2, 24)])
+def test_decode_long_shares(D, R, per):
+    """64 requests that name the same pages, hundreds of chunks a share, one to compare with."""
+    B, H, Hq, L, window, sinks = 64, 8, 16, 4003, 3500, 70
+    cache, q, k, v, lens, pos, slot = build(gq.PAGED, 1, R, Hq, H, D, L, L, per, window, sinks, D + R)
+    want, mass = ref.decode(q, k.double(), v.double(), slot, lens, pos, window, sinks, D ** -0.5)
+    cache.block_table = cache.block_table.repeat(B, 1).contiguous()
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = run(cache, q.repeat(B, 1, 1, 1), lens.repeat(B), pos.repeat(B), L, window, sinks,
+              D ** -0.5, err)
+    assert int(err) == 0
+    ref.check_output(got, want.expand(B, -1, -1, -1), mass.expand(B, -1, -1, -1), weight_bits=16)
+
+
 def test_decode_past_the_tables_of_one_launch():
     """More requests than one launch's tables hold, most of them short."""
     g = gen(1)
