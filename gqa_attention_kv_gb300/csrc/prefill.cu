@@ -67,6 +67,10 @@ constexpr uint32_t kRegsControl = 88;
 constexpr uint32_t kRegsSoftmax = 208;
 constexpr int kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
+// With sinks the f16 weights are held times 2^7, 2^15 at most: a sink that takes nearly
+// all of a row leaves the other keys weights far below its own, and those above 2^-21 of
+// the largest keep f16's 11 bits (2^-14 without).  The factor cancels in O / l.
+constexpr float kWeightLog2 = 7.0f;
 
 template <int HD>
 struct Cfg {
@@ -486,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_st_32x32b_x32(o_tmem + c0, orow);
                         }
                     }
-                    const float mref = m_run == -INFINITY ? 0.f : m_run;
+                    const float shift = kWeightLog2 - (m_run == -INFINITY ? 0.f : m_run);
                     float sum = 0.f;
                     uint32_t pk[16];
 #pragma unroll
@@ -495,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const int c = 2 * e + i;
-                            q2[i] = c < ns ? fast_exp2(fmaf(__uint_as_float(u[c]), sl2, -mref)) : 0.f;
+                            q2[i] = c < ns ? fast_exp2(fmaf(__uint_as_float(u[c]), sl2, shift)) : 0.f;
                             sum += q2[i];
                         }
                         pk[e] = pack_f16x2(q2[0], q2[1]);
@@ -587,6 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             const float mref = m_run == -INFINITY ? 0.f : m_run;
+            const float shift = SINKS ? kWeightLog2 - mref : -mref;
             float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
             for (int c0 = 0; c0 < kBN; c0 += 32) {
@@ -594,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     float x0, x1;
-                    fma2(x0, x1, s[c0 + 2 * e], s[c0 + 2 * e + 1], sl2, sl2, -mref, -mref);
+                    fma2(x0, x1, s[c0 + 2 * e], s[c0 + 2 * e + 1], sl2, sl2, shift, shift);
                     const float p0 = fast_exp2(x0);
                     const float p1 = fast_exp2(x1);
                     add2(sum0, sum1, sum0, sum1, p0, p1);

@@ -476,9 +476,10 @@ int attn_decode_sinks(const void *q, const attn_kv_cache *cache, const int32_t *
  * attn_prefill_sinks -- attn_prefill under a sliding window whose first n_sinks
  * tokens of each sequence stay visible: query i attends key t <= i with
  * t < n_sinks, window <= 0 or i - t < window.  n_sinks >= 0.  Every other
- * argument and the arithmetic are attn_prefill's, but that a NaN in v is
- * reported like a magnitude without an f16 (ATTN_ERR_UNSUPPORTED) and taken
- * as 0 when n_sinks > 0 and window > 0.
+ * argument and the arithmetic are attn_prefill's, but that with n_sinks > 0 and
+ * window > 0 the f16 softmax weights are held times 2^7 (a weight down to 2^-21
+ * of the row's largest, a sink's say, keeps 11 bits) and a NaN in v is reported
+ * like a magnitude without an f16 (ATTN_ERR_UNSUPPORTED) and taken as 0.
  */
 int attn_prefill_sinks(const void *q, const void *k, const void *v, int batch, int seq_len,
                        int window, int n_sinks, int n_q_heads, int n_kv_heads, int head_dim,

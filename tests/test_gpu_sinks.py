@@ -1,4 +1,6 @@
 """Sliding windows with sinks: decode over every cache kind, and prefill."""
+import math
+
 import pytest
 import torch
 
@@ -276,6 +278,33 @@ def test_prefill_values_that_are_not_finite():
     got = gq.attn_prefill_sinks(q.to(DEV), k.to(DEV), v.to(DEV), 32, 4, 0.1, err=err)
     assert int(err) == gq.ATTN_ERR_UNSUPPORTED
     assert torch.equal(got[:, :290], clean[:, :290])
+
+
+@pytest.mark.parametrize("D,group,sinks,window,T", [
+    (64, 1, 1, 150, 600),     # the tile of few sinks
+    (64, 7, 20, 200, 500),    # ... of 17 to 32, and heads that start at other tiles
+    (64, 2, 60, 150, 400),    # a whole tile of sinks
+    (128, 1, 1, 150, 600),
+    (128, 4, 130, 128, 700),  # two tiles of sinks
+])
+def test_prefill_small_weights_beside_a_sink(D, group, sinks, window, T):
+    """A sink with values of zero takes most of a row.  Key j of the window has
+    2^(-j / 2) of its weight and a value that stands alone in dim j: each weight
+    shows by itself, and down to 2^-20 of the sink's keeps the precision of one
+    rounding to 11 bits."""
+    n = 41
+    q, k, v = (torch.zeros(1, T, h, D) for h in (group, 1, 1))
+    q[..., 0] = 1.0
+    k[..., 0] = -60.0
+    k[0, sinks - 1, 0, 0] = 0.0
+    for j in range(n):
+        k[0, T - n - 5 + j, 0, 0] = -j / 2
+        v[0, T - n - 5 + j, 0, j] = 96.0
+    q, k, v = (x.bfloat16() for x in (q, k, v))
+    scale = math.log(2.0)
+    got = gq.attn_prefill_sinks(q.to(DEV), k.to(DEV), v.to(DEV), window, sinks, scale)
+    want, mass = ref.prefill(q, k, v, window, sinks, scale)
+    ref.check_output(got, want, mass)
 
 
 def test_prefill_agrees_with_decode():
