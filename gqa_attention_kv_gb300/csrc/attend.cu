@@ -89,6 +89,12 @@ constexpr float kRescaleLog2 = 8.0f;  // the reference maximum moves past this o
 // f16 weights are held times 2^7, 2^15 at most: those above 2^-21 of the largest keep
 // f16's 11 bits (2^-14 without), however small the largest's own value is
 constexpr float kWeightLog2 = 7.0f;
+// Scores (times log2(e)) up to which a weight is right: it is exp2 of the exact s f - M, and
+// half a step of M has to leave it below 2^16 (f16) or 2^128.  Larger ones are reported, also
+// where a K scale is so large that its factor f is cut off for s f to stay finite.
+constexpr float kScoreTopF16 = 0x1p24f, kScoreTopBf16 = 0x1p30f;
+constexpr float kFactorTop = 0x1p90f;
+constexpr float kPartWeight = 0x1p-12f;  // of the largest part: the sum of 4,096 outputs is finite
 constexpr float kScaleFloor = 5.421010862427522e-20f;  // 2^-64, the smallest scale
 
 enum Fmt { kBF16 = 0, kE4M3 = 1, kINT8 = 2 };
@@ -359,7 +365,7 @@ __device__ __forceinline__ void merge_unit(const Params &p, int64_t unit, int hs
             for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             const float m_new = fmaxf(m[r], mx), m_use = m_new == -INFINITY ? 0.f : m_new;
             const float old = fast_exp2(m[r] - m_use);
-            f[r] = fast_exp2(f[r] - m_use);
+            f[r] = kPartWeight * fast_exp2(f[r] - m_use);
             m[r] = m_new;
             sum[r] *= old;
 #pragma unroll
@@ -732,8 +738,9 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
                 const float sv = fmaxf(next_sv, kScaleFloor);
                 f_lane = fmaxf(next_sk, kScaleFloor) *
                          (FMT == kINT8 ? p.scale_log2 * 16777216.f : p.scale_log2);
+                f_lane = fminf(f_lane, kFactorTop);
                 lv_lane = fast_log2(sv);
-                inv_lane = fast_rcp(sv);
+                inv_lane = 0.25f * fast_rcp(0.25f * sv);  // subnormal from 2^126 on, not 0
             }
             const uint32_t k_buf = ring + st * 2 * G::kStepBytes, v_buf = k_buf + G::kStepBytes;
             const Note<NSUB> &note = sm.note[warp][st];
@@ -1016,6 +1023,11 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
         }
         copies_wait<0>();
         __syncwarp();  // the ring is this warp's to write
+        // (-inf: no key; an infinite score has no weight in the definition either)
+        if (fmaxf(m_run[0] == -INFINITY ? 0.f : fabsf(m_run[0]),
+                  m_run[1] == -INFINITY ? 0.f : fabsf(m_run[1])) >=
+            (FMT == kBF16 ? kScoreTopBf16 : kScoreTopF16))
+            report_error(p.err, ATTN_ERR_UNSUPPORTED);
 
         // ---- the four warps' states -> one
 #pragma unroll
@@ -1158,7 +1170,7 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const Params p) {
             for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             const float m_new = fmaxf(m, mx), m_use = m_new == -INFINITY ? 0.f : m_new;
             const float old = m == -INFINITY ? 0.f : fast_exp2(m - m_use);
-            const float f = fast_exp2(lse - m_use);
+            const float f = kPartWeight * fast_exp2(lse - m_use);
             m = m_new;
             sum *= old;
 #pragma unroll

@@ -257,6 +257,47 @@ def test_decode_scales_far_apart(fmt):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("D,R", [(64, 1), (64, 12), (128, 1), (128, 12)])
+def test_decode_largest_scales(fmt, D, R):
+    """Scores up to 2^20, where one key takes a row, are answered: products keep 2^-18
+    of their 127 (448) sum |q|, 2^-11 of a score here, and the two largest scores lie
+    further apart.  K scales from 2^103 on, whose scores pass 2^24, are reported.
+    V scales of 2^126.5, whose inverse is subnormal, stand beside 2^100."""
+    case, q, lens, pos, slot = decode_case(fmt, gq.LINEAR, 2, R, 4, 2, D, 300, 1500, 16, 0, False,
+                                           D + R)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def run(answer=True):
+        err.zero_()
+        got = gq.attn_decode(q.to(DEV), case.cuda(), lens.to(DEV), pos.to(DEV), 1500, 0, D ** -0.5,
+                             err=err)
+        if answer:
+            want, mass = ref.decode(q, ref.dequantized(fmt, case.k, case.ks, 16),
+                                    ref.dequantized(fmt, case.v, case.vs, 16), slot, lens, pos, 0,
+                                    0, D ** -0.5)
+            ref.check_output(got, want, mass)
+        return int(err)
+
+    small = case.ks.clone()
+    top = 13.0 if fmt == "int8" else 11.0
+    for b, x in ((0, 0), (3, 1), (5, 2), (17, 4), (95, 3), (100, 4)):
+        case.ks[b] = 2.0 ** (top - 4 + x) * 1.3
+    assert run() == 0
+    for b, x in ((0, 103), (3, 104), (5, 107), (17, 110), (95, 112), (100, 127)):
+        case.ks.copy_(small)
+        case.ks[b] = 2.0 ** x * 1.3
+        assert run(answer=False) == gq.ATTN_ERR_UNSUPPORTED
+    case.ks.copy_(small)
+    one = torch.tensor(1.0, dtype=torch.float64)
+    case.v.copy_(ref.encode(fmt, torch.randint(-2, 3, case.v.shape, generator=gen(1)).double(),
+                            one))
+    case.vs.fill_(2.0 ** 126.5)
+    case.vs[::3] = 2.0 ** 100
+    case.v[16:32] = 0
+    assert run() == 0
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("group", [1, 12])
 def test_decode_small_weights_beside_zeros(fmt, group):
     """Key j's weight is 2^(-j / 2) of the first key's and its value stands alone in
