@@ -95,6 +95,8 @@ constexpr float kWeightLog2 = 7.0f;
 constexpr float kScoreTopF16 = 0x1p24f, kScoreTopBf16 = 0x1p30f;
 constexpr float kFactorTop = 0x1p90f;
 constexpr float kPartWeight = 0x1p-12f;  // of the largest part: the sum of 4,096 outputs is finite
+// Weights of outputs that are added up are no smaller: 0 times an infinite one would be NaN
+constexpr float kSmallest = 0x1p-149f;
 constexpr float kScaleFloor = 5.421010862427522e-20f;  // 2^-64, the smallest scale
 
 enum Fmt { kBF16 = 0, kE4M3 = 1, kINT8 = 2 };
@@ -244,6 +246,13 @@ __device__ __forceinline__ bool word_not_finite(uint32_t w) {
         return false;
 }
 
+// The halves of a bf16 word that are not finite.
+__device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
+    return ((w & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) |
+           ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+}
+constexpr uint32_t kOnes = 0x3F803F80u;  // bf16x2
+
 __device__ __forceinline__ float fast_log2(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -369,7 +378,7 @@ __device__ __forceinline__ void merge_unit(const Params &p, int64_t unit, int hs
             m[r] = m_new;
             sum[r] *= old;
 #pragma unroll
-            for (int d = 0; d < V; ++d) acc[r][d] *= old;
+            for (int d = 0; d < V; ++d) acc[r][d] *= fmaxf(old, kSmallest);
         }
 #pragma unroll 4
         for (int k = 0; k < n; ++k) {
@@ -380,13 +389,14 @@ __device__ __forceinline__ void merge_unit(const Params &p, int64_t unit, int hs
                 const float *src =
                     p.ws_o + (((unit + c0 + k) * HG + hs) * RB + row) * HD + lane * V;
                 sum[r] += w;
+                const float wo = fmaxf(w, kSmallest);
                 if constexpr (V == 4) {
                     const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
-                    acc[r][0] += w * x.x, acc[r][1] += w * x.y;
-                    acc[r][2] += w * x.z, acc[r][3] += w * x.w;
+                    acc[r][0] += wo * x.x, acc[r][1] += wo * x.y;
+                    acc[r][2] += wo * x.z, acc[r][3] += wo * x.w;
                 } else {
                     const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
-                    acc[r][0] += w * x.x, acc[r][1] += w * x.y;
+                    acc[r][0] += wo * x.x, acc[r][1] += wo * x.y;
                 }
             }
         }
@@ -536,9 +546,7 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
         };
 
         float o[MT == 0 ? HD / 16 : HD / 8][4];
-#pragma unroll
-        for (auto &x : o) x[0] = x[1] = x[2] = x[3] = 0.f;
-        float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+        float m_run[2], l_run[2];
 
         // ---- copies of a step's keys
         constexpr int kPer = G::kRowBytes / 16;  // 16-byte pieces of a row
@@ -664,365 +672,392 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
         };
 
         const int c0 = off + warp % G::kHeadWarps * NSUB;
-        read_pages(c0);
-        locate(c0);
-        read_pages(c0 + kAhead * G::kGroup);
-#pragma unroll
-        for (int st = 0; st < G::kStages - 1; ++st) {
-            const int c = c0 + st * G::kGroup;
-            if (c < c_end) request(c, st, st);
-            copies_commit();
-        }
-        // ---- q fragments and positions, while the first keys are under way
         constexpr int kQRows = MT == 0 ? 1 : 2;
-        bool q_big = false;
-        for (int i = warp; i < HG * kSteps; i += kWarps) {
-            const int qs = i / kSteps, kk = i % kSteps;  // head of the unit, k-step
-            const int j = kk / G::kStepsPerPiece, st = kk % G::kStepsPerPiece;
-            const int d0 = (16 / G::E) * (tq + 4 * j) + 4 * st;
-#pragma unroll
-            for (int hr = 0; hr < kQRows; ++hr) {
-                uint2 x = *reinterpret_cast<const uint2 *>(qb + qs * p.group * HD +
-                                                            row_of(gq + 8 * hr) + d0);
-                if constexpr (FMT != kBF16) {  // f16 holds |q| < 65520
-                    x.x = bf16x2_to_f16x2(x.x);
-                    x.y = bf16x2_to_f16x2(x.y);
-                    q_big |= (x.x & 0x7C00u) == 0x7C00u || (x.x & 0x7C000000u) == 0x7C000000u ||
-                             (x.y & 0x7C00u) == 0x7C00u || (x.y & 0x7C000000u) == 0x7C000000u;
-                }
-                sm.q[qs][kk][lane][hr] = x.x;
-                sm.q[qs][kk][lane][kQRows + hr] = x.y;
-            }
-        }
-        if (q_big) report_error(p.err, ATTN_ERR_UNSUPPORTED);
         int rpos[2];  // positions of the two rows this thread keeps scores of
-        rpos[0] = MT == 0 ? pos_of(2 * tq) : pos_of(gq);
-        rpos[1] = MT == 0 ? pos_of(2 * tq + 1) : pos_of(gq + 8);
-        __syncthreads();
-
         float q_bias[2] = {0.f, 0.f};  // -128 2^-24 sum(q) of the two rows
-        if constexpr (FMT == kINT8) {
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-            const uint32_t a[4] = {kMinus128, kMinus128, kMinus128, kMinus128};
+        // This warp's chunks; bf16 again where an infinity in V may have become a NaN (by the
+        // lower half of its weight, which may be 0 or negative, or by a factor that is 0)
+        for (bool again = false;; again = true) {
 #pragma unroll
-            for (int kk = 0; kk < kSteps; ++kk) {
-                if constexpr (MT == 0) {
-                    mma_f16_16816(sum, a, sm.q[hs][kk][lane][0], sm.q[hs][kk][lane][1]);
-                } else {
-                    const uint32_t qa[4] = {sm.q[hs][kk][lane][0], sm.q[hs][kk][lane][1],
-                                            sm.q[hs][kk][lane][2], sm.q[hs][kk][lane][3]};
-                    mma_f16_16816(sum, qa, kMinus128, kMinus128);
-                }
+            for (auto &x : o) x[0] = x[1] = x[2] = x[3] = 0.f;
+            m_run[0] = m_run[1] = -INFINITY, l_run[0] = l_run[1] = 0.f;
+            read_pages(c0);
+            locate(c0);
+            read_pages(c0 + kAhead * G::kGroup);
+#pragma unroll
+            for (int st = 0; st < G::kStages - 1; ++st) {
+                const int c = c0 + st * G::kGroup;
+                if (c < c_end) request(c, st, st);
+                copies_commit();
             }
+            if (!again) {
+                // ---- q fragments and positions, while the first keys are under way
+                bool q_big = false;
+                for (int i = warp; i < HG * kSteps; i += kWarps) {
+                    const int qs = i / kSteps, kk = i % kSteps;  // head of the unit, k-step
+                    const int j = kk / G::kStepsPerPiece, st = kk % G::kStepsPerPiece;
+                    const int d0 = (16 / G::E) * (tq + 4 * j) + 4 * st;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) q_bias[row_e(e)] = sum[e];
-        }
-        // of 32 chunks, a lane each: what scores are multiplied with, log2 and inverse of V's scale
-        float f_lane = p.scale_log2, lv_lane = 0.f, inv_lane = 1.f;
-        int st = 0, step = 0;
-        for (int c = c0; c < c_end; c += G::kGroup, ++step, st = st + 1 == G::kStages ? 0 : st + 1) {
-            copies_wait<G::kStages - 2>();
-            __syncwarp();  // the step has landed for all lanes, and the step before is read
-            const int ahead = c + (G::kStages - 1) * G::kGroup;
-            if (ahead < c_end) {
-                const int k = (step + G::kStages - 1) % kAhead;
-                if (k == 0) {
-                    locate(ahead);
-                    read_pages(ahead + kAhead * G::kGroup);
-                }
-                request(ahead, k, st == 0 ? G::kStages - 1 : st - 1);
-            }
-            copies_commit();
-            const int of_step = step % kAhead * NSUB;  // the lane that has the step's first chunk
-            if (FMT != kBF16 && of_step == 0) {
-                const float sv = fmaxf(next_sv, kScaleFloor);
-                f_lane = fmaxf(next_sk, kScaleFloor) *
-                         (FMT == kINT8 ? p.scale_log2 * 16777216.f : p.scale_log2);
-                f_lane = fminf(f_lane, kFactorTop);
-                lv_lane = fast_log2(sv);
-                inv_lane = 0.25f * fast_rcp(0.25f * sv);  // subnormal from 2^126 on, not 0
-            }
-            const uint32_t k_buf = ring + st * 2 * G::kStepBytes, v_buf = k_buf + G::kStepBytes;
-            const Note<NSUB> &note = sm.note[warp][st];
-            const bool cur_full = note.full != 0;
-            uint32_t kw[NSUB][2][4 * G::kKPieces];
-#pragma unroll
-            for (int i = 0; i < NSUB; ++i) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int j = 0; j < G::kKPieces; ++j) {
-                        // piece tq + 4 j of row gq + 8 h
-                        const uint4 x = ld_shared_v4(k_buf + i * G::kChunkBytes +
-                                                     8 * h * G::kRowBytes +
-                                                     (k_from ^ (64 * (j & 1))) + 128 * (j >> 1));
-                        kw[i][h][4 * j] = x.x, kw[i][h][4 * j + 1] = x.y;
-                        kw[i][h][4 * j + 2] = x.z, kw[i][h][4 * j + 3] = x.w;
+                    for (int hr = 0; hr < kQRows; ++hr) {
+                        uint2 x = *reinterpret_cast<const uint2 *>(qb + qs * p.group * HD +
+                                                                    row_of(gq + 8 * hr) + d0);
+                        if constexpr (FMT != kBF16) {  // f16 holds |q| < 65520
+                            x.x = bf16x2_to_f16x2(x.x);
+                            x.y = bf16x2_to_f16x2(x.y);
+                            q_big |= (x.x & 0x7C00u) == 0x7C00u || (x.x & 0x7C000000u) == 0x7C000000u ||
+                                     (x.y & 0x7C00u) == 0x7C00u || (x.y & 0x7C000000u) == 0x7C000000u;
+                        }
+                        sm.q[qs][kk][lane][hr] = x.x;
+                        sm.q[qs][kk][lane][kQRows + hr] = x.y;
                     }
-            }
-            // ---- scores: MT 0 keys are the rows of S^T = K Q^T, MT 1 the columns of S = Q K^T.
-            // Even and odd k-steps add up apart: a product waits for half as many before it
-            constexpr int NJ = MT == 0 ? 1 : 2;
-            float s[NSUB][NJ][4];
-            float s_odd[NSUB][NJ][4];
-#pragma unroll
-            for (int i = 0; i < NSUB; ++i)
-#pragma unroll
-                for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        s[i][j][e] = FMT == kINT8 ? q_bias[row_e(e)] : 0.f;
-                        s_odd[i][j][e] = 0.f;
-                    }
-#pragma unroll
-            for (int kk = 0; kk < kSteps; ++kk) {
-                uint32_t qf[2 * kQRows];
-                if constexpr (MT == 0) {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(sm.q[hs][kk][lane]);
-                    qf[0] = x.x, qf[1] = x.y;
-                } else {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(sm.q[hs][kk][lane]);
-                    qf[0] = x.x, qf[1] = x.y, qf[2] = x.z, qf[3] = x.w;
                 }
+                if (q_big) report_error(p.err, ATTN_ERR_UNSUPPORTED);
+                rpos[0] = MT == 0 ? pos_of(2 * tq) : pos_of(gq);
+                rpos[1] = MT == 0 ? pos_of(2 * tq + 1) : pos_of(gq + 8);
+                __syncthreads();
+
+                if constexpr (FMT == kINT8) {
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const uint32_t a[4] = {kMinus128, kMinus128, kMinus128, kMinus128};
 #pragma unroll
-                for (int i = 0; i < NSUB; ++i) {
-                    uint32_t x[2][2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if constexpr (FMT == kBF16) {
-                            x[h][0] = kw[i][h][2 * kk];
-                            x[h][1] = kw[i][h][2 * kk + 1];
+                    for (int kk = 0; kk < kSteps; ++kk) {
+                        if constexpr (MT == 0) {
+                            mma_f16_16816(sum, a, sm.q[hs][kk][lane][0], sm.q[hs][kk][lane][1]);
                         } else {
-                            key_codes_to_f16<FMT>(kw[i][h][kk], x[h][0], x[h][1]);
+                            const uint32_t qa[4] = {sm.q[hs][kk][lane][0], sm.q[hs][kk][lane][1],
+                                                    sm.q[hs][kk][lane][2], sm.q[hs][kk][lane][3]};
+                            mma_f16_16816(sum, qa, kMinus128, kMinus128);
                         }
                     }
-                    if constexpr (MT == 0) {
-                        const uint32_t a[4] = {x[0][0], x[1][0], x[0][1], x[1][1]};
-                        mma16<FMT>(kk & 1 ? s_odd[i][0] : s[i][0], a, qf[0], qf[1]);
-                    } else {
-                        mma16<FMT>(s[i][0], qf, x[0][0], x[0][1]);
-                        mma16<FMT>(s[i][1], qf, x[1][0], x[1][1]);
-                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) q_bias[row_e(e)] = sum[e];
                 }
             }
+            // of 32 chunks, a lane each: what scores are multiplied with, log2 and inverse of V's scale
+            float f_lane = p.scale_log2, lv_lane = 0.f, inv_lane = 1.f;
+            int st = 0, step = 0;
+            for (int c = c0; c < c_end; c += G::kGroup, ++step, st = st + 1 == G::kStages ? 0 : st + 1) {
+                copies_wait<G::kStages - 2>();
+                __syncwarp();  // the step has landed for all lanes, and the step before is read
+                const int ahead = c + (G::kStages - 1) * G::kGroup;
+                if (ahead < c_end) {
+                    const int k = (step + G::kStages - 1) % kAhead;
+                    if (k == 0) {
+                        locate(ahead);
+                        read_pages(ahead + kAhead * G::kGroup);
+                    }
+                    request(ahead, k, st == 0 ? G::kStages - 1 : st - 1);
+                }
+                copies_commit();
+                const int of_step = step % kAhead * NSUB;  // the lane that has the step's first chunk
+                if (FMT != kBF16 && of_step == 0) {
+                    const float sv = fmaxf(next_sv, kScaleFloor);
+                    f_lane = fmaxf(next_sk, kScaleFloor) *
+                             (FMT == kINT8 ? p.scale_log2 * 16777216.f : p.scale_log2);
+                    f_lane = fminf(f_lane, kFactorTop);
+                    lv_lane = fast_log2(sv);
+                    inv_lane = 0.25f * fast_rcp(0.25f * sv);  // subnormal from 2^126 on, not 0
+                }
+                const uint32_t k_buf = ring + st * 2 * G::kStepBytes, v_buf = k_buf + G::kStepBytes;
+                const Note<NSUB> &note = sm.note[warp][st];
+                const bool cur_full = note.full != 0;
+                uint32_t kw[NSUB][2][4 * G::kKPieces];
 #pragma unroll
-            for (int i = 0; i < NSUB; ++i)
+                for (int i = 0; i < NSUB; ++i) {
 #pragma unroll
-                for (int j = 0; j < NJ; ++j)
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if constexpr (MT == 0) s[i][j][e] += s_odd[i][j][e];
-            // ---- mask and weights.  x(row, key): element e of s[i][j] is
-            // MT 0: row e & 1, key gq + 8 (e >> 1); MT 1: row e >> 1, key 8 j + 2 tq + (e & 1)
-            auto sees = [&](int i, int row, int key) {
-                const int t = real_chunk(c + i) * kChunk + key, pos = rpos[row];
-                return (cur_full || ((note.mask[i] >> key) & 1u)) && t <= pos &&
-                       (p.window <= 0 || pos - t < p.window || t < p.sinks);
-            };
-            float f[NSUB], lv[NSUB], inv_sv[NSUB];
-            const int first_t = real_chunk(c) * kChunk, end_t = first_t + NSUB * kChunk;
-            // every row sees every key of the step
-            const bool open = cur_full && end_t - 1 <= en.pmin &&
-                              (p.window <= 0 || en.pmax - first_t < p.window || end_t <= p.sinks);
-#pragma unroll
-            for (int i = 0; i < NSUB; ++i) {
-                f[i] = FMT == kBF16 ? f_lane : __shfl_sync(0xffffffffu, f_lane, of_step + i);
-                lv[i] = FMT == kBF16 ? 0.f : __shfl_sync(0xffffffffu, lv_lane, of_step + i);
-                inv_sv[i] = FMT == kBF16 ? 1.f : __shfl_sync(0xffffffffu, inv_lane, of_step + i);
-            }
-            if (!open) {
+                        for (int j = 0; j < G::kKPieces; ++j) {
+                            // piece tq + 4 j of row gq + 8 h
+                            const uint4 x = ld_shared_v4(k_buf + i * G::kChunkBytes +
+                                                         8 * h * G::kRowBytes +
+                                                         (k_from ^ (64 * (j & 1))) + 128 * (j >> 1));
+                            kw[i][h][4 * j] = x.x, kw[i][h][4 * j + 1] = x.y;
+                            kw[i][h][4 * j + 2] = x.z, kw[i][h][4 * j + 3] = x.w;
+                        }
+                }
+                // ---- scores: MT 0 keys are the rows of S^T = K Q^T, MT 1 the columns of S = Q K^T.
+                // Even and odd k-steps add up apart: a product waits for half as many before it
+                constexpr int NJ = MT == 0 ? 1 : 2;
+                float s[NSUB][NJ][4];
+                float s_odd[NSUB][NJ][4];
 #pragma unroll
                 for (int i = 0; i < NSUB; ++i)
 #pragma unroll
                     for (int j = 0; j < NJ; ++j)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int key = MT == 0 ? gq + 8 * (e >> 1) : 8 * j + 2 * tq + (e & 1);
-                            s[i][j][e] = sees(i, row_e(e), key) ? s[i][j][e] : -INFINITY;
+                            s[i][j][e] = FMT == kINT8 ? q_bias[row_e(e)] : 0.f;
+                            s_odd[i][j][e] = 0.f;
                         }
-            }
-            float alpha[2];
-            bool moved = false;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                // x = s f + lv grows with s (f > 0): its maximum is that of s
-                float mx = -INFINITY;
+                for (int kk = 0; kk < kSteps; ++kk) {
+                    uint32_t qf[2 * kQRows];
+                    if constexpr (MT == 0) {
+                        const uint2 x = *reinterpret_cast<const uint2 *>(sm.q[hs][kk][lane]);
+                        qf[0] = x.x, qf[1] = x.y;
+                    } else {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(sm.q[hs][kk][lane]);
+                        qf[0] = x.x, qf[1] = x.y, qf[2] = x.z, qf[3] = x.w;
+                    }
 #pragma unroll
-                for (int i = 0; i < NSUB; ++i) {
-                    float ms = fmaxf(s[i][0][MT == 0 ? r : 2 * r], s[i][0][MT == 0 ? r + 2 : 2 * r + 1]);
-                    if constexpr (NJ > 1) ms = max3(ms, s[i][1][2 * r], s[i][1][2 * r + 1]);
-                    mx = fmaxf(mx, fmaf(ms, f[i], lv[i]));
+                    for (int i = 0; i < NSUB; ++i) {
+                        uint32_t x[2][2];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if constexpr (FMT == kBF16) {
+                                x[h][0] = kw[i][h][2 * kk];
+                                x[h][1] = kw[i][h][2 * kk + 1];
+                            } else {
+                                key_codes_to_f16<FMT>(kw[i][h][kk], x[h][0], x[h][1]);
+                            }
+                        }
+                        if constexpr (MT == 0) {
+                            const uint32_t a[4] = {x[0][0], x[1][0], x[0][1], x[1][1]};
+                            mma16<FMT>(kk & 1 ? s_odd[i][0] : s[i][0], a, qf[0], qf[1]);
+                        } else {
+                            mma16<FMT>(s[i][0], qf, x[0][0], x[0][1]);
+                            mma16<FMT>(s[i][1], qf, x[1][0], x[1][1]);
+                        }
+                    }
                 }
-                if constexpr (MT == 0) {
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                } else {
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                }
-                const float m_old = m_run[r];
-                const float m_new = mx > m_old + kRescaleLog2 ? mx : m_old;
-                const float m_use = m_new == -INFINITY ? 0.f : m_new;
-                const float m_w = FMT == kBF16 ? m_use : m_use - kWeightLog2;
-                alpha[r] = m_new == m_old ? 1.f : fast_exp2(m_old - m_use);
-                moved |= m_new != m_old;
-                m_run[r] = m_new;
-                l_run[r] *= alpha[r];
 #pragma unroll
-                for (int i = 0; i < NSUB; ++i) {
-                    const float shift = lv[i] - m_w;
-                    float sum = 0.f;
+                for (int i = 0; i < NSUB; ++i)
 #pragma unroll
                     for (int j = 0; j < NJ; ++j)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (row_e(e) == r) {
-                                s[i][j][e] = fast_exp2(fmaf(s[i][j][e], f[i], shift));
-                                sum += s[i][j][e];
-                            }
-                    l_run[r] = fmaf(sum, inv_sv[i], l_run[r]);
+                            if constexpr (MT == 0) s[i][j][e] += s_odd[i][j][e];
+                // ---- mask and weights.  x(row, key): element e of s[i][j] is
+                // MT 0: row e & 1, key gq + 8 (e >> 1); MT 1: row e >> 1, key 8 j + 2 tq + (e & 1)
+                auto sees = [&](int i, int row, int key) {
+                    const int t = real_chunk(c + i) * kChunk + key, pos = rpos[row];
+                    return (cur_full || ((note.mask[i] >> key) & 1u)) && t <= pos &&
+                           (p.window <= 0 || pos - t < p.window || t < p.sinks);
+                };
+                float f[NSUB], lv[NSUB], inv_sv[NSUB];
+                const int first_t = real_chunk(c) * kChunk, end_t = first_t + NSUB * kChunk;
+                // every row sees every key of the step
+                const bool open = cur_full && !(FMT == kBF16 && again) && end_t - 1 <= en.pmin &&
+                                  (p.window <= 0 || en.pmax - first_t < p.window || end_t <= p.sinks);
+#pragma unroll
+                for (int i = 0; i < NSUB; ++i) {
+                    f[i] = FMT == kBF16 ? f_lane : __shfl_sync(0xffffffffu, f_lane, of_step + i);
+                    lv[i] = FMT == kBF16 ? 0.f : __shfl_sync(0xffffffffu, lv_lane, of_step + i);
+                    inv_sv[i] = FMT == kBF16 ? 1.f : __shfl_sync(0xffffffffu, inv_lane, of_step + i);
                 }
-            }
-            if (__any_sync(0xffffffffu, moved)) {
+                if (!open) {
 #pragma unroll
-                for (auto &x : o)
+                    for (int i = 0; i < NSUB; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[e] *= alpha[row_e(e)];
-            }
-            // ---- P V, a chunk at a time.  Weights as its operand: f16 (one rounding:
-            // 11 bits), or for a bf16 cache two bf16 halves (16 bits), since one
-            // bf16 rounding of P would cost as much as the output's own
-            constexpr int NP = MT == 0 ? 2 : 4;
-            constexpr int kPairs = HD / 16;            // pairs of dims of a thread
-            constexpr int kPairsPerWord = 2 / G::E;
+                        for (int j = 0; j < NJ; ++j)
 #pragma unroll
-            for (int i = 0; i < NSUB; ++i) {
-                uint32_t ph[NP], pl[NP];
-                if constexpr (MT == 0) {
-                    if constexpr (FMT == kBF16) {
-                        split_bf16x2(s[i][0][0], s[i][0][1], ph[0], pl[0]);
-                        split_bf16x2(s[i][0][2], s[i][0][3], ph[1], pl[1]);
-                        pl[0] = movmatrix_trans(pl[0]);
-                        pl[1] = movmatrix_trans(pl[1]);
-                    } else {
-                        ph[0] = pack_f16x2(s[i][0][0], s[i][0][1]);
-                        ph[1] = pack_f16x2(s[i][0][2], s[i][0][3]);
+                            for (int e = 0; e < 4; ++e) {
+                                const int key = MT == 0 ? gq + 8 * (e >> 1) : 8 * j + 2 * tq + (e & 1);
+                                s[i][j][e] = sees(i, row_e(e), key) ? s[i][j][e] : -INFINITY;
+                            }
+                }
+                float alpha[2];
+                bool moved = false;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    // x = s f + lv grows with s (f > 0): its maximum is that of s
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < NSUB; ++i) {
+                        float ms = fmaxf(s[i][0][MT == 0 ? r : 2 * r], s[i][0][MT == 0 ? r + 2 : 2 * r + 1]);
+                        if constexpr (NJ > 1) ms = max3(ms, s[i][1][2 * r], s[i][1][2 * r + 1]);
+                        mx = fmaxf(mx, fmaf(ms, f[i], lv[i]));
                     }
-                    ph[0] = movmatrix_trans(ph[0]);
-                    ph[1] = movmatrix_trans(ph[1]);
-                } else {
+                    if constexpr (MT == 0) {
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                    } else {
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    }
+                    const float m_old = m_run[r];
+                    const float m_new = mx > m_old + kRescaleLog2 ? mx : m_old;
+                    const float m_use = m_new == -INFINITY ? 0.f : m_new;
+                    const float m_w = FMT == kBF16 ? m_use : m_use - kWeightLog2;
+                    alpha[r] = m_new == m_old ? 1.f : fast_exp2(m_old - m_use);
+                    moved |= m_new != m_old;
+                    m_run[r] = m_new;
+                    l_run[r] *= alpha[r];
+#pragma unroll
+                    for (int i = 0; i < NSUB; ++i) {
+                        const float shift = lv[i] - m_w;
+                        float sum = 0.f;
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (row_e(e) == r) {
+                                    s[i][j][e] = fast_exp2(fmaf(s[i][j][e], f[i], shift));
+                                    sum += s[i][j][e];
+                                }
+                        l_run[r] = fmaf(sum, inv_sv[i], l_run[r]);
+                    }
+                }
+                if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                    for (auto &x : o)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            x[e] *= FMT == kBF16 ? fmaxf(alpha[row_e(e)], kSmallest)
+                                                 : alpha[row_e(e)];
+                }
+                // ---- P V, a chunk at a time.  Weights as its operand: f16 (one rounding:
+                // 11 bits), or for a bf16 cache two bf16 halves (16 bits), since one
+                // bf16 rounding of P would cost as much as the output's own
+                constexpr int NP = MT == 0 ? 2 : 4;
+                constexpr int kPairs = HD / 16;            // pairs of dims of a thread
+                constexpr int kPairsPerWord = 2 / G::E;
+#pragma unroll
+                for (int i = 0; i < NSUB; ++i) {
+                    uint32_t ph[NP], pl[NP];
+                    if constexpr (MT == 0) {
+                        if constexpr (FMT == kBF16) {
+                            split_bf16x2(s[i][0][0], s[i][0][1], ph[0], pl[0]);
+                            split_bf16x2(s[i][0][2], s[i][0][3], ph[1], pl[1]);
+                            pl[0] = movmatrix_trans(pl[0]);
+                            pl[1] = movmatrix_trans(pl[1]);
+                        } else {
+                            ph[0] = pack_f16x2(s[i][0][0], s[i][0][1]);
+                            ph[1] = pack_f16x2(s[i][0][2], s[i][0][3]);
+                        }
+                        ph[0] = movmatrix_trans(ph[0]);
+                        ph[1] = movmatrix_trans(ph[1]);
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            const int j = n >> 1, r = n & 1;
+                            if constexpr (FMT == kBF16)
+                                split_bf16x2(s[i][j][2 * r], s[i][j][2 * r + 1], ph[n], pl[n]);
+                            else
+                                ph[n] = pack_f16x2(s[i][j][2 * r], s[i][j][2 * r + 1]);
+                        }
+                    }
+                    // V operands of two neighbouring dims (word w of a thread's share): x[0]
+                    // and x[1] dim 0 and 1 over keys 2 tq, 2 tq + 1, x[2] and x[3] over + 8
+                    auto v_pair = [&](const uint32_t (&w)[4], int hi, uint32_t (&x)[4]) {
+                        if constexpr (FMT == kBF16) {
+                            x[0] = __byte_perm(w[0], w[1], 0x5410u);
+                            x[1] = __byte_perm(w[0], w[1], 0x7632u);
+                            x[2] = __byte_perm(w[2], w[3], 0x5410u);
+                            x[3] = __byte_perm(w[2], w[3], 0x7632u);
+                        } else {
+                            const uint32_t sel = hi ? 0x7362u : 0x5140u;
+                            codes_to_f16<FMT>(__byte_perm(w[0], w[1], sel), x[0], x[1]);
+                            codes_to_f16<FMT>(__byte_perm(w[2], w[3], sel), x[2], x[3]);
+                        }
+                    };
+                    auto add_pv = [&](const uint32_t (&x)[4], float (&oa)[4], float (&ob)[4]) {
+                        if constexpr (MT == 0) {  // O^T: dim 0 in elements 0, 1, dim 1 in 2, 3
+                            mma16<FMT>(oa, x, ph[0], ph[1]);
+                            if constexpr (FMT == kBF16) mma16<FMT>(oa, x, pl[0], pl[1]);
+                        } else {
+                            mma16<FMT>(oa, ph, x[0], x[2]);
+                            mma16<FMT>(ob, ph, x[1], x[3]);
+                            if constexpr (FMT == kBF16) {
+                                mma16<FMT>(oa, pl, x[0], x[2]);
+                                mma16<FMT>(ob, pl, x[1], x[3]);
+                            }
+                        }
+                    };
+                    uint32_t vw[4][G::kVWords];
 #pragma unroll
                     for (int n = 0; n < 4; ++n) {
-                        const int j = n >> 1, r = n & 1;
-                        if constexpr (FMT == kBF16)
-                            split_bf16x2(s[i][j][2 * r], s[i][j][2 * r + 1], ph[n], pl[n]);
-                        else
-                            ph[n] = pack_f16x2(s[i][j][2 * r], s[i][j][2 * r + 1]);
-                    }
-                }
-                // V operands of two neighbouring dims (word w of a thread's share): x[0]
-                // and x[1] dim 0 and 1 over keys 2 tq, 2 tq + 1, x[2] and x[3] over + 8
-                auto v_pair = [&](const uint32_t (&w)[4], int hi, uint32_t (&x)[4]) {
-                    if constexpr (FMT == kBF16) {
-                        x[0] = __byte_perm(w[0], w[1], 0x5410u);
-                        x[1] = __byte_perm(w[0], w[1], 0x7632u);
-                        x[2] = __byte_perm(w[2], w[3], 0x5410u);
-                        x[3] = __byte_perm(w[2], w[3], 0x7632u);
-                    } else {
-                        const uint32_t sel = hi ? 0x7362u : 0x5140u;
-                        codes_to_f16<FMT>(__byte_perm(w[0], w[1], sel), x[0], x[1]);
-                        codes_to_f16<FMT>(__byte_perm(w[2], w[3], sel), x[2], x[3]);
-                    }
-                };
-                auto add_pv = [&](const uint32_t (&x)[4], float (&oa)[4], float (&ob)[4]) {
-                    if constexpr (MT == 0) {  // O^T: dim 0 in elements 0, 1, dim 1 in 2, 3
-                        mma16<FMT>(oa, x, ph[0], ph[1]);
-                        if constexpr (FMT == kBF16) mma16<FMT>(oa, x, pl[0], pl[1]);
-                    } else {
-                        mma16<FMT>(oa, ph, x[0], x[2]);
-                        mma16<FMT>(ob, ph, x[1], x[3]);
-                        if constexpr (FMT == kBF16) {
-                            mma16<FMT>(oa, pl, x[0], x[2]);
-                            mma16<FMT>(ob, pl, x[1], x[3]);
-                        }
-                    }
-                };
-                uint32_t vw[4][G::kVWords];
+                        const uint32_t src =
+                            v_buf + i * G::kChunkBytes + 8 * (n >> 1) * G::kRowBytes;
+                        if constexpr (G::kVBytes == 8) {
+                            const uint2 x = ld_shared_v2(src + (v_from ^ (64 * (n & 1))));
+                            vw[n][0] = x.x, vw[n][1] = x.y;
+                        } else {
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const uint32_t src =
-                        v_buf + i * G::kChunkBytes + 8 * (n >> 1) * G::kRowBytes;
-                    if constexpr (G::kVBytes == 8) {
-                        const uint2 x = ld_shared_v2(src + (v_from ^ (64 * (n & 1))));
-                        vw[n][0] = x.x, vw[n][1] = x.y;
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < G::kVPieces; ++j) {
-                            const uint4 x =
-                                ld_shared_v4(src + v_from + (n & 1) * G::kRowBytes + 128 * j);
-                            vw[n][4 * j] = x.x, vw[n][4 * j + 1] = x.y;
-                            vw[n][4 * j + 2] = x.z, vw[n][4 * j + 3] = x.w;
-                        }
-                    }
-                }
-                if constexpr (FMT != kINT8) {
-                    if (!open) {
-                        // A value that is not finite reaches only the rows that see its
-                        // key: 0 times it would be NaN in every row.  Such keys are
-                        // multiplied alone, added where seen, and taken out.
-                        uint32_t odd = 0;
-#pragma unroll
-                        for (int n = 0; n < 4; ++n)
-#pragma unroll
-                            for (int w = 0; w < G::kVWords; ++w)
-                                if (word_not_finite<FMT>(vw[n][w]))
-                                    odd |= 1u << (2 * tq + (n & 1) + 8 * (n >> 1));
-                        odd = __reduce_or_sync(0xffffffffu, odd);
-                        while (odd != 0) {
-                            const int key = __ffs(odd) - 1;
-                            odd &= odd - 1;
-#pragma unroll
-                            for (int d = 0; d < kPairs; ++d) {
-                                uint32_t w[4], x[4];
-#pragma unroll
-                                for (int n = 0; n < 4; ++n)
-                                    w[n] = key == 2 * tq + (n & 1) + 8 * (n >> 1)
-                                               ? vw[n][d / kPairsPerWord]
-                                               : 0u;
-                                v_pair(w, d % kPairsPerWord, x);
-                                float ta[4] = {0.f, 0.f, 0.f, 0.f}, tb[4] = {0.f, 0.f, 0.f, 0.f};
-                                add_pv(x, ta, tb);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (sees(i, row_e(e), key)) {
-                                        o[MT == 0 ? d : 2 * d][e] += ta[e];
-                                        if constexpr (MT != 0) o[2 * d + 1][e] += tb[e];
-                                    }
+                            for (int j = 0; j < G::kVPieces; ++j) {
+                                const uint4 x =
+                                    ld_shared_v4(src + v_from + (n & 1) * G::kRowBytes + 128 * j);
+                                vw[n][4 * j] = x.x, vw[n][4 * j + 1] = x.y;
+                                vw[n][4 * j + 2] = x.z, vw[n][4 * j + 3] = x.w;
                             }
+                        }
+                    }
+                    if constexpr (FMT != kINT8) {
+                        if (!open) {
+                            // A value that is not finite reaches only the rows that see its
+                            // key: 0 times it would be NaN in every row.  Such keys are
+                            // multiplied alone, added where seen, and taken out (bf16: such
+                            // values, and by 1: any weight above 0 gives the same).
+                            uint32_t odd = 0;
 #pragma unroll
                             for (int n = 0; n < 4; ++n)
-                                if (key == 2 * tq + (n & 1) + 8 * (n >> 1))
 #pragma unroll
-                                    for (int w = 0; w < G::kVWords; ++w) vw[n][w] = 0u;
+                                for (int w = 0; w < G::kVWords; ++w)
+                                    if (word_not_finite<FMT>(vw[n][w]))
+                                        odd |= 1u << (2 * tq + (n & 1) + 8 * (n >> 1));
+                            odd = __reduce_or_sync(0xffffffffu, odd);
+                            while (odd != 0) {
+                                const int key = __ffs(odd) - 1;
+                                odd &= odd - 1;
+#pragma unroll
+                                for (int d = 0; d < kPairs; ++d) {
+                                    uint32_t w[4], x[4];
+#pragma unroll
+                                    for (int n = 0; n < 4; ++n) {
+                                        uint32_t &v = vw[n][d / kPairsPerWord];
+                                        const bool its = key == 2 * tq + (n & 1) + 8 * (n >> 1);
+                                        w[n] = !its ? 0u : FMT == kBF16 ? v & odd_halves(v) : v;
+                                        if (FMT == kBF16 && its) v &= ~odd_halves(v);
+                                    }
+                                    v_pair(w, d % kPairsPerWord, x);
+                                    float ta[4] = {0.f, 0.f, 0.f, 0.f}, tb[4] = {0.f, 0.f, 0.f, 0.f};
+                                    if constexpr (FMT != kBF16) {
+                                        add_pv(x, ta, tb);
+                                    } else if constexpr (MT == 0) {
+                                        mma16<FMT>(ta, x, kOnes, kOnes);
+                                    } else {
+                                        const uint32_t ones[4] = {kOnes, kOnes, kOnes, kOnes};
+                                        mma16<FMT>(ta, ones, x[0], x[2]);
+                                        mma16<FMT>(tb, ones, x[1], x[3]);
+                                    }
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        if (sees(i, row_e(e), key)) {
+                                            o[MT == 0 ? d : 2 * d][e] += ta[e];
+                                            if constexpr (MT != 0) o[2 * d + 1][e] += tb[e];
+                                        }
+                                }
+#pragma unroll
+                                for (int n = 0; n < 4; ++n)
+                                    if (FMT != kBF16 && key == 2 * tq + (n & 1) + 8 * (n >> 1))
+#pragma unroll
+                                        for (int w = 0; w < G::kVWords; ++w) vw[n][w] = 0u;
+                            }
                         }
                     }
-                }
 #pragma unroll
-                for (int d = 0; d < kPairs; ++d) {
-                    uint32_t w[4], x[4];
+                    for (int d = 0; d < kPairs; ++d) {
+                        uint32_t w[4], x[4];
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) w[n] = vw[n][d / kPairsPerWord];
-                    v_pair(w, d % kPairsPerWord, x);
-                    if constexpr (MT == 0)
-                        add_pv(x, o[d], o[d]);
-                    else
-                        add_pv(x, o[2 * d], o[2 * d + 1]);
+                        for (int n = 0; n < 4; ++n) w[n] = vw[n][d / kPairsPerWord];
+                        v_pair(w, d % kPairsPerWord, x);
+                        if constexpr (MT == 0)
+                            add_pv(x, o[d], o[d]);
+                        else
+                            add_pv(x, o[2 * d], o[2 * d + 1]);
+                    }
                 }
             }
+            copies_wait<0>();
+            __syncwarp();  // the ring is this warp's to write
+            if constexpr (FMT != kBF16) break;
+            bool nan = false;
+#pragma unroll
+            for (auto &x : o) nan |= isnan(x[0]) || isnan(x[1]) || isnan(x[2]) || isnan(x[3]);
+            if (again || !__any_sync(0xffffffffu, nan)) break;
         }
-        copies_wait<0>();
-        __syncwarp();  // the ring is this warp's to write
         // (-inf: no key; an infinite score has no weight in the definition either)
         if (fmaxf(m_run[0] == -INFINITY ? 0.f : fabsf(m_run[0]),
                   m_run[1] == -INFINITY ? 0.f : fabsf(m_run[1])) >=
@@ -1082,7 +1117,8 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
             }
             const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-            for (int w = 0; w < W; ++w) sm.w[w0 + w][row] = f[w] * inv;
+            for (int w = 0; w < W; ++w)
+                sm.w[w0 + w][row] = FMT == kBF16 ? fmaxf(f[w] * inv, kSmallest) : f[w] * inv;
             sm.lse[h][row] = l == 0.f ? -INFINITY : m_use + log2f(l);
         }
         __syncthreads();
@@ -1174,19 +1210,20 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const Params p) {
             m = m_new;
             sum *= old;
 #pragma unroll
-            for (int d = 0; d < V; ++d) acc[d] *= old;
+            for (int d = 0; d < V; ++d) acc[d] *= fmaxf(old, kSmallest);
             const int n = min(32, (parts.y - c0) / SPLIT + 1);
             const float *src = p.ws_o + (((unit + c0) * HG + hs) * RB + row) * HD + lane * V;
 #pragma unroll 8
             for (int k = 0; k < n; ++k, src += (int64_t)SPLIT * HG * RB * HD) {
                 const float w = __shfl_sync(0xffffffffu, f, k);
                 sum += w;
+                const float wo = fmaxf(w, kSmallest);
                 if constexpr (V == 4) {
                     const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
-                    acc[0] += w * x.x, acc[1] += w * x.y, acc[2] += w * x.z, acc[3] += w * x.w;
+                    acc[0] += wo * x.x, acc[1] += wo * x.y, acc[2] += wo * x.z, acc[3] += wo * x.w;
                 } else {
                     const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
-                    acc[0] += w * x.x, acc[1] += w * x.y;
+                    acc[0] += wo * x.x, acc[1] += wo * x.y;
                 }
             }
         }
@@ -1203,7 +1240,8 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const Params p) {
             m = m_new;
             sum = sum * fa + sm_sum[w] * fb;
 #pragma unroll
-            for (int d = 0; d < V; ++d) acc[d] = acc[d] * fa + sm_acc[w][lane * V + d] * fb;
+            for (int d = 0; d < V; ++d)
+                acc[d] = acc[d] * fmaxf(fa, kSmallest) + sm_acc[w][lane * V + d] * fmaxf(fb, kSmallest);
         }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;

@@ -457,7 +457,8 @@ int attn_prefill(const void *q, const void *k, const void *v, int batch, int seq
  *   R - n_sinks >= window + q_rows - 1.  With n_sinks 0 that is the plain ring.
  *   Every cache dtype, kind and layout that attn_decode takes (unscaled FP8 at
  *   head_dim 128).  A position below 0 marks a row without keys (zeros).  A
- *   value that is not finite reaches only the rows that attend its key.  A row's
+ *   value that is not finite reaches only the rows that attend its key (an
+ *   infinity in v makes their element that infinity).  A row's
  *   largest score, scale * q . key * log2(e), has to stay below 2^30 in magnitude
  *   over bf16 caches, 2^24 over 8-bit ones (ATTN_ERR_UNSUPPORTED is reported
  *   otherwise, and the row is unspecified).

@@ -159,6 +159,41 @@ def test_decode_values_that_are_not_finite():
     assert torch.equal(finite, want)
 
 
+@pytest.mark.parametrize("D,R,B,hi,window", [
+    (128, 1, 1, 900, 0), (64, 1, 1, 900, 0), (128, 5, 2, 2000, 1800), (64, 5, 2, 2000, 0),
+    (128, 1, 1, 40000, 0), (64, 2, 60, 700, 500)])
+def test_decode_infinite_values(D, R, B, hi, window):
+    """An infinity in V makes the element of every row that attends its key infinite,
+    with its sign, however small the key's weight is, infinities of both signs a NaN;
+    the other elements are as without it."""
+    Hq, H = 8, 2
+    cache, q, k, v, lens, pos, slot = build(gq.LINEAR, B, R, Hq, H, D, hi, hi, 0, window, 4, D + R)
+    inf = float("inf")
+    for b in range(B):
+        base = b * hi
+        for key, h, d, x in ((0, 0, 3, inf), (2, 1, 5, -inf), (hi - 1, 0, 9, inf),
+                             (hi - 300, 1, 0, inf), (hi - 301, 1, D - 1, -inf),
+                             (hi - 400, 0, 20, inf), (hi - 17, 0, 20, -inf),
+                             (hi - 250, 0, 31, inf)):
+            v[base + key, h, d] = x
+        # a weight of some 2^-200 of the largest
+        k[base + hi - 250, 0] = -13 * q[b, 0, 0]
+    cache.k.copy_(k)
+    cache.v.copy_(v)
+    want, _ = ref.decode(q, k.double(), v.double(), slot, lens, pos, window, 4, D ** -0.5)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = run(cache, q, lens, pos, hi, window, 4, D ** -0.5, err).cpu()
+    assert int(err) == 0
+    plain = torch.isfinite(want)
+    assert want[:, 0, 0, 31].eq(inf).all() and want[:, R - 1, 0, 20].isnan().all()
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got.double()[~plain].nan_to_num(0.0, inf, -inf),
+                       want[~plain].nan_to_num(0.0, inf, -inf))
+    v[~torch.isfinite(v)] = 0
+    want, mass = ref.decode(q, k.double(), v.double(), slot, lens, pos, window, 4, D ** -0.5)
+    ref.check_output(got.masked_fill(~plain, 0), want.masked_fill(~plain, 0), mass, weight_bits=16)
+
+
 def test_calls_on_a_stream_of_their_own():
     """Output and workspace that a call makes belong to the stream it is given,
     as a Stream or a handle; two calls on two streams do not disturb each other."""
