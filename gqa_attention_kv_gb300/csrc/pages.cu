@@ -231,42 +231,51 @@ __global__ void __launch_bounds__(kScanThreads) pages_fork_kernel(const ForkPara
         f.dst[j] = max(page, -1);
         return;
     }
-    int need = 0;
+    // The requests of a batch that want a page: what they copy, and the entry it becomes
+    __shared__ int copied[kScanThreads], tokens[kScanThreads];
+    __shared__ int32_t *entry[kScanThreads];
+    int moves = 0, tile = 0;  // pages below `tile` are taken
+    bool lacking = false;
     for (int base = 0; base < p.n; base += kScanThreads) {
         const int i = base + threadIdx.x;
         ForkRow f = {};
         if (i < p.n) f = fork_row(p, i, false);
         const bool some = f.dst != nullptr && f.part_page >= 0;
-        int sum;
-        const int at = need + block_scan(some ? 1 : 0, sum);
-        if (some) {  // the request stands in for the page it will get
-            p.moves[3 * at] = f.part_page;
-            p.moves[3 * at + 1] = i;
-            p.moves[3 * at + 2] = f.part;
+        int need;
+        const int at = block_scan(some ? 1 : 0, need);
+        if (some) {
+            copied[at] = f.part_page;
+            tokens[at] = f.part;
+            entry[at] = f.dst + f.full;
         }
-        need += sum;
-    }
-    __syncthreads();
-    int given = 0;
-    for (int base = 0; base < p.num_pages && given < need; base += kTile) {
-        uint32_t bits = free_bits<kPer>(p.refs, base, p.num_pages);
-        int sum;
-        int at = given + block_scan(__popc(bits), sum);
-        for (; bits != 0 && at < need; bits &= bits - 1, ++at) {
-            const int page = base + kPer * threadIdx.x + __ffs(bits) - 1, i = p.moves[3 * at + 1];
-            p.table[(int64_t)p.dst_rows[i] * p.max_blocks + p.seq_lens[i] / p.block_size] = page;
-            p.moves[3 * at + 1] = page;
-            p.refs[page] = 1;
+        int given = 0;
+        for (; tile < p.num_pages && given < need; tile += kTile) {
+            uint32_t bits = free_bits<kPer>(p.refs, tile, p.num_pages);
+            int sum;
+            int to = given + block_scan(__popc(bits), sum);
+            for (; bits != 0 && to < need; bits &= bits - 1, ++to) {
+                const int page = tile + kPer * threadIdx.x + __ffs(bits) - 1;
+                int32_t *move = p.moves + 3 * (moves + to);
+                move[0] = copied[to];
+                move[1] = page;
+                move[2] = tokens[to];
+                *entry[to] = page;
+                p.refs[page] = 1;
+            }
+            given += sum;
+            if (given >= need) break;  // the tile may hold pages for the next batch
         }
-        given += sum;
+        given = min(given, need);
+        __syncthreads();
+        for (int to = given + threadIdx.x; to < need; to += kScanThreads) *entry[to] = -1;
+        moves += given;
+        lacking |= given < need;
+        __syncthreads();
     }
-    given = min(given, need);
-    if (given < need && threadIdx.x == 0) report_error(p.err, ATTN_ERR_PAGES);
-    for (int at = given + threadIdx.x; at < need; at += kScanThreads) {
-        const int i = p.moves[3 * at + 1];
-        p.table[(int64_t)p.dst_rows[i] * p.max_blocks + p.seq_lens[i] / p.block_size] = -1;
+    if (threadIdx.x == 0) {
+        *p.n_moves = moves;
+        if (lacking) report_error(p.err, ATTN_ERR_PAGES);
     }
-    if (threadIdx.x == 0) *p.n_moves = given;
 }
 
 // One block: counts the pages in use (U), pairs pages at or above U with free

@@ -139,6 +139,32 @@ def test_fork_without_free_pages_and_with_bad_rows():
     assert int(count) == 0
 
 
+@pytest.mark.parametrize("parents,kids,free", [(3, 2, 1), (3, 2, 0), (900, 3, 2000), (900, 3, 1024),
+                                               (900, 3, 1)])
+def test_fork_that_runs_out_of_pages(parents, kids, free):
+    """The first requests get the pages that are left, of more than one batch too;
+    the moves behind *n_moves stay as they were."""
+    n, bs = parents * kids, 16
+    table = torch.full((parents + n, 2), -1, dtype=torch.int32)
+    table[:parents, 0] = torch.randperm(parents + free, generator=gen(free))[:parents].int()
+    refs = torch.zeros(parents + free, dtype=torch.int32)
+    refs[table[:parents, 0].long()] = 1
+    t, r, err = table.to(DEV), refs.to(DEV), error()
+    src = [i // kids for i in range(n)]
+    dst = [parents + i for i in range(n)]
+    lens = [1 + i % 14 if i % 5 else 16 * (i % 2) for i in range(n)]  # some without a partial page
+    moves = torch.full((n + 1, 3), -7, dtype=torch.int32, device=DEV)
+    count = error()
+    gq.attn_pages_fork(t, r, dev(src), dev(dst), dev(lens), bs, moves, count, err=err)
+    want, ok = ref.pages_fork(table, refs, src, dst, lens, bs)
+    same(table, t)
+    same(refs, r)
+    assert not ok and int(err) == gq.ATTN_ERR_PAGES and len(want) == free
+    assert int(count) == free
+    assert [tuple(m) for m in moves[:free].tolist()] == want
+    assert (moves[free:] == -7).all()
+
+
 @pytest.mark.parametrize("rows,width,pages", [(1, 1, 1), (6, 30, 400), (50, 200, 9001),
                                               (64, 3000 // 64, 70001)])
 def test_compact(rows, width, pages):
