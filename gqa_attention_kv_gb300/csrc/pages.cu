@@ -30,6 +30,9 @@ constexpr int kScanThreads = 1024;
 constexpr int kPer = 16, kTile = kScanThreads * kPer;
 constexpr int kListPer = 4, kListTile = kScanThreads * kListPer;
 constexpr int kListed = 2 * kListTile;
+// A fork's entries up to which one cluster copies them (18 a thread): free, fork and copy of
+// 48 rows of 94 entries take 20.2 us so, 22.5 with a launch of their own, a thread each.
+constexpr int kForkBlocks = 8, kForkEntries = 16 * kForkBlocks * kScanThreads;
 
 // Exclusive prefix of v over the block, and the block's sum in `sum`.  All
 // kScanThreads threads take part.
@@ -74,6 +77,12 @@ __device__ __forceinline__ uint32_t free_bits(const int32_t *refs, int base, int
             if (p + i < num_pages && refs[p + i] <= 0) bits |= 1u << i;
     }
     return bits;
+}
+
+// A barrier of the cluster's threads.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\t"
+                 "barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // The bits of those pages that are in the pool.
@@ -174,20 +183,18 @@ struct ForkParams {
     int32_t *refs;
     int num_pages;
     int32_t *moves, *n_moves, *err;
-    int per_row;
+    bool share;  // the entries have not been copied yet
 };
 
 struct ForkRow {
     int32_t *src, *dst;  // nullptr: a row outside the table
     int full, part;      // full pages, tokens of the partial one
-    int part_page;       // its page, -1 if there is none to copy
 };
 
 __device__ __forceinline__ ForkRow fork_row(const ForkParams &p, int i, bool report) {
     ForkRow f = {};
     const int s = p.src_rows[i], d = p.dst_rows[i];
     int len = p.seq_lens[i];
-    f.part_page = -1;
     bool bad = s < 0 || s >= p.table_rows || d < 0 || d >= p.table_rows || s == d;
     if (!bad) {
         f.src = p.table + (int64_t)s * p.max_blocks;
@@ -196,55 +203,73 @@ __device__ __forceinline__ ForkRow fork_row(const ForkParams &p, int i, bool rep
         if (len < 0 || len > cap) bad = true, len = len < 0 ? 0 : (int)cap;
         f.full = len / p.block_size;
         f.part = len - f.full * p.block_size;
-        if (f.part > 0) {
-            f.part_page = f.src[f.full];
-            if (f.part_page >= p.num_pages) bad = true, f.part_page = -1;
-        }
     }
     if (bad && report) report_error(p.err, ATTN_ERR_BOUNDS);
     return f;
 }
 
-// Block 0 hands out the pages for the partial last pages; the others copy the
-// rows and count the shared pages.  They do not meet: a free page stays free
-// under the counting (it only raises counts above 0), and the entry of a
-// copied page is written by block 0 alone.
-__global__ void __launch_bounds__(kScanThreads) pages_fork_kernel(const ForkParams p) {
+// The source's page j, -1 if there is none.  A free page is none of the source's: reported
+// like one outside the pool.
+__device__ __forceinline__ int fork_page(const ForkParams &p, const ForkRow &f, int j) {
+    const int page = f.src[j];
+    if (page < 0) return -1;
+    if (page < p.num_pages && p.refs[page] > 0) return page;
+    report_error(p.err, ATTN_ERR_BOUNDS);
+    return -1;
+}
+
+// Entry j of request i's new row: a full page is shared, the partial last one named for
+// the copy.
+__device__ __forceinline__ void fork_entry(const ForkParams &p, int i, int j) {
+    const ForkRow f = fork_row(p, i, j == 0);
+    if (f.dst == nullptr) return;
+    const int page = j < f.full + (f.part > 0 ? 1 : 0) ? fork_page(p, f, j) : -1;
+    if (page >= 0 && j < f.full) atomicAdd(p.refs + page, 1);
+    f.dst[j] = page;
+}
+
+// The entries of many or long rows, a thread each, before the kernel below.
+__global__ void __launch_bounds__(256) pages_share_kernel(const ForkParams p, int per_row) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int i = blockIdx.x / per_row, j = (blockIdx.x - i * per_row) * 256 + threadIdx.x;
+    if (j < p.max_blocks) fork_entry(p, i, j);
+}
+
+// A cluster: block 0 hands out the pages for the partial last pages, the others copy the
+// entries and count the shared pages.  Block 0 writes when they are done, so what is a free
+// page is what was one before the call; until then it has read the first 1,024 requests.
+__global__ void __cluster_dims__(kForkBlocks, 1, 1) __launch_bounds__(kScanThreads)
+    pages_fork_kernel(const ForkParams p) {
     pdl_wait();
     pdl_launch_dependents();
     if (blockIdx.x > 0) {
-        const int i = (blockIdx.x - 1) / p.per_row, part = (blockIdx.x - 1) - i * p.per_row;
-        const ForkRow f = fork_row(p, i, part == 0 && threadIdx.x == 0);
-        const int j = part * kScanThreads + threadIdx.x;
-        if (f.dst == nullptr || j >= p.max_blocks) return;
-        int page = -1;
-        if (j < f.full) {
-            page = f.src[j];
-            if (page >= 0 && (page >= p.num_pages || p.refs[page] <= 0)) {
-                report_error(p.err, ATTN_ERR_BOUNDS);
-                page = -1;
+        if (p.share)
+            for (int at = (blockIdx.x - 1) * kScanThreads + threadIdx.x; at < p.n * p.max_blocks;
+                 at += (kForkBlocks - 1) * kScanThreads) {
+                const int i = at / p.max_blocks;
+                fork_entry(p, i, at - i * p.max_blocks);
             }
-            if (page >= 0) atomicAdd(p.refs + page, 1);
-        } else if (j == f.full && f.part_page >= 0) {
-            return;
-        }
-        f.dst[j] = max(page, -1);
+        cluster_sync();
         return;
     }
     // The requests of a batch that want a page: what they copy, and the entry it becomes
     __shared__ int copied[kScanThreads], tokens[kScanThreads];
     __shared__ int32_t *entry[kScanThreads];
     int moves = 0, tile = 0;  // pages below `tile` are taken
-    bool lacking = false;
+    bool lacking = false, shared = false;
     for (int base = 0; base < p.n; base += kScanThreads) {
         const int i = base + threadIdx.x;
         ForkRow f = {};
         if (i < p.n) f = fork_row(p, i, false);
-        const bool some = f.dst != nullptr && f.part_page >= 0;
+        int page = -1;
+        if (f.dst != nullptr && f.part > 0)  // (the others have left it in the entry, too)
+            page = base == 0 ? fork_page(p, f, f.full) : f.dst[f.full];
+        const bool some = page >= 0;
         int need;
         const int at = block_scan(some ? 1 : 0, need);
         if (some) {
-            copied[at] = f.part_page;
+            copied[at] = page;
             tokens[at] = f.part;
             entry[at] = f.dst + f.full;
         }
@@ -253,6 +278,8 @@ __global__ void __launch_bounds__(kScanThreads) pages_fork_kernel(const ForkPara
             uint32_t bits = free_bits<kPer>(p.refs, tile, p.num_pages);
             int sum;
             int to = given + block_scan(__popc(bits), sum);
+            if (!shared) cluster_sync();
+            shared = true;
             for (; bits != 0 && to < need; bits &= bits - 1, ++to) {
                 const int page = tile + kPer * threadIdx.x + __ffs(bits) - 1;
                 int32_t *move = p.moves + 3 * (moves + to);
@@ -266,12 +293,15 @@ __global__ void __launch_bounds__(kScanThreads) pages_fork_kernel(const ForkPara
             if (given >= need) break;  // the tile may hold pages for the next batch
         }
         given = min(given, need);
+        if (!shared) cluster_sync();
+        shared = true;
         __syncthreads();
         for (int to = given + threadIdx.x; to < need; to += kScanThreads) *entry[to] = -1;
         moves += given;
         lacking |= given < need;
         __syncthreads();
     }
+    if (!shared) cluster_sync();  // n is 0
     if (threadIdx.x == 0) {
         *p.n_moves = moves;
         if (lacking) report_error(p.err, ATTN_ERR_PAGES);
@@ -443,13 +473,18 @@ int launch_pages_fork(int32_t *block_table, int max_blocks, int table_rows,
                       const int32_t *src_rows, const int32_t *dst_rows, const int32_t *seq_lens,
                       int n, int block_size, int32_t *refs, int num_pages, int32_t *moves,
                       int32_t *n_moves, int32_t *err, cudaStream_t stream) {
-    ForkParams p = {block_table, max_blocks, table_rows, src_rows, dst_rows, seq_lens,
-                    n,           block_size, refs,       num_pages, moves,   n_moves,
-                    err,         (max_blocks + kScanThreads - 1) / kScanThreads};
-    const int64_t blocks = 1 + (int64_t)n * p.per_row;
-    if (blocks >= (int64_t(1) << 31)) return ATTN_ERR_SHAPE;
-    return status(launch_pdl(pages_fork_kernel, dim3((unsigned)blocks), dim3(kScanThreads), 0,
-                             stream, p));
+    ForkParams p = {block_table, max_blocks, table_rows, src_rows, dst_rows, seq_lens, n,
+                    block_size,  refs,       num_pages,  moves,    n_moves,  err,
+                    (int64_t)n * max_blocks <= kForkEntries};
+    if (!p.share) {
+        const int per_row = (max_blocks + 255) / 256;
+        if ((int64_t)n * per_row >= (int64_t(1) << 31)) return ATTN_ERR_SHAPE;
+        const int rc = status(launch_pdl(pages_share_kernel, dim3((unsigned)(n * per_row)),
+                                         dim3(256), 0, stream, p, per_row));
+        if (rc != ATTN_OK) return rc;
+    }
+    return status(launch_pdl(pages_fork_kernel, dim3(kForkBlocks), dim3(kScanThreads), 0, stream,
+                             p));
 }
 
 size_t pages_workspace(int num_pages) { return (size_t)num_pages * sizeof(int32_t); }

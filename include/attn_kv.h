@@ -505,8 +505,8 @@ int attn_prefill_sinks(const void *q, const void *k, const void *v, int batch, i
  *                rows to copy), n_moves (int32, device) of them; entries past
  *                *n_moves are left as they were
  * Free pages are handed out lowest first, so results do not depend on timing.
- * A row, length or page outside its array skips what it names and stores
- * ATTN_ERR_BOUNDS in *err_word.  refs and workspace must be 16-byte aligned.
+ * A row, length or page outside its array, or a free page where one in use has to
+ * be named, skips what it names and stores ATTN_ERR_BOUNDS in *err_word.  refs and workspace must be 16-byte aligned.
  * Calls on one table or pool must be ordered (one stream, or events).  All may
  * be captured into graphs.  Pages named by several entries are shared: writing
  * one of them (an append that goes back into full pages) changes every row that

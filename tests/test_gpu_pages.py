@@ -165,6 +165,39 @@ def test_fork_that_runs_out_of_pages(parents, kids, free):
     assert (moves[free:] == -7).all()
 
 
+@pytest.mark.parametrize("n,width", [(1, 2), (3, 3), (1200, 3), (3, 60000)])
+def test_fork_of_rows_that_name_free_pages(n, width):
+    """A free page in the source, as a full page or the partial last one, is reported and
+    forked as none, also where the call itself hands that page out."""
+    pages = 2 * n + 6
+    table = torch.full((2 * n + 1, width), -1, dtype=torch.int32)
+    refs = torch.zeros(pages, dtype=torch.int32)
+    for i in range(n):         # page 2 i: in use; 2 i + 1: free, though named
+        table[i, :2] = torch.tensor([2 * i, 2 * i + 1])
+        refs[2 * i] = 1
+    lens = [16 + 5 if i % 3 == 0 else 32 if i % 3 == 1 else 5 for i in range(n)]
+    t, r, err = table.to(DEV), refs.to(DEV), error()
+    moves, count = torch.full((n, 3), -7, dtype=torch.int32, device=DEV), error()
+    gq.attn_pages_fork(t, r, dev(list(range(n))), dev(list(range(n, 2 * n))), dev(lens), 16, moves,
+                       count, err=err)
+    free = (refs == 0).nonzero()[:, 0].tolist()
+    want = []
+    for i in range(n):
+        if i % 3 < 2:          # page 2 i shared, none behind it
+            table[n + i, 0] = 2 * i
+            refs[2 * i] += 1
+        else:                  # five tokens of page 2 i copied
+            page = free.pop(0)
+            table[n + i, 0] = page
+            refs[page] = 1
+            want.append((2 * i, page, 5))
+    same(table, t)
+    same(refs, r)
+    assert int(err) == gq.ATTN_ERR_BOUNDS and int(count) == len(want)
+    assert [tuple(m) for m in moves[:len(want)].tolist()] == want
+    assert (moves[len(want):] == -7).all()
+
+
 @pytest.mark.parametrize("rows,width,pages", [(1, 1, 1), (6, 30, 400), (50, 200, 9001),
                                               (64, 3000 // 64, 70001)])
 def test_compact(rows, width, pages):
