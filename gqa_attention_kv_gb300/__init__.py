@@ -204,7 +204,6 @@ class KVCache:
                  dtype=ATTN_KV_BF16, k_ref=None, layout=ATTN_LAYOUT_BSHD, k_scale=None,
                  v_scale=None, scale_block=0):
         self.kind, self.k, self.v = int(kind), k, v
-        self._shape = k.shape  # what layers of one launch are compared by
         self.slots_per_seq = int(slots_per_seq)
         self.block_table = block_table
         self.block_size = int(block_size)
@@ -220,6 +219,49 @@ class KVCache:
                 if t.shape != shape or t.dtype is not torch.float32 or not t.is_contiguous():
                     raise AttnError(ATTN_ERR_SHAPE, f"KVCache: k_scale and v_scale are contiguous "
                                                     f"float32 tensors of shape {shape}")
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        object.__setattr__(self, "_usable", None)  # looked at again by the next call
+
+    def _want_usable(self, where, device):
+        """Refuses k, v and scales that a kernel would read or write out of their
+        place: of another type, size, order or device.  Returns what holds until
+        a field is set or a tensor is put elsewhere: (device, addresses, bytes of
+        k and v, their shape, what a page copy reads of the C structure)."""
+        k, v, ks, vs = self.k, self.v, self.k_scale, self.v_scale
+        store = torch.bfloat16 if self.dtype == ATTN_KV_BF16 else \
+            torch.int8 if self.dtype == ATTN_KV_INT8_SCALED else \
+            torch.float8_e4m3fn if k.dtype is torch.float8_e4m3fn else torch.uint8
+        _want(where, device, store, k, v)
+        if k.shape != v.shape or k.dim() != (4 if self.layout == ATTN_LAYOUT_BHSD else 3):
+            raise AttnError(ATTN_ERR_SHAPE, f"{where}: k and v are of one shape, [num_slots, "
+                                            "n_kv_heads, head_dim] slot-major, of four "
+                                            "dimensions head-major")
+        scales = ()
+        if self.dtype in (ATTN_KV_FP8_E4M3_SCALED, ATTN_KV_INT8_SCALED):
+            if ks is None or vs is None:
+                raise AttnError(ATTN_ERR_NULL, f"{where}: a scaled cache without its scales")
+            _want(where, device, torch.float32, ks, vs)
+            shape = (self.num_slots // max(1, self.scale_block), self.n_kv_heads)
+            if ks.shape != shape or vs.shape != shape:
+                raise AttnError(ATTN_ERR_SHAPE, f"{where}: k_scale and v_scale are {shape}")
+            scales = (ks.data_ptr(), vs.data_ptr())
+        known = (device, k.data_ptr(), v.data_ptr(), k.nbytes, scales, tuple(k.shape),
+                 _PACK(self.kind, k.data_ptr(), v.data_ptr(), self.num_slots, 0, 0,
+                       self.block_size, 0, self.dtype, 0, self.layout,
+                       *(scales or (0, 0)), self.scale_block))
+        object.__setattr__(self, "_usable", known)
+        return known
+
+    def _known(self, where, device):
+        """_want_usable, if it has not been asked since the last change."""
+        u, k, v = self._usable, self.k, self.v
+        if u is None or u[0] != device or u[1] != k.data_ptr() or u[2] != v.data_ptr() or \
+                u[3] != k.nbytes or u[3] != v.nbytes or \
+                (u[4] and u[4] != (self.k_scale.data_ptr(), self.v_scale.data_ptr())):
+            u = self._want_usable(where, device)
+        return u
 
     @property
     def n_kv_heads(self):
@@ -520,18 +562,15 @@ def attn_pages_copy(caches, moves, n_moves, err=None, stream=None):
     if isinstance(caches, KVCache):
         caches = [caches]
     _want_moves("attn_pages_copy", moves, n_moves)
-    Hkv, D, slots, shape = 1, 128, 0, None
-    if caches:
-        first = caches[0]
-        Hkv, D, slots, shape = first.n_kv_heads, first.head_dim, first.num_slots, first._shape
-    packed = []
+    device, shape, packed = _device(), None, []
     for c in caches:
-        if c._shape != shape:
+        known = c._known("attn_pages_copy", device)
+        if shape is None:
+            shape = known[5]
+        elif known[5] != shape:
             raise AttnError(ATTN_ERR_SHAPE, "attn_pages_copy: caches of different shapes")
-        packed.append(_PACK(c.kind, c.k.data_ptr(), c.v.data_ptr(), slots, 0, 0,  # what copying reads
-                            c.block_size, 0, c.dtype, 0, c.layout,
-                            0 if c.k_scale is None else c.k_scale.data_ptr(),
-                            0 if c.v_scale is None else c.v_scale.data_ptr(), c.scale_block))
+        packed.append(known[6])
+    Hkv, D = (shape[1], shape[-1]) if shape else (1, 128)
     rc = lib().attn_pages_copy(b"".join(packed), len(packed), Hkv, D, _ptr(moves), _ptr(n_moves),
                                moves.shape[0], _ptr(err), _stream(stream))
     _check(rc, "attn_pages_copy")

@@ -188,3 +188,71 @@ def test_wrappers_refuse_what_the_kernels_would_misread():
         with pytest.raises(gq.AttnError):
             gq.KVCache(gq.LINEAR, codes, codes, slots_per_seq=64, dtype=I8, k_scale=scale,
                        v_scale=other, scale_block=16)
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The wrappers over CPU tensors, with a library that notes what reaches it."""
+    import torch
+
+    class Library:
+        def __init__(self):
+            self.names = []
+
+        def __getattr__(self, name):
+            return lambda *args: self.names.append(name) or 0
+
+    fake = Library()
+    monkeypatch.setattr(gq, "lib", lambda: fake)
+    monkeypatch.setattr(gq, "attn_status_string", lambda status: "")
+    monkeypatch.setattr(gq, "_device", lambda: torch.zeros(0).get_device())  # -1: the CPU's
+    return fake.names
+
+
+def paged_layer(pages=8, H=2, D=64, dtype=gq.ATTN_KV_BF16):
+    import torch
+
+    store = {gq.ATTN_KV_BF16: torch.bfloat16, I8: torch.int8}.get(dtype, torch.uint8)
+    more = {}
+    if dtype in (E4, I8):
+        more = dict(scale_block=16, k_scale=torch.zeros(pages, H), v_scale=torch.zeros(pages, H))
+    return gq.KVCache(gq.PAGED, torch.zeros(pages * 16, H, D, dtype=store),
+                      torch.zeros(pages * 16, H, D, dtype=store), block_size=16,
+                      block_table=torch.zeros(2, 4, dtype=torch.int32), dtype=dtype, **more)
+
+
+@pytest.mark.parametrize("dtype", [gq.ATTN_KV_BF16, gq.ATTN_KV_FP8_E4M3, E4, I8])
+@pytest.mark.parametrize("name", ["k", "v"])
+def test_page_copies_look_at_tensors_that_were_replaced(calls, dtype, name):
+    """k and v of a layer may be replaced; the others' place then no longer tells theirs."""
+    import torch
+
+    moves, count = torch.zeros(3, 3, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    layers = [paged_layer(dtype=dtype) for _ in range(3)]
+    copy = lambda: gq.attn_pages_copy(layers, moves, count, stream=0)  # noqa: E731
+    copy()
+    for at in (0, 2):                      # the first layer's larger, a later one's smaller
+        old = getattr(layers[at], name)
+        new = torch.zeros(old.shape[0] * 2 if at == 0 else 16, *old.shape[1:], dtype=old.dtype)
+        setattr(layers[at], name, new)
+        with pytest.raises(gq.AttnError):
+            copy()
+        setattr(layers[at], name, old.clone())
+        copy()
+        getattr(layers[at], name).data = new   # the tensor itself made another
+        with pytest.raises(gq.AttnError):
+            copy()
+        setattr(layers[at], name, old)
+    for bad in (torch.zeros(128, 2, 128, dtype=old.dtype)[..., :64],
+                torch.zeros(128, 2, 64, dtype=torch.float32), old.view(128, 1, 128)):
+        setattr(layers[1], name, bad)
+        with pytest.raises(gq.AttnError):
+            copy()
+    setattr(layers[1], name, old)
+    if dtype in (E4, I8):
+        layers[1].k_scale = torch.zeros(4, 2)
+        with pytest.raises(gq.AttnError):
+            copy()
+        layers[1].k_scale = torch.zeros(8, 2)
+    copy()
+    assert calls == ["attn_pages_copy"] * 4
