@@ -33,6 +33,8 @@ ATTN_KV_BF16, ATTN_KV_FP8_E4M3 = 0, 1  # cache element types (attn_kv_dtype)
 ATTN_KV_FP8_E4M3_SCALED, ATTN_KV_INT8_SCALED = 2, 3
 ATTN_LAYOUT_BSHD, ATTN_LAYOUT_BHSD = 0, 1  # cache layouts (attn_kv_layout)
 
+_BYTES = (torch.uint8, torch.int8, torch.float8_e4m3fn)  # what may hold 8-bit codes
+
 _lock = threading.Lock()
 _lib = None
 
@@ -231,8 +233,7 @@ class KVCache:
         k and v, their shape, what a page copy reads of the C structure)."""
         k, v, ks, vs = self.k, self.v, self.k_scale, self.v_scale
         store = torch.bfloat16 if self.dtype == ATTN_KV_BF16 else \
-            torch.int8 if self.dtype == ATTN_KV_INT8_SCALED else \
-            torch.float8_e4m3fn if k.dtype is torch.float8_e4m3fn else torch.uint8
+            k.dtype if k.dtype in _BYTES else torch.uint8
         _want(where, device, store, k, v)
         if k.shape != v.shape or k.dim() != (4 if self.layout == ATTN_LAYOUT_BHSD else 3):
             raise AttnError(ATTN_ERR_SHAPE, f"{where}: k and v are of one shape, [num_slots, "
