@@ -31,8 +31,10 @@ ATTN_DECODE_TABLES_EARLY = 1  # attn_decode_append flags (include/attn_kv.h)
 ATTN_DECODE_CACHE_EARLY = 2
 ATTN_KV_BF16, ATTN_KV_FP8_E4M3 = 0, 1  # cache element types (attn_kv_dtype)
 ATTN_KV_FP8_E4M3_SCALED, ATTN_KV_INT8_SCALED = 2, 3
+_SCALED = (ATTN_KV_FP8_E4M3_SCALED, ATTN_KV_INT8_SCALED)
 ATTN_LAYOUT_BSHD, ATTN_LAYOUT_BHSD = 0, 1  # cache layouts (attn_kv_layout)
 
+_BF16, _I32, _I64 = torch.bfloat16, torch.int32, torch.int64
 _BYTES = (torch.uint8, torch.int8, torch.float8_e4m3fn)  # what may hold 8-bit codes
 
 _lock = threading.Lock()
@@ -214,7 +216,7 @@ class KVCache:
         self.layout = int(layout)
         self.k_scale, self.v_scale = k_scale, v_scale
         self.scale_block = int(scale_block)
-        if self.dtype in (ATTN_KV_FP8_E4M3_SCALED, ATTN_KV_INT8_SCALED) and \
+        if self.dtype in _SCALED and \
                 isinstance(k_scale, torch.Tensor) and self.scale_block > 0:
             shape = (self.num_slots // self.scale_block, self.n_kv_heads)
             for t in (k_scale, v_scale):
@@ -225,44 +227,66 @@ class KVCache:
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
         object.__setattr__(self, "_usable", None)  # looked at again by the next call
+        object.__setattr__(self, "_table", None)
 
     def _want_usable(self, where, device):
-        """Refuses k, v and scales that a kernel would read or write out of their
-        place: of another type, size, order or device.  Returns what holds until
-        a field is set or a tensor is put elsewhere: (device, addresses, bytes of
-        k and v, their shape, what a page copy reads of the C structure)."""
-        k, v, ks, vs = self.k, self.v, self.k_scale, self.v_scale
-        store = torch.bfloat16 if self.dtype == ATTN_KV_BF16 else \
-            k.dtype if k.dtype in _BYTES else torch.uint8
+        """Refuses k, v, scales and reference that a kernel would read or write out
+        of their place: of another type, size, order or device.  Returns what holds
+        until a field is set or a tensor is put elsewhere: (device, addresses of k
+        and v, their bytes, addresses of the scales, of k_ref, the shape of k and v,
+        the bytes of the C structure without the block table)."""
+        k, v, ks, vs, ref = self.k, self.v, self.k_scale, self.v_scale, self.k_ref
+        store = _BF16 if self.dtype == ATTN_KV_BF16 else k.dtype if k.dtype in _BYTES else \
+            torch.uint8
         _want(where, device, store, k, v)
         if k.shape != v.shape or k.dim() != (4 if self.layout == ATTN_LAYOUT_BHSD else 3):
             raise AttnError(ATTN_ERR_SHAPE, f"{where}: k and v are of one shape, [num_slots, "
                                             "n_kv_heads, head_dim] slot-major, of four "
                                             "dimensions head-major")
         scales = ()
-        if self.dtype in (ATTN_KV_FP8_E4M3_SCALED, ATTN_KV_INT8_SCALED):
+        if self.dtype in _SCALED:
             if ks is None or vs is None:
                 raise AttnError(ATTN_ERR_NULL, f"{where}: a scaled cache without its scales")
-            _want(where, device, torch.float32, ks, vs)
+            _want(where, device, torch.float32, ks, vs, *(() if ref is None else (ref,)))
             shape = (self.num_slots // max(1, self.scale_block), self.n_kv_heads)
-            if ks.shape != shape or vs.shape != shape:
-                raise AttnError(ATTN_ERR_SHAPE, f"{where}: k_scale and v_scale are {shape}")
+            if ks.shape != shape or vs.shape != shape or \
+                    (ref is not None and ref.numel() != self.n_kv_heads * self.head_dim):
+                raise AttnError(ATTN_ERR_SHAPE, f"{where}: k_scale and v_scale are {shape}, "
+                                                "k_ref is [n_kv_heads, head_dim]")
             scales = (ks.data_ptr(), vs.data_ptr())
-        known = (device, k.data_ptr(), v.data_ptr(), k.nbytes, scales, tuple(k.shape),
-                 _PACK(self.kind, k.data_ptr(), v.data_ptr(), self.num_slots, 0, 0,
-                       self.block_size, 0, self.dtype, 0, self.layout,
+        at = 0 if ref is None else ref.data_ptr()
+        known = (device, k.data_ptr(), v.data_ptr(), k.nbytes, scales, at, tuple(k.shape),
+                 _PACK(self.kind, k.data_ptr(), v.data_ptr(), self.num_slots, self.slots_per_seq,
+                       0, self.block_size, 0, self.dtype, at, self.layout,
                        *(scales or (0, 0)), self.scale_block))
         object.__setattr__(self, "_usable", known)
         return known
 
     def _known(self, where, device):
         """_want_usable, if it has not been asked since the last change."""
-        u, k, v = self._usable, self.k, self.v
+        u, k, v, ref = self._usable, self.k, self.v, self.k_ref
         if u is None or u[0] != device or u[1] != k.data_ptr() or u[2] != v.data_ptr() or \
                 u[3] != k.nbytes or u[3] != v.nbytes or \
-                (u[4] and u[4] != (self.k_scale.data_ptr(), self.v_scale.data_ptr())):
+                (u[4] and u[4] != (self.k_scale.data_ptr(), self.v_scale.data_ptr())) or \
+                (ref is not None and u[5] != ref.data_ptr()):
             u = self._want_usable(where, device)
         return u
+
+    def _with_table(self, where, device, batch):
+        """The bytes of the C structure, with a block table that has `batch` rows."""
+        u, bt, t = self._known(where, device), self.block_table, self._table
+        if self.kind != PAGED or bt is None:
+            return u[7]
+        if t is None or t[0] is not u or t[1] != bt.data_ptr() or t[2] != bt.nbytes:
+            _want(where, device, _I32, bt)
+            if bt.dim() != 2:
+                raise AttnError(ATTN_ERR_SHAPE, f"{where}: block_table is [batch, "
+                                                "max_blocks_per_seq]")
+            t = (u, bt.data_ptr(), bt.nbytes, bt.shape[0], self.packed())
+            object.__setattr__(self, "_table", t)
+        if t[3] < batch:
+            raise AttnError(ATTN_ERR_SHAPE, f"{where}: block_table has fewer rows than {batch}")
+        return t[4]
 
     @property
     def n_kv_heads(self):
@@ -292,11 +316,52 @@ class KVCache:
         return _Cache.from_buffer_copy(self.packed())
 
 
+def _want_new_rows(where, cache, k_new, v_new, slots, n):
+    """The n rows of an append to a scaled cache; returns its C structure's bytes."""
+    device = _device()
+    u = cache._known(where, device)
+    if not (k_new.dtype is v_new.dtype is _BF16 and slots.dtype is _I64 and
+            k_new.get_device() == v_new.get_device() == slots.get_device() == device and
+            k_new.is_contiguous() and v_new.is_contiguous() and slots.is_contiguous()):
+        _want(where, device, _BF16, k_new, v_new)
+        _want(where, device, _I64, slots)
+    shape, of_k, of_v = u[6], k_new.shape, v_new.shape
+    if (of_k != of_v or of_k != (n, shape[1], shape[-1])) and \
+            (min(k_new.numel(), v_new.numel()) < n * shape[1] * shape[-1] or
+             of_k[-1] != shape[-1] or of_v[-1] != shape[-1]) or slots.numel() < n:
+        raise AttnError(ATTN_ERR_SHAPE, f"{where}: k_new and v_new are [n, {shape[1]}, "
+                                        f"{shape[-1]}], slot_mapping [n]")
+    return u[7]
+
+
+def _want_decode(where, cache, q, out, seq_lens, positions, workspace):
+    """What a decode over a scaled cache, or under a window with sinks, reads and
+    writes; returns the cache's C structure's bytes."""
+    device = _device()
+    B, R, _, D = shape = q.shape
+    c = cache._with_table(where, device, B)
+    if not (q.dtype is out.dtype is _BF16 and seq_lens.dtype is positions.dtype is _I32 and
+            q.get_device() == out.get_device() == seq_lens.get_device() ==
+            positions.get_device() == workspace.get_device() == device and
+            q.is_contiguous() and out.is_contiguous() and seq_lens.is_contiguous() and
+            positions.is_contiguous() and workspace.is_contiguous()):
+        _want(where, device, _BF16, q, out)
+        _want(where, device, _I32, seq_lens, positions)
+        _want(where, device, workspace.dtype, workspace)
+    if seq_lens.numel() < B or positions.numel() < B * R or D != cache.head_dim or \
+            (out is not q and out.shape != shape and out.numel() < q.numel()):
+        raise AttnError(ATTN_ERR_SHAPE, f"{where}: q and out are [B, R, n_q_heads, "
+                                        f"{cache.head_dim}], seq_lens [B], positions [B * R]")
+    return c
+
+
 def attn_kv_append(k_new, v_new, slot_mapping, cache: KVCache, err=None, stream=None):
     """cache.k[slot_mapping[i]] = k_new[i] (same for v); slot_mapping int64 [n]."""
-    shape = cache.k.shape
-    rc = lib().attn_kv_append(_ptr(k_new), _ptr(v_new), _ptr(slot_mapping),
-                              slot_mapping.shape[0], cache.packed(), shape[1], shape[-1],
+    n, shape = slot_mapping.shape[0], cache.k.shape
+    c = _want_new_rows("attn_kv_append", cache, k_new, v_new, slot_mapping, n) \
+        if cache.dtype in _SCALED else cache.packed()
+    rc = lib().attn_kv_append(_ptr(k_new), _ptr(v_new), _ptr(slot_mapping), n, c, shape[1],
+                              shape[-1],
                               _ptr(err), _stream(stream))
     _check(rc, "attn_kv_append")
 
@@ -351,7 +416,8 @@ def attn_decode(q, cache: KVCache, seq_lens, positions, max_seq_len, window, sca
         need = attn_decode_workspace_size(cache, B, R, Hq, max_seq_len, window)
         if need > 0:
             workspace = _made(_zeroed, q, stream, need)
-    c = cache.packed()
+    c = _want_decode("attn_decode", cache, q, out, seq_lens, positions, workspace) \
+        if cache.dtype in _SCALED and workspace is not None else cache.packed()
     rc = lib().attn_decode(_ptr(q), c, _ptr(seq_lens), _ptr(positions), B, R,
                            int(max_seq_len), int(window), Hq, cache.n_kv_heads, D, float(scale),
                            _ptr(out), _ptr(workspace),
@@ -380,7 +446,11 @@ def attn_decode_append(q, k_new, v_new, slot_mapping, cache: KVCache, seq_lens, 
         need = attn_decode_workspace_size(cache, B, R, Hq, max_seq_len, window)
         if need > 0:
             workspace = _made(_zeroed, q, stream, need)
-    c = cache.packed()
+    if cache.dtype in _SCALED and workspace is not None:
+        c = _want_decode("attn_decode_append", cache, q, out, seq_lens, positions, workspace)
+        _want_new_rows("attn_decode_append", cache, k_new, v_new, slot_mapping, B * R)
+    else:
+        c = cache.packed()
     rc = lib().attn_decode_append(
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), _ptr(rope_inv_freq),
         c, _ptr(seq_lens),
@@ -448,12 +518,8 @@ def attn_decode_sinks(q, cache: KVCache, seq_lens, positions, max_seq_len, windo
         need = attn_decode_sinks_workspace_size(cache, B, R, Hq, max_seq_len, window, n_sinks)
         if need > 0:
             workspace = _made(_zeroed, q, stream, need)
-    device = _device()
-    _want("attn_decode_sinks", device, torch.bfloat16, q, out)
-    _want("attn_decode_sinks", device, torch.int32, seq_lens, positions)
-    if seq_lens.shape[0] < B or positions.numel() < B * R:
-        raise AttnError(ATTN_ERR_SHAPE, "attn_decode_sinks: seq_lens [B], positions [B * R]")
-    c = cache.packed()
+    c = _want_decode("attn_decode_sinks", cache, q, out, seq_lens, positions, workspace) \
+        if workspace is not None else cache.packed()
     rc = lib().attn_decode_sinks(
         _ptr(q), c, _ptr(seq_lens), _ptr(positions), B, R, int(max_seq_len),
         int(window), int(n_sinks), Hq, cache.n_kv_heads, D, float(scale), _ptr(out),
@@ -567,10 +633,10 @@ def attn_pages_copy(caches, moves, n_moves, err=None, stream=None):
     for c in caches:
         known = c._known("attn_pages_copy", device)
         if shape is None:
-            shape = known[5]
-        elif known[5] != shape:
+            shape = known[6]
+        elif known[6] != shape:
             raise AttnError(ATTN_ERR_SHAPE, "attn_pages_copy: caches of different shapes")
-        packed.append(known[6])
+        packed.append(known[7])
     Hkv, D = (shape[1], shape[-1]) if shape else (1, 128)
     rc = lib().attn_pages_copy(b"".join(packed), len(packed), Hkv, D, _ptr(moves), _ptr(n_moves),
                                moves.shape[0], _ptr(err), _stream(stream))

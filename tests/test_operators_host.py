@@ -256,3 +256,75 @@ def test_page_copies_look_at_tensors_that_were_replaced(calls, dtype, name):
         layers[1].k_scale = torch.zeros(8, 2)
     copy()
     assert calls == ["attn_pages_copy"] * 4
+
+
+def test_scaled_caches_and_sinks_refuse_what_the_kernels_would_misread(calls):
+    """Tensors of another type, size, order or device, each in a call that is right
+    without it; nothing reaches the library."""
+    import torch
+
+    bf, i32, i64 = torch.bfloat16, torch.int32, torch.int64
+    B, R, Hq, H, D = 2, 3, 4, 2, 64
+    z = torch.zeros
+    good = {"q": z(B, R, Hq, D, dtype=bf), "k_new": z(B * R, H, D, dtype=bf),
+            "v_new": z(B * R, H, D, dtype=bf), "slots": z(B * R, dtype=i64),
+            "lens": z(B, dtype=i32), "pos": z(B * R, dtype=i32), "ws": z(64, dtype=torch.uint8),
+            "out": z(B, R, Hq, D, dtype=bf)}
+
+    def append(c, a):
+        gq.attn_kv_append(a["k_new"], a["v_new"], a["slots"], c, stream=0)
+
+    def decode(c, a):
+        gq.attn_decode(a["q"], c, a["lens"], a["pos"], 64, 0, 0.1, out=a["out"],
+                       workspace=a["ws"], stream=0)
+
+    def sinks(c, a):
+        gq.attn_decode_sinks(a["q"], c, a["lens"], a["pos"], 64, 8, 2, 0.1, out=a["out"],
+                             workspace=a["ws"], stream=0)
+
+    def step(c, a):
+        gq.attn_decode_append(a["q"], a["k_new"], a["v_new"], a["slots"], c, a["lens"], a["pos"],
+                              64, 0, 0.1, out=a["out"], workspace=a["ws"], stream=0)
+
+    rows = {"k_new": [z(B * R - 1, H, D, dtype=bf), z(B * R, H, D), z(B * R, H, 2 * D, dtype=bf),
+                      z(H, B * R, D, dtype=bf).transpose(0, 1)],
+            "v_new": [z(1, H, D, dtype=bf)],
+            "slots": [z(B * R, dtype=i32), z(2 * B * R, dtype=i64)[::2]]}
+    reads = {"q": [z(B, R, Hq, D), z(B, R, Hq, 2 * D, dtype=bf),
+                   z(B, Hq, R, D, dtype=bf).transpose(1, 2)],
+             "out": [z(B, R, Hq, D), z(B, R, 1, D, dtype=bf)],
+             "lens": [z(B, dtype=i64), z(1, dtype=i32)],
+             "pos": [z(B * R, dtype=i64), z(B * R - 1, dtype=i32), z(2 * B * R, dtype=i32)[::2]],
+             "ws": [z(2, 64, dtype=torch.uint8)[:, ::2]]}
+    fields = {"k": [z(128, H, D), z(64, H, D, dtype=torch.int8), z(128, H, D, dtype=bf)],
+              "v": [z(8, H, D, dtype=torch.int8)],
+              "k_scale": [z(7, H), z(8, H).double()], "v_scale": [z(4, 2 * H), None],
+              "block_table": [z(2, 4, dtype=i64), z(1, 4, dtype=i32), z(8, dtype=i32)]}
+    table = {append: rows, decode: reads, sinks: reads, step: {**rows, **reads}}
+    for call, arguments in table.items():
+        for dtype in (E4, I8) + ((gq.ATTN_KV_BF16,) if call is sinks else ()):
+            del calls[:]
+            call(paged_layer(dtype=dtype), good)
+            assert len(calls) == 1
+            for name, bad in arguments.items():
+                for x in bad:
+                    with pytest.raises(gq.AttnError):
+                        call(paged_layer(dtype=dtype), {**good, name: x})
+            for name, bad in fields.items():
+                if (name == "block_table" and call is append) or \
+                        (name.endswith("scale") and dtype == gq.ATTN_KV_BF16):
+                    continue
+                for x in bad:
+                    if x is not None and x.dtype is bf and dtype == gq.ATTN_KV_BF16:
+                        continue
+                    layer = paged_layer(dtype=dtype)
+                    setattr(layer, name, x)
+                    with pytest.raises(gq.AttnError):
+                        call(layer, good)
+            if call is append:
+                layer = paged_layer(dtype=dtype)
+                for x in (z(H, D).double(), z(H, 2 * D)[:, ::2], z(1, D)):
+                    layer.k_ref = x
+                    with pytest.raises(gq.AttnError):
+                        call(layer, good)
+            assert len(calls) == 1
