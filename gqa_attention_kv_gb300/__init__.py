@@ -216,11 +216,12 @@ class KVCache:
         self.layout = int(layout)
         self.k_scale, self.v_scale = k_scale, v_scale
         self.scale_block = int(scale_block)
-        if self.dtype in _SCALED and \
-                isinstance(k_scale, torch.Tensor) and self.scale_block > 0:
+        if self.dtype in _SCALED and self.scale_block > 0 and \
+                (isinstance(k_scale, torch.Tensor) or isinstance(v_scale, torch.Tensor)):
             shape = (self.num_slots // self.scale_block, self.n_kv_heads)
             for t in (k_scale, v_scale):
-                if t.shape != shape or t.dtype is not torch.float32 or not t.is_contiguous():
+                if not isinstance(t, torch.Tensor) or t.shape != shape or \
+                        t.dtype is not torch.float32 or not t.is_contiguous():
                     raise AttnError(ATTN_ERR_SHAPE, f"KVCache: k_scale and v_scale are contiguous "
                                                     f"float32 tensors of shape {shape}")
 

@@ -328,3 +328,13 @@ def test_scaled_caches_and_sinks_refuse_what_the_kernels_would_misread(calls):
                     with pytest.raises(gq.AttnError):
                         call(layer, good)
             assert len(calls) == 1
+
+
+def test_a_scaled_cache_has_both_scales(calls):
+    import torch
+
+    codes, scale = torch.zeros(64, 2, 64, dtype=torch.int8), torch.ones(4, 2)
+    for k_scale, v_scale in ((scale, None), (None, scale)):
+        with pytest.raises(gq.AttnError):
+            gq.KVCache(gq.LINEAR, codes, codes, slots_per_seq=64, dtype=I8, k_scale=k_scale,
+                       v_scale=v_scale, scale_block=16)
