@@ -31,8 +31,12 @@
 //     after it was stored comes to the same new scale.  Many rows in longer blocks:
 //     14,449 rows in blocks of 32 14.5 us (24.0 by warps), of 64 15.5 (36.0), of 128
 //     16.5 (57.0); in blocks of 16 it would take 14.5.
-// Rows of a block in another order than their slots', or with skipped rows beside
+// Rows of a block in another order than their slots', or with skipped rows among
 // them, are an irregular run: written alone by the warp that has its first row.
+// Skipped rows beside a run (a padded batch) are looked through 64 at a time for the
+// row that says whether the run goes on: 14,449 rows padded to 16,384 take 17 us in
+// blocks of 16 and 23 to 25 in longer ones, one row of 4,001 22 (one skipped row after
+// another, each walked again by the warp of the run: 315, 377 to 414 and 720 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -138,6 +142,31 @@ __device__ __forceinline__ void recode(const ScaledParams &p, uint8_t *cache, in
         *c = w;
     }
     __syncwarp();
+}
+
+// From row i on (DIR 1; -1: back from it), past the rows without a slot of the cache, 64
+// of them a step: the slot of the first that has one, kNone where the call ends before.
+template <int DIR>
+__device__ __forceinline__ int64_t next_slot(const ScaledParams &p, int64_t &i) {
+    constexpr int kLoads = 2;
+    const int lane = threadIdx.x & 31;
+    for (; i >= 0 && i < p.n; i += DIR * 32 * kLoads) {
+        int64_t s[kLoads];
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            const int64_t row = i + DIR * (32 * u + lane);
+            s[u] = row >= 0 && row < p.n ? __ldg(p.slots + row) : kBad;
+        }
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            const uint32_t found = __ballot_sync(0xffffffffu, s[u] >= 0 && s[u] < p.num_slots);
+            if (found != 0) {
+                i += DIR * (32 * u + __ffs(found) - 1);
+                return __shfl_sync(0xffffffffu, s[u], __ffs(found) - 1);
+            }
+        }
+    }
+    return kNone;
 }
 
 // s' from the scale held (0 where the block starts anew) and the rows' maximum.
@@ -284,15 +313,21 @@ __global__ void __launch_bounds__(128, 6) kv_append_runs_kernel(const ScaledPara
     // rows of this window that start a run
     bool start = false;
     const int64_t before = __shfl_up_sync(0xffffffffu, my_slot, 1);
-    if (lane >= 1 && lane <= p.window && seen < p.n) {
+    const bool mine = lane >= 1 && lane <= p.window && seen < p.n;
+    bool far = false;  // the row before is skipped: rows that are do not end a run
+    if (mine) {
         if (good(my_slot)) {
-            int64_t j = seen - 1, t = before;
-            while (j >= 0 && !good(t))  // rows that are skipped do not end a run
-                if (--j >= 0) t = __ldg(p.slots + j);
-            start = j < 0 || (t >> p.shift) != (my_slot >> p.shift);
+            far = seen > 0 && !good(before);
+            start = !far && (seen == 0 || (before >> p.shift) != (my_slot >> p.shift));
         } else if (rem == 0) {
             report_error(p.err, ATTN_ERR_BOUNDS);
         }
+    }
+    for (uint32_t rows = __ballot_sync(0xffffffffu, far); rows != 0; rows &= rows - 1) {
+        const int l = __ffs(rows) - 1;
+        int64_t j = first_row - 1 + l - 2;
+        const int64_t t = next_slot<-1>(p, j);
+        if (lane == l) start = t == kNone || (t >> p.shift) != (my_slot >> p.shift);
     }
     // the scales that the runs' blocks hold, all in one trip
     const float my_scale = start ? scales[(my_slot >> p.shift) * heads + h] : 0.f;
@@ -329,6 +364,9 @@ __global__ void __launch_bounds__(128, 6) kv_append_runs_kernel(const ScaledPara
             const bool in = seen < p.n && (!good(my_slot) || (my_slot >> p.shift) == block);
             const uint32_t out = ~__ballot_sync(0xffffffffu, in) & (0xffffffffu << at_lane);
             const int stop = out == 0 ? 32 : __ffs(out) - 1;
+            const uint32_t rows = __ballot_sync(
+                0xffffffffu, lane >= at_lane && lane < stop && good(my_slot));
+            int64_t end = first_row - 1 + 32 - __clz(rows);  // behind its last row
             i1 = first_row - 1 + stop;
             fresh = __any_sync(0xffffffffu, lane >= at_lane && lane < stop && good(my_slot) &&
                                                 (my_slot & inside) == 0);
@@ -339,9 +377,13 @@ __global__ void __launch_bounds__(128, 6) kv_append_runs_kernel(const ScaledPara
                     0xffffffffu, i < p.n && (!good(s) || (s >> p.shift) == block));
                 const int take = past == 0 ? 32 : __ffs(past) - 1;
                 fresh |= __any_sync(0xffffffffu, lane < take && good(s) && (s & inside) == 0);
+                const uint32_t some = __ballot_sync(0xffffffffu, lane < take && good(s));
+                if (some != 0) end = i1 + 32 - __clz(some);
                 i1 += take;
                 if (take < 32) break;
+                if (some == 0 && next_slot<1>(p, i1) >> p.shift != block) break;
             }
+            i1 = end;
         }
         auto slot_of = [&](int64_t i) -> int64_t {  // all lanes together
             const int64_t l = i - (first_row - 1);
@@ -557,12 +599,16 @@ __global__ void __launch_bounds__(W * 32, 24 / W)
             r1 += run;
             if (run < 32) break;
         }
-        // regular: no other row of the block beside it, nor a row without a slot
-        auto apart = [&](int r) {
-            const int64_t s = slot(r);
-            return s == kNone || (s >= 0 && (s >> p.shift) != block);
-        };
-        if (apart(r0 - 1) && apart(r1)) {
+        // regular: no other row of the block beside it, also not behind rows without a slot
+        auto other_block = [&](int64_t s) { return s == kNone || (s >= 0 && (s >> p.shift) != block); };
+        bool regular = other_block(slot(r0 - 1)) && other_block(slot(r1));
+        if (!regular && (slot(r0 - 1) == kBad || slot(r1) == kBad)) {
+            int64_t i = row0 + r0 - 1;
+            regular = other_block(next_slot<-1>(p, i));
+            i = row0 + r1;
+            if (regular) regular = other_block(next_slot<1>(p, i));
+        }
+        if (regular) {
             const int64_t first = s_a - (w0 + a - r0);  // slot of the run's first row
             const bool fresh = (first & (sb - 1)) == 0;
             float amax = 0.f;
@@ -634,16 +680,22 @@ __global__ void __launch_bounds__(W * 32, 24 / W)
             continue;
         }
         // ---- an irregular run: written by the warp that has its first row
-        int64_t i = row0 + w0 + a - 1;
-        int64_t s = kNone;
-        while (i >= 0 && ((s = __ldg(p.slots + i)) < 0 || s >= p.num_slots)) --i;
-        if (i >= 0 && (s >> p.shift) == block) continue;  // its first row is another
         const int64_t i0 = row0 + w0 + a;
+        int64_t i = i0 - 1;
+        int64_t s = next_slot<-1>(p, i);
+        if (s != kNone && (s >> p.shift) == block) continue;  // its first row is another
         auto in_block = [&](int64_t t) { return t >= 0 && t < p.num_slots && (t >> p.shift) == block; };
-        int64_t i1 = i0;
-        for (;; ++i1) {
-            s = i1 < p.n ? __ldg(p.slots + i1) : kNone;
-            if (s == kNone || (s >= 0 && s < p.num_slots && (s >> p.shift) != block)) break;
+        int64_t i1 = i0;  // behind its last row
+        for (i = i0;;) {
+            if (s = next_slot<1>(p, i); s == kNone || (s >> p.shift) != block) break;
+            s = i + lane < p.n ? __ldg(p.slots + i + lane) : kBad;
+            const uint32_t past = __ballot_sync(
+                0xffffffffu, s >= 0 && s < p.num_slots && (s >> p.shift) != block);
+            const uint32_t rows = __ballot_sync(0xffffffffu, in_block(s)) &
+                                  (past == 0 ? 0xffffffffu : (past & -past) - 1u);
+            i1 = i + 32 - __clz(rows);
+            if (past != 0) break;
+            i += 32;
         }
         float amax = 0.f;
         bool fresh = false, nan = false;

@@ -505,6 +505,45 @@ def test_append_short_runs(fmt, D, H, sb, head_major, ref_vector):
         case.check()
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("D,H,sb,head_major,ref_vector", [
+    (128, 8, 16, False, False), (64, 8, 16, True, True), (128, 8, 32, False, True),
+    (64, 5, 64, False, False), (128, 4, 128, True, False), (64, 1, 32, False, False)])
+def test_append_long_stretches_of_skipped_rows(fmt, D, H, sb, head_major, ref_vector):
+    """Padded prompts: hundreds of rows without a slot before, between and behind the
+    requests' rows, and inside a block, whose rows still belong together."""
+    g = gen(D + H + sb + 2)
+    B, per = 5, 4 * sb
+    k_ref = torch.randn(H, D, generator=g) if ref_vector else None
+    case = Case(fmt, B * per, H, D, sb, per=per, head_major=head_major, k_ref=k_ref).fill(g)
+    case.cuda()
+    pad = lambda n: [-1] * n  # noqa: E731
+    at = pad(300)
+    for b in range(B):
+        lo = b * per + int(torch.randint(0, 2 * sb, (1,), generator=g))
+        hi = (b + 1) * per - int(torch.randint(0, sb, (1,), generator=g))
+        rows = list(range(lo, hi))
+        if b == 2:      # in the middle of a block
+            cut = (hi - 2 * sb) // sb * sb + sb // 2 - lo
+            rows[cut:cut] = pad(391)
+        at += rows + pad((1, 129, 37, 260, 1000)[b])
+    at = torch.tensor(at)
+    at[5], at[-900] = B * per, -(2 ** 40)
+    k, v = new_rows(g, len(at), H, D, 2.0)
+    k[at < 0], v[at < 0] = 1e30, float("nan")
+    case.append(k, v, at)
+    assert gpu_append(case, k, v, at) == gq.ATTN_ERR_BOUNDS
+    case.check()
+    # single rows apart from each other
+    slots = torch.arange(B * 4) * sb + 3
+    at = torch.full((B * 4 * 50 + 700,), -1, dtype=torch.int64)
+    at[333:333 + B * 4 * 50:50] = slots
+    k, v = new_rows(g, len(at), H, D, 2.0)
+    case.append(k, v, at)
+    assert gpu_append(case, k, v, at) == gq.ATTN_ERR_BOUNDS
+    case.check()
+
+
 @pytest.mark.parametrize("B,H,lo,hi", [(40, 2, 1, 20000),   # one long request among short ones
                                        (1, 1, 30000, 30000)])  # one unit over the whole GPU
 def test_decode_in_very_many_parts(B, H, lo, hi):
