@@ -297,6 +297,29 @@ def test_decode_largest_scales(fmt, D, R):
     assert run() == 0
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("R", [1, 6])
+def test_decode_queries_of_one_sign(D, R):
+    """INT8 keys are multiplied as code + 128, of which 128 sum(q) is taken: sums of
+    up to 255 sum |q| in 32 bits, D / 16 products and two additions of 2^-23 each,
+    times what a score is multiplied with, are what the weights may be off by."""
+    case, q, lens, pos, slot = decode_case("int8", gq.LINEAR, 2, R, 4, 2, D, 200, 900, 16, 0,
+                                           False, D + R)
+    q = (q.abs() + 2.0).bfloat16()
+    q[1] = -q[1]
+    case.ks.fill_(1.0 / 36)
+    scale = D ** -0.5
+    want, mass = ref.decode(q, ref.dequantized("int8", case.k, case.ks, 16),
+                            ref.dequantized("int8", case.v, case.vs, 16), slot, lens, pos, 0, 0,
+                            scale)
+    off = (D / 16 + 2) * 2.0 ** -23 * 255 * q.double().abs().sum(-1).max().item() * scale / 36
+    got = gq.attn_decode(q.to(DEV), case.cuda(), lens.to(DEV), pos.to(DEV), 900, 0, scale)
+    got = got.double().cpu()
+    # a weight and the sum of all by e^off each
+    bound = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2.0 ** -13 + 2 * math.expm1(off)) * mass + 1e-30
+    assert ((got - want).abs() <= bound).all()
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("group", [1, 12])
 def test_decode_small_weights_beside_zeros(fmt, group):

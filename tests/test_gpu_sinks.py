@@ -302,6 +302,28 @@ def test_prefill(B, T, Hq, H, D, window, sinks):
     ref.check_output(got[:, rows, heads], want, mass)
 
 
+@pytest.mark.parametrize("sinks", [15, 16, 17, 32, 33, 129, 150, 160, 161])
+@pytest.mark.parametrize("group", [1, 5])
+def test_prefill_tiles_of_sinks(sinks, group):
+    """head_dim 64: a last tile of 1 to 32 sinks or more, behind a whole tile or none,
+    walked at different places by the heads of a group; a NaN in V behind the sinks is
+    reported and taken as 0."""
+    g = gen(sinks + group)
+    T, H, D, window = 800, 2, 64, 90
+    q = torch.randn(1, T, H * group, D, generator=g).bfloat16()
+    k, v = (torch.randn(1, T, H, D, generator=g).bfloat16() for _ in range(2))
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for behind in (None, 0, 1, 5):
+        if behind is not None:
+            v[0, sinks + behind, 1, 7 * behind] = NAN
+        err.zero_()
+        got = gq.attn_prefill_sinks(q.to(DEV), k.to(DEV), v.to(DEV), window, sinks, D ** -0.5,
+                                    err=err)
+        assert int(err) == (0 if behind is None else gq.ATTN_ERR_UNSUPPORTED)
+        want, mass = ref.prefill(q, k, v.nan_to_num(0.0), window, sinks, D ** -0.5)
+        ref.check_output(got, want, mass)
+
+
 def test_prefill_values_that_are_not_finite():
     """K and V behind a row do not reach it; a NaN in V is reported."""
     g = gen(2)

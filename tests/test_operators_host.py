@@ -338,3 +338,50 @@ def test_a_scaled_cache_has_both_scales(calls):
         with pytest.raises(gq.AttnError):
             gq.KVCache(gq.LINEAR, codes, codes, slots_per_seq=64, dtype=I8, k_scale=k_scale,
                        v_scale=v_scale, scale_block=16)
+
+
+def test_sinks_and_page_wrappers_refuse_what_the_kernels_would_misread(calls, monkeypatch):
+    """Types, order, device and shapes, each in a call that is right without it."""
+    import torch
+
+    i32, z = torch.int32, torch.zeros
+    ints = lambda *shape: z(*shape, dtype=i32)  # noqa: E731
+    table, refs, rows, moves, one = ints(4, 6), ints(32), ints(3), ints(8, 3), ints(1)
+    space = z(4096, dtype=torch.uint8)
+    q, k = z(2, 5, 4, 64, dtype=torch.bfloat16), z(2, 5, 2, 64, dtype=torch.bfloat16)
+    cases = [
+        (lambda a, b, c, d, e: gq.attn_pages_free(a, b, c, d, e, stream=0),
+         [table, refs, rows, rows, rows]),
+        (lambda a, b, c, d, e: gq.attn_pages_reserve(a, b, c, d, e, stream=0),
+         [table, refs, rows, rows, rows]),
+        (lambda a, b, c, d, e, m, n: gq.attn_pages_fork(a, b, c, d, e, 16, m, n, stream=0),
+         [table, refs, rows, rows, rows, moves, one]),
+        (lambda a, b, m, n, u: gq.attn_pages_compact(a, b, 16, m, n, u, workspace=space, stream=0),
+         [table, refs, moves, one, one]),
+        (lambda m, n: gq.attn_pages_copy([], m, n, stream=0), [moves, one]),
+        (lambda a, b, c: gq.attn_prefill_sinks(a, b, c, 8, 4, 0.1, out=q, stream=0),
+         [q, k, k]),
+    ]
+    for call, good in cases:
+        del calls[:]
+        call(*good)
+        assert len(calls) == 1
+        for at, x in enumerate(good):
+            wide = torch.cat([x, x], -1)
+            bad = [x.double(), wide[..., ::2]]
+            if x.dim() > 1:
+                bad.append(x[..., :-1].contiguous() if x is not table else x[0])
+            for y in bad:
+                if wide[..., ::2].is_contiguous() and y is bad[1]:
+                    continue
+                with pytest.raises(gq.AttnError):
+                    call(*good[:at], y, *good[at + 1:])
+        assert len(calls) == 1
+    for call, good in cases[:3]:               # row arguments of one length
+        with pytest.raises(gq.AttnError):
+            call(*good[:4], ints(2), *good[5:])
+    monkeypatch.setattr(gq, "_device", lambda: 0)
+    for call, good in cases:                   # these tensors are the CPU's
+        with pytest.raises(gq.AttnError):
+            call(*good)
+    assert len(calls) == 1
