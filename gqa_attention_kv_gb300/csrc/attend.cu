@@ -83,7 +83,9 @@ constexpr int kGapChunks = 32;
 constexpr int kMinChunks = 4;
 // Parts of a unit that its last CTA adds up itself.  17 parts: 8.9 us of GPU time
 // against 8.3 with the merge kernel, which costs the host 3 us to launch; 76 parts:
-// 22.5 against 16.4 us.
+// 22.5 against 16.4 us.  The host decides by the longest that units can be; where one is
+// much longer than the others are, shares are cut so that it has no more parts (40
+// requests, one of 20,000 keys among 5 to 19: 21.5 us, 46 with shares of the sum alone).
 constexpr int kKernelParts = 24;
 constexpr float kRescaleLog2 = 8.0f;  // the reference maximum moves past this only (w <= 2^8)
 // f16 weights are held times 2^7, 2^15 at most: those above 2^-21 of the largest keep
@@ -337,7 +339,7 @@ struct __align__(16) Smem {
     float m[kWarps][G::RB], l[kWarps][G::RB], w[kWarps][G::RB], lse[HG][G::RB];
     Entry entry[kMaxEntries];
     int prefix[kMaxEntries + 1];
-    int last_part;
+    int last_part, longest;
     __device__ __forceinline__ float *out_row(int warp, int row) {
         return reinterpret_cast<float *>(buf[warp]) + row * G::kOStride;
     }
@@ -434,11 +436,12 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
         sm.entry[i] = make_entry(p, p.e0 + i, RB, blockIdx.x == 0);
     __syncthreads();
     if (warp == 0) {
-        int carry = 0;
+        int carry = 0, longest = 0;
         if (lane == 0) sm.prefix[0] = 0;
         for (int base = 0; base < p.n_entries; base += 32) {
             const int i = base + lane;
             const int n = i < p.n_entries ? chunks_of(sm.entry[i], p.sinks).cnt : 0;
+            longest = max(longest, n);
             int x = n > 0 ? (n + kGapChunks) * p.n_groups : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -448,10 +451,14 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
             if (i < p.n_entries) sm.prefix[i + 1] = carry + x;
             carry += __shfl_sync(0xffffffffu, x, 31);
         }
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        if (lane == 0) sm.longest = longest;
     }
     __syncthreads();
     const int total = sm.prefix[p.n_entries];
-    const int share = max(kMinChunks, (total + p.grid - 1) / p.grid);
+    int share = max(kMinChunks, (total + p.grid - 1) / p.grid);
+    if (p.ws_count != nullptr)
+        share = max(share, (sm.longest + kKernelParts - 2) / (kKernelParts - 1));
     int g = min(total, (int)min((int64_t)blockIdx.x * share, (int64_t)total));
     const int g_end = min(total, g + share);
 
@@ -1298,7 +1305,6 @@ int plan_attend(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
     if (window > 0)
         usual = std::min<int64_t>(chunks, ((int64_t)window + q_rows + sinks) / att::kChunk + 3);
     const int64_t entries = (int64_t)batch * row_blocks;
-    // rows of one head and prefixes of chunks are counted in 32 bits
     // Two KV heads a unit where the slot-major rows of a head are so short that one
     // head alone reads DRAM badly: 8-bit rows of 64 bytes leave half of every line
     // (16 x 32 heads, 2,048 to 8,192 keys: 595 MB from DRAM and 102 us, with two heads
@@ -1311,6 +1317,7 @@ int plan_attend(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
         plan->heads = 2;
     const int n_groups = n_kv_heads / plan->heads;
     const int64_t per_entry = (chunks + att::kGapChunks) * n_groups;
+    // rows of one head and prefixes of chunks are counted in 32 bits
     if (rows >= (int64_t(1) << 31) || entries >= (int64_t(1) << 31) ||
         per_entry >= (int64_t(1) << 30) ||
         cache->num_slots * n_kv_heads >= (int64_t(1) << 32))
@@ -1328,7 +1335,7 @@ int plan_attend(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
     const size_t units = (size_t)plan->per_launch * n_groups,
                  slots = (units + plan->grid) * plan->heads;
     // How many CTAs a unit spans when all are as long as they can be: past
-    // kKernelParts the merge kernel adds the parts up
+    // kKernelParts the merge kernel adds the parts up (else the kernel keeps to them)
     const int64_t share = std::max<int64_t>(
         att::kMinChunks, (int64_t)units * (usual + att::kGapChunks) / plan->grid);
     plan->merge = usual / share + 1 > att::kKernelParts;
