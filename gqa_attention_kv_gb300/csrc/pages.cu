@@ -30,9 +30,9 @@ constexpr int kScanThreads = 1024;
 constexpr int kPer = 16, kTile = kScanThreads * kPer;
 constexpr int kListPer = 4, kListTile = kScanThreads * kListPer;
 constexpr int kListed = 2 * kListTile;
-// A fork's entries up to which one cluster copies them (18 a thread): free, fork and copy of
+// A fork's entries up to which one cluster copies them (16 a thread): free, fork and copy of
 // 48 rows of 94 entries take 20.2 us so, 22.5 with a launch of their own, a thread each.
-constexpr int kForkBlocks = 8, kForkEntries = 16 * kForkBlocks * kScanThreads;
+constexpr int kForkBlocks = 8, kForkEntries = 16 * (kForkBlocks - 1) * kScanThreads;
 
 // Exclusive prefix of v over the block, and the block's sum in `sum`.  All
 // kScanThreads threads take part.
