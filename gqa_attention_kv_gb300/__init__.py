@@ -616,6 +616,7 @@ def attn_pages_compact(block_table, refs, block_size, moves, n_moves, used, work
         raise AttnError(ATTN_ERR_SHAPE, "attn_pages_compact: block_table is [rows, max_blocks]")
     if workspace is None:
         workspace = _made(_zeroed, refs, stream, attn_pages_workspace_size(refs.shape[0]))
+    _want("attn_pages_compact", _device(), workspace.dtype, workspace)
     rc = lib().attn_pages_compact(_ptr(block_table), block_table.shape[1], block_table.shape[0],
                                   int(block_size), _ptr(refs), refs.shape[0], _ptr(moves),
                                   moves.shape[0], _ptr(n_moves), _ptr(used), _ptr(workspace),

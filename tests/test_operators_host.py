@@ -377,6 +377,8 @@ def test_sinks_and_page_wrappers_refuse_what_the_kernels_would_misread(calls, mo
                 with pytest.raises(gq.AttnError):
                     call(*good[:at], y, *good[at + 1:])
         assert len(calls) == 1
+    with pytest.raises(gq.AttnError):
+        gq.attn_pages_compact(table, refs, 16, moves, one, one, workspace=z(9, 9)[:, ::2], stream=0)
     for call, good in cases[:3]:               # row arguments of one length
         with pytest.raises(gq.AttnError):
             call(*good[:4], ints(2), *good[5:])
