@@ -787,9 +787,10 @@ int launch_kv_append_scaled(const void *k_new, const void *v_new, const int64_t 
     }
     p.window = many ? kMaxWindow : 1;
     const int64_t warps = (n + p.window - 1) / p.window * per_row, blocks = (warps + 3) / 4;
-    // Past a round and a half of such warps the rows are a prompt's: nothing is gained by
-    // short runs there, and the registers they take cost 14,449 rows of 4 x 128 12.1 us
-    // against 10.9 (single rows of that many requests would take four times as long so).
+    // Past a round and a half of such warps the rows are taken for a prompt's.  At every
+    // size a prompt is a little faster without short runs, by the registers they take, and
+    // single rows several times slower: 9,000 rows of 4 x 128 as a prompt 6.9 us without
+    // and 7.4 with them, single 42 and 11; 14,449 rows 10.9 and 12.1, 60 and 16.
     if (many && 2 * warps <= (int64_t)device_sm_count() * 24 * 3)
         return head_dim == 128 ? run(int8 ? kv_append_runs_kernel<true, 128, true>
                                           : kv_append_runs_kernel<false, 128, true>, blocks, 128)

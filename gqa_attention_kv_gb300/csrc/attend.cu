@@ -42,7 +42,7 @@
 // and steps without per-key checks 74, with 32 keys a step on twelve warps an SM
 // instead of 16 on sixteen 63, with a lane for each of 32 chunks' rows and scales (13%
 // fewer instructions a key; 20% at head_dim 64) 60, with the shares cut anew 58 to 59 (4.7
-// TB/s).  One query row: 5.5 TB/s E4M3, 6.2 bf16 (64 x 2,080 keys).  What bounds it
+// TB/s).  One query row: 5.2 TB/s E4M3, 5.9 bf16 (64 x 2,080 keys).  What bounds it
 // now: the warps' own dependency chains (issue slots about half used), and at one row
 // a KV head DRAM.
 //
@@ -78,8 +78,9 @@ constexpr int kMaxEntries = 128;  // (request, row block) pairs per launch
 // 16, 60.3 with 24, 59.0 with 28, 58.3 with 32, 59.4 with 36; 64 even ones (2,080 keys)
 // 57.6 with 24, 57.1 with 32.
 constexpr int kGapChunks = 32;
-// Smallest share of a CTA.  One request of 9,000 tokens, window 1,024: 8.2 us with 4
-// chunks, 8.9 with 8, 9.8 with 16.
+// Smallest share of a CTA, with 2, 4 and 8 chunks: one request of 9,000 tokens under a
+// window of 1,024 9.05, 9.06 and 8.6 us; 512 E4M3 keys 8.4, 7.2 and 7.0; four requests of
+// 300 8.7, 8.75 and 8.4; two of 700 with 64 dims in bf16 11.1, 9.9 and 10.1.
 constexpr int kMinChunks = 4;
 // Parts of a unit that its last CTA adds up itself.  17 parts: 8.9 us of GPU time
 // against 8.3 with the merge kernel, which costs the host 3 us to launch; 76 parts:

@@ -124,7 +124,7 @@ int check_scaled(const attn_kv_cache *c, bool pointers) {
         rows = c->slots_per_seq;
     else if (c->kind == ATTN_CACHE_PAGED)
         rows = c->block_size;
-    else  // a ring overwrites blocks whose other tokens are still visible
+    else  // a ring may begin a block anew while its other tokens are still visible
         return ATTN_ERR_UNSUPPORTED;
     if (rows < 1 || rows % sb != 0 || c->num_slots % sb != 0) return ATTN_ERR_SHAPE;
     if (pointers) {

@@ -34,7 +34,8 @@
 //               FP16, because one bf16 rounding of P is too coarse; f16 keeps
 //               11 significant bits), O rescaled in TMEM only when the running
 //               max grew by more than 2^8 (the result is unchanged; rescaling
-//               is lazy; P stays below 2^8).  P is released in two halves of
+//               is lazy; P stays below 2^8, with sinks, where it is held
+//               times 2^7, below 2^15).  P is released in two halves of
 //               64 keys, so PV on the first half runs while the second is
 //               exponentiated.
 //               Epilogue: O / l -> bf16 -> shared (over Q_a) -> TMA store,
@@ -170,10 +171,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // The tile of sinks before the window that holds 32 of them or fewer (the last
     // one): every row sees those keys and no other of the tile, so only they are
-    // converted, exponentiated and multiplied with V.  At head_dim 64, 1,500 tokens
-    // under a window of 750 with 4 sinks take 22.2 us with it, 23.5 without (23.2
-    // without sinks); at head_dim 128 the other way round, 14,449 tokens under a
-    // window of 4,096 with 1 sink 665 against 645 us: there it is left out.
+    // converted, exponentiated and multiplied with V.  At head_dim 64 it pays where CTAs
+    // walk few tiles: 700 tokens under a window of 200 with 20 sinks 8.8 us with it, 9.1
+    // without; 1,500 under 750 with 4 sinks 21.6 and 20.8, 4,000 under 1,000 44.3 and
+    // 43.6.  At head_dim 128 it does not: 1,500 under 500 with 20 sinks 19.0 and 18.0,
+    // 14,449 under 4,096 with 1 sink 661 and 643: there it is left out.
     int j_narrow = -1;
     if (SINKS && n_sink > 0 && p.sinks - (n_sink - 1) * kBN <= 32) {
         j_narrow = n_sink - 1 - rot;

@@ -143,8 +143,8 @@ typedef enum {
  *     value = code * v_scale[slot / scale_block][head]
  * A request's slots (LINEAR) or a page (PAGED) hold whole blocks: slots_per_seq
  * or block_size, and num_slots, are multiples of scale_block.  RING caches are
- * not supported: a block begun anew would take the scale of tokens that are
- * still visible with it.  head_dim 64 or 128, both layouts.  The last three
+ * not supported: a block begun anew would take the scale of tokens that may
+ * still be visible with it.  head_dim 64 or 128, both layouts.  The last three
  * fields of the struct are read for these dtypes only.
  *
  * attn_kv_append keeps the scales.  For each block and head, with x the call's
