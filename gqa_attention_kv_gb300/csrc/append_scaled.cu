@@ -29,14 +29,15 @@
 //     with the run's first row stores the scale and, where it grew, recodes the
 //     block's slots that the run does not write; a warp elsewhere that reads the scale
 //     after it was stored comes to the same new scale.  Many rows in longer blocks:
-//     14,449 rows in blocks of 32 14.5 us (24.0 by warps), of 64 15.5 (36.0), of 128
-//     16.5 (57.0); in blocks of 16 it would take 14.5.
+//     14,449 rows of 4 x 128 in blocks of 32 17.7 us (27 by warps), of 64 18.3 (39), of
+//     128 19.3 (61); in blocks of 16 it would take 17.4.
 // Rows of a block in another order than their slots', or with skipped rows among
 // them, are an irregular run: written alone by the warp that has its first row.
 // Skipped rows beside a run (a padded batch) are looked through 64 at a time for the
-// row that says whether the run goes on: 14,449 rows padded to 16,384 take 17 us in
-// blocks of 16 and 23 to 25 in longer ones, one row of 4,001 22 (one skipped row after
-// another, each walked again by the warp of the run: 315, 377 to 414 and 720 us).
+// row that says whether the run goes on: 14,449 rows padded to 16,384, into one cache again
+// and again, take 17 us in blocks of 16 and 23 to 25 in longer ones (9.6 and 14.3 to 16.1
+// without padding), one row of 4,001 19 to 22; one skipped row after another, each walked
+// again by the warp of the run, 315, 377 to 414 and 635 to 720 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
