@@ -280,10 +280,7 @@ class KVCache:
             return u[7]
         if t is None or t[0] is not u or t[1] != bt.data_ptr() or t[2] != bt.nbytes:
             _want(where, device, _I32, bt)
-            if bt.dim() != 2:
-                raise AttnError(ATTN_ERR_SHAPE, f"{where}: block_table is [batch, "
-                                                "max_blocks_per_seq]")
-            t = (u, bt.data_ptr(), bt.nbytes, bt.shape[0], self.packed())
+            t = (u, bt.data_ptr(), bt.nbytes, bt.numel() // max(1, bt.shape[-1]), self.packed())
             object.__setattr__(self, "_table", t)
         if t[3] < batch:
             raise AttnError(ATTN_ERR_SHAPE, f"{where}: block_table has fewer rows than {batch}")

@@ -300,6 +300,9 @@ def test_scaled_caches_and_sinks_refuse_what_the_kernels_would_misread(calls):
               "v": [z(8, H, D, dtype=torch.int8)],
               "k_scale": [z(7, H), z(8, H).double()], "v_scale": [z(4, 2 * H), None],
               "block_table": [z(2, 4, dtype=i64), z(1, 4, dtype=i32), z(8, dtype=i32)]}
+    single = paged_layer()
+    single.block_table = z(4, dtype=i32)           # a request's row by itself
+    sinks(single, {**good, "q": good["q"][:1], "out": good["out"][:1]})
     table = {append: rows, decode: reads, sinks: reads, step: {**rows, **reads}}
     for call, arguments in table.items():
         for dtype in (E4, I8) + ((gq.ATTN_KV_BF16,) if call is sinks else ()):
