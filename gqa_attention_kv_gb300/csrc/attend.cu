@@ -1066,7 +1066,7 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
             for (auto &x : o) nan |= isnan(x[0]) || isnan(x[1]) || isnan(x[2]) || isnan(x[3]);
             if (again || !__any_sync(0xffffffffu, nan)) break;
         }
-        // (-inf: no key; an infinite score has no weight in the definition either)
+        // (-inf: no key seen)
         if (fmaxf(m_run[0] == -INFINITY ? 0.f : fabsf(m_run[0]),
                   m_run[1] == -INFINITY ? 0.f : fabsf(m_run[1])) >=
             (FMT == kBF16 ? kScoreTopBf16 : kScoreTopF16))

@@ -301,9 +301,9 @@ int attn_decode_kernel_launches(const attn_kv_cache *cache, int batch, int q_row
  *   ATTN_ERR_UNSUPPORTED; magnitudes under 2^-14 lose precision), the scales
  *   multiply scores and softmax weights in float32, and the weights are rounded
  *   once to f16.  A scale is finite and at least 2^-64 (one below reads as
- *   2^-64).  A row's largest score, scale * q . key * log2(e), has to stay below
- *   2^24 in magnitude (ATTN_ERR_UNSUPPORTED is reported otherwise, and the row
- *   is unspecified).  Its workspace is like any other's (zero-filled before its
+ *   2^-64).  Scores, scale * q . key * log2(e), have to stay below 2^24 in
+ *   magnitude: where the largest of a stretch of keys does not,
+ *   ATTN_ERR_UNSUPPORTED is reported and the row is unspecified.  Its workspace is like any other's (zero-filled before its
  *   first use).
  *   A group of 64 or more query rows (q_rows x n_q_heads / n_kv_heads) over a
  *   linear slot-major bf16 cache is a prefill chunk and computes as
@@ -458,10 +458,10 @@ int attn_prefill(const void *q, const void *k, const void *v, int batch, int seq
  *   Every cache dtype, kind and layout that attn_decode takes (unscaled FP8 at
  *   head_dim 128).  A position below 0 marks a row without keys (zeros).  A
  *   value that is not finite reaches only the rows that attend its key (an
- *   infinity in v makes their element that infinity).  A row's
- *   largest score, scale * q . key * log2(e), has to stay below 2^30 in magnitude
- *   over bf16 caches, 2^24 over 8-bit ones (ATTN_ERR_UNSUPPORTED is reported
- *   otherwise, and the row is unspecified).
+ *   infinity in v makes their element that infinity).  Scores, scale * q . key *
+ *   log2(e), have to stay below 2^30 in magnitude over bf16 caches, 2^24 over
+ *   8-bit ones: where the largest of a stretch of keys does not,
+ *   ATTN_ERR_UNSUPPORTED is reported and the row is unspecified.
  *   workspace: at least attn_decode_sinks_workspace_size(...) bytes (which
  *   returns (size_t)-1 for arguments this call would reject), 16-byte aligned,
  *   zero-filled before its first use; one workspace may serve this call and
