@@ -207,15 +207,11 @@ class KVCache:
     def __init__(self, kind, k, v, slots_per_seq=0, block_table=None, block_size=0,
                  dtype=ATTN_KV_BF16, k_ref=None, layout=ATTN_LAYOUT_BSHD, k_scale=None,
                  v_scale=None, scale_block=0):
-        self.kind, self.k, self.v = int(kind), k, v
-        self.slots_per_seq = int(slots_per_seq)
-        self.block_table = block_table
-        self.block_size = int(block_size)
-        self.dtype = int(dtype)
-        self.k_ref = k_ref
-        self.layout = int(layout)
-        self.k_scale, self.v_scale = k_scale, v_scale
-        self.scale_block = int(scale_block)
+        self.__dict__.update(
+            kind=int(kind), k=k, v=v, slots_per_seq=int(slots_per_seq), block_table=block_table,
+            block_size=int(block_size), dtype=int(dtype), k_ref=k_ref, layout=int(layout),
+            k_scale=k_scale, v_scale=v_scale, scale_block=int(scale_block),
+            _usable=None, _table=None)  # (a setattr each would cost 2 us)
         if self.dtype in _SCALED and self.scale_block > 0 and \
                 (isinstance(k_scale, torch.Tensor) or isinstance(v_scale, torch.Tensor)):
             shape = (self.num_slots // self.scale_block, self.n_kv_heads)
@@ -227,8 +223,8 @@ class KVCache:
 
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
-        object.__setattr__(self, "_usable", None)  # looked at again by the next call
-        object.__setattr__(self, "_table", None)
+        seen = self.__dict__  # looked at again by the next call
+        seen["_usable"] = seen["_table"] = None
 
     def _want_usable(self, where, device):
         """Refuses k, v, scales and reference that a kernel would read or write out
@@ -260,7 +256,7 @@ class KVCache:
                  _PACK(self.kind, k.data_ptr(), v.data_ptr(), self.num_slots, self.slots_per_seq,
                        0, self.block_size, 0, self.dtype, at, self.layout,
                        *(scales or (0, 0)), self.scale_block))
-        object.__setattr__(self, "_usable", known)
+        self.__dict__["_usable"] = known
         return known
 
     def _known(self, where, device):
@@ -281,7 +277,7 @@ class KVCache:
         if t is None or t[0] is not u or t[1] != bt.data_ptr() or t[2] != bt.nbytes:
             _want(where, device, _I32, bt)
             t = (u, bt.data_ptr(), bt.nbytes, bt.numel() // max(1, bt.shape[-1]), self.packed())
-            object.__setattr__(self, "_table", t)
+            self.__dict__["_table"] = t
         if t[3] < batch:
             raise AttnError(ATTN_ERR_SHAPE, f"{where}: block_table has fewer rows than {batch}")
         return t[4]
