@@ -10,6 +10,7 @@ missing or a call is refused, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import struct
 import threading
@@ -33,6 +34,7 @@ ATTN_KV_BF16, ATTN_KV_FP8_E4M3 = 0, 1  # cache element types (attn_kv_dtype)
 ATTN_KV_FP8_E4M3_SCALED, ATTN_KV_INT8_SCALED = 2, 3
 _SCALED = (ATTN_KV_FP8_E4M3_SCALED, ATTN_KV_INT8_SCALED)
 ATTN_LAYOUT_BSHD, ATTN_LAYOUT_BHSD = 0, 1  # cache layouts (attn_kv_layout)
+ATTN_ROPE_PAIRS, ATTN_ROPE_HALF = 0, 1  # which dims turn together (attn_rope_layout)
 
 _BF16, _I32, _I64 = torch.bfloat16, torch.int32, torch.int64
 _BYTES = (torch.uint8, torch.int8, torch.float8_e4m3fn)  # what may hold 8-bit codes
@@ -63,6 +65,7 @@ class _Cache(ctypes.Structure):
 
 # _Cache in its C layout: packing it costs half of what building a ctypes structure does
 _PACK = struct.Struct("@iPPqiPiiiPiPPi0P").pack
+_PACK_ROPE = struct.Struct("@PiifPPf0P").pack  # an attn_rope
 
 
 def lib():
@@ -107,6 +110,19 @@ def lib():
             L.attn_decode_sinks.argtypes = [p, cp, p, p, i32, i32, i32, i32, i32, i32, i32, i32,
                                             ctypes.c_float, p, p, sz, p, p]
             L.attn_decode_sinks.restype = i32
+            L.attn_decode_shared_workspace_size.argtypes = [cp, i32, i32, i32, i32, i32, i32, i32,
+                                                            i32]
+            L.attn_decode_shared_workspace_size.restype = sz
+            L.attn_decode_shared.argtypes = [p, cp, i32, p, p, p, p, i32, i32, i32, i32, i32, i32,
+                                             i32, i32, ctypes.c_float, p, p, sz, p, p]
+            L.attn_decode_shared.restype = i32
+            L.attn_qk_rope.argtypes = [p, i64, p, i64, p, i64, p, i32, i32, i32, p, p, p]
+            L.attn_qk_rope.restype = i32
+            L.attn_qk_rope_append.argtypes = [p, i64, p, i64, p, i64, p, p, i64, p, cp, i32, i32,
+                                              i32, p, p, p, p]
+            L.attn_qk_rope_append.restype = i32
+            L.attn_kv_read.argtypes = [p, i64, cp, i32, i32, p, p, p, p]
+            L.attn_kv_read.restype = i32
             L.attn_prefill_sinks.argtypes = [p, p, p, i32, i32, i32, i32, i32, i32, i32,
                                              ctypes.c_float, p, p, p]
             L.attn_prefill_sinks.restype = i32
@@ -538,6 +554,227 @@ def attn_prefill_sinks(q, k, v, window, n_sinks, scale, out=None, err=None, stre
                                   _stream(stream))
     _check(rc, "attn_prefill_sinks")
     return out
+
+
+def attn_decode_shared_workspace_size(cache: KVCache, batch, q_rows, n_q_heads, max_seq_len,
+                                      max_prefix_len, window=0) -> int:
+    n = lib().attn_decode_shared_workspace_size(cache.packed(), batch, q_rows, n_q_heads,
+                                                cache.n_kv_heads, cache.head_dim, max_seq_len,
+                                                max_prefix_len, window)
+    if n == ctypes.c_size_t(-1).value:
+        raise AttnError(ATTN_ERR_SHAPE, "attn_decode_shared_workspace_size")
+    return int(n)
+
+
+def attn_decode_shared(q, cache: KVCache, seq_lens, positions, prefix_rows, prefix_lens,
+                       max_seq_len, max_prefix_len, window, scale, out=None, workspace=None,
+                       err=None, stream=None):
+    """attn_decode for a batch whose requests share prefixes: key position
+    t < prefix_lens[b] of request b is read where row prefix_rows[b] (of the
+    block table, or a window of a linear cache) has it, once for all
+    neighbouring requests with that row and length.  prefix_rows, prefix_lens
+    int32 [B]; max_prefix_len bounds the lengths.  A workspace (at least
+    attn_decode_shared_workspace_size bytes, zero-filled before its first use)
+    is allocated if not given."""
+    B, R, Hq, D = q.shape
+    if out is None:
+        out = _made(torch.empty_like, q, stream)
+    if workspace is None:
+        need = attn_decode_shared_workspace_size(cache, B, R, Hq, max_seq_len, max_prefix_len,
+                                                 window)
+        if need > 0:
+            workspace = _made(_zeroed, q, stream, need)
+    if workspace is not None:
+        c = _want_decode("attn_decode_shared", cache, q, out, seq_lens, positions, workspace)
+        if not (prefix_rows.dtype is prefix_lens.dtype is _I32 and
+                prefix_rows.get_device() == prefix_lens.get_device() == q.get_device() and
+                prefix_rows.is_contiguous() and prefix_lens.is_contiguous()):
+            _want("attn_decode_shared", _device(), _I32, prefix_rows, prefix_lens)
+        if prefix_rows.numel() < B or prefix_lens.numel() < B:
+            raise AttnError(ATTN_ERR_SHAPE, "attn_decode_shared: prefix_rows and prefix_lens are "
+                                            "[B]")
+    else:
+        c = cache.packed()
+    if cache.kind == PAGED:
+        t = cache.block_table
+        n_rows = 0 if t is None else t.numel() // max(1, t.shape[-1])
+    else:
+        n_rows = min(cache.num_slots // max(1, cache.slots_per_seq), (1 << 31) - 1)
+    rc = lib().attn_decode_shared(
+        _ptr(q), c, n_rows, _ptr(seq_lens), _ptr(positions), _ptr(prefix_rows),
+        _ptr(prefix_lens), B, R, int(max_seq_len), int(max_prefix_len), int(window), Hq,
+        cache.n_kv_heads, D, float(scale), _ptr(out), _ptr(workspace),
+        0 if workspace is None else workspace.nbytes, _ptr(err), _stream(stream))
+    _check(rc, "attn_decode_shared")
+    return out
+
+
+def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_len=0,
+                     beta_fast=32.0, beta_slow=1.0, device=None):
+    """(inv_freq, factor) of a Rope: base ** (-2 i / rot_dim), i < rot_dim / 2, as
+    float32 on `device`, changed for contexts `factor` times as long as a model was
+    trained on by `scaling`:
+      None      as they are
+      "linear"  all divided by factor (positions interpolated)
+      "ntk"     base * factor ** (rot_dim / (rot_dim - 2)), so that the slowest is
+                divided by factor and the fastest keeps its value
+      "yarn"    those that turn less than beta_slow times in original_len tokens
+                divided by factor, those that turn more than beta_fast times kept, a
+                linear ramp between (over i), and cosines and sines times
+                0.1 ln(factor) + 1 (YaRN, arXiv 2309.00071)"""
+    half = rot_dim // 2
+    if rot_dim < 0 or rot_dim % 2 or not base > 1 or not factor > 0 or \
+            scaling not in (None, "linear", "ntk", "yarn") or \
+            (scaling == "ntk" and rot_dim < 4) or \
+            (scaling == "yarn" and not (original_len > 0 and factor >= 1 and
+                                        beta_fast > beta_slow > 0)):
+        raise AttnError(ATTN_ERR_SHAPE, "rope_frequencies")
+    i = torch.arange(half, dtype=torch.float64)
+    times = 1.0
+    if scaling == "ntk":
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    inv = float(base) ** (-i / max(1, half))
+    if scaling == "linear":
+        inv = inv / factor
+    elif scaling == "yarn":
+        def turns_at(turns):  # the (fractional) i that turns so often in original_len
+            return half * math.log(original_len / (turns * 2 * math.pi)) / math.log(base)
+
+        lo = max(math.floor(turns_at(beta_fast)), 0)
+        hi = max(min(math.ceil(turns_at(beta_slow)), rot_dim - 1), lo + 1e-3)
+        slow = ((i - lo) / (hi - lo)).clamp(0, 1)
+        inv = inv * (1 - slow) + inv / factor * slow
+        times = 0.1 * math.log(factor) + 1.0
+    return inv.float().to(device), times
+
+
+class Rope:
+    """What attn_qk_rope does to a head's rows: rotary embedding of the first
+    2 * len(inv_freq) dims (inv_freq float32 on the device, None: no rotation),
+    paired as layout says, cosines and sines times factor; RMS norms with q_weight
+    and k_weight (float32 [head_dim], None: not normalised) and eps."""
+
+    def __init__(self, inv_freq, layout=ATTN_ROPE_HALF, factor=1.0, q_weight=None, k_weight=None,
+                 eps=1e-6):
+        self.inv_freq, self.layout, self.factor = inv_freq, int(layout), float(factor)
+        self.q_weight, self.k_weight, self.eps = q_weight, k_weight, float(eps)
+
+    @property
+    def rot_dim(self):
+        return 0 if self.inv_freq is None else 2 * self.inv_freq.numel()
+
+    def _packed(self, where, device, head_dim):
+        given = [t for t in (self.inv_freq, self.q_weight, self.k_weight) if t is not None]
+        _want(where, device, torch.float32, *given)
+        for t in (self.q_weight, self.k_weight):
+            if t is not None and t.numel() != head_dim:
+                raise AttnError(ATTN_ERR_SHAPE, f"{where}: q_weight and k_weight are [{head_dim}]")
+        return _PACK_ROPE(_ptr(self.inv_freq) or 0, self.rot_dim, self.layout, self.factor,
+                          _ptr(self.q_weight) or 0, _ptr(self.k_weight) or 0, self.eps)
+
+
+def _want_heads(where, device, n, *tensors):
+    """Refuses q, k or v that are not bf16 rows [n, heads, head_dim] whose heads stand
+    next to each other; returns the strides of their tokens."""
+    strides = []
+    for t in tensors:
+        if t.dtype is not _BF16 or t.get_device() != device or t.dim() != 3:
+            raise AttnError(ATTN_ERR_UNSUPPORTED, f"{where}: q, k and v are bf16 [n, heads, "
+                                                  "head_dim] on the current device")
+        _, heads, dim = t.shape
+        if t.shape[0] != n or dim != tensors[0].shape[2]:
+            raise AttnError(ATTN_ERR_SHAPE, f"{where}: q, k and v have n rows and one head_dim")
+        step, of_head, of_dim = t.stride()
+        if n and ((dim > 1 and of_dim != 1) or (heads > 1 and of_head != dim)):
+            raise AttnError(ATTN_ERR_UNSUPPORTED, f"{where}: a token's heads are not contiguous")
+        strides.append(step if n > 1 else heads * dim)
+    return strides
+
+
+def _new_like(t, shape):
+    return torch.empty(shape, dtype=t.dtype, device=t.device)
+
+
+def attn_qk_rope(q, k, positions, rope: Rope, q_out=None, k_out=None, stream=None):
+    """Norms and rotary embedding of q bf16 [n, Hq, D] and k bf16 [n, Hkv, D] at
+    positions int32 [n] (what Rope says, in one pass).  The tokens of q and k may be
+    any stride apart (views of a fused projection).  Returns (q_out, k_out),
+    contiguous; either may be its input (in place)."""
+    n, Hq, D = q.shape
+    device = _device()
+    qs, ks = _want_heads("attn_qk_rope", device, n, q, k)
+    if q_out is None:
+        q_out = _made(_new_like, q, stream, q.shape)
+    if k_out is None:
+        k_out = _made(_new_like, k, stream, k.shape)
+    _want("attn_qk_rope", device, _BF16, q_out, k_out)
+    _want("attn_qk_rope", device, _I32, positions)
+    if q_out.shape != q.shape or k_out.shape != k.shape or positions.numel() < n:
+        raise AttnError(ATTN_ERR_SHAPE, "attn_qk_rope: q_out and k_out are shaped like q and k, "
+                                        "positions is [n]")
+    rc = lib().attn_qk_rope(_ptr(q), qs, _ptr(k), ks, _ptr(positions), n,
+                            rope._packed("attn_qk_rope", device, D), Hq,
+                            k.shape[1], D, _ptr(q_out), _ptr(k_out), _stream(stream))
+    _check(rc, "attn_qk_rope")
+    return q_out, k_out
+
+
+def attn_qk_rope_append(q, k, v, positions, slot_mapping, cache: KVCache, rope: Rope, q_out=None,
+                        k_out=None, err=None, stream=None):
+    """attn_qk_rope, then attn_kv_append of the new keys and of v bf16 [n, Hkv, D]
+    at slot_mapping int64 [n], in one launch (two for caches with scales).  k_out, if
+    given, receives the new keys too.  Returns q_out."""
+    n, Hq, D = q.shape
+    where, device = "attn_qk_rope_append", _device()
+    scaled = cache.dtype in _SCALED
+    if scaled and n > 1 and not v.is_contiguous():
+        v = _made(torch.Tensor.contiguous, v, stream)
+    qs, ks, vs = _want_heads(where, device, n, q, k, v)
+    if q_out is None:
+        q_out = _made(_new_like, q, stream, q.shape)
+    if k_out is None and scaled:
+        k_out = _made(_new_like, k, stream, k.shape)
+    _want(where, device, _BF16, q_out, *(() if k_out is None else (k_out,)))
+    _want(where, device, _I32, positions)
+    _want(where, device, _I64, slot_mapping)
+    known = cache._known(where, device)
+    if k.shape != v.shape or k.shape[1] != known[6][1] or D != known[6][-1]:
+        raise AttnError(ATTN_ERR_SHAPE, f"{where}: k and v are [n, {known[6][1]}, {known[6][-1]}]")
+    if q_out.shape != q.shape or (k_out is not None and k_out.shape != k.shape) or \
+            positions.numel() < n or slot_mapping.numel() < n:
+        raise AttnError(ATTN_ERR_SHAPE, f"{where}: q_out and k_out are shaped like q and k, "
+                                        "positions and slot_mapping are [n]")
+    rc = lib().attn_qk_rope_append(
+        _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(positions), _ptr(slot_mapping), n,
+        rope._packed(where, device, D), known[7], Hq, k.shape[1], D,
+        _ptr(q_out), _ptr(k_out), _ptr(err), _stream(stream))
+    _check(rc, where)
+    return q_out
+
+
+def attn_kv_read(slot_mapping, cache: KVCache, k_out=None, v_out=None, err=None, stream=None):
+    """(k_out, v_out) bf16 [n, Hkv, D]: the cache's rows at slot_mapping int64 [n], for
+    8-bit caches the values of their codes (keys plus k_ref).  Slots outside the cache
+    give zeros and ATTN_ERR_BOUNDS in err."""
+    where, device = "attn_kv_read", _device()
+    known = cache._known(where, device)
+    _want(where, device, _I64, slot_mapping)
+    shape = (slot_mapping.numel(), known[6][1], known[6][-1])
+    if k_out is None:
+        k_out = _made(_rows_like, slot_mapping, stream, shape)
+    if v_out is None:
+        v_out = _made(_rows_like, slot_mapping, stream, shape)
+    _want(where, device, _BF16, k_out, v_out)
+    if k_out.shape != shape or v_out.shape != shape:
+        raise AttnError(ATTN_ERR_SHAPE, f"{where}: k_out and v_out are {shape}")
+    rc = lib().attn_kv_read(_ptr(slot_mapping), shape[0], known[7], shape[1], shape[2],
+                            _ptr(k_out), _ptr(v_out), _ptr(err), _stream(stream))
+    _check(rc, where)
+    return k_out, v_out
+
+
+def _rows_like(t, shape):
+    return torch.empty(shape, dtype=_BF16, device=t.device)
 
 
 def _want_rows(where, block_table, refs, rows, a, b):

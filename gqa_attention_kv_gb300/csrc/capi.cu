@@ -447,6 +447,212 @@ int attn_decode_sinks(const void *q, const attn_kv_cache *cache, const int32_t *
 
 namespace {
 
+// What shared prefixes ask beyond check_decode_shape.
+int check_shared(const attn_kv_cache *cache, int batch, int n_q_heads, int n_kv_heads,
+                 int max_prefix_len) {
+    if (max_prefix_len < 0) return ATTN_ERR_SHAPE;
+    if (cache->kind == ATTN_CACHE_RING) return ATTN_ERR_UNSUPPORTED;
+    if (batch > 4096 || n_q_heads / n_kv_heads > 128) return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+// [a, a + an) and [b, b + bn) have a byte in common.
+bool overlap(const void *a, int64_t an, const void *b, int64_t bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && an > 0 && bn > 0 && x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
+}
+
+// The arguments attn_qk_rope and attn_qk_rope_append share (n > 0).
+int check_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+               int64_t v_stride, const int32_t *positions, int64_t n, const attn_rope *rope,
+               int n_q_heads, int n_kv_heads, int head_dim, const void *q_out, const void *k_out) {
+    if (!q || !k || !positions || !q_out) return ATTN_ERR_NULL;
+    if (rope->rot_dim > 0 && !rope->inv_freq) return ATTN_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_out))
+        return ATTN_ERR_ALIGN;
+    for (const void *f : {static_cast<const void *>(rope->inv_freq),
+                          static_cast<const void *>(rope->q_weight),
+                          static_cast<const void *>(rope->k_weight)})
+        if (reinterpret_cast<uintptr_t>(f) & 3u) return ATTN_ERR_ALIGN;
+    const int64_t q_row = (int64_t)n_q_heads * head_dim, k_row = (int64_t)n_kv_heads * head_dim;
+    if (n > 1 && (q_stride < q_row || k_stride < k_row || q_stride % 8 || k_stride % 8))
+        return ATTN_ERR_SHAPE;
+    if (n > 1 && v && (v_stride < k_row || v_stride % 8)) return ATTN_ERR_SHAPE;
+    // outputs beside the inputs, or exactly in their place
+    const int64_t q_in = 2 * ((n - 1) * q_stride + q_row), k_in = 2 * ((n - 1) * k_stride + k_row),
+                  v_in = 2 * ((n - 1) * v_stride + k_row);
+    const int64_t q_bytes = 2 * n * q_row, k_bytes = 2 * n * k_row;
+    if (overlap(q_out, q_bytes, k_out, k_bytes) || overlap(q_out, q_bytes, k, k_in) ||
+        overlap(q_out, q_bytes, v, v_in) || overlap(k_out, k_bytes, q, q_in) ||
+        overlap(k_out, k_bytes, v, v_in))
+        return ATTN_ERR_SHAPE;
+    if (overlap(q_out, q_bytes, q, q_in) && (q_out != q || (n > 1 && q_stride != q_row)))
+        return ATTN_ERR_SHAPE;
+    if (overlap(k_out, k_bytes, k, k_in) && (k_out != k || (n > 1 && k_stride != k_row)))
+        return ATTN_ERR_SHAPE;
+    return ATTN_OK;
+}
+
+// ... and those that hold whatever n is.
+int check_rope_shape(int64_t n, const attn_rope *rope, int n_q_heads, int n_kv_heads,
+                     int head_dim) {
+    if (!rope) return ATTN_ERR_NULL;
+    if (n < 0 || n_q_heads < 1 || n_kv_heads < 1 || n_q_heads > (1 << 20) ||
+        n_kv_heads > (1 << 20) || n > (int64_t(1) << 31))
+        return ATTN_ERR_SHAPE;
+    if (head_dim != 64 && head_dim != 128) return ATTN_ERR_UNSUPPORTED;
+    if (rope->layout != ATTN_ROPE_PAIRS && rope->layout != ATTN_ROPE_HALF)
+        return ATTN_ERR_UNSUPPORTED;
+    if (rope->rot_dim < 0 || rope->rot_dim > head_dim || rope->rot_dim % 2 ||
+        !std::isfinite(rope->factor))
+        return ATTN_ERR_SHAPE;
+    if ((rope->q_weight || rope->k_weight) && !(rope->eps >= 1e-30f && std::isfinite(rope->eps)))
+        return ATTN_ERR_SHAPE;
+    return ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t attn_decode_shared_workspace_size(const attn_kv_cache *cache, int batch, int q_rows,
+                                         int n_q_heads, int n_kv_heads, int head_dim,
+                                         int max_seq_len, int max_prefix_len, int window) {
+    gqa::SharedPlan plan;
+    if (check_decode_shape(cache, batch, q_rows, n_q_heads, n_kv_heads, head_dim, max_seq_len,
+                           window) != ATTN_OK ||
+        check_shared(cache, batch, n_q_heads, n_kv_heads, max_prefix_len) != ATTN_OK)
+        return (size_t)-1;
+    if (batch == 0) return 0;
+    if (gqa::plan_shared(cache, batch, q_rows, n_q_heads, n_kv_heads, head_dim, max_seq_len,
+                         max_prefix_len, window, &plan) != ATTN_OK)
+        return (size_t)-1;
+    return plan.workspace;
+}
+
+int attn_decode_shared(const void *q, const attn_kv_cache *cache, int n_rows,
+                       const int32_t *seq_lens, const int32_t *positions,
+                       const int32_t *prefix_rows, const int32_t *prefix_lens, int batch,
+                       int q_rows, int max_seq_len, int max_prefix_len, int window, int n_q_heads,
+                       int n_kv_heads, int head_dim, float scale, void *out, void *workspace,
+                       size_t workspace_bytes, int32_t *err_word, attn_stream_t stream) {
+    int rc = check_decode_shape(cache, batch, q_rows, n_q_heads, n_kv_heads, head_dim,
+                                max_seq_len, window);
+    if (rc == ATTN_OK) rc = check_shared(cache, batch, n_q_heads, n_kv_heads, max_prefix_len);
+    if (rc != ATTN_OK) return rc;
+    gqa::DecodePlan decode;
+    rc = gqa::validate_decode(q, cache, seq_lens, positions, batch, q_rows, max_seq_len, window,
+                              n_q_heads, n_kv_heads, head_dim, scale, out, &decode);
+    if (rc != ATTN_OK) return rc;
+    if (n_rows < batch || (cache->kind == ATTN_CACHE_LINEAR &&
+                           (int64_t)n_rows * cache->slots_per_seq > cache->num_slots))
+        return ATTN_ERR_SHAPE;
+    if (batch == 0) return ATTN_OK;
+    if (!prefix_rows || !prefix_lens) return ATTN_ERR_NULL;
+    if (gqa::kv_scaled(cache->dtype))
+        if (rc = check_scaled(cache, true); rc != ATTN_OK) return rc;
+    gqa::SharedPlan plan;
+    rc = gqa::plan_shared(cache, batch, q_rows, n_q_heads, n_kv_heads, head_dim, max_seq_len,
+                          max_prefix_len, window, &plan);
+    if (rc != ATTN_OK) return rc;
+    if (!workspace) return ATTN_ERR_NULL;
+    if (workspace_bytes < plan.workspace) return ATTN_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return ATTN_ERR_ALIGN;
+    return gqa::launch_shared(plan, q, cache, n_rows, seq_lens, positions, prefix_rows,
+                              prefix_lens, batch, q_rows, max_seq_len, max_prefix_len, window,
+                              n_q_heads, n_kv_heads, head_dim, scale, out, workspace, err_word,
+                              reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_qk_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                 const int32_t *positions, int64_t n, const attn_rope *rope, int n_q_heads,
+                 int n_kv_heads, int head_dim, void *q_out, void *k_out, attn_stream_t stream) {
+    if (int rc = check_rope_shape(n, rope, n_q_heads, n_kv_heads, head_dim); rc != ATTN_OK)
+        return rc;
+    if (n == 0) return ATTN_OK;
+    if (!k_out) return ATTN_ERR_NULL;
+    if (int rc = check_rope(q, q_stride, k, k_stride, nullptr, 0, positions, n, rope, n_q_heads,
+                            n_kv_heads, head_dim, q_out, k_out);
+        rc != ATTN_OK)
+        return rc;
+    return gqa::launch_qk_rope(q, q_stride, k, k_stride, nullptr, 0, positions, nullptr, n, rope,
+                               nullptr, n_q_heads, n_kv_heads, head_dim, q_out, k_out, nullptr,
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_qk_rope_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                        const void *v, int64_t v_stride, const int32_t *positions,
+                        const int64_t *slot_mapping, int64_t n, const attn_rope *rope,
+                        const attn_kv_cache *cache, int n_q_heads, int n_kv_heads, int head_dim,
+                        void *q_out, void *k_out, int32_t *err_word, attn_stream_t stream) {
+    if (!cache) return ATTN_ERR_NULL;
+    if (int rc = check_rope_shape(n, rope, n_q_heads, n_kv_heads, head_dim); rc != ATTN_OK)
+        return rc;
+    const bool scaled = gqa::kv_scaled(cache->dtype);
+    if (cache->dtype != ATTN_KV_BF16 && cache->dtype != ATTN_KV_FP8_E4M3 && !scaled)
+        return ATTN_ERR_UNSUPPORTED;
+    if (cache->dtype == ATTN_KV_FP8_E4M3 && head_dim != 128) return ATTN_ERR_UNSUPPORTED;
+    if (cache->num_slots < 1) return ATTN_ERR_SHAPE;
+    if (int rc = check_layout(cache); rc != ATTN_OK) return rc;
+    if (n == 0) return ATTN_OK;
+    if (!v || !slot_mapping || !cache->k || !cache->v || (scaled && !k_out)) return ATTN_ERR_NULL;
+    if (!aligned16(cache->k) || !aligned16(cache->v) ||
+        (cache->dtype == ATTN_KV_FP8_E4M3 && cache->k_ref && !aligned16(cache->k_ref)))
+        return ATTN_ERR_ALIGN;
+    if (int rc = check_rope(q, q_stride, k, k_stride, v, v_stride, positions, n, rope, n_q_heads,
+                            n_kv_heads, head_dim, q_out, k_out);
+        rc != ATTN_OK)
+        return rc;
+    if (scaled) {
+        if (int rc = check_scaled(cache, true); rc != ATTN_OK) return rc;
+        if (n > 1 && v_stride != (int64_t)n_kv_heads * head_dim) return ATTN_ERR_UNSUPPORTED;
+        if (int rc = gqa::launch_qk_rope(q, q_stride, k, k_stride, nullptr, 0, positions, nullptr,
+                                         n, rope, nullptr, n_q_heads, n_kv_heads, head_dim, q_out,
+                                         k_out, nullptr, reinterpret_cast<cudaStream_t>(stream));
+            rc != ATTN_OK)
+            return rc;
+        return gqa::launch_kv_append_scaled(k_out, v, slot_mapping, n, cache, n_kv_heads, head_dim,
+                                            err_word, reinterpret_cast<cudaStream_t>(stream));
+    }
+    return gqa::launch_qk_rope(q, q_stride, k, k_stride, v, v_stride, positions, slot_mapping, n,
+                               rope, cache, n_q_heads, n_kv_heads, head_dim, q_out, k_out,
+                               err_word, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_kv_read(const int64_t *slot_mapping, int64_t n, const attn_kv_cache *cache,
+                 int n_kv_heads, int head_dim, void *k_out, void *v_out, int32_t *err_word,
+                 attn_stream_t stream) {
+    if (!cache) return ATTN_ERR_NULL;
+    if (n < 0 || n_kv_heads < 1 || n_kv_heads > (1 << 20)) return ATTN_ERR_SHAPE;
+    if (head_dim != 64 && head_dim != 128) return ATTN_ERR_UNSUPPORTED;
+    const bool scaled = gqa::kv_scaled(cache->dtype);
+    if (cache->dtype != ATTN_KV_BF16 && cache->dtype != ATTN_KV_FP8_E4M3 && !scaled)
+        return ATTN_ERR_UNSUPPORTED;
+    if (cache->dtype == ATTN_KV_FP8_E4M3 && head_dim != 128) return ATTN_ERR_UNSUPPORTED;
+    if (n == 0) return ATTN_OK;
+    if (!slot_mapping || !cache->k || !cache->v || !k_out || !v_out) return ATTN_ERR_NULL;
+    if (cache->num_slots < 1) return ATTN_ERR_SHAPE;
+    if (int rc = check_layout(cache); rc != ATTN_OK) return rc;
+    if (!aligned16(cache->k) || !aligned16(cache->v) || !aligned16(k_out) || !aligned16(v_out) ||
+        (cache->dtype != ATTN_KV_BF16 && cache->k_ref && !aligned16(cache->k_ref)))
+        return ATTN_ERR_ALIGN;
+    if (scaled)
+        if (int rc = check_scaled(cache, true); rc != ATTN_OK) return rc;
+    const int64_t bytes = 2 * n * n_kv_heads * head_dim;
+    const int64_t held = cache->num_slots * n_kv_heads * head_dim *
+                         (cache->dtype == ATTN_KV_BF16 ? 2 : 1);
+    for (const void *to : {k_out, v_out})
+        if (overlap(to, bytes, cache->k, held) || overlap(to, bytes, cache->v, held))
+            return ATTN_ERR_SHAPE;
+    if (overlap(k_out, bytes, v_out, bytes)) return ATTN_ERR_SHAPE;
+    return gqa::launch_kv_read(slot_mapping, n, cache, n_kv_heads, head_dim, k_out, v_out,
+                               err_word, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
+
+namespace {
+
 int prefill(const void *q, const void *k, const void *v, int batch, int seq_len, int window,
             int n_sinks, int n_q_heads, int n_kv_heads, int head_dim, float scale, void *out,
             int32_t *err_word, attn_stream_t stream) {

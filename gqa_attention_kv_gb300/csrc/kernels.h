@@ -176,6 +176,32 @@ int launch_attend(const AttendPlan &plan, const void *q, const attn_kv_cache *ca
                   int window, int sinks, int n_q_heads, int n_kv_heads, int head_dim, float scale,
                   void *out, void *workspace, int32_t *err, cudaStream_t stream);
 
+// Norms and rotary embedding of q and k (rope.cu); cache null: none is written to.
+int launch_qk_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                   int64_t v_stride, const int32_t *positions, const int64_t *slot_mapping,
+                   int64_t n, const attn_rope *r, const attn_kv_cache *cache, int n_q_heads,
+                   int n_kv_heads, int head_dim, void *q_out, void *k_out, int32_t *err,
+                   cudaStream_t stream);
+
+// Cache slots as bf16 rows (read.cu).
+int launch_kv_read(const int64_t *slot_mapping, int64_t n, const attn_kv_cache *cache,
+                   int n_kv_heads, int head_dim, void *k_out, void *v_out, int32_t *err,
+                   cudaStream_t stream);
+
+// Decode with shared prefixes (shared.cu).
+struct SharedPlan {
+    size_t workspace;
+};
+
+int plan_shared(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads, int n_kv_heads,
+                int head_dim, int max_seq_len, int max_prefix_len, int window, SharedPlan *plan);
+
+int launch_shared(const SharedPlan &plan, const void *q, const attn_kv_cache *cache, int n_rows,
+                  const int32_t *seq_lens, const int32_t *positions, const int32_t *prefix_rows,
+                  const int32_t *prefix_lens, int batch, int q_rows, int max_seq_len,
+                  int max_prefix_len, int window, int n_q_heads, int n_kv_heads, int head_dim,
+                  float scale, void *out, void *workspace, int32_t *err, cudaStream_t stream);
+
 // Page operations (pages.cu).
 int launch_pages_free(int32_t *block_table, int max_blocks, int table_rows, const int32_t *rows,
                       const int32_t *from_block, const int32_t *to_block, int n, int32_t *refs,

@@ -13,6 +13,11 @@
  *   attn_decode_sinks, attn_prefill_sinks
  *                   the same under a sliding window whose first few tokens
  *                   (sinks) stay visible
+ *   attn_decode_shared  decode for a batch whose requests share prefixes
+ *   attn_qk_rope, attn_qk_rope_append
+ *                   norms of q and k for each head and their rotary embedding,
+ *                   the keys and values written to the cache by the same launch
+ *   attn_kv_read    cache slots read back as bf16 rows
  *   attn_pages_*    pages of a paged cache: reserved, freed, forked, compacted
  *                   and copied on the device
  *
@@ -217,6 +222,92 @@ int attn_kv_append(const void *k_new, const void *v_new, const int64_t *slot_map
  */
 int attn_kv_reference(const void *k, int64_t n, int n_kv_heads, int head_dim, float *ref,
                       attn_stream_t stream);
+
+/*
+ * attn_kv_read -- rows of a cache as bf16: the inverse of attn_kv_append, for
+ * every dtype, kind and layout (a prefix kept in 8 bits as the keys and values
+ * of a prefill; a request moved to another cache).  The pages have no
+ * counterpart to it.
+ *
+ *   slot_mapping  int64 [n], device
+ *   k_out, v_out  bf16 [n, n_kv_heads, head_dim], device: row i is slot
+ *                 slot_mapping[i], its elements or code (times the scale of its
+ *                 block and head, one below 2^-64 read as 2^-64), for keys plus
+ *                 k_ref, in float32, rounded once.  A slot outside the cache
+ *                 gives a row of zeros and stores ATTN_ERR_BOUNDS in *err_word.
+ *   n             rows to read (0 is a no-op).  A slot may be read many times.
+ * The outputs do not overlap the cache.  k_ref is 16-byte aligned.
+ */
+int attn_kv_read(const int64_t *slot_mapping, int64_t n, const attn_kv_cache *cache,
+                 int n_kv_heads, int head_dim, void *k_out, void *v_out, int32_t *err_word,
+                 attn_stream_t stream);
+
+typedef enum {
+    ATTN_ROPE_PAIRS = 0, /* dims 2i and 2i + 1 of a head turn together */
+    ATTN_ROPE_HALF = 1   /* dims i and i + rot_dim / 2 do */
+} attn_rope_layout;
+
+/*
+ * What attn_qk_rope does to the rows of a head (read on the host during the
+ * call; the arrays are device memory, 4-byte aligned):
+ *   norm      x <- x * weight / sqrt(mean(x^2) + eps), where q_weight (for q) or
+ *             k_weight (for k) is not NULL
+ *   rotation  of the first rot_dim dims, by the angles a_i = p * inv_freq[i] at
+ *             position p: (x1, x2) <- factor * (x1 cos a_i - x2 sin a_i,
+ *                                               x2 cos a_i + x1 sin a_i)
+ * inv_freq holds whatever a model's long-context scaling makes of the
+ * frequencies (finite, magnitudes up to 2^16), factor what it multiplies the
+ * cosines and sines with (1 without).  Angles are exact to 2^-31 of a turn at
+ * every int32 position, so far positions lose nothing.  Arithmetic is float32,
+ * rounded once to bf16.
+ */
+typedef struct {
+    const float *inv_freq;  /* [rot_dim / 2]; NULL with rot_dim 0 */
+    int32_t rot_dim;        /* even, 0 .. head_dim */
+    int32_t layout;         /* attn_rope_layout */
+    float factor;           /* finite */
+    const float *q_weight;  /* [head_dim], or NULL: q is not normalised */
+    const float *k_weight;  /* [head_dim], or NULL: k is not normalised */
+    float eps;              /* finite, at least 1e-30 (read with weights only) */
+} attn_rope;
+
+/*
+ * attn_qk_rope -- norms of queries and keys for each head and their rotary
+ * embedding, in one pass (Voxtral notes, "RoPE", whose interleaved pairs are
+ * ATTN_ROPE_PAIRS; the norms and the other layout have no counterpart on the
+ * pages).
+ *
+ *   q, k       bf16, device, n tokens: token i's heads stand one after another
+ *              (n_q_heads or n_kv_heads rows of head_dim) at element
+ *              i * q_stride (k_stride): the rows of a fused projection need no
+ *              copy.  Strides are multiples of 8 and at least a token's row;
+ *              bases are 16-byte aligned.
+ *   positions  int32 [n], device
+ *   n          tokens (0 is a no-op)
+ *   q_out      bf16 [n, n_q_heads, head_dim]; k_out bf16 [n, n_kv_heads,
+ *              head_dim].  Each may be its own input where that is contiguous
+ *              (in place); other overlaps of outputs and inputs are refused
+ *              (ATTN_ERR_SHAPE).
+ * attn_qk_rope_append -- the same, and attn_kv_append of the new keys and of v
+ * into the cache, by the same launch: exactly the rows that attn_qk_rope and
+ * attn_kv_append give.  v's rows are laid out like k's, v_stride apart.
+ *   slot_mapping  as attn_kv_append's (out-of-range slots skip the cache's row
+ *                 and store ATTN_ERR_BOUNDS in *err_word; q_out and k_out are
+ *                 written all the same)
+ *   k_out         may be NULL, but for caches with scales, whose blocks are
+ *                 encoded by a second launch that reads it; there v is
+ *                 contiguous (v_stride n_kv_heads * head_dim,
+ *                 ATTN_ERR_UNSUPPORTED otherwise).
+ * Every cache dtype, kind and layout.
+ */
+int attn_qk_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                 const int32_t *positions, int64_t n, const attn_rope *rope, int n_q_heads,
+                 int n_kv_heads, int head_dim, void *q_out, void *k_out, attn_stream_t stream);
+int attn_qk_rope_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                        const void *v, int64_t v_stride, const int32_t *positions,
+                        const int64_t *slot_mapping, int64_t n, const attn_rope *rope,
+                        const attn_kv_cache *cache, int n_q_heads, int n_kv_heads, int head_dim,
+                        void *q_out, void *k_out, int32_t *err_word, attn_stream_t stream);
 
 /*
  * attn_decode_workspace_size -- bytes of device scratch attn_decode needs for
@@ -478,6 +569,47 @@ int attn_decode_sinks(const void *q, const attn_kv_cache *cache, const int32_t *
                       int n_sinks, int n_q_heads, int n_kv_heads, int head_dim, float scale,
                       void *out, void *workspace, size_t workspace_bytes, int32_t *err_word,
                       attn_stream_t stream);
+
+/*
+ * attn_decode_shared -- attn_decode for a batch whose requests share prefixes
+ * (an instruction text, the forks of one prompt): the keys that several requests
+ * begin with are read, and multiplied with all their rows, once.  The pages have
+ * no counterpart to it.
+ *
+ *   n_rows        rows of the block table (PAGED) or windows of slots_per_seq
+ *                 slots (LINEAR): batch of them at least.  A prefix may lie in a
+ *                 row that is no request of the batch.
+ *   prefix_rows   int32 [batch], device: in [0, n_rows)
+ *   prefix_lens   int32 [batch], device: in [0, max_prefix_len].  Key position
+ *                 t < prefix_lens[b] of request b is read where row
+ *                 prefix_rows[b] has it, every other where request b has it.
+ *                 0: the request shares nothing (its prefix_rows entry is not
+ *                 looked at).  Request b's own slots or table entries before its
+ *                 prefix's length are not read.
+ *                 Neighbouring requests with the same row and length are worked
+ *                 on together; order and grouping do not change what is computed.
+ *                 An entry outside its range stores ATTN_ERR_BOUNDS: a length is
+ *                 clipped, a prefix in a row that is not there is skipped.
+ *   max_prefix_len   host-side upper bound of prefix_lens[], >= 0
+ * Which keys a row attends is attn_decode's rule (seq_lens counts the prefix).
+ * LINEAR and PAGED caches of every dtype and layout; RING is not supported.
+ * n_q_heads / n_kv_heads at most 128, batch at most 4,096.
+ *   workspace: at least attn_decode_shared_workspace_size(...) bytes (which
+ *   returns (size_t)-1 for arguments this call would reject), 16-byte aligned,
+ *   zero-filled before its first use; one workspace may serve this call,
+ *   attn_decode and attn_decode_sinks.  Calls whose kernels overlap on the GPU,
+ *   graphs replayed at the same time among them, need separate workspaces.
+ * Every other argument and status is attn_decode's.
+ */
+size_t attn_decode_shared_workspace_size(const attn_kv_cache *cache, int batch, int q_rows,
+                                         int n_q_heads, int n_kv_heads, int head_dim,
+                                         int max_seq_len, int max_prefix_len, int window);
+int attn_decode_shared(const void *q, const attn_kv_cache *cache, int n_rows,
+                       const int32_t *seq_lens, const int32_t *positions,
+                       const int32_t *prefix_rows, const int32_t *prefix_lens, int batch,
+                       int q_rows, int max_seq_len, int max_prefix_len, int window, int n_q_heads,
+                       int n_kv_heads, int head_dim, float scale, void *out, void *workspace,
+                       size_t workspace_bytes, int32_t *err_word, attn_stream_t stream);
 
 /*
  * attn_prefill_sinks -- attn_prefill under a sliding window whose first n_sinks
