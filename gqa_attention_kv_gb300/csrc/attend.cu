@@ -125,6 +125,9 @@ struct Params {
     float *ws_o, *ws_lse;
     int2 *ws_parts;     // per unit: first and last CTA (merge kernel)
     int32_t *ws_count;  // per unit: parts stored (0 between calls), or nullptr: merge kernel
+    // only keys t >= from[b] (clipped to 0 .. from_cap), every unit left as parts; or nullptr
+    const int32_t *from;
+    int from_cap;
     int32_t *err;
 };
 
@@ -321,6 +324,10 @@ __device__ __forceinline__ Entry make_entry(const Params &p, int e, int rb_rows,
     t.lo = p.window > 0 ? max(0, min(t.hi, oldest - p.window + 1)) : 0;
     if (p.kind == ATTN_CACHE_RING)  // what the turning part of the ring still holds
         t.lo = max(t.lo, min(t.hi, len - (p.slots_per_seq - p.sinks)));
+    if (p.from != nullptr) {
+        t.lo = max(t.lo, max(0, min(p.from[b], p.from_cap)));
+        if (t.lo >= t.hi) t.lo = t.hi = 0;
+    }
     return t;
 }
 
@@ -1130,7 +1137,7 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
             sm.lse[h][row] = l == 0.f ? -INFINITY : m_use + log2f(l);
         }
         __syncthreads();
-        const bool whole = first == last;
+        const bool whole = first == last && p.from == nullptr;
         const int64_t slot = (int64_t)(unit + blockIdx.x) * HG;  // unique: shares are contiguous
         for (int i = threadIdx.x; i < HG * n_rows * (HD / 4); i += kThreads) {
             const int hr = i / (HD / 4), d = (i % (HD / 4)) * 4;
@@ -1353,11 +1360,14 @@ int plan_attend(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
     return ATTN_OK;
 }
 
-int launch_attend(const AttendPlan &plan, const void *q, const attn_kv_cache *cache,
-                  const int32_t *seq_lens, const int32_t *positions, int q_rows, int max_seq_len,
-                  int window, int sinks, int n_q_heads, int n_kv_heads, int head_dim, float scale,
-                  void *out, void *workspace, int32_t *err, cudaStream_t stream) {
-    att::Params p = {};
+namespace att {
+
+// The kernels' parameters but for the launch's entries.
+Params params_of(const AttendPlan &plan, const void *q, const attn_kv_cache *cache,
+                 const int32_t *seq_lens, const int32_t *positions, int q_rows, int max_seq_len,
+                 int window, int sinks, int n_q_heads, int n_kv_heads, float scale, void *out,
+                 void *workspace, int32_t *err) {
+    Params p = {};
     p.q = static_cast<const __nv_bfloat16 *>(q);
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.k = static_cast<const uint8_t *>(cache->k);
@@ -1402,36 +1412,74 @@ int launch_attend(const AttendPlan &plan, const void *q, const attn_kv_cache *ca
     p.ws_lse = reinterpret_cast<float *>(ws + plan.lse_offset);
     p.ws_o = reinterpret_cast<float *>(ws + plan.o_offset);
     p.err = err;
-    const int fmt = cache->dtype == ATTN_KV_BF16          ? att::kBF16
-                    : cache->dtype == ATTN_KV_INT8_SCALED ? att::kINT8
-                                                          : att::kE4M3;
+    return p;
+}
+
+// The launch of p.n_entries entries from p.e0 on; merge: and of the merge kernel.
+int run(const Params &p, const AttendPlan &plan, const attn_kv_cache *cache, int head_dim,
+        bool merge, cudaStream_t stream) {
+    int rc = ATTN_ERR_UNSUPPORTED;
+    auto go = [&](auto fmt_c) {
+        constexpr int F = decltype(fmt_c)::value;
+        if (head_dim == 128) {
+            rc = plan.mt == 0 ? launch<F, 128, 0, 1>(p, merge, stream)
+                              : launch<F, 128, 1, 1>(p, merge, stream);
+        } else if (plan.mt == 0) {
+            rc = plan.heads == 1 ? launch<F, 64, 0, 1>(p, merge, stream)
+                                 : launch<F, 64, 0, 2>(p, merge, stream);
+        } else {
+            if (plan.heads == 1)
+                rc = launch<F, 64, 1, 1>(p, merge, stream);
+            else if constexpr (F != kBF16)
+                rc = launch<F, 64, 1, 2>(p, merge, stream);
+        }
+    };
+    if (cache->dtype == ATTN_KV_BF16)
+        go(std::integral_constant<int, kBF16>{});
+    else if (cache->dtype == ATTN_KV_INT8_SCALED)
+        go(std::integral_constant<int, kINT8>{});
+    else
+        go(std::integral_constant<int, kE4M3>{});
+    return rc;
+}
+
+}  // namespace att
+
+int launch_attend(const AttendPlan &plan, const void *q, const attn_kv_cache *cache,
+                  const int32_t *seq_lens, const int32_t *positions, int q_rows, int max_seq_len,
+                  int window, int sinks, int n_q_heads, int n_kv_heads, int head_dim, float scale,
+                  void *out, void *workspace, int32_t *err, cudaStream_t stream) {
+    att::Params p = att::params_of(plan, q, cache, seq_lens, positions, q_rows, max_seq_len, window,
+                                   sinks, n_q_heads, n_kv_heads, scale, out, workspace, err);
     for (p.e0 = 0; p.e0 < plan.entries; p.e0 += plan.per_launch) {
         p.n_entries = std::min(plan.per_launch, plan.entries - p.e0);
-        int rc = ATTN_ERR_UNSUPPORTED;
-        auto run = [&](auto fmt_c) {
-            constexpr int F = decltype(fmt_c)::value;
-            if (head_dim == 128) {
-                rc = plan.mt == 0 ? att::launch<F, 128, 0, 1>(p, plan.merge, stream)
-                                  : att::launch<F, 128, 1, 1>(p, plan.merge, stream);
-            } else if (plan.mt == 0) {
-                rc = plan.heads == 1 ? att::launch<F, 64, 0, 1>(p, plan.merge, stream)
-                                     : att::launch<F, 64, 0, 2>(p, plan.merge, stream);
-            } else {
-                if (plan.heads == 1)
-                    rc = att::launch<F, 64, 1, 1>(p, plan.merge, stream);
-                else if constexpr (F != att::kBF16)
-                    rc = att::launch<F, 64, 1, 2>(p, plan.merge, stream);
-            }
-        };
-        if (fmt == att::kBF16)
-            run(std::integral_constant<int, att::kBF16>{});
-        else if (fmt == att::kE4M3)
-            run(std::integral_constant<int, att::kE4M3>{});
-        else
-            run(std::integral_constant<int, att::kINT8>{});
-        if (rc != ATTN_OK) return rc;
+        if (int rc = att::run(p, plan, cache, head_dim, plan.merge, stream); rc != ATTN_OK)
+            return rc;
     }
     return ATTN_OK;
+}
+
+int launch_attend_parts(const AttendPlan &plan, int e0, const int32_t *from, int from_cap,
+                        const void *q, const attn_kv_cache *cache, const int32_t *seq_lens,
+                        const int32_t *positions, int q_rows, int max_seq_len, int window,
+                        int n_q_heads, int n_kv_heads, int head_dim, float scale, void *out,
+                        void *workspace, int32_t *err, cudaStream_t stream, AttendParts *parts) {
+    att::Params p = att::params_of(plan, q, cache, seq_lens, positions, q_rows, max_seq_len, window,
+                                   0, n_q_heads, n_kv_heads, scale, out, workspace, err);
+    p.from = from;
+    p.from_cap = from_cap;
+    p.e0 = e0;
+    p.n_entries = std::min(plan.per_launch, plan.entries - e0);
+    parts->o = p.ws_o;
+    parts->lse = p.ws_lse;
+    parts->parts = p.ws_parts;
+    parts->rb = plan.mt == 0 ? 8 : 16;
+    parts->heads = plan.heads;
+    parts->row_blocks = plan.row_blocks;
+    parts->e0 = e0;
+    parts->n_entries = p.n_entries;
+    parts->held = cache->dtype == ATTN_KV_BF16 ? 0.f : att::kWeightLog2;
+    return att::run(p, plan, cache, head_dim, false, stream);
 }
 
 }  // namespace gqa

@@ -525,7 +525,7 @@ size_t attn_decode_shared_workspace_size(const attn_kv_cache *cache, int batch, 
         return (size_t)-1;
     if (batch == 0) return 0;
     if (gqa::plan_shared(cache, batch, q_rows, n_q_heads, n_kv_heads, head_dim, max_seq_len,
-                         max_prefix_len, window, &plan) != ATTN_OK)
+                         window, &plan) != ATTN_OK)
         return (size_t)-1;
     return plan.workspace;
 }
@@ -553,7 +553,7 @@ int attn_decode_shared(const void *q, const attn_kv_cache *cache, int n_rows,
         if (rc = check_scaled(cache, true); rc != ATTN_OK) return rc;
     gqa::SharedPlan plan;
     rc = gqa::plan_shared(cache, batch, q_rows, n_q_heads, n_kv_heads, head_dim, max_seq_len,
-                          max_prefix_len, window, &plan);
+                          window, &plan);
     if (rc != ATTN_OK) return rc;
     if (!workspace) return ATTN_ERR_NULL;
     if (workspace_bytes < plan.workspace) return ATTN_ERR_WORKSPACE;

@@ -176,6 +176,23 @@ int launch_attend(const AttendPlan &plan, const void *q, const attn_kv_cache *ca
                   int window, int sinks, int n_q_heads, int n_kv_heads, int head_dim, float scale,
                   void *out, void *workspace, int32_t *err, cudaStream_t stream);
 
+// What attend.cu leaves of keys at and behind a position of each request: partial states
+// for a merge of the caller's (unit = (entry, KV heads together), see attend_merge_kernel).
+struct AttendParts {
+    const float *o, *lse;
+    const int2 *parts;  // per unit: first and last (less than the first: none)
+    int rb, heads, row_blocks, e0, n_entries;
+    float held;  // lse holds log2 of the sum of weights times 2^held
+};
+
+// One launch of the plan, its entries from e0 on, over keys t >= from[b] (clipped to
+// 0 .. from_cap).
+int launch_attend_parts(const AttendPlan &plan, int e0, const int32_t *from, int from_cap,
+                        const void *q, const attn_kv_cache *cache, const int32_t *seq_lens,
+                        const int32_t *positions, int q_rows, int max_seq_len, int window,
+                        int n_q_heads, int n_kv_heads, int head_dim, float scale, void *out,
+                        void *workspace, int32_t *err, cudaStream_t stream, AttendParts *parts);
+
 // Norms and rotary embedding of q and k (rope.cu); cache null: none is written to.
 int launch_qk_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                    int64_t v_stride, const int32_t *positions, const int64_t *slot_mapping,
@@ -190,11 +207,12 @@ int launch_kv_read(const int64_t *slot_mapping, int64_t n, const attn_kv_cache *
 
 // Decode with shared prefixes (shared.cu).
 struct SharedPlan {
-    size_t workspace;
+    AttendPlan own;  // of the keys that are not shared
+    size_t rows_offset, lse_offset, o_offset, workspace;
 };
 
 int plan_shared(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads, int n_kv_heads,
-                int head_dim, int max_seq_len, int max_prefix_len, int window, SharedPlan *plan);
+                int head_dim, int max_seq_len, int window, SharedPlan *plan);
 
 int launch_shared(const SharedPlan &plan, const void *q, const attn_kv_cache *cache, int n_rows,
                   const int32_t *seq_lens, const int32_t *positions, const int32_t *prefix_rows,

@@ -2,14 +2,46 @@
 //
 // What is computed: attn_decode's softmax over the visible keys of each row, where key t of
 // request b lies in its own slots for t >= prefix_lens[b] and in those of row
-// prefix_rows[b] before.  The plainest form: a warp a query row and head, a running maximum
-// and sum in float32, every key read by every row.
+// prefix_rows[b] before.  A softmax over the union of two sets of keys is joined from their
+// states: with O, l the weighted sum and the sum of weights 2^(x - M) of a set,
+//     out = sum_s 2^(M_s) O_s / sum_s 2^(M_s) l_s.
+// The keys in front are common to all rows of a group (neighbouring requests with the same
+// row and length), so they are one dense contraction, N R G query rows of a KV head against
+// every key, and go to tcgen05 here; the keys behind are each request's own and go to
+// attend.cu; shared_merge_kernel joins the parts of both.
+//
+// GB300 mapping of the shared part.  A group's rows (N requests x R rows x G heads of a KV
+// head) are packed into the M dimension of 128-row tiles, 128 / G positions a tile: q viewed
+// as {D, heads, positions} gives a tile by one TMA box a 64 dims.  A CTA takes a pair of
+// such tiles of one KV head and a range of key tiles (128 keys); the ranges of all (group,
+// KV head, pair) fill the SMs once.  Where a group has one tile only, the CTA's two softmax
+// warpgroups take every other key tile of it each (with a state each): a lone tile's chain
+// product - softmax - product would else leave the tensor cores and the softmax waiting for
+// one another.
+//   warp 0       loads: TMA boxes of whole runs of keys (a page, or 128 of a linear cache), one
+//                a lane; where pages are no multiple of 8 keys, 16-byte cp.async by row
+//   warp 1       one thread issues tcgen05.mma: S = Q K^T, O += P V (f16, P from TMEM)
+//   warps 2, 3   bring what is loaded into the form that is multiplied: V of a bf16 cache to
+//                f16 in place, 8-bit codes to f16 (exact) from a ring of their own; keys
+//                outside the group's range become zeros
+//   warps 4..11  softmax, a thread a row of a tile; weights rounded once to f16 and written
+//                over S in TMEM
+// The plan is made on the device from lengths, rows and positions, by every CTA for itself
+// (a captured graph follows them); CTAs are persistent for batches of more pairs than SMs.
+//
+// Scales of 8-bit caches leave the products as in attend.cu: K's multiplies the scores, V's
+// enters the weights' exponent, l sums w / vs.  Weights are held times 2^7 (those down to
+// 2^-21 of the largest keep f16's 11 bits).  A CTA leaves O normalised by the plain sum of its
+// weights (at most the largest |v| or code, so f16 holds it: 2^-11, a quarter of the output's
+// bf16 half step), and the logarithms of both sums.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -17,108 +49,1177 @@
 namespace gqa {
 namespace shr {
 
+constexpr int kBM = 128;       // rows of a tile (two of them a CTA)
+constexpr int kBN = 128;       // keys of a tile
+constexpr int kThreads = 384;  // three warpgroups
+// As the chunk kernel: launched at 168 registers a thread, 4x32x96 + 8x32x200 = 63,488 <= 384x168
+constexpr uint32_t kRegsLaunch = 168;
+constexpr uint32_t kRegsControl = 96;
+constexpr uint32_t kRegsSoftmax = 200;
+constexpr int kTmemCols = 512;
+constexpr float kRescaleLog2 = 8.0f;    // the reference maximum moves past this only
+constexpr float kWeightLog2 = 7.0f;     // weights are held times 2^7: at most 2^15
+constexpr float kScoreTop = 0x1p24f;    // larger scores are reported (as in attend.cu)
+constexpr float kFactorTop = 0x1p90f;
+constexpr float kScaleFloor = 0x1p-64f; // the smallest scale
+constexpr float kPartWeight = 0x1p-12f;
+constexpr float kSmallest = 0x1p-149f;
+constexpr int kMaxBatch = 4096;         // requests: the plan's tables lie in the K and V rings
+
 enum Fmt { kBF16 = 0, kE4M3 = 1, kINT8 = 2 };
 
+template <int FMT, int HD>
+struct Cfg {
+    static constexpr bool kCodes = FMT != kBF16;
+    static constexpr int kHalves = HD / 64;
+    // bf16: the rings that TMA fills; 8-bit: f16 tiles converted from a ring of codes
+    static constexpr int kKStages = kCodes ? (HD == 128 ? 2 : 3) : HD == 128 ? 3 : 4;
+    static constexpr int kVStages = kCodes ? (HD == 128 ? 2 : 3) : HD == 128 ? 2 : 4;
+    static constexpr int kRawStages = kCodes ? (HD == 128 ? 2 : 6) : 0;
+    static constexpr int kQBytes = kBM * HD * 2;
+    static constexpr int kTileBytes = kBN * HD * 2;        // of K or V, 16 bits an element
+    static constexpr int kRawBytes = kCodes ? kBN * HD : 0;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffK = kOffQ + 2 * kQBytes;
+    static constexpr int kOffV = kOffK + kKStages * kTileBytes;
+    static constexpr int kOffRaw = kOffV + kVStages * kTileBytes;
+    static constexpr int kOffBar = kOffRaw + kRawStages * kRawBytes;
+    static constexpr int kNumBars = 3 * kKStages + 3 * kVStages + 2 * kRawStages + 10;
+    static constexpr size_t kSmem = 1024 + kOffBar + kNumBars * 8 + 16;
+    // the plan: 7 tables of a word a request, the chunks' masks and counts
+    static_assert(kOffBar - kOffK >= (7 * kMaxBatch + 8 + kMaxBatch / 32 * 2) * 4, "plan");
+};
+
 struct Params {
-    const __nv_bfloat16 *q;
-    __nv_bfloat16 *out;
+    int batch, q_rows, window, n_kv_heads, group, rt, sms;
+    int n_rows, slots_per_seq, block_size, max_blocks, num_pages, cap, prefix_cap;
+    int box_rows;  // keys of a TMA box; 0: rows are gathered
+    int map_rows;  // extent of the maps' second dimension
+    bool paged, head_major;
+    const int32_t *block_table, *seq_lens, *positions, *prefix_rows, *prefix_lens;
     const uint8_t *k, *v;
     const float *ks, *vs;
     int scale_shift;
-    int kind, slots_per_seq, block_size, max_blocks, num_pages, n_rows;
     KvPlace place;
-    const int32_t *block_table, *seq_lens, *positions, *prefix_rows, *prefix_lens;
-    int batch, q_rows, n_q_heads, n_kv_heads, group, window, max_seq_len, max_prefix_len;
     float scale_log2;
+    int4 *ws_rows;   // [batch * q_rows]: first row of ws_o for KV head 0, rows a part, parts
+    float2 *ws_lse;  // per row: log2 of the sum of weights, and of weights over scales
+    uint16_t *ws_o;  // per row: HD f16
     int32_t *err;
 };
 
+// What a CTA works on.
+struct Piece {
+    int start, n_pos;  // the group's first position (b * q_rows) and its positions
+    int prow, lo, hi;  // its prefix's row, the keys that some row of it may see
+    int kt0, n_kt;     // key tiles
+    int kvh, pair, split;
+    int parts, base;   // parts of a row, first row of ws_o
+};
+
+// The keys [lo, hi) of its prefix that some row of request b attends.
+__device__ __forceinline__ void request_range(const Params &p, int b, bool report, int &row,
+                                              int &plen, int &lo, int &hi) {
+    int len = p.seq_lens[b];
+    plen = p.prefix_lens[b];
+    row = p.prefix_rows[b];
+    bool odd = len < 0 || len > p.cap || plen < 0 || plen > p.prefix_cap;
+    len = max(0, min(len, p.cap));
+    plen = max(0, min(plen, p.prefix_cap));
+    int pmax = -1, oldest = INT32_MAX;
+    for (int r = 0; r < p.q_rows; ++r) {
+        const int pos = p.positions[(int64_t)b * p.q_rows + r];
+        pmax = max(pmax, pos);
+        if (pos >= 0) oldest = min(oldest, pos);
+    }
+    if (plen == 0) row = -1;
+    const bool absent = plen > 0 && (row < 0 || row >= p.n_rows);
+    if (report && (odd || absent)) report_error(p.err, ATTN_ERR_BOUNDS);
+    hi = absent ? 0 : (int)min((int64_t)min(len, plen), (int64_t)pmax + 1);
+    lo = p.window > 0 ? max(0, oldest - p.window + 1) : 0;
+    if (hi <= lo) hi = 0, lo = INT32_MAX;
+}
+
+// The plan: groups, their pieces, and the piece that is asked for (n_kt 0: none).  `mem` is
+// scratch in shared memory; every thread of the CTA calls this and passes its last barrier.
+// Of U units (group, KV head, pair of tiles) that weigh their key tiles each is cut into
+// 1 + floor((SMs - U) tiles / sum) pieces, so that all are at most the SMs, or U.
+__device__ void make_plan(const Params &p, int32_t *mem, int want, bool tables, Piece &mine,
+                          int &total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int B = p.batch, chunks = (B + 31) / 32;
+    int32_t *r_lo = mem, *r_hi = r_lo + kMaxBatch, *g_start = r_hi + kMaxBatch;
+    int32_t *g_lo = g_start + kMaxBatch + 8, *g_hi = g_lo + kMaxBatch, *g_parts = g_hi + kMaxBatch;
+    int32_t *g_base = g_parts + kMaxBatch, *c_mask = g_base + kMaxBatch;
+    int32_t *c_base = c_mask + kMaxBatch / 32;
+    __shared__ int s_groups, s_total;
+    __shared__ Piece s_mine;
+    for (int c = warp; c < chunks; c += kThreads / 32) {
+        const int b = c * 32 + lane;
+        bool first = false;
+        if (b < B) {
+            int row, plen, lo, hi;
+            request_range(p, b, blockIdx.x == 0 && tables, row, plen, lo, hi);
+            r_lo[b] = lo, r_hi[b] = hi;
+            g_lo[b] = INT32_MAX, g_hi[b] = 0;
+            first = b == 0;
+            if (!first) {
+                const int plen_b = max(0, min(p.prefix_lens[b - 1], p.prefix_cap));
+                first = plen != plen_b || (plen > 0 && row != p.prefix_rows[b - 1]);
+            }
+        }
+        const uint32_t mask = __ballot_sync(0xffffffffu, first);
+        if (lane == 0) c_mask[c] = (int32_t)mask;
+    }
+    if (threadIdx.x == 0) s_mine.n_kt = 0;
+    __syncthreads();
+    if (warp == 0) {
+        int carry = 0;
+        for (int c0 = 0; c0 < chunks; c0 += 32) {
+            const int n = c0 + lane < chunks ? __popc((uint32_t)c_mask[c0 + lane]) : 0;
+            int x = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (c0 + lane < chunks) c_base[c0 + lane] = carry + x - n;
+            carry += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0) {
+            s_groups = carry;
+            g_start[carry] = B;
+        }
+    }
+    __syncthreads();
+    auto group_of = [&](int b) {
+        const uint32_t upto = 0xffffffffu >> (31 - (b & 31));
+        return c_base[b >> 5] + __popc((uint32_t)c_mask[b >> 5] & upto) - 1;
+    };
+    for (int b = threadIdx.x; b < B; b += kThreads) {
+        const int g = group_of(b);
+        if ((uint32_t)c_mask[b >> 5] >> (b & 31) & 1u) g_start[g] = b;
+        if (r_hi[b] > 0) {
+            atomicMin(&g_lo[g], r_lo[b]);
+            atomicMax(&g_hi[g], r_hi[b]);
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const int groups = s_groups;
+        auto tiles_of = [&](int g) {
+            return g_hi[g] > 0 ? (g_hi[g] + kBN - 1) / kBN - g_lo[g] / kBN : 0;
+        };
+        auto pairs_of = [&](int g) {
+            return ((g_start[g + 1] - g_start[g]) * p.q_rows + 2 * p.rt - 1) / (2 * p.rt);
+        };
+        int64_t work = 0;
+        int units = 0;
+        for (int g = lane; g < groups; g += 32) {
+            const int t = tiles_of(g), u = t > 0 ? pairs_of(g) * p.n_kv_heads : 0;
+            units += u;
+            work += (int64_t)u * t;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            units += __shfl_xor_sync(0xffffffffu, units, o);
+            work += __shfl_xor_sync(0xffffffffu, work, o);
+        }
+        const int spare = max(0, p.sms - units);
+        int at = 0, row = 0;  // pieces and rows of ws_o before this round's groups
+        for (int g0 = 0; g0 < groups; g0 += 32) {
+            const int g = g0 + lane;
+            int n = 0, rows = 0, cut = 0, pairs = 0, tiles = 0, n_pos = 0;
+            bool two = false;
+            if (g < groups) tiles = tiles_of(g);
+            if (tiles > 0) {
+                n_pos = (g_start[g + 1] - g_start[g]) * p.q_rows;
+                pairs = pairs_of(g);
+                cut = (int)min((int64_t)tiles, 1 + (int64_t)spare * tiles / work);
+                n = pairs * p.n_kv_heads * cut;
+                two = n_pos <= p.rt;  // one tile: two parts a piece
+                rows = (two ? 2 : 1) * cut * p.n_kv_heads * n_pos * p.group;
+            }
+            int x = n, y = rows;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int a = __shfl_up_sync(0xffffffffu, x, o), b = __shfl_up_sync(0xffffffffu, y, o);
+                if (lane >= o) x += a, y += b;
+            }
+            const int before = at + x - n, base = row + y - rows;
+            if (g < groups) {
+                g_parts[g] = (two ? 2 : 1) * cut;
+                g_base[g] = base;
+            }
+            if (want >= before && want < before + n) {
+                const int i = want - before, unit = i / cut;
+                Piece m;
+                m.start = g_start[g] * p.q_rows;
+                m.n_pos = n_pos;
+                m.prow = p.prefix_rows[g_start[g]];
+                m.lo = g_lo[g], m.hi = g_hi[g];
+                m.split = i - unit * cut;
+                const int64_t t = tiles;
+                m.kt0 = m.lo / kBN + (int)(m.split * t / cut);
+                m.n_kt = m.lo / kBN + (int)((m.split + 1) * t / cut) - m.kt0;
+                m.kvh = unit / pairs;
+                m.pair = unit - m.kvh * pairs;
+                m.parts = (two ? 2 : 1) * cut;
+                m.base = base;
+                s_mine = m;
+            }
+            at += __shfl_sync(0xffffffffu, x, 31);
+            row += __shfl_sync(0xffffffffu, y, 31);
+        }
+        if (lane == 0) s_total = at;
+    }
+    __syncthreads();
+    // where the merge finds a position's parts
+    if (tables)
+        for (int i = blockIdx.x * kThreads + threadIdx.x; i < B * p.q_rows;
+             i += gridDim.x * kThreads) {
+            const int b = i / p.q_rows, g = group_of(b), n = g_start[g + 1] - g_start[g];
+            p.ws_rows[i] = make_int4(g_base[g] + (i - g_start[g] * p.q_rows) * p.group,
+                                     n * p.q_rows * p.group, g_parts[g], 0);
+        }
+    mine = s_mine;
+    total = s_total;
+}
+
+// Four codes -> two f16x2 words; exact.  INT8: a byte with its sign bit flipped is c + 128;
+// behind the byte 0x64 it is the f16 1024 + (c + 128).
+template <int FMT>
+__device__ __forceinline__ void codes_to_f16(uint32_t x, uint32_t &lo, uint32_t &hi) {
+    if constexpr (FMT == kE4M3) {
+        lo = e4m3x2_to_f16x2(x);
+        hi = e4m3x2_to_f16x2(x >> 16);
+    } else {
+        x ^= 0x80808080u;
+        const uint32_t bias = 0x64806480u;  // 1152, twice
+        lo = __byte_perm(x, 0x64646464u, 0x4140u);
+        hi = __byte_perm(x, 0x64646464u, 0x4342u);
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(bias));
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(bias));
+    }
+}
+
+// max(a, |b|, |c|), NaN if one is
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+    return d;
+}
+
+__device__ __forceinline__ float fast_log2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mbar_inval(uint64_t *bar) {
+    asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(on ? 16 : 0)
+                 : "memory");
+}
+
+// f16 words whose exponent is all ones become 0 in each half.
+__device__ __forceinline__ uint32_t drop_nan(uint32_t w) {
+    if ((w & 0x7C00u) == 0x7C00u) w &= 0xFFFF0000u;
+    if ((w & 0x7C000000u) == 0x7C000000u) w &= 0x0000FFFFu;
+    return w;
+}
+
 template <int FMT, int HD>
-__global__ void __launch_bounds__(128) shared_simple_kernel(const Params p) {
-    constexpr int V = HD / 32;
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const Params p) {
+    using C = Cfg<FMT, HD>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sQ = smem + C::kOffQ, *sK = smem + C::kOffK, *sV = smem + C::kOffV;
+    uint8_t *sRaw = smem + C::kOffRaw;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
+    uint64_t *k_full = bars;                     // [kKStages] loaded (bf16)
+    uint64_t *k_empty = k_full + C::kKStages;    // [kKStages] multiplied
+    uint64_t *k_conv = k_empty + C::kKStages;    // [kKStages] ready, where warps 2 and 3 pass it on
+    uint64_t *v_full = k_conv + C::kKStages;     // [kVStages]
+    uint64_t *v_empty = v_full + C::kVStages;
+    uint64_t *v_conv = v_empty + C::kVStages;
+    uint64_t *raw_full = v_conv + C::kVStages;   // [kRawStages] codes
+    uint64_t *raw_empty = raw_full + C::kRawStages;
+    uint64_t *q_full = raw_empty + C::kRawStages;
+    uint64_t *q_conv = q_full + 1;
+    uint64_t *s_full = q_conv + 1;  // [2]
+    uint64_t *p_full = s_full + 2;  // [2 tiles][2 key halves]
+    uint64_t *o_done = p_full + 4;
+    uint64_t *mma_done = o_done + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kNumBars);
+    __shared__ int s_bad;  // a page of the piece's keys is not in the pool
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = p.group, R = p.q_rows, used = p.rt * G;
+    const bool gather = p.box_rows == 0;
+
+    // Tile rows past the packed queries are never loaded: zeros
+    if (used < kBM)
+        for (int i = threadIdx.x; i < 2 * C::kHalves * (kBM - used) * 8; i += kThreads) {
+            const int piece = i & 7, row = used + (i >> 3) % (kBM - used);
+            const int th = (i >> 3) / (kBM - used);  // tile * halves + half
+            *reinterpret_cast<uint4 *>(sQ + th * (kBM * 128) + row * 128 + piece * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, kTmemCols);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&tm_q);
+        if (!gather) {
+            prefetch_tensormap(&tm_k);
+            prefetch_tensormap(&tm_v);
+        }
+    }
+    pdl_wait();  // everything below may come from the previous kernel
+    pdl_launch_dependents();
+
+    int total = INT32_MAX;
+    for (int want = blockIdx.x; want < total; want += gridDim.x) {
+    if (threadIdx.x == 0) {
+        for (int i = 0; want != (int)blockIdx.x && i < C::kNumBars; ++i) mbar_inval(&bars[i]);
+        const int loads = gather ? 32 : 1;
+        for (int s = 0; s < C::kKStages; ++s) {
+            mbar_init(&k_full[s], loads);
+            mbar_init(&k_empty[s], 1);
+            mbar_init(&k_conv[s], 64);  // every thread of warps 2 and 3
+        }
+        for (int s = 0; s < C::kVStages; ++s) {
+            mbar_init(&v_full[s], loads);
+            mbar_init(&v_empty[s], 1);
+            mbar_init(&v_conv[s], 64);
+        }
+        for (int s = 0; s < C::kRawStages; ++s) {
+            mbar_init(&raw_full[s], loads);
+            mbar_init(&raw_empty[s], 64);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_conv, 256);
+        mbar_init(&s_full[0], 1);
+        mbar_init(&s_full[1], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], 128);
+        mbar_init(o_done, 1);
+        mbar_init(mma_done, 1);
+        fence_barrier_init();
+        s_bad = 0;
+    }
+    Piece w;
+    make_plan(p, reinterpret_cast<int32_t *>(sK), want, want == (int)blockIdx.x, w, total);
+    fence_proxy_async_smem();  // the plan's words and the zeros in Q, before copies and products
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (w.n_kt == 0) break;  // (the same for the whole CTA)
+    const uint32_t tmem = *tmem_slot;
+    const int first_pos = w.pair * 2 * p.rt;         // of the group's positions
+    const bool dual = w.n_pos <= p.rt;               // one tile, two streams of key tiles
+    const int n_tiles = w.n_pos - first_pos > p.rt ? 2 : 1;
+    const int32_t *table = p.paged ? p.block_table + (int64_t)w.prow * p.max_blocks : nullptr;
+    auto page_of = [&](int t) { return __ldg(table + t / p.block_size); };
+
+    if (warp < 4) {
+        setmaxnreg_dec<kRegsControl>();
+        if (warp == 0) {
+            // ------------------------------------------------------------ loads
+            if (lane == 0) {
+                mbar_arrive_expect_tx(q_full, n_tiles * C::kHalves * used * 128);
+                for (int a = 0; a < n_tiles; ++a)
+                    for (int hf = 0; hf < C::kHalves; ++hf)
+                        tma_load_3d(sQ + a * C::kQBytes + hf * (kBM * 128), &tm_q, hf * 64,
+                                    w.kvh * G, w.start + first_pos + a * p.rt, q_full);
+            }
+            __syncwarp();
+            constexpr int kBytes = FMT == kBF16 ? C::kTileBytes : C::kRawBytes;
+            const int boxes = gather ? 0 : kBN / p.box_rows;
+            auto fetch = [&](bool is_v, int tile, uint8_t *dst, uint64_t *bar) {
+                if (!gather) {
+                    if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
+                    __syncwarp();
+                    if (lane < boxes) {
+                        const int t = tile * kBN + lane * p.box_rows;
+                        bool on = t < w.hi && t + p.box_rows > w.lo;
+                        // slot-major: slot y; head-major: row y of (block, head) z
+                        int y = 0, z = 0;
+                        if (p.paged) {
+                            if (on) {
+                                const int page = page_of(t);
+                                on = (unsigned)page < (unsigned)p.num_pages;
+                                y = t % p.block_size;
+                                if (p.head_major)
+                                    z = page * p.n_kv_heads + w.kvh;
+                                else
+                                    y += page * p.block_size;
+                            }
+                        } else if (p.head_major) {
+                            y = t, z = w.prow * p.n_kv_heads + w.kvh;
+                        } else {
+                            y = w.prow * p.slots_per_seq + t;
+                        }
+                        if (!on) y = p.map_rows, z = 0;  // outside the tensor: zeros
+                        const CUtensorMap *map = is_v ? &tm_v : &tm_k;
+                        const int x = p.head_major ? 0 : w.kvh * HD;
+                        if constexpr (FMT == kBF16) {
+                            for (int hf = 0; hf < C::kHalves; ++hf)
+                                tma_load_3d(dst + hf * (kBN * 128) + lane * p.box_rows * 128, map,
+                                            x + hf * 64, y, z, bar);
+                        } else {
+                            tma_load_3d(dst + lane * p.box_rows * HD, map, x, y, z, bar);
+                        }
+                    }
+                    __syncwarp();
+                    return;
+                }
+                // row by row: lane l finds rows l, l + 32, l + 64 and l + 96
+                const uint8_t *src = is_v ? p.v : p.k;
+                constexpr int kPieces = kBytes / kBN / 16;  // of a row
+                const uint32_t to = smem_u32(dst);
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    const int t = tile * kBN + i * 32 + lane;
+                    int64_t off = -1;
+                    if (t < w.hi && t >= w.lo) {
+                        const int page = page_of(t);
+                        if ((unsigned)page < (unsigned)p.num_pages)
+                            off = p.place.head_offset(
+                                (int64_t)page * p.block_size + t % p.block_size, w.kvh);
+                    }
+#pragma unroll 4
+                    for (int n = 0; n < kPieces; ++n) {
+                        const int rr = n * (32 / kPieces) + lane / kPieces, piece = lane % kPieces;
+                        const int64_t at = __shfl_sync(0xffffffffu, off, rr);
+                        const int r = i * 32 + rr;
+                        copy16(to + (piece >> 3) * (kBN * 128) + r * 128 +
+                                   (((piece & 7) ^ (r & 7)) << 4),
+                               src + (at < 0 ? 0 : at + piece * 16), at >= 0);
+                    }
+                }
+                cp_async_arrive_noinc(bar);
+            };
+            // K one tile ahead of V
+            int kj = 0, vj = 0;
+            while (kj < w.n_kt || vj < w.n_kt) {
+                const bool is_v = !(kj < w.n_kt && (kj <= vj + 1 || vj >= w.n_kt));
+                const int j = is_v ? vj : kj;
+                bool ok = true;
+                if constexpr (FMT == kBF16) {
+                    const int stages = is_v ? C::kVStages : C::kKStages, st = j % stages;
+                    if (j >= stages)
+                        ok = mbar_wait(is_v ? &v_empty[st] : &k_empty[st], ((j / stages) - 1) & 1,
+                                       p.err);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    fetch(is_v, w.kt0 + j, (is_v ? sV : sK) + st * C::kTileBytes,
+                          is_v ? &v_full[st] : &k_full[st]);
+                } else {
+                    const int n = kj + vj, st = n % C::kRawStages;
+                    if (n >= C::kRawStages)
+                        ok = mbar_wait(&raw_empty[st], ((n / C::kRawStages) - 1) & 1, p.err);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    fetch(is_v, w.kt0 + j, sRaw + st * C::kRawBytes, &raw_full[st]);
+                }
+                if (is_v)
+                    ++vj;
+                else
+                    ++kj;
+            }
+            // No copy may still be landing when the CTA exits (normally all have been read)
+            if constexpr (FMT == kBF16) {
+                for (int j = max(0, kj - C::kKStages); j < kj; ++j)
+                    mbar_wait(&k_full[j % C::kKStages], (j / C::kKStages) & 1, p.err);
+                for (int j = max(0, vj - C::kVStages); j < vj; ++j)
+                    mbar_wait(&v_full[j % C::kVStages], (j / C::kVStages) & 1, p.err);
+            } else {
+                for (int n = max(0, kj + vj - C::kRawStages); n < kj + vj; ++n)
+                    mbar_wait(&raw_full[n % C::kRawStages], (n / C::kRawStages) & 1, p.err);
+            }
+            mbar_wait(q_full, 0, p.err);
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ products
+            if (lane == 0) {
+                constexpr uint32_t idesc_qk = FMT == kBF16 ? idesc_bf16_f32(kBM, kBN, 0, 0)
+                                                           : idesc_f16_f32(kBM, kBN, 0, 0);
+                constexpr uint32_t idesc_pv = idesc_f16_f32(kBM, HD, 0, 1);
+                const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+                const uint64_t k_desc0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
+                const uint64_t v_desc0 = smem_desc_sw128(smem_u32(sV), kBN * 128, 1024);
+                // scores of Q tile qt into S a
+                auto issue_qk = [&](int a, int qt, int kst) {
+                    const uint64_t qd = q_desc + (uint64_t)((qt * C::kQBytes) >> 4);
+                    const uint64_t kd = k_desc0 + (uint64_t)((kst * C::kTileBytes) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < HD / 16; ++kk) {
+                        const uint64_t off =
+                            (uint64_t)(((kk >> 2) * (kBM * 128) + (kk & 3) * 32) >> 4);
+                        tc_mma_ss(tmem + a * 128, qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
+                    }
+                    tc_commit(&s_full[a]);
+                };
+                auto issue_pv_half = [&](int a, int vst, int hh, bool first) {
+                    const uint64_t vd = v_desc0 + (uint64_t)((vst * C::kTileBytes) >> 4);
+                    const uint32_t p_tmem = tmem + a * 128;
+                    const uint32_t o_tmem = tmem + 256 + a * HD;
+#pragma unroll
+                    for (int k4 = 0; k4 < kBN / 32; ++k4) {
+                        const int kk = hh * (kBN / 32) + k4;
+                        tc_mma_ts(o_tmem, p_tmem + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4),
+                                  idesc_pv, (!first || k4 > 0) ? 1u : 0u);
+                    }
+                };
+                auto k_ready = [&](int j) {
+                    const int st = j % C::kKStages, ph = (j / C::kKStages) & 1;
+                    return mbar_wait(FMT != kBF16 || gather ? &k_conv[st] : &k_full[st], ph, p.err);
+                };
+                // the weights of a stream's jj-th key tile, tile j, into its output
+                auto pv = [&](int a, int j, int jj) {
+                    for (int hh = 0; hh < 2; ++hh) {
+                        if (!mbar_wait(&p_full[a * 2 + hh], jj & 1, p.err)) return false;
+                        tc_fence_after();
+                        issue_pv_half(a, j % C::kVStages, hh, jj == 0 && hh == 0);
+                    }
+                    return true;
+                };
+                bool ok = mbar_wait(FMT == kBF16 ? q_full : q_conv, 0, p.err);
+                if (dual) {
+                    // tile j belongs to stream j & 1
+                    for (int j = 0; ok && j < min(2, w.n_kt); ++j) {
+                        ok = k_ready(j);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_qk(j, 0, j % C::kKStages);
+                        tc_commit(&k_empty[j % C::kKStages]);
+                    }
+                    for (int j = 0; ok && j < w.n_kt; ++j) {
+                        ok = mbar_wait(&v_conv[j % C::kVStages], (j / C::kVStages) & 1, p.err) &&
+                             pv(j & 1, j, j >> 1);
+                        if (!ok) break;
+                        tc_commit(&v_empty[j % C::kVStages]);
+                        if (j + 2 < w.n_kt) {
+                            ok = k_ready(j + 2);
+                            if (!ok) break;
+                            tc_fence_after();
+                            issue_qk(j & 1, 0, (j + 2) % C::kKStages);
+                            tc_commit(&k_empty[(j + 2) % C::kKStages]);
+                        }
+                    }
+                } else {
+                    ok = ok && k_ready(0);
+                    if (ok) {
+                        tc_fence_after();
+                        for (int a = 0; a < n_tiles; ++a) issue_qk(a, a, 0);
+                        tc_commit(&k_empty[0]);
+                    }
+                    for (int j = 0; ok && j < w.n_kt; ++j) {
+                        ok = mbar_wait(&v_conv[j % C::kVStages], (j / C::kVStages) & 1, p.err);
+                        const int kst = (j + 1) % C::kKStages;
+                        for (int a = 0; ok && a < n_tiles; ++a) {
+                            ok = pv(a, j, j);
+                            if (!ok) break;
+                            if (a == n_tiles - 1) tc_commit(&v_empty[j % C::kVStages]);
+                            if (j + 1 < w.n_kt) {
+                                if (a == 0) {
+                                    ok = k_ready(j + 1);
+                                    if (!ok) break;
+                                    tc_fence_after();
+                                }
+                                issue_qk(a, a, kst);
+                                if (a == n_tiles - 1) tc_commit(&k_empty[kst]);
+                            }
+                        }
+                    }
+                }
+                tc_commit(o_done);
+                tc_commit(mma_done);
+                mbar_wait(mma_done, 0, p.err);
+            }
+        } else {
+            // ------------------------------------------------------------ into f16
+            const int ct = threadIdx.x - 64;  // 0 .. 63
+            // keys of a tile that lie in the group's range
+            auto inside = [&](int tile, int row) {
+                const int t = tile * kBN + row;
+                return t >= w.lo && t < w.hi;
+            };
+            auto whole = [&](int tile) {
+                return tile * kBN >= w.lo && tile * kBN + kBN <= w.hi;
+            };
+            // f16 NaN among this thread's pieces of a V tile become 0
+            auto clean = [&](uint32_t at) {
+                report_error(p.err, ATTN_ERR_UNSUPPORTED);
+                for (int i = ct; i < C::kTileBytes / 16; i += 64) {
+                    uint4 x = ld_shared_v4(at + i * 16);
+                    x.x = drop_nan(x.x), x.y = drop_nan(x.y);
+                    x.z = drop_nan(x.z), x.w = drop_nan(x.w);
+                    st_shared_v4(at + i * 16, x);
+                }
+            };
+            // a tile of bf16 V in place
+            auto v_in_place = [&](int tile, uint32_t at) {
+                const bool all = whole(tile);
+                float amax = 0.f;
+#pragma unroll 4
+                for (int i = ct; i < C::kTileBytes / 16; i += 64) {
+                    uint4 x = ld_shared_v4(at + i * 16);
+                    if (!all && !inside(tile, (i >> 3) & (kBN - 1))) x = make_uint4(0u, 0u, 0u, 0u);
+                    uint32_t *u = &x.x;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float x0 = __uint_as_float(u[e] << 16);
+                        const float x1 = __uint_as_float(u[e] & 0xFFFF0000u);
+                        amax = max3_abs_nan(amax, x0, x1);
+                        u[e] = pack_f16x2_sat(x0, x1);
+                    }
+                    st_shared_v4(at + i * 16, x);
+                }
+                if (!(amax < 65536.f)) clean(at);
+            };
+            // A tile of codes from `from` into an f16 tile.  Eight lanes read 4 pieces (16 codes)
+            // of rows r and r ^ 5 (128-byte rows, swizzled) or of two rows (64-byte ones), so
+            // that neither their loads nor their stores (pieces 2 i and 2 i + 1 of f16 rows of
+            // 128 bytes, swizzled) meet in a bank.
+            auto widen = [&](bool is_v, int tile, uint32_t from, uint32_t to) {
+                const bool all = !is_v || whole(tile);
+                constexpr int kRounds = HD / 64 * (kBN / 8) / 2;  // of 8 rows x 4 pieces a warp
+#pragma unroll 2
+                for (int i = 0; i < kRounds; ++i) {
+                    const int unit = i * 2 + (ct >> 5);  // (8 rows, 64 dims)
+                    const int hf = unit % C::kHalves, r8 = unit / C::kHalves;
+                    const int l = ct & 31, ph = l >> 3, second = (l >> 2) & 1;
+                    const int row = r8 * 8 + (HD == 128 ? (second ? ph ^ 5 : ph) : 2 * ph + second);
+                    const int piece = l & 3;  // of the 64 dims
+                    uint4 x = ld_shared_v4(
+                        HD == 128 ? from + row * 128 + (((hf * 4 + piece) ^ (row & 7)) << 4)
+                                  : from + row * 64 + piece * 16);
+                    if (!all && !inside(tile, row)) x = make_uint4(0u, 0u, 0u, 0u);
+                    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t h[8], odd = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        codes_to_f16<FMT>(u[e], h[2 * e], h[2 * e + 1]);
+                        if (FMT == kE4M3)  // a code of NaN, 0x7F or 0xFF
+                            odd |= ((u[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                    }
+                    if (is_v && odd != 0) {
+                        report_error(p.err, ATTN_ERR_UNSUPPORTED);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) h[e] = drop_nan(h[e]);
+                    }
+                    const uint32_t base = to + hf * (kBN * 128) + row * 128;
+                    st_shared_v4(base + (((2 * piece) ^ (row & 7)) << 4),
+                                 make_uint4(h[0], h[1], h[2], h[3]));
+                    st_shared_v4(base + (((2 * piece + 1) ^ (row & 7)) << 4),
+                                 make_uint4(h[4], h[5], h[6], h[7]));
+                }
+            };
+            int kj = 0, vj = 0, n = 0;
+            bool ok = true;
+            while (ok && (kj < w.n_kt || vj < w.n_kt)) {
+                const bool is_v = !(kj < w.n_kt && (kj <= vj + 1 || vj >= w.n_kt));
+                const int j = is_v ? vj++ : kj++;
+                const int stages = is_v ? C::kVStages : C::kKStages, st = j % stages;
+                const uint32_t ph = (j / stages) & 1;
+                const uint32_t at = smem_u32((is_v ? sV : sK) + st * C::kTileBytes);
+                if constexpr (FMT == kBF16) {
+                    if (!is_v && !gather) continue;
+                    ok = mbar_wait(is_v ? &v_full[st] : &k_full[st], ph, p.err);
+                    if (!ok) break;
+                    if (is_v) {
+                        v_in_place(w.kt0 + j, at);
+                    } else {
+                        // copied by cp.async: written again, so that this thread's fence
+                        // covers what the tensor cores read
+#pragma unroll 4
+                        for (int i = ct; i < C::kTileBytes / 16; i += 64)
+                            st_shared_v4(at + i * 16, ld_shared_v4(at + i * 16));
+                    }
+                } else {
+                    const int rs = n % C::kRawStages;
+                    ok = mbar_wait(&raw_full[rs], (n / C::kRawStages) & 1, p.err);
+                    if (ok && j >= stages)
+                        ok = mbar_wait(is_v ? &v_empty[st] : &k_empty[st], ph ^ 1, p.err);
+                    if (!ok) break;
+                    widen(is_v, w.kt0 + j, smem_u32(sRaw + rs * C::kRawBytes), at);
+                    fence_proxy_async_smem();
+                    mbar_arrive(&raw_empty[rs]);
+                    ++n;
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(is_v ? &v_conv[st] : &k_conv[st]);
+            }
+        }
+    } else {
+        setmaxnreg_inc<kRegsSoftmax>();
+        // ---------------------------------------------------------------- softmax
+        const int a = (warp - 4) >> 2;     // which tile, or stream
+        const int quad = warp & 3;         // TMEM lane quadrant of this warp
+        const int row = quad * 32 + lane;  // tile row = TMEM lane
+        const int st = threadIdx.x - 128;  // 0 .. 255
+        // a page that is not there is reported, and its keys are looked for in every tile
+        if (p.paged) {
+            const int b0 = max(w.lo, w.kt0 * kBN) / p.block_size;
+            const int b1 = (min(w.hi, (w.kt0 + w.n_kt) * kBN) + p.block_size - 1) / p.block_size;
+            bool bad = false;
+            for (int i = b0 + st; i < b1; i += 256)
+                bad |= (unsigned)__ldg(table + i) >= (unsigned)p.num_pages;
+            if (bad) {
+                s_bad = 1;
+                report_error(p.err, ATTN_ERR_BOUNDS);
+            }
+        }
+        if constexpr (FMT != kBF16) {
+            // q to f16 in place
+            if (mbar_wait(q_full, 0, p.err)) {
+                const uint32_t at = smem_u32(sQ);
+                uint32_t big = 0;
+                for (int i = st; i < n_tiles * C::kQBytes / 16; i += 256) {
+                    uint4 x = ld_shared_v4(at + i * 16);
+                    uint32_t *u = &x.x;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t h = bf16x2_to_f16x2(u[e]);
+                        // overflowed, NaN aside (which stays one, in its row)
+                        if ((h & 0x7FFFu) == 0x7C00u || (h & 0x7FFF0000u) == 0x7C000000u) big = 1;
+                        u[e] = h;
+                    }
+                    st_shared_v4(at + i * 16, x);
+                }
+                if (big) report_error(p.err, ATTN_ERR_UNSUPPORTED);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(q_conv);
+        }
+        asm volatile("bar.sync 3, 256;" ::: "memory");
+        const bool any_bad = *reinterpret_cast<volatile int *>(&s_bad) != 0;
+
+        const int tile_pos = first_pos + (dual ? 0 : a * p.rt);  // the tile's first position
+        const int live_rows = min(used, (w.n_pos - tile_pos) * G);
+        const bool live = row < live_rows;
+        int qi = -1, key_cap = -1;  // the row's position, and the last shared key it may see
+        if (live) {
+            const int i = w.start + tile_pos + row / G, b = i / R;
+            qi = p.positions[i];
+            const int len = max(0, min(p.seq_lens[b], p.cap));
+            key_cap = min(min(qi, len - 1), max(0, min(p.prefix_lens[b], p.prefix_cap)) - 1);
+        }
+        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+        const uint32_t s_tmem = tmem + a * 128 + lane_base;
+        const uint32_t o_tmem = tmem + 256 + a * HD + lane_base;
+        const float sl2 = p.scale_log2;
+        float m_run = -INFINITY, l_run = 0.f, w_run = 0.f;
+        bool ok = true;
+        // this warpgroup's key tiles
+        const int j0 = dual ? a : 0, step = dual ? 2 : 1;
+        const int mine = a < n_tiles || dual ? (w.n_kt - j0 + step - 1) / step : 0;
+        // scales of the 16 keys 16 (lane % 8) .. of a tile, read a tile ahead
+        float next_k = 1.f, next_v = 1.f;
+        auto read_scales = [&](int j) {
+            next_k = next_v = 1.f;
+            const int t = (w.kt0 + j) * kBN + 16 * (lane & 7);
+            if (p.ks == nullptr || j >= w.n_kt || t >= w.hi || t + 16 <= w.lo) return;
+            int64_t slot;
+            if (p.paged) {
+                const int page = page_of(t);
+                if ((unsigned)page >= (unsigned)p.num_pages) return;
+                slot = (int64_t)page * p.block_size + t % p.block_size;
+            } else {
+                slot = (int64_t)w.prow * p.slots_per_seq + t;
+            }
+            const int64_t at = (slot >> p.scale_shift) * p.n_kv_heads + w.kvh;
+            next_k = __ldg(p.ks + at);
+            next_v = __ldg(p.vs + at);
+        };
+        if constexpr (FMT != kBF16) read_scales(j0);
+        for (int jj = 0; jj < mine; ++jj) {
+            const int j = j0 + jj * step;
+            float f_lane = sl2, lv_lane = 0.f, inv_lane = 1.f;
+            if constexpr (FMT != kBF16) {
+                if (p.ks != nullptr) {
+                    const float sv = fmaxf(next_v, kScaleFloor);
+                    f_lane = fminf(fmaxf(fmaxf(next_k, kScaleFloor) * sl2, 0x1p-126f), kFactorTop);
+                    lv_lane = fast_log2(sv);
+                    inv_lane = 0.25f * fast_rcp(0.25f * sv);  // subnormal from 2^126 on, not 0
+                }
+                read_scales(j + step);
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(&s_full[a], jj & 1, p.err));
+            if (!ok) break;
+            tc_fence_after();
+            float s[kBN];
+            {
+                uint32_t(&u)[kBN] = *reinterpret_cast<uint32_t(*)[kBN]>(s);
+                tmem_ld_32x32b_x32(s_tmem + 0, *reinterpret_cast<uint32_t(*)[32]>(u + 0));
+                tmem_ld_32x32b_x32(s_tmem + 32, *reinterpret_cast<uint32_t(*)[32]>(u + 32));
+                tmem_ld_32x32b_x32(s_tmem + 64, *reinterpret_cast<uint32_t(*)[32]>(u + 64));
+                tmem_ld_32x32b_x32(s_tmem + 96, *reinterpret_cast<uint32_t(*)[32]>(u + 96));
+                tmem_wait_ld();
+                tmem_regs_after_wait(u);
+            }
+            const int key0 = (w.kt0 + j) * kBN;
+            if (key0 + kBN - 1 > key_cap || (p.window > 0 && qi - key0 >= p.window)) {
+                // the row sees columns lo <= c <= hi (c = key - key0)
+                const int hi = key_cap - key0;
+                const int lo = p.window > 0 ? qi - p.window + 1 - key0 : 0;
+#pragma unroll
+                for (int c = 0; c < kBN; ++c) s[c] = (c <= hi && c >= lo) ? s[c] : -INFINITY;
+            }
+            if (any_bad) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < kBN; c0 += 32) {
+                    const int t = key0 + c0 + lane;
+                    const bool bad = t >= w.lo && t < w.hi &&
+                                     (unsigned)page_of(t) >= (unsigned)p.num_pages;
+                    const uint32_t mask = __ballot_sync(0xffffffffu, bad);
+#pragma unroll
+                    for (int c = 0; c < kBN; ++c)
+                        if ((c & ~31) == c0 && (mask >> (c & 31) & 1u)) s[c] = -INFINITY;
+                }
+            }
+            float mx;
+            float f[8], lv[8], inv[8];  // of 16 keys each
+            if constexpr (FMT == kBF16) {
+                float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
+#pragma unroll
+                for (int c = 4; c + 8 <= kBN; c += 8) {  // columns 4 .. kBN - 5
+                    mx0 = max3(mx0, s[c], s[c + 1]);
+                    mx1 = max3(mx1, s[c + 2], s[c + 3]);
+                    mx2 = max3(mx2, s[c + 4], s[c + 5]);
+                    mx3 = max3(mx3, s[c + 6], s[c + 7]);
+                }
+                mx0 = max3(mx0, s[kBN - 4], s[kBN - 3]);  // the last four columns
+                mx1 = max3(mx1, s[kBN - 2], s[kBN - 1]);
+                mx = max3(mx0, mx1, fmaxf(mx2, mx3)) * sl2;
+            } else {
+                mx = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    f[i] = __shfl_sync(0xffffffffu, f_lane, i);
+                    lv[i] = __shfl_sync(0xffffffffu, lv_lane, i);
+                    inv[i] = __shfl_sync(0xffffffffu, inv_lane, i);
+                    // x = s f + lv grows with s (f > 0): its maximum is that of s
+                    const float *x = s + 16 * i;
+                    float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[4], x[5]);
+                    m0 = max3(m0, x[6], x[7]), m1 = max3(m1, x[8], x[9]);
+                    m0 = max3(m0, x[10], x[11]), m1 = max3(m1, x[12], x[13]);
+                    mx = fmaxf(mx, fmaf(max3(m0, m1, fmaxf(x[14], x[15])), f[i], lv[i]));
+                }
+            }
+            float alpha = 1.f;
+            if (mx > m_run + kRescaleLog2 || m_run == -INFINITY) {
+                const float m_new = mx == -INFINITY ? m_run : mx;
+                alpha = m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_new);
+                m_run = m_new;
+            }
+            if (jj > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+                for (int c0 = 0; c0 < HD; c0 += 32) {
+                    uint32_t orow[32];
+                    tmem_ld_32x32b_x32(o_tmem + c0, orow);
+                    tmem_wait_ld();
+                    tmem_regs_after_wait(orow);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        orow[e] = __float_as_uint(__uint_as_float(orow[e]) * alpha);
+                    tmem_st_32x32b_x32(o_tmem + c0, orow);
+                }
+            }
+            const float m_w = (m_run == -INFINITY ? 0.f : m_run) - kWeightLog2;
+            float sum0 = 0.f, sum1 = 0.f, over = 0.f;
+#pragma unroll
+            for (int c0 = 0; c0 < kBN; c0 += 32) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int i = (c0 + 2 * e) / 16;
+                    float x0, x1;
+                    if constexpr (FMT == kBF16)
+                        fma2(x0, x1, s[c0 + 2 * e], s[c0 + 2 * e + 1], sl2, sl2, -m_w, -m_w);
+                    else
+                        fma2(x0, x1, s[c0 + 2 * e], s[c0 + 2 * e + 1], f[i], f[i], lv[i] - m_w,
+                             lv[i] - m_w);
+                    const float p0 = fast_exp2(x0);
+                    const float p1 = fast_exp2(x1);
+                    add2(sum0, sum1, sum0, sum1, p0, p1);
+                    pk[e] = pack_f16x2(p0, p1);
+                    if (FMT != kBF16 && (e & 7) == 7) {  // the end of 16 keys
+                        over = fmaf(sum0 + sum1, inv[i], over);
+                        w_run = (i == 0 ? w_run * alpha : w_run) + (sum0 + sum1);
+                        sum0 = sum1 = 0.f;
+                    }
+                }
+                // P over its own S columns: 32 keys in 16 columns
+                tmem_st_32x32b_x16(s_tmem + c0 / 2, pk);
+                if (c0 == kBN / 2 - 32 || c0 == kBN - 32) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(&p_full[a * 2 + (c0 >= kBN / 2 ? 1 : 0)]);
+                }
+            }
+            l_run = l_run * alpha + (FMT == kBF16 ? sum0 + sum1 : over);
+        }
+        if (m_run != -INFINITY && !(fabsf(m_run) < kScoreTop))
+            report_error(p.err, ATTN_ERR_UNSUPPORTED);
+        // ---- the state of each row: O over the sum of its weights, and both sums
+        if (ok) mbar_wait(o_done, 0, p.err);
+        __syncwarp();
+        tc_fence_after();
+        if constexpr (FMT == kBF16) w_run = l_run;
+        const bool any = !(w_run == 0.f);  // a key was seen (or a NaN met)
+        const float norm = any ? 1.f / w_run : 0.f;
+        const int part = dual ? 2 * w.split + a : w.split;
+        const int64_t row0 = (int64_t)w.base +
+                             ((int64_t)w.kvh * w.parts + part) * ((int64_t)w.n_pos * G) +
+                             (int64_t)tile_pos * G;
+        if (dual || a < n_tiles) {
+            // Through shared memory (the K ring for a = 0, the V ring for a = 1: the last
+            // product has read them) as swizzled 128-byte rows of 64 dims, and out in whole
+            // lines: a row a thread would write into 32 lines an instruction
+            uint8_t *stage = a == 0 ? sK : sV;
+#pragma unroll
+            for (int c0 = 0; c0 < HD; c0 += 32) {
+                uint32_t orow[32];
+                if (mine > 0) {  // warpgroup-uniform: O was accumulated into
+                    tmem_ld_32x32b_x32(o_tmem + c0, orow);
+                    tmem_wait_ld();
+                    tmem_regs_after_wait(orow);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) orow[e] = 0u;
+                }
+                auto v = [&](int e) { return any ? __uint_as_float(orow[e]) * norm : 0.f; };
+                const uint32_t base = smem_u32(stage + (c0 / 64) * (kBM * 128) + row * 128);
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    const int piece = ((c0 & 63) >> 3) + q4;
+                    st_shared_v4(base + ((piece ^ (row & 7)) << 4),
+                                 make_uint4(pack_f16x2(v(8 * q4), v(8 * q4 + 1)),
+                                            pack_f16x2(v(8 * q4 + 2), v(8 * q4 + 3)),
+                                            pack_f16x2(v(8 * q4 + 4), v(8 * q4 + 5)),
+                                            pack_f16x2(v(8 * q4 + 6), v(8 * q4 + 7))));
+                }
+            }
+            if (live) {
+                const float at = (m_run == -INFINITY ? 0.f : m_run) - kWeightLog2;
+                p.ws_lse[row0 + row] = any ? make_float2(at + __log2f(w_run), at + __log2f(l_run))
+                                           : make_float2(-INFINITY, -INFINITY);
+            }
+            if (a == 0)
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+            else
+                asm volatile("bar.sync 2, 128;" ::: "memory");
+            uint4 *dst = reinterpret_cast<uint4 *>(p.ws_o + row0 * HD);
+            for (int i = row; i < live_rows * (HD / 8); i += 128) {
+                const int r = i / (HD / 8), piece = i % (HD / 8);
+                dst[i] = ld_shared_v4(smem_u32(stage + (piece >> 3) * (kBM * 128) + r * 128) +
+                                      (((piece & 7) ^ (r & 7)) << 4));
+            }
+        }
+    }
+    __syncwarp();  // the lanes of the product's warp wait here for lane 0
+    if (want + (int)gridDim.x >= total) break;
+    // another piece: registers as they were for the plan, and everything read
+    if (warp < 4)
+        setmaxnreg_inc<kRegsLaunch>();
+    else
+        setmaxnreg_dec<kRegsLaunch>();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(*tmem_slot, kTmemCols);
+}
+
+struct MergeParams {
+    const int4 *ws_rows;
+    const float2 *ws_lse;
+    const uint16_t *ws_o;
+    AttendParts own;  // of the keys behind the prefixes
+    __nv_bfloat16 *out;
+    int q_rows, rows, n_q_heads, n_kv_heads, group;
+};
+
+// A row of the output from its parts: those of the shared keys, then those of its own.
+// SPLIT warps a row, each every SPLIT-th part, a lane HD / 32 dims; the sums of 32 parts come in one
+// load, the parts' outputs then wait for nothing.
+template <int HD, int SPLIT>
+__global__ void __launch_bounds__(256) shared_merge_kernel(const MergeParams p) {
+    constexpr int V = HD / 32, kRows = 8 / SPLIT;
+    __shared__ float sm_acc[8][HD];
+    __shared__ float sm_m[8], sm_sum[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const AttendParts &a = p.own;
+    const int64_t i = (int64_t)blockIdx.x * kRows + warp / SPLIT;
+    const int64_t head = i / a.rb;  // KV heads of all entries
+    const int row = (int)(i - head * a.rb);
+    const int entry = (int)(head / p.n_kv_heads), kvh = (int)(head - (int64_t)entry * p.n_kv_heads);
+    const int e = a.e0 + entry, b = e / a.row_blocks, q_row = (e - b * a.row_blocks) * a.rb + row;
+    const bool live = entry < a.n_entries && q_row < p.rows;
+    const int r = q_row / p.group, gh = q_row - r * p.group;
     pdl_wait();
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (i >= (int64_t)p.batch * p.q_rows * p.n_q_heads) return;
-    const int h = (int)(i % p.n_q_heads), kvh = h / p.group;
-    const int64_t row = i / p.n_q_heads;
-    const int b = (int)(row / p.q_rows);
-    int len = p.seq_lens[b];
-    const int cap = p.kind == ATTN_CACHE_LINEAR ? min(p.max_seq_len, p.slots_per_seq) : p.max_seq_len;
-    if (len < 0 || len > cap) {
-        report_error(p.err, ATTN_ERR_BOUNDS);
-        len = max(0, min(len, cap));
-    }
-    int plen = p.prefix_lens[b], prow = 0;
-    if (plen < 0 || plen > p.max_prefix_len) {
-        report_error(p.err, ATTN_ERR_BOUNDS);
-        plen = max(0, min(plen, p.max_prefix_len));
-    }
-    bool good = true;
-    if (plen > 0) {
-        prow = p.prefix_rows[b];
-        good = prow >= 0 && prow < p.n_rows;
-        if (!good) report_error(p.err, ATTN_ERR_BOUNDS);
-    }
-    const int pos = p.positions[row];
-    const int hi = min(len, pos + 1), lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-    float q[V], o[V] = {}, m = -INFINITY, l = 0.f;
-    for (int d = 0; d < V; ++d) q[d] = __bfloat162float(p.q[i * HD + lane * V + d]);
-    for (int t = lo; t < hi; ++t) {
-        const bool pre = t < plen;
-        if (pre && !good) continue;
-        const int r = pre ? prow : b;
-        int64_t slot;
-        if (p.kind == ATTN_CACHE_PAGED) {
-            const int page = p.block_table[(int64_t)r * p.max_blocks + t / p.block_size];
-            if (page < 0 || page >= p.num_pages) {
-                report_error(p.err, ATTN_ERR_BOUNDS);
-                continue;
+    if (SPLIT == 1 && !live) return;
+    float m = -INFINITY, sum = 0.f, acc[V] = {};
+    if (live) {
+        const int64_t unit = head / a.heads;
+        const int hs = (int)(head - unit * a.heads);
+        const int4 at = __ldcg(p.ws_rows + (int64_t)b * p.q_rows + r);
+        const int2 own = __ldcg(a.parts + unit);
+        const int n1 = at.z, n = n1 + own.y - own.x + 1;
+        const int64_t row1 = (int64_t)at.x + gh + (int64_t)kvh * n1 * at.y;  // + part * at.y
+        // parts of the own keys: (unit + c) heads + hs, row `row`
+        const int64_t row2 = ((unit + own.x) * a.heads + hs) * a.rb + row;
+        const int64_t step2 = (int64_t)a.heads * a.rb;
+        for (int x0 = warp % SPLIT; x0 < n; x0 += 32 * SPLIT) {
+            const int x = x0 + lane * SPLIT;
+            float2 lse = make_float2(-INFINITY, -INFINITY);
+            if (x < n1) {
+                lse = __ldcg(p.ws_lse + row1 + (int64_t)x * at.y);
+            } else if (x < n) {
+                lse.x = lse.y = __ldcg(a.lse + row2 + (x - n1) * step2) - a.held;
             }
-            slot = (int64_t)page * p.block_size + t % p.block_size;
-        } else {
-            slot = (int64_t)r * p.slots_per_seq + t;
-        }
-        const int64_t at = p.place.head_offset(slot, kvh);
-        float k[V], v[V];
-        for (int d = 0; d < V; ++d) {
-            const int e = lane * V + d;
-            if constexpr (FMT == kBF16) {
-                k[d] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.k + at)[e]);
-                v[d] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.v + at)[e]);
-            } else if constexpr (FMT == kINT8) {
-                k[d] = (float)(int8_t)p.k[at + e];
-                v[d] = (float)(int8_t)p.v[at + e];
-            } else {
-                const uint32_t w = e4m3x2_to_f16x2(p.k[at + e] | (uint32_t)p.v[at + e] << 8);
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-                k[d] = f.x;
-                v[d] = f.y;
+            float mx = lse.y;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float m_new = fmaxf(m, mx), m_use = m_new == -INFINITY ? 0.f : m_new;
+            const float old = m == -INFINITY ? 0.f : fast_exp2(m - m_use);
+            const float fo = kPartWeight * fast_exp2(lse.x - m_use);
+            float fs = kPartWeight * fast_exp2(lse.y - m_use);
+            m = m_new;
+#pragma unroll
+            for (int d = 0; d < V; ++d) acc[d] *= fmaxf(old, kSmallest);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) fs += __shfl_xor_sync(0xffffffffu, fs, o);
+            sum = sum * old + fs;
+            const int in_round = min(32, (n - x0 + SPLIT - 1) / SPLIT);
+            const int shared = max(0, min(in_round, (n1 - x0 + SPLIT - 1) / SPLIT));
+            const uint16_t *src1 = p.ws_o + (row1 + (int64_t)x0 * at.y) * HD + lane * V;
+#pragma unroll 8
+            for (int k = 0; k < shared; ++k) {
+                const float w = __shfl_sync(0xffffffffu, fo, k);
+                const uint16_t *src = src1 + (int64_t)k * SPLIT * at.y * HD;
+                uint32_t raw[V / 2];
+                if constexpr (V == 4) {
+                    const uint2 t = __ldcg(reinterpret_cast<const uint2 *>(src));
+                    raw[0] = t.x, raw[1] = t.y;
+                } else {
+                    raw[0] = __ldcg(reinterpret_cast<const unsigned int *>(src));
+                }
+#pragma unroll
+                for (int d = 0; d < V / 2; ++d) {
+                    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&raw[d]));
+                    acc[2 * d] += w * y.x;
+                    acc[2 * d + 1] += w * y.y;
+                }
+            }
+#pragma unroll 4
+            for (int k = shared; k < in_round; ++k) {
+                // no weight is 0: 0 times an infinite output would be NaN
+                const float w = fmaxf(__shfl_sync(0xffffffffu, fo, k), kSmallest);
+                const float *src =
+                    a.o + (row2 + (int64_t)(x0 + k * SPLIT - n1) * step2) * HD + lane * V;
+                if constexpr (V == 4) {
+                    const float4 y = __ldcg(reinterpret_cast<const float4 *>(src));
+                    acc[0] += w * y.x, acc[1] += w * y.y, acc[2] += w * y.z, acc[3] += w * y.w;
+                } else {
+                    const float2 y = __ldcg(reinterpret_cast<const float2 *>(src));
+                    acc[0] += w * y.x, acc[1] += w * y.y;
+                }
             }
         }
-        float s = 0.f, ks = 1.f, vs = 1.f;
-        for (int d = 0; d < V; ++d) s = fmaf(q[d], k[d], s);
-        for (int o2 = 16; o2 > 0; o2 >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o2);
-        if (p.ks != nullptr) {
-            ks = fmaxf(p.ks[(slot >> p.scale_shift) * p.n_kv_heads + kvh], 0x1p-64f);
-            vs = fmaxf(p.vs[(slot >> p.scale_shift) * p.n_kv_heads + kvh], 0x1p-64f);
-        }
-        s *= ks * p.scale_log2;
-        const float mn = fmaxf(m, s), f = exp2f(m - mn), w = exp2f(s - mn);
-        m = mn;
-        l = l * f + w;
-        for (int d = 0; d < V; ++d) o[d] = o[d] * f + w * vs * v[d];
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    for (int d = 0; d < V; ++d) p.out[i * HD + lane * V + d] = __float2bfloat16(o[d] * inv);
+    if constexpr (SPLIT > 1) {
+#pragma unroll
+        for (int d = 0; d < V; ++d) sm_acc[warp][lane * V + d] = acc[d];
+        if (lane == 0) sm_m[warp] = m, sm_sum[warp] = sum;
+        __syncthreads();
+        if (warp % SPLIT != 0 || !live) return;
+        for (int w = warp + 1; w < warp + SPLIT; ++w) {
+            const float m_new = fmaxf(m, sm_m[w]), m_use = m_new == -INFINITY ? 0.f : m_new;
+            const float fa = fast_exp2(m - m_use), fb = fast_exp2(sm_m[w] - m_use);
+            m = m_new;
+            sum = sum * fa + sm_sum[w] * fb;
+#pragma unroll
+            for (int d = 0; d < V; ++d)
+                acc[d] = acc[d] * fmaxf(fa, kSmallest) + sm_acc[w][lane * V + d] * fmaxf(fb, kSmallest);
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(
+        p.out + (((int64_t)b * p.q_rows + r) * p.n_q_heads + kvh * p.group + gh) * HD + lane * V);
+#pragma unroll
+    for (int d = 0; d < V / 2; ++d) dst[d] = pack_bf16x2(acc[2 * d] * inv, acc[2 * d + 1] * inv);
+}
+
+template <int FMT, int HD>
+int launch_prefix(const Params &p, const CUtensorMap &tq, const CUtensorMap &tk,
+                  const CUtensorMap &tv, cudaStream_t stream) {
+    static std::atomic<uint64_t> configured{0};  // a bit per device
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (!(configured.load(std::memory_order_relaxed) & bit)) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(prefix_kernel<FMT, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)Cfg<FMT, HD>::kSmem);
+        if (e != cudaSuccess) {
+            note_cuda_error(e);
+            return ATTN_ERR_CUDA;
+        }
+        configured.fetch_or(bit, std::memory_order_relaxed);
+    }
+    const cudaError_t e = launch_pdl(prefix_kernel<FMT, HD>, dim3((unsigned)p.sms), dim3(kThreads),
+                                     Cfg<FMT, HD>::kSmem, stream, tq, tk, tv, p);
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+template <int HD>
+cudaError_t launch_merge(const MergeParams &p, bool split, cudaStream_t stream) {
+    const int64_t rows = (int64_t)p.own.n_entries * p.n_kv_heads * p.own.rb;
+    return split ? launch_pdl(shared_merge_kernel<HD, 4>, dim3((unsigned)((rows + 1) / 2)), dim3(256),
+                              0, stream, p)
+                 : launch_pdl(shared_merge_kernel<HD, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256),
+                              0, stream, p);
 }
 
 }  // namespace shr
 
 int plan_shared(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads, int n_kv_heads,
-                int head_dim, int max_seq_len, int max_prefix_len, int window, SharedPlan *plan) {
-    plan->workspace = 256;
+                int head_dim, int max_seq_len, int window, SharedPlan *plan) {
+    if (batch > shr::kMaxBatch) return ATTN_ERR_UNSUPPORTED;
+    if (int rc = plan_attend(cache, batch, q_rows, n_q_heads, n_kv_heads, head_dim, max_seq_len,
+                             window, 0, &plan->own);
+        rc != ATTN_OK)
+        return rc;
+    plan->own.merge = true;  // its parts are left to shared_merge_kernel
+    // Parts of the shared keys: each row's first part or two, and those that units of at most
+    // 256 rows are cut into beyond (at most one for every SM)
+    const int64_t rows = (int64_t)batch * q_rows * n_q_heads;
+    const int64_t parts = 2 * rows + (int64_t)2 * shr::kBM * device_sm_count();
+    if (parts >= (int64_t(1) << 30)) return ATTN_ERR_SHAPE;
+    auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    plan->rows_offset = up(plan->own.workspace);
+    plan->lse_offset = up(plan->rows_offset + (size_t)batch * q_rows * sizeof(int4));
+    plan->o_offset = up(plan->lse_offset + (size_t)parts * sizeof(float2));
+    plan->workspace = plan->o_offset + (size_t)parts * head_dim * 2;
     return ATTN_OK;
 }
 
@@ -128,53 +1229,110 @@ int launch_shared(const SharedPlan &plan, const void *q, const attn_kv_cache *ca
                   int max_prefix_len, int window, int n_q_heads, int n_kv_heads, int head_dim,
                   float scale, void *out, void *workspace, int32_t *err, cudaStream_t stream) {
     shr::Params p = {};
-    p.q = static_cast<const __nv_bfloat16 *>(q);
-    p.out = static_cast<__nv_bfloat16 *>(out);
-    p.k = static_cast<const uint8_t *>(cache->k);
-    p.v = static_cast<const uint8_t *>(cache->v);
-    const bool scaled = kv_scaled(cache->dtype);
-    p.ks = scaled ? cache->k_scale : nullptr;
-    p.vs = scaled ? cache->v_scale : nullptr;
-    if (scaled)
-        while ((1 << p.scale_shift) < cache->scale_block) ++p.scale_shift;
-    p.kind = cache->kind;
+    const bool scaled = kv_scaled(cache->dtype), codes = cache->dtype != ATTN_KV_BF16;
+    const int esize = codes ? 1 : 2;
+    p.batch = batch;
+    p.q_rows = q_rows;
+    p.window = window;
+    p.n_kv_heads = n_kv_heads;
+    p.group = n_q_heads / n_kv_heads;
+    p.rt = shr::kBM / p.group;
+    p.sms = device_sm_count();
+    p.n_rows = n_rows;
     p.slots_per_seq = cache->slots_per_seq;
     p.block_size = cache->block_size;
     p.max_blocks = cache->max_blocks_per_seq;
-    p.num_pages = cache->kind == ATTN_CACHE_PAGED ? (int)(cache->num_slots / cache->block_size) : 0;
-    p.n_rows = n_rows;
-    p.place = kv_place(cache, n_kv_heads, head_dim, cache->dtype == ATTN_KV_BF16 ? 2 : 1);
-    p.block_table = cache->block_table;
+    p.paged = cache->kind == ATTN_CACHE_PAGED;
+    p.num_pages = p.paged ? (int)(cache->num_slots / cache->block_size) : 0;
+    p.cap = p.paged ? max_seq_len : std::min(max_seq_len, cache->slots_per_seq);
+    p.prefix_cap = std::min(max_prefix_len, p.cap);
+    p.head_major = cache->layout == ATTN_LAYOUT_BHSD;
+    p.block_table = p.paged ? cache->block_table : nullptr;
     p.seq_lens = seq_lens;
     p.positions = positions;
     p.prefix_rows = prefix_rows;
     p.prefix_lens = prefix_lens;
-    p.batch = batch;
-    p.q_rows = q_rows;
-    p.n_q_heads = n_q_heads;
-    p.n_kv_heads = n_kv_heads;
-    p.group = n_q_heads / n_kv_heads;
-    p.window = window;
-    p.max_seq_len = max_seq_len;
-    p.max_prefix_len = std::min(max_prefix_len,
-                                cache->kind == ATTN_CACHE_LINEAR ? cache->slots_per_seq : max_seq_len);
+    p.k = static_cast<const uint8_t *>(cache->k);
+    p.v = static_cast<const uint8_t *>(cache->v);
+    p.ks = scaled ? cache->k_scale : nullptr;
+    p.vs = scaled ? cache->v_scale : nullptr;
+    if (scaled)
+        while ((1 << p.scale_shift) < cache->scale_block) ++p.scale_shift;
+    p.place = kv_place(cache, n_kv_heads, head_dim, esize);
     p.scale_log2 = scale * 1.4426950408889634f;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.ws_rows = reinterpret_cast<int4 *>(ws + plan.rows_offset);
+    p.ws_lse = reinterpret_cast<float2 *>(ws + plan.lse_offset);
+    p.ws_o = reinterpret_cast<uint16_t *>(ws + plan.o_offset);
     p.err = err;
-    const int64_t rows = (int64_t)batch * q_rows * n_q_heads;
-    auto go = [&](auto kernel) {
-        return launch_pdl(kernel, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, p);
-    };
-    cudaError_t e;
+    // the largest power of two of keys that lie together wherever a tile begins; TMA boxes of
+    // less than 8 would not begin on a swizzle's period
+    p.box_rows = shr::kBN;
+    if (p.paged) {
+        p.box_rows = std::min(cache->block_size & -cache->block_size, shr::kBN);
+        if (p.box_rows < 8) p.box_rows = 0;
+    }
+
+    CUtensorMap tq, tk = {}, tv = {};
+    const uint64_t dq[3] = {(uint64_t)head_dim, (uint64_t)n_q_heads, (uint64_t)batch * q_rows};
+    const uint64_t sq[2] = {(uint64_t)head_dim * 2, (uint64_t)n_q_heads * head_dim * 2};
+    const uint32_t bq[3] = {64, (uint32_t)p.group, (uint32_t)p.rt};
+    bool ok = encode_tensor_map(&tq, q, 3, dq, sq, bq, true);
+    if (p.box_rows > 0) {
+        const uint64_t row = (uint64_t)head_dim * esize;
+        uint64_t d[3], s[2];
+        if (p.head_major) {
+            const uint64_t rows = p.paged ? cache->block_size : cache->slots_per_seq;
+            d[0] = head_dim, d[1] = rows, d[2] = (uint64_t)cache->num_slots / rows * n_kv_heads;
+            s[0] = row, s[1] = rows * row;
+        } else {
+            d[0] = (uint64_t)n_kv_heads * head_dim, d[1] = cache->num_slots, d[2] = 1;
+            s[0] = n_kv_heads * row, s[1] = (uint64_t)cache->num_slots * n_kv_heads * row;
+        }
+        p.map_rows = (int)d[1];
+        const uint32_t box[3] = {codes ? (uint32_t)head_dim : 64u, (uint32_t)p.box_rows, 1};
+        const bool swizzle = !codes || head_dim == 128;
+        ok = ok && encode_tensor_map(&tk, cache->k, 3, d, s, box, swizzle, codes) &&
+             encode_tensor_map(&tv, cache->v, 3, d, s, box, swizzle, codes);
+    }
+    if (!ok) {
+        note_cuda_error(cudaErrorInvalidValue);
+        return ATTN_ERR_CUDA;
+    }
+    int rc;
     if (cache->dtype == ATTN_KV_BF16)
-        e = head_dim == 128 ? go(shr::shared_simple_kernel<shr::kBF16, 128>)
-                            : go(shr::shared_simple_kernel<shr::kBF16, 64>);
+        rc = head_dim == 128 ? shr::launch_prefix<shr::kBF16, 128>(p, tq, tk, tv, stream)
+                             : shr::launch_prefix<shr::kBF16, 64>(p, tq, tk, tv, stream);
     else if (cache->dtype == ATTN_KV_INT8_SCALED)
-        e = head_dim == 128 ? go(shr::shared_simple_kernel<shr::kINT8, 128>)
-                            : go(shr::shared_simple_kernel<shr::kINT8, 64>);
+        rc = head_dim == 128 ? shr::launch_prefix<shr::kINT8, 128>(p, tq, tk, tv, stream)
+                             : shr::launch_prefix<shr::kINT8, 64>(p, tq, tk, tv, stream);
     else
-        e = head_dim == 128 ? go(shr::shared_simple_kernel<shr::kE4M3, 128>)
-                            : go(shr::shared_simple_kernel<shr::kE4M3, 64>);
-    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+        rc = head_dim == 128 ? shr::launch_prefix<shr::kE4M3, 128>(p, tq, tk, tv, stream)
+                             : shr::launch_prefix<shr::kE4M3, 64>(p, tq, tk, tv, stream);
+    if (rc != ATTN_OK) return rc;
+
+    shr::MergeParams m = {};
+    m.ws_rows = p.ws_rows;
+    m.ws_lse = p.ws_lse;
+    m.ws_o = p.ws_o;
+    m.out = static_cast<__nv_bfloat16 *>(out);
+    m.q_rows = q_rows;
+    m.rows = q_rows * p.group;
+    m.n_q_heads = n_q_heads;
+    m.n_kv_heads = n_kv_heads;
+    m.group = p.group;
+    // A row of few KV heads lies in many parts
+    const bool split = p.sms > 8 * n_kv_heads;
+    for (int e0 = 0; e0 < plan.own.entries; e0 += plan.own.per_launch) {
+        rc = launch_attend_parts(plan.own, e0, prefix_lens, p.prefix_cap, q, cache, seq_lens,
+                                 positions, q_rows, max_seq_len, window, n_q_heads, n_kv_heads,
+                                 head_dim, scale, out, workspace, err, stream, &m.own);
+        if (rc != ATTN_OK) return rc;
+        const cudaError_t e = head_dim == 128 ? shr::launch_merge<128>(m, split, stream)
+                                              : shr::launch_merge<64>(m, split, stream);
+        if (e != cudaSuccess) return ATTN_ERR_CUDA;
+    }
+    return ATTN_OK;
 }
 
 }  // namespace gqa

@@ -224,6 +224,28 @@ def test_late_maxima_and_small_weights(D):
         c.check(scale=1.0)
 
 
+def test_values_that_are_not_finite():
+    """Behind the prefix's end and in masked places they reach nothing; shared ones without
+    an f16 are reported."""
+    c = Case("bf16", gq.LINEAR, one_group(3, 200), [5, 6, 7], 1, 8, 2, 128, 16, 5)
+    c.check()  # NaN everywhere else already
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    base = c.run()
+    for bad in (float("inf"), NAN, 70000.0):
+        c.cache.v[:300] = torch.where(c.cache.v[:300].isfinite(), c.cache.v[:300], 0)
+        keep = c.cache.v[17].clone()
+        c.cache.v[17, 0, 3] = bad
+        err.zero_()
+        out = c.run(err=err)
+        assert int(err) == gq.ATTN_ERR_UNSUPPORTED
+        assert torch.isfinite(out).all() and torch.equal(out[:, :, 4:], base[:, :, 4:])
+        c.cache.v[17] = keep
+    # a key that is not finite makes its heads' rows NaN, not the others
+    c.cache.k[17, 0, 0] = NAN
+    out = c.run()
+    assert torch.isnan(out[:, :, :4]).all() and torch.equal(out[:, :, 4:], base[:, :, 4:])
+
+
 def test_reports():
     c = Case("bf16", gq.PAGED, one_group(3, 200), [5, 6, 7], 1, 8, 2, 128, 16, 5)
     good = c.run()
