@@ -73,6 +73,7 @@ constexpr int kChunk = 16;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxEntries = 128;  // (request, row block) pairs per launch
+constexpr int kPartEntries = 256;  // ... of launch_attend_parts
 // What a change of unit costs a CTA, in chunks: in the share arithmetic every unit is
 // followed by so many of nothing.  64 ragged requests (64 to 4,096 keys): 65.1 us with
 // 16, 60.3 with 24, 59.0 with 28, 58.3 with 32, 59.4 with 36; 64 even ones (2,080 keys)
@@ -338,15 +339,15 @@ struct __align__(16) Note {
     uint32_t full, mask[NSUB];
 };
 
-template <int FMT, int HD, int MT, int HG>
+template <int FMT, int HD, int MT, int HG, int ENTRIES>
 struct __align__(16) Smem {
     using G = Geo<FMT, HD, MT, HG>;
     uint8_t buf[kWarps][G::kRingBytes];  // at the end of a unit a warp's output rows
     uint32_t q[HG][HD / 16][32][MT == 0 ? 2 : 4];  // q fragments of a unit, as a lane reads them
     Note<G::NSUB> note[kWarps][G::kStages];
     float m[kWarps][G::RB], l[kWarps][G::RB], w[kWarps][G::RB], lse[HG][G::RB];
-    Entry entry[kMaxEntries];
-    int prefix[kMaxEntries + 1];
+    Entry entry[ENTRIES];
+    int prefix[ENTRIES + 1];
     int last_part, longest;
     __device__ __forceinline__ float *out_row(int warp, int row) {
         return reinterpret_cast<float *>(buf[warp]) + row * G::kOStride;
@@ -426,14 +427,15 @@ __device__ __forceinline__ void merge_unit(const Params &p, int64_t unit, int hs
     }
 }
 
-template <int FMT, int HD, int MT, int HG>
+template <int FMT, int HD, int MT, int HG, int ENTRIES>
 __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
     attend_kernel(const Params p) {
     using G = Geo<FMT, HD, MT, HG>;
     constexpr int RB = G::RB;
     constexpr int kSteps = HD / 16;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    Smem<FMT, HD, MT, HG> &sm = *reinterpret_cast<Smem<FMT, HD, MT, HG> *>(smem_raw);
+    using S = Smem<FMT, HD, MT, HG, ENTRIES>;
+    S &sm = *reinterpret_cast<S *>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gq = lane >> 2, tq = lane & 3;
     pdl_wait();
@@ -1268,26 +1270,28 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const Params p) {
     for (int d = 0; d < V / 2; ++d) dst[d] = pack_bf16x2(acc[2 * d] * inv, acc[2 * d + 1] * inv);
 }
 
-template <int FMT, int HD, int MT, int HG>
+template <int FMT, int HD, int MT, int HG, int ENTRIES = kMaxEntries>
 int launch(const Params &p, bool merge, cudaStream_t stream) {
     constexpr int RB = MT == 0 ? 8 : 16;
-    constexpr size_t kBytes = sizeof(Smem<FMT, HD, MT, HG>);
+    constexpr size_t kBytes = sizeof(Smem<FMT, HD, MT, HG, ENTRIES>);
+    auto kernel = attend_kernel<FMT, HD, MT, HG, ENTRIES>;
     static std::atomic<uint64_t> configured{0};  // a bit per device
     int dev = 0;
     cudaGetDevice(&dev);
     const uint64_t bit = uint64_t(1) << (dev & 63);
     if (!(configured.load(std::memory_order_relaxed) & bit)) {
         const cudaError_t e = cudaFuncSetAttribute(
-            attend_kernel<FMT, HD, MT, HG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes);
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes);
         if (e != cudaSuccess) {
             note_cuda_error(e);
             return ATTN_ERR_CUDA;
         }
         configured.fetch_or(bit, std::memory_order_relaxed);
     }
-    const cudaError_t e0 = launch_pdl(attend_kernel<FMT, HD, MT, HG>, dim3((unsigned)p.grid), dim3(kThreads), kBytes,
-                                      stream, p);
+    const cudaError_t e0 =
+        launch_pdl(kernel, dim3((unsigned)p.grid), dim3(kThreads), kBytes, stream, p);
     if (e0 != cudaSuccess) return ATTN_ERR_CUDA;
+    if constexpr (ENTRIES != kMaxEntries) return ATTN_OK;  // (its merge is the caller's)
     if (!merge) return ATTN_OK;
     // Units that lie in many parts (few units, long contexts) have eight warps a row
     const int64_t units = (int64_t)p.n_entries * p.n_groups, rows = units * HG * RB;
@@ -1301,8 +1305,15 @@ int launch(const Params &p, bool merge, cudaStream_t stream) {
 
 }  // namespace att
 
+// KV heads of a unit of launch_attend_parts
+static int part_heads(const attn_kv_cache *cache, int mt, int n_kv_heads) {
+    const int most = cache->dtype == ATTN_KV_BF16 && mt == 0 ? 4 : 2;
+    return n_kv_heads % most == 0 ? most : n_kv_heads % 2 == 0 ? 2 : 1;
+}
+
 int plan_attend(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads, int n_kv_heads,
-                int head_dim, int max_seq_len, int window, int sinks, AttendPlan *plan) {
+                int head_dim, int max_seq_len, int window, int sinks, AttendPlan *plan,
+                bool parts) {
     const int64_t rows = (int64_t)q_rows * (n_q_heads / n_kv_heads);
     plan->mt = rows <= 8 ? 0 : 1;
     const int rb = plan->mt == 0 ? 8 : 16;
@@ -1323,6 +1334,7 @@ int plan_attend(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
     if (cache->layout == ATTN_LAYOUT_BSHD && head_dim == 64 && n_kv_heads % 2 == 0 &&
         (cache->dtype != ATTN_KV_BF16 || plan->mt == 0))
         plan->heads = 2;
+    if (parts) plan->heads = part_heads(cache, plan->mt, n_kv_heads);
     const int n_groups = n_kv_heads / plan->heads;
     const int64_t per_entry = (chunks + att::kGapChunks) * n_groups;
     // rows of one head and prefixes of chunks are counted in 32 bits
@@ -1333,7 +1345,7 @@ int plan_attend(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
     plan->row_blocks = (int)row_blocks;
     plan->entries = (int)entries;
     plan->per_launch = (int)std::max<int64_t>(
-        1, std::min<int64_t>(std::min<int64_t>(entries, att::kMaxEntries),
+        1, std::min<int64_t>(std::min<int64_t>(entries, parts ? att::kPartEntries : att::kMaxEntries),
                              (int64_t(1) << 30) / per_entry));
     const int per_sm = cache->dtype != ATTN_KV_BF16 ? 3 : head_dim == 64 ? 3 : 2;
     const int64_t needed = ((int64_t)plan->per_launch * (usual + att::kGapChunks) * n_groups +
@@ -1346,7 +1358,7 @@ int plan_attend(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
     // kKernelParts the merge kernel adds the parts up (else the kernel keeps to them)
     const int64_t share = std::max<int64_t>(
         att::kMinChunks, (int64_t)units * (usual + att::kGapChunks) / plan->grid);
-    plan->merge = usual / share + 1 > att::kKernelParts;
+    plan->merge = parts || usual / share + 1 > att::kKernelParts;
     // the counters are attn_decode's (zero between calls: one workspace serves both),
     // the rest lies behind them
     DecodePlan dp;
@@ -1415,32 +1427,38 @@ Params params_of(const AttendPlan &plan, const void *q, const attn_kv_cache *cac
     return p;
 }
 
-// The launch of p.n_entries entries from p.e0 on; merge: and of the merge kernel.
+// One of the kernels for a cache's format, the plan's rows and its heads
+template <typename F>
+int by_format(const attn_kv_cache *cache, F go) {
+    if (cache->dtype == ATTN_KV_BF16) return go(std::integral_constant<int, kBF16>{});
+    if (cache->dtype == ATTN_KV_INT8_SCALED) return go(std::integral_constant<int, kINT8>{});
+    return go(std::integral_constant<int, kE4M3>{});
+}
+
+// The launch of p.n_entries entries from p.e0 on, and of the merge kernel.
 int run(const Params &p, const AttendPlan &plan, const attn_kv_cache *cache, int head_dim,
-        bool merge, cudaStream_t stream) {
-    int rc = ATTN_ERR_UNSUPPORTED;
-    auto go = [&](auto fmt_c) {
+        cudaStream_t stream) {
+    return by_format(cache, [&](auto fmt_c) -> int {
         constexpr int F = decltype(fmt_c)::value;
-        if (head_dim == 128) {
-            rc = plan.mt == 0 ? launch<F, 128, 0, 1>(p, merge, stream)
-                              : launch<F, 128, 1, 1>(p, merge, stream);
-        } else if (plan.mt == 0) {
-            rc = plan.heads == 1 ? launch<F, 64, 0, 1>(p, merge, stream)
-                                 : launch<F, 64, 0, 2>(p, merge, stream);
-        } else {
-            if (plan.heads == 1)
-                rc = launch<F, 64, 1, 1>(p, merge, stream);
-            else if constexpr (F != kBF16)
-                rc = launch<F, 64, 1, 2>(p, merge, stream);
-        }
-    };
-    if (cache->dtype == ATTN_KV_BF16)
-        go(std::integral_constant<int, kBF16>{});
-    else if (cache->dtype == ATTN_KV_INT8_SCALED)
-        go(std::integral_constant<int, kINT8>{});
-    else
-        go(std::integral_constant<int, kE4M3>{});
-    return rc;
+        if (head_dim == 128)
+            return plan.mt == 0 ? launch<F, 128, 0, 1>(p, plan.merge, stream)
+                                : launch<F, 128, 1, 1>(p, plan.merge, stream);
+        if (plan.mt == 0)
+            return plan.heads == 1 ? launch<F, 64, 0, 1>(p, plan.merge, stream)
+                                   : launch<F, 64, 0, 2>(p, plan.merge, stream);
+        if (plan.heads == 1) return launch<F, 64, 1, 1>(p, plan.merge, stream);
+        if constexpr (F != kBF16) return launch<F, 64, 1, 2>(p, plan.merge, stream);
+        return ATTN_ERR_UNSUPPORTED;
+    });
+}
+
+// ... of launch_attend_parts
+template <int FMT, int HD, int MT>
+int run_parts(const Params &p, int heads, cudaStream_t stream) {
+    if constexpr (FMT == kBF16 && MT == 0)
+        if (heads == 4) return launch<FMT, HD, MT, 4, kPartEntries>(p, false, stream);
+    return heads == 2 ? launch<FMT, HD, MT, 2, kPartEntries>(p, false, stream)
+                      : launch<FMT, HD, MT, 1, kPartEntries>(p, false, stream);
 }
 
 }  // namespace att
@@ -1453,8 +1471,7 @@ int launch_attend(const AttendPlan &plan, const void *q, const attn_kv_cache *ca
                                    sinks, n_q_heads, n_kv_heads, scale, out, workspace, err);
     for (p.e0 = 0; p.e0 < plan.entries; p.e0 += plan.per_launch) {
         p.n_entries = std::min(plan.per_launch, plan.entries - p.e0);
-        if (int rc = att::run(p, plan, cache, head_dim, plan.merge, stream); rc != ATTN_OK)
-            return rc;
+        if (int rc = att::run(p, plan, cache, head_dim, stream); rc != ATTN_OK) return rc;
     }
     return ATTN_OK;
 }
@@ -1479,7 +1496,14 @@ int launch_attend_parts(const AttendPlan &plan, int e0, const int32_t *from, int
     parts->e0 = e0;
     parts->n_entries = p.n_entries;
     parts->held = cache->dtype == ATTN_KV_BF16 ? 0.f : att::kWeightLog2;
-    return att::run(p, plan, cache, head_dim, false, stream);
+    return att::by_format(cache, [&](auto fmt_c) -> int {
+        constexpr int F = decltype(fmt_c)::value;
+        if (head_dim == 128)
+            return plan.mt == 0 ? att::run_parts<F, 128, 0>(p, plan.heads, stream)
+                                : att::run_parts<F, 128, 1>(p, plan.heads, stream);
+        return plan.mt == 0 ? att::run_parts<F, 64, 0>(p, plan.heads, stream)
+                            : att::run_parts<F, 64, 1>(p, plan.heads, stream);
+    });
 }
 
 }  // namespace gqa

@@ -167,9 +167,11 @@ struct AttendPlan {
     size_t count_offset, parts_offset, lse_offset, o_offset, workspace;
 };
 
-// ATTN_OK, or ATTN_ERR_SHAPE for sizes past the kernel's index range.
+// ATTN_OK, or ATTN_ERR_SHAPE for sizes past the kernel's index range.  parts: for
+// launch_attend_parts.
 int plan_attend(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads, int n_kv_heads,
-                int head_dim, int max_seq_len, int window, int sinks, AttendPlan *plan);
+                int head_dim, int max_seq_len, int window, int sinks, AttendPlan *plan,
+                bool parts = false);
 
 int launch_attend(const AttendPlan &plan, const void *q, const attn_kv_cache *cache,
                   const int32_t *seq_lens, const int32_t *positions, int q_rows, int max_seq_len,

@@ -21,10 +21,10 @@
 //   warp 0       loads: TMA boxes of whole runs of keys (a page, or 128 of a linear cache), one
 //                a lane; where pages are no multiple of 8 keys, 16-byte cp.async by row
 //   warp 1       one thread issues tcgen05.mma: S = Q K^T, O += P V (f16, P from TMEM)
-//   warps 2, 3   bring what is loaded into the form that is multiplied: V of a bf16 cache to
+//   warps 4..7   bring what is loaded into the form that is multiplied: V of a bf16 cache to
 //                f16 in place, 8-bit codes to f16 (exact) from a ring of their own; keys
 //                outside the group's range become zeros
-//   warps 4..11  softmax, a thread a row of a tile; weights rounded once to f16 and written
+//   warps 8..15  softmax, a thread a row of a tile; weights rounded once to f16 and written
 //                over S in TMEM
 // The plan is made on the device from lengths, rows and positions, by every CTA for itself
 // (a captured graph follows them); CTAs are persistent for batches of more pairs than SMs.
@@ -42,6 +42,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -51,11 +52,7 @@ namespace shr {
 
 constexpr int kBM = 128;       // rows of a tile (two of them a CTA)
 constexpr int kBN = 128;       // keys of a tile
-constexpr int kThreads = 384;  // three warpgroups
-// As the chunk kernel: launched at 168 registers a thread, 4x32x96 + 8x32x200 = 63,488 <= 384x168
-constexpr uint32_t kRegsLaunch = 168;
-constexpr uint32_t kRegsControl = 96;
-constexpr uint32_t kRegsSoftmax = 200;
+constexpr int kThreads = 512;  // four warpgroups of 128 registers a thread
 constexpr int kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.0f;    // the reference maximum moves past this only
 constexpr float kWeightLog2 = 7.0f;     // weights are held times 2^7: at most 2^15
@@ -68,26 +65,43 @@ constexpr int kMaxBatch = 4096;         // requests: the plan's tables lie in th
 
 enum Fmt { kBF16 = 0, kE4M3 = 1, kINT8 = 2 };
 
+// Shared memory: Q tile 0, K, V, codes, in stages of 128 keys.  A load is under way for about
+// 2 us, longer than a tile's products, and a stage is taken from its request until its last
+// product, so depth is what counts: of five bf16 tiles of 128 dims V, which also waits for its
+// conversion and for the weights, has three (two: 2.3 us a pair of tiles, three: see DESIGN's
+// figures).  Where there is no Q tile 1 its place is one more K stage, or two of codes.
 template <int FMT, int HD>
 struct Cfg {
     static constexpr bool kCodes = FMT != kBF16;
     static constexpr int kHalves = HD / 64;
     // bf16: the rings that TMA fills; 8-bit: f16 tiles converted from a ring of codes
-    static constexpr int kKStages = kCodes ? (HD == 128 ? 2 : 3) : HD == 128 ? 3 : 4;
-    static constexpr int kVStages = kCodes ? (HD == 128 ? 2 : 3) : HD == 128 ? 2 : 4;
-    static constexpr int kRawStages = kCodes ? (HD == 128 ? 2 : 6) : 0;
+    static constexpr int kKStages = kCodes ? (HD == 128 ? 1 : 2) : HD == 128 ? 2 : 4;
+    static constexpr int kVStages = kCodes ? 2 : HD == 128 ? 3 : 5;
+    static constexpr int kRawStages = kCodes ? (HD == 128 ? 4 : 8) : 0;
     static constexpr int kQBytes = kBM * HD * 2;
     static constexpr int kTileBytes = kBN * HD * 2;        // of K or V, 16 bits an element
     static constexpr int kRawBytes = kCodes ? kBN * HD : 0;
-    static constexpr int kOffQ = 0;
-    static constexpr int kOffK = kOffQ + 2 * kQBytes;
-    static constexpr int kOffV = kOffK + kKStages * kTileBytes;
-    static constexpr int kOffRaw = kOffV + kVStages * kTileBytes;
-    static constexpr int kOffBar = kOffRaw + kRawStages * kRawBytes;
-    static constexpr int kNumBars = 3 * kKStages + 3 * kVStages + 2 * kRawStages + 10;
+    static constexpr int kOffK = kQBytes;
+    static constexpr int kOffQ1 = kOffK + kKStages * kTileBytes;
+    static constexpr int kOffRaw = kOffQ1 + kQBytes;       // (grows back over Q tile 1)
+    static constexpr int kOffV = kOffRaw + kRawStages * kRawBytes;
+    static constexpr int kOffBar = kOffV + kVStages * kTileBytes;
+    static constexpr int kMaxK = kKStages + (kCodes ? 0 : 1);  // with Q tile 1's place
+    static constexpr int kMaxRaw = kCodes ? kRawStages + 2 : 0;
+    static constexpr int kNumBars = 3 * kMaxK + 3 * kVStages + 2 * kMaxRaw + 10;
     static constexpr size_t kSmem = 1024 + kOffBar + kNumBars * 8 + 16;
+    static_assert(kSmem + 256 <= 227 * 1024, "shared memory");
     // the plan: 7 tables of a word a request, the chunks' masks and counts
     static_assert(kOffBar - kOffK >= (7 * kMaxBatch + 8 + kMaxBatch / 32 * 2) * 4, "plan");
+};
+
+// A stage of a ring, and how often it has been gone round (0 or 1)
+struct Turn {
+    int st = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++st == stages) st = 0, ph ^= 1;
+    }
 };
 
 struct Params {
@@ -95,6 +109,8 @@ struct Params {
     int n_rows, slots_per_seq, block_size, max_blocks, num_pages, cap, prefix_cap;
     int box_rows;  // keys of a TMA box; 0: rows are gathered
     int map_rows;  // extent of the maps' second dimension
+    uint32_t page_mul;
+    int page_shift;
     bool paged, head_major;
     const int32_t *block_table, *seq_lens, *positions, *prefix_rows, *prefix_lens;
     const uint8_t *k, *v;
@@ -144,8 +160,7 @@ __device__ __forceinline__ void request_range(const Params &p, int b, bool repor
 // scratch in shared memory; every thread of the CTA calls this and passes its last barrier.
 // Of U units (group, KV head, pair of tiles) that weigh their key tiles each is cut into
 // 1 + floor((SMs - U) tiles / sum) pieces, so that all are at most the SMs, or U.
-__device__ void make_plan(const Params &p, int32_t *mem, int want, bool tables, Piece &mine,
-                          int &total) {
+__device__ int make_plan(const Params &p, int32_t *mem, int want, bool tables, Piece &mine) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int B = p.batch, chunks = (B + 31) / 32;
     int32_t *r_lo = mem, *r_hi = r_lo + kMaxBatch, *g_start = r_hi + kMaxBatch;
@@ -153,7 +168,6 @@ __device__ void make_plan(const Params &p, int32_t *mem, int want, bool tables, 
     int32_t *g_base = g_parts + kMaxBatch, *c_mask = g_base + kMaxBatch;
     int32_t *c_base = c_mask + kMaxBatch / 32;
     __shared__ int s_groups, s_total;
-    __shared__ Piece s_mine;
     for (int c = warp; c < chunks; c += kThreads / 32) {
         const int b = c * 32 + lane;
         bool first = false;
@@ -171,7 +185,7 @@ __device__ void make_plan(const Params &p, int32_t *mem, int want, bool tables, 
         const uint32_t mask = __ballot_sync(0xffffffffu, first);
         if (lane == 0) c_mask[c] = (int32_t)mask;
     }
-    if (threadIdx.x == 0) s_mine.n_kt = 0;
+    if (threadIdx.x == 0) mine.n_kt = 0;
     __syncthreads();
     if (warp == 0) {
         int carry = 0;
@@ -266,7 +280,7 @@ __device__ void make_plan(const Params &p, int32_t *mem, int want, bool tables, 
                 m.pair = unit - m.kvh * pairs;
                 m.parts = (two ? 2 : 1) * cut;
                 m.base = base;
-                s_mine = m;
+                mine = m;
             }
             at += __shfl_sync(0xffffffffu, x, 31);
             row += __shfl_sync(0xffffffffu, y, 31);
@@ -282,8 +296,7 @@ __device__ void make_plan(const Params &p, int32_t *mem, int want, bool tables, 
             p.ws_rows[i] = make_int4(g_base[g] + (i - g_start[g] * p.q_rows) * p.group,
                                      n * p.q_rows * p.group, g_parts[g], 0);
         }
-    mine = s_mine;
-    total = s_total;
+    return s_total;
 }
 
 // Four codes -> two f16x2 words; exact.  INT8: a byte with its sign bit flipped is c + 128;
@@ -301,13 +314,6 @@ __device__ __forceinline__ void codes_to_f16(uint32_t x, uint32_t &lo, uint32_t 
         asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(bias));
         asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(bias));
     }
-}
-
-// max(a, |b|, |c|), NaN if one is
-__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
-    return d;
 }
 
 __device__ __forceinline__ float fast_log2(float x) {
@@ -332,6 +338,41 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, bool on
                  : "memory");
 }
 
+// Instructions of one thread, chosen by `on`, in code that the whole warp runs: addresses and
+// descriptors stay in uniform registers (behind `if (lane == 0)` every product first moves six
+// words there, 75 cycles a product against the 64 that it takes).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t on;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(on));
+    return on != 0;
+}
+__device__ __forceinline__ void mma_ss_if(bool on, uint32_t d, uint64_t a, uint64_t b,
+                                          uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"((uint32_t)on)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(bool on, uint32_t d, uint32_t a, uint64_t b,
+                                          uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"((uint32_t)on)
+        : "memory");
+}
+__device__ __forceinline__ void commit_if(bool on, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar)),
+        "r"((uint32_t)on)
+        : "memory");
+}
+
 // f16 words whose exponent is all ones become 0 in each half.
 __device__ __forceinline__ uint32_t drop_nan(uint32_t w) {
     if ((w & 0x7C00u) == 0x7C00u) w &= 0xFFFF0000u;
@@ -347,18 +388,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *sQ = smem + C::kOffQ, *sK = smem + C::kOffK, *sV = smem + C::kOffV;
-    uint8_t *sRaw = smem + C::kOffRaw;
+    uint8_t *sQ = smem, *sK = smem + C::kOffK, *sQ1 = smem + C::kOffQ1, *sV = smem + C::kOffV;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
-    uint64_t *k_full = bars;                     // [kKStages] loaded (bf16)
-    uint64_t *k_empty = k_full + C::kKStages;    // [kKStages] multiplied
-    uint64_t *k_conv = k_empty + C::kKStages;    // [kKStages] ready, where warps 2 and 3 pass it on
-    uint64_t *v_full = k_conv + C::kKStages;     // [kVStages]
+    uint64_t *k_full = bars;                  // [kMaxK] loaded (bf16)
+    uint64_t *k_empty = k_full + C::kMaxK;    // [kMaxK] multiplied
+    uint64_t *k_conv = k_empty + C::kMaxK;    // [kMaxK] ready, where warps 4 to 7 pass it on
+    uint64_t *v_full = k_conv + C::kMaxK;     // [kVStages]
     uint64_t *v_empty = v_full + C::kVStages;
     uint64_t *v_conv = v_empty + C::kVStages;
-    uint64_t *raw_full = v_conv + C::kVStages;   // [kRawStages] codes
-    uint64_t *raw_empty = raw_full + C::kRawStages;
-    uint64_t *q_full = raw_empty + C::kRawStages;
+    uint64_t *raw_full = v_conv + C::kVStages;   // [kMaxRaw] codes
+    uint64_t *raw_empty = raw_full + C::kMaxRaw;
+    uint64_t *q_full = raw_empty + C::kMaxRaw;
     uint64_t *q_conv = q_full + 1;
     uint64_t *s_full = q_conv + 1;  // [2]
     uint64_t *p_full = s_full + 2;  // [2 tiles][2 key halves]
@@ -366,19 +406,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *mma_done = o_done + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kNumBars);
     __shared__ int s_bad;  // a page of the piece's keys is not in the pool
+    __shared__ Piece w;    // (its fields are read where they are used: registers are short)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.group, R = p.q_rows, used = p.rt * G;
     const bool gather = p.box_rows == 0;
 
-    // Tile rows past the packed queries are never loaded: zeros
-    if (used < kBM)
-        for (int i = threadIdx.x; i < 2 * C::kHalves * (kBM - used) * 8; i += kThreads) {
-            const int piece = i & 7, row = used + (i >> 3) % (kBM - used);
-            const int th = (i >> 3) / (kBM - used);  // tile * halves + half
-            *reinterpret_cast<uint4 *>(sQ + th * (kBM * 128) + row * 128 + piece * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-        }
     if (warp == 1) {
         tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
@@ -398,19 +431,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; want != (int)blockIdx.x && i < C::kNumBars; ++i) mbar_inval(&bars[i]);
         const int loads = gather ? 32 : 1;
-        for (int s = 0; s < C::kKStages; ++s) {
+        for (int s = 0; s < C::kMaxK; ++s) {
             mbar_init(&k_full[s], loads);
             mbar_init(&k_empty[s], 1);
-            mbar_init(&k_conv[s], 64);  // every thread of warps 2 and 3
+            mbar_init(&k_conv[s], 128);  // every thread of warps 4 to 7
         }
         for (int s = 0; s < C::kVStages; ++s) {
             mbar_init(&v_full[s], loads);
             mbar_init(&v_empty[s], 1);
-            mbar_init(&v_conv[s], 64);
+            mbar_init(&v_conv[s], 128);
         }
-        for (int s = 0; s < C::kRawStages; ++s) {
+        for (int s = 0; s < C::kMaxRaw; ++s) {
             mbar_init(&raw_full[s], loads);
-            mbar_init(&raw_empty[s], 64);
+            mbar_init(&raw_empty[s], 128);
         }
         mbar_init(q_full, 1);
         mbar_init(q_conv, 256);
@@ -422,8 +455,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_barrier_init();
         s_bad = 0;
     }
-    Piece w;
-    make_plan(p, reinterpret_cast<int32_t *>(sK), want, want == (int)blockIdx.x, w, total);
+    total = make_plan(p, reinterpret_cast<int32_t *>(sK), want, want == (int)blockIdx.x, w);
+    // Tile rows past the packed queries are never loaded: zeros
+    if (used < kBM)
+        for (int i = threadIdx.x; i < 2 * C::kHalves * (kBM - used) * 8; i += kThreads) {
+            const int piece = i & 7, row = used + (i >> 3) % (kBM - used);
+            const int th = (i >> 3) / (kBM - used);  // tile * halves + half
+            *reinterpret_cast<uint4 *>((th < C::kHalves ? sQ : sQ1) + th % C::kHalves * (kBM * 128) +
+                                       row * 128 + piece * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
     fence_proxy_async_smem();  // the plan's words and the zeros in Q, before copies and products
     tc_fence_before();
     __syncthreads();
@@ -433,74 +473,79 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int first_pos = w.pair * 2 * p.rt;         // of the group's positions
     const bool dual = w.n_pos <= p.rt;               // one tile, two streams of key tiles
     const int n_tiles = w.n_pos - first_pos > p.rt ? 2 : 1;
+    const int k_stages = C::kKStages + (!C::kCodes && dual ? 1 : 0);
+    const int raw_stages = C::kRawStages + (C::kCodes && dual ? 2 : 0);
+    uint8_t *sRaw = smem + C::kOffRaw - (dual ? C::kQBytes : 0);
     const int32_t *table = p.paged ? p.block_table + (int64_t)w.prow * p.max_blocks : nullptr;
-    auto page_of = [&](int t) { return __ldg(table + t / p.block_size); };
+    // t / block_size = t m / 2^(31 + L) for 0 <= t < 2^31, m = floor(2^(31 + L) / block_size) + 1,
+    // 2^L >= block_size: m is less than 1 / block_size too large in the product
+    auto block_of = [&](int t) { return (int)(((uint64_t)t * p.page_mul) >> p.page_shift); };
+    auto page_of = [&](int t) { return __ldg(table + block_of(t)); };
 
-    if (warp < 4) {
-        setmaxnreg_dec<kRegsControl>();
+    if (warp < 8) {
         if (warp == 0) {
             // ------------------------------------------------------------ loads
             if (lane == 0) {
                 mbar_arrive_expect_tx(q_full, n_tiles * C::kHalves * used * 128);
                 for (int a = 0; a < n_tiles; ++a)
                     for (int hf = 0; hf < C::kHalves; ++hf)
-                        tma_load_3d(sQ + a * C::kQBytes + hf * (kBM * 128), &tm_q, hf * 64,
+                        tma_load_3d((a == 0 ? sQ : sQ1) + hf * (kBM * 128), &tm_q, hf * 64,
                                     w.kvh * G, w.start + first_pos + a * p.rt, q_full);
             }
             __syncwarp();
             constexpr int kBytes = FMT == kBF16 ? C::kTileBytes : C::kRawBytes;
-            const int boxes = gather ? 0 : kBN / p.box_rows;
-            auto fetch = [&](bool is_v, int tile, uint8_t *dst, uint64_t *bar) {
-                if (!gather) {
-                    if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
-                    __syncwarp();
-                    if (lane < boxes) {
-                        const int t = tile * kBN + lane * p.box_rows;
-                        bool on = t < w.hi && t + p.box_rows > w.lo;
-                        // slot-major: slot y; head-major: row y of (block, head) z
-                        int y = 0, z = 0;
-                        if (p.paged) {
-                            if (on) {
-                                const int page = page_of(t);
-                                on = (unsigned)page < (unsigned)p.num_pages;
-                                y = t % p.block_size;
-                                if (p.head_major)
-                                    z = page * p.n_kv_heads + w.kvh;
-                                else
-                                    y += page * p.block_size;
-                            }
-                        } else if (p.head_major) {
-                            y = t, z = w.prow * p.n_kv_heads + w.kvh;
-                        } else {
-                            y = w.prow * p.slots_per_seq + t;
-                        }
-                        if (!on) y = p.map_rows, z = 0;  // outside the tensor: zeros
-                        const CUtensorMap *map = is_v ? &tm_v : &tm_k;
-                        const int x = p.head_major ? 0 : w.kvh * HD;
-                        if constexpr (FMT == kBF16) {
-                            for (int hf = 0; hf < C::kHalves; ++hf)
-                                tma_load_3d(dst + hf * (kBN * 128) + lane * p.box_rows * 128, map,
-                                            x + hf * 64, y, z, bar);
-                        } else {
-                            tma_load_3d(dst + lane * p.box_rows * HD, map, x, y, z, bar);
-                        }
-                    }
-                    __syncwarp();
-                    return;
+            const int n_kt = w.n_kt, kt0 = w.kt0, lo = w.lo, hi = w.hi, prow = w.prow, kvh = w.kvh;
+            // this lane's box of a tile: whether it holds keys, its page, where it lies
+            const int box0 = lane * p.box_rows;
+            const bool boxed = !gather && box0 < kBN;
+            const int x0 = p.head_major ? 0 : kvh * HD;
+            auto holds = [&](int j) {
+                const int t = (kt0 + j) * kBN + box0;
+                return boxed && j < n_kt && t < hi && t + p.box_rows > lo;
+            };
+            auto read_page = [&](int j) {
+                return p.paged && holds(j) ? page_of((kt0 + j) * kBN + box0) : 0;
+            };
+            auto place = [&](int j, int page) {
+                const int t = (kt0 + j) * kBN + box0;
+                if (!holds(j) || (p.paged && (unsigned)page >= (unsigned)p.num_pages))
+                    return make_int2(p.map_rows, 0);  // outside the tensor: zeros
+                // slot-major: slot y; head-major: row y of (block, head) z
+                if (p.paged) {
+                    const int r = t - block_of(t) * p.block_size;
+                    return p.head_major ? make_int2(r, page * p.n_kv_heads + kvh)
+                                        : make_int2(page * p.block_size + r, 0);
                 }
-                // row by row: lane l finds rows l, l + 32, l + 64 and l + 96
-                const uint8_t *src = is_v ? p.v : p.k;
+                return p.head_major ? make_int2(t, prow * p.n_kv_heads + kvh)
+                                    : make_int2(prow * p.slots_per_seq + t, 0);
+            };
+            auto send = [&](const CUtensorMap *map, int2 at, uint8_t *dst, uint64_t *bar) {
+                if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
+                __syncwarp();
+                if (boxed) {
+                    if constexpr (FMT == kBF16) {
+                        for (int hf = 0; hf < C::kHalves; ++hf)
+                            tma_load_3d(dst + hf * (kBN * 128) + box0 * 128, map, x0 + hf * 64, at.x,
+                                        at.y, bar);
+                    } else {
+                        tma_load_3d(dst + box0 * HD, map, x0, at.x, at.y, bar);
+                    }
+                }
+                __syncwarp();
+            };
+            // row by row: lane l finds rows l, l + 32, l + 64 and l + 96
+            auto gather_rows = [&](const uint8_t *src, int j, uint8_t *dst, uint64_t *bar) {
                 constexpr int kPieces = kBytes / kBN / 16;  // of a row
                 const uint32_t to = smem_u32(dst);
 #pragma unroll 1
                 for (int i = 0; i < 4; ++i) {
-                    const int t = tile * kBN + i * 32 + lane;
+                    const int t = (kt0 + j) * kBN + i * 32 + lane;
                     int64_t off = -1;
-                    if (t < w.hi && t >= w.lo) {
+                    if (t < hi && t >= lo) {
                         const int page = page_of(t);
                         if ((unsigned)page < (unsigned)p.num_pages)
                             off = p.place.head_offset(
-                                (int64_t)page * p.block_size + t % p.block_size, w.kvh);
+                                (int64_t)page * p.block_size + (t - block_of(t) * p.block_size), kvh);
                     }
 #pragma unroll 4
                     for (int n = 0; n < kPieces; ++n) {
@@ -514,46 +559,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 cp_async_arrive_noinc(bar);
             };
-            // K one tile ahead of V
+            // K and V of a tile in turn (V behind the next K would wait for that K's stage, and
+            // the product for V); a tile's pages are read a tile before they are wanted
             int kj = 0, vj = 0;
-            while (kj < w.n_kt || vj < w.n_kt) {
-                const bool is_v = !(kj < w.n_kt && (kj <= vj + 1 || vj >= w.n_kt));
-                const int j = is_v ? vj : kj;
-                bool ok = true;
-                if constexpr (FMT == kBF16) {
-                    const int stages = is_v ? C::kVStages : C::kKStages, st = j % stages;
-                    if (j >= stages)
-                        ok = mbar_wait(is_v ? &v_empty[st] : &k_empty[st], ((j / stages) - 1) & 1,
-                                       p.err);
-                    if (!__all_sync(0xffffffffu, ok)) break;
-                    fetch(is_v, w.kt0 + j, (is_v ? sV : sK) + st * C::kTileBytes,
-                          is_v ? &v_full[st] : &k_full[st]);
-                } else {
-                    const int n = kj + vj, st = n % C::kRawStages;
-                    if (n >= C::kRawStages)
-                        ok = mbar_wait(&raw_empty[st], ((n / C::kRawStages) - 1) & 1, p.err);
-                    if (!__all_sync(0xffffffffu, ok)) break;
-                    fetch(is_v, w.kt0 + j, sRaw + st * C::kRawBytes, &raw_full[st]);
-                }
-                if (is_v)
-                    ++vj;
+            Turn kt, vt, rt;
+            auto load = [&](auto v_c, int j, int2 at) {
+                constexpr bool kV = decltype(v_c)::value;
+                Turn &t = C::kCodes ? rt : kV ? vt : kt;
+                uint64_t *empty = C::kCodes ? raw_empty : kV ? v_empty : k_empty;
+                uint64_t *full = C::kCodes ? raw_full : kV ? v_full : k_full;
+                uint8_t *to = (C::kCodes ? sRaw : kV ? sV : sK) + t.st * kBytes;
+                const bool ok = mbar_wait(&empty[t.st], t.ph ^ 1, p.err);
+                if (!__all_sync(0xffffffffu, ok)) return false;
+                if (gather)
+                    gather_rows(kV ? p.v : p.k, j, to, &full[t.st]);
                 else
-                    ++kj;
+                    send(kV ? &tm_v : &tm_k, at, to, &full[t.st]);
+                t.next(C::kCodes ? raw_stages : kV ? C::kVStages : k_stages);
+                return true;
+            };
+            int page = read_page(0);
+            for (bool ok = true; ok && vj < n_kt;) {
+                const int2 at = place(kj, page);
+                page = read_page(kj + 1);
+                ok = load(std::false_type{}, kj, at);
+                kj += ok;
+                ok = ok && load(std::true_type{}, vj, at);
+                vj += ok;
             }
             // No copy may still be landing when the CTA exits (normally all have been read)
-            if constexpr (FMT == kBF16) {
-                for (int j = max(0, kj - C::kKStages); j < kj; ++j)
-                    mbar_wait(&k_full[j % C::kKStages], (j / C::kKStages) & 1, p.err);
-                for (int j = max(0, vj - C::kVStages); j < vj; ++j)
-                    mbar_wait(&v_full[j % C::kVStages], (j / C::kVStages) & 1, p.err);
+            auto landed = [&](uint64_t *full, int n, int stages) {
+                for (int j = max(0, n - stages); j < n; ++j)
+                    mbar_wait(&full[j % stages], (j / stages) & 1, p.err);
+            };
+            if constexpr (C::kCodes) {
+                landed(raw_full, kj + vj, raw_stages);
             } else {
-                for (int n = max(0, kj + vj - C::kRawStages); n < kj + vj; ++n)
-                    mbar_wait(&raw_full[n % C::kRawStages], (n / C::kRawStages) & 1, p.err);
+                landed(k_full, kj, k_stages);
+                landed(v_full, vj, C::kVStages);
             }
             mbar_wait(q_full, 0, p.err);
         } else if (warp == 1) {
             // ------------------------------------------------------------ products
-            if (lane == 0) {
+            {
+                const bool on = elect_one();
                 constexpr uint32_t idesc_qk = FMT == kBF16 ? idesc_bf16_f32(kBM, kBN, 0, 0)
                                                            : idesc_f16_f32(kBM, kBN, 0, 0);
                 constexpr uint32_t idesc_pv = idesc_f16_f32(kBM, HD, 0, 1);
@@ -562,15 +611,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t v_desc0 = smem_desc_sw128(smem_u32(sV), kBN * 128, 1024);
                 // scores of Q tile qt into S a
                 auto issue_qk = [&](int a, int qt, int kst) {
-                    const uint64_t qd = q_desc + (uint64_t)((qt * C::kQBytes) >> 4);
+                    const uint64_t qd = q_desc + (uint64_t)((qt * C::kOffQ1) >> 4);
                     const uint64_t kd = k_desc0 + (uint64_t)((kst * C::kTileBytes) >> 4);
 #pragma unroll
                     for (int kk = 0; kk < HD / 16; ++kk) {
                         const uint64_t off =
                             (uint64_t)(((kk >> 2) * (kBM * 128) + (kk & 3) * 32) >> 4);
-                        tc_mma_ss(tmem + a * 128, qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
+                        mma_ss_if(on, tmem + a * 128, qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
                     }
-                    tc_commit(&s_full[a]);
+                    commit_if(on, &s_full[a]);
                 };
                 auto issue_pv_half = [&](int a, int vst, int hh, bool first) {
                     const uint64_t vd = v_desc0 + (uint64_t)((vst * C::kTileBytes) >> 4);
@@ -579,79 +628,82 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int k4 = 0; k4 < kBN / 32; ++k4) {
                         const int kk = hh * (kBN / 32) + k4;
-                        tc_mma_ts(o_tmem, p_tmem + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4),
-                                  idesc_pv, (!first || k4 > 0) ? 1u : 0u);
+                        mma_ts_if(on, o_tmem, p_tmem + kk * 8,
+                                  vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
+                                  (!first || k4 > 0) ? 1u : 0u);
                     }
                 };
-                auto k_ready = [&](int j) {
-                    const int st = j % C::kKStages, ph = (j / C::kKStages) & 1;
-                    return mbar_wait(FMT != kBF16 || gather ? &k_conv[st] : &k_full[st], ph, p.err);
+                Turn kt, vt;
+                uint64_t *k_in = C::kCodes || gather ? k_conv : k_full;
+                auto k_ready = [&] { return mbar_wait(&k_in[kt.st], kt.ph, p.err); };
+                auto k_done = [&] {
+                    commit_if(on, &k_empty[kt.st]);
+                    kt.next(k_stages);
                 };
-                // the weights of a stream's jj-th key tile, tile j, into its output
-                auto pv = [&](int a, int j, int jj) {
+                // the weights of a stream's jj-th key tile into its output
+                auto pv = [&](int a, int jj) {
                     for (int hh = 0; hh < 2; ++hh) {
                         if (!mbar_wait(&p_full[a * 2 + hh], jj & 1, p.err)) return false;
                         tc_fence_after();
-                        issue_pv_half(a, j % C::kVStages, hh, jj == 0 && hh == 0);
+                        issue_pv_half(a, vt.st, hh, jj == 0 && hh == 0);
                     }
                     return true;
                 };
+                const int n_kt = w.n_kt;
                 bool ok = mbar_wait(FMT == kBF16 ? q_full : q_conv, 0, p.err);
                 if (dual) {
                     // tile j belongs to stream j & 1
-                    for (int j = 0; ok && j < min(2, w.n_kt); ++j) {
-                        ok = k_ready(j);
+                    for (int j = 0; ok && j < min(2, n_kt); ++j) {
+                        ok = k_ready();
                         if (!ok) break;
                         tc_fence_after();
-                        issue_qk(j, 0, j % C::kKStages);
-                        tc_commit(&k_empty[j % C::kKStages]);
+                        issue_qk(j, 0, kt.st);
+                        k_done();
                     }
-                    for (int j = 0; ok && j < w.n_kt; ++j) {
-                        ok = mbar_wait(&v_conv[j % C::kVStages], (j / C::kVStages) & 1, p.err) &&
-                             pv(j & 1, j, j >> 1);
+                    for (int j = 0; ok && j < n_kt; ++j) {
+                        ok = mbar_wait(&v_conv[vt.st], vt.ph, p.err) && pv(j & 1, j >> 1);
                         if (!ok) break;
-                        tc_commit(&v_empty[j % C::kVStages]);
-                        if (j + 2 < w.n_kt) {
-                            ok = k_ready(j + 2);
+                        commit_if(on, &v_empty[vt.st]);
+                        vt.next(C::kVStages);
+                        if (j + 2 < n_kt) {
+                            ok = k_ready();
                             if (!ok) break;
                             tc_fence_after();
-                            issue_qk(j & 1, 0, (j + 2) % C::kKStages);
-                            tc_commit(&k_empty[(j + 2) % C::kKStages]);
+                            issue_qk(j & 1, 0, kt.st);
+                            k_done();
                         }
                     }
                 } else {
-                    ok = ok && k_ready(0);
+                    ok = ok && k_ready();
                     if (ok) {
                         tc_fence_after();
-                        for (int a = 0; a < n_tiles; ++a) issue_qk(a, a, 0);
-                        tc_commit(&k_empty[0]);
+                        for (int a = 0; a < n_tiles; ++a) issue_qk(a, a, kt.st);
+                        k_done();
                     }
-                    for (int j = 0; ok && j < w.n_kt; ++j) {
-                        ok = mbar_wait(&v_conv[j % C::kVStages], (j / C::kVStages) & 1, p.err);
-                        const int kst = (j + 1) % C::kKStages;
+                    for (int j = 0; ok && j < n_kt; ++j) {
+                        const bool more = j + 1 < n_kt;
+                        ok = mbar_wait(&v_conv[vt.st], vt.ph, p.err);
                         for (int a = 0; ok && a < n_tiles; ++a) {
-                            ok = pv(a, j, j);
+                            ok = pv(a, j) && (!more || a > 0 || k_ready());
                             if (!ok) break;
-                            if (a == n_tiles - 1) tc_commit(&v_empty[j % C::kVStages]);
-                            if (j + 1 < w.n_kt) {
-                                if (a == 0) {
-                                    ok = k_ready(j + 1);
-                                    if (!ok) break;
-                                    tc_fence_after();
-                                }
-                                issue_qk(a, a, kst);
-                                if (a == n_tiles - 1) tc_commit(&k_empty[kst]);
+                            if (a == n_tiles - 1) commit_if(on, &v_empty[vt.st]);
+                            if (more) {
+                                tc_fence_after();
+                                issue_qk(a, a, kt.st);
                             }
                         }
+                        if (more) k_done();
+                        vt.next(C::kVStages);
                     }
                 }
-                tc_commit(o_done);
-                tc_commit(mma_done);
+                commit_if(on, o_done);
+                commit_if(on, mma_done);
                 mbar_wait(mma_done, 0, p.err);
             }
-        } else {
+        } else if (warp >= 4) {
             // ------------------------------------------------------------ into f16
-            const int ct = threadIdx.x - 64;  // 0 .. 63
+            constexpr int kConv = 128;          // threads
+            const int ct = threadIdx.x - 128;
             // keys of a tile that lie in the group's range
             auto inside = [&](int tile, int row) {
                 const int t = tile * kBN + row;
@@ -663,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // f16 NaN among this thread's pieces of a V tile become 0
             auto clean = [&](uint32_t at) {
                 report_error(p.err, ATTN_ERR_UNSUPPORTED);
-                for (int i = ct; i < C::kTileBytes / 16; i += 64) {
+                for (int i = ct; i < C::kTileBytes / 16; i += kConv) {
                     uint4 x = ld_shared_v4(at + i * 16);
                     x.x = drop_nan(x.x), x.y = drop_nan(x.y);
                     x.z = drop_nan(x.z), x.w = drop_nan(x.w);
@@ -673,22 +725,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             // a tile of bf16 V in place
             auto v_in_place = [&](int tile, uint32_t at) {
                 const bool all = whole(tile);
-                float amax = 0.f;
-#pragma unroll 4
-                for (int i = ct; i < C::kTileBytes / 16; i += 64) {
-                    uint4 x = ld_shared_v4(at + i * 16);
-                    if (!all && !inside(tile, (i >> 3) & (kBN - 1))) x = make_uint4(0u, 0u, 0u, 0u);
-                    uint32_t *u = &x.x;
+                __half2 most = __half2half2(__ushort_as_half(0));  // largest magnitudes
+                constexpr int kBatch = 8;  // pieces read before one is written
+                for (int i0 = ct; i0 < C::kTileBytes / 16; i0 += kConv * kBatch) {
+                    uint4 x[kBatch];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float x0 = __uint_as_float(u[e] << 16);
-                        const float x1 = __uint_as_float(u[e] & 0xFFFF0000u);
-                        amax = max3_abs_nan(amax, x0, x1);
-                        u[e] = pack_f16x2_sat(x0, x1);
+                    for (int b = 0; b < kBatch; ++b)
+                        x[b] = ld_shared_v4(at + (i0 + kConv * b) * 16);
+#pragma unroll
+                    for (int b = 0; b < kBatch; ++b) {
+                        const int i = i0 + kConv * b;
+                        if (!all && !inside(tile, (i >> 3) & (kBN - 1)))
+                            x[b] = make_uint4(0u, 0u, 0u, 0u);
+                        uint32_t *u = &x[b].x;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            u[e] = bf16x2_to_f16x2_sat(u[e]);
+                            most = __hmax2_nan(
+                                most, __habs2(*reinterpret_cast<const __half2 *>(&u[e])));
+                        }
+                        st_shared_v4(at + i * 16, x[b]);
                     }
-                    st_shared_v4(at + i * 16, x);
                 }
-                if (!(amax < 65536.f)) clean(at);
+                // 65504 itself is no bf16: only saturated values and NaN reach it
+                const uint32_t top = *reinterpret_cast<const uint32_t *>(&most);
+                if (__vcmpgeu2(top, 0x7BFF7BFFu) != 0) clean(at);
             };
             // A tile of codes from `from` into an f16 tile.  Eight lanes read 4 pieces (16 codes)
             // of rows r and r ^ 5 (128-byte rows, swizzled) or of two rows (64-byte ones), so
@@ -696,48 +757,60 @@ __global__ void __launch_bounds__(kThreads, 1)
             // 128 bytes, swizzled) meet in a bank.
             auto widen = [&](bool is_v, int tile, uint32_t from, uint32_t to) {
                 const bool all = !is_v || whole(tile);
-                constexpr int kRounds = HD / 64 * (kBN / 8) / 2;  // of 8 rows x 4 pieces a warp
-#pragma unroll 2
-                for (int i = 0; i < kRounds; ++i) {
-                    const int unit = i * 2 + (ct >> 5);  // (8 rows, 64 dims)
-                    const int hf = unit % C::kHalves, r8 = unit / C::kHalves;
-                    const int l = ct & 31, ph = l >> 3, second = (l >> 2) & 1;
-                    const int row = r8 * 8 + (HD == 128 ? (second ? ph ^ 5 : ph) : 2 * ph + second);
-                    const int piece = l & 3;  // of the 64 dims
-                    uint4 x = ld_shared_v4(
-                        HD == 128 ? from + row * 128 + (((hf * 4 + piece) ^ (row & 7)) << 4)
-                                  : from + row * 64 + piece * 16);
-                    if (!all && !inside(tile, row)) x = make_uint4(0u, 0u, 0u, 0u);
-                    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t h[8], odd = 0;
+                constexpr int kRounds = HD / 64 * (kBN / 8) / 4;  // of 8 rows x 4 pieces a warp
+                constexpr int kBatch = 4;  // pieces read before one is written
+                const int l = ct & 31, ph = l >> 3, second = (l >> 2) & 1, piece = l & 3;
+                auto half_of = [&](int i) { return (i * 4 + (ct >> 5)) % C::kHalves; };
+                auto row_of = [&](int i) {  // unit 4 i + warp: (8 rows, 64 dims)
+                    return (i * 4 + (ct >> 5)) / C::kHalves * 8 +
+                           (HD == 128 ? (second ? ph ^ 5 : ph) : 2 * ph + second);
+                };
+#pragma unroll 1
+                for (int i0 = 0; i0 < kRounds; i0 += kBatch) {
+                    uint4 x[kBatch];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        codes_to_f16<FMT>(u[e], h[2 * e], h[2 * e + 1]);
-                        if (FMT == kE4M3)  // a code of NaN, 0x7F or 0xFF
-                            odd |= ((u[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                    for (int b = 0; b < kBatch; ++b) {
+                        const int row = row_of(i0 + b);
+                        x[b] = ld_shared_v4(
+                            HD == 128
+                                ? from + row * 128 + (((half_of(i0 + b) * 4 + piece) ^ (row & 7)) << 4)
+                                : from + row * 64 + piece * 16);
                     }
-                    if (is_v && odd != 0) {
-                        report_error(p.err, ATTN_ERR_UNSUPPORTED);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) h[e] = drop_nan(h[e]);
+                    for (int b = 0; b < kBatch; ++b) {
+                        const int row = row_of(i0 + b);
+                        if (!all && !inside(tile, row)) x[b] = make_uint4(0u, 0u, 0u, 0u);
+                        const uint32_t u[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
+                        uint32_t h[8], odd = 0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            codes_to_f16<FMT>(u[e], h[2 * e], h[2 * e + 1]);
+                            if (FMT == kE4M3)  // a code of NaN, 0x7F or 0xFF
+                                odd |= ((u[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                        }
+                        if (is_v && odd != 0) {
+                            report_error(p.err, ATTN_ERR_UNSUPPORTED);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) h[e] = drop_nan(h[e]);
+                        }
+                        const uint32_t base = to + half_of(i0 + b) * (kBN * 128) + row * 128;
+                        st_shared_v4(base + (((2 * piece) ^ (row & 7)) << 4),
+                                     make_uint4(h[0], h[1], h[2], h[3]));
+                        st_shared_v4(base + (((2 * piece + 1) ^ (row & 7)) << 4),
+                                     make_uint4(h[4], h[5], h[6], h[7]));
                     }
-                    const uint32_t base = to + hf * (kBN * 128) + row * 128;
-                    st_shared_v4(base + (((2 * piece) ^ (row & 7)) << 4),
-                                 make_uint4(h[0], h[1], h[2], h[3]));
-                    st_shared_v4(base + (((2 * piece + 1) ^ (row & 7)) << 4),
-                                 make_uint4(h[4], h[5], h[6], h[7]));
                 }
             };
-            int kj = 0, vj = 0, n = 0;
+            Turn kt, vt, rt;
             bool ok = true;
-            while (ok && (kj < w.n_kt || vj < w.n_kt)) {
-                const bool is_v = !(kj < w.n_kt && (kj <= vj + 1 || vj >= w.n_kt));
-                const int j = is_v ? vj++ : kj++;
-                const int stages = is_v ? C::kVStages : C::kKStages, st = j % stages;
-                const uint32_t ph = (j / stages) & 1;
+            for (int i = 0; i < 2 * w.n_kt; ++i) {
+                const bool is_v = i & 1;
+                const int j = i >> 1;
+                if (FMT == kBF16 && !is_v && !gather) continue;
+                const int st = is_v ? vt.st : kt.st;
+                const uint32_t ph = is_v ? vt.ph : kt.ph;
                 const uint32_t at = smem_u32((is_v ? sV : sK) + st * C::kTileBytes);
                 if constexpr (FMT == kBF16) {
-                    if (!is_v && !gather) continue;
                     ok = mbar_wait(is_v ? &v_full[st] : &k_full[st], ph, p.err);
                     if (!ok) break;
                     if (is_v) {
@@ -746,31 +819,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // copied by cp.async: written again, so that this thread's fence
                         // covers what the tensor cores read
 #pragma unroll 4
-                        for (int i = ct; i < C::kTileBytes / 16; i += 64)
+                        for (int i = ct; i < C::kTileBytes / 16; i += kConv)
                             st_shared_v4(at + i * 16, ld_shared_v4(at + i * 16));
                     }
                 } else {
-                    const int rs = n % C::kRawStages;
-                    ok = mbar_wait(&raw_full[rs], (n / C::kRawStages) & 1, p.err);
-                    if (ok && j >= stages)
-                        ok = mbar_wait(is_v ? &v_empty[st] : &k_empty[st], ph ^ 1, p.err);
+                    ok = mbar_wait(&raw_full[rt.st], rt.ph, p.err) &&
+                         mbar_wait(is_v ? &v_empty[st] : &k_empty[st], ph ^ 1, p.err);
                     if (!ok) break;
-                    widen(is_v, w.kt0 + j, smem_u32(sRaw + rs * C::kRawBytes), at);
+                    widen(is_v, w.kt0 + j, smem_u32(sRaw + rt.st * C::kRawBytes), at);
                     fence_proxy_async_smem();
-                    mbar_arrive(&raw_empty[rs]);
-                    ++n;
+                    mbar_arrive(&raw_empty[rt.st]);
+                    rt.next(raw_stages);
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(is_v ? &v_conv[st] : &k_conv[st]);
+                if (is_v)
+                    vt.next(C::kVStages);
+                else
+                    kt.next(k_stages);
             }
         }
     } else {
-        setmaxnreg_inc<kRegsSoftmax>();
         // ---------------------------------------------------------------- softmax
-        const int a = (warp - 4) >> 2;     // which tile, or stream
+        const int a = (warp - 8) >> 2;     // which tile, or stream
         const int quad = warp & 3;         // TMEM lane quadrant of this warp
         const int row = quad * 32 + lane;  // tile row = TMEM lane
-        const int st = threadIdx.x - 128;  // 0 .. 255
+        const int st = threadIdx.x - 256;  // 0 .. 255
         // a page that is not there is reported, and its keys are looked for in every tile
         if (p.paged) {
             const int b0 = max(w.lo, w.kt0 * kBN) / p.block_size;
@@ -786,9 +860,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (FMT != kBF16) {
             // q to f16 in place
             if (mbar_wait(q_full, 0, p.err)) {
-                const uint32_t at = smem_u32(sQ);
                 uint32_t big = 0;
                 for (int i = st; i < n_tiles * C::kQBytes / 16; i += 256) {
+                    const int tile = i / (C::kQBytes / 16);
+                    const uint32_t at = smem_u32(tile == 0 ? sQ : sQ1 - C::kQBytes);
                     uint4 x = ld_shared_v4(at + i * 16);
                     uint32_t *u = &x.x;
 #pragma unroll
@@ -837,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (p.paged) {
                 const int page = page_of(t);
                 if ((unsigned)page >= (unsigned)p.num_pages) return;
-                slot = (int64_t)page * p.block_size + t % p.block_size;
+                slot = (int64_t)page * p.block_size + (t - block_of(t) * p.block_size);
             } else {
                 slot = (int64_t)w.prow * p.slots_per_seq + t;
             }
@@ -861,65 +936,77 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, mbar_wait(&s_full[a], jj & 1, p.err));
             if (!ok) break;
             tc_fence_after();
-            float s[kBN];
-            {
-                uint32_t(&u)[kBN] = *reinterpret_cast<uint32_t(*)[kBN]>(s);
-                tmem_ld_32x32b_x32(s_tmem + 0, *reinterpret_cast<uint32_t(*)[32]>(u + 0));
-                tmem_ld_32x32b_x32(s_tmem + 32, *reinterpret_cast<uint32_t(*)[32]>(u + 32));
-                tmem_ld_32x32b_x32(s_tmem + 64, *reinterpret_cast<uint32_t(*)[32]>(u + 64));
-                tmem_ld_32x32b_x32(s_tmem + 96, *reinterpret_cast<uint32_t(*)[32]>(u + 96));
-                tmem_wait_ld();
-                tmem_regs_after_wait(u);
-            }
             const int key0 = (w.kt0 + j) * kBN;
-            if (key0 + kBN - 1 > key_cap || (p.window > 0 && qi - key0 >= p.window)) {
-                // the row sees columns lo <= c <= hi (c = key - key0)
-                const int hi = key_cap - key0;
-                const int lo = p.window > 0 ? qi - p.window + 1 - key0 : 0;
-#pragma unroll
-                for (int c = 0; c < kBN; ++c) s[c] = (c <= hi && c >= lo) ? s[c] : -INFINITY;
-            }
-            if (any_bad) {
-#pragma unroll 1
-                for (int c0 = 0; c0 < kBN; c0 += 32) {
+            // the row sees columns lo <= c <= hi (c = key - key0)
+            const int hi = key_cap - key0, lo = p.window > 0 ? qi - p.window + 1 - key0 : 0;
+            const bool masked = hi < kBN - 1 || lo > 0 || any_bad;
+            // Scores of columns c0 .. c0 + 31, -inf where the row does not see the key, back in
+            // TMEM too
+            auto mask = [&](float(&s)[32], int c0) {
+                uint32_t see = c0 > hi || c0 + 31 < lo ? 0u : 0xffffffffu;
+                if (hi - c0 < 31) see &= (2u << max(0, hi - c0)) - 1u;
+                if (lo > c0) see &= 0xffffffffu << min(31, lo - c0);
+                if (any_bad) {
                     const int t = key0 + c0 + lane;
-                    const bool bad = t >= w.lo && t < w.hi &&
-                                     (unsigned)page_of(t) >= (unsigned)p.num_pages;
-                    const uint32_t mask = __ballot_sync(0xffffffffu, bad);
-#pragma unroll
-                    for (int c = 0; c < kBN; ++c)
-                        if ((c & ~31) == c0 && (mask >> (c & 31) & 1u)) s[c] = -INFINITY;
+                    see &= ~__ballot_sync(0xffffffffu,
+                                          t >= w.lo && t < w.hi &&
+                                              (unsigned)page_of(t) >= (unsigned)p.num_pages);
                 }
+#pragma unroll
+                for (int c = 0; c < 32; ++c) s[c] = see >> c & 1u ? s[c] : -INFINITY;
+                tmem_st_32x32b_x32(s_tmem + c0, *reinterpret_cast<uint32_t(*)[32]>(s));
+            };
+            // S is read from TMEM twice, 64 columns at a time, and the loops are kept rolled:
+            // all 128 in registers leave too few for the rest, and unrolled code waits for the
+            // instruction cache (the two warpgroups run different parts of it)
+            float s0[32], s1[32];
+            uint32_t(&u0)[32] = *reinterpret_cast<uint32_t(*)[32]>(s0);
+            uint32_t(&u1)[32] = *reinterpret_cast<uint32_t(*)[32]>(s1);
+            float mx = -INFINITY;
+            auto top = [&](const float(&s)[32], int c0) {
+                if constexpr (FMT == kBF16) {
+                    float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
+#pragma unroll
+                    for (int c = 4; c + 8 <= 32; c += 8) {
+                        m0 = max3(m0, s[c], s[c + 1]);
+                        m1 = max3(m1, s[c + 2], s[c + 3]);
+                        m2 = max3(m2, s[c + 4], s[c + 5]);
+                        m3 = max3(m3, s[c + 6], s[c + 7]);
+                    }
+                    m0 = max3(m0, s[28], s[29]), m1 = max3(m1, s[30], s[31]);
+                    mx = max3(mx, max3(m0, m1, m2), m3);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        // x = s f + lv grows with s (f > 0): its maximum is that of s
+                        const float *x = s + 16 * i;
+                        float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[4], x[5]);
+                        m0 = max3(m0, x[6], x[7]), m1 = max3(m1, x[8], x[9]);
+                        m0 = max3(m0, x[10], x[11]), m1 = max3(m1, x[12], x[13]);
+                        mx = fmaxf(mx, fmaf(max3(m0, m1, fmaxf(x[14], x[15])),
+                                            __shfl_sync(0xffffffffu, f_lane, c0 / 16 + i),
+                                            __shfl_sync(0xffffffffu, lv_lane, c0 / 16 + i)));
+                    }
+                }
+            };
+            const bool any_masked = __any_sync(0xffffffffu, masked);
+#pragma unroll 1
+            for (int c0 = 0; c0 < kBN; c0 += 64) {
+                tmem_ld_32x32b_x32(s_tmem + c0, u0);
+                tmem_ld_32x32b_x32(s_tmem + c0 + 32, u1);
+                tmem_wait_ld();
+                tmem_regs_after_wait(u0);
+                tmem_regs_after_wait(u1);
+                if (any_masked) {
+                    mask(s0, c0);
+                    mask(s1, c0 + 32);
+                    tmem_wait_st();
+                }
+                top(s0, c0);
+                top(s1, c0 + 32);
             }
-            float mx;
-            float f[8], lv[8], inv[8];  // of 16 keys each
-            if constexpr (FMT == kBF16) {
-                float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
-#pragma unroll
-                for (int c = 4; c + 8 <= kBN; c += 8) {  // columns 4 .. kBN - 5
-                    mx0 = max3(mx0, s[c], s[c + 1]);
-                    mx1 = max3(mx1, s[c + 2], s[c + 3]);
-                    mx2 = max3(mx2, s[c + 4], s[c + 5]);
-                    mx3 = max3(mx3, s[c + 6], s[c + 7]);
-                }
-                mx0 = max3(mx0, s[kBN - 4], s[kBN - 3]);  // the last four columns
-                mx1 = max3(mx1, s[kBN - 2], s[kBN - 1]);
-                mx = max3(mx0, mx1, fmaxf(mx2, mx3)) * sl2;
-            } else {
-                mx = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    f[i] = __shfl_sync(0xffffffffu, f_lane, i);
-                    lv[i] = __shfl_sync(0xffffffffu, lv_lane, i);
-                    inv[i] = __shfl_sync(0xffffffffu, inv_lane, i);
-                    // x = s f + lv grows with s (f > 0): its maximum is that of s
-                    const float *x = s + 16 * i;
-                    float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[4], x[5]);
-                    m0 = max3(m0, x[6], x[7]), m1 = max3(m1, x[8], x[9]);
-                    m0 = max3(m0, x[10], x[11]), m1 = max3(m1, x[12], x[13]);
-                    mx = fmaxf(mx, fmaf(max3(m0, m1, fmaxf(x[14], x[15])), f[i], lv[i]));
-                }
-            }
+            tmem_ld_32x32b_x32(s_tmem, u0);  // (under way meanwhile)
+            if constexpr (FMT == kBF16) mx *= sl2;
             float alpha = 1.f;
             if (mx > m_run + kRescaleLog2 || m_run == -INFINITY) {
                 const float m_new = mx == -INFINITY ? m_run : mx;
@@ -927,51 +1014,61 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m_run = m_new;
             }
             if (jj > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll
+#pragma unroll 1
                 for (int c0 = 0; c0 < HD; c0 += 32) {
-                    uint32_t orow[32];
-                    tmem_ld_32x32b_x32(o_tmem + c0, orow);
+                    tmem_ld_32x32b_x32(o_tmem + c0, u1);
                     tmem_wait_ld();
-                    tmem_regs_after_wait(orow);
+                    tmem_regs_after_wait(u1);
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        orow[e] = __float_as_uint(__uint_as_float(orow[e]) * alpha);
-                    tmem_st_32x32b_x32(o_tmem + c0, orow);
+                        u1[e] = __float_as_uint(__uint_as_float(u1[e]) * alpha);
+                    tmem_st_32x32b_x32(o_tmem + c0, u1);
                 }
             }
             const float m_w = (m_run == -INFINITY ? 0.f : m_run) - kWeightLog2;
-            float sum0 = 0.f, sum1 = 0.f, over = 0.f;
-#pragma unroll
-            for (int c0 = 0; c0 < kBN; c0 += 32) {
+            float sum = 0.f, over = 0.f;
+            // weights of columns c0 .. c0 + 31: over their own S columns, 32 keys in 16
+            auto weigh = [&](float(&s)[32], int c0) {
                 uint32_t pk[16];
+                float sum0 = 0.f, sum1 = 0.f, f = sl2, shift = -m_w;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const int i = (c0 + 2 * e) / 16;
+                    if (FMT != kBF16 && (e & 7) == 0) {
+                        f = __shfl_sync(0xffffffffu, f_lane, c0 / 16 + e / 8);
+                        shift = __shfl_sync(0xffffffffu, lv_lane, c0 / 16 + e / 8) - m_w;
+                    }
                     float x0, x1;
-                    if constexpr (FMT == kBF16)
-                        fma2(x0, x1, s[c0 + 2 * e], s[c0 + 2 * e + 1], sl2, sl2, -m_w, -m_w);
-                    else
-                        fma2(x0, x1, s[c0 + 2 * e], s[c0 + 2 * e + 1], f[i], f[i], lv[i] - m_w,
-                             lv[i] - m_w);
-                    const float p0 = fast_exp2(x0);
-                    const float p1 = fast_exp2(x1);
+                    fma2(x0, x1, s[2 * e], s[2 * e + 1], f, f, shift, shift);
+                    const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
                     add2(sum0, sum1, sum0, sum1, p0, p1);
                     pk[e] = pack_f16x2(p0, p1);
                     if (FMT != kBF16 && (e & 7) == 7) {  // the end of 16 keys
-                        over = fmaf(sum0 + sum1, inv[i], over);
-                        w_run = (i == 0 ? w_run * alpha : w_run) + (sum0 + sum1);
+                        sum += sum0 + sum1;
+                        over = fmaf(sum0 + sum1,
+                                    __shfl_sync(0xffffffffu, inv_lane, c0 / 16 + e / 8), over);
                         sum0 = sum1 = 0.f;
                     }
                 }
-                // P over its own S columns: 32 keys in 16 columns
+                if (FMT == kBF16) sum += sum0 + sum1;
                 tmem_st_32x32b_x16(s_tmem + c0 / 2, pk);
-                if (c0 == kBN / 2 - 32 || c0 == kBN - 32) {
-                    tmem_wait_st();
-                    tc_fence_before();
-                    mbar_arrive(&p_full[a * 2 + (c0 >= kBN / 2 ? 1 : 0)]);
-                }
+            };
+            // (P of 32 columns lies in front of the S that is still to be read)
+#pragma unroll 1
+            for (int c0 = 0; c0 < kBN; c0 += 64) {
+                tmem_wait_ld();
+                tmem_regs_after_wait(u0);
+                tmem_ld_32x32b_x32(s_tmem + c0 + 32, u1);
+                weigh(s0, c0);
+                tmem_wait_ld();
+                tmem_regs_after_wait(u1);
+                if (c0 + 64 < kBN) tmem_ld_32x32b_x32(s_tmem + c0 + 64, u0);
+                weigh(s1, c0 + 32);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&p_full[a * 2 + c0 / 64]);
             }
-            l_run = l_run * alpha + (FMT == kBF16 ? sum0 + sum1 : over);
+            l_run = l_run * alpha + (FMT == kBF16 ? sum : over);
+            w_run = w_run * alpha + sum;
         }
         if (m_run != -INFINITY && !(fabsf(m_run) < kScoreTop))
             report_error(p.err, ATTN_ERR_UNSUPPORTED);
@@ -979,7 +1076,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) mbar_wait(o_done, 0, p.err);
         __syncwarp();
         tc_fence_after();
-        if constexpr (FMT == kBF16) w_run = l_run;
         const bool any = !(w_run == 0.f);  // a key was seen (or a NaN met)
         const float norm = any ? 1.f / w_run : 0.f;
         const int part = dual ? 2 * w.split + a : w.split;
@@ -991,7 +1087,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // product has read them) as swizzled 128-byte rows of 64 dims, and out in whole
             // lines: a row a thread would write into 32 lines an instruction
             uint8_t *stage = a == 0 ? sK : sV;
-#pragma unroll
+#pragma unroll 1
             for (int c0 = 0; c0 < HD; c0 += 32) {
                 uint32_t orow[32];
                 if (mine > 0) {  // warpgroup-uniform: O was accumulated into
@@ -1033,12 +1129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();  // the lanes of the product's warp wait here for lane 0
     if (want + (int)gridDim.x >= total) break;
-    // another piece: registers as they were for the plan, and everything read
-    if (warp < 4)
-        setmaxnreg_inc<kRegsLaunch>();
-    else
-        setmaxnreg_dec<kRegsLaunch>();
-    tc_fence_before();
+    tc_fence_before();  // another piece: everything has been read
     __syncthreads();
     tc_fence_after();
     }
@@ -1055,6 +1146,7 @@ struct MergeParams {
     AttendParts own;  // of the keys behind the prefixes
     __nv_bfloat16 *out;
     int q_rows, rows, n_q_heads, n_kv_heads, group;
+    int first_row, n_rows;  // the launch's rows of a KV head, over the whole batch
 };
 
 // A row of the output from its parts: those of the shared keys, then those of its own.
@@ -1063,17 +1155,17 @@ struct MergeParams {
 template <int HD, int SPLIT>
 __global__ void __launch_bounds__(256) shared_merge_kernel(const MergeParams p) {
     constexpr int V = HD / 32, kRows = 8 / SPLIT;
-    __shared__ float sm_acc[8][HD];
+    __shared__ float sm_acc[SPLIT > 1 ? 8 : 1][HD];
     __shared__ float sm_m[8], sm_sum[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const AttendParts &a = p.own;
+    // rows (entry, row of its block, head of the group) of each KV head in turn
     const int64_t i = (int64_t)blockIdx.x * kRows + warp / SPLIT;
-    const int64_t head = i / a.rb;  // KV heads of all entries
-    const int row = (int)(i - head * a.rb);
-    const int entry = (int)(head / p.n_kv_heads), kvh = (int)(head - (int64_t)entry * p.n_kv_heads);
-    const int e = a.e0 + entry, b = e / a.row_blocks, q_row = (e - b * a.row_blocks) * a.rb + row;
-    const bool live = entry < a.n_entries && q_row < p.rows;
+    const int kvh = (int)(i / p.n_rows), q = (int)(i - (int64_t)kvh * p.n_rows) + p.first_row;
+    const int b = q / p.rows, q_row = q - b * p.rows, rb = q_row / a.rb, row = q_row - rb * a.rb;
+    const bool live = kvh < p.n_kv_heads;
     const int r = q_row / p.group, gh = q_row - r * p.group;
+    const int64_t head = (int64_t)(b * a.row_blocks + rb - a.e0) * p.n_kv_heads + kvh;
     pdl_wait();
     pdl_launch_dependents();
     if (SPLIT == 1 && !live) return;
@@ -1193,7 +1285,7 @@ int launch_prefix(const Params &p, const CUtensorMap &tq, const CUtensorMap &tk,
 
 template <int HD>
 cudaError_t launch_merge(const MergeParams &p, bool split, cudaStream_t stream) {
-    const int64_t rows = (int64_t)p.own.n_entries * p.n_kv_heads * p.own.rb;
+    const int64_t rows = (int64_t)p.n_rows * p.n_kv_heads;
     return split ? launch_pdl(shared_merge_kernel<HD, 4>, dim3((unsigned)((rows + 1) / 2)), dim3(256),
                               0, stream, p)
                  : launch_pdl(shared_merge_kernel<HD, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256),
@@ -1206,10 +1298,9 @@ int plan_shared(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
                 int head_dim, int max_seq_len, int window, SharedPlan *plan) {
     if (batch > shr::kMaxBatch) return ATTN_ERR_UNSUPPORTED;
     if (int rc = plan_attend(cache, batch, q_rows, n_q_heads, n_kv_heads, head_dim, max_seq_len,
-                             window, 0, &plan->own);
+                             window, 0, &plan->own, true);
         rc != ATTN_OK)
         return rc;
-    plan->own.merge = true;  // its parts are left to shared_merge_kernel
     // Parts of the shared keys: each row's first part or two, and those that units of at most
     // 256 rows are cut into beyond (at most one for every SM)
     const int64_t rows = (int64_t)batch * q_rows * n_q_heads;
@@ -1271,6 +1362,10 @@ int launch_shared(const SharedPlan &plan, const void *q, const attn_kv_cache *ca
     if (p.paged) {
         p.box_rows = std::min(cache->block_size & -cache->block_size, shr::kBN);
         if (p.box_rows < 8) p.box_rows = 0;
+        int l = 0;
+        while ((int64_t(1) << l) < cache->block_size) ++l;
+        p.page_shift = 31 + l;
+        p.page_mul = (uint32_t)((uint64_t(1) << p.page_shift) / cache->block_size + 1);
     }
 
     CUtensorMap tq, tk = {}, tv = {};
@@ -1321,13 +1416,22 @@ int launch_shared(const SharedPlan &plan, const void *q, const attn_kv_cache *ca
     m.n_q_heads = n_q_heads;
     m.n_kv_heads = n_kv_heads;
     m.group = p.group;
-    // A row of few KV heads lies in many parts
-    const bool split = p.sms > 8 * n_kv_heads;
+    // Four warps a row where rows lie in many parts (if all requests are one group) and are few
+    const int64_t pairs = ((int64_t)batch * q_rows + 2 * p.rt - 1) / (2 * p.rt);
+    const bool split = p.sms > 8 * n_kv_heads * pairs &&
+                       (int64_t)batch * q_rows * n_q_heads <= (int64_t)p.sms * 16;
     for (int e0 = 0; e0 < plan.own.entries; e0 += plan.own.per_launch) {
         rc = launch_attend_parts(plan.own, e0, prefix_lens, p.prefix_cap, q, cache, seq_lens,
                                  positions, q_rows, max_seq_len, window, n_q_heads, n_kv_heads,
                                  head_dim, scale, out, workspace, err, stream, &m.own);
         if (rc != ATTN_OK) return rc;
+        // rows of entries e0 .. e0 + n_entries - 1 (a request's last block may be short)
+        auto row_of = [&](int e) {
+            const int b = e / plan.own.row_blocks;
+            return b * m.rows + (e - b * plan.own.row_blocks) * m.own.rb;
+        };
+        m.first_row = row_of(e0);
+        m.n_rows = row_of(e0 + m.own.n_entries) - m.first_row;
         const cudaError_t e = head_dim == 128 ? shr::launch_merge<128>(m, split, stream)
                                               : shr::launch_merge<64>(m, split, stream);
         if (e != cudaSuccess) return ATTN_ERR_CUDA;
