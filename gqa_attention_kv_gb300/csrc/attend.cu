@@ -129,6 +129,13 @@ struct Params {
     // only keys t >= from[b] (clipped to 0 .. from_cap), every unit left as parts; or nullptr
     const int32_t *from;
     int from_cap;
+    // The launch before this one leaves nothing that this one reads: it is waited for last, so
+    // that whoever waits for this launch has waited for both
+    bool late_wait;
+    // launch_attend_parts: shares, `pieces` of them, are taken one after another by whichever
+    // CTA is free (`next` counts them), so CTAs that start late do no harm; else one each
+    int32_t *next;
+    int pieces;
     int32_t *err;
 };
 
@@ -438,8 +445,10 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
     S &sm = *reinterpret_cast<S *>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gq = lane >> 2, tq = lane & 3;
-    pdl_wait();
+    if (!p.late_wait) pdl_wait();
     pdl_launch_dependents();
+    int after = (int)blockIdx.x;  // thread 0: the share that comes next
+    if (p.next != nullptr && threadIdx.x == 0) after = atomicAdd(p.next, 1);
 
     // ---- the launch's work, the same in every CTA
     for (int i = threadIdx.x; i < p.n_entries; i += kThreads)
@@ -466,11 +475,9 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
     }
     __syncthreads();
     const int total = sm.prefix[p.n_entries];
-    int share = max(kMinChunks, (total + p.grid - 1) / p.grid);
+    int share = max(kMinChunks, (total + p.pieces - 1) / p.pieces);
     if (p.ws_count != nullptr)
         share = max(share, (sm.longest + kKernelParts - 2) / (kKernelParts - 1));
-    int g = min(total, (int)min((int64_t)blockIdx.x * share, (int64_t)total));
-    const int g_end = min(total, g + share);
 
     if (blockIdx.x == 0) {
         // rows of a unit without keys are zeros, and it has no parts
@@ -491,6 +498,17 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
         }
     }
 
+    for (;;) {
+    int piece = blockIdx.x;
+    if (p.next != nullptr) {
+        if (threadIdx.x == 0) sm.last_part = after;
+        __syncthreads();
+        piece = sm.last_part;
+        if ((int64_t)piece * share >= total) break;
+        if (threadIdx.x == 0) after = atomicAdd(p.next, 1);  // (under way meanwhile)
+    }
+    int g = min(total, (int)min((int64_t)piece * share, (int64_t)total));
+    const int g_end = min(total, g + share);
     while (g < g_end) {
         // ---- the next piece of a unit
         int lo_e = 0, hi_e = p.n_entries;
@@ -692,6 +710,22 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
         constexpr int kQRows = MT == 0 ? 1 : 2;
         int rpos[2];  // positions of the two rows this thread keeps scores of
         float q_bias[2] = {0.f, 0.f};  // -128 2^-24 sum(q) of the two rows
+        // q fragments and positions are asked for before the keys, or they would come behind them
+        constexpr int kMine = (HG * kSteps + kWarps - 1) / kWarps;
+        uint2 q_in[kMine][kQRows];
+#pragma unroll
+        for (int n = 0; n < kMine; ++n) {
+            const int i = warp + n * kWarps, qs = i / kSteps, kk = i % kSteps;  // head, k-step
+            const int j = kk / G::kStepsPerPiece, st = kk % G::kStepsPerPiece;
+            const int d0 = (16 / G::E) * (tq + 4 * j) + 4 * st;
+            if (i < HG * kSteps)
+#pragma unroll
+                for (int hr = 0; hr < kQRows; ++hr)
+                    q_in[n][hr] = *reinterpret_cast<const uint2 *>(qb + qs * p.group * HD +
+                                                                   row_of(gq + 8 * hr) + d0);
+        }
+        rpos[0] = MT == 0 ? pos_of(2 * tq) : pos_of(gq);
+        rpos[1] = MT == 0 ? pos_of(2 * tq + 1) : pos_of(gq + 8);
         // This warp's chunks; bf16 again where an infinity in V may have become a NaN (by the
         // lower half of its weight, which may be 0 or negative, or by a factor that is 0)
         for (bool again = false;; again = true) {
@@ -708,16 +742,14 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
                 copies_commit();
             }
             if (!again) {
-                // ---- q fragments and positions, while the first keys are under way
                 bool q_big = false;
-                for (int i = warp; i < HG * kSteps; i += kWarps) {
-                    const int qs = i / kSteps, kk = i % kSteps;  // head of the unit, k-step
-                    const int j = kk / G::kStepsPerPiece, st = kk % G::kStepsPerPiece;
-                    const int d0 = (16 / G::E) * (tq + 4 * j) + 4 * st;
+#pragma unroll
+                for (int n = 0; n < kMine; ++n) {
+                    const int i = warp + n * kWarps, qs = i / kSteps, kk = i % kSteps;
+                    if (i >= HG * kSteps) break;
 #pragma unroll
                     for (int hr = 0; hr < kQRows; ++hr) {
-                        uint2 x = *reinterpret_cast<const uint2 *>(qb + qs * p.group * HD +
-                                                                    row_of(gq + 8 * hr) + d0);
+                        uint2 x = q_in[n][hr];
                         if constexpr (FMT != kBF16) {  // f16 holds |q| < 65520
                             x.x = bf16x2_to_f16x2(x.x);
                             x.y = bf16x2_to_f16x2(x.y);
@@ -729,8 +761,6 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
                     }
                 }
                 if (q_big) report_error(p.err, ATTN_ERR_UNSUPPORTED);
-                rpos[0] = MT == 0 ? pos_of(2 * tq) : pos_of(gq);
-                rpos[1] = MT == 0 ? pos_of(2 * tq + 1) : pos_of(gq + 8);
                 __syncthreads();
 
                 if constexpr (FMT == kINT8) {
@@ -1140,7 +1170,7 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
         }
         __syncthreads();
         const bool whole = first == last && p.from == nullptr;
-        const int64_t slot = (int64_t)(unit + blockIdx.x) * HG;  // unique: shares are contiguous
+        const int64_t slot = (int64_t)(unit + piece) * HG;  // unique: shares are contiguous
         for (int i = threadIdx.x; i < HG * n_rows * (HD / 4); i += kThreads) {
             const int hr = i / (HD / 4), d = (i % (HD / 4)) * 4;
             const int h = HG == 1 ? 0 : hr / n_rows, row = hr - h * n_rows;
@@ -1184,6 +1214,9 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
         __syncthreads();  // the shared states are free again
         g += c_end - off;
     }
+    if (p.next == nullptr) break;
+    }
+    if (p.late_wait) pdl_wait();
 }
 
 // Adds the partial states of every unit that more than one CTA held, in part
@@ -1352,8 +1385,9 @@ int plan_attend(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
                             att::kMinChunks - 1) / att::kMinChunks;
     plan->grid = (int)std::max<int64_t>(
         1, std::min<int64_t>(needed, (int64_t)per_sm * device_sm_count()));
+    plan->pieces = parts ? 2 * plan->grid : plan->grid;
     const size_t units = (size_t)plan->per_launch * n_groups,
-                 slots = (units + plan->grid) * plan->heads;
+                 slots = (units + plan->pieces) * plan->heads;
     // How many CTAs a unit spans when all are as long as they can be: past
     // kKernelParts the merge kernel adds the parts up (else the kernel keeps to them)
     const int64_t share = std::max<int64_t>(
@@ -1416,7 +1450,7 @@ Params params_of(const AttendPlan &plan, const void *q, const attn_kv_cache *cac
     p.window = window;
     p.sinks = window > 0 ? sinks : 0;  // without a window every key is visible
     p.max_seq_len = max_seq_len;
-    p.grid = plan.grid;
+    p.grid = p.pieces = plan.grid;
     p.scale_log2 = scale * 1.4426950408889634f;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.ws_parts = reinterpret_cast<int2 *>(ws + plan.parts_offset);
@@ -1480,11 +1514,15 @@ int launch_attend_parts(const AttendPlan &plan, int e0, const int32_t *from, int
                         const void *q, const attn_kv_cache *cache, const int32_t *seq_lens,
                         const int32_t *positions, int q_rows, int max_seq_len, int window,
                         int n_q_heads, int n_kv_heads, int head_dim, float scale, void *out,
-                        void *workspace, int32_t *err, cudaStream_t stream, AttendParts *parts) {
+                        void *workspace, int32_t *err, cudaStream_t stream, bool late_wait,
+                        int32_t *next, AttendParts *parts) {
     att::Params p = att::params_of(plan, q, cache, seq_lens, positions, q_rows, max_seq_len, window,
                                    0, n_q_heads, n_kv_heads, scale, out, workspace, err);
     p.from = from;
     p.from_cap = from_cap;
+    p.late_wait = late_wait;
+    p.next = next;
+    p.pieces = plan.pieces;
     p.e0 = e0;
     p.n_entries = std::min(plan.per_launch, plan.entries - e0);
     parts->o = p.ws_o;

@@ -163,6 +163,7 @@ struct AttendPlan {
     int mt;     // 0: up to 8 rows per unit, 1: 16
     int heads;  // KV heads of a unit
     int row_blocks, entries, per_launch, grid, launches;
+    int pieces;  // shares that the work of a launch is cut into
     bool merge;  // the parts of a unit are added up by a second kernel
     size_t count_offset, parts_offset, lse_offset, o_offset, workspace;
 };
@@ -188,12 +189,15 @@ struct AttendParts {
 };
 
 // One launch of the plan, its entries from e0 on, over keys t >= from[b] (clipped to
-// 0 .. from_cap).
+// 0 .. from_cap).  late_wait: what the stream's launch before this one writes is not read by
+// this one (but by whoever merges the parts), and that launch waited for everything before it.
+// next: a counter that is 0 when the launch begins.
 int launch_attend_parts(const AttendPlan &plan, int e0, const int32_t *from, int from_cap,
                         const void *q, const attn_kv_cache *cache, const int32_t *seq_lens,
                         const int32_t *positions, int q_rows, int max_seq_len, int window,
                         int n_q_heads, int n_kv_heads, int head_dim, float scale, void *out,
-                        void *workspace, int32_t *err, cudaStream_t stream, AttendParts *parts);
+                        void *workspace, int32_t *err, cudaStream_t stream, bool late_wait,
+                        int32_t *next, AttendParts *parts);
 
 // Norms and rotary embedding of q and k (rope.cu); cache null: none is written to.
 int launch_qk_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
@@ -210,7 +214,7 @@ int launch_kv_read(const int64_t *slot_mapping, int64_t n, const attn_kv_cache *
 // Decode with shared prefixes (shared.cu).
 struct SharedPlan {
     AttendPlan own;  // of the keys that are not shared
-    size_t rows_offset, lse_offset, o_offset, workspace;
+    size_t rows_offset, lse_offset, next_offset, o_offset, workspace;
 };
 
 int plan_shared(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads, int n_kv_heads,

@@ -42,6 +42,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cstdlib>
 #include <type_traits>
 
 #include "kernels.h"
@@ -52,7 +53,6 @@ namespace shr {
 
 constexpr int kBM = 128;       // rows of a tile (two of them a CTA)
 constexpr int kBN = 128;       // keys of a tile
-constexpr int kThreads = 512;  // four warpgroups of 128 registers a thread
 constexpr int kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.0f;    // the reference maximum moves past this only
 constexpr float kWeightLog2 = 7.0f;     // weights are held times 2^7: at most 2^15
@@ -74,6 +74,8 @@ template <int FMT, int HD>
 struct Cfg {
     static constexpr bool kCodes = FMT != kBF16;
     static constexpr int kHalves = HD / 64;
+    static constexpr int kConv = kCodes ? 256 : 128;           // threads of the conversion
+    static constexpr int kThreads = 128 + kConv + 256;
     // bf16: the rings that TMA fills; 8-bit: f16 tiles converted from a ring of codes
     static constexpr int kKStages = kCodes ? (HD == 128 ? 1 : 2) : HD == 128 ? 2 : 4;
     static constexpr int kVStages = kCodes ? 2 : HD == 128 ? 3 : 5;
@@ -121,6 +123,8 @@ struct Params {
     int4 *ws_rows;   // [batch * q_rows]: first row of ws_o for KV head 0, rows a part, parts
     float2 *ws_lse;  // per row: log2 of the sum of weights, and of weights over scales
     uint16_t *ws_o;  // per row: HD f16
+    int32_t *ws_next;  // [launches]: attend.cu's counters of shares, set to 0 here
+    int launches;
     int32_t *err;
 };
 
@@ -161,6 +165,7 @@ __device__ __forceinline__ void request_range(const Params &p, int b, bool repor
 // Of U units (group, KV head, pair of tiles) that weigh their key tiles each is cut into
 // 1 + floor((SMs - U) tiles / sum) pieces, so that all are at most the SMs, or U.
 __device__ int make_plan(const Params &p, int32_t *mem, int want, bool tables, Piece &mine) {
+    const int kThreads = blockDim.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int B = p.batch, chunks = (B + 31) / 32;
     int32_t *r_lo = mem, *r_hi = r_lo + kMaxBatch, *g_start = r_hi + kMaxBatch;
@@ -381,10 +386,11 @@ __device__ __forceinline__ uint32_t drop_nan(uint32_t w) {
 }
 
 template <int FMT, int HD>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const Params p) {
     using C = Cfg<FMT, HD>;
+    constexpr int kThreads = C::kThreads, kConv = C::kConv;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -392,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     uint64_t *k_full = bars;                  // [kMaxK] loaded (bf16)
     uint64_t *k_empty = k_full + C::kMaxK;    // [kMaxK] multiplied
-    uint64_t *k_conv = k_empty + C::kMaxK;    // [kMaxK] ready, where warps 4 to 7 pass it on
+    uint64_t *k_conv = k_empty + C::kMaxK;    // [kMaxK] ready, where the conversion passes it on
     uint64_t *v_full = k_conv + C::kMaxK;     // [kVStages]
     uint64_t *v_empty = v_full + C::kVStages;
     uint64_t *v_conv = v_empty + C::kVStages;
@@ -424,6 +430,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     pdl_wait();  // everything below may come from the previous kernel
+    if (blockIdx.x == 0) {
+        for (int i = threadIdx.x; i < p.launches; i += kThreads) atomicExch(p.ws_next + i, 0);
+        __threadfence();
+        __syncthreads();
+    }
     pdl_launch_dependents();
 
     int total = INT32_MAX;
@@ -434,16 +445,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < C::kMaxK; ++s) {
             mbar_init(&k_full[s], loads);
             mbar_init(&k_empty[s], 1);
-            mbar_init(&k_conv[s], 128);  // every thread of warps 4 to 7
+            mbar_init(&k_conv[s], kConv);
         }
         for (int s = 0; s < C::kVStages; ++s) {
             mbar_init(&v_full[s], loads);
             mbar_init(&v_empty[s], 1);
-            mbar_init(&v_conv[s], 128);
+            mbar_init(&v_conv[s], kConv);
         }
         for (int s = 0; s < C::kMaxRaw; ++s) {
             mbar_init(&raw_full[s], loads);
-            mbar_init(&raw_empty[s], 128);
+            mbar_init(&raw_empty[s], kConv);
         }
         mbar_init(q_full, 1);
         mbar_init(q_conv, 256);
@@ -482,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto block_of = [&](int t) { return (int)(((uint64_t)t * p.page_mul) >> p.page_shift); };
     auto page_of = [&](int t) { return __ldg(table + block_of(t)); };
 
-    if (warp < 8) {
+    if (warp < 4 + kConv / 32) {
         if (warp == 0) {
             // ------------------------------------------------------------ loads
             if (lane == 0) {
@@ -702,7 +713,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp >= 4) {
             // ------------------------------------------------------------ into f16
-            constexpr int kConv = 128;          // threads
             const int ct = threadIdx.x - 128;
             // keys of a tile that lie in the group's range
             auto inside = [&](int tile, int row) {
@@ -757,12 +767,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             // 128 bytes, swizzled) meet in a bank.
             auto widen = [&](bool is_v, int tile, uint32_t from, uint32_t to) {
                 const bool all = !is_v || whole(tile);
-                constexpr int kRounds = HD / 64 * (kBN / 8) / 4;  // of 8 rows x 4 pieces a warp
-                constexpr int kBatch = 4;  // pieces read before one is written
+                constexpr int kW = kConv / 32, kRounds = HD / 64 * (kBN / 8) / kW;  // of 8 rows x 4 pieces a warp
+                constexpr int kBatch = kRounds < 4 ? kRounds : 4;  // pieces read before one is written
                 const int l = ct & 31, ph = l >> 3, second = (l >> 2) & 1, piece = l & 3;
-                auto half_of = [&](int i) { return (i * 4 + (ct >> 5)) % C::kHalves; };
-                auto row_of = [&](int i) {  // unit 4 i + warp: (8 rows, 64 dims)
-                    return (i * 4 + (ct >> 5)) / C::kHalves * 8 +
+                auto half_of = [&](int i) { return (i * kW + (ct >> 5)) % C::kHalves; };
+                auto row_of = [&](int i) {  // unit kW i + warp: (8 rows, 64 dims)
+                    return (i * kW + (ct >> 5)) / C::kHalves * 8 +
                            (HD == 128 ? (second ? ph ^ 5 : ph) : 2 * ph + second);
                 };
 #pragma unroll 1
@@ -841,10 +851,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ---------------------------------------------------------------- softmax
-        const int a = (warp - 8) >> 2;     // which tile, or stream
+        const int a = (warp - 4 - kConv / 32) >> 2;  // which tile, or stream
         const int quad = warp & 3;         // TMEM lane quadrant of this warp
         const int row = quad * 32 + lane;  // tile row = TMEM lane
-        const int st = threadIdx.x - 256;  // 0 .. 255
+        const int st = threadIdx.x - (kThreads - 256);  // 0 .. 255
         // a page that is not there is reported, and its keys are looked for in every tile
         if (p.paged) {
             const int b0 = max(w.lo, w.kt0 * kBN) / p.block_size;
@@ -1278,7 +1288,8 @@ int launch_prefix(const Params &p, const CUtensorMap &tq, const CUtensorMap &tk,
         }
         configured.fetch_or(bit, std::memory_order_relaxed);
     }
-    const cudaError_t e = launch_pdl(prefix_kernel<FMT, HD>, dim3((unsigned)p.sms), dim3(kThreads),
+    const cudaError_t e = launch_pdl(prefix_kernel<FMT, HD>, dim3((unsigned)p.sms),
+                                     dim3(Cfg<FMT, HD>::kThreads),
                                      Cfg<FMT, HD>::kSmem, stream, tq, tk, tv, p);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
@@ -1309,9 +1320,37 @@ int plan_shared(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     plan->rows_offset = up(plan->own.workspace);
     plan->lse_offset = up(plan->rows_offset + (size_t)batch * q_rows * sizeof(int4));
-    plan->o_offset = up(plan->lse_offset + (size_t)parts * sizeof(float2));
+    plan->next_offset = up(plan->lse_offset + (size_t)parts * sizeof(float2));
+    plan->o_offset = up(plan->next_offset + (size_t)plan->own.entries * sizeof(int32_t));
     plan->workspace = plan->o_offset + (size_t)parts * head_dim * 2;
     return ATTN_OK;
+}
+
+// The SMs that the shared part takes.  attend.cu's CTAs start at once on the others and follow on
+// each that is left, so that the two parts run side by side.  Of the pieces that a unit (KV head,
+// pair of tiles) can be cut into, as many as end soonest by the host's bounds (lengths are known on
+// the device only): a piece takes 9 us and 1.75 a pair of tiles and 128 keys (1.2 a single tile),
+// an SM reads 36 bytes of own keys a nanosecond.
+static int prefix_sms(int batch, int q_rows, int group, int n_kv_heads, int head_dim, int esize,
+                      int max_seq_len, int max_prefix_len) {
+    const int sms = device_sm_count(), rt = shr::kBM / group;
+    const int64_t pos = (int64_t)batch * q_rows;
+    const int64_t units = (pos + 2 * rt - 1) / (2 * rt) * n_kv_heads;
+    if (units > sms / 2) return sms;
+    const int64_t tiles = (max_prefix_len + 127) / 128;
+    const double tile = (pos <= rt ? 1.2 : 1.75) * head_dim / 128;
+    const double own = 0.5 * batch * (double)(max_seq_len - max_prefix_len) * n_kv_heads *
+                       head_dim * 2 * esize / 36e3;  // microseconds of an SM
+    int64_t best = 1;
+    double least = 1e30;
+    for (int64_t k = 1; k * units <= sms && k <= std::max<int64_t>(1, tiles); ++k) {
+        const double t = 9 + (double)((tiles + k - 1) / k) * tile;
+        // the own keys: on the other SMs until then, on all after
+        const double left = own - t * (double)(sms - k * units);
+        const double end = t + std::max(0.0, left / sms);
+        if (end < least) least = end, best = k;
+    }
+    return (int)(best * units);
 }
 
 int launch_shared(const SharedPlan &plan, const void *q, const attn_kv_cache *cache, int n_rows,
@@ -1328,7 +1367,8 @@ int launch_shared(const SharedPlan &plan, const void *q, const attn_kv_cache *ca
     p.n_kv_heads = n_kv_heads;
     p.group = n_q_heads / n_kv_heads;
     p.rt = shr::kBM / p.group;
-    p.sms = device_sm_count();
+    p.sms = getenv("SHR_MODE") && atoi(getenv("SHR_MODE")) == 1 ? device_sm_count() : getenv("SHR_X") ? atoi(getenv("SHR_X")) : prefix_sms(batch, q_rows, p.group, n_kv_heads, head_dim, esize, max_seq_len,
+                       std::min(max_prefix_len, max_seq_len));
     p.n_rows = n_rows;
     p.slots_per_seq = cache->slots_per_seq;
     p.block_size = cache->block_size;
@@ -1355,6 +1395,8 @@ int launch_shared(const SharedPlan &plan, const void *q, const attn_kv_cache *ca
     p.ws_rows = reinterpret_cast<int4 *>(ws + plan.rows_offset);
     p.ws_lse = reinterpret_cast<float2 *>(ws + plan.lse_offset);
     p.ws_o = reinterpret_cast<uint16_t *>(ws + plan.o_offset);
+    p.ws_next = reinterpret_cast<int32_t *>(ws + plan.next_offset);
+    p.launches = (plan.own.entries + plan.own.per_launch - 1) / plan.own.per_launch;
     p.err = err;
     // the largest power of two of keys that lie together wherever a tile begins; TMA boxes of
     // less than 8 would not begin on a swizzle's period
@@ -1423,7 +1465,8 @@ int launch_shared(const SharedPlan &plan, const void *q, const attn_kv_cache *ca
     for (int e0 = 0; e0 < plan.own.entries; e0 += plan.own.per_launch) {
         rc = launch_attend_parts(plan.own, e0, prefix_lens, p.prefix_cap, q, cache, seq_lens,
                                  positions, q_rows, max_seq_len, window, n_q_heads, n_kv_heads,
-                                 head_dim, scale, out, workspace, err, stream, &m.own);
+                                 head_dim, scale, out, workspace, err, stream, e0 == 0,
+                                 p.ws_next + e0 / plan.own.per_launch, &m.own);
         if (rc != ATTN_OK) return rc;
         // rows of entries e0 .. e0 + n_entries - 1 (a request's last block may be short)
         auto row_of = [&](int e) {
