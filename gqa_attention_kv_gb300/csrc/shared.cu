@@ -176,16 +176,23 @@ __device__ int make_plan(const Params &p, int32_t *mem, int want, bool tables, P
     for (int c = warp; c < chunks; c += kThreads / 32) {
         const int b = c * 32 + lane;
         bool first = false;
+        int before_plen = 0, before_row = 0, row = 0, plen = 0;
         if (b < B) {
-            int row, plen, lo, hi;
+            int lo, hi;
             request_range(p, b, blockIdx.x == 0 && tables, row, plen, lo, hi);
             r_lo[b] = lo, r_hi[b] = hi;
             g_lo[b] = INT32_MAX, g_hi[b] = 0;
-            first = b == 0;
-            if (!first) {
-                const int plen_b = max(0, min(p.prefix_lens[b - 1], p.prefix_cap));
-                first = plen != plen_b || (plen > 0 && row != p.prefix_rows[b - 1]);
+            before_plen = plen, before_row = row;
+        }
+        // the neighbour before: its length and row (-1 where it has no prefix)
+        before_plen = __shfl_up_sync(0xffffffffu, before_plen, 1);
+        before_row = __shfl_up_sync(0xffffffffu, before_row, 1);
+        if (b < B) {
+            if (lane == 0 && b > 0) {
+                before_plen = max(0, min(p.prefix_lens[b - 1], p.prefix_cap));
+                before_row = before_plen > 0 ? p.prefix_rows[b - 1] : -1;
             }
+            first = b == 0 || before_plen != plen || before_row != row;
         }
         const uint32_t mask = __ballot_sync(0xffffffffu, first);
         if (lane == 0) c_mask[c] = (int32_t)mask;
@@ -254,7 +261,9 @@ __device__ int make_plan(const Params &p, int32_t *mem, int want, bool tables, P
             if (tiles > 0) {
                 n_pos = (g_start[g + 1] - g_start[g]) * p.q_rows;
                 pairs = pairs_of(g);
-                cut = (int)min((int64_t)tiles, 1 + (int64_t)spare * tiles / work);
+                const uint32_t most = (uint32_t)spare * (uint32_t)tiles;  // (tiles <= 2^24)
+                cut = min(tiles, 1 + (work < (int64_t(1) << 32) ? (int)(most / (uint32_t)work)
+                                                                : (int)(most / work)));
                 n = pairs * p.n_kv_heads * cut;
                 two = n_pos <= p.rt;  // one tile: two parts a piece
                 rows = (two ? 2 : 1) * cut * p.n_kv_heads * n_pos * p.group;
@@ -278,9 +287,9 @@ __device__ int make_plan(const Params &p, int32_t *mem, int want, bool tables, P
                 m.prow = p.prefix_rows[g_start[g]];
                 m.lo = g_lo[g], m.hi = g_hi[g];
                 m.split = i - unit * cut;
-                const int64_t t = tiles;
-                m.kt0 = m.lo / kBN + (int)(m.split * t / cut);
-                m.n_kt = m.lo / kBN + (int)((m.split + 1) * t / cut) - m.kt0;
+                const int whole = tiles / cut, rest = tiles - whole * cut;
+                m.kt0 = m.lo / kBN + m.split * whole + min(m.split, rest);
+                m.n_kt = whole + (m.split < rest ? 1 : 0);
                 m.kvh = unit / pairs;
                 m.pair = unit - m.kvh * pairs;
                 m.parts = (two ? 2 : 1) * cut;
@@ -1213,37 +1222,58 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const MergeParams p) 
             sum = sum * old + fs;
             const int in_round = min(32, (n - x0 + SPLIT - 1) / SPLIT);
             const int shared = max(0, min(in_round, (n1 - x0 + SPLIT - 1) / SPLIT));
+            // the outputs of kBatch parts are asked for before one is used
+            constexpr int kBatch = 8;
             const uint16_t *src1 = p.ws_o + (row1 + (int64_t)x0 * at.y) * HD + lane * V;
-#pragma unroll 8
-            for (int k = 0; k < shared; ++k) {
-                const float w = __shfl_sync(0xffffffffu, fo, k);
-                const uint16_t *src = src1 + (int64_t)k * SPLIT * at.y * HD;
-                uint32_t raw[V / 2];
-                if constexpr (V == 4) {
-                    const uint2 t = __ldcg(reinterpret_cast<const uint2 *>(src));
-                    raw[0] = t.x, raw[1] = t.y;
-                } else {
-                    raw[0] = __ldcg(reinterpret_cast<const unsigned int *>(src));
+            for (int k0 = 0; k0 < shared; k0 += kBatch) {
+                uint2 raw[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const uint16_t *src = src1 + (int64_t)(k0 + i) * SPLIT * at.y * HD;
+                    raw[i] = make_uint2(0u, 0u);
+                    if (k0 + i < shared) {
+                        if constexpr (V == 4)
+                            raw[i] = __ldcg(reinterpret_cast<const uint2 *>(src));
+                        else
+                            raw[i].x = __ldcg(reinterpret_cast<const unsigned int *>(src));
+                    }
                 }
 #pragma unroll
-                for (int d = 0; d < V / 2; ++d) {
-                    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&raw[d]));
-                    acc[2 * d] += w * y.x;
-                    acc[2 * d + 1] += w * y.y;
+                for (int i = 0; i < kBatch; ++i) {
+                    const float w = __shfl_sync(0xffffffffu, fo, (k0 + i) & 31);
+                    if (k0 + i < shared)
+#pragma unroll
+                        for (int d = 0; d < V / 2; ++d) {
+                            const float2 y = __half22float2(
+                                *reinterpret_cast<const __half2 *>(d == 0 ? &raw[i].x : &raw[i].y));
+                            acc[2 * d] += w * y.x;
+                            acc[2 * d + 1] += w * y.y;
+                        }
                 }
             }
-#pragma unroll 4
-            for (int k = shared; k < in_round; ++k) {
-                // no weight is 0: 0 times an infinite output would be NaN
-                const float w = fmaxf(__shfl_sync(0xffffffffu, fo, k), kSmallest);
-                const float *src =
-                    a.o + (row2 + (int64_t)(x0 + k * SPLIT - n1) * step2) * HD + lane * V;
-                if constexpr (V == 4) {
-                    const float4 y = __ldcg(reinterpret_cast<const float4 *>(src));
-                    acc[0] += w * y.x, acc[1] += w * y.y, acc[2] += w * y.z, acc[3] += w * y.w;
-                } else {
-                    const float2 y = __ldcg(reinterpret_cast<const float2 *>(src));
-                    acc[0] += w * y.x, acc[1] += w * y.y;
+            for (int k0 = shared; k0 < in_round; k0 += kBatch / 2) {
+                float4 raw[kBatch / 2];
+#pragma unroll
+                for (int i = 0; i < kBatch / 2; ++i) {
+                    const float *src =
+                        a.o + (row2 + (int64_t)(x0 + (k0 + i) * SPLIT - n1) * step2) * HD + lane * V;
+                    if (k0 + i < in_round) {
+                        if constexpr (V == 4) {
+                            raw[i] = __ldcg(reinterpret_cast<const float4 *>(src));
+                        } else {
+                            const float2 y = __ldcg(reinterpret_cast<const float2 *>(src));
+                            raw[i].x = y.x, raw[i].y = y.y;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch / 2; ++i) {
+                    // no weight is 0: 0 times an infinite output would be NaN
+                    const float w = fmaxf(__shfl_sync(0xffffffffu, fo, (k0 + i) & 31), kSmallest);
+                    if (k0 + i < in_round) {
+                        acc[0] += w * raw[i].x, acc[1] += w * raw[i].y;
+                        if constexpr (V == 4) acc[2] += w * raw[i].z, acc[3] += w * raw[i].w;
+                    }
                 }
             }
         }
