@@ -74,8 +74,9 @@ template <int FMT, int HD>
 struct Cfg {
     static constexpr bool kCodes = FMT != kBF16;
     static constexpr int kHalves = HD / 64;
-    static constexpr int kConv = kCodes ? 256 : 128;           // threads of the conversion
-    static constexpr int kThreads = 128 + kConv + 256;
+    // threads that convert a tensor's tiles: K's and V's codes have warps of their own
+    static constexpr int kConv = 128;
+    static constexpr int kThreads = 128 + (kCodes ? 2 : 1) * kConv + 256;
     // bf16: the rings that TMA fills; 8-bit: f16 tiles converted from a ring of codes
     static constexpr int kKStages = kCodes ? (HD == 128 ? 1 : 2) : HD == 128 ? 2 : 4;
     static constexpr int kVStages = kCodes ? 2 : HD == 128 ? 3 : 5;
@@ -502,7 +503,7 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
     auto block_of = [&](int t) { return (int)(((uint64_t)t * p.page_mul) >> p.page_shift); };
     auto page_of = [&](int t) { return __ldg(table + block_of(t)); };
 
-    if (warp < 4 + kConv / 32) {
+    if (warp < kThreads / 32 - 8) {
         if (warp == 0) {
             // ------------------------------------------------------------ loads
             if (lane == 0) {
@@ -722,7 +723,7 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
             }
         } else if (warp >= 4) {
             // ------------------------------------------------------------ into f16
-            const int ct = threadIdx.x - 128;
+            const int ct = threadIdx.x & (kConv - 1);
             // keys of a tile that lie in the group's range
             auto inside = [&](int tile, int row) {
                 const int t = tile * kBN + row;
@@ -822,45 +823,52 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
             };
             Turn kt, vt, rt;
             bool ok = true;
-            for (int i = 0; i < 2 * w.n_kt; ++i) {
-                const bool is_v = i & 1;
-                const int j = i >> 1;
-                if (FMT == kBF16 && !is_v && !gather) continue;
-                const int st = is_v ? vt.st : kt.st;
-                const uint32_t ph = is_v ? vt.ph : kt.ph;
-                const uint32_t at = smem_u32((is_v ? sV : sK) + st * C::kTileBytes);
-                if constexpr (FMT == kBF16) {
-                    ok = mbar_wait(is_v ? &v_full[st] : &k_full[st], ph, p.err);
+            if constexpr (C::kCodes) {
+                const bool is_v = warp >= 8;
+                const int stages = is_v ? C::kVStages : k_stages;
+                uint64_t *empty = is_v ? v_empty : k_empty, *done = is_v ? v_conv : k_conv;
+                const uint32_t to = smem_u32(is_v ? sV : sK);
+                if (is_v) rt.next(raw_stages);  // (the ring holds K and V in turn)
+                for (int j = 0; j < w.n_kt; ++j) {
+                    ok = mbar_wait(&raw_full[rt.st], rt.ph, p.err) &&
+                         mbar_wait(&empty[vt.st], vt.ph ^ 1, p.err);
                     if (!ok) break;
-                    if (is_v) {
-                        v_in_place(w.kt0 + j, at);
-                    } else {
-                        // copied by cp.async: written again, so that this thread's fence
+                    widen(is_v, w.kt0 + j, smem_u32(sRaw + rt.st * C::kRawBytes),
+                          to + vt.st * C::kTileBytes);
+                    fence_proxy_async_smem();
+                    mbar_arrive(&done[vt.st]);
+                    mbar_arrive(&raw_empty[rt.st]);
+                    vt.next(stages);
+                    rt.next(raw_stages);
+                    rt.next(raw_stages);
+                }
+            } else {
+                for (int j = 0; j < w.n_kt; ++j) {
+                    if (gather) {
+                        // K copied by cp.async: written again, so that this thread's fence
                         // covers what the tensor cores read
+                        const uint32_t at = smem_u32(sK + kt.st * C::kTileBytes);
+                        ok = mbar_wait(&k_full[kt.st], kt.ph, p.err);
+                        if (!ok) break;
 #pragma unroll 4
                         for (int i = ct; i < C::kTileBytes / 16; i += kConv)
                             st_shared_v4(at + i * 16, ld_shared_v4(at + i * 16));
+                        fence_proxy_async_smem();
+                        mbar_arrive(&k_conv[kt.st]);
+                        kt.next(k_stages);
                     }
-                } else {
-                    ok = mbar_wait(&raw_full[rt.st], rt.ph, p.err) &&
-                         mbar_wait(is_v ? &v_empty[st] : &k_empty[st], ph ^ 1, p.err);
+                    ok = mbar_wait(&v_full[vt.st], vt.ph, p.err);
                     if (!ok) break;
-                    widen(is_v, w.kt0 + j, smem_u32(sRaw + rt.st * C::kRawBytes), at);
+                    v_in_place(w.kt0 + j, smem_u32(sV + vt.st * C::kTileBytes));
                     fence_proxy_async_smem();
-                    mbar_arrive(&raw_empty[rt.st]);
-                    rt.next(raw_stages);
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(is_v ? &v_conv[st] : &k_conv[st]);
-                if (is_v)
+                    mbar_arrive(&v_conv[vt.st]);
                     vt.next(C::kVStages);
-                else
-                    kt.next(k_stages);
+                }
             }
         }
     } else {
         // ---------------------------------------------------------------- softmax
-        const int a = (warp - 4 - kConv / 32) >> 2;  // which tile, or stream
+        const int a = (warp >> 2) & 1 ^ (C::kCodes ? 1 : 0);  // which tile, or stream
         const int quad = warp & 3;         // TMEM lane quadrant of this warp
         const int row = quad * 32 + lane;  // tile row = TMEM lane
         const int st = threadIdx.x - (kThreads - 256);  // 0 .. 255
