@@ -1339,8 +1339,8 @@ int launch(const Params &p, bool merge, cudaStream_t stream) {
 }  // namespace att
 
 // KV heads of a unit of launch_attend_parts
-static int part_heads(const attn_kv_cache *cache, int mt, int n_kv_heads) {
-    const int most = cache->dtype == ATTN_KV_BF16 && mt == 0 ? 4 : 2;
+static int part_heads(const attn_kv_cache *cache, int mt, int n_kv_heads, int head_dim) {
+    const int most = (cache->dtype == ATTN_KV_BF16 || head_dim == 64) && mt == 0 ? 4 : 2;
     return n_kv_heads % most == 0 ? most : n_kv_heads % 2 == 0 ? 2 : 1;
 }
 
@@ -1367,7 +1367,7 @@ int plan_attend(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
     if (cache->layout == ATTN_LAYOUT_BSHD && head_dim == 64 && n_kv_heads % 2 == 0 &&
         (cache->dtype != ATTN_KV_BF16 || plan->mt == 0))
         plan->heads = 2;
-    if (parts) plan->heads = part_heads(cache, plan->mt, n_kv_heads);
+    if (parts) plan->heads = part_heads(cache, plan->mt, n_kv_heads, head_dim);
     const int n_groups = n_kv_heads / plan->heads;
     const int64_t per_entry = (chunks + att::kGapChunks) * n_groups;
     // rows of one head and prefixes of chunks are counted in 32 bits
@@ -1489,7 +1489,7 @@ int run(const Params &p, const AttendPlan &plan, const attn_kv_cache *cache, int
 // ... of launch_attend_parts
 template <int FMT, int HD, int MT>
 int run_parts(const Params &p, int heads, cudaStream_t stream) {
-    if constexpr (FMT == kBF16 && MT == 0)
+    if constexpr ((FMT == kBF16 || HD == 64) && MT == 0)
         if (heads == 4) return launch<FMT, HD, MT, 4, kPartEntries>(p, false, stream);
     return heads == 2 ? launch<FMT, HD, MT, 2, kPartEntries>(p, false, stream)
                       : launch<FMT, HD, MT, 1, kPartEntries>(p, false, stream);

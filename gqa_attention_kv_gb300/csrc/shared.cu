@@ -42,7 +42,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <cstdlib>
 #include <type_traits>
 
 #include "kernels.h"
@@ -163,8 +162,8 @@ __device__ __forceinline__ void request_range(const Params &p, int b, bool repor
 
 // The plan: groups, their pieces, and the piece that is asked for (n_kt 0: none).  `mem` is
 // scratch in shared memory; every thread of the CTA calls this and passes its last barrier.
-// Of U units (group, KV head, pair of tiles) that weigh their key tiles each is cut into
-// 1 + floor((SMs - U) tiles / sum) pieces, so that all are at most the SMs, or U.
+// Of U units (group, KV head, pair of tiles) that weigh their key tiles each is cut into so many
+// pieces (else 1 + floor((SMs - U) tiles / sum)) that all are at most the SMs, or U.
 __device__ int make_plan(const Params &p, int32_t *mem, int want, bool tables, Piece &mine) {
     const int kThreads = blockDim.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -252,7 +251,23 @@ __device__ int make_plan(const Params &p, int32_t *mem, int want, bool tables, P
             units += __shfl_xor_sync(0xffffffffu, units, o);
             work += __shfl_xor_sync(0xffffffffu, work, o);
         }
+        // Of U units, each cut into pieces of at most s key tiles: the least s whose pieces are no
+        // more than the SMs lies between work / SMs and work / (SMs - U); 32 of those are tried
         const int spare = max(0, p.sms - units);
+        int most = 0;  // s, or 0: units are cut in proportion
+        if (groups <= 32 && spare > 0 && work < (int64_t(1) << 31) && work > 0) {
+            const int t = lane < groups ? tiles_of(lane) : 0;
+            const int u = t > 0 ? pairs_of(lane) * p.n_kv_heads : 0;
+            const int s0 = ((int)work + p.sms - 1) / p.sms, s1 = ((int)work + spare - 1) / spare;
+            const int s = s0 + (int)(((int64_t)(s1 - s0) * lane + 30) / 31);
+            int n = 0;
+            for (int g = 0; g < groups; ++g) {
+                const int tg = __shfl_sync(0xffffffffu, t, g), ug = __shfl_sync(0xffffffffu, u, g);
+                n += ug * ((tg + s - 1) / s);
+            }
+            const uint32_t fits = __ballot_sync(0xffffffffu, n <= p.sms);
+            most = fits != 0 ? __shfl_sync(0xffffffffu, s, __ffs(fits) - 1) : 0;
+        }
         int at = 0, row = 0;  // pieces and rows of ws_o before this round's groups
         for (int g0 = 0; g0 < groups; g0 += 32) {
             const int g = g0 + lane;
@@ -262,9 +277,8 @@ __device__ int make_plan(const Params &p, int32_t *mem, int want, bool tables, P
             if (tiles > 0) {
                 n_pos = (g_start[g + 1] - g_start[g]) * p.q_rows;
                 pairs = pairs_of(g);
-                const uint32_t most = (uint32_t)spare * (uint32_t)tiles;  // (tiles <= 2^24)
-                cut = min(tiles, 1 + (work < (int64_t(1) << 32) ? (int)(most / (uint32_t)work)
-                                                                : (int)(most / work)));
+                cut = most > 0 ? (tiles + most - 1) / most
+                               : min(tiles, 1 + (int)((int64_t)spare * tiles / work));
                 n = pairs * p.n_kv_heads * cut;
                 two = n_pos <= p.rt;  // one tile: two parts a piece
                 rows = (two ? 2 : 1) * cut * p.n_kv_heads * n_pos * p.group;
@@ -1180,7 +1194,7 @@ struct MergeParams {
 // SPLIT warps a row, each every SPLIT-th part, a lane HD / 32 dims; the sums of 32 parts come in one
 // load, the parts' outputs then wait for nothing.
 template <int HD, int SPLIT>
-__global__ void __launch_bounds__(256) shared_merge_kernel(const MergeParams p) {
+__global__ void __launch_bounds__(256, SPLIT == 1 ? 4 : 2) shared_merge_kernel(const MergeParams p) {
     constexpr int V = HD / 32, kRows = 8 / SPLIT;
     __shared__ float sm_acc[SPLIT > 1 ? 8 : 1][HD];
     __shared__ float sm_m[8], sm_sum[8];
@@ -1231,7 +1245,7 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const MergeParams p) 
             const int in_round = min(32, (n - x0 + SPLIT - 1) / SPLIT);
             const int shared = max(0, min(in_round, (n1 - x0 + SPLIT - 1) / SPLIT));
             // the outputs of kBatch parts are asked for before one is used
-            constexpr int kBatch = 8;
+            constexpr int kBatch = SPLIT == 1 ? 4 : 8;
             const uint16_t *src1 = p.ws_o + (row1 + (int64_t)x0 * at.y) * HD + lane * V;
             for (int k0 = 0; k0 < shared; k0 += kBatch) {
                 uint2 raw[kBatch];
@@ -1367,27 +1381,39 @@ int plan_shared(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
 // The SMs that the shared part takes.  attend.cu's CTAs start at once on the others and follow on
 // each that is left, so that the two parts run side by side.  Of the pieces that a unit (KV head,
 // pair of tiles) can be cut into, as many as end soonest by the host's bounds (lengths are known on
-// the device only): a piece takes 9 us and 1.75 a pair of tiles and 128 keys (1.2 a single tile),
-// an SM reads 36 bytes of own keys a nanosecond.
+// the device only): a piece takes 9 us and 1.65 a pair of tiles and 128 keys (1.2 a single tile; over
+// codes 2.4 and 1.6), an SM reads 36 bytes (28) of own keys a nanosecond.
 static int prefix_sms(int batch, int q_rows, int group, int n_kv_heads, int head_dim, int esize,
-                      int max_seq_len, int max_prefix_len) {
+                      int max_seq_len, int max_prefix_len, int own_units) {
     const int sms = device_sm_count(), rt = shr::kBM / group;
     const int64_t pos = (int64_t)batch * q_rows;
     const int64_t units = (pos + 2 * rt - 1) / (2 * rt) * n_kv_heads;
     if (units > sms / 2) return sms;
     const int64_t tiles = (max_prefix_len + 127) / 128;
-    const double tile = (pos <= rt ? 1.2 : 1.75) * head_dim / 128;
+    const double tile = esize == 2 ? (pos <= rt ? 1.2 : 1.65) : (pos <= rt ? 1.6 : 2.4);
+    // microseconds of an SM: its rate, and a round trip or three for every change of unit
     const double own = 0.5 * batch * (double)(max_seq_len - max_prefix_len) * n_kv_heads *
-                       head_dim * 2 * esize / 36e3;  // microseconds of an SM
-    int64_t best = 1;
-    double least = 1e30;
-    for (int64_t k = 1; k * units <= sms && k <= std::max<int64_t>(1, tiles); ++k) {
+                           head_dim * 2 * esize / (esize == 2 ? 36e3 : 28e3) +
+                       (double)own_units * (esize == 2 ? 2.5 : 3.0);
+    auto end_of = [&](int64_t k) {
         const double t = 9 + (double)((tiles + k - 1) / k) * tile;
         // the own keys: on the other SMs until then, on all after
         const double left = own - t * (double)(sms - k * units);
-        const double end = t + std::max(0.0, left / sms);
-        if (end < least) least = end, best = k;
-    }
+        return t + (left > 0 ? 4 + left / sms : 0);
+    };
+    // ... of those about as good the most: late own keys cost less than a late shared part, which
+    // is what a batch of several groups would have
+    int64_t best = 1;
+    double least = 1e30;
+    for (int pass = 0; pass < 2; ++pass)
+        for (int64_t k = 1; k * units <= sms && k <= std::max<int64_t>(1, tiles); ++k) {
+            if (k > 1 && (tiles + k - 1) / k == (tiles + k - 2) / (k - 1)) continue;
+            const double end = end_of(k);
+            if (pass == 0)
+                least = std::min(least, end);
+            else if (end <= 1.03 * least)
+                best = k;
+        }
     return (int)(best * units);
 }
 
@@ -1405,8 +1431,9 @@ int launch_shared(const SharedPlan &plan, const void *q, const attn_kv_cache *ca
     p.n_kv_heads = n_kv_heads;
     p.group = n_q_heads / n_kv_heads;
     p.rt = shr::kBM / p.group;
-    p.sms = getenv("SHR_MODE") && atoi(getenv("SHR_MODE")) == 1 ? device_sm_count() : getenv("SHR_X") ? atoi(getenv("SHR_X")) : prefix_sms(batch, q_rows, p.group, n_kv_heads, head_dim, esize, max_seq_len,
-                       std::min(max_prefix_len, max_seq_len));
+    p.sms = prefix_sms(batch, q_rows, p.group, n_kv_heads, head_dim, esize, max_seq_len,
+                       std::min(max_prefix_len, max_seq_len),
+                       plan.own.entries * (n_kv_heads / plan.own.heads));
     p.n_rows = n_rows;
     p.slots_per_seq = cache->slots_per_seq;
     p.block_size = cache->block_size;
