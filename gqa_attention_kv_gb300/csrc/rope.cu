@@ -39,6 +39,7 @@ namespace rope {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnroll = 4;  // passes (of two or four rows) whose loads are in flight
+constexpr int kBlocks = 6;  // of an SM
 
 // Where the halves of a pair stand
 enum Mode {
@@ -89,10 +90,16 @@ __device__ __forceinline__ uint64_t turn_fraction(float inv_freq) {
 }
 
 template <int HD, int MODE, bool NORM>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const Params p) {
     constexpr int kLanes = HD / 8;         // lanes of a row
     constexpr int kRows = 32 / kLanes;     // rows of a pass
-    __shared__ float2 turns[kWarps][HD / 2];  // cosine and sine of each frequency
+    __shared__ __align__(16) float2 turns[kWarps][HD / 2];  // cosine and sine of each frequency
+    __shared__ __align__(16) float weights[NORM ? 2 : 1][NORM ? HD : 4];
+    // Of queries and keys, for each dim what it and the other one of its pair are multiplied with
+    // (turn and weight); dims d0 + 2 i and + 1 of all lanes stand together, or the lanes would
+    // meet in four banks
+    constexpr int kTypes = NORM ? 2 : 1;
+    __shared__ float4 factors[kWarps][kTypes][4][kLanes];
     __shared__ float parked[MODE == kHalvesAny ? kWarps : 1][MODE == kHalvesAny ? kRows * HD : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = lane / kLanes, piece = lane % kLanes, d0 = piece * 8;
@@ -101,21 +108,19 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
     pdl_wait();
     pdl_launch_dependents();
 
-    uint64_t step[2] = {0, 0};  // of frequencies lane and lane + 32
+    uint64_t step[HD / 64];  // of frequencies lane and lane + 32
 #pragma unroll
     for (int i = 0; i < HD / 64; ++i)
-        if (lane + 32 * i < half) step[i] = turn_fraction(__ldg(p.inv_freq + lane + 32 * i));
-    float qw[8], kw[8];
+        step[i] = lane + 32 * i < half ? turn_fraction(__ldg(p.inv_freq + lane + 32 * i)) : 0;
     if constexpr (NORM) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            qw[i] = p.q_weight != nullptr ? __ldg(p.q_weight + d0 + i) : 1.f;
-            kw[i] = p.k_weight != nullptr ? __ldg(p.k_weight + d0 + i) : 1.f;
+        for (int i = threadIdx.x; i < HD; i += kThreads) {
+            weights[0][i] = p.q_weight != nullptr ? __ldg(p.q_weight + i) : 1.f;
+            weights[1][i] = p.k_weight != nullptr ? __ldg(p.k_weight + i) : 1.f;
         }
+        __syncthreads();
     }
     // the lane that holds the other halves of this lane's pairs (kHalves)
-    const bool turned = d0 < p.rot;
-    const int other = MODE != kHalves || !turned
+    const int other = MODE != kHalves || d0 >= p.rot
                           ? lane
                           : sub * kLanes + (d0 < half ? piece + half / 8 : piece - half / 8);
 
@@ -129,18 +134,21 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
         const int64_t slot = p.slots != nullptr ? __ldg(p.slots + t) : 0;
         const bool stored = p.slots != nullptr && slot >= 0 && slot < p.num_slots;
 
-        auto load = [&](int h, uint4 &w) {
-            if (h >= end) return;
-            const __nv_bfloat16 *src =
-                h < p.n_q_heads                  ? p.q + t * p.q_stride + h * HD
-                : h < p.n_q_heads + p.n_kv_heads ? p.k + t * p.k_stride + (h - p.n_q_heads) * HD
-                                                 : p.v + t * p.v_stride +
-                                                       (h - p.n_q_heads - p.n_kv_heads) * HD;
-            w = __ldcs(reinterpret_cast<const uint4 *>(src + d0));
-        };
-        uint4 next[kUnroll];
+        uint4 now[kUnroll];
+        auto load = [&](int h0) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) load(first + u * kRows + sub, next[u]);
+            for (int u = 0; u < kUnroll; ++u) {
+                const int h = h0 + u * kRows + sub;
+                const __nv_bfloat16 *src =
+                    h < p.n_q_heads                  ? p.q + t * p.q_stride + h * HD
+                    : h < p.n_q_heads + p.n_kv_heads ? p.k + t * p.k_stride + (h - p.n_q_heads) * HD
+                                                     : p.v + t * p.v_stride +
+                                                           (h - p.n_q_heads - p.n_kv_heads) * HD;
+                now[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (h < end) now[u] = __ldcs(reinterpret_cast<const uint4 *>(src + d0));
+            }
+        };
+        load(first);  // (under way while the angles are computed)
 
         if (p.slots != nullptr && !stored && lane == 0 && first == 0)
             report_error(p.err, ATTN_ERR_BOUNDS);
@@ -154,35 +162,71 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
                 turns[warp][lane + 32 * i] = make_float2(c * p.factor, s * p.factor);
             }
         __syncwarp();
-        // kPairs: of pairs d0 / 2 + i, i < 4; else of dims d0 + i, the sine with the sign
-        // that the other half of the pair gets
-        constexpr int kTurns = MODE == kPairs ? 4 : 8;
-        float c[kTurns], s[kTurns];
 #pragma unroll
-        for (int i = 0; i < kTurns; ++i) {
-            const int d = d0 + (MODE == kPairs ? 2 * i : i);
-            c[i] = 1.f, s[i] = 0.f;
-            if (d < p.rot) {
-                const float2 x =
-                    turns[warp][MODE == kPairs ? d / 2 : d < half ? d : d - half];
-                c[i] = x.x;
-                s[i] = MODE != kPairs && d < half ? -x.y : x.y;
+        for (int i = 0; i < HD / 32; ++i) {
+            const int d = lane + 32 * i;
+            const bool low = MODE == kPairs ? !(d & 1) : d < half;
+            const int pair = d >= p.rot ? d : MODE == kPairs ? d ^ 1 : low ? d + half : d - half;
+            float2 turn = make_float2(1.f, 0.f);
+            if (d < p.rot) turn = turns[warp][MODE == kPairs ? d / 2 : low ? d : d - half];
+            if (low) turn.y = -turn.y;
+#pragma unroll
+            for (int t2 = 0; t2 < kTypes; ++t2) {
+                float2 &f =
+                    reinterpret_cast<float2 *>(&factors[warp][t2][(d & 7) >> 1][d >> 3])[d & 1];
+                f = NORM ? make_float2(turn.x * weights[t2][d], turn.y * weights[t2][pair]) : turn;
             }
         }
+        __syncwarp();
+        float4 held[4];  // without norms one set serves all rows
+        if constexpr (!NORM)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) held[i] = factors[warp][0][i][piece];
 
         for (int h0 = first; h0 < end; h0 += kUnroll * kRows) {
-            uint4 now[kUnroll];
+            if (h0 != first) load(h0);
+            float r[kUnroll];  // 1 / sqrt(mean square)
+            if constexpr (NORM) {
+                auto square_sums = [&](float by, float(&sum)[kUnroll]) {
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                now[u] = next[u];
-                load(h0 + (kUnroll + u) * kRows + sub, next[u]);
+                    for (int u = 0; u < kUnroll; ++u) {
+                        const uint32_t raw[4] = {now[u].x, now[u].y, now[u].z, now[u].w};
+                        sum[u] = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float a = __uint_as_float(raw[i] << 16) * by;
+                            const float b = __uint_as_float(raw[i] & 0xFFFF0000u) * by;
+                            sum[u] = fmaf(a, a, fmaf(b, b, sum[u]));
+                        }
+                    }
+#pragma unroll
+                    for (int o = 1; o < kLanes; o <<= 1)
+#pragma unroll
+                        for (int u = 0; u < kUnroll; ++u)
+                            sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], o);
+                };
+                float sum[kUnroll];
+                square_sums(1.f, sum);
+                bool over = false;
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    r[u] = rsqrtf(sum[u] * (1.f / HD) + p.eps);
+                    over |= isinf(sum[u]);
+                }
+                // squares past float32: those of x 2^-64, beside which eps is nothing
+                if (__any_sync(0xffffffffu, over)) {
+                    float small[kUnroll];
+                    square_sums(0x1p-64f, small);
+#pragma unroll
+                    for (int u = 0; u < kUnroll; ++u)
+                        if (isinf(sum[u])) r[u] = 0x1p-64f * rsqrtf(small[u] * (1.f / HD));
+                }
             }
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 if (h0 + u * kRows >= end) break;
                 const int h = h0 + u * kRows + sub;
                 const bool is_q = h < p.n_q_heads, is_v = h >= p.n_q_heads + p.n_kv_heads;
-                if (h >= end) now[u] = make_uint4(0u, 0u, 0u, 0u);
                 const uint32_t raw[4] = {now[u].x, now[u].y, now[u].z, now[u].w};
                 float x[8];
 #pragma unroll
@@ -190,49 +234,17 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
                     x[2 * i] = __uint_as_float(raw[i] << 16);
                     x[2 * i + 1] = __uint_as_float(raw[i] & 0xFFFF0000u);
                 }
-                if constexpr (NORM) {
-                    auto square_sum = [&](float by) {
-                        float sum = 0.f;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) sum = fmaf(x[i] * by, x[i] * by, sum);
-#pragma unroll
-                        for (int o = 1; o < kLanes; o <<= 1)
-                            sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                        return sum;
-                    };
-                    float sum = square_sum(1.f), r = rsqrtf(sum * (1.f / HD) + p.eps);
-                    // squares past float32: those of x 2^-64, beside which eps is nothing
-                    if (__any_sync(0xffffffffu, isinf(sum))) {
-                        const float small = square_sum(0x1p-64f);
-                        if (isinf(sum)) r = 0x1p-64f * rsqrtf(small * (1.f / HD));
-                    }
-                    if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = x[i] * r * (is_q ? qw[i] : kw[i]);
-                }
-                float y[8];
+                float z[8];  // the others of the pairs
                 if constexpr (MODE == kPairs) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool on = d0 + 2 * i < p.rot;
-                        y[2 * i] = on ? fmaf(x[2 * i], c[i], -(x[2 * i + 1] * s[i])) : x[2 * i];
-                        y[2 * i + 1] = on ? fmaf(x[2 * i + 1], c[i], x[2 * i] * s[i]) : x[2 * i + 1];
-                    }
+                    for (int i = 0; i < 8; ++i) z[i] = x[i ^ 1];
                 } else if constexpr (MODE == kHalves) {
-                    float z[8];  // the other halves
-                    if constexpr (NORM) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) z[i] = __shfl_sync(0xffffffffu, x[i], other);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t w = __shfl_sync(0xffffffffu, raw[i], other);
-                            z[2 * i] = __uint_as_float(w << 16);
-                            z[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t w = __shfl_sync(0xffffffffu, raw[i], other);
+                        z[2 * i] = __uint_as_float(w << 16);
+                        z[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
                     }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = turned ? fmaf(x[i], c[i], z[i] * s[i]) : x[i];
                 } else {
                     float *row = parked[warp] + sub * HD;
                     __syncwarp();
@@ -242,10 +254,25 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int d = d0 + i;
-                        y[i] = x[i];
-                        if (d < p.rot)
-                            y[i] = fmaf(x[i], c[i], row[d < half ? d + half : d - half] * s[i]);
+                        z[i] = d < p.rot ? row[d < half ? d + half : d - half] : 0.f;
                     }
+                }
+                float y[8];
+                const float by =
+                    NORM && (is_q ? p.q_weight : p.k_weight) != nullptr ? r[u] : 1.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 g = NORM ? factors[warp][is_q ? 0 : kTypes - 1][i][piece] : held[i];
+                    const int d = d0 + 2 * i;
+                    // whole pieces turn or stay, but for odd numbers of dims
+                    const bool on0 = MODE == kHalves ? d0 < p.rot : d < p.rot;
+                    const bool on1 = MODE == kHalves ? d0 < p.rot : d + 1 < p.rot;
+                    const float a = NORM ? x[2 * i] * by : x[2 * i];
+                    const float b = NORM ? x[2 * i + 1] * by : x[2 * i + 1];
+                    const float za = NORM ? z[2 * i] * by : z[2 * i];
+                    const float zb = NORM ? z[2 * i + 1] * by : z[2 * i + 1];
+                    y[2 * i] = on0 ? fmaf(a, g.x, za * g.y) : a * g.x;
+                    y[2 * i + 1] = on1 ? fmaf(b, g.z, zb * g.w) : b * g.z;
                 }
                 uint4 out;
                 out.x = is_v ? raw[0] : pack_bf16x2(y[0], y[1]);
@@ -341,12 +368,14 @@ int launch_qk_rope(const void *q, int64_t q_stride, const void *k, int64_t k_str
                      : r->rot_dim % 16 == 0       ? rope::kHalves
                                                   : rope::kHalvesAny;
     const int rows = 32 / (head_dim / 8), passes = (p.n_heads + rows - 1) / rows;
-    // a token's passes are dealt to as many warps as leave every SM about sixteen
-    const int64_t warps = (int64_t)device_sm_count() * 16;
-    p.chunk_passes = (int)std::min<int64_t>(passes, std::max<int64_t>(1, n * passes / warps));
+    // a token's passes are dealt to as many warps as the GPU holds at a time
+    const int64_t blocks_held = (int64_t)device_sm_count() * rope::kBlocks;
+    const int64_t chunks = std::min<int64_t>(
+        passes, std::max<int64_t>(1, blocks_held * rope::kWarps / n));
+    p.chunk_passes = (int)((passes + chunks - 1) / chunks);
     p.chunks = (passes + p.chunk_passes - 1) / p.chunk_passes;
     const int64_t blocks = (n * p.chunks + rope::kWarps - 1) / rope::kWarps;
-    const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)device_sm_count() * 8);
+    const unsigned grid = (unsigned)std::min<int64_t>(blocks, blocks_held);
     const bool norm = r->q_weight != nullptr || r->k_weight != nullptr;
     const cudaError_t e = head_dim == 128 ? rope::launch<128>(p, mode, norm, grid, stream)
                                           : rope::launch<64>(p, mode, norm, grid, stream);
