@@ -659,21 +659,34 @@ class Rope:
         self.inv_freq, self.layout, self.factor = inv_freq, int(layout), float(factor)
         self.q_weight, self.k_weight, self.eps = q_weight, k_weight, float(eps)
 
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        self.__dict__["_usable"] = None  # looked at again by the next call
+
     @property
     def rot_dim(self):
         return 0 if self.inv_freq is None else 2 * self.inv_freq.numel()
 
     def _packed(self, where, device, head_dim):
-        given = [t for t in (self.inv_freq, self.q_weight, self.k_weight) if t is not None]
-        _want(where, device, torch.float32, *given)
-        for t in (self.q_weight, self.k_weight):
-            if t is not None and t.numel() != head_dim:
-                raise AttnError(ATTN_ERR_SHAPE, f"{where}: q_weight and k_weight are [{head_dim}]")
-        return _PACK_ROPE(_ptr(self.inv_freq) or 0, self.rot_dim, self.layout, self.factor,
-                          _ptr(self.q_weight) or 0, _ptr(self.k_weight) or 0, self.eps)
+        """The bytes of an attn_rope, its tensors looked at again when one is set or put
+        elsewhere."""
+        u, f, q, k = self._usable, self.inv_freq, self.q_weight, self.k_weight
+        at = (device, head_dim, 0 if f is None else f.data_ptr(),
+              0 if q is None else q.data_ptr(), 0 if k is None else k.data_ptr(),
+              0 if f is None else f.nbytes)
+        if u is None or u[0] != at:
+            _want(where, device, torch.float32, *(t for t in (f, q, k) if t is not None))
+            for t in (q, k):
+                if t is not None and t.numel() != head_dim:
+                    raise AttnError(ATTN_ERR_SHAPE,
+                                    f"{where}: q_weight and k_weight are [{head_dim}]")
+            u = (at, _PACK_ROPE(at[2], self.rot_dim, self.layout, self.factor, at[3], at[4],
+                                self.eps))
+            self.__dict__["_usable"] = u
+        return u[1]
 
 
-def _want_heads(where, device, n, *tensors):
+def _want_heads(where, device, n, dim, *tensors):
     """Refuses q, k or v that are not bf16 rows [n, heads, head_dim] whose heads stand
     next to each other; returns the strides of their tokens."""
     strides = []
@@ -681,8 +694,8 @@ def _want_heads(where, device, n, *tensors):
         if t.dtype is not _BF16 or t.get_device() != device or t.dim() != 3:
             raise AttnError(ATTN_ERR_UNSUPPORTED, f"{where}: q, k and v are bf16 [n, heads, "
                                                   "head_dim] on the current device")
-        _, heads, dim = t.shape
-        if t.shape[0] != n or dim != tensors[0].shape[2]:
+        rows, heads, last = t.shape
+        if rows != n or last != dim:
             raise AttnError(ATTN_ERR_SHAPE, f"{where}: q, k and v have n rows and one head_dim")
         step, of_head, of_dim = t.stride()
         if n and ((dim > 1 and of_dim != 1) or (heads > 1 and of_head != dim)):
@@ -700,22 +713,28 @@ def attn_qk_rope(q, k, positions, rope: Rope, q_out=None, k_out=None, stream=Non
     positions int32 [n] (what Rope says, in one pass).  The tokens of q and k may be
     any stride apart (views of a fused projection).  Returns (q_out, k_out),
     contiguous; either may be its input (in place)."""
-    n, Hq, D = q.shape
-    device = _device()
-    qs, ks = _want_heads("attn_qk_rope", device, n, q, k)
+    where, device = "attn_qk_rope", _device()
+    of_q, of_k = q.shape, k.shape
+    if len(of_q) != 3 or len(of_k) != 3:
+        raise AttnError(ATTN_ERR_SHAPE, f"{where}: q and k are [n, heads, head_dim]")
+    n, Hq, D = of_q
+    qs, ks = _want_heads(where, device, n, D, q, k)
     if q_out is None:
-        q_out = _made(_new_like, q, stream, q.shape)
+        q_out = _made(_new_like, q, stream, of_q)
     if k_out is None:
-        k_out = _made(_new_like, k, stream, k.shape)
-    _want("attn_qk_rope", device, _BF16, q_out, k_out)
-    _want("attn_qk_rope", device, _I32, positions)
-    if q_out.shape != q.shape or k_out.shape != k.shape or positions.numel() < n:
-        raise AttnError(ATTN_ERR_SHAPE, "attn_qk_rope: q_out and k_out are shaped like q and k, "
+        k_out = _made(_new_like, k, stream, of_k)
+    if not (q_out.dtype is k_out.dtype is _BF16 and positions.dtype is _I32 and
+            q_out.get_device() == k_out.get_device() == positions.get_device() == device and
+            q_out.is_contiguous() and k_out.is_contiguous() and positions.is_contiguous()):
+        _want(where, device, _BF16, q_out, k_out)
+        _want(where, device, _I32, positions)
+    if q_out.shape != of_q or k_out.shape != of_k or positions.numel() < n:
+        raise AttnError(ATTN_ERR_SHAPE, f"{where}: q_out and k_out are shaped like q and k, "
                                         "positions is [n]")
-    rc = lib().attn_qk_rope(_ptr(q), qs, _ptr(k), ks, _ptr(positions), n,
-                            rope._packed("attn_qk_rope", device, D), Hq,
-                            k.shape[1], D, _ptr(q_out), _ptr(k_out), _stream(stream))
-    _check(rc, "attn_qk_rope")
+    rc = lib().attn_qk_rope(q.data_ptr(), qs, k.data_ptr(), ks, positions.data_ptr(), n,
+                            rope._packed(where, device, D), Hq, of_k[1], D, q_out.data_ptr(),
+                            k_out.data_ptr(), _stream(stream))
+    _check(rc, where)
     return q_out, k_out
 
 
@@ -724,30 +743,39 @@ def attn_qk_rope_append(q, k, v, positions, slot_mapping, cache: KVCache, rope: 
     """attn_qk_rope, then attn_kv_append of the new keys and of v bf16 [n, Hkv, D]
     at slot_mapping int64 [n], in one launch (two for caches with scales).  k_out, if
     given, receives the new keys too.  Returns q_out."""
-    n, Hq, D = q.shape
     where, device = "attn_qk_rope_append", _device()
+    of_q, of_k = q.shape, k.shape
+    if len(of_q) != 3 or len(of_k) != 3:
+        raise AttnError(ATTN_ERR_SHAPE, f"{where}: q and k are [n, heads, head_dim]")
+    n, Hq, D = of_q
     scaled = cache.dtype in _SCALED
     if scaled and n > 1 and not v.is_contiguous():
         v = _made(torch.Tensor.contiguous, v, stream)
-    qs, ks, vs = _want_heads(where, device, n, q, k, v)
+    qs, ks, vs = _want_heads(where, device, n, D, q, k, v)
     if q_out is None:
-        q_out = _made(_new_like, q, stream, q.shape)
+        q_out = _made(_new_like, q, stream, of_q)
     if k_out is None and scaled:
-        k_out = _made(_new_like, k, stream, k.shape)
-    _want(where, device, _BF16, q_out, *(() if k_out is None else (k_out,)))
-    _want(where, device, _I32, positions)
-    _want(where, device, _I64, slot_mapping)
+        k_out = _made(_new_like, k, stream, of_k)
+    if not (q_out.dtype is _BF16 and positions.dtype is _I32 and slot_mapping.dtype is _I64 and
+            q_out.get_device() == positions.get_device() == slot_mapping.get_device() == device and
+            q_out.is_contiguous() and positions.is_contiguous() and slot_mapping.is_contiguous()):
+        _want(where, device, _BF16, q_out)
+        _want(where, device, _I32, positions)
+        _want(where, device, _I64, slot_mapping)
+    if k_out is not None:
+        _want(where, device, _BF16, k_out)
     known = cache._known(where, device)
-    if k.shape != v.shape or k.shape[1] != known[6][1] or D != known[6][-1]:
+    _want_ref(where, cache, device)
+    if of_k != v.shape or of_k[1] != known[6][1] or D != known[6][-1]:
         raise AttnError(ATTN_ERR_SHAPE, f"{where}: k and v are [n, {known[6][1]}, {known[6][-1]}]")
-    if q_out.shape != q.shape or (k_out is not None and k_out.shape != k.shape) or \
+    if q_out.shape != of_q or (k_out is not None and k_out.shape != of_k) or \
             positions.numel() < n or slot_mapping.numel() < n:
         raise AttnError(ATTN_ERR_SHAPE, f"{where}: q_out and k_out are shaped like q and k, "
                                         "positions and slot_mapping are [n]")
     rc = lib().attn_qk_rope_append(
-        _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(positions), _ptr(slot_mapping), n,
-        rope._packed(where, device, D), known[7], Hq, k.shape[1], D,
-        _ptr(q_out), _ptr(k_out), _ptr(err), _stream(stream))
+        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(),
+        slot_mapping.data_ptr(), n, rope._packed(where, device, D), known[7], Hq, of_k[1], D,
+        q_out.data_ptr(), _ptr(k_out), _ptr(err), _stream(stream))
     _check(rc, where)
     return q_out
 
@@ -758,19 +786,34 @@ def attn_kv_read(slot_mapping, cache: KVCache, k_out=None, v_out=None, err=None,
     give zeros and ATTN_ERR_BOUNDS in err."""
     where, device = "attn_kv_read", _device()
     known = cache._known(where, device)
-    _want(where, device, _I64, slot_mapping)
+    _want_ref(where, cache, device)
+    if not (slot_mapping.dtype is _I64 and slot_mapping.get_device() == device and
+            slot_mapping.is_contiguous()):
+        _want(where, device, _I64, slot_mapping)
     shape = (slot_mapping.numel(), known[6][1], known[6][-1])
     if k_out is None:
         k_out = _made(_rows_like, slot_mapping, stream, shape)
     if v_out is None:
         v_out = _made(_rows_like, slot_mapping, stream, shape)
-    _want(where, device, _BF16, k_out, v_out)
+    if not (k_out.dtype is v_out.dtype is _BF16 and
+            k_out.get_device() == v_out.get_device() == device and
+            k_out.is_contiguous() and v_out.is_contiguous()):
+        _want(where, device, _BF16, k_out, v_out)
     if k_out.shape != shape or v_out.shape != shape:
         raise AttnError(ATTN_ERR_SHAPE, f"{where}: k_out and v_out are {shape}")
-    rc = lib().attn_kv_read(_ptr(slot_mapping), shape[0], known[7], shape[1], shape[2],
-                            _ptr(k_out), _ptr(v_out), _ptr(err), _stream(stream))
+    rc = lib().attn_kv_read(slot_mapping.data_ptr(), shape[0], known[7], shape[1], shape[2],
+                            k_out.data_ptr(), v_out.data_ptr(), _ptr(err), _stream(stream))
     _check(rc, where)
     return k_out, v_out
+
+
+def _want_ref(where, cache, device):
+    """The reference vector of an unscaled E4M3 cache (a scaled one's is looked at with
+    its scales)."""
+    if cache.dtype == ATTN_KV_FP8_E4M3 and cache.k_ref is not None:
+        _want(where, device, torch.float32, cache.k_ref)
+        if cache.k_ref.numel() != cache.n_kv_heads * cache.head_dim:
+            raise AttnError(ATTN_ERR_SHAPE, f"{where}: k_ref is [n_kv_heads, head_dim]")
 
 
 def _rows_like(t, shape):

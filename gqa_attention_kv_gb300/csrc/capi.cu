@@ -603,6 +603,12 @@ int attn_qk_rope_append(const void *q, int64_t q_stride, const void *k, int64_t 
                             n_kv_heads, head_dim, q_out, k_out);
         rc != ATTN_OK)
         return rc;
+    const int64_t held = cache->num_slots * n_kv_heads * head_dim *
+                         (cache->dtype == ATTN_KV_BF16 ? 2 : 1);
+    const int64_t q_bytes = 2 * n * n_q_heads * head_dim, k_bytes = 2 * n * n_kv_heads * head_dim;
+    for (const void *of : {static_cast<const void *>(cache->k), static_cast<const void *>(cache->v)})
+        if (overlap(q_out, q_bytes, of, held) || overlap(k_out, k_bytes, of, held))
+            return ATTN_ERR_SHAPE;
     if (scaled) {
         if (int rc = check_scaled(cache, true); rc != ATTN_OK) return rc;
         if (n > 1 && v_stride != (int64_t)n_kv_heads * head_dim) return ATTN_ERR_UNSUPPORTED;
