@@ -4,11 +4,13 @@
 // scale of the slot's block and head), for keys plus k_ref, formed in float32 and rounded
 // once to bf16.
 //
-// A gather bound by HBM: one warp per (row, tensor), as in the append, a lane 8 elements at
-// a time (8 or 16 bytes in, 16 out), kUnroll such pieces in flight.
+// A gather bound by HBM: a warp a row of both tensors, a lane 8 elements at a time (8 or 16
+// bytes in, 16 out), kUnroll such pieces in flight.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -27,7 +29,8 @@ struct Params {
     const int64_t *slots;
     int64_t n, num_slots;
     KvPlace place;
-    int head_pieces, row_pieces;  // pieces of 8 elements
+    int head_shift, row_pieces;  // pieces of 8 elements: log2 of a head's, a row's
+    int parts;  // warps of a row
     __nv_bfloat16 *k_out, *v_out;
     int32_t *err;
 };
@@ -57,46 +60,48 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const Params p) {
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-    for (int64_t it = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < 2 * p.n;
+    const int64_t head_stride = (p.place.rows == 0 ? 1 : p.place.rows) * (int64_t)p.place.head_bytes;
+    for (int64_t it = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < p.n * p.parts;
          it += warps) {
-        const int64_t row = it >> 1;
-        const bool is_v = it & 1;
+        const int64_t row = p.parts == 1 ? it : it / p.parts;
+        const int part = (int)(it - row * p.parts);
         const int64_t slot = __ldg(p.slots + row);
-        uint4 *dst = reinterpret_cast<uint4 *>(is_v ? p.v_out : p.k_out) + row * p.row_pieces;
-        if (slot < 0 || slot >= p.num_slots) {
-            if (lane == 0 && !is_v) report_error(p.err, ATTN_ERR_BOUNDS);
-            for (int i = lane; i < p.row_pieces; i += 32) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-            continue;
-        }
-        const uint8_t *src = (is_v ? p.v : p.k) + p.place.head_offset(slot, 0);
-        const int64_t head_stride =
-            (p.place.rows == 0 ? 1 : p.place.rows) * (int64_t)p.place.head_bytes;
-        const float *scales = is_v ? p.vs : p.ks;
-        if (FMT != kBF16 && scales != nullptr)
-            scales += (slot >> p.scale_shift) * p.place.n_kv_heads;
-        for (int i0 = lane; i0 < p.row_pieces; i0 += 32 * kUnroll) {
+        const bool there = slot >= 0 && slot < p.num_slots;
+        if (!there && lane == 0 && part == 0) report_error(p.err, ATTN_ERR_BOUNDS);
+        const int64_t at = there ? p.place.head_offset(slot, 0) : 0;
+        const int64_t scale_at = (there ? slot >> p.scale_shift : 0) * p.place.n_kv_heads;
+        // pieces 0 .. row_pieces - 1 are K's, the others V's
+        for (int i0 = part * 32 * kUnroll + lane; i0 < 2 * p.row_pieces;
+             i0 += p.parts * 32 * kUnroll) {
             uint4 a[kUnroll];
             float s[kUnroll];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const int i = i0 + 32 * u, h = i / p.head_pieces, at = i - h * p.head_pieces;
-                if (i >= p.row_pieces) break;
+                const bool is_v = i0 + 32 * u >= p.row_pieces;
+                const int i = i0 + 32 * u - (is_v ? p.row_pieces : 0);
+                const int h = i >> p.head_shift, piece = i & ((1 << p.head_shift) - 1);
+                a[u] = make_uint4(0u, 0u, 0u, 0u);
+                s[u] = 1.f;
+                if (i >= p.row_pieces || !there) continue;
+                const uint8_t *src = (is_v ? p.v : p.k) + at + h * head_stride;
                 if constexpr (FMT == kBF16) {
-                    a[u] = __ldg(reinterpret_cast<const uint4 *>(src + h * head_stride) + at);
+                    a[u] = __ldg(reinterpret_cast<const uint4 *>(src) + piece);
                 } else {
-                    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(src + h * head_stride) + at);
+                    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(src) + piece);
                     a[u].x = w.x, a[u].y = w.y;
-                    s[u] = scales != nullptr ? fmaxf(__ldg(scales + h), kScaleFloor) : 1.f;
+                    const float *scales = is_v ? p.vs : p.ks;
+                    if (scales != nullptr) s[u] = fmaxf(__ldg(scales + scale_at + h), kScaleFloor);
                 }
             }
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const int i = i0 + 32 * u;
-                if (i >= p.row_pieces) break;
+                const bool is_v = i0 + 32 * u >= p.row_pieces;
+                const int i = i0 + 32 * u - (is_v ? p.row_pieces : 0);
+                if (i >= p.row_pieces) continue;
                 if constexpr (FMT != kBF16) {
                     float x[8];
                     widen<FMT == kINT8>(make_uint2(a[u].x, a[u].y), x);
-                    if (!is_v && p.k_ref != nullptr) {
+                    if (!is_v && p.k_ref != nullptr && there) {
                         const float4 r0 = __ldg(reinterpret_cast<const float4 *>(p.k_ref) + 2 * i);
                         const float4 r1 = __ldg(reinterpret_cast<const float4 *>(p.k_ref) + 2 * i + 1);
                         const float r[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
@@ -109,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const Params p) {
                     a[u] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
                                       pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
                 }
-                dst[i] = a[u];
+                reinterpret_cast<uint4 *>(is_v ? p.v_out : p.k_out)[row * p.row_pieces + i] = a[u];
             }
         }
     }
@@ -133,14 +138,17 @@ int launch_kv_read(const int64_t *slot_mapping, int64_t n, const attn_kv_cache *
     p.n = n;
     p.num_slots = cache->num_slots;
     p.place = kv_place(cache, n_kv_heads, head_dim, cache->dtype == ATTN_KV_BF16 ? 2 : 1);
-    p.head_pieces = head_dim / 8;
-    p.row_pieces = n_kv_heads * p.head_pieces;
+    p.head_shift = head_dim == 128 ? 4 : 3;
+    p.row_pieces = n_kv_heads << p.head_shift;
     p.k_out = static_cast<__nv_bfloat16 *>(k_out);
     p.v_out = static_cast<__nv_bfloat16 *>(v_out);
     p.err = err;
     const int per_block = rd::kThreads / 32;
-    int64_t blocks = (2 * n + per_block - 1) / per_block;
     const int64_t cap = (int64_t)device_sm_count() * 16;
+    // few rows: a warp for each kUnroll pieces a lane
+    const int64_t most = (2 * (int64_t)p.row_pieces + 32 * rd::kUnroll - 1) / (32 * rd::kUnroll);
+    p.parts = (int)std::max<int64_t>(1, std::min<int64_t>(most, cap * per_block / n));
+    int64_t blocks = (n * p.parts + per_block - 1) / per_block;
     if (blocks > cap) blocks = cap;
     auto go = [&](auto kernel) {
         return launch_pdl(kernel, dim3((unsigned)blocks), dim3(rd::kThreads), 0, stream, p);
