@@ -549,6 +549,8 @@ int attn_decode_shared(const void *q, const attn_kv_cache *cache, int n_rows,
         return ATTN_ERR_SHAPE;
     if (batch == 0) return ATTN_OK;
     if (!prefix_rows || !prefix_lens) return ATTN_ERR_NULL;
+    const int64_t q_bytes = (int64_t)2 * batch * q_rows * n_q_heads * head_dim;
+    if (overlap(q, q_bytes, out, q_bytes)) return ATTN_ERR_SHAPE;
     if (gqa::kv_scaled(cache->dtype))
         if (rc = check_scaled(cache, true); rc != ATTN_OK) return rc;
     gqa::SharedPlan plan;

@@ -609,6 +609,7 @@ int attn_decode_sinks(const void *q, const attn_kv_cache *cache, const int32_t *
  *   zero-filled before its first use; one workspace may serve this call,
  *   attn_decode and attn_decode_sinks.  Calls whose kernels overlap on the GPU,
  *   graphs replayed at the same time among them, need separate workspaces.
+ *   out does not overlap q (ATTN_ERR_SHAPE).
  * Every other argument and status is attn_decode's.
  */
 size_t attn_decode_shared_workspace_size(const attn_kv_cache *cache, int batch, int q_rows,

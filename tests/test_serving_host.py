@@ -112,7 +112,7 @@ def test_read_refusals(lib):  # noqa: F811
 
 
 def shared_rc(lib, c, rows=None, B=2, R=1, L=512, P=256, W=0, Hq=32, H=8, D=128, scale=0.1,  # noqa: F811
-              prows=256, plens=512, ws=1 << 20, ws_bytes=BIG, q=16, out=32):
+              prows=256, plens=512, ws=1 << 20, ws_bytes=BIG, q=1 << 24, out=2 << 24):
     cs = c.struct()
     return lib.attn_decode_shared(q, ctypes.byref(cs), B if rows is None else rows, 64, 128, prows,
                                   plens, B, R, L, P, W, Hq, H, D, scale, out, ws, ws_bytes, None,
@@ -124,7 +124,8 @@ def test_shared_refusals(lib):  # noqa: F811
     for bad in (dict(prows=None), dict(plens=None), dict(q=None), dict(out=None), dict(ws=None)):
         assert shared_rc(lib, plain, **bad) == gq.ATTN_ERR_NULL, bad
     for bad in (dict(P=-1), dict(rows=1), dict(rows=3), dict(B=-1), dict(R=0), dict(L=0),
-                dict(scale=0.0), dict(scale=math.nan), dict(Hq=30)):
+                dict(scale=0.0), dict(scale=math.nan), dict(Hq=30), dict(out=1 << 24),
+                dict(out=(1 << 24) + 16)):
         assert shared_rc(lib, plain, **bad) == gq.ATTN_ERR_SHAPE, bad
     for bad in (dict(q=8), dict(out=40), dict(ws=(1 << 20) + 8)):
         assert shared_rc(lib, plain, **bad) == gq.ATTN_ERR_ALIGN, bad
