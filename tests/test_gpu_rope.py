@@ -177,19 +177,18 @@ def make_cache(kind, dtype, slots, H, D, per, head_major):
                       layout=gq.ATTN_LAYOUT_BHSD if head_major else gq.ATTN_LAYOUT_BSHD, **more)
 
 
-@pytest.mark.parametrize("dtype,D", [(gq.ATTN_KV_BF16, 64), (gq.ATTN_KV_BF16, 128),
-                                     (gq.ATTN_KV_FP8_E4M3, 128),
-                                     (gq.ATTN_KV_FP8_E4M3_SCALED, 64),
-                                     (gq.ATTN_KV_INT8_SCALED, 128)])
-@pytest.mark.parametrize("kind,head_major", [(gq.LINEAR, False), (gq.PAGED, True),
-                                             (gq.RING, False)])
+@pytest.mark.parametrize("dtype,D,kind,head_major", [
+    (dtype, D, kind, head_major)
+    for dtype, D in ((gq.ATTN_KV_BF16, 64), (gq.ATTN_KV_BF16, 128), (gq.ATTN_KV_FP8_E4M3, 128),
+                     (gq.ATTN_KV_FP8_E4M3_SCALED, 64), (gq.ATTN_KV_INT8_SCALED, 128))
+    for kind, head_major in ((gq.LINEAR, False), (gq.PAGED, True), (gq.RING, False))
+    # rings of scaled blocks are refused
+    if kind != gq.RING or dtype in (gq.ATTN_KV_BF16, gq.ATTN_KV_FP8_E4M3)])
 @pytest.mark.parametrize("layout,rot,norm,n", [(HALF, 64, True, 40), (PAIRS, 32, False, 7),
                                                (HALF, 20, True, 1000)])
 def test_append_is_rope_then_append(dtype, D, kind, head_major, layout, rot, norm, n):
     """Bit for bit the two calls, for every cache; slots outside are skipped."""
     scaled = dtype in (gq.ATTN_KV_FP8_E4M3_SCALED, gq.ATTN_KV_INT8_SCALED)
-    if kind == gq.RING and scaled:
-        pytest.skip("rings of scaled blocks are refused")
     H, per = 3, 32
     (q, k, v, pos, rope), want, v_cpu = make(n, 9, H, D, rot, layout, norm, n)
     slots = (n + 40 + per - 1) // per * per

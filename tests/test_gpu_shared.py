@@ -351,6 +351,32 @@ def test_many_requests():
     Case("bf16", gq.PAGED, prefix, tails, 1, 4, 2, 64, 8, 30).check()
 
 
+@pytest.mark.parametrize("fmt,D,G,kind", [("bf16", 64, 1, gq.PAGED), ("int8", 64, 2, gq.LINEAR),
+                                          ("bf16", 128, 70, gq.LINEAR), ("e4m3", 128, 3, gq.PAGED)])
+def test_more_units_than_sms(fmt, D, G, kind):
+    """Forty groups of eight KV heads: a CTA works on one piece after another, tiles full and
+    alone in turn, rows of a tile that hold no query."""
+    prefix, first = [], 0
+    for i in range(40):
+        size = (1, 2, 5)[i % 3]
+        prefix += [(first, 17 + 31 * (i % 7))] * size
+        first += size
+    tails = [1 + i % 5 for i in range(first)]
+    H = 8 if G < 70 else 5
+    Case(fmt, kind, prefix, tails, 1, G * H, H, D, 16, 40 + D + G).check()
+
+
+def test_own_keys_of_many_requests_in_two_launches():
+    """Past 256 (request, row block) pairs, each with own keys of several chunks."""
+    n = 300
+    c = Case("bf16", gq.LINEAR, one_group(n, 40), [1 + (7 * i) % 90 for i in range(n)], 1, 2, 1, 64,
+             8, 77)
+    c.check()
+    c = Case("int8", gq.LINEAR, one_group(150, 40), [40 + i % 50 for i in range(150)], 20, 2, 2, 64,
+             16, 78)  # two blocks of rows a request
+    c.check()
+
+
 def test_a_long_prefix_and_offsets_past_32_bits():
     """Slots whose bytes lie past 2^32 from the cache's start, keys in constant stretches:
     the answer is known."""
