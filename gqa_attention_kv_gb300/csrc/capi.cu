@@ -453,6 +453,7 @@ int check_shared(const attn_kv_cache *cache, int batch, int n_q_heads, int n_kv_
     if (max_prefix_len < 0) return ATTN_ERR_SHAPE;
     if (cache->kind == ATTN_CACHE_RING) return ATTN_ERR_UNSUPPORTED;
     if (batch > 4096 || n_q_heads / n_kv_heads > 128) return ATTN_ERR_UNSUPPORTED;
+    if (cache->num_slots > INT32_MAX / n_kv_heads) return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;
 }
 
@@ -475,6 +476,8 @@ int check_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                           static_cast<const void *>(rope->k_weight)})
         if (reinterpret_cast<uintptr_t>(f) & 3u) return ATTN_ERR_ALIGN;
     const int64_t q_row = (int64_t)n_q_heads * head_dim, k_row = (int64_t)n_kv_heads * head_dim;
+    constexpr int64_t kFar = int64_t(1) << 30;  // (n of them fit 63 bits)
+    if (n > 1 && (q_stride > kFar || k_stride > kFar || (v && v_stride > kFar))) return ATTN_ERR_SHAPE;
     if (n > 1 && (q_stride < q_row || k_stride < k_row || q_stride % 8 || k_stride % 8))
         return ATTN_ERR_SHAPE;
     if (n > 1 && v && (v_stride < k_row || v_stride % 8)) return ATTN_ERR_SHAPE;
@@ -631,7 +634,8 @@ int attn_kv_read(const int64_t *slot_mapping, int64_t n, const attn_kv_cache *ca
                  int n_kv_heads, int head_dim, void *k_out, void *v_out, int32_t *err_word,
                  attn_stream_t stream) {
     if (!cache) return ATTN_ERR_NULL;
-    if (n < 0 || n_kv_heads < 1 || n_kv_heads > (1 << 20)) return ATTN_ERR_SHAPE;
+    if (n < 0 || n > (int64_t(1) << 31) || n_kv_heads < 1 || n_kv_heads > (1 << 20))
+        return ATTN_ERR_SHAPE;
     if (head_dim != 64 && head_dim != 128) return ATTN_ERR_UNSUPPORTED;
     const bool scaled = gqa::kv_scaled(cache->dtype);
     if (cache->dtype != ATTN_KV_BF16 && cache->dtype != ATTN_KV_FP8_E4M3 && !scaled)

@@ -255,7 +255,7 @@ __device__ int make_plan(const Params &p, int32_t *mem, int want, bool tables, P
         // more than the SMs lies between work / SMs and work / (SMs - U); 32 of those are tried
         const int spare = max(0, p.sms - units);
         int most = 0;  // s, or 0: units are cut in proportion
-        if (groups <= 32 && spare > 0 && work < (int64_t(1) << 31) && work > 0) {
+        if (groups <= 32 && spare > 0 && work < (int64_t(1) << 30) && work > 0) {
             const int t = lane < groups ? tiles_of(lane) : 0;
             const int u = t > 0 ? pairs_of(lane) * p.n_kv_heads : 0;
             const int s0 = ((int)work + p.sms - 1) / p.sms, s1 = ((int)work + spare - 1) / spare;
@@ -930,7 +930,7 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
         int qi = -1, key_cap = -1;  // the row's position, and the last shared key it may see
         if (live) {
             const int i = w.start + tile_pos + row / G, b = i / R;
-            qi = p.positions[i];
+            qi = max(p.positions[i], -1);  // (below zero: no keys)
             const int len = max(0, min(p.seq_lens[b], p.cap));
             key_cap = min(min(qi, len - 1), max(0, min(p.prefix_lens[b], p.prefix_cap)) - 1);
         }

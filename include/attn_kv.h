@@ -257,9 +257,10 @@ typedef enum {
  *                                               x2 cos a_i + x1 sin a_i)
  * inv_freq holds whatever a model's long-context scaling makes of the
  * frequencies (finite, magnitudes up to 2^16), factor what it multiplies the
- * cosines and sines with (1 without).  Angles are exact to 2^-31 of a turn at
- * every int32 position, so far positions lose nothing.  Arithmetic is float32,
- * rounded once to bf16.
+ * cosines and sines with (1 without).  Angles are formed in integers modulo a turn:
+ * for a frequency below 2^e, e >= 1, to 2^(e-31) of a turn at every int32 position,
+ * so far positions lose nothing.  From there on arithmetic is float32, rounded once
+ * to bf16.
  */
 typedef struct {
     const float *inv_freq;  /* [rot_dim / 2]; NULL with rot_dim 0 */
@@ -280,7 +281,7 @@ typedef struct {
  *   q, k       bf16, device, n tokens: token i's heads stand one after another
  *              (n_q_heads or n_kv_heads rows of head_dim) at element
  *              i * q_stride (k_stride): the rows of a fused projection need no
- *              copy.  Strides are multiples of 8 and at least a token's row;
+ *              copy.  Strides are multiples of 8, a token's row at least and 2^30 at most;
  *              bases are 16-byte aligned.
  *   positions  int32 [n], device
  *   n          tokens (0 is a no-op)
@@ -593,7 +594,8 @@ int attn_decode_sinks(const void *q, const attn_kv_cache *cache, const int32_t *
  *   max_prefix_len   host-side upper bound of prefix_lens[], >= 0
  * Which keys a row attends is attn_decode's rule (seq_lens counts the prefix).
  * LINEAR and PAGED caches of every dtype and layout; RING is not supported.
- * n_q_heads / n_kv_heads at most 128, batch at most 4,096.
+ * n_q_heads / n_kv_heads at most 128, batch at most 4,096, num_slots * n_kv_heads
+ * below 2^31.
  *   The shared keys' products run on tensor cores: over a bf16 cache Q K^T takes
  *   q and k as bf16, over an 8-bit one q is rounded to f16 (a magnitude of 65520
  *   or more is reported as ATTN_ERR_UNSUPPORTED); softmax weights are rounded

@@ -110,8 +110,8 @@ def test_far_positions(layout):
         want[..., one] = x[..., one] * c - x[..., two] * s
         want[..., two] = x[..., two] * c + x[..., one] * s
         size[..., one] = size[..., two] = 1.25 * (x[..., one].abs() + x[..., two].abs())
-        # the fraction of a turn: 2^-64 of a turn's unit for each of up to 2^(e + 1) p steps,
-        # e <= 4: 2^36 2^-64, nothing beside 2^-31
+        # the fraction of a turn: frequencies below 2^5 to 2^-26 of a turn, within what the
+        # float of half turns is allowed
         check(y, (want, size))
 
 

@@ -199,6 +199,17 @@ def test_rows_without_keys_and_short_lengths(fmt):
     assert not got[0].any() and not got[4, 0].any()
 
 
+def test_positions_far_below_zero():
+    """They attend nothing, wherever the key tiles lie; a window beside them may be any int32."""
+    c = Case("bf16", gq.LINEAR, one_group(5, 300), [4] * 5, 2, 8, 2, 128, 16, 6)
+    low = -2 ** 31
+    c.pos = torch.tensor([low, 303, 302, low + 1, -2, low + 299, 302, 303, 300, low], dtype=torch.int32)
+    for window in (0, 2 ** 31 - 1, 20):
+        c.window = window
+        got = c.check()
+        assert not got[0, 0].any() and not got[1, 1].any() and not got[2].any()
+
+
 def test_own_slots_before_the_prefix_are_not_read():
     """... nor anything behind a request's last key; table entries there are -1."""
     c = Case("bf16", gq.PAGED, one_group(3, 96), [1, 40, 2], 1, 8, 2, 128, 16, 5)
@@ -339,6 +350,38 @@ def test_stream_graph_and_one_workspace():
                               128 ** -0.5, workspace=big)
         ref.check_output(gq.attn_decode(flat.q.to(DEV), flat.cache, *a, 200, 0, 128 ** -0.5,
                                         workspace=big), exact, mass, weight_bits=11)
+
+
+def test_two_calls_at_once():
+    """On two streams, eager and as graphs, each with its workspace."""
+    cases = [Case("bf16", gq.PAGED, one_group(30, 900), list(range(1, 31)), 1, 8, 2, 128, 16, 7),
+             Case("int8", gq.LINEAR, one_group(9, 2000), list(range(1, 10)), 2, 16, 4, 64, 16, 8)]
+    calls, wants, outs, streams, graphs = [], [], [], [], []
+    for c in cases:
+        wants.append(c.run())
+        need = gq.attn_decode_shared_workspace_size(c.cache, c.q.shape[0], c.R, c.q.shape[2],
+                                                    c.longest, c.max_prefix)
+        ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
+        outs.append(torch.empty_like(wants[-1]))
+        on = [x.to(DEV) for x in (c.lens, c.pos, c.prows, c.plens)]
+        calls.append(lambda c=c, q=c.q.to(DEV), on=on, out=outs[-1], ws=ws: gq.attn_decode_shared(
+            q, c.cache, *on, c.longest, c.max_prefix, 0, c.D ** -0.5, out=out, workspace=ws))
+        streams.append(torch.cuda.Stream())
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            calls[-1]()
+    torch.cuda.synchronize()
+    for go in (calls, [g.replay for g in graphs]):
+        for out in outs:
+            out.fill_(NAN)
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for s, f in zip(streams, go):
+                with torch.cuda.stream(s):
+                    f()
+        torch.cuda.synchronize()
+        for out, want in zip(outs, wants):
+            assert torch.equal(out, want)
 
 
 def test_many_requests():

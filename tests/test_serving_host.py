@@ -39,7 +39,7 @@ def test_rope_refusals(lib):  # noqa: F811
         assert rope_rc(lib, **bad) == null, bad
     assert lib.attn_qk_rope(16, 0, 16, 0, 64, 4, None, 32, 8, 128, 16, 16, None) == null
     for bad in (dict(n=-1), dict(Hq=0), dict(H=0), dict(qs=4100), dict(qs=4088),
-                dict(ks=1016), dict(ks=1028), dict(r=rope(rot=-2)), dict(r=rope(rot=7)),
+                dict(ks=1016), dict(ks=1028), dict(qs=2 ** 30 + 8), dict(ks=2 ** 40), dict(r=rope(rot=-2)), dict(r=rope(rot=7)),
                 dict(r=rope(rot=130)), dict(r=rope(factor=math.inf)), dict(r=rope(factor=math.nan)),
                 dict(r=rope(qw=64, eps=0.0)), dict(r=rope(kw=64, eps=math.nan)),
                 dict(r=rope(kw=64, eps=1e-31)), dict(r=rope(kw=64, eps=math.inf)),
@@ -97,7 +97,7 @@ def test_read_refusals(lib):  # noqa: F811
     for bad in (dict(slots=None), dict(ko=None), dict(vo=None)):
         assert read_rc(lib, plain, **bad) == gq.ATTN_ERR_NULL
     assert lib.attn_kv_read(64, 4, None, 8, 128, 16, 32, None, None) == gq.ATTN_ERR_NULL
-    for bad in (dict(n=-1), dict(H=0), dict(vo=(1 << 20) + 16), dict(ko=16 << 20),
+    for bad in (dict(n=-1), dict(n=2 ** 31 + 1), dict(H=0), dict(vo=(1 << 20) + 16), dict(ko=16 << 20),
                 dict(vo=(32 << 20) + 1024)):
         assert read_rc(lib, plain, **bad) == gq.ATTN_ERR_SHAPE, bad
     for bad in (dict(ko=(1 << 20) + 8), dict(vo=(2 << 20) + 4)):
@@ -132,6 +132,8 @@ def test_shared_refusals(lib):  # noqa: F811
     for bad in (dict(D=96), dict(Hq=8 * 129)):
         assert shared_rc(lib, plain, **bad) == gq.ATTN_ERR_UNSUPPORTED, bad
     assert shared_rc(lib, cache(gq.RING, gq.ATTN_KV_BF16), W=64) == gq.ATTN_ERR_UNSUPPORTED
+    vast = cache(dtype=gq.ATTN_KV_BF16, slots=2 ** 28)  # times 8 heads: 2^31
+    assert shared_rc(lib, vast) == gq.ATTN_ERR_UNSUPPORTED
     many = cache(gq.PAGED, gq.ATTN_KV_BF16, sps=0, bs=16)
     assert shared_rc(lib, many, B=4097) == gq.ATTN_ERR_UNSUPPORTED
     need = gq.attn_decode_shared_workspace_size(plain, 2, 1, 32, 512, 256)
