@@ -189,9 +189,9 @@ struct AttendParts {
 };
 
 // One launch of the plan, its entries from e0 on, over keys t >= from[b] (clipped to
-// 0 .. from_cap).  late_wait: what the stream's launch before this one writes is not read by
-// this one (but by whoever merges the parts), and that launch waited for everything before it.
-// next: a counter that is 0 when the launch begins.
+// 0 .. from_cap).  late_wait: what the stream's launch before this one writes after letting it
+// begin is not read by this one (but by whoever merges the parts), and that launch waited for
+// everything before it.  next: a counter that is 0 when the launch begins.
 int launch_attend_parts(const AttendPlan &plan, int e0, const int32_t *from, int from_cap,
                         const void *q, const attn_kv_cache *cache, const int32_t *seq_lens,
                         const int32_t *positions, int q_rows, int max_seq_len, int window,

@@ -18,13 +18,13 @@
 // warpgroups take every other key tile of it each (with a state each): a lone tile's chain
 // product - softmax - product would else leave the tensor cores and the softmax waiting for
 // one another.
-//   warp 0       loads: TMA boxes of whole runs of keys (a page, or 128 of a linear cache), one
-//                a lane; where pages are no multiple of 8 keys, 16-byte cp.async by row
+//   warps 0, 2   load K and V: TMA boxes of whole runs of keys (a page, or 128 of a linear cache),
+//                one a lane; where pages are no multiple of 8 keys, 16-byte cp.async by row
 //   warp 1       one thread issues tcgen05.mma: S = Q K^T, O += P V (f16, P from TMEM)
-//   warps 4..7   bring what is loaded into the form that is multiplied: V of a bf16 cache to
-//                f16 in place, 8-bit codes to f16 (exact) from a ring of their own; keys
-//                outside the group's range become zeros
-//   warps 8..15  softmax, a thread a row of a tile; weights rounded once to f16 and written
+//   warps 4..    bring what is loaded into the form that is multiplied: V of a bf16 cache to
+//                f16 in place (warps 4..7), 8-bit codes to f16 (exact) from a ring of their own
+//                (K warps 4..7, V warps 8..11); values outside the group's range become zeros
+//   the last 8   softmax, a thread a row of a tile; weights rounded once to f16 and written
 //                over S in TMEM
 // The plan is made on the device from lengths, rows and positions, by every CTA for itself
 // (a captured graph follows them); CTAs are persistent for batches of more pairs than SMs.
@@ -67,8 +67,8 @@ enum Fmt { kBF16 = 0, kE4M3 = 1, kINT8 = 2 };
 // Shared memory: Q tile 0, K, V, codes, in stages of 128 keys.  A load is under way for about
 // 2 us, longer than a tile's products, and a stage is taken from its request until its last
 // product, so depth is what counts: of five bf16 tiles of 128 dims V, which also waits for its
-// conversion and for the weights, has three (two: 2.3 us a pair of tiles, three: see DESIGN's
-// figures).  Where there is no Q tile 1 its place is one more K stage, or two of codes.
+// conversion and for the weights, has three.  Where there is no Q tile 1 its place is one more K
+// stage, or two of codes (as a second tile of converted K it was no faster).
 template <int FMT, int HD>
 struct Cfg {
     static constexpr bool kCodes = FMT != kBF16;
@@ -88,7 +88,10 @@ struct Cfg {
     static constexpr int kOffRaw = kOffQ1 + kQBytes;       // (grows back over Q tile 1)
     static constexpr int kOffV = kOffRaw + kRawStages * kRawBytes;
     static constexpr int kOffBar = kOffV + kVStages * kTileBytes;
-    static constexpr int kMaxK = kKStages + (kCodes ? 0 : 1);  // with Q tile 1's place
+    // K is passed on and taken back in parts: whole bf16 tiles, 64 dims of converted codes
+    static constexpr int kKSplit = kCodes ? kHalves : 1;
+    static constexpr int kKPart = kTileBytes / kKSplit;
+    static constexpr int kMaxK = kKStages * kKSplit + (kCodes ? 0 : 1);  // with Q tile 1's place
     static constexpr int kMaxRaw = kCodes ? kRawStages + 2 : 0;
     static constexpr int kNumBars = 3 * kMaxK + 3 * kVStages + 2 * kMaxRaw + 10;
     static constexpr size_t kSmem = 1024 + kOffBar + kNumBars * 8 + 16;
@@ -508,7 +511,7 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
     const int first_pos = w.pair * 2 * p.rt;         // of the group's positions
     const bool dual = w.n_pos <= p.rt;               // one tile, two streams of key tiles
     const int n_tiles = w.n_pos - first_pos > p.rt ? 2 : 1;
-    const int k_stages = C::kKStages + (!C::kCodes && dual ? 1 : 0);
+    const int k_stages = C::kKStages * C::kKSplit + (!C::kCodes && dual ? 1 : 0);  // of parts
     const int raw_stages = C::kRawStages + (C::kCodes && dual ? 2 : 0);
     uint8_t *sRaw = smem + C::kOffRaw - (dual ? C::kQBytes : 0);
     const int32_t *table = p.paged ? p.block_table + (int64_t)w.prow * p.max_blocks : nullptr;
@@ -518,9 +521,10 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
     auto page_of = [&](int t) { return __ldg(table + block_of(t)); };
 
     if (warp < kThreads / 32 - 8) {
-        if (warp == 0) {
+        if (warp == 0 || warp == 2) {
             // ------------------------------------------------------------ loads
-            if (lane == 0) {
+            const bool is_v = warp == 2;
+            if (!is_v && lane == 0) {
                 mbar_arrive_expect_tx(q_full, n_tiles * C::kHalves * used * 128);
                 for (int a = 0; a < n_tiles; ++a)
                     for (int hf = 0; hf < C::kHalves; ++hf)
@@ -594,46 +598,35 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
                 }
                 cp_async_arrive_noinc(bar);
             };
-            // K and V of a tile in turn (V behind the next K would wait for that K's stage, and
-            // the product for V); a tile's pages are read a tile before they are wanted
-            int kj = 0, vj = 0;
-            Turn kt, vt, rt;
-            auto load = [&](auto v_c, int j, int2 at) {
-                constexpr bool kV = decltype(v_c)::value;
-                Turn &t = C::kCodes ? rt : kV ? vt : kt;
-                uint64_t *empty = C::kCodes ? raw_empty : kV ? v_empty : k_empty;
-                uint64_t *full = C::kCodes ? raw_full : kV ? v_full : k_full;
-                uint8_t *to = (C::kCodes ? sRaw : kV ? sV : sK) + t.st * kBytes;
+            // a tile's pages are read a tile before they are wanted; the ring of codes holds K and
+            // V in turn
+            uint64_t *empty = C::kCodes ? raw_empty : is_v ? v_empty : k_empty;
+            uint64_t *full = C::kCodes ? raw_full : is_v ? v_full : k_full;
+            uint8_t *ring = C::kCodes ? sRaw : is_v ? sV : sK;
+            const CUtensorMap *map = is_v ? &tm_v : &tm_k;
+            const int stages = C::kCodes ? raw_stages : is_v ? C::kVStages : k_stages;
+            Turn t;
+            if (C::kCodes && is_v) t.next(stages);
+            int j = 0, page = read_page(0);
+            for (; j < n_kt; ++j) {
+                const int2 at = place(j, page);
+                page = read_page(j + 1);
                 const bool ok = mbar_wait(&empty[t.st], t.ph ^ 1, p.err);
-                if (!__all_sync(0xffffffffu, ok)) return false;
+                if (!__all_sync(0xffffffffu, ok)) break;
                 if (gather)
-                    gather_rows(kV ? p.v : p.k, j, to, &full[t.st]);
+                    gather_rows(is_v ? p.v : p.k, j, ring + t.st * kBytes, &full[t.st]);
                 else
-                    send(kV ? &tm_v : &tm_k, at, to, &full[t.st]);
-                t.next(C::kCodes ? raw_stages : kV ? C::kVStages : k_stages);
-                return true;
-            };
-            int page = read_page(0);
-            for (bool ok = true; ok && vj < n_kt;) {
-                const int2 at = place(kj, page);
-                page = read_page(kj + 1);
-                ok = load(std::false_type{}, kj, at);
-                kj += ok;
-                ok = ok && load(std::true_type{}, vj, at);
-                vj += ok;
+                    send(map, at, ring + t.st * kBytes, &full[t.st]);
+                t.next(stages);
+                if (C::kCodes) t.next(stages);
             }
             // No copy may still be landing when the CTA exits (normally all have been read)
-            auto landed = [&](uint64_t *full, int n, int stages) {
-                for (int j = max(0, n - stages); j < n; ++j)
-                    mbar_wait(&full[j % stages], (j / stages) & 1, p.err);
-            };
-            if constexpr (C::kCodes) {
-                landed(raw_full, kj + vj, raw_stages);
-            } else {
-                landed(k_full, kj, k_stages);
-                landed(v_full, vj, C::kVStages);
+            const int every = C::kCodes ? 2 : 1, first = C::kCodes && is_v ? 1 : 0;
+            for (int i = max(0, j - stages / every); i < j; ++i) {
+                const int n = i * every + first;
+                mbar_wait(&full[n % stages], (n / stages) & 1, p.err);
             }
-            mbar_wait(q_full, 0, p.err);
+            if (!is_v) mbar_wait(q_full, 0, p.err);
         } else if (warp == 1) {
             // ------------------------------------------------------------ products
             {
@@ -644,17 +637,33 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
                 const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
                 const uint64_t k_desc0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
                 const uint64_t v_desc0 = smem_desc_sw128(smem_u32(sV), kBN * 128, 1024);
-                // scores of Q tile qt into S a
-                auto issue_qk = [&](int a, int qt, int kst) {
+                Turn kt, vt;
+                uint64_t *k_in = C::kCodes || gather ? k_conv : k_full;
+                // Scores of Q tile qt into S a, when their K is there (wait: it may not be); done:
+                // the tile of K is not wanted again
+                auto issue_qk = [&](int a, int qt, bool wait, bool done) {
                     const uint64_t qd = q_desc + (uint64_t)((qt * C::kOffQ1) >> 4);
-                    const uint64_t kd = k_desc0 + (uint64_t)((kst * C::kTileBytes) >> 4);
+                    Turn t = kt;
 #pragma unroll
-                    for (int kk = 0; kk < HD / 16; ++kk) {
-                        const uint64_t off =
-                            (uint64_t)(((kk >> 2) * (kBM * 128) + (kk & 3) * 32) >> 4);
-                        mma_ss_if(on, tmem + a * 128, qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
+                    for (int part = 0; part < C::kKSplit; ++part) {
+                        if (wait && !mbar_wait(&k_in[t.st], t.ph, p.err)) return false;
+                        tc_fence_after();
+                        const uint64_t kd = k_desc0 + (uint64_t)((t.st * C::kKPart) >> 4);
+                        constexpr int kSteps = HD / 16 / C::kKSplit;
+#pragma unroll
+                        for (int k = 0; k < kSteps; ++k) {
+                            const int kk = part * kSteps + k;
+                            mma_ss_if(on, tmem + a * 128,
+                                      qd + (uint64_t)(((kk >> 2) * (kBM * 128) + (kk & 3) * 32) >> 4),
+                                      kd + (uint64_t)(((k >> 2) * (kBN * 128) + (k & 3) * 32) >> 4),
+                                      idesc_qk, kk > 0 ? 1u : 0u);
+                        }
+                        if (done) commit_if(on, &k_empty[t.st]);
+                        t.next(k_stages);
                     }
                     commit_if(on, &s_full[a]);
+                    if (done) kt = t;
+                    return true;
                 };
                 auto issue_pv_half = [&](int a, int vst, int hh, bool first) {
                     const uint64_t vd = v_desc0 + (uint64_t)((vst * C::kTileBytes) >> 4);
@@ -667,13 +676,6 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
                                   vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
                                   (!first || k4 > 0) ? 1u : 0u);
                     }
-                };
-                Turn kt, vt;
-                uint64_t *k_in = C::kCodes || gather ? k_conv : k_full;
-                auto k_ready = [&] { return mbar_wait(&k_in[kt.st], kt.ph, p.err); };
-                auto k_done = [&] {
-                    commit_if(on, &k_empty[kt.st]);
-                    kt.next(k_stages);
                 };
                 // the weights of a stream's jj-th key tile into its output
                 auto pv = [&](int a, int jj) {
@@ -688,46 +690,25 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
                 bool ok = mbar_wait(FMT == kBF16 ? q_full : q_conv, 0, p.err);
                 if (dual) {
                     // tile j belongs to stream j & 1
-                    for (int j = 0; ok && j < min(2, n_kt); ++j) {
-                        ok = k_ready();
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_qk(j, 0, kt.st);
-                        k_done();
-                    }
+                    for (int j = 0; ok && j < min(2, n_kt); ++j) ok = issue_qk(j, 0, true, true);
                     for (int j = 0; ok && j < n_kt; ++j) {
                         ok = mbar_wait(&v_conv[vt.st], vt.ph, p.err) && pv(j & 1, j >> 1);
                         if (!ok) break;
                         commit_if(on, &v_empty[vt.st]);
                         vt.next(C::kVStages);
-                        if (j + 2 < n_kt) {
-                            ok = k_ready();
-                            if (!ok) break;
-                            tc_fence_after();
-                            issue_qk(j & 1, 0, kt.st);
-                            k_done();
-                        }
+                        if (j + 2 < n_kt) ok = issue_qk(j & 1, 0, true, true);
                     }
                 } else {
-                    ok = ok && k_ready();
-                    if (ok) {
-                        tc_fence_after();
-                        for (int a = 0; a < n_tiles; ++a) issue_qk(a, a, kt.st);
-                        k_done();
-                    }
+                    for (int a = 0; ok && a < n_tiles; ++a)
+                        ok = issue_qk(a, a, a == 0, a == n_tiles - 1);
                     for (int j = 0; ok && j < n_kt; ++j) {
-                        const bool more = j + 1 < n_kt;
                         ok = mbar_wait(&v_conv[vt.st], vt.ph, p.err);
                         for (int a = 0; ok && a < n_tiles; ++a) {
-                            ok = pv(a, j) && (!more || a > 0 || k_ready());
+                            ok = pv(a, j);
                             if (!ok) break;
                             if (a == n_tiles - 1) commit_if(on, &v_empty[vt.st]);
-                            if (more) {
-                                tc_fence_after();
-                                issue_qk(a, a, kt.st);
-                            }
+                            if (j + 1 < n_kt) ok = issue_qk(a, a, a == 0, a == n_tiles - 1);
                         }
-                        if (more) k_done();
                         vt.next(C::kVStages);
                     }
                 }
@@ -785,54 +766,48 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
                 const uint32_t top = *reinterpret_cast<const uint32_t *>(&most);
                 if (__vcmpgeu2(top, 0x7BFF7BFFu) != 0) clean(at);
             };
-            // A tile of codes from `from` into an f16 tile.  Eight lanes read 4 pieces (16 codes)
-            // of rows r and r ^ 5 (128-byte rows, swizzled) or of two rows (64-byte ones), so
-            // that neither their loads nor their stores (pieces 2 i and 2 i + 1 of f16 rows of
-            // 128 bytes, swizzled) meet in a bank.
-            auto widen = [&](bool is_v, int tile, uint32_t from, uint32_t to) {
+            // 64 dims of a tile of codes (half hf) from `from` into f16 rows at `to`.  Eight lanes
+            // read 4 pieces (16 codes) of rows r and r ^ 5 (128-byte rows, swizzled) or of two rows
+            // (64-byte ones), so that neither their loads nor their stores (pieces 2 i and 2 i + 1
+            // of f16 rows of 128 bytes, swizzled) meet in a bank.
+            auto widen = [&](bool is_v, int tile, uint32_t from, int hf, uint32_t to) {
                 const bool all = !is_v || whole(tile);
-                constexpr int kW = kConv / 32, kRounds = HD / 64 * (kBN / 8) / kW;  // of 8 rows x 4 pieces a warp
-                constexpr int kBatch = kRounds < 4 ? kRounds : 4;  // pieces read before one is written
+                constexpr int kRounds = kBN / 8 / (kConv / 32);  // of 8 rows a warp
                 const int l = ct & 31, ph = l >> 3, second = (l >> 2) & 1, piece = l & 3;
-                auto half_of = [&](int i) { return (i * kW + (ct >> 5)) % C::kHalves; };
-                auto row_of = [&](int i) {  // unit kW i + warp: (8 rows, 64 dims)
-                    return (i * kW + (ct >> 5)) / C::kHalves * 8 +
-                           (HD == 128 ? (second ? ph ^ 5 : ph) : 2 * ph + second);
-                };
-#pragma unroll 1
-                for (int i0 = 0; i0 < kRounds; i0 += kBatch) {
-                    uint4 x[kBatch];
+                const int row0 = (ct >> 5) * 8 + (HD == 128 ? (second ? ph ^ 5 : ph) : 2 * ph + second);
+                // rows row0, row0 + 32, ..: their swizzle is the same
+                uint32_t src = HD == 128 ? from + row0 * 128 + (((hf * 4 + piece) ^ (row0 & 7)) << 4)
+                                         : from + row0 * 64 + piece * 16;
+                uint32_t dst0 = to + row0 * 128 + (((2 * piece) ^ (row0 & 7)) << 4);
+                uint32_t dst1 = to + row0 * 128 + (((2 * piece + 1) ^ (row0 & 7)) << 4);
+                // (rolled: eight pieces at once took as long, and with all warps' code long the
+                // instruction cache is short)
+                uint4 next = ld_shared_v4(src);
+#pragma unroll 2
+                for (int i = 0; i < kRounds; ++i) {
+                    const uint4 x = next;
+                    src += 32 * (HD == 128 ? 128 : 64);
+                    if (i + 1 < kRounds) next = ld_shared_v4(src);
+                    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t h[8], odd = 0;
 #pragma unroll
-                    for (int b = 0; b < kBatch; ++b) {
-                        const int row = row_of(i0 + b);
-                        x[b] = ld_shared_v4(
-                            HD == 128
-                                ? from + row * 128 + (((half_of(i0 + b) * 4 + piece) ^ (row & 7)) << 4)
-                                : from + row * 64 + piece * 16);
-                    }
+                    for (int e = 0; e < 4; ++e) codes_to_f16<FMT>(u[e], h[2 * e], h[2 * e + 1]);
+                    if (is_v) {
+                        const bool on = all || inside(tile, row0 + 32 * i);
+                        if (FMT == kE4M3) {
 #pragma unroll
-                    for (int b = 0; b < kBatch; ++b) {
-                        const int row = row_of(i0 + b);
-                        if (!all && !inside(tile, row)) x[b] = make_uint4(0u, 0u, 0u, 0u);
-                        const uint32_t u[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
-                        uint32_t h[8], odd = 0;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            codes_to_f16<FMT>(u[e], h[2 * e], h[2 * e + 1]);
-                            if (FMT == kE4M3)  // a code of NaN, 0x7F or 0xFF
-                                odd |= ((u[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                            for (int e = 0; e < 4; ++e) odd |= (u[e] & 0x7F7F7F7Fu) + 0x01010101u;
+                            odd &= 0x80808080u;  // a code of NaN, 0x7F or 0xFF
                         }
-                        if (is_v && odd != 0) {
-                            report_error(p.err, ATTN_ERR_UNSUPPORTED);
+                        if (odd != 0 || !on) {
+                            if (on) report_error(p.err, ATTN_ERR_UNSUPPORTED);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) h[e] = drop_nan(h[e]);
+                            for (int e = 0; e < 8; ++e) h[e] = on ? drop_nan(h[e]) : 0u;
                         }
-                        const uint32_t base = to + half_of(i0 + b) * (kBN * 128) + row * 128;
-                        st_shared_v4(base + (((2 * piece) ^ (row & 7)) << 4),
-                                     make_uint4(h[0], h[1], h[2], h[3]));
-                        st_shared_v4(base + (((2 * piece + 1) ^ (row & 7)) << 4),
-                                     make_uint4(h[4], h[5], h[6], h[7]));
                     }
+                    st_shared_v4(dst0, make_uint4(h[0], h[1], h[2], h[3]));
+                    st_shared_v4(dst1, make_uint4(h[4], h[5], h[6], h[7]));
+                    dst0 += 32 * 128, dst1 += 32 * 128;
                 }
             };
             Turn kt, vt, rt;
@@ -841,18 +816,24 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
                 const bool is_v = warp >= 8;
                 const int stages = is_v ? C::kVStages : k_stages;
                 uint64_t *empty = is_v ? v_empty : k_empty, *done = is_v ? v_conv : k_conv;
-                const uint32_t to = smem_u32(is_v ? sV : sK);
+                const uint32_t ring = smem_u32(is_v ? sV : sK);
                 if (is_v) rt.next(raw_stages);  // (the ring holds K and V in turn)
-                for (int j = 0; j < w.n_kt; ++j) {
-                    ok = mbar_wait(&raw_full[rt.st], rt.ph, p.err) &&
-                         mbar_wait(&empty[vt.st], vt.ph ^ 1, p.err);
-                    if (!ok) break;
-                    widen(is_v, w.kt0 + j, smem_u32(sRaw + rt.st * C::kRawBytes),
-                          to + vt.st * C::kTileBytes);
-                    fence_proxy_async_smem();
-                    mbar_arrive(&done[vt.st]);
+                for (int j = 0; ok && j < w.n_kt; ++j) {
+                    ok = mbar_wait(&raw_full[rt.st], rt.ph, p.err);
+                    // V by tiles, K by halves
+#pragma unroll 1
+                    for (int hf = 0; ok && hf < C::kHalves; ++hf) {
+                        if (!is_v || hf == 0) ok = mbar_wait(&empty[vt.st], vt.ph ^ 1, p.err);
+                        if (!ok) break;
+                        const uint32_t at = is_v ? vt.st * C::kTileBytes + hf * (kBN * 128)
+                                                 : vt.st * C::kKPart;
+                        widen(is_v, w.kt0 + j, smem_u32(sRaw + rt.st * C::kRawBytes), hf, ring + at);
+                        if (is_v && hf + 1 < C::kHalves) continue;
+                        fence_proxy_async_smem();
+                        mbar_arrive(&done[vt.st]);
+                        vt.next(stages);
+                    }
                     mbar_arrive(&raw_empty[rt.st]);
-                    vt.next(stages);
                     rt.next(raw_stages);
                     rt.next(raw_stages);
                 }
