@@ -17,7 +17,9 @@
 // KV head, pair) fill the SMs once.  Where a group has one tile only, the CTA's two softmax
 // warpgroups take every other key tile of it each (with a state each): a lone tile's chain
 // product - softmax - product would else leave the tensor cores and the softmax waiting for
-// one another.
+// one another (four groups of 30 requests over E4M3 61.3 us, with lone tiles 70; 32 x 4 rows over
+// INT8 32.8 and 38.2; where few key tiles are left for an SM it costs a part more, two requests over
+// 512 keys 15.6 and 14.8).
 //   warps 0, 2   load K and V: TMA boxes of whole runs of keys (a page, or 128 of a linear cache),
 //                one a lane; where pages are no multiple of 8 keys, 16-byte cp.async by row
 //   warp 1       one thread issues tcgen05.mma: S = Q K^T, O += P V (f16, P from TMEM)
@@ -28,6 +30,14 @@
 //                over S in TMEM
 // The plan is made on the device from lengths, rows and positions, by every CTA for itself
 // (a captured graph follows them); CTAs are persistent for batches of more pairs than SMs.
+//
+// What bounds it.  A pair of tiles (head_dim 128, bf16) takes 1.6 us a key tile, of which its products
+// are 1.0: the softmax (S read from TMEM twice, a chain of ~2,100 cycles a tile) and the loads' issue
+// run beside them, at 45% of the issue slots; 256 requests over 32,768 shared keys, 32/8 heads: 155 us,
+// 890 TFLOP/s.  A lone tile takes 1.3 us (its K and V are 7.6 TB/s over all SMs), over codes 1.7 to 2.0:
+// four warps widen K and four V, 170 to 300 cycles for each 16 codes of a thread, beside the softmax
+// warps.  A step over few keys is a chain: the plan 3 us, the first tiles, the merge 3 us (two
+// requests over 512 keys 15.6 us).
 //
 // Scales of 8-bit caches leave the products as in attend.cu: K's multiplies the scores, V's
 // enters the weights' exponent, l sums w / vs.  Weights are held times 2^7 (those down to
@@ -1173,7 +1183,8 @@ struct MergeParams {
 
 // A row of the output from its parts: those of the shared keys, then those of its own.
 // SPLIT warps a row, each every SPLIT-th part, a lane HD / 32 dims; the sums of 32 parts come in one
-// load, the parts' outputs then wait for nothing.
+// load, the parts' outputs then wait for nothing.  Bound by those two round trips behind the last
+// of both launches (~3 us; 8.5 us cold for 2,048 rows of 128 dims, 5.8 MB read).
 template <int HD, int SPLIT>
 __global__ void __launch_bounds__(256, SPLIT == 1 ? 4 : 2) shared_merge_kernel(const MergeParams p) {
     constexpr int V = HD / 32, kRows = 8 / SPLIT;
@@ -1363,7 +1374,9 @@ int plan_shared(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
 // each that is left, so that the two parts run side by side.  Of the pieces that a unit (KV head,
 // pair of tiles) can be cut into, as many as end soonest by the host's bounds (lengths are known on
 // the device only): a piece takes 9 us and 1.65 a pair of tiles and 128 keys (1.2 a single tile; over
-// codes 2.4 and 1.6), an SM reads 36 bytes (28) of own keys a nanosecond.
+// codes 2.4 and 1.6), an SM reads 36 bytes (28) of own keys a nanosecond.  On every SM first, the own
+// keys after: 64 requests over 4,096 and 64 to 1,024 keys 67.8 us, side by side 47.8; 16 over 14,449
+// and up to 2,000 43.2 and 32.2; four E4M3 groups 68.9 and 61.3; two short requests the same.
 static int prefix_sms(int batch, int q_rows, int group, int n_kv_heads, int head_dim, int esize,
                       int max_seq_len, int max_prefix_len, int own_units) {
     const int sms = device_sm_count(), rt = shr::kBM / group;
@@ -1504,7 +1517,9 @@ int launch_shared(const SharedPlan &plan, const void *q, const attn_kv_cache *ca
     m.n_q_heads = n_q_heads;
     m.n_kv_heads = n_kv_heads;
     m.group = p.group;
-    // Four warps a row where rows lie in many parts (if all requests are one group) and are few
+    // Four warps a row where rows lie in many parts (if all requests are one group) and are few:
+    // 16 requests of 28/4 heads over 14,449 keys 32.2 us, with one warp 42.4; 64 of 32/8 over 4,096
+    // 47.8 with one, 55.8 with four; 256 over 32,768 155 and 188
     const int64_t pairs = ((int64_t)batch * q_rows + 2 * p.rt - 1) / (2 * p.rt);
     const bool split = p.sms > 8 * n_kv_heads * pairs &&
                        (int64_t)batch * q_rows * n_q_heads <= (int64_t)p.sms * 16;
