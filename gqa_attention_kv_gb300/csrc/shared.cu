@@ -281,7 +281,7 @@ __device__ int make_plan(const Params &p, int32_t *mem, int want, bool tables, P
             const uint32_t fits = __ballot_sync(0xffffffffu, n <= p.sms);
             most = fits != 0 ? __shfl_sync(0xffffffffu, s, __ffs(fits) - 1) : 0;
         }
-        int at = 0, row = 0;  // pieces and rows of ws_o before this round's groups
+        int at = 0, row = 0;  // pieces and rows of ws_o before these groups
         for (int g0 = 0; g0 < groups; g0 += 32) {
             const int g = g0 + lane;
             int n = 0, rows = 0, cut = 0, pairs = 0, tiles = 0, n_pos = 0;
