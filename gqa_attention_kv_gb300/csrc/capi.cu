@@ -449,8 +449,9 @@ namespace {
 
 // What shared prefixes ask beyond check_decode_shape.
 int check_shared(const attn_kv_cache *cache, int batch, int n_q_heads, int n_kv_heads,
-                 int max_prefix_len) {
-    if (max_prefix_len < 0) return ATTN_ERR_SHAPE;
+                 int max_seq_len, int max_prefix_len) {
+    // (the last key tile's end is an int too)
+    if (max_prefix_len < 0 || max_seq_len > INT32_MAX - 256) return ATTN_ERR_SHAPE;
     if (cache->kind == ATTN_CACHE_RING) return ATTN_ERR_UNSUPPORTED;
     if (batch > 4096 || n_q_heads / n_kv_heads > 128) return ATTN_ERR_UNSUPPORTED;
     if (cache->num_slots > INT32_MAX / n_kv_heads) return ATTN_ERR_UNSUPPORTED;
@@ -477,7 +478,8 @@ int check_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
         if (reinterpret_cast<uintptr_t>(f) & 3u) return ATTN_ERR_ALIGN;
     const int64_t q_row = (int64_t)n_q_heads * head_dim, k_row = (int64_t)n_kv_heads * head_dim;
     constexpr int64_t kFar = int64_t(1) << 30;  // (n of them fit 63 bits)
-    if (n > 1 && (q_stride > kFar || k_stride > kFar || (v && v_stride > kFar))) return ATTN_ERR_SHAPE;
+    if (n > 1 && (q_stride > kFar || k_stride > kFar || (v && v_stride > kFar)))
+        return ATTN_ERR_SHAPE;
     if (n > 1 && (q_stride < q_row || k_stride < k_row || q_stride % 8 || k_stride % 8))
         return ATTN_ERR_SHAPE;
     if (n > 1 && v && (v_stride < k_row || v_stride % 8)) return ATTN_ERR_SHAPE;
@@ -524,7 +526,7 @@ size_t attn_decode_shared_workspace_size(const attn_kv_cache *cache, int batch, 
     gqa::SharedPlan plan;
     if (check_decode_shape(cache, batch, q_rows, n_q_heads, n_kv_heads, head_dim, max_seq_len,
                            window) != ATTN_OK ||
-        check_shared(cache, batch, n_q_heads, n_kv_heads, max_prefix_len) != ATTN_OK)
+        check_shared(cache, batch, n_q_heads, n_kv_heads, max_seq_len, max_prefix_len) != ATTN_OK)
         return (size_t)-1;
     if (batch == 0) return 0;
     if (gqa::plan_shared(cache, batch, q_rows, n_q_heads, n_kv_heads, head_dim, max_seq_len,
@@ -541,7 +543,8 @@ int attn_decode_shared(const void *q, const attn_kv_cache *cache, int n_rows,
                        size_t workspace_bytes, int32_t *err_word, attn_stream_t stream) {
     int rc = check_decode_shape(cache, batch, q_rows, n_q_heads, n_kv_heads, head_dim,
                                 max_seq_len, window);
-    if (rc == ATTN_OK) rc = check_shared(cache, batch, n_q_heads, n_kv_heads, max_prefix_len);
+    if (rc == ATTN_OK)
+        rc = check_shared(cache, batch, n_q_heads, n_kv_heads, max_seq_len, max_prefix_len);
     if (rc != ATTN_OK) return rc;
     gqa::DecodePlan decode;
     rc = gqa::validate_decode(q, cache, seq_lens, positions, batch, q_rows, max_seq_len, window,

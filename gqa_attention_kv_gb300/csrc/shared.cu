@@ -1159,7 +1159,7 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
             }
         }
     }
-    __syncwarp();  // the lanes of the product's warp wait here for lane 0
+    __syncwarp();  // (lanes that elected ones of their warp went ahead of)
     if (want + (int)gridDim.x >= total) break;
     tc_fence_before();  // another piece: everything has been read
     __syncthreads();

@@ -595,7 +595,7 @@ int attn_decode_sinks(const void *q, const attn_kv_cache *cache, const int32_t *
  * Which keys a row attends is attn_decode's rule (seq_lens counts the prefix).
  * LINEAR and PAGED caches of every dtype and layout; RING is not supported.
  * n_q_heads / n_kv_heads at most 128, batch at most 4,096, num_slots * n_kv_heads
- * below 2^31.
+ * below 2^31, max_seq_len below 2^31 - 256.
  *   The shared keys' products run on tensor cores: over a bf16 cache Q K^T takes
  *   q and k as bf16, over an 8-bit one q is rounded to f16 (a magnitude of 65520
  *   or more is reported as ATTN_ERR_UNSUPPORTED); softmax weights are rounded

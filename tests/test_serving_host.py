@@ -123,7 +123,7 @@ def test_shared_refusals(lib):  # noqa: F811
     plain = cache(dtype=gq.ATTN_KV_BF16)
     for bad in (dict(prows=None), dict(plens=None), dict(q=None), dict(out=None), dict(ws=None)):
         assert shared_rc(lib, plain, **bad) == gq.ATTN_ERR_NULL, bad
-    for bad in (dict(P=-1), dict(rows=1), dict(rows=3), dict(B=-1), dict(R=0), dict(L=0),
+    for bad in (dict(P=-1), dict(rows=1), dict(rows=3), dict(L=2 ** 31 - 256), dict(B=-1), dict(R=0), dict(L=0),
                 dict(scale=0.0), dict(scale=math.nan), dict(Hq=30), dict(out=1 << 24),
                 dict(out=(1 << 24) + 16)):
         assert shared_rc(lib, plain, **bad) == gq.ATTN_ERR_SHAPE, bad
