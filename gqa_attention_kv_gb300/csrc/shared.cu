@@ -751,7 +751,8 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
             auto v_in_place = [&](int tile, uint32_t at) {
                 const bool all = whole(tile);
                 __half2 most = __half2half2(__ushort_as_half(0));  // largest magnitudes
-                constexpr int kBatch = 8;  // pieces read before one is written
+                constexpr int kBatch = 4;  // pieces read before one is written (eight: 1% slower)
+#pragma unroll 1
                 for (int i0 = ct; i0 < C::kTileBytes / 16; i0 += kConv * kBatch) {
                     uint4 x[kBatch];
 #pragma unroll
