@@ -356,6 +356,7 @@ struct __align__(16) Smem {
     Entry entry[ENTRIES];
     int prefix[ENTRIES + 1];
     int last_part, longest;
+    int share_at[2];  // the share that the CTA works on, in turn
     __device__ __forceinline__ float *out_row(int warp, int row) {
         return reinterpret_cast<float *>(buf[warp]) + row * G::kOStride;
     }
@@ -498,12 +499,14 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, HD, MT, HG>::CTAS)
         }
     }
 
-    for (;;) {
+    for (int turn = 0;; turn ^= 1) {
     int piece = blockIdx.x;
     if (p.next != nullptr) {
-        if (threadIdx.x == 0) sm.last_part = after;
+        // Two places in turn: a share that lies in a gap passes no other barrier, so one of them is
+        // only written again behind the next round's, which follows every thread's read of it
+        if (threadIdx.x == 0) sm.share_at[turn] = after;
         __syncthreads();
-        piece = sm.last_part;
+        piece = sm.share_at[turn];
         if ((int64_t)piece * share >= total) break;
         if (threadIdx.x == 0) after = atomicAdd(p.next, 1);  // (under way meanwhile)
     }
