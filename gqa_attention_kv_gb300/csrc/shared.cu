@@ -41,9 +41,14 @@
 //
 // Scales of 8-bit caches leave the products as in attend.cu: K's multiplies the scores, V's
 // enters the weights' exponent, l sums w / vs.  Weights are held times 2^7 (those down to
-// 2^-21 of the largest keep f16's 11 bits).  A CTA leaves O normalised by the plain sum of its
-// weights (at most the largest |v| or code, so f16 holds it: 2^-11, a quarter of the output's
-// bf16 half step), and the logarithms of both sums.
+// 2^-21 of the largest keep f16's 11 bits).  Values of a bf16 cache have such a scale too, or f16
+// would lose them from 2^-14 on: those of a tile are multiplied with a power of two (exactly) and the
+// weights of its keys divided by it.  The power of the tile before is tried, 1 at first; where the
+// tile's largest value, which the conversion finds by the way, leaves 2^-4 .. 2^15 by it, the tile is
+// read and converted again with its own (256 requests over 32,768 keys 158 us; with a first round
+// over every tile 165, without powers of two 152).  A CTA leaves O normalised by the plain sum of its
+// weights and held times a power of two of its row, in f16 (2^-11, a quarter of the output's bf16
+// half step), and the logarithms of both sums.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -67,6 +72,9 @@ constexpr float kRescaleLog2 = 8.0f;    // the reference maximum moves past this
 constexpr float kWeightLog2 = 7.0f;     // weights are held times 2^7: at most 2^15
 constexpr float kScoreTop = 0x1p24f;    // larger scores are reported (as in attend.cu)
 constexpr float kFactorTop = 0x1p90f;
+// A tile's values are held times 2^80 at most: 128 weights of 2^15, times that, over 2^24 tiles are
+// a finite sum; keys whose weights vanish beside another tile's have less than 2^-53 of its own.
+constexpr int kShiftTop = 80;
 constexpr float kScaleFloor = 0x1p-64f; // the smallest scale
 constexpr float kPartWeight = 0x1p-12f;
 constexpr float kSmallest = 0x1p-149f;
@@ -134,7 +142,8 @@ struct Params {
     KvPlace place;
     float scale_log2;
     int4 *ws_rows;   // [batch * q_rows]: first row of ws_o for KV head 0, rows a part, parts
-    float2 *ws_lse;  // per row: log2 of the sum of weights, and of weights over scales
+    // per row: log2 of the sum of weights (by what ws_o is held times), and of weights over scales
+    float2 *ws_lse;
     uint16_t *ws_o;  // per row: HD f16
     int32_t *ws_next;  // [launches]: attend.cu's counters of shares, set to 0 here
     int launches;
@@ -422,6 +431,13 @@ __device__ __forceinline__ uint32_t drop_nan(uint32_t w) {
     return w;
 }
 
+// bf16 NaN become 0 in each half.
+__device__ __forceinline__ uint32_t drop_bf16_nan(uint32_t w) {
+    if ((w & 0x7FFFu) > 0x7F80u) w &= 0xFFFF0000u;
+    if ((w & 0x7FFF0000u) > 0x7F800000u) w &= 0x0000FFFFu;
+    return w;
+}
+
 template <int FMT, int HD>
 __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -450,6 +466,9 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kNumBars);
     __shared__ int s_bad;  // a page of the piece's keys is not in the pool
     __shared__ Piece w;    // (its fields are read where they are used: registers are short)
+    // bf16: log2 of what a stage of V is multiplied with, and that
+    __shared__ float2 s_by[C::kVStages];
+    __shared__ uint32_t s_top[2][kConv / 32];  // ... largest magnitudes, by warp
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.group, R = p.q_rows, used = p.rt * G;
@@ -737,21 +756,40 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
             auto whole = [&](int tile) {
                 return tile * kBN >= w.lo && tile * kBN + kBN <= w.hi;
             };
-            // f16 NaN among this thread's pieces of a V tile become 0
-            auto clean = [&](uint32_t at) {
-                report_error(p.err, ATTN_ERR_UNSUPPORTED);
-                for (int i = ct; i < C::kTileBytes / 16; i += kConv) {
-                    uint4 x = ld_shared_v4(at + i * 16);
-                    x.x = drop_nan(x.x), x.y = drop_nan(x.y);
-                    x.z = drop_nan(x.z), x.w = drop_nan(x.w);
-                    st_shared_v4(at + i * 16, x);
-                }
+            // The largest of the four warps' values (two tables in turn: one is written again behind
+            // the next barrier)
+            int table_at = 0;
+            auto largest = [&](__nv_bfloat162 most) {
+                const uint32_t two = *reinterpret_cast<const uint32_t *>(&most);
+                const uint32_t mine = __reduce_max_sync(0xffffffffu, max(two >> 16, two & 0xFFFFu));
+                uint32_t *to = s_top[table_at];
+                table_at ^= 1;
+                if (lane == 0) to[ct >> 5] = mine;
+                asm volatile("bar.sync 4, %0;" ::"n"(kConv) : "memory");
+                uint32_t top = to[0];
+#pragma unroll
+                for (int i = 1; i < kConv / 32; ++i) top = max(top, to[i]);
+                return top;
             };
-            // a tile of bf16 V in place
-            auto v_in_place = [&](int tile, uint32_t at) {
+            const __nv_bfloat162 zero2 = __bfloat162bfloat162(__ushort_as_bfloat16(0));
+            auto size_of = [](__nv_bfloat162 most, uint32_t u) {
+                return __hmax2_nan(most, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&u)));
+            };
+            auto power = [](int shift) {
+                return __bfloat162bfloat162(
+                    __ushort_as_bfloat16((unsigned short)((127 + shift) << 7)));
+            };
+            auto to_f16 = [](uint32_t u, __nv_bfloat162 by) {
+                const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&u), by);
+                return bf16x2_to_f16x2_sat(*reinterpret_cast<const uint32_t *>(&y));
+            };
+            // A tile of bf16 V in place, to f16 times 2^shift; returns the largest |x| of its keys in
+            // the group's range, as a bf16 pattern
+            auto v_in_place = [&](int tile, uint32_t at, auto scaled, int shift) {
                 const bool all = whole(tile);
-                __half2 most = __half2half2(__ushort_as_half(0));  // largest magnitudes
                 constexpr int kBatch = 4;  // pieces read before one is written (eight: 1% slower)
+                __nv_bfloat162 most = zero2;
+                const __nv_bfloat162 by = power(shift);
 #pragma unroll 1
                 for (int i0 = ct; i0 < C::kTileBytes / 16; i0 += kConv * kBatch) {
                     uint4 x[kBatch];
@@ -766,16 +804,52 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
                         uint32_t *u = &x[b].x;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            u[e] = bf16x2_to_f16x2_sat(u[e]);
-                            most = __hmax2_nan(
-                                most, __habs2(*reinterpret_cast<const __half2 *>(&u[e])));
+                            most = size_of(most, u[e]);
+                            u[e] = decltype(scaled)::value ? to_f16(u[e], by)
+                                                           : bf16x2_to_f16x2_sat(u[e]);
                         }
                         st_shared_v4(at + i * 16, x[b]);
                     }
                 }
-                // 65504 itself is no bf16: only saturated values and NaN reach it
-                const uint32_t top = *reinterpret_cast<const uint32_t *>(&most);
-                if (__vcmpgeu2(top, 0x7BFF7BFFu) != 0) clean(at);
+                return largest(most);
+            };
+            // The same from the cache, where the power of two was not right (shift: the one to come),
+            // NaN as zeros; returns the shift taken
+            auto v_again = [&](int tile, uint32_t at) {
+                auto piece = [&](int i) {  // piece i of the tile in shared memory (swizzled)
+                    const int r = (i >> 3) & (kBN - 1), t = tile * kBN + r;
+                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                    if (!inside(tile, r)) return x;
+                    int64_t slot = (int64_t)w.prow * p.slots_per_seq + t;
+                    if (p.paged) {
+                        const int page = page_of(t);
+                        if ((unsigned)page >= (unsigned)p.num_pages) return x;
+                        slot = (int64_t)page * p.block_size + (t - block_of(t) * p.block_size);
+                    }
+                    x = __ldg(reinterpret_cast<const uint4 *>(
+                        p.v + p.place.head_offset(slot, w.kvh) + (i / (kBN * 8)) * 128 +
+                        (((i ^ r) & 7) << 4)));
+                    x.x = drop_bf16_nan(x.x), x.y = drop_bf16_nan(x.y);
+                    x.z = drop_bf16_nan(x.z), x.w = drop_bf16_nan(x.w);
+                    return x;
+                };
+                __nv_bfloat162 most = zero2;
+#pragma unroll 1
+                for (int i = ct; i < C::kTileBytes / 16; i += kConv) {
+                    const uint4 x = piece(i);
+                    most = size_of(size_of(most, x.x), x.y);
+                    most = size_of(size_of(most, x.z), x.w);
+                }
+                // the largest to 2^9 .. 2^10: tiles of 2^-13 to 2^5 times its size come in between
+                const int shift = min(max(136 - (int)(largest(most) >> 7), 0), kShiftTop);
+                const __nv_bfloat162 by = power(shift);
+#pragma unroll 1
+                for (int i = ct; i < C::kTileBytes / 16; i += kConv) {
+                    const uint4 x = piece(i);
+                    st_shared_v4(at + i * 16, make_uint4(to_f16(x.x, by), to_f16(x.y, by),
+                                                         to_f16(x.z, by), to_f16(x.w, by)));
+                }
+                return shift;
             };
             // 64 dims of a tile of codes (half hf) from `from` into f16 rows at `to`.  Eight lanes
             // read 4 pieces (16 codes) of rows r and r ^ 5 (128-byte rows, swizzled) or of two rows
@@ -823,6 +897,7 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
             };
             Turn kt, vt, rt;
             bool ok = true;
+            int shift = 0;  // log2 of what values are multiplied with
             if constexpr (C::kCodes) {
                 const bool is_v = warp >= 8;
                 const int stages = is_v ? C::kVStages : k_stages;
@@ -854,8 +929,7 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
                         // K copied by cp.async: written again, so that this thread's fence
                         // covers what the tensor cores read
                         const uint32_t at = smem_u32(sK + kt.st * C::kTileBytes);
-                        ok = mbar_wait(&k_full[kt.st], kt.ph, p.err);
-                        if (!ok) break;
+                        if (ok) ok = mbar_wait(&k_full[kt.st], kt.ph, p.err);
 #pragma unroll 4
                         for (int i = ct; i < C::kTileBytes / 16; i += kConv)
                             st_shared_v4(at + i * 16, ld_shared_v4(at + i * 16));
@@ -863,9 +937,26 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
                         mbar_arrive(&k_conv[kt.st]);
                         kt.next(k_stages);
                     }
-                    ok = mbar_wait(&v_full[vt.st], vt.ph, p.err);
-                    if (!ok) break;
-                    v_in_place(w.kt0 + j, smem_u32(sV + vt.st * C::kTileBytes));
+                    // (no way out where a wait ran out: the four warps meet at a barrier)
+                    if (ok) ok = mbar_wait(&v_full[vt.st], vt.ph, p.err);
+                    const uint32_t at = smem_u32(sV + vt.st * C::kTileBytes);
+                    const int tile = w.kt0 + j;
+                    const uint32_t top = shift == 0
+                                             ? v_in_place(tile, at, std::false_type{}, 0)
+                                             : v_in_place(tile, at, std::true_type{}, shift);
+                    // f16 holds 65504 at most, and of what is 2^-4 at least all that counts: a
+                    // value below 2^-14 is off by 2^-21 of the largest at most
+                    const int size = (int)(top >> 7) + shift - 127;
+                    if (top >= 0x4780u || size > (shift == 0 ? 15 : 14) ||
+                        (top != 0 && size < -4 && shift < kShiftTop)) {
+                        if (top >= 0x4780u) report_error(p.err, ATTN_ERR_UNSUPPORTED);
+                        shift = v_again(tile, at);
+                    }
+                    // (zeros weigh nothing beside any other tile)
+                    if (ct == 0) {
+                        const int of = top == 0 ? kShiftTop : shift;
+                        s_by[vt.st] = make_float2((float)of, __int_as_float((127 + of) << 23));
+                    }
                     fence_proxy_async_smem();
                     mbar_arrive(&v_conv[vt.st]);
                     vt.next(C::kVStages);
@@ -934,6 +1025,8 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
         bool ok = true;
         // this warpgroup's key tiles
         const int j0 = dual ? a : 0, step = dual ? 2 : 1;
+        Turn vt;  // ... and their stages of V
+        if (j0 > 0) vt.next(C::kVStages);
         const int mine = a < n_tiles || dual ? (w.n_kt - j0 + step - 1) / step : 0;
         // scales of the 16 keys 16 (lane % 8) .. of a tile, read a tile ahead
         float next_k = 1.f, next_v = 1.f;
@@ -966,7 +1059,20 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
                 }
                 read_scales(j + step);
             }
-            ok = __all_sync(0xffffffffu, mbar_wait(&s_full[a], jj & 1, p.err));
+            // bf16: log2 of what the tile's values were multiplied with, and that (the stage is not
+            // converted again before this warpgroup's weights are there).  Where it is waited for
+            // shows: pairs before S (256 requests over 32,768 keys 158 us, behind the maximum 166),
+            // lone tiles behind the maximum (two requests 16.0 us, before S 16.7)
+            float2 by = make_float2(0.f, 1.f);
+            auto wait_v = [&] {
+                if (!mbar_wait(&v_conv[vt.st], vt.ph, p.err)) return false;
+                by = s_by[vt.st];
+                vt.next(C::kVStages);
+                if (dual) vt.next(C::kVStages);
+                return true;
+            };
+            if (FMT == kBF16 && !dual) ok = wait_v();
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[a], jj & 1, p.err));
             if (!ok) break;
             tc_fence_after();
             const int key0 = (w.kt0 + j) * kBN;
@@ -1038,8 +1144,12 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
                 top(s0, c0);
                 top(s1, c0 + 32);
             }
+            if constexpr (FMT == kBF16) {
+                if (dual) ok = __all_sync(0xffffffffu, wait_v());
+                if (!ok) break;
+                mx = fmaf(mx, sl2, -by.x);
+            }
             tmem_ld_32x32b_x32(s_tmem, u0);  // (under way meanwhile)
-            if constexpr (FMT == kBF16) mx *= sl2;
             float alpha = 1.f;
             if (mx > m_run + kRescaleLog2 || m_run == -INFINITY) {
                 const float m_new = mx == -INFINITY ? m_run : mx;
@@ -1063,7 +1173,7 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
             // weights of columns c0 .. c0 + 31: over their own S columns, 32 keys in 16
             auto weigh = [&](float(&s)[32], int c0) {
                 uint32_t pk[16];
-                float sum0 = 0.f, sum1 = 0.f, f = sl2, shift = -m_w;
+                float sum0 = 0.f, sum1 = 0.f, f = sl2, shift = -m_w - by.x;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     if (FMT != kBF16 && (e & 7) == 0) {
@@ -1100,7 +1210,7 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
                 tc_fence_before();
                 mbar_arrive(&p_full[a * 2 + c0 / 64]);
             }
-            l_run = l_run * alpha + (FMT == kBF16 ? sum : over);
+            l_run = l_run * alpha + (FMT == kBF16 ? sum * by.y : over);
             w_run = w_run * alpha + sum;
         }
         if (m_run != -INFINITY && !(fabsf(m_run) < kScoreTop))
@@ -1110,7 +1220,7 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
         __syncwarp();
         tc_fence_after();
         const bool any = !(w_run == 0.f);  // a key was seen (or a NaN met)
-        const float norm = any ? 1.f / w_run : 0.f;
+        float norm = any ? 1.f / w_run : 0.f;
         const int part = dual ? 2 * w.split + a : w.split;
         const int64_t row0 = (int64_t)w.base +
                              ((int64_t)w.kvh * w.parts + part) * ((int64_t)w.n_pos * G) +
@@ -1120,9 +1230,8 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
             // product has read them) as swizzled 128-byte rows of 64 dims, and out in whole
             // lines: a row a thread would write into 32 lines an instruction
             uint8_t *stage = a == 0 ? sK : sV;
-#pragma unroll 1
-            for (int c0 = 0; c0 < HD; c0 += 32) {
-                uint32_t orow[32];
+            uint32_t orow[32];
+            auto read_o = [&](int c0) {
                 if (mine > 0) {  // warpgroup-uniform: O was accumulated into
                     tmem_ld_32x32b_x32(o_tmem + c0, orow);
                     tmem_wait_ld();
@@ -1131,6 +1240,22 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) orow[e] = 0u;
                 }
+            };
+            // The row's largest output to 2^12 .. 2^13 (f16 ends at 2^16)
+            float most = 0.f;
+#pragma unroll 1
+            for (int c0 = 0; c0 < HD; c0 += 32) {
+                read_o(c0);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) most = fmaxf(most, fabsf(__uint_as_float(orow[e])));
+            }
+            const int held = most > 0.f && isfinite(most * norm)
+                                 ? min(max(139 - (int)(__float_as_uint(most * norm) >> 23), -30), 40)
+                                 : 0;
+            norm *= __int_as_float((127 + held) << 23);
+#pragma unroll 1
+            for (int c0 = 0; c0 < HD; c0 += 32) {
+                read_o(c0);
                 auto v = [&](int e) { return any ? __uint_as_float(orow[e]) * norm : 0.f; };
                 const uint32_t base = smem_u32(stage + (c0 / 64) * (kBM * 128) + row * 128);
 #pragma unroll
@@ -1145,7 +1270,8 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
             }
             if (live) {
                 const float at = (m_run == -INFINITY ? 0.f : m_run) - kWeightLog2;
-                p.ws_lse[row0 + row] = any ? make_float2(at + __log2f(w_run), at + __log2f(l_run))
+                p.ws_lse[row0 + row] = any ? make_float2(at - (float)held + __log2f(w_run),
+                                                         at + __log2f(l_run))
                                            : make_float2(-INFINITY, -INFINITY);
             }
             if (a == 0)

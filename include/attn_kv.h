@@ -597,15 +597,17 @@ int attn_decode_sinks(const void *q, const attn_kv_cache *cache, const int32_t *
  * n_q_heads / n_kv_heads at most 128, batch at most 4,096, num_slots * n_kv_heads
  * below 2^31, max_seq_len below 2^31 - 256.
  *   The shared keys' products run on tensor cores: over a bf16 cache Q K^T takes
- *   q and k as bf16, over an 8-bit one q is rounded to f16 (a magnitude of 65520
- *   or more is reported as ATTN_ERR_UNSUPPORTED); softmax weights are rounded
- *   once to f16, and a shared value of a bf16 cache that has no f16 (a magnitude
- *   of 65520 or more, an infinity) is saturated to 65504, a NaN of any cache
- *   taken as 0, with ATTN_ERR_UNSUPPORTED in *err_word.  Scores, scale * q . key
- *   * log2(e), have to stay below 2^24 in magnitude, or ATTN_ERR_UNSUPPORTED is
- *   reported and the row is unspecified.  Keys that a row does not attend do not
- *   reach it, whatever they hold; its own keys and values are read as
- *   attn_decode_sinks reads them.
+ *   q and k as bf16, over an 8-bit one q is rounded to f16 (below 2^-14 in steps of
+ *   2^-24; a magnitude of 65520 or more is reported as ATTN_ERR_UNSUPPORTED).
+ *   Softmax weights are rounded once to f16, and so are the values of a bf16 cache,
+ *   times a power of two: what a value loses is at most 2^-21 of the largest of the
+ *   128 shared keys it is multiplied with (2^-105 where all are smaller than 2^-84).
+ *   A magnitude of 65520 or more is saturated to 65504, a NaN of any cache taken as 0,
+ *   with ATTN_ERR_UNSUPPORTED in *err_word.  Scores, scale * q . key * log2(e), have
+ *   to stay below 2^24 in magnitude, or ATTN_ERR_UNSUPPORTED is reported and the row is
+ *   unspecified (one that overflows to -infinity has weight 0).  Keys that a row does
+ *   not attend do not reach it, whatever they hold, but for that loss of values beside
+ *   them; its own keys and values are read as attn_decode_sinks reads them.
  *   workspace: at least attn_decode_shared_workspace_size(...) bytes (which
  *   returns (size_t)-1 for arguments this call would reject), 16-byte aligned,
  *   zero-filled before its first use; one workspace may serve this call,

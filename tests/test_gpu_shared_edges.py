@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import gqa_attention_kv_gb300 as gq
+import kv_reference as ref
 from test_gpu_shared import DEV, Case, one_group
 
 pytestmark = pytest.mark.gpu
@@ -21,3 +22,123 @@ def test_shares_that_lie_in_gaps(fmt, n, H, D):
     ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
     for _ in range(50):
         assert torch.equal(c.run(workspace=ws), want)
+
+
+def weights(c, b, r, h, scale):
+    """Softmax weights of the keys that a row attends (a head of KV head h's group), and their
+    slots."""
+    n, pos = int(c.lens[b]), int(c.pos[b * c.R + r])
+    slots = torch.tensor([c.slot(b, t) for t in range(min(n, pos + 1))
+                          if not c.window or pos - t < c.window])
+    G = c.q.shape[2] // c.H
+    s = scale * (c.q[b, r, h * G:(h + 1) * G].double() @ c.kd[slots, h].T)
+    return torch.softmax(s, -1), slots
+
+
+def check_spread(c):
+    """A softmax over n spread keys is about sqrt(n) smaller than the sum of |p v|, so a bound by
+    that sum does not see what an output's own magnitude loses.  Bounds: the output's rounding,
+    2^-8 of it; 2^-13 of sum |p v| for scores and sums in 32 bits; weights, each off by at most
+    2^-11 of itself by itself, by Hoeffding within 7 2^-11 sqrt(sum p^2 v^2) but for one in 10^10;
+    and the parts' outputs, whose rounding is 2^-11 of sums of p v over the part, of the same
+    size again (values of either sign)."""
+    scale = c.D ** -0.5
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = c.run(err=err).double().cpu()
+    assert int(err) == 0
+    want, mass = c.want()
+    G = c.q.shape[2] // c.H
+    for b in range(c.q.shape[0]):
+        for r in range(c.R):
+            for h in range(c.H):
+                p, slots = weights(c, b, r, h, scale)
+                size = (p ** 2 @ c.vd[slots, h] ** 2).sqrt()
+                at = (b, r, slice(h * G, (h + 1) * G))
+                bound = 2.0 ** -8 * want[at].abs() + 2.0 ** -13 * mass[at] + 14 * 2.0 ** -11 * size
+                over = ((got[at] - want[at]).abs() / bound).max().item()
+                assert over <= 1.0, f"{over:.3f} of the bound"
+
+
+def put_values(c, v):
+    """Values [slots, H, D] (64 bits) of a case; its cache holds them rounded."""
+    if c.fmt == "bf16":
+        v = v.float().bfloat16()
+        c.vd, raw = v.double(), v
+    else:
+        raw = ref.encode("e4m3", v, torch.tensor(1.0, dtype=torch.float64))
+        c.vd = ref.code_values("e4m3", raw)
+    c.cache.v.copy_(raw.to(DEV))
+
+
+@pytest.mark.parametrize("low", [0, 10, 14, 16, 20, 24, 40, 60, 75])
+@pytest.mark.parametrize("n,D,own", [(2, 128, 3), (40, 64, 1)])
+def test_small_values(low, n, D, own):
+    """bf16 values of 2^-low over 4,096 shared keys keep what attn_decode keeps of them: lone
+    tiles and pairs."""
+    c = Case("bf16", gq.LINEAR, one_group(n, 4096 if n == 2 else 1500), [own] * n, 1, 8, 2, D, 16,
+             low + n, hole=False)
+    put_values(c, c.vd * 2.0 ** -low)
+    check_spread(c)
+    c.check()
+
+
+def test_small_codes():
+    """E4M3 codes of a few steps of its smallest, over 4,096 keys."""
+    c = Case("fp8", gq.LINEAR, one_group(2, 4096), [3, 5], 1, 8, 2, 128, 16, 2, hole=False)
+    put_values(c, torch.randn(c.vd.shape, generator=torch.Generator().manual_seed(3),
+                              dtype=torch.float64) * 2.0 ** -8)
+    check_spread(c)
+
+
+@pytest.mark.parametrize("n", [3, 40])
+@pytest.mark.parametrize("large,small", [(2.0 ** 10, 2.0 ** -20), (1.0, 2.0 ** -45),
+                                         (2.0 ** 12, 0.0), (0.0, 2.0 ** -30)])
+def test_values_of_different_size_along_the_prefix(n, large, small):
+    """Key tiles of large values, of small ones and of zeros; rows that attend all of them, the
+    first ones only, or by their window the last ones only, within the bound of what they attend."""
+    c = Case("bf16", gq.LINEAR, one_group(n, 900), [40] * n, 1, 8, 2, 128, 16, 5, hole=False)
+    size = torch.ones(c.vd.shape[0], 1, 1, dtype=torch.float64) * small
+    size[:256] = large
+    size[640:] = small * 2.0 ** -7
+    put_values(c, c.vd * size)
+    c.lens = torch.tensor([[940, 200, 700][i % 3] for i in range(n)], dtype=torch.int32)
+    c.pos = c.lens - 1
+    for c.window in (0, 60):
+        c.check()
+    # weights that fall to the first keys by 2^-40, or rise to them
+    c.q[:] = 0
+    c.q[..., 0] = 1
+    c.window = 0
+    for ends in ((0.0, 27.0), (27.0, 0.0)):
+        c.kd[:, :, 0] = torch.linspace(*ends, c.kd.shape[0])[:, None].bfloat16().double()
+        c.cache.k.copy_(c.kd.bfloat16().to(DEV))
+        c.check(scale=1.0)
+
+
+def test_values_that_are_not_finite_beside_small_ones():
+    """A NaN is taken as 0 and reported, and the tile's other values keep their bits."""
+    c = Case("bf16", gq.PAGED, one_group(5, 700), [3, 4, 5, 6, 7], 1, 8, 2, 128, 16, 5, hole=False)
+    put_values(c, c.vd * 2.0 ** -30)
+    c.check()
+    at = c.slot(0, 150)
+    c.cache.v[at, 1, 7] = float("nan")
+    c.vd[at, 1, 7] = 0.0
+    want, mass = c.want()
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = c.run(err=err)
+    assert int(err) == gq.ATTN_ERR_UNSUPPORTED
+    ref.check_output(got, want, mass, weight_bits=10)
+
+
+def test_absent_pages_beside_small_values():
+    """The second reading of a tile skips a page that is not in the pool too."""
+    c = Case("bf16", gq.PAGED, one_group(3, 600), [3, 4, 5], 1, 8, 2, 64, 16, 6, hole=False)
+    put_values(c, c.vd * 2.0 ** -30)
+    c.cache.block_table[0, 5] = -1
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = c.run(err=err)
+    assert int(err) == gq.ATTN_ERR_BOUNDS
+    slot = c.slot
+    c.slot = lambda b, t: -1 if 80 <= t < 96 else slot(b, t)
+    want, mass = c.want()
+    ref.check_output(got, want, mass, weight_bits=10)
