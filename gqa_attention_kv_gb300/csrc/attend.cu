@@ -129,11 +129,13 @@ struct Params {
     // only keys t >= from[b] (clipped to 0 .. from_cap), every unit left as parts; or nullptr
     const int32_t *from;
     int from_cap;
-    // This launch reads nothing that the one before it writes after letting it begin: that one is
-    // waited for last, so that whoever waits for this launch has waited for both
+    // This launch reads and writes nothing that the one before it writes, and that one let it begin
+    // behind its own wait for everything earlier: it is waited for last, so that whoever waits for
+    // this launch has waited for both
     bool late_wait;
     // launch_attend_parts: shares, `pieces` of them, are taken one after another by whichever
-    // CTA is free (`next` counts them), so CTAs that start late do no harm; else one each
+    // CTA is free (`next` counts them, from the 0 at which the merge of the call before left it),
+    // so CTAs that start late do no harm; else one each
     int32_t *next;
     int pieces;
     int32_t *err;
@@ -1526,19 +1528,20 @@ int launch_attend_parts(const AttendPlan &plan, int e0, const int32_t *from, int
                         const int32_t *positions, int q_rows, int max_seq_len, int window,
                         int n_q_heads, int n_kv_heads, int head_dim, float scale, void *out,
                         void *workspace, int32_t *err, cudaStream_t stream, bool late_wait,
-                        int32_t *next, AttendParts *parts) {
+                        AttendParts *parts) {
     att::Params p = att::params_of(plan, q, cache, seq_lens, positions, q_rows, max_seq_len, window,
                                    0, n_q_heads, n_kv_heads, scale, out, workspace, err);
     p.from = from;
     p.from_cap = from_cap;
     p.late_wait = late_wait;
-    p.next = next;
+    p.next = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + plan.count_offset);
     p.pieces = plan.pieces;
     p.e0 = e0;
     p.n_entries = std::min(plan.per_launch, plan.entries - e0);
     parts->o = p.ws_o;
     parts->lse = p.ws_lse;
     parts->parts = p.ws_parts;
+    parts->next = p.next;
     parts->rb = plan.mt == 0 ? 8 : 16;
     parts->heads = plan.heads;
     parts->row_blocks = plan.row_blocks;

@@ -184,6 +184,7 @@ int launch_attend(const AttendPlan &plan, const void *q, const attn_kv_cache *ca
 struct AttendParts {
     const float *o, *lse;
     const int2 *parts;  // per unit: first and last (less than the first: none)
+    int32_t *next;      // the launch's counter of shares, to be left at 0
     int rb, heads, row_blocks, e0, n_entries;
     float held;  // lse holds log2 of the sum of weights times 2^held
 };
@@ -191,13 +192,14 @@ struct AttendParts {
 // One launch of the plan, its entries from e0 on, over keys t >= from[b] (clipped to
 // 0 .. from_cap).  late_wait: what the stream's launch before this one writes after letting it
 // begin is not read by this one (but by whoever merges the parts), and that launch waited for
-// everything before it.  next: a counter that is 0 when the launch begins.
+// everything before it.  The first of the workspace's counters (0 between calls) counts the shares;
+// whoever merges the parts sets it to 0 again.
 int launch_attend_parts(const AttendPlan &plan, int e0, const int32_t *from, int from_cap,
                         const void *q, const attn_kv_cache *cache, const int32_t *seq_lens,
                         const int32_t *positions, int q_rows, int max_seq_len, int window,
                         int n_q_heads, int n_kv_heads, int head_dim, float scale, void *out,
                         void *workspace, int32_t *err, cudaStream_t stream, bool late_wait,
-                        int32_t *next, AttendParts *parts);
+                        AttendParts *parts);
 
 // Norms and rotary embedding of q and k (rope.cu); cache null: none is written to.
 int launch_qk_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
@@ -214,7 +216,7 @@ int launch_kv_read(const int64_t *slot_mapping, int64_t n, const attn_kv_cache *
 // Decode with shared prefixes (shared.cu).
 struct SharedPlan {
     AttendPlan own;  // of the keys that are not shared
-    size_t rows_offset, lse_offset, next_offset, o_offset, workspace;
+    size_t rows_offset, lse_offset, o_offset, workspace;
 };
 
 int plan_shared(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads, int n_kv_heads,

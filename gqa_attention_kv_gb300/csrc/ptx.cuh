@@ -114,7 +114,9 @@ __device__ __forceinline__ void setmaxnreg_inc() {
 // ------------------------------------------------- programmatic dependent launch
 // Block until the grids this one depends on have completed and their memory
 // is visible.  Every kernel of the library calls it before touching memory a
-// previous kernel on the stream may write or read.
+// previous kernel on the stream may write or read, but for the own keys' launch of
+// a decode with shared prefixes: it touches nothing that the launch right before it
+// writes, which lets it begin behind its own call, and calls this at its end.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Allow the next kernel on the stream to begin launching (it still waits in

@@ -145,8 +145,6 @@ struct Params {
     // per row: log2 of the sum of weights (by what ws_o is held times), and of weights over scales
     float2 *ws_lse;
     uint16_t *ws_o;  // per row: HD f16
-    int32_t *ws_next;  // [launches]: attend.cu's counters of shares, set to 0 here
-    int launches;
     int32_t *err;
 };
 
@@ -485,12 +483,9 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
             prefetch_tensormap(&tm_v);
         }
     }
-    pdl_wait();  // everything below may come from the previous kernel
-    if (blockIdx.x == 0) {
-        for (int i = threadIdx.x; i < p.launches; i += kThreads) atomicExch(p.ws_next + i, 0);
-        __threadfence();
-        __syncthreads();
-    }
+    // Everything below may come from the previous kernel.  The own keys' launch begins behind this
+    // wait of every CTA, so it reads what that one left without a wait of its own.
+    pdl_wait();
     pdl_launch_dependents();
 
     int total = INT32_MAX;
@@ -1328,6 +1323,7 @@ __global__ void __launch_bounds__(256, SPLIT == 1 ? 4 : 2) shared_merge_kernel(c
     const int64_t head = (int64_t)(b * a.row_blocks + rb - a.e0) * p.n_kv_heads + kvh;
     pdl_wait();
     pdl_launch_dependents();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.next = 0;
     if (SPLIT == 1 && !live) return;
     float m = -INFINITY, sum = 0.f, acc[V] = {};
     if (live) {
@@ -1491,8 +1487,7 @@ int plan_shared(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     plan->rows_offset = up(plan->own.workspace);
     plan->lse_offset = up(plan->rows_offset + (size_t)batch * q_rows * sizeof(int4));
-    plan->next_offset = up(plan->lse_offset + (size_t)parts * sizeof(float2));
-    plan->o_offset = up(plan->next_offset + (size_t)plan->own.entries * sizeof(int32_t));
+    plan->o_offset = up(plan->lse_offset + (size_t)parts * sizeof(float2));
     plan->workspace = plan->o_offset + (size_t)parts * head_dim * 2;
     return ATTN_OK;
 }
@@ -1581,8 +1576,6 @@ int launch_shared(const SharedPlan &plan, const void *q, const attn_kv_cache *ca
     p.ws_rows = reinterpret_cast<int4 *>(ws + plan.rows_offset);
     p.ws_lse = reinterpret_cast<float2 *>(ws + plan.lse_offset);
     p.ws_o = reinterpret_cast<uint16_t *>(ws + plan.o_offset);
-    p.ws_next = reinterpret_cast<int32_t *>(ws + plan.next_offset);
-    p.launches = (plan.own.entries + plan.own.per_launch - 1) / plan.own.per_launch;
     p.err = err;
     // the largest power of two of keys that lie together wherever a tile begins; TMA boxes of
     // less than 8 would not begin on a swizzle's period
@@ -1653,8 +1646,7 @@ int launch_shared(const SharedPlan &plan, const void *q, const attn_kv_cache *ca
     for (int e0 = 0; e0 < plan.own.entries; e0 += plan.own.per_launch) {
         rc = launch_attend_parts(plan.own, e0, prefix_lens, p.prefix_cap, q, cache, seq_lens,
                                  positions, q_rows, max_seq_len, window, n_q_heads, n_kv_heads,
-                                 head_dim, scale, out, workspace, err, stream, e0 == 0,
-                                 p.ws_next + e0 / plan.own.per_launch, &m.own);
+                                 head_dim, scale, out, workspace, err, stream, e0 == 0, &m.own);
         if (rc != ATTN_OK) return rc;
         // rows of entries e0 .. e0 + n_entries - 1 (a request's last block may be short)
         auto row_of = [&](int e) {

@@ -90,6 +90,29 @@ def test_small_codes():
     check_spread(c)
 
 
+def test_the_counter_of_shares_is_left_at_zero():
+    """... by calls of one launch and of two, whatever lies behind the workspace's counters; a
+    decode and a window with sinks find their counters as they need them."""
+    few = Case("bf16", gq.LINEAR, one_group(5, 300), [7, 8, 40, 1, 90], 1, 8, 2, 128, 16, 1, hole=False)
+    many = Case("bf16", gq.LINEAR, one_group(300, 40), [1 + i % 50 for i in range(300)], 1, 2, 1, 64,
+                8, 2, hole=False)
+    flat = Case("bf16", gq.LINEAR, [(0, 0), (1, 0)], [900, 100], 1, 8, 2, 128, 16, 3, hole=False)
+    need = max(gq.attn_decode_shared_workspace_size(c.cache, c.q.shape[0], 1, c.q.shape[2], c.longest,
+                                                    c.max_prefix) for c in (few, many))
+    need = max(need, gq.attn_decode_workspace_size(flat.cache, 2, 1, 8, 900))
+    ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
+    wants = few.check(), many.check()
+    a = [x.to(DEV) for x in (flat.lens, flat.pos)]
+    exact, mass = flat.want()
+    for _ in range(3):
+        for c, want in zip((few, many), wants):
+            assert torch.equal(c.run(workspace=ws), want)
+            assert not ws[:1024].any()
+        ref.check_output(gq.attn_decode(flat.q.to(DEV), flat.cache, *a, 900, 0, 128 ** -0.5,
+                                        workspace=ws), exact, mass)
+        ws[-8192:] = 0xFF  # (partial states)
+
+
 @pytest.mark.parametrize("n", [3, 40])
 @pytest.mark.parametrize("large,small", [(2.0 ** 10, 2.0 ** -20), (1.0, 2.0 ** -45),
                                          (2.0 ** 12, 0.0), (0.0, 2.0 ** -30)])
