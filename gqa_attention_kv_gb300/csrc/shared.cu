@@ -967,7 +967,8 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
         // a page that is not there is reported, and its keys are looked for in every tile
         if (p.paged) {
             const int b0 = max(w.lo, w.kt0 * kBN) / p.block_size;
-            const int b1 = (min(w.hi, (w.kt0 + w.n_kt) * kBN) + p.block_size - 1) / p.block_size;
+            // (the last key's page; no sum of an end and a page's size, which may pass 31 bits)
+            const int b1 = (min(w.hi, (w.kt0 + w.n_kt) * kBN) - 1) / p.block_size + 1;
             bool bad = false;
             for (int i = b0 + st; i < b1; i += 256)
                 bad |= (unsigned)__ldg(table + i) >= (unsigned)p.num_pages;

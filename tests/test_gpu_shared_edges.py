@@ -165,3 +165,40 @@ def test_absent_pages_beside_small_values():
     c.slot = lambda b, t: -1 if 80 <= t < 96 else slot(b, t)
     want, mass = c.want()
     ref.check_output(got, want, mass, weight_bits=10)
+
+
+@pytest.mark.parametrize("bs", [1 << 20, 300])
+def test_prefixes_that_end_near_2_31(bs):
+    """Under a window, with two pages that serve every table entry: one that is not there is
+    reported and masked, though its end lies past 2^31."""
+    end, window, D = 2 ** 31 - 270, 700, 64
+    base = end - 1000  # (the reference counts from here on)
+    g = torch.Generator().manual_seed(bs)
+    pool = torch.randn(2, 2 * bs, 1, D, generator=g).bfloat16()
+    table = torch.zeros(3, -(-(end + 10) // bs), dtype=torch.int32, device=DEV)
+    table[:, 1::2] = 1
+    cache = gq.KVCache(gq.PAGED, pool[0].to(DEV), pool[1].to(DEV), block_table=table, block_size=bs)
+    q = torch.randn(2, 1, 4, D, generator=g).bfloat16()
+    i32 = dict(dtype=torch.int32)
+    lens = torch.tensor([end + 3, end + 9], **i32)
+    args = [x.to(DEV) for x in (lens, lens - 1, torch.full((2,), 2, **i32),
+                                torch.full((2,), end, **i32))]
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def check(absent):
+        def slot(b, t):
+            t += base
+            return -1 if t < end and t // bs == absent else t // bs % 2 * bs + t % bs
+
+        want, mass = ref.decode(q, pool[0].double(), pool[1].double(), slot, lens - base,
+                                lens - 1 - base, window, 0, D ** -0.5)
+        got = gq.attn_decode_shared(q.to(DEV), cache, *args, end + 10, end, window, D ** -0.5,
+                                    err=err)
+        ref.check_output(got, want, mass, weight_bits=10)
+
+    check(-1)
+    assert int(err) == 0
+    absent = (end - 300) // bs
+    table[2, absent] = -1
+    check(absent)
+    assert int(err) == gq.ATTN_ERR_BOUNDS
