@@ -79,6 +79,7 @@ constexpr float kScaleFloor = 0x1p-64f; // the smallest scale
 constexpr float kPartWeight = 0x1p-12f;
 constexpr float kSmallest = 0x1p-149f;
 constexpr int kMaxBatch = 4096;         // requests: the plan's tables lie in the K and V rings
+constexpr int kGroupSteps = 13;         // powers of two of groups, 1 .. kMaxBatch
 
 enum Fmt { kBF16 = 0, kE4M3 = 1, kINT8 = 2 };
 
@@ -128,7 +129,8 @@ struct Turn {
 };
 
 struct Params {
-    int batch, q_rows, window, n_kv_heads, group, rt, sms;
+    int batch, q_rows, window, n_kv_heads, group, rt;
+    int sms[kGroupSteps];  // CTAs that work where 2^i groups, or more, share a prefix
     int n_rows, slots_per_seq, block_size, max_blocks, num_pages, cap, prefix_cap;
     int box_rows;  // keys of a TMA box; 0: rows are gathered
     int map_rows;  // extent of the maps' second dimension
@@ -180,11 +182,31 @@ __device__ __forceinline__ void request_range(const Params &p, int b, bool repor
     if (hi <= lo) hi = 0, lo = INT32_MAX;
 }
 
+// How many groups share a prefix (the plan's count, from nothing but lengths and rows).
+__device__ __forceinline__ int sharing_groups(const Params &p) {
+    int n = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += blockDim.x) {
+        const int b = b0 + (int)threadIdx.x;
+        bool first = false;
+        if (b < p.batch) {
+            const int plen = max(0, min(p.prefix_lens[b], p.prefix_cap));
+            first = plen > 0 && (b == 0 || p.prefix_rows[b] != p.prefix_rows[b - 1] ||
+                                 plen != max(0, min(p.prefix_lens[b - 1], p.prefix_cap)));
+        }
+        n += __syncthreads_count(first);
+    }
+    return n;
+}
+__device__ __forceinline__ int working_ctas(const Params &p, int groups) {
+    return p.sms[31 - __clz(max(1, groups))];
+}
+
 // The plan: groups, their pieces, and the piece that is asked for (n_kt 0: none).  `mem` is
-// scratch in shared memory; every thread of the CTA calls this and passes its last barrier.
-// Of U units (group, KV head, pair of tiles) that weigh their key tiles each is cut into so many
+// scratch in shared memory; every thread of the CTA calls this and passes its last barrier.  ctas:
+// how many CTAs work.  Of U units (group, KV head, pair of tiles) that weigh their key tiles each is cut into so many
 // pieces (else 1 + floor((SMs - U) tiles / sum)) that all are at most the SMs, or U.
-__device__ int make_plan(const Params &p, int32_t *mem, int want, bool tables, Piece &mine) {
+__device__ int make_plan(const Params &p, int32_t *mem, int want, bool tables, Piece &mine,
+                         int &ctas) {
     const int kThreads = blockDim.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int B = p.batch, chunks = (B + 31) / 32;
@@ -192,7 +214,7 @@ __device__ int make_plan(const Params &p, int32_t *mem, int want, bool tables, P
     int32_t *g_lo = g_start + kMaxBatch + 8, *g_hi = g_lo + kMaxBatch, *g_parts = g_hi + kMaxBatch;
     int32_t *g_base = g_parts + kMaxBatch, *c_mask = g_base + kMaxBatch;
     int32_t *c_base = c_mask + kMaxBatch / 32;
-    __shared__ int s_groups, s_total;
+    __shared__ int s_groups, s_total, s_ctas;
     for (int c = warp; c < chunks; c += kThreads / 32) {
         const int b = c * 32 + lane;
         bool first = false;
@@ -215,14 +237,16 @@ __device__ int make_plan(const Params &p, int32_t *mem, int want, bool tables, P
             first = b == 0 || before_plen != plen || before_row != row;
         }
         const uint32_t mask = __ballot_sync(0xffffffffu, first);
-        if (lane == 0) c_mask[c] = (int32_t)mask;
+        const uint32_t sharing = __ballot_sync(0xffffffffu, first && plen > 0);
+        if (lane == 0) c_mask[c] = (int32_t)mask, c_base[c] = __popc(sharing);
     }
     if (threadIdx.x == 0) mine.n_kt = 0;
     __syncthreads();
     if (warp == 0) {
-        int carry = 0;
+        int carry = 0, sharing = 0;
         for (int c0 = 0; c0 < chunks; c0 += 32) {
             const int n = c0 + lane < chunks ? __popc((uint32_t)c_mask[c0 + lane]) : 0;
+            if (c0 + lane < chunks) sharing += c_base[c0 + lane];
             int x = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -232,12 +256,15 @@ __device__ int make_plan(const Params &p, int32_t *mem, int want, bool tables, P
             if (c0 + lane < chunks) c_base[c0 + lane] = carry + x - n;
             carry += __shfl_sync(0xffffffffu, x, 31);
         }
+        sharing = __reduce_add_sync(0xffffffffu, sharing);
         if (lane == 0) {
             s_groups = carry;
             g_start[carry] = B;
+            s_ctas = working_ctas(p, sharing);
         }
     }
     __syncthreads();
+    ctas = s_ctas;
     auto group_of = [&](int b) {
         const uint32_t upto = 0xffffffffu >> (31 - (b & 31));
         return c_base[b >> 5] + __popc((uint32_t)c_mask[b >> 5] & upto) - 1;
@@ -273,19 +300,19 @@ __device__ int make_plan(const Params &p, int32_t *mem, int want, bool tables, P
         }
         // Of U units, each cut into pieces of at most s key tiles: the least s whose pieces are no
         // more than the SMs lies between work / SMs and work / (SMs - U); 32 of those are tried
-        const int spare = max(0, p.sms - units);
+        const int spare = max(0, ctas - units);
         int most = 0;  // s, or 0: units are cut in proportion
         if (groups <= 32 && spare > 0 && work < (int64_t(1) << 30) && work > 0) {
             const int t = lane < groups ? tiles_of(lane) : 0;
             const int u = t > 0 ? pairs_of(lane) * p.n_kv_heads : 0;
-            const int s0 = ((int)work + p.sms - 1) / p.sms, s1 = ((int)work + spare - 1) / spare;
+            const int s0 = ((int)work + ctas - 1) / ctas, s1 = ((int)work + spare - 1) / spare;
             const int s = s0 + (int)(((int64_t)(s1 - s0) * lane + 30) / 31);
             int n = 0;
             for (int g = 0; g < groups; ++g) {
                 const int tg = __shfl_sync(0xffffffffu, t, g), ug = __shfl_sync(0xffffffffu, u, g);
                 n += ug * ((tg + s - 1) / s);
             }
-            const uint32_t fits = __ballot_sync(0xffffffffu, n <= p.sms);
+            const uint32_t fits = __ballot_sync(0xffffffffu, n <= ctas);
             most = fits != 0 ? __shfl_sync(0xffffffffu, s, __ffs(fits) - 1) : 0;
         }
         int at = 0, row = 0;  // pieces and rows of ws_o before these groups
@@ -339,8 +366,7 @@ __device__ int make_plan(const Params &p, int32_t *mem, int want, bool tables, P
     __syncthreads();
     // where the merge finds a position's parts
     if (tables)
-        for (int i = blockIdx.x * kThreads + threadIdx.x; i < B * p.q_rows;
-             i += gridDim.x * kThreads) {
+        for (int i = blockIdx.x * kThreads + threadIdx.x; i < B * p.q_rows; i += ctas * kThreads) {
             const int b = i / p.q_rows, g = group_of(b), n = g_start[g + 1] - g_start[g];
             p.ws_rows[i] = make_int4(g_base[g] + (i - g_start[g] * p.q_rows) * p.group,
                                      n * p.q_rows * p.group, g_parts[g], 0);
@@ -472,6 +498,13 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
     const int G = p.group, R = p.q_rows, used = p.rt * G;
     const bool gather = p.box_rows == 0;
 
+    if ((int)blockIdx.x >= p.sms[0]) {
+        // at work only if there are more groups than one: out of the own keys' way else (with the
+        // whole plan first 64 requests over 4,096 keys took 49.6 us)
+        pdl_wait();
+        pdl_launch_dependents();
+        if ((int)blockIdx.x >= working_ctas(p, sharing_groups(p))) return;
+    }
     if (warp == 1) {
         tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
@@ -488,8 +521,8 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
     pdl_wait();
     pdl_launch_dependents();
 
-    int total = INT32_MAX;
-    for (int want = blockIdx.x; want < total; want += gridDim.x) {
+    int total = INT32_MAX, ctas = 1;
+    for (int want = blockIdx.x; want < total; want += ctas) {
     if (threadIdx.x == 0) {
         for (int i = 0; want != (int)blockIdx.x && i < C::kNumBars; ++i) mbar_inval(&bars[i]);
         const int loads = gather ? 32 : 1;
@@ -517,7 +550,8 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
         fence_barrier_init();
         s_bad = 0;
     }
-    total = make_plan(p, reinterpret_cast<int32_t *>(sK), want, want == (int)blockIdx.x, w);
+    total = make_plan(p, reinterpret_cast<int32_t *>(sK), want, want == (int)blockIdx.x, w,
+                      ctas);
     // Tile rows past the packed queries are never loaded: zeros
     if (used < kBM)
         for (int i = threadIdx.x; i < 2 * C::kHalves * (kBM - used) * 8; i += kThreads) {
@@ -1283,7 +1317,7 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
         }
     }
     __syncwarp();  // (lanes that elected ones of their warp went ahead of)
-    if (want + (int)gridDim.x >= total) break;
+    if (want + ctas >= total) break;
     tc_fence_before();  // another piece: everything has been read
     __syncthreads();
     tc_fence_after();
@@ -1456,8 +1490,8 @@ int launch_prefix(const Params &p, const CUtensorMap &tq, const CUtensorMap &tk,
         }
         configured.fetch_or(bit, std::memory_order_relaxed);
     }
-    const cudaError_t e = launch_pdl(prefix_kernel<FMT, HD>, dim3((unsigned)p.sms),
-                                     dim3(Cfg<FMT, HD>::kThreads),
+    const unsigned grid = (unsigned)*std::max_element(p.sms, p.sms + kGroupSteps);
+    const cudaError_t e = launch_pdl(prefix_kernel<FMT, HD>, dim3(grid), dim3(Cfg<FMT, HD>::kThreads),
                                      Cfg<FMT, HD>::kSmem, stream, tq, tk, tv, p);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
@@ -1493,18 +1527,23 @@ int plan_shared(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
     return ATTN_OK;
 }
 
-// The SMs that the shared part takes.  attend.cu's CTAs start at once on the others and follow on
-// each that is left, so that the two parts run side by side.  Of the pieces that a unit (KV head,
-// pair of tiles) can be cut into, as many as end soonest by the host's bounds (lengths are known on
-// the device only): a piece takes 9 us and 1.65 a pair of tiles and 128 keys (1.2 a single tile; over
-// codes 2.4 and 1.6), an SM reads 36 bytes (28) of own keys a nanosecond.  On every SM first, the own
-// keys after: 64 requests over 4,096 and 64 to 1,024 keys 67.8 us, side by side 47.8; 16 over 14,449
-// and up to 2,000 43.2 and 32.2; four E4M3 groups 68.9 and 61.3; two short requests the same.
+// The SMs that the shared part takes where `groups` groups share a prefix.  attend.cu's CTAs start at
+// once on the others and follow on each that is left, so that the two parts run side by side.  Of the
+// pieces that a unit (KV head, pair of tiles) can be cut into, as many as end soonest by the host's
+// bounds (lengths are known on the device only): a piece takes 9 us and 1.65 a pair of tiles and 128
+// keys (1.2 a single tile; over codes 2.4 and 1.6; measured with 128 dims, and taken for 64 too), an
+// SM reads 36 bytes (28) of own keys a nanosecond.  On every SM first, the own keys after: 64 requests
+// over 4,096 and 64 to 1,024 keys 67.8 us, side by side 47.8; 16 over 14,449 and up to 2,000 43.2 and
+// 32.2; four E4M3 groups 68.9 and 61.3; two short requests the same.  Every group has a unit for each
+// KV head: with what is right for one group, 64 requests in 32 groups of up to 128 shared keys took
+// 285 us on 8 SMs, one piece after another (43 with their own number; 16 groups 148 and 37).  CTAs
+// past one group's number look for themselves, which costs a batch of one group up to 1 us.
 static int prefix_sms(int batch, int q_rows, int group, int n_kv_heads, int head_dim, int esize,
-                      int max_seq_len, int max_prefix_len, int own_units) {
+                      int max_seq_len, int max_prefix_len, int own_units, int groups) {
     const int sms = device_sm_count(), rt = shr::kBM / group;
-    const int64_t pos = (int64_t)batch * q_rows;
-    const int64_t units = (pos + 2 * rt - 1) / (2 * rt) * n_kv_heads;
+    const int64_t pos = ((int64_t)batch * q_rows + groups - 1) / groups;  // of one of them
+    const int64_t units =
+        (((int64_t)batch * q_rows + 2 * rt - 1) / (2 * rt) + groups - 1) * n_kv_heads;
     if (units > sms / 2) return sms;
     const int64_t tiles = (max_prefix_len + 127) / 128;
     const double tile = esize == 2 ? (pos <= rt ? 1.2 : 1.65) : (pos <= rt ? 1.6 : 2.4);
@@ -1548,9 +1587,11 @@ int launch_shared(const SharedPlan &plan, const void *q, const attn_kv_cache *ca
     p.n_kv_heads = n_kv_heads;
     p.group = n_q_heads / n_kv_heads;
     p.rt = shr::kBM / p.group;
-    p.sms = prefix_sms(batch, q_rows, p.group, n_kv_heads, head_dim, esize, max_seq_len,
-                       std::min(max_prefix_len, max_seq_len),
-                       plan.own.entries * (n_kv_heads / plan.own.heads));
+    // (the groups are known on the device only)
+    for (int i = 0; i < shr::kGroupSteps && (1 << i) <= batch; ++i)
+        p.sms[i] = prefix_sms(batch, q_rows, p.group, n_kv_heads, head_dim, esize, max_seq_len,
+                              std::min(max_prefix_len, max_seq_len),
+                              plan.own.entries * (n_kv_heads / plan.own.heads), 1 << i);
     p.n_rows = n_rows;
     p.slots_per_seq = cache->slots_per_seq;
     p.block_size = cache->block_size;
@@ -1642,8 +1683,8 @@ int launch_shared(const SharedPlan &plan, const void *q, const attn_kv_cache *ca
     // 16 requests of 28/4 heads over 14,449 keys 32.2 us, with one warp 42.4; 64 of 32/8 over 4,096
     // 47.8 with one, 55.8 with four; 256 over 32,768 155 and 188
     const int64_t pairs = ((int64_t)batch * q_rows + 2 * p.rt - 1) / (2 * p.rt);
-    const bool split = p.sms > 8 * n_kv_heads * pairs &&
-                       (int64_t)batch * q_rows * n_q_heads <= (int64_t)p.sms * 16;
+    const bool split = p.sms[0] > 8 * n_kv_heads * pairs &&
+                       (int64_t)batch * q_rows * n_q_heads <= (int64_t)p.sms[0] * 16;
     for (int e0 = 0; e0 < plan.own.entries; e0 += plan.own.per_launch) {
         rc = launch_attend_parts(plan.own, e0, prefix_lens, p.prefix_cap, q, cache, seq_lens,
                                  positions, q_rows, max_seq_len, window, n_q_heads, n_kv_heads,

@@ -202,3 +202,42 @@ def test_prefixes_that_end_near_2_31(bs):
     table[2, absent] = -1
     check(absent)
     assert int(err) == gq.ATTN_ERR_BOUNDS
+
+
+@pytest.mark.parametrize("fmt,D", [("bf16", 64), ("int8", 64), ("e4m3", 128)])
+def test_any_number_of_groups(fmt, D):
+    """The CTAs at work follow the groups, which a replay of one graph changes: one, a few, as many
+    as requests, none, equal lengths in other rows, one row at other lengths."""
+    n = 70
+    c = Case(fmt, gq.LINEAR, one_group(n, 90), [1 + i % 9 for i in range(n)], 1, 4, 2, D, 16, 9 + D,
+             hole=False)
+    need = gq.attn_decode_shared_workspace_size(c.cache, n, 1, 4, c.longest, c.max_prefix)
+    ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
+    q, lens, pos, prows, plens = (x.to(DEV) for x in (c.q, c.lens, c.pos, c.prows, c.plens))
+    out = torch.empty_like(q)
+    graph = torch.cuda.CUDAGraph()
+    c.run()
+    with torch.cuda.graph(graph):
+        gq.attn_decode_shared(q, c.cache, lens, pos, prows, plens, c.longest, c.max_prefix, 0,
+                              D ** -0.5, out=out, workspace=ws)
+    for i, of in enumerate([lambda b: (0, 90), lambda b: (b // 30, 90), lambda b: (b, 90),
+                            lambda b: (0, 90 if b < 35 else 40), lambda b: (b, 0),
+                            lambda b: (b // 4, 30 + b // 4), lambda b: (b % 2, 90),
+                            lambda b: (0, 90 * (b % 2))]):
+        at = [of(b) for b in range(n)]
+        c.prows.copy_(torch.tensor([a[0] for a in at]))
+        c.plens.copy_(torch.tensor([a[1] for a in at]))
+        prows.copy_(c.prows), plens.copy_(c.plens)
+        graph.replay()
+        want, mass = c.want()
+        ref.check_output(out, want, mass, weight_bits=10)
+
+
+def test_more_groups_than_a_block_counts_at_once():
+    """1,300 requests in 700 groups."""
+    prefix, first = [], 0
+    for i in range(700):
+        size = 1 + (i % 7 < 6)
+        prefix += [(first, 0 if i % 11 == 5 else 10 + i % 60)] * size
+        first += size
+    Case("bf16", gq.PAGED, prefix, [1 + i % 4 for i in range(first)], 1, 2, 1, 64, 16, 31).check()
