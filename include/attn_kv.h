@@ -393,7 +393,11 @@ int attn_decode_kernel_launches(const attn_kv_cache *cache, int batch, int q_row
  *   ATTN_ERR_UNSUPPORTED; magnitudes under 2^-14 lose precision), the scales
  *   multiply scores and softmax weights in float32, and the weights are rounded
  *   once to f16.  A scale is finite and at least 2^-64 (one below reads as
- *   2^-64).  Scores, scale * q . key * log2(e), have to stay below 2^24 in
+ *   2^-64), and those of the values that a row attends lie within 2^100 of one
+ *   another: a weight is summed times its key's scale over the largest, in
+ *   float32, where 2^-133 of the largest is lost (of the smallest scale's keys
+ *   then 2^-33; further apart, keys that count).
+ *   Scores, scale * q . key * log2(e), have to stay below 2^24 in
  *   magnitude: where the largest of a stretch of keys does not,
  *   ATTN_ERR_UNSUPPORTED is reported and the row is unspecified.  Its workspace is like any other's (zero-filled before its
  *   first use).
@@ -603,9 +607,9 @@ int attn_decode_sinks(const void *q, const attn_kv_cache *cache, const int32_t *
  * decide how many SMs the two parts of the work get: loose bounds cost time, as do
  * many groups.
  * Which keys a row attends is attn_decode's rule (seq_lens counts the prefix).
- * LINEAR and PAGED caches of every dtype and layout; RING is not supported.
- * n_q_heads / n_kv_heads at most 128, batch at most 4,096, num_slots * n_kv_heads
- * below 2^31, max_seq_len below 2^31 - 256.
+ * LINEAR and PAGED caches of every dtype and layout, scales as attn_decode has
+ * them; RING is not supported.  n_q_heads / n_kv_heads at most 128, batch at most
+ * 4,096, num_slots * n_kv_heads below 2^31, max_seq_len below 2^31 - 256.
  *   The shared keys' products run on tensor cores: over a bf16 cache Q K^T takes
  *   q and k as bf16, over an 8-bit one q is rounded to f16 (below 2^-14 in steps of
  *   2^-24; a magnitude of 65520 or more is reported as ATTN_ERR_UNSUPPORTED).

@@ -5,7 +5,7 @@ import torch
 
 import gqa_attention_kv_gb300 as gq
 import kv_reference as ref
-from test_gpu_shared import DEV, Case, one_group
+from test_gpu_shared import DEV, DTYPE, Case, one_group
 
 pytestmark = pytest.mark.gpu
 
@@ -167,17 +167,23 @@ def test_absent_pages_beside_small_values():
     ref.check_output(got, want, mass, weight_bits=10)
 
 
-@pytest.mark.parametrize("bs", [1 << 20, 300])
-def test_prefixes_that_end_near_2_31(bs):
+@pytest.mark.parametrize("fmt,bs", [("bf16", 1 << 20), ("bf16", 300), ("int8", 320)])
+def test_prefixes_that_end_near_2_31(fmt, bs):
     """Under a window, with two pages that serve every table entry: one that is not there is
     reported and masked, though its end lies past 2^31."""
     end, window, D = 2 ** 31 - 270, 700, 64
     base = end - 1000  # (the reference counts from here on)
     g = torch.Generator().manual_seed(bs)
-    pool = torch.randn(2, 2 * bs, 1, D, generator=g).bfloat16()
+    pool, more = torch.randn(2, 2 * bs, 1, D, generator=g).bfloat16(), {}
+    if fmt == "int8":
+        pool = (pool * 30).clamp(-127, 127).to(torch.int8)
+        scale = torch.full((2 * bs // 16, 1), 2.0 ** -5, device=DEV)
+        more = dict(dtype=DTYPE[fmt], k_scale=scale, v_scale=scale.clone(), scale_block=16)
+    values = pool.double() if fmt == "bf16" else pool.double() * 2.0 ** -5
     table = torch.zeros(3, -(-(end + 10) // bs), dtype=torch.int32, device=DEV)
     table[:, 1::2] = 1
-    cache = gq.KVCache(gq.PAGED, pool[0].to(DEV), pool[1].to(DEV), block_table=table, block_size=bs)
+    cache = gq.KVCache(gq.PAGED, pool[0].to(DEV), pool[1].to(DEV), block_table=table, block_size=bs,
+                       **more)
     q = torch.randn(2, 1, 4, D, generator=g).bfloat16()
     i32 = dict(dtype=torch.int32)
     lens = torch.tensor([end + 3, end + 9], **i32)
@@ -190,7 +196,7 @@ def test_prefixes_that_end_near_2_31(bs):
             t += base
             return -1 if t < end and t // bs == absent else t // bs % 2 * bs + t % bs
 
-        want, mass = ref.decode(q, pool[0].double(), pool[1].double(), slot, lens - base,
+        want, mass = ref.decode(q, values[0], values[1], slot, lens - base,
                                 lens - 1 - base, window, 0, D ** -0.5)
         got = gq.attn_decode_shared(q.to(DEV), cache, *args, end + 10, end, window, D ** -0.5,
                                     err=err)
@@ -241,3 +247,50 @@ def test_more_groups_than_a_block_counts_at_once():
         prefix += [(first, 0 if i % 11 == 5 else 10 + i % 60)] * size
         first += size
     Case("bf16", gq.PAGED, prefix, [1 + i % 4 for i in range(first)], 1, 2, 1, 64, 16, 31).check()
+
+
+def put_scales(c, ks, vs, sb=16):
+    """Scales [slots / sb, heads] of a case (64 bits); smaller ones than 2^-64 are read as that."""
+    code = {"k": c.cache.k, "v": c.cache.v}
+    for name, x in (("k", ks.float()), ("v", vs.float())):
+        getattr(c.cache, name + "_scale").copy_(x.to(DEV))
+        values = ref.dequantized(c.fmt, code[name].cpu(), x.clamp(min=ref.FLOOR), sb)
+        setattr(c, name + "d", values)
+
+
+@pytest.mark.parametrize("n", [4, 40])
+@pytest.mark.parametrize("fmt,kind,D", [("e4m3", gq.LINEAR, 128), ("int8", gq.PAGED, 64),
+                                        ("int8", gq.LINEAR, 128), ("e4m3", gq.PAGED, 64)])
+def test_scales_at_their_ends(fmt, kind, D, n):
+    """Values' scales from 0 to 2^119 (codes of 127 and 448 end below bf16's 2^128) and keys' from 0
+    on; blocks side by side, across the border of prefix and own keys too, that differ by up to 2^100
+    (a weight times vs / vs_max is held times 2^7 in float32, which ends at 2^-126: 2^-33 of a weight
+    whose scale is 2^-100 of the largest, 250 of which are nothing beside the bound's 2^-13)."""
+    c = Case(fmt, kind, one_group(n, 200), [1 + i % 50 for i in range(n)], 1, 8, 2, D, 16, n + D,
+             hole=False)
+    shape = c.cache.k_scale.shape
+    g = torch.Generator().manual_seed(D + n)
+    ones = torch.ones(shape, dtype=torch.float64)
+    usual = ones * (1.0 / 128 if fmt == "int8" else 1.0 / 64)
+
+    def powers(lo, hi):
+        return 2.0 ** torch.randint(lo, hi + 1, shape, generator=g).double()
+
+    for ks, vs in ((usual, ones * 0.0), (usual, ones * 2.0 ** -70), (usual, ones * 2.0 ** -64),
+                   (usual, ones * 2.0 ** 119), (usual, powers(-30, 30)), (usual, powers(-64, 36)),
+                   (usual, powers(19, 119)),
+                   (ones * 0.0, usual), (ones * 2.0 ** -64, powers(-10, 10)),
+                   (usual * powers(-8, 2), usual), (usual * powers(-30, 0), powers(-3, 3))):
+        put_scales(c, ks, vs)
+        c.check()
+
+
+@pytest.mark.parametrize("fmt,kind", [("int8", gq.LINEAR), ("e4m3", gq.PAGED), ("fp8", gq.LINEAR)])
+def test_positions_at_the_ends_of_int32(fmt, kind):
+    c = Case(fmt, kind, one_group(5, 300), [4] * 5, 2, 8, 2, 128, 16, 6, hole=False)
+    low, high = -2 ** 31, 2 ** 31 - 1
+    c.pos = torch.tensor([low, 303, 302, low + 1, -2, low + 299, 302, high, 300, low],
+                         dtype=torch.int32)
+    for c.window in (0, 2 ** 31 - 1, 20):
+        got = c.check()
+        assert not got[0, 0].any() and not got[1, 1].any() and not got[2].any()
