@@ -855,7 +855,7 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
                         if ((unsigned)page >= (unsigned)p.num_pages) return x;
                         slot = (int64_t)page * p.block_size + (t - block_of(t) * p.block_size);
                     }
-                    x = __ldg(reinterpret_cast<const uint4 *>(
+                    x = __ldcg(reinterpret_cast<const uint4 *>(
                         p.v + p.place.head_offset(slot, w.kvh) + (i / (kBN * 8)) * 128 +
                         (((i ^ r) & 7) << 4)));
                     x.x = drop_bf16_nan(x.x), x.y = drop_bf16_nan(x.y);
@@ -1531,8 +1531,9 @@ int plan_shared(const attn_kv_cache *cache, int batch, int q_rows, int n_q_heads
 // once on the others and follow on each that is left, so that the two parts run side by side.  Of the
 // pieces that a unit (KV head, pair of tiles) can be cut into, as many as end soonest by the host's
 // bounds (lengths are known on the device only): a piece takes 9 us and 1.65 a pair of tiles and 128
-// keys (1.2 a single tile; over codes 2.4 and 1.6; measured with 128 dims, and taken for 64 too), an
-// SM reads 36 bytes (28) of own keys a nanosecond.  On every SM first, the own keys after: 64 requests
+// keys (1.2 a single tile; over codes 2.4 and 1.6; 64 dims do best by the same: with three quarters
+// of it for them 64 bf16 requests over 4,096 keys 34.4 us, so 31.8, and 16 over 14,449 24.1 and 25.8),
+// an SM reads 36 bytes (28) of own keys a nanosecond.  On every SM first, the own keys after: 64 requests
 // over 4,096 and 64 to 1,024 keys 67.8 us, side by side 47.8; 16 over 14,449 and up to 2,000 43.2 and
 // 32.2; four E4M3 groups 68.9 and 61.3; two short requests the same.  Every group has a unit for each
 // KV head: with what is right for one group, 64 requests in 32 groups of up to 128 shared keys took
