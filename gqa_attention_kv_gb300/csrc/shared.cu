@@ -43,10 +43,10 @@
 // enters the weights' exponent, l sums w / vs.  Weights are held times 2^7 (those down to
 // 2^-21 of the largest keep f16's 11 bits).  Values of a bf16 cache have such a scale too, or f16
 // would lose them from 2^-14 on: those of a tile are multiplied with a power of two (exactly) and the
-// weights of its keys divided by it.  The power of the tile before is tried, 1 at first; where the
+// weights of its keys divided by it.  The power of the tile before is tried; where the
 // tile's largest value, which the conversion finds by the way, leaves 2^-4 .. 2^15 by it, the tile is
-// read and converted again with its own (256 requests over 32,768 keys 158 us; with a first round
-// over every tile 165, without powers of two 152).  A CTA leaves O normalised by the plain sum of its
+// read and converted again with its own (256 requests over 32,768 keys 160 us; with a first round
+// over every tile 166, without powers of two 152).  A CTA leaves O normalised by the plain sum of its
 // weights and held times a power of two of its row, in f16 (2^-11, a quarter of the output's bf16
 // half step), and the logarithms of both sums.
 #include <cuda.h>
@@ -814,7 +814,7 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
             };
             // A tile of bf16 V in place, to f16 times 2^shift; returns the largest |x| of its keys in
             // the group's range, as a bf16 pattern
-            auto v_in_place = [&](int tile, uint32_t at, auto scaled, int shift) {
+            auto v_in_place = [&](int tile, uint32_t at, int shift) {
                 const bool all = whole(tile);
                 constexpr int kBatch = 4;  // pieces read before one is written (eight: 1% slower)
                 __nv_bfloat162 most = zero2;
@@ -834,17 +834,37 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             most = size_of(most, u[e]);
-                            u[e] = decltype(scaled)::value ? to_f16(u[e], by)
-                                                           : bf16x2_to_f16x2_sat(u[e]);
+                            u[e] = to_f16(u[e], by);
                         }
                         st_shared_v4(at + i * 16, x[b]);
                     }
                 }
                 return largest(most);
             };
-            // The same from the cache, where the power of two was not right (shift: the one to come),
-            // NaN as zeros; returns the shift taken
-            auto v_again = [&](int tile, uint32_t at) {
+            // The power of two that brings a largest value to 2^9 .. 2^10: tiles of 2^-13 to 2^5 times
+            // its size do by it
+            auto shift_of = [](uint32_t top) {
+                return min(max(136 - (int)(top >> 7), 0), kShiftTop);
+            };
+            // ... that a piece begins with: by a quarter of its first tile (a wrong guess costs what
+            // v_again takes: two requests over 512 keys of 2^-10 27.2 us where 1 was tried first and the
+            // tile read piece by piece, 16.9 so)
+            auto first_guess = [&](int tile, uint32_t at) {
+                __nv_bfloat162 most = zero2;
+#pragma unroll
+                for (int b = 0; b < C::kTileBytes / 16 / kConv / 4; ++b) {
+                    const int i = ct + kConv * b * 4;
+                    const uint4 x = ld_shared_v4(at + i * 16);
+                    if (!inside(tile, (i >> 3) & (kBN - 1))) continue;
+                    most = size_of(size_of(most, x.x), x.y);
+                    most = size_of(size_of(most, x.z), x.w);
+                }
+                const uint32_t top = largest(most);
+                return top == 0 ? 0 : shift_of(top);
+            };
+            // The same from the cache, where the power of two was not right for a largest value `top`
+            // (a NaN, which is taken as 0: whatever the others' is); returns the shift taken
+            auto v_again = [&](int tile, uint32_t at, uint32_t top) {
                 auto piece = [&](int i) {  // piece i of the tile in shared memory (swizzled)
                     const int r = (i >> 3) & (kBN - 1), t = tile * kBN + r;
                     uint4 x = make_uint4(0u, 0u, 0u, 0u);
@@ -855,28 +875,34 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
                         if ((unsigned)page >= (unsigned)p.num_pages) return x;
                         slot = (int64_t)page * p.block_size + (t - block_of(t) * p.block_size);
                     }
-                    x = __ldcg(reinterpret_cast<const uint4 *>(
+                    return __ldcg(reinterpret_cast<const uint4 *>(
                         p.v + p.place.head_offset(slot, w.kvh) + (i / (kBN * 8)) * 128 +
                         (((i ^ r) & 7) << 4)));
-                    x.x = drop_bf16_nan(x.x), x.y = drop_bf16_nan(x.y);
-                    x.z = drop_bf16_nan(x.z), x.w = drop_bf16_nan(x.w);
-                    return x;
                 };
-                __nv_bfloat162 most = zero2;
+                if (top > 0x7F80u) {
+                    __nv_bfloat162 most = zero2;
 #pragma unroll 1
-                for (int i = ct; i < C::kTileBytes / 16; i += kConv) {
-                    const uint4 x = piece(i);
-                    most = size_of(size_of(most, x.x), x.y);
-                    most = size_of(size_of(most, x.z), x.w);
+                    for (int i = ct; i < C::kTileBytes / 16; i += kConv) {
+                        const uint4 x = piece(i);
+                        most = size_of(size_of(most, drop_bf16_nan(x.x)), drop_bf16_nan(x.y));
+                        most = size_of(size_of(most, drop_bf16_nan(x.z)), drop_bf16_nan(x.w));
+                    }
+                    top = largest(most);
                 }
-                // the largest to 2^9 .. 2^10: tiles of 2^-13 to 2^5 times its size come in between
-                const int shift = min(max(136 - (int)(largest(most) >> 7), 0), kShiftTop);
+                const int shift = shift_of(top);
                 const __nv_bfloat162 by = power(shift);
 #pragma unroll 1
-                for (int i = ct; i < C::kTileBytes / 16; i += kConv) {
-                    const uint4 x = piece(i);
-                    st_shared_v4(at + i * 16, make_uint4(to_f16(x.x, by), to_f16(x.y, by),
-                                                         to_f16(x.z, by), to_f16(x.w, by)));
+                for (int i0 = ct; i0 < C::kTileBytes / 16; i0 += kConv * 4) {
+                    uint4 x[4];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) x[b] = piece(i0 + kConv * b);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        uint32_t *u = &x[b].x;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) u[e] = to_f16(drop_bf16_nan(u[e]), by);
+                        st_shared_v4(at + (i0 + kConv * b) * 16, x[b]);
+                    }
                 }
                 return shift;
             };
@@ -953,6 +979,9 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
                     rt.next(raw_stages);
                 }
             } else {
+                // (no way out where a wait ran out: the four warps meet at a barrier)
+                ok = mbar_wait(&v_full[0], 0, p.err);
+                shift = first_guess(w.kt0, smem_u32(sV));
                 for (int j = 0; j < w.n_kt; ++j) {
                     if (gather) {
                         // K copied by cp.async: written again, so that this thread's fence
@@ -966,20 +995,17 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
                         mbar_arrive(&k_conv[kt.st]);
                         kt.next(k_stages);
                     }
-                    // (no way out where a wait ran out: the four warps meet at a barrier)
                     if (ok) ok = mbar_wait(&v_full[vt.st], vt.ph, p.err);
                     const uint32_t at = smem_u32(sV + vt.st * C::kTileBytes);
                     const int tile = w.kt0 + j;
-                    const uint32_t top = shift == 0
-                                             ? v_in_place(tile, at, std::false_type{}, 0)
-                                             : v_in_place(tile, at, std::true_type{}, shift);
+                    const uint32_t top = v_in_place(tile, at, shift);
                     // f16 holds 65504 at most, and of what is 2^-4 at least all that counts: a
                     // value below 2^-14 is off by 2^-21 of the largest at most
                     const int size = (int)(top >> 7) + shift - 127;
                     if (top >= 0x4780u || size > (shift == 0 ? 15 : 14) ||
                         (top != 0 && size < -4 && shift < kShiftTop)) {
                         if (top >= 0x4780u) report_error(p.err, ATTN_ERR_UNSUPPORTED);
-                        shift = v_again(tile, at);
+                        shift = v_again(tile, at, top);
                     }
                     // (zeros weigh nothing beside any other tile)
                     if (ct == 0) {

@@ -294,3 +294,28 @@ def test_positions_at_the_ends_of_int32(fmt, kind):
     for c.window in (0, 2 ** 31 - 1, 20):
         got = c.check()
         assert not got[0, 0].any() and not got[1, 1].any() and not got[2].any()
+
+
+@pytest.mark.parametrize("n,per,kind", [(2, 16, gq.LINEAR), (40, 16, gq.PAGED), (3, 5, gq.PAGED)])
+def test_values_whose_size_jumps(n, per, kind):
+    """Key tiles each of a size that the one before does not foretell, the first one's later keys
+    too; pages that are gathered row by row."""
+    c = Case("bf16", kind, one_group(n, 1500), [1 + i % 30 for i in range(n)], 1, 8, 2, 128, per, n,
+             hole=False)
+    lead = torch.tensor([c.slot(0, t) for t in range(1500)])
+    g = torch.Generator().manual_seed(n)
+    for first in (0, -40, 12):
+        size = torch.ones(c.vd.shape[0], 1, 1, dtype=torch.float64) * 2.0 ** -10
+        powers = torch.randint(-60, 13, (12,), generator=g)
+        powers[0] = first
+        size[lead, 0, 0] = 2.0 ** powers[torch.arange(1500) // 128].double()
+        size[lead[100:128]] *= 2.0 ** (-20 if first > 0 else 10)
+        values = torch.randn(c.vd.shape, generator=g, dtype=torch.float64)
+        put_values(c, (values * size).clamp(-60000, 60000))
+        c.check()
+        # rows that only attend one tile's keys, by their windows
+        c.lens = torch.tensor([130 + 37 * (i % 30) for i in range(n)], dtype=torch.int32)
+        c.pos, c.window = c.lens - 1, 60
+        c.check()
+        c.lens = c.plens + torch.tensor([1 + i % 30 for i in range(n)], dtype=torch.int32)
+        c.pos, c.window = c.lens - 1, 0
