@@ -27,8 +27,11 @@
 // a warp a token 11.9; 1,500 of 32/32 x 64 12.9 and 15.0; a prompt the same).
 //
 // Measured: 14,449 tokens of 28/4 x 128 44.7 us (5.29 TB/s, 78% of a copy's rate; 64% of the issue slots),
-// with norms 55.6 (the sums of squares' shuffles and the factors of both weights), interleaved 44.2,
-// appended to a linear cache 51.7.
+// with norms 55.7 (the sums of squares' shuffles and the factors of both weights: 71% of the issue
+// slots), interleaved 44.2, appended to a linear cache 51.6 (bf16) or 52.2 (E4M3).  1,500 tokens of
+// 32/32 x 64 with norms into a linear cache 12.8 (42% of a copy's rate): 56% of the issue slots at 17
+// warps an SM; a warp asks for a round of rows and waits for it, three times, and V's rows, a third of
+// them, go through the norm's sums and products to be written as they came.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>

@@ -24,20 +24,21 @@
 //                one a lane; where pages are no multiple of 8 keys, 16-byte cp.async by row
 //   warp 1       one thread issues tcgen05.mma: S = Q K^T, O += P V (f16, P from TMEM)
 //   warps 4..    bring what is loaded into the form that is multiplied: V of a bf16 cache to
-//                f16 in place (warps 4..7), 8-bit codes to f16 (exact) from a ring of their own
+//                f16 times a power of two in place (warps 4..7), 8-bit codes to f16 (exact) from a ring of their own
 //                (K warps 4..7, V warps 8..11); values outside the group's range become zeros
 //   the last 8   softmax, a thread a row of a tile; weights rounded once to f16 and written
 //                over S in TMEM
 // The plan is made on the device from lengths, rows and positions, by every CTA for itself
 // (a captured graph follows them); CTAs are persistent for batches of more pairs than SMs.
 //
-// What bounds it.  A pair of tiles (head_dim 128, bf16) takes 1.6 us a key tile, of which its products
-// are 1.0: the softmax (S read from TMEM twice, a chain of ~2,100 cycles a tile) and the loads' issue
-// run beside them, at 45% of the issue slots; 256 requests over 32,768 shared keys, 32/8 heads: 155 us,
-// 890 TFLOP/s.  A lone tile takes 1.3 us (its K and V are 7.6 TB/s over all SMs), over codes 1.7 to 2.0:
-// four warps widen K and four V, 170 to 300 cycles for each 16 codes of a thread, beside the softmax
-// warps.  A step over few keys is a chain: the plan 3 us, the first tiles, the merge 3 us (two
-// requests over 512 keys 15.6 us).
+// What bounds it.  A pair of tiles (head_dim 128, bf16) takes 1.75 us a key tile, of which its products
+// are 1.0: the softmax (S read from TMEM twice, a chain of ~2,100 cycles a tile), V's conversion and the
+// loads' issue run beside them, at 48% of the issue slots; 256 requests over 32,768 shared keys, 32/8
+// heads: 159 to 164 us, 840 to 870 TFLOP/s, of which ~31 are no key tiles (plan, first and last tiles,
+// own keys, merge).  A lone tile takes 1.3 us (its K and V are 7.6 TB/s over all SMs), over codes 1.7 to
+// 2.0: four warps widen K and four V, 170 to 300 cycles for each 16 codes of a thread, beside the
+// softmax warps.  A step over few keys is a chain: the plan 3 us, the first tiles, the merge 3 us (two
+// requests over 512 keys 16.8 us).
 //
 // Scales of 8-bit caches leave the products as in attend.cu: K's multiplies the scores, V's
 // enters the weights' exponent, l sums w / vs.  Weights are held times 2^7 (those down to
