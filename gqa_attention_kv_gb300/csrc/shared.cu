@@ -366,7 +366,7 @@ __device__ int make_plan(const Params &p, int32_t *mem, int want, bool tables, P
     }
     __syncthreads();
     // where the merge finds a position's parts
-    if (tables)
+    if (tables && (int)blockIdx.x < ctas)
         for (int i = blockIdx.x * kThreads + threadIdx.x; i < B * p.q_rows; i += ctas * kThreads) {
             const int b = i / p.q_rows, g = group_of(b), n = g_start[g + 1] - g_start[g];
             p.ws_rows[i] = make_int4(g_base[g] + (i - g_start[g] * p.q_rows) * p.group,
@@ -565,7 +565,9 @@ __global__ void __launch_bounds__(Cfg<FMT, HD>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (w.n_kt == 0) break;  // (the same for the whole CTA)
+    // (the same for the whole CTA; it may lie past those that work, which for two groups can be
+    // fewer than for one: its piece is then another's second one)
+    if (w.n_kt == 0 || (int)blockIdx.x >= ctas) break;
     const uint32_t tmem = *tmem_slot;
     const int first_pos = w.pair * 2 * p.rt;         // of the group's positions
     const bool dual = w.n_pos <= p.rt;               // one tile, two streams of key tiles
@@ -1579,25 +1581,27 @@ static int prefix_sms(int batch, int q_rows, int group, int n_kv_heads, int head
     const double own = 0.5 * batch * (double)(max_seq_len - max_prefix_len) * n_kv_heads *
                            head_dim * 2 * esize / (esize == 2 ? 36e3 : 28e3) +
                        (double)own_units * (esize == 2 ? 2.5 : 3.0);
-    auto end_of = [&](int64_t k) {
-        const double t = 9 + (double)((tiles + k - 1) / k) * tile;
+    auto end_of = [&](uint32_t most_tiles, int k) {
+        const double t = 9 + most_tiles * tile;
         // the own keys: on the other SMs until then, on all after
         const double left = own - t * (double)(sms - k * units);
         return t + (left > 0 ? 4 + left / sms : 0);
     };
     // ... of those about as good the most: late own keys cost less than a late shared part, which
     // is what a batch of several groups would have
-    int64_t best = 1;
+    constexpr int kMost = 256;
+    double ends[kMost + 1];
+    const int ks = (int)std::min<int64_t>({sms / units, std::max<int64_t>(1, tiles), kMost});
     double least = 1e30;
-    for (int pass = 0; pass < 2; ++pass)
-        for (int64_t k = 1; k * units <= sms && k <= std::max<int64_t>(1, tiles); ++k) {
-            if (k > 1 && (tiles + k - 1) / k == (tiles + k - 2) / (k - 1)) continue;
-            const double end = end_of(k);
-            if (pass == 0)
-                least = std::min(least, end);
-            else if (end <= 1.03 * least)
-                best = k;
-        }
+    uint32_t before = 0;
+    for (int k = 1; k <= ks; ++k) {
+        const uint32_t most_tiles = ((uint32_t)tiles + k - 1) / k;
+        ends[k] = most_tiles == before ? 1e30 : end_of(most_tiles, k);
+        before = most_tiles;
+        least = std::min(least, ends[k]);
+    }
+    int best = ks;
+    while (best > 1 && ends[best] > 1.03 * least) --best;
     return (int)(best * units);
 }
 

@@ -319,3 +319,14 @@ def test_values_whose_size_jumps(n, per, kind):
         c.check()
         c.lens = c.plens + torch.tensor([1 + i % 30 for i in range(n)], dtype=torch.int32)
         c.pos, c.window = c.lens - 1, 0
+
+
+@pytest.mark.parametrize("n,groups,H,prefix,own", [(7, 3, 8, 300, 40), (120, 64, 1, 900, 3),
+                                                   (60, 31, 2, 200, 2), (90, 45, 4, 40, 1)])
+def test_more_pieces_than_ctas_at_work(n, groups, H, prefix, own):
+    """Groups between the powers of two that CTAs are counted for: pieces past their number are taken
+    in a second round, by the CTAs at work only."""
+    at = [(i * groups // n) for i in range(n)]
+    lead = [at.index(a) for a in at]
+    Case("bf16", gq.LINEAR, [(b, prefix + a % 7) for b, a in zip(lead, at)],
+         [1 + i % own for i in range(n)], 1, 2 * H, H, 64, 16, n + groups).check()
