@@ -597,10 +597,10 @@ int attn_decode_sinks(const void *q, const attn_kv_cache *cache, const int32_t *
  *                 An entry outside its range stores ATTN_ERR_BOUNDS: a length is
  *                 clipped, a prefix in a row that is not there is skipped.
  *   max_prefix_len   host-side upper bound of prefix_lens[], >= 0
- * When it pays: a call costs 15 to 20 us where attn_decode over the same forked
+ * When it pays: a call costs 17 to 20 us where attn_decode over the same forked
  * table takes 9, so keys that groups read once have to be many.  32/8 heads of 128,
  * up to 200 own keys, against attn_decode (us): two requests over 512 shared bf16
- * keys 16 (10), over 32,768 50 (45); 16 over 512 20 (15), over 2,048 22 (28), over
+ * keys 17 (10), over 32,768 50 (45); 16 over 512 20 (15), over 2,048 22 (28), over
  * 14,449 40 (127); 64 over 512 27 (34), over 4,096 29 (140); 120 in five groups of
  * 2,048 45 (93); 64 in pairs of 2,048 67 (52).  Over INT8 from about twice the keys
  * on: 16 over 2,048 22 (18), 64 over 2,048 27 (45).  max_seq_len and max_prefix_len
