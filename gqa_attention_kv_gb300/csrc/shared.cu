@@ -24,8 +24,9 @@
 //                one a lane; where pages are no multiple of 8 keys, 16-byte cp.async by row
 //   warp 1       one thread issues tcgen05.mma: S = Q K^T, O += P V (f16, P from TMEM)
 //   warps 4..    bring what is loaded into the form that is multiplied: V of a bf16 cache to
-//                f16 times a power of two in place (warps 4..7), 8-bit codes to f16 (exact) from a ring of their own
-//                (K warps 4..7, V warps 8..11); values outside the group's range become zeros
+//                f16 times a power of two in place (warps 4..7), 8-bit codes to f16 (exact) from
+//                a ring of their own (K warps 4..7, V warps 8..11); values outside the group's range
+//                become zeros
 //   the last 8   softmax, a thread a row of a tile; weights rounded once to f16 and written
 //                over S in TMEM
 // The plan is made on the device from lengths, rows and positions, by every CTA for itself
@@ -44,10 +45,10 @@
 // enters the weights' exponent, l sums w / vs.  Weights are held times 2^7 (those down to
 // 2^-21 of the largest keep f16's 11 bits).  Values of a bf16 cache have such a scale too, or f16
 // would lose them from 2^-14 on: those of a tile are multiplied with a power of two (exactly) and the
-// weights of its keys divided by it.  The power of the tile before is tried; where the
-// tile's largest value, which the conversion finds by the way, leaves 2^-4 .. 2^15 by it, the tile is
-// read and converted again with its own (256 requests over 32,768 keys 160 us; with a first round
-// over every tile 166, without powers of two 152).  A CTA leaves O normalised by the plain sum of its
+// weights of its keys divided by it.  The power of the tile before is tried (of a quarter of the first
+// tile at first); where the tile's largest value, which the conversion finds by the way, leaves 2^-4 ..
+// 2^15 by it, the tile is read and converted again with its own (256 requests over 32,768 keys 160 us;
+// with a first round over every tile 166, without powers of two 152).  A CTA leaves O normalised by the plain sum of its
 // weights and held times a power of two of its row, in f16 (2^-11, a quarter of the output's bf16
 // half step), and the logarithms of both sums.
 #include <cuda.h>
@@ -204,8 +205,9 @@ __device__ __forceinline__ int working_ctas(const Params &p, int groups) {
 
 // The plan: groups, their pieces, and the piece that is asked for (n_kt 0: none).  `mem` is
 // scratch in shared memory; every thread of the CTA calls this and passes its last barrier.  ctas:
-// how many CTAs work.  Of U units (group, KV head, pair of tiles) that weigh their key tiles each is cut into so many
-// pieces (else 1 + floor((SMs - U) tiles / sum)) that all are at most the SMs, or U.
+// how many CTAs work (sharing_groups has to agree: a CTA that left by it takes no piece).  Of U units
+// (group, KV head, pair of tiles) that weigh their key tiles each is cut into so many pieces (else
+// 1 + floor((CTAs - U) tiles / sum)) that all are at most the CTAs, or U.
 __device__ int make_plan(const Params &p, int32_t *mem, int want, bool tables, Piece &mine,
                          int &ctas) {
     const int kThreads = blockDim.x;
@@ -300,7 +302,7 @@ __device__ int make_plan(const Params &p, int32_t *mem, int want, bool tables, P
             work += __shfl_xor_sync(0xffffffffu, work, o);
         }
         // Of U units, each cut into pieces of at most s key tiles: the least s whose pieces are no
-        // more than the SMs lies between work / SMs and work / (SMs - U); 32 of those are tried
+        // more than the CTAs lies between work / CTAs and work / (CTAs - U); 32 of those are tried
         const int spare = max(0, ctas - units);
         int most = 0;  // s, or 0: units are cut in proportion
         if (groups <= 32 && spare > 0 && work < (int64_t(1) << 30) && work > 0) {

@@ -399,8 +399,8 @@ int attn_decode_kernel_launches(const attn_kv_cache *cache, int batch, int q_row
  *   then 2^-33; further apart, keys that count).
  *   Scores, scale * q . key * log2(e), have to stay below 2^24 in
  *   magnitude: where the largest of a stretch of keys does not,
- *   ATTN_ERR_UNSUPPORTED is reported and the row is unspecified.  Its workspace is like any other's (zero-filled before its
- *   first use).
+ *   ATTN_ERR_UNSUPPORTED is reported and the row is unspecified.  Its workspace is
+ *   like any other's (zero-filled before its first use).
  *   A group of 64 or more query rows (q_rows x n_q_heads / n_kv_heads) over a
  *   linear slot-major bf16 cache is a prefill chunk and computes as
  *   attn_prefill does: P V from f16 softmax weights and f16 values, with the
